@@ -30,6 +30,10 @@ int fetch_error_attn_bf16(int* where);
 int fetch_error_attn_block(int* where);
 int fetch_error_rope(int* where);
 int fetch_error_ring_step(int* where);
+int fetch_error_rope_apply(int* where);
+int fetch_error_chunk_attn(int* where);
+int fetch_error_attn_weights(int* where);
+int fetch_error_evict(int* where);
 
 }  // namespace ra
 

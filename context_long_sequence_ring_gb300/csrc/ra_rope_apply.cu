@@ -1,0 +1,200 @@
+// Rotary positions on strided rows: both pairings, part of the head, any
+// frequency table, and the gradient direction.
+//
+// Mathematics.  Pair i of a row at position m is turned by the angle
+// m * f_i: (a, b) -> mscale * (a cos - b sin, b cos + a sin).  The backward
+// direction is the transposed rotation, i.e. the angle -m * f_i.
+// Angles are taken in turns, m * phi_i with phi_i = f_i / 2 pi held as an
+// unevaluated sum of two floats.  m * hi is split exactly into p + e with one
+// FMA, the whole turns rint(p) drop out exactly, and the rest goes to
+// sincospif: the angle error is about 1e-7 turns at any position below 2^24.
+#include <algorithm>
+#include <cmath>
+
+#include "ra_common.cuh"
+
+RA_DEFINE_ERROR_FETCH(fetch_error_rope_apply)
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = 128;           // rot <= 256
+constexpr int kPositionLimit = 1 << 24;  // positions are exact in a float below this
+
+struct Params {
+  const void* src;
+  void* dst;
+  const int32_t* idx;
+  const int32_t* positions;
+  int64_t src_rows, src_rs, src_hs, dst_rs, dst_hs, rows;
+  int32_t H, d, rot;
+  float mscale, sign;
+  float2 phase[kMaxPairs];  // phi_i as hi + lo
+};
+
+// mscale * cos and mscale * sin (signed by the direction) of pair i at position m.
+__device__ __forceinline__ void turn(const Params& p, int i, float m, float& c, float& s) {
+  const float2 ph = p.phase[i];
+  const float t = m * ph.x;
+  const float err = fmaf(m, ph.x, -t);           // m * hi = t + err exactly
+  const float f = (t - rintf(t)) + fmaf(m, ph.y, err);
+  sincospif(2.0f * f, &s, &c);
+  c *= p.mscale;
+  s *= p.mscale * p.sign;
+}
+
+// Source row of output row r; -1 for a zero row.
+__device__ __forceinline__ int64_t source_row(const Params& p, int64_t r) {
+  if (!p.idx) return r;
+  const int32_t s = p.idx[r];
+  if (s >= p.src_rows) {
+    ra_record_error(RA_ERR_DEVICE_BOUNDS, 400);
+    return -1;
+  }
+  return s;
+}
+
+__device__ __forceinline__ float position(const Params& p, int64_t r) {
+  const int32_t m = p.positions[r];
+  if (m < 0 || m >= kPositionLimit) {
+    ra_record_error(RA_ERR_DEVICE_BOUNDS, 401);
+    return 0.f;
+  }
+  return static_cast<float>(m);
+}
+
+__device__ __forceinline__ float load1(const __nv_bfloat16* x) { return __bfloat162float(*x); }
+__device__ __forceinline__ float load1(const float* x) { return *x; }
+__device__ __forceinline__ void store1(__nv_bfloat16* x, float v) { *x = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store1(float* x, float v) { *x = v; }
+
+// Element-wise form for any stride and alignment: one thread per (row, unit),
+// units 0 .. rot/2-1 the pairs, the others the elements past rot.
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constant__ Params p) {
+  const int half = p.rot / 2;
+  const int units = half + (p.d - p.rot);
+  const int64_t total = p.rows * units;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; w < total; w += stride) {
+    const int64_t r = w / units;
+    const int u = static_cast<int>(w - r * units);
+    const int64_t s = source_row(p, r);
+    const bool pair = u < half;
+    const int e0 = pair ? (INTER ? 2 * u : u) : p.rot + (u - half);
+    const int e1 = INTER ? e0 + 1 : e0 + half;
+    float c = 1.f, sn = 0.f;
+    if (pair && s >= 0) turn(p, u, position(p, r), c, sn);
+    const T* x = static_cast<const T*>(p.src) + s * p.src_rs;
+    T* y = static_cast<T*>(p.dst) + r * p.dst_rs;
+    for (int h = 0; h < p.H; ++h, x += p.src_hs, y += p.dst_hs) {
+      if (!pair) {
+        y[e0] = s >= 0 ? x[e0] : T(0.f);
+        continue;
+      }
+      const float a = s >= 0 ? load1(x + e0) : 0.f, b = s >= 0 ? load1(x + e1) : 0.f;
+      store1(y + e0, a * c - b * sn);
+      store1(y + e1, b * c + a * sn);
+    }
+  }
+}
+
+// Whether the elements of [rows, H, d] at these strides are all apart.
+bool apart(int64_t rows, int64_t rs, int64_t H, int64_t hs, int64_t d) {
+  if (rows > 1 && H > 1)
+    return (hs >= d && rs >= (H - 1) * hs + d) || (rs >= d && hs >= (rows - 1) * rs + d);
+  return (rows <= 1 || rs >= d) && (H <= 1 || hs >= d);
+}
+
+}  // namespace
+
+extern "C" ra_status ra_rope_apply(const void* src, int64_t src_rows, int64_t src_row_stride,
+                                   int64_t src_head_stride, void* dst, int64_t dst_row_stride,
+                                   int64_t dst_head_stride, int64_t rows, int32_t H, int32_t d, int32_t rot,
+                                   ra_dtype dt, ra_rope_style style, const int32_t* idx, const int32_t* positions,
+                                   const double* inv_freq, double mscale, int32_t backward, ra_stream stream) {
+  ra::clear_error();
+  RA_REQUIRE(dt == RA_BF16 || dt == RA_F32, "dtype must be RA_BF16 or RA_F32");
+  RA_REQUIRE(style == RA_ROPE_HALF || style == RA_ROPE_INTERLEAVED, "unknown rope style");
+  RA_REQUIRE(H >= 1 && d >= 1 && d <= 1024, "H >= 1 and 1 <= d <= 1024 required");
+  RA_REQUIRE(rot >= 2 && rot % 2 == 0 && rot <= d && rot <= 2 * kMaxPairs, "rot must be even, in [2, min(d, %d)]",
+             2 * kMaxPairs);
+  RA_REQUIRE(rows >= 0 && src_rows >= 0, "negative size");
+  RA_REQUIRE(idx || rows == src_rows, "without idx, rows must equal src_rows");
+  const int64_t lim = int64_t(1) << 40;
+  RA_REQUIRE(src_row_stride >= 0 && src_head_stride >= 0 && dst_row_stride >= 0 && dst_head_stride >= 0 &&
+                 src_row_stride < lim && src_head_stride < lim && dst_row_stride < lim && dst_head_stride < lim &&
+                 rows < (int64_t(1) << 31) && src_rows < (int64_t(1) << 31),
+             "strides must be in [0, 2^40), rows in [0, 2^31)");
+  RA_REQUIRE(inv_freq != nullptr && std::isfinite(mscale), "inv_freq must be given and mscale finite");
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int i = 0; i < rot / 2; ++i)
+    RA_REQUIRE(std::fabs(inv_freq[i]) <= two_pi, "inv_freq[%d] must be in [-2 pi, 2 pi]", i);
+  if (rows == 0) return RA_OK;
+  RA_REQUIRE(src && dst && positions, "NULL pointer");
+  RA_REQUIRE(apart(rows, dst_row_stride, H, dst_head_stride, d), "the elements of dst must not alias one another");
+  const int es = dt == RA_BF16 ? 2 : 4;
+  const uintptr_t s0 = reinterpret_cast<uintptr_t>(src), d0 = reinterpret_cast<uintptr_t>(dst);
+  RA_REQUIRE((s0 | d0) % es == 0, "src and dst must be aligned to their elements");
+  const bool same = src == dst && (rows == 1 || src_row_stride == dst_row_stride) &&
+                    (H == 1 || src_head_stride == dst_head_stride);
+  if (idx || !same) {
+    const uintptr_t s1 =
+        s0 + es * (std::max<int64_t>(src_rows - 1, 0) * src_row_stride + (H - 1) * src_head_stride + d);
+    const uintptr_t d1 = d0 + es * ((rows - 1) * dst_row_stride + (H - 1) * dst_head_stride + d);
+    RA_REQUIRE(d1 <= s0 || s1 <= d0, "dst must be src itself with its strides (without idx) or not overlap it");
+  }
+
+  Params p;
+  p.src = src; p.dst = dst; p.idx = idx; p.positions = positions;
+  p.src_rows = src_rows; p.src_rs = src_row_stride; p.src_hs = src_head_stride;
+  p.dst_rs = dst_row_stride; p.dst_hs = dst_head_stride; p.rows = rows;
+  p.H = H; p.d = d; p.rot = rot;
+  p.mscale = static_cast<float>(mscale);
+  p.sign = backward ? -1.f : 1.f;
+  for (int i = 0; i < kMaxPairs; ++i) {
+    const double phi = i < rot / 2 ? inv_freq[i] / two_pi : 0.0;
+    const float hi = static_cast<float>(phi);
+    p.phase[i] = make_float2(hi, static_cast<float>(phi - static_cast<double>(hi)));
+  }
+  const int64_t units = rot / 2 + (d - rot);
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ra::ceil_div(rows * units, kThreads), 152 * 64));
+  const bool inter = style == RA_ROPE_INTERLEAVED;
+  if (dt == RA_BF16) {
+    if (inter) rope_any_kernel<__nv_bfloat16, true><<<blocks, kThreads, 0, stream>>>(p);
+    else rope_any_kernel<__nv_bfloat16, false><<<blocks, kThreads, 0, stream>>>(p);
+  } else {
+    if (inter) rope_any_kernel<float, true><<<blocks, kThreads, 0, stream>>>(p);
+    else rope_any_kernel<float, false><<<blocks, kThreads, 0, stream>>>(p);
+  }
+  RA_LAUNCH_CHECK("rope_any_kernel");
+  return RA_OK;
+}
+
+extern "C" ra_status ra_rope_frequencies(ra_rope_scaling scaling, double base, int32_t rot, double factor,
+                                         double trained_len, double* inv_freq, double* mscale) {
+  ra::clear_error();
+  RA_REQUIRE(scaling >= RA_ROPE_NONE && scaling <= RA_ROPE_YARN, "unknown scaling");
+  RA_REQUIRE(base > 1.0 && std::isfinite(base), "base must be finite and > 1");
+  RA_REQUIRE(rot >= 2 && rot % 2 == 0 && rot <= 2 * kMaxPairs, "rot must be even, in [2, %d]", 2 * kMaxPairs);
+  RA_REQUIRE(factor >= 1.0 && std::isfinite(factor), "factor must be finite and >= 1");
+  RA_REQUIRE(scaling != RA_ROPE_YARN || (trained_len >= 1.0 && std::isfinite(trained_len)),
+             "trained_len must be finite and >= 1");
+  RA_REQUIRE(scaling != RA_ROPE_NTK || rot > 2, "RA_ROPE_NTK needs rot > 2");
+  RA_REQUIRE(inv_freq != nullptr, "inv_freq is NULL");
+  const double two_pi = 6.283185307179586476925286766559;
+  const double b = scaling == RA_ROPE_NTK ? base * std::pow(factor, static_cast<double>(rot) / (rot - 2)) : base;
+  RA_REQUIRE(std::isfinite(b), "base * factor^(rot/(rot-2)) overflows");
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = std::pow(b, -2.0 * i / rot);
+    if (scaling == RA_ROPE_LINEAR) f /= factor;
+    if (scaling == RA_ROPE_YARN) {
+      const double turns = trained_len * f / two_pi;
+      const double g = std::min(1.0, std::max(0.0, (turns - 1.0) / 31.0));
+      f = (1.0 - g) * f / factor + g * f;
+    }
+    inv_freq[i] = f;
+  }
+  if (mscale) *mscale = scaling == RA_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  return RA_OK;
+}

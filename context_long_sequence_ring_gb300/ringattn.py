@@ -19,6 +19,8 @@ from .build import LIB
 RA_OK, RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_CUDA, RA_ERR_TIMEOUT, RA_ERR_DEVICE_BOUNDS = range(6)
 RA_F32, RA_BF16 = 0, 1
 LAYOUTS = {"natural": 0, "zigzag": 1}
+ROPE_STYLES = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 _c = ctypes
 _vp, _i32, _i64, _u64, _f32, _sz = _c.c_void_p, _c.c_int32, _c.c_int64, _c.c_uint64, _c.c_float, _c.c_size_t
@@ -57,6 +59,16 @@ SIGNATURES = {
                               _i32, _i64, _f32, _i32, _vp, _vp, _c.POINTER(_i32), _vp],
     "ra_cp_lse_rescale": [_vp, _vp, _i32, _i32, _i64, _i32, _i32, _vp, _vp, _vp],
     "ra_cp_head_split": [_vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp],
+    "ra_rope_apply": [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _c.c_int, _c.c_int, _vp, _vp, _vp,
+                      _c.c_double, _i32, _vp],
+    "ra_rope_frequencies": [_c.c_int, _c.c_double, _i32, _c.c_double, _c.c_double, _vp, _c.POINTER(_c.c_double)],
+    "ra_cp_chunk_attn_workspace_size": [_i32, _i32, _i32, _c.POINTER(_sz)],
+    "ra_cp_chunk_attn": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i64,
+                         _i32, _f32, _vp, _c.c_int, _vp, _vp, _sz, _vp],
+    "ra_cp_attn_weights": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                           _i64, _i32, _f32, _vp, _vp, _vp],
+    "ra_cp_evict": [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _c.c_int, _i32, _i32, _i32, _i32, _i32, _i32, _i64,
+                    _i32, _i32, _i32, _vp, _vp, _vp],
     "ra_selftest_wait_timeout": [_i64, _vp],
     "ra_synth_fill": [_u64, _i64, _vp, _i32, _vp, _vp],
 }
@@ -120,6 +132,20 @@ def _need_cuda(*ts):
             raise ValueError("tensor must be contiguous")
 
 
+def _need_here(dtype, *ts):
+    """Contiguous tensors of one dtype (None: any) on the current CUDA device."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            _need_cuda(t)
+        if t.device.index != dev:
+            raise ValueError("tensor must be on the current CUDA device")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError("dtype must be %s, not %s" % (dtype, t.dtype))
+
+
 def _dt(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return RA_BF16
@@ -179,6 +205,48 @@ def rope_gather(src: torch.Tensor, positions: torch.Tensor, idx: Optional[torch.
     _check(lib().ra_rope_gather(_ptr(src), src.shape[0], src.shape[1], src.shape[2], _dt(src),
                                 _ptr(idx) if idx is not None else None, rows, _ptr(positions), float(base),
                                 _ptr(out), _stream()))
+    return out
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     trained_len: float = 32768.0):
+    """Frequency table of ``rope_apply``: (inv_freq float64 [rot/2] on the host, mscale), base^(-2i/rot) as it
+    is ("none") or changed for contexts ``factor`` times the trained length ("linear", "ntk", "yarn")."""
+    f, m = torch.empty(max(rot // 2, 0), dtype=torch.float64), _c.c_double(1.0)
+    _check(lib().ra_rope_frequencies(ROPE_SCALINGS[scaling], float(base), rot, float(factor), float(trained_len),
+                                     _ptr(f), _c.byref(m)))
+    return f, m.value
+
+
+def rope_apply(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, mscale: float = 1.0,
+               style: str = "half", idx: Optional[torch.Tensor] = None, backward: bool = False,
+               out: Optional[torch.Tensor] = None):
+    """Rotary positions of x [rows, H, d] (any strides with the last one 1): the first 2*len(inv_freq)
+    components of each head are turned, the others copied.  inv_freq float64 on the host
+    (``rope_frequencies``); positions int32, one per OUTPUT row.  out[r] comes from x[idx[r]] with idx
+    (zero rows where idx < 0), else from x[r]; without idx, out may be x (in place).  ``backward`` turns
+    by the negative angles: the gradient of x from the gradient of out."""
+    _need_here(torch.int32, positions, idx)
+    if x.dim() != 3 or (out is not None and out.dim() != 3):
+        raise ValueError("x and out must be [rows, H, d]")
+    rows, H, d = x.shape
+    n = rows if idx is None else idx.numel()
+    if out is None:
+        out = torch.empty((n, H, d), dtype=x.dtype, device=x.device)
+    if not (x.is_cuda and x.device == out.device == positions.device):
+        raise ValueError("x and out must be on the current CUDA device")
+    if out.shape != (n, H, d) or out.dtype != x.dtype:
+        raise ValueError("out must be %s of x's dtype" % ((n, H, d),))
+    if d > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
+        raise ValueError("the elements of a head must be contiguous")
+    if positions.numel() != n:
+        raise ValueError("one position per output row")
+    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 vector on the host")
+    xs, os_ = x.stride(), out.stride()
+    _check(lib().ra_rope_apply(x.data_ptr(), rows, xs[0], xs[1], out.data_ptr(), os_[0], os_[1], n, H, d,
+                               2 * inv_freq.numel(), _dt(x), ROPE_STYLES[style], _ptr(idx), positions.data_ptr(),
+                               inv_freq.data_ptr(), float(mscale), 1 if backward else 0, _stream()))
     return out
 
 
@@ -497,6 +565,112 @@ def cp_lse_rescale_fn():
     def rescale(o_local, lse_all, w, o_scaled, lse_total):
         cp_lse_rescale(o_local, lse_all, w, o_scaled, lse_total)
     return rescale
+
+
+def _need_paged(q, cache, block_table, query_start_loc, ctx_lens, pcp: int, dcp: int):
+    """Checks shared by the operators on a packed batch of queries and the paged cache."""
+    _need_here(torch.bfloat16, q, cache)
+    _need_here(torch.int32, block_table, query_start_loc, ctx_lens)
+    if q.dim() != 3 or cache.dim() != 5 or block_table.dim() != 2:
+        raise ValueError("q must be [T, Hq, d], the cache [W, NB, Hkv, bs, d], block_table [R, max_vblocks]")
+    if cache.shape[0] != pcp * dcp:
+        raise ValueError("cache has %d devices, pcp*dcp = %d" % (cache.shape[0], pcp * dcp))
+    if cache.shape[4] != q.shape[2]:
+        raise ValueError("q and the cache must have the same head dim")
+    R = block_table.shape[0]
+    if query_start_loc.numel() != R + 1 or ctx_lens.numel() != R:
+        raise ValueError("block_table has %d requests: query_start_loc needs R+1 entries, ctx_lens R" % R)
+
+
+def cp_chunk_attn_workspace_size(Hq: int, Hkv: int, d: int) -> int:
+    n = _sz(0)
+    _check(lib().ra_cp_chunk_attn_workspace_size(Hq, Hkv, d, _c.byref(n)))
+    return n.value
+
+
+def cp_chunk_attn(q, k_cache, v_cache, block_table, query_start_loc, ctx_lens, interleave: int, pcp: int, dcp: int,
+                  causal: bool = True, scale: Optional[float] = None, out_dtype=torch.bfloat16, workspace=None,
+                  o=None, lse=None):
+    """Attention of a packed batch of new tokens, q [T, Hq, d] (request r has rows query_start_loc[r] ..
+    query_start_loc[r+1], the last ones of its ctx_lens[r] cached tokens), over the sharded paged cache
+    -> (O [T, Hq, d], LSE [T, Hq]).  Rows of no request are left as they were (undefined in a new O)."""
+    _need_paged(q, k_cache, block_table, query_start_loc, ctx_lens, pcp, dcp)
+    T, Hq, d = q.shape
+    _, NB, Hkv, bs, _ = k_cache.shape
+    _need_here(torch.bfloat16, v_cache)
+    _need_here(None, workspace, o)
+    _need_here(torch.float32, lse)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    if workspace is None:
+        workspace = torch.empty(cp_chunk_attn_workspace_size(Hq, Hkv, d), dtype=torch.uint8, device=q.device)
+    if o is None:
+        o = torch.empty((T, Hq, d), dtype=out_dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    if o.shape != q.shape or lse.shape != q.shape[:2]:
+        raise ValueError("o must be [T, Hq, d], lse [T, Hq]")
+    _check(lib().ra_cp_chunk_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                  query_start_loc.data_ptr(), ctx_lens.data_ptr(), T, block_table.shape[0], Hq, Hkv, d,
+                                  bs, interleave, pcp, dcp, block_table.shape[1], NB, 1 if causal else 0,
+                                  float(scale or 0.0), o.data_ptr(), _dt(o), lse.data_ptr(), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _stream()))
+    return o, lse
+
+
+def cp_attn_weights(q, lse, k_cache, block_table, query_start_loc, ctx_lens, interleave: int, pcp: int, dcp: int,
+                    w_in=None, w_out=None, causal: bool = True, scale: Optional[float] = None):
+    """Accumulated attention weight of every cached token, per K/V head -> w_out fp32 [W, NB, Hkv, bs]: w_in
+    (None: 0; the chunk's own tokens start from 0) plus the softmax weights of the queries q [T, Hq, d] with
+    their lse [T, Hq].  w_out may be w_in; slots of no token are left as they were (0 in a new w_out)."""
+    _need_paged(q, k_cache, block_table, query_start_loc, ctx_lens, pcp, dcp)
+    _need_here(torch.float32, lse, w_in, w_out)
+    T, Hq, d = q.shape
+    _, NB, Hkv, bs, _ = k_cache.shape
+    if w_out is None:
+        w_out = torch.zeros(k_cache.shape[:4], dtype=torch.float32, device=q.device)
+    if lse.shape != q.shape[:2]:
+        raise ValueError("lse must be [T, Hq]")
+    if w_out.shape != k_cache.shape[:4] or (w_in is not None and w_in.shape != k_cache.shape[:4]):
+        raise ValueError("the weights must be [W, NB, Hkv, bs]")
+    _check(lib().ra_cp_attn_weights(q.data_ptr(), lse.data_ptr(), k_cache.data_ptr(), block_table.data_ptr(),
+                                    query_start_loc.data_ptr(), ctx_lens.data_ptr(), T, block_table.shape[0], Hq, Hkv,
+                                    d, bs, interleave, pcp, dcp, block_table.shape[1], NB, 1 if causal else 0,
+                                    float(scale or 0.0), _ptr(w_in), w_out.data_ptr(), _stream()))
+    return w_out
+
+
+def cp_evict(k_cache, v_cache, weights, block_table, ctx_lens, keep: int, interleave: int, pcp: int, dcp: int,
+             n_sink: int = 0, n_recent: int = 0, dst_block_table=None, kept=None, new_lens=None):
+    """Cut every request's cached context to ``keep`` tokens per K/V head (the first n_sink, the last n_recent
+    and the heaviest of the others by ``weights`` fp32 [W, NB, Hkv, bs]) and pack them in order, with their
+    weights, into the blocks of dst_block_table [R, .] (None: the request's own blocks).  Returns (kept int32
+    [R, Hkv, keep]: former positions, -1 past the end; new_lens int32 [R])."""
+    _need_here(None, k_cache, v_cache)
+    _need_here(torch.float32, weights)
+    _need_here(torch.int32, block_table, ctx_lens, dst_block_table, kept, new_lens)
+    if k_cache.dim() != 5 or block_table.dim() != 2:
+        raise ValueError("the cache must be [W, NB, Hkv, bs, d], block_table [R, max_vblocks]")
+    W, NB, Hkv, bs, d = k_cache.shape
+    R = block_table.shape[0]
+    if W != pcp * dcp:
+        raise ValueError("cache has %d devices, pcp*dcp = %d" % (W, pcp * dcp))
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or weights.shape != k_cache.shape[:4]:
+        raise ValueError("v_cache must be like k_cache, weights [W, NB, Hkv, bs]")
+    if ctx_lens.numel() != R or (dst_block_table is not None and
+                                 (dst_block_table.dim() != 2 or dst_block_table.shape[0] != R)):
+        raise ValueError("ctx_lens and dst_block_table must have one entry per request")
+    if kept is None:
+        kept = torch.empty((R, Hkv, max(keep, 0)), dtype=torch.int32, device=k_cache.device)
+    if new_lens is None:
+        new_lens = torch.empty(R, dtype=torch.int32, device=k_cache.device)
+    if kept.numel() != R * Hkv * keep or new_lens.numel() != R:
+        raise ValueError("kept must be [R, Hkv, keep], new_lens [R]")
+    _check(lib().ra_cp_evict(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), block_table.data_ptr(),
+                             _ptr(dst_block_table), ctx_lens.data_ptr(), R, Hkv, d, _dt(k_cache), bs, interleave, pcp,
+                             dcp, block_table.shape[1], 0 if dst_block_table is None else dst_block_table.shape[1], NB,
+                             keep, n_sink, n_recent, kept.data_ptr(), new_lens.data_ptr(), _stream()))
+    return kept, new_lens
 
 
 # ---------------------------------------------------------------------- misc

@@ -134,6 +134,69 @@ ra_status ra_rope_gather(const void* src, int64_t src_rows, int32_t H, int32_t d
                          void* dst, ra_stream stream);
 
 /* ------------------------------------------------------------------------
+ * ra_rope_apply -- rotary positions of Q or K heads in the forms that models
+ * use beyond ra_rope_gather: either pairing, part of the head, any frequency
+ * table (scaled for long contexts), strided rows, and the gradient direction:
+ *   dst[r, h, :rot] = mscale * Rot(positions[r]) src[s, h, :rot],
+ *   dst[r, h, rot:] = src[s, h, rot:],   s = idx ? idx[r] : r
+ * (a zero row where idx[r] < 0).  Rot(m) turns the i-th pair (a, b) by the
+ * angle m * inv_freq[i]: (a cos - b sin, b cos + a sin); backward != 0 turns it
+ * by the negative angle, which is the transpose: the gradient of src is
+ * ra_rope_apply(gradient of dst, backward = 1), with idx the inverse
+ * permutation if the forward call had one.
+ * Sources: rotary form as ra_rope_gather; scaling: see ra_rope_frequencies.
+ *
+ * src        device dt (RA_BF16 or RA_F32): element (row, head, e) at
+ *            src + row*src_row_stride + head*src_head_stride + e (strides in
+ *            elements, >= 0; e.g. the Q and K heads of a fused projection).
+ * dst        device dt out, addressed the same way; its elements must not
+ *            alias one another.  dst may be src with the same strides when
+ *            idx is NULL (in place); otherwise the two extents must not overlap.
+ * rows       output rows; src_rows: rows of src (== rows without idx).
+ * d, rot     head dim 1 .. 1024 and the rotated part, even, 2 .. min(d, 256).
+ * style      RA_ROPE_HALF: pair i is (i, i + rot/2); RA_ROPE_INTERLEAVED:
+ *            (2i, 2i+1).
+ * positions  device int32 [rows]: position of each OUTPUT row, in [0, 2^24)
+ *            (ra_rope_gather takes them per source row).
+ * inv_freq   host double [rot/2]: radians per position, |x| <= 2 pi.
+ * Angles are formed in turns with an error-free product (their error does not
+ * grow with the position); the rotation is fp32, rounded once to dt.  Rows of
+ * 16-byte aligned vectors are moved as such; other strides and alignments
+ * run an element-wise kernel with the same results.
+ * An idx >= src_rows (zero row) or a position out of range (taken as 0) is a
+ * device-side bounds error.
+ * ---------------------------------------------------------------------- */
+typedef enum ra_rope_style { RA_ROPE_HALF = 0, RA_ROPE_INTERLEAVED = 1 } ra_rope_style;
+
+ra_status ra_rope_apply(const void* src, int64_t src_rows, int64_t src_row_stride, int64_t src_head_stride,
+                        void* dst, int64_t dst_row_stride, int64_t dst_head_stride, int64_t rows, int32_t H,
+                        int32_t d, int32_t rot, ra_dtype dt, ra_rope_style style, const int32_t* idx,
+                        const int32_t* positions, const double* inv_freq, double mscale, int32_t backward,
+                        ra_stream stream);
+
+/* ------------------------------------------------------------------------
+ * ra_rope_frequencies -- the frequency tables of ra_rope_apply, on the host.
+ * theta_i = base^(-2i/rot), i = 0 .. rot/2-1, changed for contexts `factor`
+ * times the trained length (guijiagi.com tag page "Ring Attention", article on
+ * the evolution of long-context techniques, its table of extrapolation
+ * methods: position interpolation, NTK-aware, YaRN):
+ *   RA_ROPE_NONE    theta_i
+ *   RA_ROPE_LINEAR  theta_i / factor
+ *   RA_ROPE_NTK     base' = base * factor^(rot/(rot-2)) (rot > 2), which keeps
+ *                   theta_0 and divides the last theta by factor
+ *   RA_ROPE_YARN    (1-g) theta_i / factor + g theta_i, g the ramp from 0 at 1
+ *                   turn to 1 at 32 turns of theta_i over trained_len, linear in the
+ *                   number of turns trained_len * theta_i / 2 pi
+ * mscale (may be NULL): 1, or 0.1 ln(factor) + 1 for RA_ROPE_YARN (the
+ * attention temperature, applied to Q and K each).
+ * Needs base > 1, factor >= 1, trained_len >= 1 (YARN), all finite.
+ * ---------------------------------------------------------------------- */
+typedef enum ra_rope_scaling { RA_ROPE_NONE = 0, RA_ROPE_LINEAR = 1, RA_ROPE_NTK = 2, RA_ROPE_YARN = 3 } ra_rope_scaling;
+
+ra_status ra_rope_frequencies(ra_rope_scaling scaling, double base, int32_t rot, double factor, double trained_len,
+                              double* inv_freq, double* mscale);
+
+/* ------------------------------------------------------------------------
  * ra_ring_attn_fwd -- causal or full GQA attention forward computed in ring
  * order over N virtual context-parallel ranks with blockwise online softmax.
  * Sources: "Parallelism-CP" diagram (Q/K/V split along the sequence, K/V
@@ -493,6 +556,118 @@ ra_status ra_cp_lse_rescale(const float* o_local, const float* lse_all, int32_t 
  * ---------------------------------------------------------------------- */
 ra_status ra_cp_head_split(const float* o_local, const float* lse_local, int32_t W, int64_t R, int32_t Hq,
                            int32_t d, float* o_split, float* lse_split, ra_stream stream);
+
+/* ------------------------------------------------------------------------
+ * ra_cp_chunk_attn -- attention of a chunk of new tokens per request over the
+ * sharded paged cache: pieces of a chunked prefill, drafted tokens and single
+ * tokens, in one packed batch, read from the cache where it lies (no
+ * ra_cp_kv_gather).  Source: vLLM-Ascend "Context Parallel (CP)", chunked
+ * prefill and DCP/PCP decode (attention over the KV shards, merged by LSE; on
+ * one GPU all W = pcp*dcp devices are virtual); section "Block table".
+ *
+ * The chunk's own K/V are in the cache already (ra_cp_slot_mapping +
+ * ra_cp_kv_scatter): request r has ctx_lens[r] tokens in it, of which its
+ * n_r = query_start_loc[r+1] - query_start_loc[r] queries are the last n_r, so
+ * query i of the request is at position ctx_lens[r] - n_r + i.
+ *
+ * q           device bf16 [T, Hq, d], packed request after request.
+ * query_start_loc device int32 [R+1], non-decreasing, within [0, T].
+ * ctx_lens    device int32 [R].
+ * k_cache, v_cache, block_table, block_size, interleave, pcp, dcp,
+ * max_vblocks, num_blocks: as ra_cp_decode; blocks may be shared by requests.
+ * causal      != 0: a query sees the tokens at positions <= its own; 0: all
+ *             ctx_lens[r] tokens (e.g. the states of an encoder).
+ * o           device [T, Hq, d] out in out_dt; lse device float [T, Hq] out,
+ *             natural log (may be NULL).  Rows outside every request (before
+ *             query_start_loc[0], from query_start_loc[R] on) are left as
+ *             they were.  A query that sees nothing (ctx_lens[r] <
+ *             n_r leaves the first ones at negative positions; ctx_lens[r] = 0)
+ *             gets O 0, LSE -inf.
+ * Slots past ctx_lens[r] are never used, whatever they hold (NaN too); V of a
+ * token below ctx_lens[r] must be finite where a query of the same request
+ * does not see it.
+ * workspace   device scratch of ra_cp_chunk_attn_workspace_size() bytes,
+ *             16-byte aligned: fp32 partials of contexts that several CTAs
+ *             share.  Calls that overlap on the GPU need one each.
+ * Requires Hq % Hkv == 0, Hq/Hkv <= 64, d in {64, 128}, block_size % 16 == 0,
+ * block_size % interleave == 0, T*Hq < 2^31, pcp*dcp*num_blocks*Hkv < 2^31;
+ * bf16 only.  The work is split over the GPU on the device from the lengths found
+ * there, so a captured call may be replayed with other lengths.
+ * Device bounds errors: a request whose query range is decreasing or outside [0, T]
+ * (left out), a context longer than max_vblocks virtual blocks (cut), a block
+ * id outside [0, num_blocks) (its tokens are left out).
+ * ---------------------------------------------------------------------- */
+ra_status ra_cp_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t d, size_t* bytes);
+
+ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                           const int32_t* query_start_loc, const int32_t* ctx_lens, int64_t T, int32_t R, int32_t Hq,
+                           int32_t Hkv, int32_t d, int32_t block_size, int32_t interleave, int32_t pcp, int32_t dcp,
+                           int32_t max_vblocks, int64_t num_blocks, int32_t causal, float scale, void* o,
+                           ra_dtype out_dt, float* lse, void* workspace, size_t ws_bytes, ra_stream stream);
+
+/* ------------------------------------------------------------------------
+ * ra_cp_attn_weights -- the attention weight that every cached token receives
+ * from a chunk of queries, accumulated beside the cache for ra_cp_evict:
+ *   w_out[x, g] = (old ? w_in[x, g] : 0)
+ *                 + sum over the request's queries i that see token x and the
+ *                   query heads h of K/V head g of e^{scale q_ih.k_xg - lse_ih}
+ * for every token x < ctx_lens[r] and K/V head g.  With causal != 0 the chunk's
+ * own tokens (the last n_r, the positions of the queries) are not old: they
+ * start from 0, so that a slot's former content is of no account.  causal = 0:
+ * all tokens are old.
+ *
+ * q, query_start_loc, ctx_lens, k_cache, block table and sizes: as
+ * ra_cp_chunk_attn.  The queries may be the last ones of a longer chunk.
+ * lse         device float [T, Hq]: natural-log sum of exp(scaled scores), as
+ *             ra_cp_chunk_attn or ra_cp_decode gives it; a query whose lse is
+ *             -inf (it saw nothing) adds nothing.
+ * w_in        device float [W, num_blocks, Hkv, block_size], or NULL for all 0.
+ * w_out       device float, same shape, out; may be w_in.  Slots that hold no
+ *             token < ctx_lens[r] of a request are left as they were.
+ * A block that holds tokens of several requests (below their ctx_lens) gets
+ * the value of one of them, which one is not defined.
+ * Sums are fp32 in an order fixed by the sizes.  Same limits and device bounds errors
+ * as ra_cp_chunk_attn (tokens of a bad block are left out).
+ * ---------------------------------------------------------------------- */
+ra_status ra_cp_attn_weights(const void* q, const float* lse, const void* k_cache, const int32_t* block_table,
+                             const int32_t* query_start_loc, const int32_t* ctx_lens, int64_t T, int32_t R,
+                             int32_t Hq, int32_t Hkv, int32_t d, int32_t block_size, int32_t interleave, int32_t pcp,
+                             int32_t dcp, int32_t max_vblocks, int64_t num_blocks, int32_t causal, float scale,
+                             const float* w_in, float* w_out, ra_stream stream);
+
+/* ------------------------------------------------------------------------
+ * ra_cp_evict -- cut every request's cached context to `keep` tokens by
+ * accumulated attention weight, per K/V head, and pack what is kept.
+ * A request with ctx_lens[r] <= keep keeps all its tokens.  Of any other,
+ * each K/V head keeps the first n_sink tokens, the last n_recent, and of the
+ * others the keep - n_sink - n_recent of largest weight (of equal weights the
+ * earlier token; NaN counts as the lightest, -0 as 0).  The kept tokens stay in
+ * order: the j-th becomes token j of the packed context, its K, V and weight
+ * moved to the slot of token j.
+ *
+ * k_cache, v_cache device [W, num_blocks, Hkv, block_size, d] (dtype dt),
+ *             weights device float [W, num_blocks, Hkv, block_size]: changed
+ *             in place.
+ * block_table device int32 [R, max_vblocks]; ctx_lens device int32 [R].
+ * dst_block_table device int32 [R, dst_max_vblocks]: the blocks that take the
+ *             packed context (none of them in block_table below ctx_lens), or
+ *             NULL: packed into the request's own blocks.
+ * kept        device int32 [R, Hkv, keep] out: former position of packed
+ *             token j, -1 from new_lens[r] on.
+ * new_lens    device int32 [R] out: min(ctx_lens[r], keep).  Not ctx_lens.
+ * No block may be in two requests' tables below their ctx_lens (or in two
+ * destination tables).
+ * Requires 0 <= n_sink, n_recent; n_sink + n_recent <= keep, keep >= 1;
+ * block_size % interleave == 0; d * element size a multiple of 16 bytes.
+ * Device bounds errors: a context longer than max_vblocks virtual blocks
+ * (cut), a bad source block id (its tokens count as lightest and move as zeros), a
+ * destination outside the table or the cache (not written).
+ * ---------------------------------------------------------------------- */
+ra_status ra_cp_evict(void* k_cache, void* v_cache, float* weights, const int32_t* block_table,
+                      const int32_t* dst_block_table, const int32_t* ctx_lens, int32_t R, int32_t Hkv, int32_t d,
+                      ra_dtype dt, int32_t block_size, int32_t interleave, int32_t pcp, int32_t dcp,
+                      int32_t max_vblocks, int32_t dst_max_vblocks, int64_t num_blocks, int32_t keep,
+                      int32_t n_sink, int32_t n_recent, int32_t* kept, int32_t* new_lens, ra_stream stream);
 
 /* ------------------------------------------------------------------------
  * ra_cp_decode_noalloc -- ra_cp_decode for callers that cannot allocate
