@@ -1,90 +1,974 @@
 // Attention of a chunk of new tokens per request over the sharded paged cache.
 //
-// Simple form: one warp per (query, head) runs the softmax over the visible
-// tokens in one pass, with a running maximum and sum in fp32.
-#include <math_constants.h>
-
+// Mathematics.  O_i = sum_x e^{s_ix} v_x / sum_x e^{s_ix} over the visible
+// tokens x, in one pass with a running maximum m and sum l per row; a context
+// that several CTAs share is joined from their (m, l, O) with weights 2^{m - M}.
+//
+// Rows.  The G query heads of a K/V head read the same keys, so a tile of 128
+// rows holds floor(128/G) tokens with all their G heads (one TMA box of Q).
+// Two score tiles ("slots") are in flight per CTA so that one slot's softmax
+// runs while the tensor core serves the other:
+//   pair   the request has more rows than one tile: the slots are two row
+//          tiles, and every K/V tile feeds both (tensor-bound, 2 x 128 rows
+//          per K/V byte);
+//   split  one row tile (single tokens, drafts): the slots take alternate K/V
+//          tiles, each with its own running (m, l, O), joined at the end from
+//          tensor memory (HBM-bound: a K/V tile of 64 KB takes the SM's share of
+//          HBM bandwidth about 1.45 us, one slot's chain of score product, softmax
+//          and P.V about 1.3 us, two of them half of that).
+//
+// Keys.  The cache is read where it lies: a "unit" is u consecutive slots of a
+// block on one device (u = 16, 32 or 64, a divisor of the block size), one TMA
+// box per 64 columns; units are ordered by virtual block, slot, device, so that
+// a prefix of the units covers a prefix of the context up to one interleave
+// group, and a tile is 128/u units.  Within a unit positions grow with the
+// slot, so every mask is a prefix per unit.  V rows of slots past the context
+// (which may hold NaN) are zeroed in shared memory by a warp of their own in
+// the tiles that have any; units of a bad block are read out of bounds, which
+// TMA fills with zeros.
+//
+// Work.  The keys that all row tiles of all heads and requests meet are laid
+// out on one axis of cost, cut into equal parts, one per CTA (152): long and
+// short contexts, prompts and single tokens balance without any plan from the
+// host.  A part starts or ends inside at most two row tiles; their partial
+// (m, l, O) go to the workspace (at most two per CTA) and a second small kernel
+// joins them.
+//
+// Roles (384 threads): warp 0 TMA, warp 1 MMA issue, warp 2 zeroing of dead V
+// rows, warps 4-7 and 8-11 softmax of slots 0 and 1.
+// Tensor memory: S_h = columns [128h, +128) with P_h (bf16) over its first 64,
+// O_h = columns [256 + 128h, +D).
 #include <algorithm>
 
+#include "ra_attn_tc.cuh"
 #include "ra_paged.cuh"
 
 RA_DEFINE_ERROR_FETCH(fetch_error_chunk_attn)
 
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kCtas = 152;         // parts of the work, one CTA per SM of a GB300
+constexpr int kChunkThreads = 384;
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRowBlocks = 8;
 
-struct ChunkParams {
-  const __nv_bfloat16 *q, *kc, *vc;
+struct ChunkArgs {
   const int32_t *qsl, *ctx;
   Paged c;
   int64_t T;
-  int R, Hq, G, causal;
+  int R, Hq, G, causal, out_bf16;
+  int u, upt, nsub;               // slots of a unit, units of a tile, units of a block
+  int tpt;                        // tokens of a row tile
   float scale_log2;
-  void* o;
-  float* lse;
+  void* o;                        // [T, Hq, D]
+  float* lse;                     // [T, Hq] or NULL
+  float* o_part;                  // [2 * kCtas][256][D]
+  float2* ml_part;                // [2 * kCtas][256]
+  long long wait_limit;
 };
 
-// Largest r with qsl[r] <= t, of requests 0 .. R-1.
-__device__ __forceinline__ int request_of(const int32_t* __restrict__ qsl, int R, int64_t t) {
-  int lo = 0, hi = R - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(qsl[mid]) <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
+// ------------------------------------------------------------------ work
+// A request as the work division sees it.  Costs are in keys times a factor:
+// a pair tile takes about 5/4 of the time of a split tile.
+struct Req {
+  int r, q0, n, L, items;         // request, first query row, queries, context, row tiles (pairs of them) per head
+  long long pos0;                 // position of query 0
+  long long base, slope, f;       // cost of item k: f * (base + slope * (k + 1))
+  bool pair;
+  __device__ long long prefix(long long k) const { return f * (k * base + slope * (k * (k + 1) / 2)); }
+};
+
+constexpr long long kItemOverhead = 192;  // keys: prologue and epilogue of a row tile
+constexpr long long kMinShare = 4 * 256;  // cost of the smallest part of a CTA
+
+__device__ __forceinline__ Req load_req(const ChunkArgs& a, int r) {
+  Req q;
+  q.r = r;
+  query_range(a.qsl, r, a.T, q.q0, q.n, 510);
+  const int32_t ctx = a.ctx[r];
+  q.L = paged_len(a.c, ctx, 511);
+  q.pos0 = static_cast<long long>(ctx) - q.n;
+  q.pair = q.n > a.tpt;
+  const int tpi = q.pair ? 2 * a.tpt : a.tpt;
+  q.items = (q.n + tpi - 1) / tpi;
+  const long long before = q.pos0 < 0 ? 0 : (q.pos0 < q.L ? q.pos0 : q.L);
+  q.base = kItemOverhead + (a.causal ? before : q.L);
+  q.slope = a.causal ? tpi : 0;
+  q.f = q.pair ? 5 : 4;
+  return q;
 }
 
-template <int D, bool OUT_BF16>
-__global__ void __launch_bounds__(256) chunk_simple_kernel(const ChunkParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (blockIdx.x == 0) {
-    int a, b;
-    for (int i = threadIdx.x; i < p.R; i += blockDim.x) query_range(p.qsl, i, p.T, a, b, 500);
-  }
-  if (row >= p.T * p.Hq) return;
-  const int64_t t = row / p.Hq;
-  const int h = static_cast<int>(row % p.Hq), g = h / p.G;
-  const int r = request_of(p.qsl, p.R, t);
-  int q0, n;
-  query_range(p.qsl, r, p.T, q0, n, 500);
-  if (t < q0 || t >= q0 + n) return;
-  const int L = paged_len(p.c, p.ctx[r], 501);
-  const int64_t last = p.causal ? static_cast<int64_t>(p.ctx[r]) - n + (t - q0) : L - 1;
-  const int seen = static_cast<int>(last + 1 < L ? last + 1 : L);
-  float q[E], acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(p.q[row * D + lane + 32 * e]) * p.scale_log2;
-    acc[e] = 0.f;
-  }
-  float m = -CUDART_INF_F, l = 0.f;
-  for (int x = 0; x < seen; ++x) {
-    const int64_t at = paged_row(p.c, r, x, g, 502);
-    if (at < 0) continue;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += q[e] * __bfloat162float(p.kc[at * D + lane + 32 * e]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float mn = fmaxf(m, s);
-    if (mn == -CUDART_INF_F) continue;
-    const float a = exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    l = l * a + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * __bfloat162float(p.vc[at * D + lane + 32 * e]);
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if (OUT_BF16) static_cast<__nv_bfloat16*>(p.o)[row * D + lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
-    else static_cast<float*>(p.o)[row * D + lane + 32 * e] = acc[e] * inv;
-  }
-  if (p.lse && lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+// Visible tokens of query i: positions below the returned value.
+__device__ __forceinline__ int limit_of(const ChunkArgs& a, const Req& q, int i) {
+  if (!a.causal) return q.L;
+  const long long lim = q.pos0 + i + 1;
+  return lim < 0 ? 0 : (lim < q.L ? static_cast<int>(lim) : q.L);
 }
+
+// Units that hold a token below lim: a prefix of the units.
+__device__ __forceinline__ int units_below(const ChunkArgs& a, int lim) {
+  if (lim <= 0) return 0;
+  const int vb = lim / a.c.V, o = lim - vb * a.c.V;
+  int k = vb * a.nsub * a.c.W;
+  if (o > 0) {
+    const int p = a.c.W * a.c.I, q = (o - 1) / p, rem = (o - 1) - q * p;
+    const int sub = (q * a.c.I + min(rem, a.c.I - 1)) / a.u;   // last unit row with a token below
+    const int s0 = sub * a.u, first = (s0 / a.c.I) * p + s0 % a.c.I;
+    k += sub * a.c.W + min(a.c.W, (o - first + a.c.I - 1) / a.c.I);
+  }
+  return k;
+}
+
+// Units from the start all of whose tokens are below lim.
+__device__ __forceinline__ int units_within(const ChunkArgs& a, int lim) {
+  const int vb = lim / a.c.V, o = lim - vb * a.c.V;
+  return (vb * a.nsub + (o / (a.c.W * a.c.I)) * a.c.I / a.u) * a.c.W;
+}
+
+__device__ __forceinline__ int tiles_of(const ChunkArgs& a, const Req& q, int k) {
+  const int tpi = q.pair ? 2 * a.tpt : a.tpt;
+  const int last = min(q.n, (k + 1) * tpi) - 1;
+  return (units_below(a, limit_of(a, q, last)) + a.upt - 1) / a.upt;
+}
+
+// Tiles [t0, t1) of an item of nt tiles and cost [at, at + cost) that part [lo, hi) takes.
+__device__ __forceinline__ void cut(long long lo, long long hi, long long at, long long cost, int nt, int& t0, int& t1) {
+  t0 = lo <= at ? 0 : static_cast<int>((lo - at) * nt / cost);
+  t1 = hi >= at + cost ? nt : static_cast<int>((hi - at) * nt / cost);
+}
+
+struct Plan {
+  long long total;
+  int parts;
+  __device__ long long lo(int c) const { return total / parts * c + total % parts * c / parts; }
+};
+
+// The total cost, and the request that holds cost position `lo_of(plan)` with the cost
+// before it, found by all NT threads of the block (smem scratch).
+template <int NT>
+struct PlanScratch {
+  long long warp_sum[NT / 32];
+  long long pre;
+  int r;
+};
+template <int NT>
+__device__ __forceinline__ long long block_scan(long long v, PlanScratch<NT>& s, long long& sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s.warp_sum[warp] = x;
+  __syncthreads();
+  long long before = 0;
+  sum = 0;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) {
+    const long long w = s.warp_sum[i];
+    if (i < warp) before += w;
+    sum += w;
+  }
+  return before + x - v;
+}
+template <int NT>
+__device__ __forceinline__ void make_plan(const ChunkArgs& a, int part, PlanScratch<NT>& s, Plan& plan, int& r,
+                                          long long& pre) {
+  long long total = 0, mine = 0, cost = 0, sum;
+  for (int base = 0; base < a.R; base += NT) {
+    const int i = base + threadIdx.x;
+    cost = 0;
+    if (i < a.R) {
+      const Req q = load_req(a, i);
+      cost = a.c.Hkv * q.prefix(q.items);
+    }
+    mine = total + block_scan<NT>(cost, s, sum);
+    total += sum;
+  }
+  plan.total = total;
+  const long long most = total / kMinShare;
+  plan.parts = most < 1 ? 1 : (most < kCtas ? static_cast<int>(most) : kCtas);
+  if (threadIdx.x == 0) s.r = -1;
+  __syncthreads();
+  if (part < plan.parts && total > 0) {
+    const long long lo = plan.lo(part);
+    long long at = 0;
+    for (int base = 0; base < a.R; base += NT) {
+      const int i = base + threadIdx.x;
+      if (a.R > NT) {
+        cost = 0;
+        if (i < a.R) {
+          const Req q = load_req(a, i);
+          cost = a.c.Hkv * q.prefix(q.items);
+        }
+        mine = at + block_scan<NT>(cost, s, sum);
+        at += sum;
+      }
+      if (cost > 0 && mine <= lo && lo < mine + cost) {
+        s.r = i;
+        s.pre = mine;
+      }
+    }
+  }
+  __syncthreads();
+  r = s.r;
+  pre = s.pre;
+}
+
+// One row tile (pair) of a part: K/V tiles [t0, t1) of nt.
+struct Segment {
+  Req q;
+  int g, k, nt, t0, t1;
+};
+
+// Walks the items of part [lo, hi) in order; every role runs its own.
+struct SegIter {
+  const ChunkArgs& a;
+  long long lo, hi, at;
+  Req q;
+  int r, g, k;
+  bool live;
+  __device__ SegIter(const ChunkArgs& args, const Plan& plan, int part, int r0, long long pre) : a(args) {
+    lo = plan.lo(part);
+    hi = plan.lo(part + 1);
+    r = r0;
+    live = r0 >= 0;
+    if (!live) return;
+    q = load_req(a, r);
+    const long long per_head = q.prefix(q.items);
+    g = static_cast<int>((lo - pre) / per_head);
+    const long long off = lo - pre - g * per_head;
+    int x = 0, y = q.items - 1;   // largest k with prefix(k) <= off
+    while (x < y) {
+      const int mid = (x + y + 1) >> 1;
+      if (q.prefix(mid) <= off) x = mid; else y = mid - 1;
+    }
+    k = x;
+    at = pre + g * per_head + q.prefix(k);
+  }
+  // The next segment of the part that has tiles, or an item that sees nothing; false at the end.
+  __device__ bool next(Segment& s) {
+    while (live && at < hi) {
+      const long long cost = q.f * (q.base + q.slope * (k + 1));
+      s.q = q;
+      s.g = g;
+      s.k = k;
+      s.nt = tiles_of(a, q, k);
+      cut(lo, hi, at, cost, s.nt, s.t0, s.t1);
+      const bool mine = s.nt == 0 ? lo <= at : s.t1 > s.t0;
+      at += cost;
+      if (++k == q.items) {
+        k = 0;
+        if (++g == a.c.Hkv) {
+          g = 0;
+          do {
+            if (++r >= a.R) { live = false; break; }
+            q = load_req(a, r);
+          } while (q.items == 0);
+        }
+      }
+      if (mine) return true;
+    }
+    return false;
+  }
+};
+
+// ------------------------------------------------------------------ softmax
+// One online-softmax step of the row at tensor-memory address s_addr; as
+// softmax_row, with the mask given as a functor on 32-column chunks, and rows
+// that are not in use (their scores may be NaN) left out of the votes.
+template <class Mask>
+__device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool masked, bool row_ok, const Mask& mask,
+                                              float scale, float& m, float& l, uint32_t (&pk)[BN / 2]) {
+  const uint64_t sc2 = f2pack(scale, scale);
+  if (!first) {
+    const uint64_t negm2 = f2pack(-m, -m);
+    bool grow = __any_sync(0xffffffffu, row_ok && m == -CUDART_INF_F);
+    float lsum = 0.f;
+    uint32_t xa[32], xb[32];
+    tmem_ld32(s_addr, xa);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < BN / 32; ++c) {
+      if (grow) break;
+      uint32_t (&x)[32] = (c & 1) ? xb : xa;
+      uint32_t (&y)[32] = (c & 1) ? xa : xb;
+      if (c + 1 < BN / 32) tmem_ld32(s_addr + 32 * (c + 1), y);
+      if (masked) mask(x, c);
+      uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+      chunk_exp_pack(x, sc2, negm2, acc0, acc1, &pk[16 * c]);
+      float a0, a1, b0, b1;
+      f2unpack(acc0, a0, a1);
+      f2unpack(acc1, b0, b1);
+      const float cs = (a0 + a1) + (b0 + b1);
+      if (__any_sync(0xffffffffu, row_ok && !(cs <= kChunkSumLimit))) { grow = true; tmem_wait_ld(); break; }
+      lsum += cs;
+      if (c + 1 < BN / 32) tmem_wait_ld();
+    }
+    if (!grow) {
+      l += lsum;
+      return 1.f;
+    }
+  }
+  float mx = -CUDART_INF_F;
+#pragma unroll
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t x[32];
+    tmem_ld32(s_addr + 32 * c, x);
+    tmem_wait_ld();
+    if (masked) mask(x, c);
+    mx = fmaxf(mx, chunk_mask_max(x, 32 * c, false, 0));
+  }
+  const float m_tile = mx * scale;
+  const bool need = first || (m_tile > m + 8.f);
+  const float m_use = need ? fmaxf(m, m_tile) : m;
+  const float m_ref = (m_use == -CUDART_INF_F) ? 0.f : m_use;
+  const float alpha = first ? 0.f : ex2(m - m_ref);
+  const uint64_t negm2 = f2pack(-m_ref, -m_ref);
+  uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t x[32];
+    tmem_ld32(s_addr + 32 * c, x);
+    tmem_wait_ld();
+    if (masked) mask(x, c);
+    chunk_exp_pack(x, sc2, negm2, acc0, acc1, &pk[16 * c]);
+  }
+  float a0, a1, b0, b1;
+  f2unpack(acc0, a0, a1);
+  f2unpack(acc1, b0, b1);
+  const float rs = (a0 + a1) + (b0 + b1);
+  l = first ? rs : l * alpha + rs;
+  m = m_use;
+  return first ? 1.f : alpha;
+}
+
+// Visible slots (a prefix, 0..u) of unit `unit` for a row that sees positions below lim.
+__device__ __forceinline__ int unit_visible(const ChunkArgs& a, int64_t r_row, bool check, int unit, int lim) {
+  const int per_vb = a.nsub * a.c.W;
+  const int vb = unit / per_vb, rem = unit - vb * per_vb;
+  const int sub = rem / a.c.W, w = rem - sub * a.c.W;
+  const int y = lim - vb * a.c.V - w * a.c.I;
+  if (y <= 0) return 0;
+  if (check) {  // some block of this CTA's work was bad: leave out its tokens
+    const int32_t b = vb < a.c.max_vb ? a.c.table[r_row * a.c.max_vb + vb] : -1;
+    if (b < 0 || b >= a.c.num_blocks) return 0;
+  }
+  const int p = a.c.W * a.c.I, q = y / p;
+  return max(0, min(a.u, q * a.c.I + min(y - q * p, a.c.I) - sub * a.u));
+}
+
+// ------------------------------------------------------------------ the kernel
+template <int D>
+constexpr int kStages = D == 128 ? 5 : 8;   // K/V tiles in flight (32 or 16 KB each)
+
+template <int D>
+struct __align__(1024) ChunkSmem {
+  uint8_t q[2][BM * D * 2];
+  uint8_t kv[kStages<D>][BN * D * 2];
+  uint64_t q_full[2], q_empty[2], kv_full[kStages<D>], kv_empty[kStages<D>], v_dirty[kStages<D>], v_clean[kStages<D>];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2], ml_full, ml_empty, drain;
+  float2 ml[BM];
+  PlanScratch<kChunkThreads> plan;
+  uint32_t tmem_base;
+  int abort_flag, bad_block;
+};
+
+// mbar_wait by a whole warp with one outcome for all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit, int site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit, site));
+}
+
+template <int NS>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ void advance() {
+    if (++st == NS) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ChunkArgs a) {
+  constexpr int SLABS = D / 64, NS = kStages<D>;
+  constexpr uint32_t kTileBytes = BM * D * 2;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(BM, BN, 0, 0);
+  constexpr uint32_t kIdescO = idesc_bf16_f32(BM, D, 0, 1);
+
+  extern __shared__ uint8_t smem_raw[];
+  ChunkSmem<D>& sm = *reinterpret_cast<ChunkSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sm.abort_flag;
+  const long long lim = a.wait_limit;
+
+  Plan plan;
+  int r0;
+  long long pre;
+  make_plan<kChunkThreads>(a, blockIdx.x, sm.plan, plan, r0, pre);
+  if (r0 < 0) return;   // no work for this CTA
+
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&sm.q_full[b]), 1);
+      mbar_init(smem_u32(&sm.q_empty[b]), 1);
+      mbar_init(smem_u32(&sm.s_full[b]), 1);
+      mbar_init(smem_u32(&sm.p_full[b]), 128);
+      mbar_init(smem_u32(&sm.pv_done[b]), 1);
+      mbar_init(smem_u32(&sm.o_empty[b]), 128);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(smem_u32(&sm.kv_full[s]), 1);
+      mbar_init(smem_u32(&sm.kv_empty[s]), 1);
+      mbar_init(smem_u32(&sm.v_dirty[s]), 1);
+      mbar_init(smem_u32(&sm.v_clean[s]), 1);
+    }
+    mbar_init(smem_u32(&sm.ml_full), 128);
+    mbar_init(smem_u32(&sm.ml_empty), 128);
+    mbar_init(smem_u32(&sm.drain), 1);
+    sm.abort_flag = 0;
+    sm.bad_block = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sm.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  SegIter it(a, plan, blockIdx.x, r0, pre);
+  Segment sg;
+
+  // Order of the K/V ring in a segment: K_0 .. K_{la-1}, then V_j, K_{j+la} for each j, with la = 1
+  // (pair: both slots meet tile j) or 2 (split: slot j & 1 meets tile j).
+  if (warp == 0) {
+    // ============================================================ TMA producer (whole warp: a unit per lane)
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    Ring<NS> ring;
+    uint32_t issued = 0;                      // ring entries so far
+    uint32_t q_cnt[2] = {0, 0};
+    int q_next = 0;
+    bool ok = true;
+    const int per_vb = a.nsub * a.c.W;
+    const int oob = static_cast<int>(a.c.W * a.c.num_blocks * a.c.Hkv);   // past the last block: zero fill
+    while (ok && it.next(sg)) {
+      const int nt = sg.t1 - sg.t0;
+      if (nt <= 0) continue;
+      const int la = sg.q.pair ? 1 : 2, nq = sg.q.pair ? 2 : 1;
+      const int dirty = units_within(a, sg.q.L) / a.upt - sg.t0;   // first tile with slots past the context
+      for (int h = 0; h < nq && ok; ++h) {
+        const int b = sg.q.pair ? h : q_next;
+        ok = warp_wait(smem_u32(&sm.q_empty[b]), (q_cnt[b] & 1) ^ 1, abort_flag, lim, 520);
+        if (!ok) break;
+        ++q_cnt[b];
+        if (lane == 0) {
+          const uint32_t qb = smem_u32(&sm.q_full[b]);
+          mbar_arrive_expect_tx(qb, SLABS * a.tpt * a.G * 128);
+          const int row = sg.q.q0 + (nq * sg.k + h) * a.tpt;
+          for (int s = 0; s < SLABS; ++s)
+            tma_load_3d(smem_u32(sm.q[b] + s * BM * 128), &tmQ, qb, 64 * s, sg.g * a.G, row);
+        }
+        __syncwarp();
+      }
+      if (!sg.q.pair) q_next ^= 1;
+      auto load_tile = [&](const CUtensorMap* map, int blk, int s0, int w, bool to_clean) -> bool {
+        if (!warp_wait(smem_u32(&sm.kv_empty[ring.st]), ring.ph ^ 1, abort_flag, lim, 521)) return false;
+        const uint32_t bar = smem_u32(&sm.kv_full[ring.st]);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, kTileBytes);
+          if (to_clean) mbar_arrive(smem_u32(&sm.v_dirty[ring.st]));
+        }
+        __syncwarp();
+        if (lane < a.upt) {
+          const int hb = blk < 0 ? oob : static_cast<int>((w * a.c.num_blocks + blk) * a.c.Hkv + sg.g);
+          for (int s = 0; s < SLABS; ++s)
+            tma_load_3d(smem_u32(sm.kv[ring.st] + s * BN * 128 + lane * a.u * 128), map, bar, 64 * s, s0, hb);
+        }
+        ++issued;
+        ring.advance();
+        return true;
+      };
+      // lane's unit of tile j: device, slot, block (-1: past the table or bad)
+      auto locate = [&](int j, int& blk, int& s0, int& w) {
+        const int unit = (sg.t0 + j) * a.upt + lane;
+        const int vb = unit / per_vb, rem = unit - vb * per_vb, sub = rem / a.c.W;
+        w = rem - sub * a.c.W;
+        s0 = sub * a.u;
+        blk = -1;
+        if (lane < a.upt && static_cast<int64_t>(vb) * a.c.V < sg.q.L) {
+          blk = a.c.table[static_cast<int64_t>(sg.q.r) * a.c.max_vb + vb];
+          if (blk < 0 || blk >= a.c.num_blocks) {
+            ra_record_error(RA_ERR_DEVICE_BOUNDS, 512);
+            *reinterpret_cast<volatile int*>(&sm.bad_block) = 1;
+            blk = -1;
+          }
+        }
+        __syncwarp();
+      };
+      // the blocks of K tile j + la are looked up while tile j + la - 1 is waited for, and kept for its V
+      int bk[3], sk[3], wk[3];
+      for (int j = 0; j < la && j < nt && ok; ++j) {
+        locate(j, bk[j], sk[j], wk[j]);
+        ok = load_tile(&tmK, bk[j], sk[j], wk[j], false);
+      }
+      for (int j = 0; j < nt && ok; ++j) {
+        if (j + la < nt) locate(j + la, bk[la], sk[la], wk[la]);
+        if (!(ok = load_tile(&tmV, bk[0], sk[0], wk[0], j >= dirty))) break;
+        if (j + la < nt && !(ok = load_tile(&tmK, bk[la], sk[la], wk[la], false))) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          bk[i] = bk[i + 1];
+          sk[i] = sk[i + 1];
+          wk[i] = wk[i + 1];
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      // let the copies already in flight land before the CTA exits: the last load of each buffer
+      for (int b = 0; b < 2; ++b)
+        if (q_cnt[b]) mbar_wait_quiesce(smem_u32(&sm.q_full[b]), (q_cnt[b] - 1) & 1, 1 << 22);
+      for (int s = 0; s < NS; ++s) {
+        const uint32_t n = issued / NS + (static_cast<uint32_t>(s) < issued % NS ? 1 : 0);
+        if (n) mbar_wait_quiesce(smem_u32(&sm.kv_full[s]), (n - 1) & 1, 1 << 22);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ============================================================ MMA issuer
+    if (lane == 0) {
+      Ring<NS> ring;
+      uint32_t pf[2] = {0, 0}, q_cnt[2] = {0, 0}, seg = 0, clean_ph = 0;
+      int q_next = 0;
+      bool ok = true;
+      const uint64_t dq0 = desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+      const uint64_t dk0 = desc_sw128(smem_u32(sm.kv[0]), 16, 1024);
+      const uint64_t dv0 = desc_sw128(smem_u32(sm.kv[0]), BN * 128, 1024);
+      auto issue_s = [&](int h, int b, int st) {
+        const uint64_t dq = dq0 + b * (kTileBytes >> 4), dk = dk0 + st * (kTileBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+          mma_bf16_ss(tmem + h * BN, dq + off16, dk + off16, kIdescS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(smem_u32(&sm.s_full[h]));
+      };
+      auto issue_pv = [&](int h, int st, bool first) {
+        const uint64_t dv = dv0 + st * (kTileBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_bf16_ts(tmem + kColO + h * BN, tmem + h * BN + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdescO,
+                      (kk > 0 || !first) ? 1u : 0u);
+        mma_commit(smem_u32(&sm.pv_done[h]));
+      };
+      // the V tile at the ring's head is in place, its dead rows zeroed
+      auto wait_v = [&](int j, int dirty) -> bool {
+        if (!mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 531)) return false;
+        if (j >= dirty) {
+          if (!mbar_wait(smem_u32(&sm.v_clean[ring.st]), (clean_ph >> ring.st) & 1, abort_flag, lim, 532)) return false;
+          clean_ph ^= 1u << ring.st;
+        }
+        return true;
+      };
+      while (ok && it.next(sg)) {
+        const int nt = sg.t1 - sg.t0;
+        if (nt <= 0) continue;
+        const int dirty = units_within(a, sg.q.L) / a.upt - sg.t0;   // first tile with slots past the context
+        const bool pair = sg.q.pair;
+        const int qb = pair ? 0 : q_next;
+        if (!(ok = mbar_wait(smem_u32(&sm.q_full[qb]), q_cnt[qb] & 1, abort_flag, lim, 530))) break;
+        ++q_cnt[qb];
+        if (pair) {
+          if (!(ok = mbar_wait(smem_u32(&sm.q_full[1]), q_cnt[1] & 1, abort_flag, lim, 530))) break;
+          ++q_cnt[1];
+        } else {
+          q_next ^= 1;
+        }
+        auto q_release = [&] {
+          mma_commit(smem_u32(&sm.q_empty[qb]));
+          if (pair) mma_commit(smem_u32(&sm.q_empty[1]));
+        };
+        const uint32_t oph = (seg & 1) ^ 1;
+        if (pair) {
+          if (!(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 533))) break;
+          tc_fence_after();
+          issue_s(0, 0, ring.st);
+          issue_s(1, 1, ring.st);
+          mma_commit(smem_u32(&sm.kv_empty[ring.st]));
+          ring.advance();
+          if (nt == 1) q_release();
+          for (int j = 0; j < nt; ++j) {
+            const bool more = j + 1 < nt;
+            if (!(ok = wait_v(j, dirty))) break;
+            const int sv = ring.st;
+            ring.advance();
+            if (more && !(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 534))) break;
+            if (j == 0 && !(ok = mbar_wait(smem_u32(&sm.o_empty[0]), oph, abort_flag, lim, 535))) break;
+            if (j == 0 && !(ok = mbar_wait(smem_u32(&sm.o_empty[1]), oph, abort_flag, lim, 536))) break;
+            if (!(ok = mbar_wait(smem_u32(&sm.p_full[0]), pf[0] & 1, abort_flag, lim, 537))) break;
+            ++pf[0];
+            tc_fence_after();
+            issue_pv(0, sv, j == 0);
+            if (more) issue_s(0, 0, ring.st);
+            if (!(ok = mbar_wait(smem_u32(&sm.p_full[1]), pf[1] & 1, abort_flag, lim, 538))) break;
+            ++pf[1];
+            tc_fence_after();
+            issue_pv(1, sv, j == 0);
+            mma_commit(smem_u32(&sm.kv_empty[sv]));
+            if (more) {
+              issue_s(1, 1, ring.st);
+              mma_commit(smem_u32(&sm.kv_empty[ring.st]));
+              ring.advance();
+              if (j + 2 == nt) q_release();
+            }
+          }
+        } else {
+          for (int j = 0; j < 2 && j < nt; ++j) {
+            if (!(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 533))) break;
+            tc_fence_after();
+            issue_s(j, qb, ring.st);
+            mma_commit(smem_u32(&sm.kv_empty[ring.st]));
+            ring.advance();
+          }
+          if (!ok) break;
+          if (nt <= 2) q_release();
+          for (int j = 0; j < nt; ++j) {
+            const int h = j & 1;
+            const bool more = j + 2 < nt;
+            if (!(ok = wait_v(j, dirty))) break;
+            const int sv = ring.st;
+            ring.advance();
+            if (more && !(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 534))) break;
+            if (j < 2 && !(ok = mbar_wait(smem_u32(&sm.o_empty[h]), oph, abort_flag, lim, 535))) break;
+            if (!(ok = mbar_wait(smem_u32(&sm.p_full[h]), pf[h] & 1, abort_flag, lim, 537))) break;
+            ++pf[h];
+            tc_fence_after();
+            issue_pv(h, sv, j < 2);
+            mma_commit(smem_u32(&sm.kv_empty[sv]));
+            if (more) {
+              issue_s(h, qb, ring.st);
+              mma_commit(smem_u32(&sm.kv_empty[ring.st]));
+              ring.advance();
+              if (j + 3 == nt) q_release();
+            }
+          }
+        }
+        ++seg;
+      }
+      mma_commit(smem_u32(&sm.drain));
+      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, ok ? lim : (1 << 22)) && ok) {
+        *abort_flag = 1;
+        ra_record_error(RA_ERR_TIMEOUT, 539);
+      }
+    }
+  } else if (warp == 2) {
+    // ============================================================ zeroing of V rows past the context
+    // A dirty tile is taken up once the producer has announced it: from then on its stage's barrier can
+    // only move from loading to loaded, so that the parity waited for is the right one.
+    Ring<NS> ring;
+    uint32_t dirty_ph = 0;
+    bool ok = true;
+    while (ok && it.next(sg)) {
+      const int nt = sg.t1 - sg.t0;
+      if (nt <= 0) continue;
+      const int la = sg.q.pair ? 1 : 2;
+      const int dirty = units_within(a, sg.q.L) / a.upt - sg.t0;
+      for (int j = 0; j < min(la, nt); ++j) ring.advance();
+      for (int j = 0; j < nt; ++j) {
+        if (j >= dirty) {
+          if (!(ok = warp_wait(smem_u32(&sm.v_dirty[ring.st]), (dirty_ph >> ring.st) & 1, abort_flag, lim, 540))) break;
+          dirty_ph ^= 1u << ring.st;
+          if (!(ok = warp_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 541))) break;
+          for (int i = lane; i < BN; i += 32) {
+            const int unit = (sg.t0 + j) * a.upt + i / a.u;
+            if (i % a.u >= unit_visible(a, sg.q.r, false, unit, sg.q.L)) {
+#pragma unroll
+              for (int s = 0; s < SLABS; ++s)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  *reinterpret_cast<uint4*>(sm.kv[ring.st] + s * BN * 128 + i * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.v_clean[ring.st]));
+          __syncwarp();
+        }
+        ring.advance();
+        if (j + la < nt) ring.advance();
+      }
+    }
+  } else if (warp >= 4) {
+    // ============================================================ softmax + epilogue (slot h)
+    const int h = (warp - 4) >> 2;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t colS = h * BN, colO = kColO + h * BN;
+    const int row_tok = row / a.G, row_head = row - row_tok * a.G;
+    uint32_t s_cnt = 0, pv_cnt[2] = {0, 0}, splits = 0;
+    bool ok = true;
+    while (ok && it.next(sg)) {
+      const int nt = sg.t1 - sg.t0;
+      const bool pair = sg.q.pair;
+      const int tok = (pair ? 2 * sg.k + h : sg.k) * a.tpt + row_tok;
+      const bool row_ok = row_tok < a.tpt && tok < sg.q.n;
+      const int64_t orow = static_cast<int64_t>(sg.q.q0 + tok) * a.Hq + sg.g * a.G + row_head;
+      if (nt <= 0) {   // the tile sees nothing
+        if (row_ok && (pair || h == 0)) {
+          for (int e = 0; e < D; e += 8) {
+            if (a.out_bf16) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + orow * D + e) = make_uint4(0, 0, 0, 0);
+            else {
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * D + e);
+              dst[0] = dst[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
+          if (a.lse) a.lse[orow] = -CUDART_INF_F;
+        }
+        continue;
+      }
+      // visible positions of this row, and the first tile in which the slot's first row sees a part only
+      const int vis = limit_of(a, sg.q, min(tok, sg.q.n - 1));
+      const int first_tok = min((pair ? 2 * sg.k + h : sg.k) * a.tpt, sg.q.n - 1);
+      const int clean = units_within(a, limit_of(a, sg.q, first_tok)) / a.upt;
+      const bool warp_live = __any_sync(0xffffffffu, row_ok);
+      float m = -CUDART_INF_F, l = 0.f;
+      const int step = pair ? 1 : 2;
+      int n_mine = 0;                      // tiles of this slot so far
+      for (int j = pair ? 0 : h; j < nt; j += step) {
+        if (!(ok = warp_wait(smem_u32(&sm.s_full[h]), s_cnt & 1, abort_flag, lim, 550 + h))) break;
+        ++s_cnt;
+        tc_fence_after();
+        if (warp_live) {
+          const bool bad = *reinterpret_cast<volatile int*>(&sm.bad_block) != 0;
+          const int tile = sg.t0 + j;
+          auto mask = [&](uint32_t (&x)[32], int c) {
+            // visible columns of each 16 of the chunk: a prefix of its unit
+            int lim16[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int col = 32 * c + 16 * q, ui = col / a.u;
+              lim16[q] = unit_visible(a, sg.q.r, bad, tile * a.upt + ui, vis) - (col - ui * a.u);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((i & 15) >= lim16[i >> 4]) x[i] = __float_as_uint(-CUDART_INF_F);
+          };
+          uint32_t pk[BN / 2];
+          const float alpha = softmax_step(t_lane + colS, n_mine == 0, tile >= clean || bad, row_ok, mask, a.scale_log2, m, l, pk);
+          if (n_mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // O_h must hold the previous P.V before it is rescaled
+            if (!(ok = warp_wait(smem_u32(&sm.pv_done[h]), (pv_cnt[h] + n_mine - 1) & 1, abort_flag, lim, 552 + h))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c4 = 0; c4 < D / 32; ++c4) {
+              uint32_t orr[32];
+              tmem_ld32(t_lane + colO + 32 * c4, orr);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) * alpha);
+              tmem_st32(t_lane + colO + 32 * c4, orr);
+            }
+          }
+          tmem_st32(t_lane + colS, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+          tmem_st32(t_lane + colS + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+          tmem_wait_st();
+        }
+        ++n_mine;
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sm.p_full[h]));
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- epilogue
+      const bool whole = nt == sg.nt;
+      const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (sg.t0 == 0 ? 1 : 0);
+      pv_cnt[0] += pair ? nt : (nt + 1) / 2;   // both slots' products so far, whichever this thread waits for
+      pv_cnt[1] += pair ? nt : nt / 2;
+      if (!pair && h == 1) {
+        // hand (m, l) to slot 0, which joins the two accumulators
+        if (!(ok = warp_wait(smem_u32(&sm.ml_empty), (splits & 1) ^ 1, abort_flag, lim, 560))) break;
+        sm.ml[row] = make_float2(n_mine ? m : -CUDART_INF_F, n_mine ? l : 0.f);
+        mbar_arrive(smem_u32(&sm.ml_full));
+        ++splits;
+        continue;
+      }
+      if (!(ok = warp_wait(smem_u32(&sm.pv_done[h]), (pv_cnt[h] - 1) & 1, abort_flag, lim, 554 + h))) break;
+      float f0 = 1.f, f1 = 0.f;
+      bool two = false;
+      if (!pair) {
+        if (!(ok = warp_wait(smem_u32(&sm.ml_full), splits & 1, abort_flag, lim, 561))) break;
+        ++splits;
+        const float2 ml1 = sm.ml[row];
+        mbar_arrive(smem_u32(&sm.ml_empty));
+        two = nt > 1;
+        if (two && !(ok = warp_wait(smem_u32(&sm.pv_done[1]), (pv_cnt[1] - 1) & 1, abort_flag, lim, 556))) break;
+        const float M = fmaxf(m, ml1.x);
+        f0 = M == -CUDART_INF_F ? 0.f : ex2(m - M);
+        f1 = M == -CUDART_INF_F ? 0.f : ex2(ml1.x - M);
+        l = l * f0 + ml1.y * f1;
+        m = M;
+      }
+      tc_fence_after();
+      const float inv_l = !whole ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+      f0 *= inv_l;
+      f1 *= inv_l;
+      if (warp_live) {
+        float* po = a.o_part + ((part * 2 + (pair ? h : 0)) * BM + row) * D;
+#pragma unroll
+        for (int c4 = 0; c4 < D / 32; ++c4) {
+          uint32_t x[32];
+          tmem_ld32(t_lane + colO + 32 * c4, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f0);
+          if (two) {
+            uint32_t y[32];
+            tmem_ld32(t_lane + kColO + BN + 32 * c4, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(y[i]) * f1);
+          }
+          if (row_ok) {
+            if (whole && a.out_bf16) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + orow * D + 32 * c4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = f2_bf16x2(__uint_as_float(x[8 * i + 2 * e]), __uint_as_float(x[8 * i + 2 * e + 1]));
+                dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>((whole ? static_cast<float*>(a.o) + orow * D : po) + 32 * c4);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sm.o_empty[h]));
+      if (!pair) mbar_arrive(smem_u32(&sm.o_empty[1]));
+      if (row_ok) {
+        if (!whole) a.ml_part[(part * 2 + (pair ? h : 0)) * BM + row] = make_float2(m, l);
+        else if (a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------ joining
+// Row tiles that a boundary between parts cuts: block b takes the tile that holds the boundary
+// between parts b and b + 1, if it is the first boundary inside that tile.  A warp per row.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkArgs a) {
+  constexpr int E = D / 32;
+  __shared__ PlanScratch<kMergeThreads> scratch;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.x + 1;
+  Plan plan;
+  int r;
+  long long pre;
+  make_plan<kMergeThreads>(a, b, scratch, plan, r, pre);
+  if (b >= plan.parts || r < 0) return;
+  SegIter it(a, plan, b, r, pre);
+  // the item at the start of part b
+  const long long at = it.at, cost = it.q.f * (it.q.base + it.q.slope * (it.k + 1));
+  if (plan.lo(b) <= at || plan.lo(b - 1) > at) return;
+  const int nt = tiles_of(a, it.q, it.k);
+  if (nt == 0) return;
+  int last = b, used = 0;
+  for (int c = b - 1; c < plan.parts; ++c) {
+    if (plan.lo(c) >= at + cost) break;
+    int t0, t1;
+    cut(plan.lo(c), plan.lo(c + 1), at, cost, nt, t0, t1);
+    used += t1 > t0;
+    last = c;
+  }
+  if (used <= 1) return;
+  const int slots = it.q.pair ? 2 : 1;
+  for (int i = blockIdx.y * (kMergeThreads / 32) + warp; i < slots * BM; i += gridDim.y * (kMergeThreads / 32)) {
+    const int h = i / BM, row = i % BM, rt = row / a.G;
+    const int tok = (slots * it.k + h) * a.tpt + rt;
+    if (rt >= a.tpt || tok >= it.q.n) continue;
+    float M = -CUDART_INF_F, l = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int c = b - 1; c <= last; ++c) {
+      int t0, t1;
+      cut(plan.lo(c), plan.lo(c + 1), at, cost, nt, t0, t1);
+      if (t1 <= t0) continue;
+      const int64_t p = ((2 * static_cast<int64_t>(c) + (t0 == 0 ? 1 : 0)) * 2 + h) * BM + row;
+      const float2 ml = a.ml_part[p];
+      if (!(ml.y > 0.f)) continue;      // this part saw nothing for the row
+      const float mn = fmaxf(M, ml.x), w0 = ex2(M - mn), w1 = ex2(ml.x - mn);
+      M = mn;
+      l = l * w0 + ml.y * w1;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = acc[e] * w0 + w1 * a.o_part[p * D + lane + 32 * e];
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int64_t orow = static_cast<int64_t>(it.q.q0 + tok) * a.Hq + it.g * a.G + (row - rt * a.G);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (a.out_bf16) static_cast<__nv_bfloat16*>(a.o)[orow * D + lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
+      else static_cast<float*>(a.o)[orow * D + lane + 32 * e] = acc[e] * inv;
+    }
+    if (a.lse && lane == 0) a.lse[orow] = l > 0.f ? (M + log2f(l)) * kLn2 : -CUDART_INF_F;
+  }
+}
+
+// Three-dimensional bf16 map with 64-column boxes in the 128-byte swizzle the MMA descriptors expect.
+ra_status chunk_map(CUtensorMap* map, const void* base, int D, int64_t n1, int64_t n2, uint32_t box1, uint32_t box2) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(n1) * D * 2};
+  cuuint32_t box[3] = {64, box1, box2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return RA_OK;
+}
+
+template <int D>
+ra_status launch_chunk(const void* q, const void* k, const void* v, const ChunkArgs& a, cudaStream_t stream) {
+  CUtensorMap mq, mk, mv;
+  ra_status st;
+  const int64_t blocks = a.c.W * a.c.num_blocks * a.c.Hkv;
+  if ((st = chunk_map(&mq, q, D, a.Hq, a.T, a.G, a.tpt)) != RA_OK) return st;
+  if ((st = chunk_map(&mk, k, D, a.c.bs, blocks, a.u, 1)) != RA_OK) return st;
+  if ((st = chunk_map(&mv, v, D, a.c.bs, blocks, a.u, 1)) != RA_OK) return st;
+  const size_t smem = sizeof(ChunkSmem<D>) + 1024;
+  RA_CUDA_TRY(cudaFuncSetAttribute(chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(smem)));
+  chunk_attn_kernel<D><<<kCtas, kChunkThreads, smem, stream>>>(mq, mk, mv, a);
+  RA_LAUNCH_CHECK("chunk_attn_kernel");
+  chunk_merge_kernel<D><<<dim3(kCtas - 1, kMergeRowBlocks), kMergeThreads, 0, stream>>>(a);
+  RA_LAUNCH_CHECK("chunk_merge_kernel");
+  return RA_OK;
+}
+
+int64_t part_floats(int d) { return static_cast<int64_t>(2 * kCtas) * 2 * BM * d; }
 
 }  // namespace
 
@@ -92,7 +976,7 @@ extern "C" ra_status ra_cp_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, in
   ra::clear_error();
   RA_REQUIRE(bytes != nullptr, "bytes is NULL");
   RA_REQUIRE(Hq >= 1 && Hkv >= 1 && d >= 1, "sizes must be >= 1");
-  *bytes = 16;
+  *bytes = static_cast<size_t>(part_floats(d) * 4 + part_floats(1) * 8);
   return RA_OK;
 }
 
@@ -120,24 +1004,18 @@ extern "C" ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const 
   size_t need = 0;
   if ((st = ra_cp_chunk_attn_workspace_size(Hq, Hkv, d, &need)) != RA_OK) return st;
   RA_REQUIRE(ws_bytes >= need, "workspace too small (%zu < %zu bytes)", ws_bytes, need);
-  ChunkParams p;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.kc = static_cast<const __nv_bfloat16*>(k_cache);
-  p.vc = static_cast<const __nv_bfloat16*>(v_cache);
-  p.qsl = query_start_loc; p.ctx = ctx_lens;
-  p.c = make_paged(block_table, Hkv, block_size, interleave, pcp, dcp, max_vblocks, num_blocks);
-  p.T = T; p.R = R; p.Hq = Hq; p.G = Hq / Hkv; p.causal = causal ? 1 : 0;
-  p.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(d))) * 1.4426950408889634f;
-  p.o = o; p.lse = lse;
-  const unsigned blocks = static_cast<unsigned>(ra::ceil_div(T * Hq, 8));
-  const bool bf = out_dt == RA_BF16;
-  if (d == 128) {
-    if (bf) chunk_simple_kernel<128, true><<<blocks, 256, 0, stream>>>(p);
-    else chunk_simple_kernel<128, false><<<blocks, 256, 0, stream>>>(p);
-  } else {
-    if (bf) chunk_simple_kernel<64, true><<<blocks, 256, 0, stream>>>(p);
-    else chunk_simple_kernel<64, false><<<blocks, 256, 0, stream>>>(p);
-  }
-  RA_LAUNCH_CHECK("chunk_simple_kernel");
-  return RA_OK;
+  ChunkArgs a;
+  a.qsl = query_start_loc; a.ctx = ctx_lens;
+  a.c = make_paged(block_table, Hkv, block_size, interleave, pcp, dcp, max_vblocks, num_blocks);
+  a.T = T; a.R = R; a.Hq = Hq; a.G = Hq / Hkv; a.causal = causal ? 1 : 0; a.out_bf16 = out_dt == RA_BF16;
+  a.u = block_size % 32 == 0 ? 32 : 16;
+  a.upt = BN / a.u;
+  a.nsub = block_size / a.u;
+  a.tpt = BM / a.G;
+  a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(d))) * 1.4426950408889634f;
+  a.o = o; a.lse = lse;
+  a.o_part = static_cast<float*>(workspace);
+  a.ml_part = reinterpret_cast<float2*>(a.o_part + part_floats(d));
+  a.wait_limit = ra::wait_limit();
+  return d == 128 ? launch_chunk<128>(q, k_cache, v_cache, a, stream) : launch_chunk<64>(q, k_cache, v_cache, a, stream);
 }
