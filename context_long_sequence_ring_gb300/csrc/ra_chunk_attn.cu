@@ -50,14 +50,15 @@ namespace {
 constexpr int kCtas = 152;         // parts of the work, one CTA per SM of a GB300
 constexpr int kChunkThreads = 384;
 constexpr int kMergeThreads = 256;
-constexpr int kMergeRowBlocks = 8;
+constexpr int kMergeRowBlocks = 4;
 
 struct ChunkArgs {
   const int32_t *qsl, *ctx;
   Paged c;
   int64_t T;
   int R, Hq, G, causal, out_bf16;
-  int u, upt, nsub;               // slots of a unit, units of a tile, units of a block
+  int lu, lupt, nsub;             // log2 slots of a unit, log2 units of a tile, units of a block
+  FastDiv by_vbu;                 // by the units of a virtual block
   int tpt;                        // tokens of a row tile
   float scale_log2;
   void* o;                        // [T, Hq, D]
@@ -108,39 +109,45 @@ __device__ __forceinline__ int limit_of(const ChunkArgs& a, const Req& q, int i)
 // Units that hold a token below lim: a prefix of the units.
 __device__ __forceinline__ int units_below(const ChunkArgs& a, int lim) {
   if (lim <= 0) return 0;
-  const int vb = lim / a.c.V, o = lim - vb * a.c.V;
-  int k = vb * a.nsub * a.c.W;
+  int o, rem;
+  int k = a.c.by_V.div(lim, o) * a.nsub * a.c.W;
   if (o > 0) {
-    const int p = a.c.W * a.c.I, q = (o - 1) / p, rem = (o - 1) - q * p;
-    const int sub = (q * a.c.I + min(rem, a.c.I - 1)) / a.u;   // last unit row with a token below
-    const int s0 = sub * a.u, first = (s0 / a.c.I) * p + s0 % a.c.I;
-    k += sub * a.c.W + min(a.c.W, (o - first + a.c.I - 1) / a.c.I);
+    const int q = a.c.by_WI.div(o - 1, rem);
+    const int sub = (q * a.c.I + min(rem, a.c.I - 1)) >> a.lu;   // last unit row with a token below
+    int off;
+    const int first = a.c.by_I.div(sub << a.lu, off) * a.c.W * a.c.I + off;
+    k += sub * a.c.W + min(a.c.W, a.c.by_I.div(o - first + a.c.I - 1));
   }
   return k;
 }
 
 // Units from the start all of whose tokens are below lim.
 __device__ __forceinline__ int units_within(const ChunkArgs& a, int lim) {
-  const int vb = lim / a.c.V, o = lim - vb * a.c.V;
-  return (vb * a.nsub + (o / (a.c.W * a.c.I)) * a.c.I / a.u) * a.c.W;
+  int o;
+  const int vb = a.c.by_V.div(lim, o);
+  return (vb * a.nsub + ((a.c.by_WI.div(o) * a.c.I) >> a.lu)) * a.c.W;
 }
 
 __device__ __forceinline__ int tiles_of(const ChunkArgs& a, const Req& q, int k) {
   const int tpi = q.pair ? 2 * a.tpt : a.tpt;
   const int last = min(q.n, (k + 1) * tpi) - 1;
-  return (units_below(a, limit_of(a, q, last)) + a.upt - 1) / a.upt;
+  return (units_below(a, limit_of(a, q, last)) + (1 << a.lupt) - 1) >> a.lupt;
 }
 
-// Tiles [t0, t1) of an item of nt tiles and cost [at, at + cost) that part [lo, hi) takes.
+// Tiles [t0, t1) of an item of nt tiles and cost [at, at + cost) that part [lo, hi) takes.  Fractions are
+// taken in fp32: a boundary gives the same tile to both of its sides, whatever its rounding.
+__device__ __forceinline__ int cut_at(long long off, long long cost, int nt) {
+  return min(nt, static_cast<int>(__fdividef(static_cast<float>(off), static_cast<float>(cost)) * static_cast<float>(nt)));
+}
 __device__ __forceinline__ void cut(long long lo, long long hi, long long at, long long cost, int nt, int& t0, int& t1) {
-  t0 = lo <= at ? 0 : static_cast<int>((lo - at) * nt / cost);
-  t1 = hi >= at + cost ? nt : static_cast<int>((hi - at) * nt / cost);
+  t0 = lo <= at ? 0 : cut_at(lo - at, cost, nt);
+  t1 = hi >= at + cost ? nt : cut_at(hi - at, cost, nt);
 }
 
+// Part c of the work is [lo(c), lo(c + 1)), empty from the first c with lo(c) = total on.
 struct Plan {
-  long long total;
-  int parts;
-  __device__ long long lo(int c) const { return total / parts * c + total % parts * c / parts; }
+  long long total, share;
+  __device__ long long lo(int c) const { return min(total, share * c); }
 };
 
 // The total cost, and the request that holds cost position `lo_of(plan)` with the cost
@@ -188,12 +195,11 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, int part, PlanScra
     total += sum;
   }
   plan.total = total;
-  const long long most = total / kMinShare;
-  plan.parts = most < 1 ? 1 : (most < kCtas ? static_cast<int>(most) : kCtas);
+  plan.share = max(kMinShare, (total + kCtas - 1) / kCtas);
   if (threadIdx.x == 0) s.r = -1;
   __syncthreads();
-  if (part < plan.parts && total > 0) {
-    const long long lo = plan.lo(part);
+  const long long lo = plan.lo(part);
+  if (lo < total) {
     long long at = 0;
     for (int base = 0; base < a.R; base += NT) {
       const int i = base + threadIdx.x;
@@ -217,13 +223,16 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, int part, PlanScra
   pre = s.pre;
 }
 
-// One row tile (pair) of a part: K/V tiles [t0, t1) of nt.
+// One row tile (pair) of a part, as the roles read it: K/V tiles [t0, t0 + nt) of `all`.
 struct Segment {
-  Req q;
-  int g, k, nt, t0, t1;
+  int r, g, q0, n, L, pos0;  // request, K/V head, its first query row, queries, context, position of query 0
+  int tok0, t0, nt, all;     // first token of slot 0; tiles
+  int dirty, clean0, clean1; // first tile (of this segment) with slots past the context; first tile of the item
+                             // that rows of slot 0 / 1 see a part of only
+  int pair;                  // 1 pair, 0 split, -1 end of the part
 };
 
-// Walks the items of part [lo, hi) in order; every role runs its own.
+// Walks the items of part [lo, hi) in order.
 struct SegIter {
   const ChunkArgs& a;
   long long lo, hi, at;
@@ -237,9 +246,12 @@ struct SegIter {
     live = r0 >= 0;
     if (!live) return;
     q = load_req(a, r);
-    const long long per_head = q.prefix(q.items);
-    g = static_cast<int>((lo - pre) / per_head);
-    const long long off = lo - pre - g * per_head;
+    const long long per_head = q.prefix(q.items), d = lo - pre;
+    g = static_cast<int>(__fdividef(static_cast<float>(d), static_cast<float>(per_head)));   // one off at most
+    g = min(g, a.c.Hkv - 1);
+    if (g * per_head > d) --g;
+    if ((g + 1) * per_head <= d) ++g;
+    const long long off = d - g * per_head;
     int x = 0, y = q.items - 1;   // largest k with prefix(k) <= off
     while (x < y) {
       const int mid = (x + y + 1) >> 1;
@@ -252,12 +264,20 @@ struct SegIter {
   __device__ bool next(Segment& s) {
     while (live && at < hi) {
       const long long cost = q.f * (q.base + q.slope * (k + 1));
-      s.q = q;
-      s.g = g;
-      s.k = k;
-      s.nt = tiles_of(a, q, k);
-      cut(lo, hi, at, cost, s.nt, s.t0, s.t1);
-      const bool mine = s.nt == 0 ? lo <= at : s.t1 > s.t0;
+      s.all = tiles_of(a, q, k);
+      int t1;
+      cut(lo, hi, at, cost, s.all, s.t0, t1);
+      const bool mine = s.all == 0 ? lo <= at : t1 > s.t0;
+      if (mine) {
+        s.r = r; s.g = g; s.q0 = q.q0; s.n = q.n; s.L = q.L;
+        s.pos0 = static_cast<int>(q.pos0 < -q.n ? -q.n : q.pos0);   // below -n: nothing is visible either way
+        s.pair = q.pair;
+        s.tok0 = k * (q.pair ? 2 * a.tpt : a.tpt);
+        s.nt = t1 - s.t0;
+        s.dirty = (units_within(a, q.L) >> a.lupt) - s.t0;
+        s.clean0 = units_within(a, limit_of(a, q, s.tok0)) >> a.lupt;
+        s.clean1 = q.pair ? units_within(a, limit_of(a, q, min(s.tok0 + a.tpt, q.n - 1))) >> a.lupt : s.clean0;
+      }
       at += cost;
       if (++k == q.items) {
         k = 0;
@@ -347,20 +367,23 @@ __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool 
 
 // Visible slots (a prefix, 0..u) of unit `unit` for a row that sees positions below lim.
 __device__ __forceinline__ int unit_visible(const ChunkArgs& a, int64_t r_row, bool check, int unit, int lim) {
-  const int per_vb = a.nsub * a.c.W;
-  const int vb = unit / per_vb, rem = unit - vb * per_vb;
-  const int sub = rem / a.c.W, w = rem - sub * a.c.W;
+  int rem, w;
+  const int vb = a.by_vbu.div(unit, rem), sub = a.c.by_W.div(rem, w);
   const int y = lim - vb * a.c.V - w * a.c.I;
   if (y <= 0) return 0;
   if (check) {  // some block of this CTA's work was bad: leave out its tokens
     const int32_t b = vb < a.c.max_vb ? a.c.table[r_row * a.c.max_vb + vb] : -1;
     if (b < 0 || b >= a.c.num_blocks) return 0;
   }
-  const int p = a.c.W * a.c.I, q = y / p;
-  return max(0, min(a.u, q * a.c.I + min(y - q * p, a.c.I) - sub * a.u));
+  int part;
+  const int q = a.c.by_WI.div(y, part);
+  return max(0, min(1 << a.lu, q * a.c.I + min(part, a.c.I) - (sub << a.lu)));
 }
 
 // ------------------------------------------------------------------ the kernel
+constexpr int kSegs = 4;          // segments announced ahead
+constexpr int kSegReaders = 11;   // warps that read them: TMA, MMA, zeroing and 8 of softmax
+
 template <int D>
 constexpr int kStages = D == 128 ? 5 : 8;   // K/V tiles in flight (32 or 16 KB each)
 
@@ -369,8 +392,10 @@ struct __align__(1024) ChunkSmem {
   uint8_t q[2][BM * D * 2];
   uint8_t kv[kStages<D>][BN * D * 2];
   uint64_t q_full[2], q_empty[2], kv_full[kStages<D>], kv_empty[kStages<D>], v_dirty[kStages<D>], v_clean[kStages<D>];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2], ml_full, ml_empty, drain;
   float2 ml[BM];
+  Segment seg[kSegs];
   PlanScratch<kChunkThreads> plan;
   uint32_t tmem_base;
   int abort_flag, bad_block;
@@ -390,6 +415,23 @@ struct Ring {
       st = 0;
       ph ^= 1;
     }
+  }
+};
+
+// A role's reading of the announced segments, in order.
+struct SegReader {
+  uint32_t at = 0;
+  template <class Smem>
+  __device__ bool next(Smem& sm, Segment& s, volatile int* abort_flag, long long limit, bool whole_warp) {
+    const int i = at & (kSegs - 1);
+    const uint32_t bar = smem_u32(&sm.seg_full[i]), ph = (at / kSegs) & 1;
+    const bool ok = whole_warp ? warp_wait(bar, ph, abort_flag, limit, 570) : mbar_wait(bar, ph, abort_flag, limit, 571);
+    if (!ok) return false;
+    s = sm.seg[i];
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || (threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.seg_empty[i]));
+    ++at;
+    return s.pair >= 0;
   }
 };
 
@@ -423,6 +465,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(smem_u32(&sm.pv_done[b]), 1);
       mbar_init(smem_u32(&sm.o_empty[b]), 128);
     }
+    for (int s = 0; s < kSegs; ++s) {
+      mbar_init(smem_u32(&sm.seg_full[s]), 1);
+      mbar_init(smem_u32(&sm.seg_empty[s]), kSegReaders);
+    }
     for (int s = 0; s < NS; ++s) {
       mbar_init(smem_u32(&sm.kv_full[s]), 1);
       mbar_init(smem_u32(&sm.kv_empty[s]), 1);
@@ -444,7 +490,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  SegIter it(a, plan, blockIdx.x, r0, pre);
+  // the joining kernel may come up and make its plan meanwhile; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  SegReader segs;
   Segment sg;
 
   // Order of the K/V ring in a segment: K_0 .. K_{la-1}, then V_j, K_{j+la} for each j, with la = 1
@@ -461,28 +509,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint32_t q_cnt[2] = {0, 0};
     int q_next = 0;
     bool ok = true;
-    const int per_vb = a.nsub * a.c.W;
     const int oob = static_cast<int>(a.c.W * a.c.num_blocks * a.c.Hkv);   // past the last block: zero fill
-    while (ok && it.next(sg)) {
-      const int nt = sg.t1 - sg.t0;
+    while (ok && segs.next(sm, sg, abort_flag, lim, true)) {
+      const int nt = sg.nt;
       if (nt <= 0) continue;
-      const int la = sg.q.pair ? 1 : 2, nq = sg.q.pair ? 2 : 1;
-      const int dirty = units_within(a, sg.q.L) / a.upt - sg.t0;   // first tile with slots past the context
+      const int la = sg.pair ? 1 : 2, nq = sg.pair ? 2 : 1;
       for (int h = 0; h < nq && ok; ++h) {
-        const int b = sg.q.pair ? h : q_next;
+        const int b = sg.pair ? h : q_next;
         ok = warp_wait(smem_u32(&sm.q_empty[b]), (q_cnt[b] & 1) ^ 1, abort_flag, lim, 520);
         if (!ok) break;
         ++q_cnt[b];
         if (lane == 0) {
           const uint32_t qb = smem_u32(&sm.q_full[b]);
           mbar_arrive_expect_tx(qb, SLABS * a.tpt * a.G * 128);
-          const int row = sg.q.q0 + (nq * sg.k + h) * a.tpt;
+          const int row = sg.q0 + sg.tok0 + h * a.tpt;
           for (int s = 0; s < SLABS; ++s)
             tma_load_3d(smem_u32(sm.q[b] + s * BM * 128), &tmQ, qb, 64 * s, sg.g * a.G, row);
         }
         __syncwarp();
       }
-      if (!sg.q.pair) q_next ^= 1;
+      if (!sg.pair) q_next ^= 1;
       auto load_tile = [&](const CUtensorMap* map, int blk, int s0, int w, bool to_clean) -> bool {
         if (!warp_wait(smem_u32(&sm.kv_empty[ring.st]), ring.ph ^ 1, abort_flag, lim, 521)) return false;
         const uint32_t bar = smem_u32(&sm.kv_full[ring.st]);
@@ -491,10 +537,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (to_clean) mbar_arrive(smem_u32(&sm.v_dirty[ring.st]));
         }
         __syncwarp();
-        if (lane < a.upt) {
+        if (lane >> a.lupt == 0) {
           const int hb = blk < 0 ? oob : static_cast<int>((w * a.c.num_blocks + blk) * a.c.Hkv + sg.g);
           for (int s = 0; s < SLABS; ++s)
-            tma_load_3d(smem_u32(sm.kv[ring.st] + s * BN * 128 + lane * a.u * 128), map, bar, 64 * s, s0, hb);
+            tma_load_3d(smem_u32(sm.kv[ring.st] + s * BN * 128 + (lane << a.lu) * 128), map, bar, 64 * s, s0, hb);
         }
         ++issued;
         ring.advance();
@@ -502,13 +548,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       };
       // lane's unit of tile j: device, slot, block (-1: past the table or bad)
       auto locate = [&](int j, int& blk, int& s0, int& w) {
-        const int unit = (sg.t0 + j) * a.upt + lane;
-        const int vb = unit / per_vb, rem = unit - vb * per_vb, sub = rem / a.c.W;
-        w = rem - sub * a.c.W;
-        s0 = sub * a.u;
+        int rem;
+        const int vb = a.by_vbu.div(((sg.t0 + j) << a.lupt) + lane, rem);
+        s0 = a.c.by_W.div(rem, w) << a.lu;
         blk = -1;
-        if (lane < a.upt && static_cast<int64_t>(vb) * a.c.V < sg.q.L) {
-          blk = a.c.table[static_cast<int64_t>(sg.q.r) * a.c.max_vb + vb];
+        if (lane >> a.lupt == 0 && static_cast<int64_t>(vb) * a.c.V < sg.L) {
+          blk = a.c.table[static_cast<int64_t>(sg.r) * a.c.max_vb + vb];
           if (blk < 0 || blk >= a.c.num_blocks) {
             ra_record_error(RA_ERR_DEVICE_BOUNDS, 512);
             *reinterpret_cast<volatile int*>(&sm.bad_block) = 1;
@@ -525,7 +570,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       for (int j = 0; j < nt && ok; ++j) {
         if (j + la < nt) locate(j + la, bk[la], sk[la], wk[la]);
-        if (!(ok = load_tile(&tmV, bk[0], sk[0], wk[0], j >= dirty))) break;
+        if (!(ok = load_tile(&tmV, bk[0], sk[0], wk[0], j >= sg.dirty))) break;
         if (j + la < nt && !(ok = load_tile(&tmK, bk[la], sk[la], wk[la], false))) break;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -535,7 +580,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
     }
-    if (!ok && lane == 0) {
+    if ((!ok || *abort_flag) && lane == 0) {
       // let the copies already in flight land before the CTA exits: the last load of each buffer
       for (int b = 0; b < 2; ++b)
         if (q_cnt[b]) mbar_wait_quiesce(smem_u32(&sm.q_full[b]), (q_cnt[b] - 1) & 1, 1 << 22);
@@ -581,11 +626,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         return true;
       };
-      while (ok && it.next(sg)) {
-        const int nt = sg.t1 - sg.t0;
+      while (ok && segs.next(sm, sg, abort_flag, lim, false)) {
+        const int nt = sg.nt;
         if (nt <= 0) continue;
-        const int dirty = units_within(a, sg.q.L) / a.upt - sg.t0;   // first tile with slots past the context
-        const bool pair = sg.q.pair;
+        const int dirty = sg.dirty;
+        const bool pair = sg.pair;
         const int qb = pair ? 0 : q_next;
         if (!(ok = mbar_wait(smem_u32(&sm.q_full[qb]), q_cnt[qb] & 1, abort_flag, lim, 530))) break;
         ++q_cnt[qb];
@@ -679,20 +724,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     Ring<NS> ring;
     uint32_t dirty_ph = 0;
     bool ok = true;
-    while (ok && it.next(sg)) {
-      const int nt = sg.t1 - sg.t0;
+    while (ok && segs.next(sm, sg, abort_flag, lim, true)) {
+      const int nt = sg.nt;
       if (nt <= 0) continue;
-      const int la = sg.q.pair ? 1 : 2;
-      const int dirty = units_within(a, sg.q.L) / a.upt - sg.t0;
+      const int la = sg.pair ? 1 : 2;
       for (int j = 0; j < min(la, nt); ++j) ring.advance();
       for (int j = 0; j < nt; ++j) {
-        if (j >= dirty) {
+        if (j >= sg.dirty) {
           if (!(ok = warp_wait(smem_u32(&sm.v_dirty[ring.st]), (dirty_ph >> ring.st) & 1, abort_flag, lim, 540))) break;
           dirty_ph ^= 1u << ring.st;
           if (!(ok = warp_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 541))) break;
           for (int i = lane; i < BN; i += 32) {
-            const int unit = (sg.t0 + j) * a.upt + i / a.u;
-            if (i % a.u >= unit_visible(a, sg.q.r, false, unit, sg.q.L)) {
+            const int ui = i >> a.lu;
+            if (i - (ui << a.lu) >= unit_visible(a, sg.r, false, ((sg.t0 + j) << a.lupt) + ui, sg.L)) {
 #pragma unroll
               for (int s = 0; s < SLABS; ++s)
 #pragma unroll
@@ -709,6 +753,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (j + la < nt) ring.advance();
       }
     }
+  } else if (warp == 3) {
+    // ============================================================ segments of this part, announced to the other roles
+    if (lane == 0) {
+      SegIter it(a, plan, blockIdx.x, r0, pre);
+      bool more = true;
+      for (uint32_t i = 0; more; ++i) {
+        more = it.next(sg);
+        if (!more) sg.pair = -1;
+        const int b = i & (kSegs - 1);
+        if (!mbar_wait(smem_u32(&sm.seg_empty[b]), ((i / kSegs) & 1) ^ 1, abort_flag, lim, 572)) break;
+        sm.seg[b] = sg;
+        mbar_arrive(smem_u32(&sm.seg_full[b]));
+      }
+    }
   } else if (warp >= 4) {
     // ============================================================ softmax + epilogue (slot h)
     const int h = (warp - 4) >> 2;
@@ -719,12 +777,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int row_tok = row / a.G, row_head = row - row_tok * a.G;
     uint32_t s_cnt = 0, pv_cnt[2] = {0, 0}, splits = 0;
     bool ok = true;
-    while (ok && it.next(sg)) {
-      const int nt = sg.t1 - sg.t0;
-      const bool pair = sg.q.pair;
-      const int tok = (pair ? 2 * sg.k + h : sg.k) * a.tpt + row_tok;
-      const bool row_ok = row_tok < a.tpt && tok < sg.q.n;
-      const int64_t orow = static_cast<int64_t>(sg.q.q0 + tok) * a.Hq + sg.g * a.G + row_head;
+    while (ok && segs.next(sm, sg, abort_flag, lim, true)) {
+      const int nt = sg.nt;
+      const bool pair = sg.pair;
+      const int tok = sg.tok0 + (pair ? h * a.tpt : 0) + row_tok;
+      const bool row_ok = row_tok < a.tpt && tok < sg.n;
+      const int64_t orow = static_cast<int64_t>(sg.q0 + tok) * a.Hq + sg.g * a.G + row_head;
       if (nt <= 0) {   // the tile sees nothing
         if (row_ok && (pair || h == 0)) {
           for (int e = 0; e < D; e += 8) {
@@ -739,9 +797,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         continue;
       }
       // visible positions of this row, and the first tile in which the slot's first row sees a part only
-      const int vis = limit_of(a, sg.q, min(tok, sg.q.n - 1));
-      const int first_tok = min((pair ? 2 * sg.k + h : sg.k) * a.tpt, sg.q.n - 1);
-      const int clean = units_within(a, limit_of(a, sg.q, first_tok)) / a.upt;
+      const int vis = a.causal ? max(0, min(sg.L, sg.pos0 + min(tok, sg.n - 1) + 1)) : sg.L;
+      const int clean = h ? sg.clean1 : sg.clean0;
       const bool warp_live = __any_sync(0xffffffffu, row_ok);
       float m = -CUDART_INF_F, l = 0.f;
       const int step = pair ? 1 : 2;
@@ -758,8 +815,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             int lim16[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const int col = 32 * c + 16 * q, ui = col / a.u;
-              lim16[q] = unit_visible(a, sg.q.r, bad, tile * a.upt + ui, vis) - (col - ui * a.u);
+              const int col = 32 * c + 16 * q, ui = col >> a.lu;
+              lim16[q] = unit_visible(a, sg.r, bad, (tile << a.lupt) + ui, vis) - (col - (ui << a.lu));
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -791,7 +848,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
-      const bool whole = nt == sg.nt;
+      const bool whole = nt == sg.all;
       const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (sg.t0 == 0 ? 1 : 0);
       pv_cnt[0] += pair ? nt : (nt + 1) / 2;   // both slots' products so far, whichever this thread waits for
       pv_cnt[1] += pair ? nt : nt / 2;
@@ -881,55 +938,87 @@ template <int D>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkArgs a) {
   constexpr int E = D / 32;
   __shared__ PlanScratch<kMergeThreads> scratch;
+  __shared__ int parts[kCtas];
+  long long cost_sum;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.x + 1;
   Plan plan;
   int r;
   long long pre;
   make_plan<kMergeThreads>(a, b, scratch, plan, r, pre);
-  if (b >= plan.parts || r < 0) return;
+  if (r < 0) return;
   SegIter it(a, plan, b, r, pre);
   // the item at the start of part b
   const long long at = it.at, cost = it.q.f * (it.q.base + it.q.slope * (it.k + 1));
   if (plan.lo(b) <= at || plan.lo(b - 1) > at) return;
   const int nt = tiles_of(a, it.q, it.k);
   if (nt == 0) return;
-  int last = b, used = 0;
-  for (int c = b - 1; c < plan.parts; ++c) {
-    if (plan.lo(c) >= at + cost) break;
+  // the partials of the item: of part b - 1, which holds its start, and the ones that follow
+  int c = b - 1 + threadIdx.x, at_part = -1;
+  if (c < kCtas && plan.lo(c) < at + cost) {
     int t0, t1;
     cut(plan.lo(c), plan.lo(c + 1), at, cost, nt, t0, t1);
-    used += t1 > t0;
-    last = c;
+    if (t1 > t0) at_part = 2 * c + (t0 == 0 ? 1 : 0);
   }
+  int used;
+  const int rank = static_cast<int>(block_scan<kMergeThreads>(at_part >= 0, scratch, cost_sum));
+  used = static_cast<int>(cost_sum);
   if (used <= 1) return;
+  if (at_part >= 0) parts[rank] = at_part;
+  __syncthreads();
+  // the partials are complete, and visible, once the first kernel is
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int slots = it.q.pair ? 2 : 1;
   for (int i = blockIdx.y * (kMergeThreads / 32) + warp; i < slots * BM; i += gridDim.y * (kMergeThreads / 32)) {
     const int h = i / BM, row = i % BM, rt = row / a.G;
     const int tok = (slots * it.k + h) * a.tpt + rt;
     if (rt >= a.tpt || tok >= it.q.n) continue;
-    float M = -CUDART_INF_F, l = 0.f, acc[E];
+    // lane p holds (m, l) of partial p, then its weight 2^(m - M); partials that saw nothing have weight 0
+    float M = -CUDART_INF_F, l = 0.f;
+    __align__(16) float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int c = b - 1; c <= last; ++c) {
-      int t0, t1;
-      cut(plan.lo(c), plan.lo(c + 1), at, cost, nt, t0, t1);
-      if (t1 <= t0) continue;
-      const int64_t p = ((2 * static_cast<int64_t>(c) + (t0 == 0 ? 1 : 0)) * 2 + h) * BM + row;
-      const float2 ml = a.ml_part[p];
-      if (!(ml.y > 0.f)) continue;      // this part saw nothing for the row
-      const float mn = fmaxf(M, ml.x), w0 = ex2(M - mn), w1 = ex2(ml.x - mn);
-      M = mn;
-      l = l * w0 + ml.y * w1;
+    for (int p0 = 0; p0 < used; p0 += 32) {
+      float2 ml = make_float2(-CUDART_INF_F, 0.f);
+      if (p0 + lane < used) ml = a.ml_part[(parts[p0 + lane] * 2 + h) * BM + row];
+      float mn = ml.y > 0.f ? ml.x : -CUDART_INF_F;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * w0 + w1 * a.o_part[p * D + lane + 32 * e];
+      for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      mn = fmaxf(M, mn);
+      if (mn == -CUDART_INF_F) continue;
+      const float w = ml.y > 0.f ? ex2(ml.x - mn) : 0.f, old = ex2(M - mn);
+      float ls = w * ml.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+      M = mn;
+      l = l * old + ls;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= old;
+      const int np = min(32, used - p0);
+#pragma unroll 4
+      for (int p = 0; p < np; ++p) {
+        const float wp = __shfl_sync(0xffffffffu, w, p);
+        const float* src = a.o_part + (static_cast<int64_t>(parts[p0 + p] * 2 + h) * BM + row) * D + E * lane;
+        __align__(16) float v[E];
+        if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+        else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += wp * v[e];
+      }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const int64_t orow = static_cast<int64_t>(it.q.q0 + tok) * a.Hq + it.g * a.G + (row - rt * a.G);
+    if (a.out_bf16) {
+      __align__(8) uint32_t w[E / 2];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (a.out_bf16) static_cast<__nv_bfloat16*>(a.o)[orow * D + lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
-      else static_cast<float*>(a.o)[orow * D + lane + 32 * e] = acc[e] * inv;
+      for (int e = 0; e < E; e += 2) w[e / 2] = f2_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + orow * D + E * lane);
+      if (E == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(w);
+      else *dst = w[0];
+    } else {
+      float* dst = static_cast<float*>(a.o) + orow * D + E * lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) dst[e] = acc[e] * inv;
     }
     if (a.lse && lane == 0) a.lse[orow] = l > 0.f ? (M + log2f(l)) * kLn2 : -CUDART_INF_F;
   }
@@ -956,15 +1045,23 @@ ra_status launch_chunk(const void* q, const void* k, const void* v, const ChunkA
   ra_status st;
   const int64_t blocks = a.c.W * a.c.num_blocks * a.c.Hkv;
   if ((st = chunk_map(&mq, q, D, a.Hq, a.T, a.G, a.tpt)) != RA_OK) return st;
-  if ((st = chunk_map(&mk, k, D, a.c.bs, blocks, a.u, 1)) != RA_OK) return st;
-  if ((st = chunk_map(&mv, v, D, a.c.bs, blocks, a.u, 1)) != RA_OK) return st;
+  if ((st = chunk_map(&mk, k, D, a.c.bs, blocks, 1 << a.lu, 1)) != RA_OK) return st;
+  if ((st = chunk_map(&mv, v, D, a.c.bs, blocks, 1 << a.lu, 1)) != RA_OK) return st;
   const size_t smem = sizeof(ChunkSmem<D>) + 1024;
   RA_CUDA_TRY(cudaFuncSetAttribute(chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    static_cast<int>(smem)));
   chunk_attn_kernel<D><<<kCtas, kChunkThreads, smem, stream>>>(mq, mk, mv, a);
   RA_LAUNCH_CHECK("chunk_attn_kernel");
-  chunk_merge_kernel<D><<<dim3(kCtas - 1, kMergeRowBlocks), kMergeThreads, 0, stream>>>(a);
-  RA_LAUNCH_CHECK("chunk_merge_kernel");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCtas - 1, kMergeRowBlocks);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  RA_CUDA_TRY(cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D>, a));
   return RA_OK;
 }
 
@@ -1008,9 +1105,10 @@ extern "C" ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const 
   a.qsl = query_start_loc; a.ctx = ctx_lens;
   a.c = make_paged(block_table, Hkv, block_size, interleave, pcp, dcp, max_vblocks, num_blocks);
   a.T = T; a.R = R; a.Hq = Hq; a.G = Hq / Hkv; a.causal = causal ? 1 : 0; a.out_bf16 = out_dt == RA_BF16;
-  a.u = block_size % 32 == 0 ? 32 : 16;
-  a.upt = BN / a.u;
-  a.nsub = block_size / a.u;
+  a.lu = block_size % 32 == 0 ? 5 : 4;
+  a.lupt = 7 - a.lu;
+  a.nsub = block_size >> a.lu;
+  a.by_vbu = fast_div(static_cast<int64_t>(a.nsub) * a.c.W);
   a.tpt = BM / a.G;
   a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(d))) * 1.4426950408889634f;
   a.o = o; a.lse = lse;

@@ -8,9 +8,35 @@
 
 namespace {
 
+// Division of n in [0, 2^31) by a fixed d >= 1: q = n * m >> (31 + l), m = ceil(2^(31+l) / d), l = ceil(log2 d)
+// (exact because m * d - 2^(31+l) < d <= 2^l).
+struct FastDiv {
+  uint32_t m, d;
+  int sh;
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * m) >> sh);
+  }
+  __device__ __forceinline__ int div(int n, int& rem) const {
+    const int q = div(n);
+    rem = n - q * static_cast<int>(d);
+    return q;
+  }
+};
+
+inline FastDiv fast_div(int64_t d) {
+  int l = 0;
+  while ((int64_t(1) << l) < d) ++l;
+  FastDiv f;
+  f.d = static_cast<uint32_t>(d);
+  f.sh = 31 + l;
+  f.m = static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + d - 1) / d);
+  return f;
+}
+
 struct Paged {
   const int32_t* table;  // [R, max_vb]
   int max_vb, bs, I, W, V, Hkv;
+  FastDiv by_V, by_I, by_W, by_WI;
   int64_t num_blocks;
 };
 
@@ -36,8 +62,8 @@ __device__ __forceinline__ int64_t paged_block(const Paged& c, int64_t r, int vb
 
 // Row (of d elements, or of one weight) of token x for K/V head g; -1 where its block is bad.
 __device__ __forceinline__ int64_t paged_row(const Paged& c, int64_t r, int x, int g, int site) {
-  const int vb = x / c.V, o = x - vb * c.V;
-  const int lbi = o / c.I, q = lbi / c.W;
+  int o;
+  const int vb = c.by_V.div(x, o), lbi = c.by_I.div(o), q = c.by_W.div(lbi);
   const int64_t b = paged_block(c, r, vb, site);
   if (b < 0) return -1;
   return (((lbi - q * c.W) * c.num_blocks + b) * c.Hkv + g) * c.bs + q * c.I + (o - lbi * c.I);
@@ -78,6 +104,8 @@ inline Paged make_paged(const int32_t* table, int32_t Hkv, int32_t block_size, i
   Paged c;
   c.table = table; c.max_vb = max_vblocks; c.bs = block_size; c.I = interleave;
   c.W = pcp * dcp; c.V = block_size * c.W; c.Hkv = Hkv; c.num_blocks = num_blocks;
+  c.by_V = fast_div(c.V); c.by_I = fast_div(c.I); c.by_W = fast_div(c.W);
+  c.by_WI = fast_div(static_cast<int64_t>(c.W) * c.I);
   return c;
 }
 

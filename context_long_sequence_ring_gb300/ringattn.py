@@ -117,7 +117,7 @@ def _check(status: int):
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -134,13 +134,15 @@ def _need_cuda(*ts):
 
 def _need_here(dtype, *ts):
     """Contiguous tensors of one dtype (None: any) on the current CUDA device."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    dev = None
     for t in ts:
         if t is None:
             continue
         if not t.is_cuda or not t.is_contiguous():
             _need_cuda(t)
-        if t.device.index != dev:
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
             raise ValueError("tensor must be on the current CUDA device")
         if dtype is not None and t.dtype != dtype:
             raise ValueError("dtype must be %s, not %s" % (dtype, t.dtype))
