@@ -50,7 +50,7 @@ namespace {
 constexpr int kCtas = 152;         // parts of the work, one CTA per SM of a GB300
 constexpr int kChunkThreads = 384;
 constexpr int kMergeThreads = 256;
-constexpr int kMergeRowBlocks = 4;
+constexpr int kMergeRowBlocks = 8;
 
 struct ChunkArgs {
   const int32_t *qsl, *ctx;
@@ -65,6 +65,7 @@ struct ChunkArgs {
   float* lse;                     // [T, Hq] or NULL
   float* o_part;                  // [2 * kCtas][256][D]
   float2* ml_part;                // [2 * kCtas][256]
+  struct Join* join;              // [kCtas]
   long long wait_limit;
 };
 
@@ -152,14 +153,14 @@ struct Plan {
 
 // The total cost, and the request that holds cost position `lo_of(plan)` with the cost
 // before it, found by all NT threads of the block (smem scratch).
-template <int NT>
 struct PlanScratch {
-  long long warp_sum[NT / 32];
+  long long warp_sum[kChunkThreads / 32];
   long long pre;
   int r;
+  Req q;
 };
-template <int NT>
-__device__ __forceinline__ long long block_scan(long long v, PlanScratch<NT>& s, long long& sum) {
+__device__ __forceinline__ long long block_scan(long long v, PlanScratch& s, long long& sum) {
+  constexpr int NT = kChunkThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long x = v;
 #pragma unroll
@@ -180,24 +181,24 @@ __device__ __forceinline__ long long block_scan(long long v, PlanScratch<NT>& s,
   }
   return before + x - v;
 }
-template <int NT>
-__device__ __forceinline__ void make_plan(const ChunkArgs& a, int part, PlanScratch<NT>& s, Plan& plan, int& r,
-                                          long long& pre) {
+// Fills the scratch with the request that holds the start of part `part` (r = -1: the part is empty).
+__device__ __forceinline__ void make_plan(const ChunkArgs& a, int part, PlanScratch& s, Plan& plan) {
+  constexpr int NT = kChunkThreads;
   long long total = 0, mine = 0, cost = 0, sum;
+  Req q;
+  if (threadIdx.x == 0) s.r = -1;
   for (int base = 0; base < a.R; base += NT) {
     const int i = base + threadIdx.x;
     cost = 0;
     if (i < a.R) {
-      const Req q = load_req(a, i);
+      q = load_req(a, i);
       cost = a.c.Hkv * q.prefix(q.items);
     }
-    mine = total + block_scan<NT>(cost, s, sum);
+    mine = total + block_scan(cost, s, sum);
     total += sum;
   }
   plan.total = total;
   plan.share = max(kMinShare, (total + kCtas - 1) / kCtas);
-  if (threadIdx.x == 0) s.r = -1;
-  __syncthreads();
   const long long lo = plan.lo(part);
   if (lo < total) {
     long long at = 0;
@@ -206,21 +207,20 @@ __device__ __forceinline__ void make_plan(const ChunkArgs& a, int part, PlanScra
       if (a.R > NT) {
         cost = 0;
         if (i < a.R) {
-          const Req q = load_req(a, i);
+          q = load_req(a, i);
           cost = a.c.Hkv * q.prefix(q.items);
         }
-        mine = at + block_scan<NT>(cost, s, sum);
+        mine = at + block_scan(cost, s, sum);
         at += sum;
       }
       if (cost > 0 && mine <= lo && lo < mine + cost) {
         s.r = i;
         s.pre = mine;
+        s.q = q;
       }
     }
   }
   __syncthreads();
-  r = s.r;
-  pre = s.pre;
 }
 
 // One row tile (pair) of a part, as the roles read it: K/V tiles [t0, t0 + nt) of `all`.
@@ -232,20 +232,27 @@ struct Segment {
   int pair;                  // 1 pair, 0 split, -1 end of the part
 };
 
+// A row tile that several parts share, as its first part leaves it for the joining kernel.
+struct Join {
+  Segment s;
+  long long at, cost, total, share;
+  int used;                  // 0: this part has none
+};
+
 // Walks the items of part [lo, hi) in order.
 struct SegIter {
   const ChunkArgs& a;
-  long long lo, hi, at;
+  long long lo, hi, at, cost;
   Req q;
   int r, g, k;
-  bool live;
-  __device__ SegIter(const ChunkArgs& args, const Plan& plan, int part, int r0, long long pre) : a(args) {
+  bool live, fresh;          // fresh: (r, g, k) has not been looked at yet
+  __device__ SegIter(const ChunkArgs& args, const Plan& plan, int part, const PlanScratch& ps) : a(args) {
     lo = plan.lo(part);
     hi = plan.lo(part + 1);
-    r = r0;
-    live = r0 >= 0;
-    if (!live) return;
-    q = load_req(a, r);
+    r = ps.r;
+    q = ps.q;
+    live = fresh = true;
+    const long long pre = ps.pre;
     const long long per_head = q.prefix(q.items), d = lo - pre;
     g = static_cast<int>(__fdividef(static_cast<float>(d), static_cast<float>(per_head)));   // one off at most
     g = min(g, a.c.Hkv - 1);
@@ -260,38 +267,38 @@ struct SegIter {
     k = x;
     at = pre + g * per_head + q.prefix(k);
   }
+  __device__ void advance() {
+    at += cost;
+    if (++k < q.items) return;
+    k = 0;
+    if (++g < a.c.Hkv) return;
+    g = 0;
+    do {
+      if (++r >= a.R) { live = false; return; }
+      q = load_req(a, r);
+    } while (q.items == 0);
+  }
   // The next segment of the part that has tiles, or an item that sees nothing; false at the end.
   __device__ bool next(Segment& s) {
-    while (live && at < hi) {
-      const long long cost = q.f * (q.base + q.slope * (k + 1));
+    while (true) {
+      if (!fresh) advance();
+      fresh = false;
+      if (!live || at >= hi) return false;
+      cost = q.f * (q.base + q.slope * (k + 1));
       s.all = tiles_of(a, q, k);
       int t1;
       cut(lo, hi, at, cost, s.all, s.t0, t1);
-      const bool mine = s.all == 0 ? lo <= at : t1 > s.t0;
-      if (mine) {
-        s.r = r; s.g = g; s.q0 = q.q0; s.n = q.n; s.L = q.L;
-        s.pos0 = static_cast<int>(q.pos0 < -q.n ? -q.n : q.pos0);   // below -n: nothing is visible either way
-        s.pair = q.pair;
-        s.tok0 = k * (q.pair ? 2 * a.tpt : a.tpt);
-        s.nt = t1 - s.t0;
-        s.dirty = (units_within(a, q.L) >> a.lupt) - s.t0;
-        s.clean0 = units_within(a, limit_of(a, q, s.tok0)) >> a.lupt;
-        s.clean1 = q.pair ? units_within(a, limit_of(a, q, min(s.tok0 + a.tpt, q.n - 1))) >> a.lupt : s.clean0;
-      }
-      at += cost;
-      if (++k == q.items) {
-        k = 0;
-        if (++g == a.c.Hkv) {
-          g = 0;
-          do {
-            if (++r >= a.R) { live = false; break; }
-            q = load_req(a, r);
-          } while (q.items == 0);
-        }
-      }
-      if (mine) return true;
+      if (s.all == 0 ? lo > at : t1 <= s.t0) continue;
+      s.r = r; s.g = g; s.q0 = q.q0; s.n = q.n; s.L = q.L;
+      s.pos0 = static_cast<int>(q.pos0 < -q.n ? -q.n : q.pos0);   // below -n: nothing is visible either way
+      s.pair = q.pair;
+      s.tok0 = k * (q.pair ? 2 * a.tpt : a.tpt);
+      s.nt = t1 - s.t0;
+      s.dirty = (units_within(a, q.L) >> a.lupt) - s.t0;
+      s.clean0 = units_within(a, limit_of(a, q, s.tok0)) >> a.lupt;
+      s.clean1 = q.pair ? units_within(a, limit_of(a, q, min(s.tok0 + a.tpt, q.n - 1))) >> a.lupt : s.clean0;
+      return true;
     }
-    return false;
   }
 };
 
@@ -365,19 +372,40 @@ __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool 
   return first ? 1.f : alpha;
 }
 
-// Visible slots (a prefix, 0..u) of unit `unit` for a row that sees positions below lim.
-__device__ __forceinline__ int unit_visible(const ChunkArgs& a, int64_t r_row, bool check, int unit, int lim) {
-  int rem, w;
-  const int vb = a.by_vbu.div(unit, rem), sub = a.c.by_W.div(rem, w);
+// Visible slots (a prefix, 0..u) of unit (vb, sub, w) for a row that sees positions below lim.
+__device__ __forceinline__ int unit_visible(const ChunkArgs& a, int vb, int sub, int w, int lim) {
   const int y = lim - vb * a.c.V - w * a.c.I;
   if (y <= 0) return 0;
-  if (check) {  // some block of this CTA's work was bad: leave out its tokens
-    const int32_t b = vb < a.c.max_vb ? a.c.table[r_row * a.c.max_vb + vb] : -1;
-    if (b < 0 || b >= a.c.num_blocks) return 0;
-  }
   int part;
   const int q = a.c.by_WI.div(y, part);
   return max(0, min(1 << a.lu, q * a.c.I + min(part, a.c.I) - (sub << a.lu)));
+}
+
+// Visible columns (a prefix, 0..16) of each 16 columns of a tile, 8 bits each.  `check`: some block of this
+// CTA's work was bad, leave out the tokens of such blocks.
+__device__ __forceinline__ void tile_limits(const ChunkArgs& a, int r, bool check, int tile, int lim, uint32_t (&lm)[2]) {
+  int rem, w, v = 0;
+  int vb = a.by_vbu.div(tile << a.lupt, rem), sub = a.c.by_W.div(rem, w);
+  lm[0] = lm[1] = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (a.lu == 4 || !(i & 1)) {
+      v = unit_visible(a, vb, sub, w, lim);
+      if (check && v > 0) {
+        const int32_t b = vb < a.c.max_vb ? a.c.table[static_cast<int64_t>(r) * a.c.max_vb + vb] : -1;
+        if (b < 0 || b >= a.c.num_blocks) v = 0;
+      }
+      if (++w == a.c.W) {
+        w = 0;
+        if (++sub == a.nsub) {
+          sub = 0;
+          ++vb;
+        }
+      }
+    }
+    lm[i >> 2] |= static_cast<uint32_t>(min(v, 16)) << (8 * (i & 3));
+    v = max(v - 16, 0);
+  }
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -396,10 +424,12 @@ struct __align__(1024) ChunkSmem {
   uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2], ml_full, ml_empty, drain;
   float2 ml[BM];
   Segment seg[kSegs];
-  PlanScratch<kChunkThreads> plan;
+  PlanScratch plan;
   uint32_t tmem_base;
   int abort_flag, bad_block;
 };
+
+static_assert(sizeof(ChunkSmem<128>) + 1024 <= 232448 && sizeof(ChunkSmem<64>) + 1024 <= 232448, "227 KB of shared memory");
 
 // mbar_wait by a whole warp with one outcome for all lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit, int site) {
@@ -451,10 +481,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const long long lim = a.wait_limit;
 
   Plan plan;
-  int r0;
-  long long pre;
-  make_plan<kChunkThreads>(a, blockIdx.x, sm.plan, plan, r0, pre);
-  if (r0 < 0) return;   // no work for this CTA
+  make_plan(a, blockIdx.x, sm.plan, plan);
+  if (sm.plan.r < 0) {   // no work for this CTA
+    if (threadIdx.x == 0) a.join[blockIdx.x].used = 0;
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
@@ -546,38 +577,51 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         ring.advance();
         return true;
       };
-      // lane's unit of tile j: device, slot, block (-1: past the table or bad)
-      auto locate = [&](int j, int& blk, int& s0, int& w) {
+      // lane's unit of tile j: device, slot, id of its block; the id is looked at one tile later, so that its
+      // load is in flight while the ring is waited for
+      struct Unit {
+        int s0, w, blk;
+      };
+      auto locate = [&](int j) {
+        Unit x;
         int rem;
         const int vb = a.by_vbu.div(((sg.t0 + j) << a.lupt) + lane, rem);
-        s0 = a.c.by_W.div(rem, w) << a.lu;
-        blk = -1;
-        if (lane >> a.lupt == 0 && static_cast<int64_t>(vb) * a.c.V < sg.L) {
-          blk = a.c.table[static_cast<int64_t>(sg.r) * a.c.max_vb + vb];
-          if (blk < 0 || blk >= a.c.num_blocks) {
-            ra_record_error(RA_ERR_DEVICE_BOUNDS, 512);
-            *reinterpret_cast<volatile int*>(&sm.bad_block) = 1;
-            blk = -1;
-          }
+        x.s0 = a.c.by_W.div(rem, x.w) << a.lu;
+        x.blk = -1;
+        if (j < nt && lane >> a.lupt == 0 && static_cast<int64_t>(vb) * a.c.V < sg.L) {
+          x.blk = a.c.table[static_cast<int64_t>(sg.r) * a.c.max_vb + vb];
+          if (x.blk < 0) x.blk = INT32_MAX;   // in the context, so that a bad id is one
+        }
+        return x;
+      };
+      auto checked = [&](Unit& x) {
+        if (x.blk >= a.c.num_blocks) {
+          ra_record_error(RA_ERR_DEVICE_BOUNDS, 512);
+          *reinterpret_cast<volatile int*>(&sm.bad_block) = 1;
+          x.blk = -1;
         }
         __syncwarp();
       };
-      // the blocks of K tile j + la are looked up while tile j + la - 1 is waited for, and kept for its V
-      int bk[3], sk[3], wk[3];
-      for (int j = 0; j < la && j < nt && ok; ++j) {
-        locate(j, bk[j], sk[j], wk[j]);
-        ok = load_tile(&tmK, bk[j], sk[j], wk[j], false);
+      // v: unit of V_j, (k1: of the K tile after it when la = 2), k: of K_{j+la}, ahead: the one after that
+      Unit v = locate(0), k1 = v, k;
+      if (la == 2) k1 = locate(1);
+      k = locate(la);
+      checked(v);
+      ok = load_tile(&tmK, v.blk, v.s0, v.w, false);
+      if (ok && la == 2 && nt > 1) {
+        checked(k1);
+        ok = load_tile(&tmK, k1.blk, k1.s0, k1.w, false);
       }
       for (int j = 0; j < nt && ok; ++j) {
-        if (j + la < nt) locate(j + la, bk[la], sk[la], wk[la]);
-        if (!(ok = load_tile(&tmV, bk[0], sk[0], wk[0], j >= sg.dirty))) break;
-        if (j + la < nt && !(ok = load_tile(&tmK, bk[la], sk[la], wk[la], false))) break;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          bk[i] = bk[i + 1];
-          sk[i] = sk[i + 1];
-          wk[i] = wk[i + 1];
+        const Unit ahead = locate(j + la + 1);
+        if (!(ok = load_tile(&tmV, v.blk, v.s0, v.w, j >= sg.dirty))) break;
+        if (j + la < nt) {
+          checked(k);
+          if (!(ok = load_tile(&tmK, k.blk, k.s0, k.w, false))) break;
         }
+        v = la == 2 ? k1 : k;
+        k1 = k;
+        k = ahead;
       }
     }
     if ((!ok || *abort_flag) && lane == 0) {
@@ -734,9 +778,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (!(ok = warp_wait(smem_u32(&sm.v_dirty[ring.st]), (dirty_ph >> ring.st) & 1, abort_flag, lim, 540))) break;
           dirty_ph ^= 1u << ring.st;
           if (!(ok = warp_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 541))) break;
-          for (int i = lane; i < BN; i += 32) {
-            const int ui = i >> a.lu;
-            if (i - (ui << a.lu) >= unit_visible(a, sg.r, false, ((sg.t0 + j) << a.lupt) + ui, sg.L)) {
+          uint32_t lm[2];
+          tile_limits(a, sg.r, false, sg.t0 + j, sg.L, lm);
+#pragma unroll
+          for (int i0 = 0; i0 < BN; i0 += 32) {
+            const int i = i0 + lane;
+            if ((lane & 15) >= static_cast<int>((lm[i0 >> 6] >> (8 * ((i0 >> 4) & 3) + (lane & 16 ? 8 : 0))) & 255)) {
 #pragma unroll
               for (int s = 0; s < SLABS; ++s)
 #pragma unroll
@@ -756,8 +803,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   } else if (warp == 3) {
     // ============================================================ segments of this part, announced to the other roles
     if (lane == 0) {
-      SegIter it(a, plan, blockIdx.x, r0, pre);
-      bool more = true;
+      SegIter it(a, plan, blockIdx.x, sm.plan);
+      bool more = true, left = false;
       for (uint32_t i = 0; more; ++i) {
         more = it.next(sg);
         if (!more) sg.pair = -1;
@@ -765,7 +812,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (!mbar_wait(smem_u32(&sm.seg_empty[b]), ((i / kSegs) & 1) ^ 1, abort_flag, lim, 572)) break;
         sm.seg[b] = sg;
         mbar_arrive(smem_u32(&sm.seg_full[b]));
+        if (more && sg.t0 == 0 && sg.nt < sg.all) {
+          a.join[blockIdx.x] = Join{sg, it.at, it.cost, plan.total, plan.share, 1};
+          left = true;
+        }
       }
+      if (!left) a.join[blockIdx.x].used = 0;
     }
   } else if (warp >= 4) {
     // ============================================================ softmax + epilogue (slot h)
@@ -810,20 +862,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (warp_live) {
           const bool bad = *reinterpret_cast<volatile int*>(&sm.bad_block) != 0;
           const int tile = sg.t0 + j;
+          const bool masked = tile >= clean || bad;
+          uint32_t lm[2] = {0, 0};
+          if (masked) tile_limits(a, sg.r, bad, tile, vis, lm);
           auto mask = [&](uint32_t (&x)[32], int c) {
-            // visible columns of each 16 of the chunk: a prefix of its unit
-            int lim16[2];
+            const uint32_t b = lm[c >> 1] >> (16 * (c & 1));
+            const int l0 = b & 255, l1 = (b >> 8) & 255;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int col = 32 * c + 16 * q, ui = col >> a.lu;
-              lim16[q] = unit_visible(a, sg.r, bad, (tile << a.lupt) + ui, vis) - (col - (ui << a.lu));
+            for (int i = 0; i < 16; ++i) {
+              if (i >= l0) x[i] = __float_as_uint(-CUDART_INF_F);
+              if (i >= l1) x[16 + i] = __float_as_uint(-CUDART_INF_F);
             }
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if ((i & 15) >= lim16[i >> 4]) x[i] = __float_as_uint(-CUDART_INF_F);
           };
           uint32_t pk[BN / 2];
-          const float alpha = softmax_step(t_lane + colS, n_mine == 0, tile >= clean || bad, row_ok, mask, a.scale_log2, m, l, pk);
+          const float alpha = softmax_step(t_lane + colS, n_mine == 0, masked, row_ok, mask, a.scale_log2, m, l, pk);
           if (n_mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
             // O_h must hold the previous P.V before it is rescaled
             if (!(ok = warp_wait(smem_u32(&sm.pv_done[h]), (pv_cnt[h] + n_mine - 1) & 1, abort_flag, lim, 552 + h))) break;
@@ -932,47 +984,39 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 }
 
 // ------------------------------------------------------------------ joining
-// Row tiles that a boundary between parts cuts: block b takes the tile that holds the boundary
-// between parts b and b + 1, if it is the first boundary inside that tile.  A warp per row.
+// Row tiles that several parts share: block (c, y) takes the one that part c starts, if it does.  A warp per row.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkArgs a) {
   constexpr int E = D / 32;
-  __shared__ PlanScratch<kMergeThreads> scratch;
-  __shared__ int parts[kCtas];
-  long long cost_sum;
+  __shared__ int parts[kCtas], n_parts;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.x + 1;
-  Plan plan;
-  int r;
-  long long pre;
-  make_plan<kMergeThreads>(a, b, scratch, plan, r, pre);
-  if (r < 0) return;
-  SegIter it(a, plan, b, r, pre);
-  // the item at the start of part b
-  const long long at = it.at, cost = it.q.f * (it.q.base + it.q.slope * (it.k + 1));
-  if (plan.lo(b) <= at || plan.lo(b - 1) > at) return;
-  const int nt = tiles_of(a, it.q, it.k);
-  if (nt == 0) return;
-  // the partials of the item: of part b - 1, which holds its start, and the ones that follow
-  int c = b - 1 + threadIdx.x, at_part = -1;
-  if (c < kCtas && plan.lo(c) < at + cost) {
-    int t0, t1;
-    cut(plan.lo(c), plan.lo(c + 1), at, cost, nt, t0, t1);
-    if (t1 > t0) at_part = 2 * c + (t0 == 0 ? 1 : 0);
-  }
-  int used;
-  const int rank = static_cast<int>(block_scan<kMergeThreads>(at_part >= 0, scratch, cost_sum));
-  used = static_cast<int>(cost_sum);
-  if (used <= 1) return;
-  if (at_part >= 0) parts[rank] = at_part;
-  __syncthreads();
-  // the partials are complete, and visible, once the first kernel is
+  // what the first kernel wrote is complete, and visible, once it has ended
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int slots = it.q.pair ? 2 : 1;
-  for (int i = blockIdx.y * (kMergeThreads / 32) + warp; i < slots * BM; i += gridDim.y * (kMergeThreads / 32)) {
-    const int h = i / BM, row = i % BM, rt = row / a.G;
-    const int tok = (slots * it.k + h) * a.tpt + rt;
-    if (rt >= a.tpt || tok >= it.q.n) continue;
+  const Join& jn = a.join[blockIdx.x];
+  if (jn.used == 0) return;
+  const Segment sg = jn.s;
+  const int slots = sg.pair ? 2 : 1;
+  const int rows = min(sg.n - sg.tok0, slots * a.tpt) * a.G;
+  if (static_cast<int>(blockIdx.y) * (kMergeThreads / 32) >= rows) return;
+  if (warp == 0) {
+    // the partials, in order: of this part, and of those that follow
+    const Plan plan{jn.total, jn.share};
+    const long long at = jn.at, cost = jn.cost;
+    int n = 0;
+    for (int c0 = blockIdx.x; c0 < kCtas && plan.lo(c0) < at + cost; c0 += 32) {
+      const int c = c0 + lane;
+      int t0 = 0, t1 = 0;
+      if (c < kCtas && plan.lo(c) < at + cost) cut(plan.lo(c), plan.lo(c + 1), at, cost, sg.all, t0, t1);
+      const unsigned b = __ballot_sync(0xffffffffu, t1 > t0);
+      if (t1 > t0) parts[n + __popc(b & ((1u << lane) - 1))] = 2 * c + (t0 == 0 ? 1 : 0);
+      n += __popc(b);
+    }
+    if (lane == 0) n_parts = n;
+  }
+  __syncthreads();
+  const int used = n_parts;
+  for (int i = blockIdx.y * (kMergeThreads / 32) + warp; i < rows; i += gridDim.y * (kMergeThreads / 32)) {
+    const int tok = i / a.G, h = tok >= a.tpt ? 1 : 0, row = i - h * a.tpt * a.G;
     // lane p holds (m, l) of partial p, then its weight 2^(m - M); partials that saw nothing have weight 0
     float M = -CUDART_INF_F, l = 0.f;
     __align__(16) float acc[E];
@@ -1007,7 +1051,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
       }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int64_t orow = static_cast<int64_t>(it.q.q0 + tok) * a.Hq + it.g * a.G + (row - rt * a.G);
+    const int64_t orow = static_cast<int64_t>(sg.q0 + sg.tok0 + tok) * a.Hq + sg.g * a.G + (i - tok * a.G);
     if (a.out_bf16) {
       __align__(8) uint32_t w[E / 2];
 #pragma unroll
@@ -1053,7 +1097,7 @@ ra_status launch_chunk(const void* q, const void* k, const void* v, const ChunkA
   chunk_attn_kernel<D><<<kCtas, kChunkThreads, smem, stream>>>(mq, mk, mv, a);
   RA_LAUNCH_CHECK("chunk_attn_kernel");
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCtas - 1, kMergeRowBlocks);
+  cfg.gridDim = dim3(kCtas, kMergeRowBlocks);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -1073,7 +1117,7 @@ extern "C" ra_status ra_cp_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, in
   ra::clear_error();
   RA_REQUIRE(bytes != nullptr, "bytes is NULL");
   RA_REQUIRE(Hq >= 1 && Hkv >= 1 && d >= 1, "sizes must be >= 1");
-  *bytes = static_cast<size_t>(part_floats(d) * 4 + part_floats(1) * 8);
+  *bytes = static_cast<size_t>(part_floats(d) * 4 + part_floats(1) * 8 + kCtas * sizeof(Join));
   return RA_OK;
 }
 
@@ -1114,6 +1158,7 @@ extern "C" ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const 
   a.o = o; a.lse = lse;
   a.o_part = static_cast<float*>(workspace);
   a.ml_part = reinterpret_cast<float2*>(a.o_part + part_floats(d));
+  a.join = reinterpret_cast<Join*>(a.ml_part + part_floats(1));
   a.wait_limit = ra::wait_limit();
   return d == 128 ? launch_chunk<128>(q, k_cache, v_cache, a, stream) : launch_chunk<64>(q, k_cache, v_cache, a, stream);
 }

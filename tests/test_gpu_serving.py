@@ -220,14 +220,16 @@ def test_chunk_attn_replayed_with_other_lengths(ra):
                   k=torch.zeros((2, 90, Hkv, bs, d), dtype=BF, device=DEV), v=torch.zeros((2, 90, Hkv, bs, d), dtype=BF, device=DEV))
         ws = torch.empty(ra.cp_chunk_attn_workspace_size(Hq, Hkv, d), dtype=torch.uint8, device=DEV)
         o, lse = torch.zeros((40, Hq, d), dtype=BF, device=DEV), torch.zeros((40, Hq), device=DEV)
-        call = lambda: ra.cp_chunk_attn(st["q"], st["k"], st["v"], st["t"], st["s"], st["c"], I, pcp, dcp, workspace=ws, o=o,  # noqa
-                                        lse=lse)
+
+        def call():
+            ra.cp_chunk_attn(st["q"], st["k"], st["v"], st["t"], st["s"], st["c"], I, pcp, dcp, workspace=ws, o=o, lse=lse)
+
         call()
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             call()
-        graphs.append((st, o, lse, g, call))
+        graphs.append((st, o, lse, g, ws))     # the workspace lives as long as its graph
     for ctx, n in [([1000, 3, 64], [1, 1, 1]), ([700, 40, 1], [30, 9, 1]), ([5, 1200, 0], [5, 20, 0])]:
         refs = []
         for i, (st, o, lse, g, _) in enumerate(graphs):
