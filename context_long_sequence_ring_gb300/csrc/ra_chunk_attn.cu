@@ -151,76 +151,51 @@ struct Plan {
   __device__ long long lo(int c) const { return min(total, share * c); }
 };
 
-// The total cost, and the request that holds cost position `lo_of(plan)` with the cost
-// before it, found by all NT threads of the block (smem scratch).
-struct PlanScratch {
-  long long warp_sum[kChunkThreads / 32];
-  long long pre;
-  int r;
-  Req q;
-};
-__device__ __forceinline__ long long block_scan(long long v, PlanScratch& s, long long& sum) {
-  constexpr int NT = kChunkThreads;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) s.warp_sum[warp] = x;
-  __syncthreads();
-  long long before = 0;
-  sum = 0;
-#pragma unroll
-  for (int i = 0; i < NT / 32; ++i) {
-    const long long w = s.warp_sum[i];
-    if (i < warp) before += w;
-    sum += w;
-  }
-  return before + x - v;
-}
-// Fills the scratch with the request that holds the start of part `part` (r = -1: the part is empty).
-__device__ __forceinline__ void make_plan(const ChunkArgs& a, int part, PlanScratch& s, Plan& plan) {
-  constexpr int NT = kChunkThreads;
-  long long total = 0, mine = 0, cost = 0, sum;
-  Req q;
-  if (threadIdx.x == 0) s.r = -1;
-  for (int base = 0; base < a.R; base += NT) {
-    const int i = base + threadIdx.x;
+// The total cost and, in the lane that returns true, the request that holds the start of part `part` with the
+// cost before it (none: the part is empty).  One warp, a request per lane.
+__device__ __forceinline__ bool make_plan(const ChunkArgs& a, int part, Plan& plan, Req& q, long long& pre) {
+  const int lane = threadIdx.x & 31;
+  long long total = 0, cost = 0;
+  for (int base = 0; base < a.R; base += 32) {
     cost = 0;
-    if (i < a.R) {
-      q = load_req(a, i);
+    if (base + lane < a.R) {
+      q = load_req(a, base + lane);
       cost = a.c.Hkv * q.prefix(q.items);
     }
-    mine = total + block_scan(cost, s, sum);
+    pre = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += y;
+    }
+    const long long sum = __shfl_sync(0xffffffffu, pre, 31);
+    pre += total - cost;
     total += sum;
   }
   plan.total = total;
   plan.share = max(kMinShare, (total + kCtas - 1) / kCtas);
   const long long lo = plan.lo(part);
-  if (lo < total) {
-    long long at = 0;
-    for (int base = 0; base < a.R; base += NT) {
-      const int i = base + threadIdx.x;
-      if (a.R > NT) {
-        cost = 0;
-        if (i < a.R) {
-          q = load_req(a, i);
-          cost = a.c.Hkv * q.prefix(q.items);
-        }
-        mine = at + block_scan(cost, s, sum);
-        at += sum;
-      }
-      if (cost > 0 && mine <= lo && lo < mine + cost) {
-        s.r = i;
-        s.pre = mine;
-        s.q = q;
-      }
+  if (lo >= total) return false;
+  if (a.R <= 32) return pre <= lo && lo < pre + cost;
+  long long at = 0;
+  for (int base = 0; base < a.R; base += 32) {
+    cost = 0;
+    if (base + lane < a.R) {
+      q = load_req(a, base + lane);
+      cost = a.c.Hkv * q.prefix(q.items);
     }
+    pre = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += y;
+    }
+    const long long sum = __shfl_sync(0xffffffffu, pre, 31);
+    pre += at - cost;
+    at += sum;
+    if (at > lo) return pre <= lo && lo < pre + cost;
   }
-  __syncthreads();
+  return false;
 }
 
 // One row tile (pair) of a part, as the roles read it: K/V tiles [t0, t0 + nt) of `all`.
@@ -246,13 +221,14 @@ struct SegIter {
   Req q;
   int r, g, k;
   bool live, fresh;          // fresh: (r, g, k) has not been looked at yet
-  __device__ SegIter(const ChunkArgs& args, const Plan& plan, int part, const PlanScratch& ps) : a(args) {
+  __device__ SegIter(const ChunkArgs& args, const Plan& plan, int part, const Req& first, long long pre, bool any)
+      : a(args), q(first) {
+    live = any;
+    if (!any) return;
     lo = plan.lo(part);
     hi = plan.lo(part + 1);
-    r = ps.r;
-    q = ps.q;
-    live = fresh = true;
-    const long long pre = ps.pre;
+    r = q.r;
+    fresh = true;
     const long long per_head = q.prefix(q.items), d = lo - pre;
     g = static_cast<int>(__fdividef(static_cast<float>(d), static_cast<float>(per_head)));   // one off at most
     g = min(g, a.c.Hkv - 1);
@@ -303,14 +279,30 @@ struct SegIter {
 };
 
 // ------------------------------------------------------------------ softmax
-// One online-softmax step of the row at tensor-memory address s_addr; as
-// softmax_row, with the mask given as a functor on 32-column chunks, and rows
-// that are not in use (their scores may be NaN) left out of the votes.
-template <class Mask>
-__device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool masked, bool row_ok, const Mask& mask,
-                                              float scale, float& m, float& l, uint32_t (&pk)[BN / 2]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// One online-softmax step of the row at tensor-memory address s_addr (BN fp32
+// columns, raw Q.K^T): P in bf16 pairs goes over the first BN/2 columns, m
+// (log2 units) and l are updated; returns the factor O must be scaled by.
+// As in the ring kernel a tile is first taken in one pass against the running
+// maximum, which stands while no chunk's sum of p exceeds 2^8; a tile in which it
+// does, a first tile and a masked one take two passes (maximum, then exps).
+// The two passes are rolled loops: they run once or twice per row tile, where
+// fetching unrolled code took longer than running it.
+// lm: visible columns of each 16, 8 bits each.  Rows that are not in use may
+// hold NaN scores: they are left out of the votes.
+__device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool masked, bool row_ok, uint64_t lm,
+                                              float scale, float& m, float& l) {
   const uint64_t sc2 = f2pack(scale, scale);
-  if (!first) {
+  if (!first && !masked) {
+    uint32_t pk[BN / 2];
     const uint64_t negm2 = f2pack(-m, -m);
     bool grow = __any_sync(0xffffffffu, row_ok && m == -CUDART_INF_F);
     float lsum = 0.f;
@@ -323,7 +315,6 @@ __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool 
       uint32_t (&x)[32] = (c & 1) ? xb : xa;
       uint32_t (&y)[32] = (c & 1) ? xa : xb;
       if (c + 1 < BN / 32) tmem_ld32(s_addr + 32 * (c + 1), y);
-      if (masked) mask(x, c);
       uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
       chunk_exp_pack(x, sc2, negm2, acc0, acc1, &pk[16 * c]);
       float a0, a1, b0, b1;
@@ -336,17 +327,29 @@ __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool 
     }
     if (!grow) {
       l += lsum;
+      tmem_st32(s_addr, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+      tmem_st32(s_addr + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
       return 1.f;
     }
   }
-  float mx = -CUDART_INF_F;
-#pragma unroll
-  for (int c = 0; c < BN / 32; ++c) {
-    uint32_t x[32];
+  auto load = [&](uint32_t (&x)[32], int c) {
     tmem_ld32(s_addr + 32 * c, x);
     tmem_wait_ld();
-    if (masked) mask(x, c);
-    mx = fmaxf(mx, chunk_mask_max(x, 32 * c, false, 0));
+    if (masked) {
+      const int l0 = static_cast<int>(lm >> (16 * c)) & 255, l1 = static_cast<int>(lm >> (16 * c + 8)) & 255;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i >= l0) x[i] = __float_as_uint(-CUDART_INF_F);
+        if (i >= l1) x[16 + i] = __float_as_uint(-CUDART_INF_F);
+      }
+    }
+  };
+  float mx = -CUDART_INF_F;
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t x[32];
+    load(x, c);
+    mx = fmaxf(mx, chunk_mask_max(x, 0, false, 0));
   }
   const float m_tile = mx * scale;
   const bool need = first || (m_tile > m + 8.f);
@@ -355,13 +358,12 @@ __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool 
   const float alpha = first ? 0.f : ex2(m - m_ref);
   const uint64_t negm2 = f2pack(-m_ref, -m_ref);
   uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-  for (int c = 0; c < BN / 32; ++c) {
-    uint32_t x[32];
-    tmem_ld32(s_addr + 32 * c, x);
-    tmem_wait_ld();
-    if (masked) mask(x, c);
-    chunk_exp_pack(x, sc2, negm2, acc0, acc1, &pk[16 * c]);
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {   // P of chunk c goes over scores that have been read
+    uint32_t x[32], pk[16];
+    load(x, c);
+    chunk_exp_pack(x, sc2, negm2, acc0, acc1, pk);
+    tmem_st16(s_addr + 16 * c, pk);
   }
   float a0, a1, b0, b1;
   f2unpack(acc0, a0, a1);
@@ -383,11 +385,11 @@ __device__ __forceinline__ int unit_visible(const ChunkArgs& a, int vb, int sub,
 
 // Visible columns (a prefix, 0..16) of each 16 columns of a tile, 8 bits each.  `check`: some block of this
 // CTA's work was bad, leave out the tokens of such blocks.
-__device__ __forceinline__ void tile_limits(const ChunkArgs& a, int r, bool check, int tile, int lim, uint32_t (&lm)[2]) {
+__device__ __forceinline__ void tile_limits(const ChunkArgs& a, int r, bool check, int tile, int lim, uint64_t& lm) {
   int rem, w, v = 0;
   int vb = a.by_vbu.div(tile << a.lupt, rem), sub = a.c.by_W.div(rem, w);
-  lm[0] = lm[1] = 0;
-#pragma unroll
+  lm = 0;
+#pragma unroll 1
   for (int i = 0; i < 8; ++i) {
     if (a.lu == 4 || !(i & 1)) {
       v = unit_visible(a, vb, sub, w, lim);
@@ -403,7 +405,7 @@ __device__ __forceinline__ void tile_limits(const ChunkArgs& a, int r, bool chec
         }
       }
     }
-    lm[i >> 2] |= static_cast<uint32_t>(min(v, 16)) << (8 * (i & 3));
+    lm |= static_cast<uint64_t>(min(v, 16)) << (8 * i);
     v = max(v - 16, 0);
   }
 }
@@ -424,7 +426,6 @@ struct __align__(1024) ChunkSmem {
   uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2], ml_full, ml_empty, drain;
   float2 ml[BM];
   Segment seg[kSegs];
-  PlanScratch plan;
   uint32_t tmem_base;
   int abort_flag, bad_block;
 };
@@ -479,13 +480,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm.abort_flag;
   const long long lim = a.wait_limit;
-
-  Plan plan;
-  make_plan(a, blockIdx.x, sm.plan, plan);
-  if (sm.plan.r < 0) {   // no work for this CTA
-    if (threadIdx.x == 0) a.join[blockIdx.x].used = 0;
-    return;
-  }
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
@@ -778,12 +772,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (!(ok = warp_wait(smem_u32(&sm.v_dirty[ring.st]), (dirty_ph >> ring.st) & 1, abort_flag, lim, 540))) break;
           dirty_ph ^= 1u << ring.st;
           if (!(ok = warp_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 541))) break;
-          uint32_t lm[2];
+          uint64_t lm;
           tile_limits(a, sg.r, false, sg.t0 + j, sg.L, lm);
-#pragma unroll
+#pragma unroll 1
           for (int i0 = 0; i0 < BN; i0 += 32) {
             const int i = i0 + lane;
-            if ((lane & 15) >= static_cast<int>((lm[i0 >> 6] >> (8 * ((i0 >> 4) & 3) + (lane & 16 ? 8 : 0))) & 255)) {
+            if ((lane & 15) >= (static_cast<int>(lm >> (8 * (i >> 4))) & 255)) {
 #pragma unroll
               for (int s = 0; s < SLABS; ++s)
 #pragma unroll
@@ -802,11 +796,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   } else if (warp == 3) {
     // ============================================================ segments of this part, announced to the other roles
-    if (lane == 0) {
-      SegIter it(a, plan, blockIdx.x, sm.plan);
-      bool more = true, left = false;
-      for (uint32_t i = 0; more; ++i) {
-        more = it.next(sg);
+    Plan plan;
+    Req first;
+    long long pre;
+    const bool mine = make_plan(a, blockIdx.x, plan, first, pre);
+    const unsigned owner = __ballot_sync(0xffffffffu, mine);
+    if (mine || (owner == 0 && lane == 0)) {
+      bool more = mine, left = false;
+      if (!mine) first = Req{};
+      SegIter it(a, plan, blockIdx.x, first, pre, mine);
+      uint32_t i = 0;
+      do {
+        if (more) more = it.next(sg);
         if (!more) sg.pair = -1;
         const int b = i & (kSegs - 1);
         if (!mbar_wait(smem_u32(&sm.seg_empty[b]), ((i / kSegs) & 1) ^ 1, abort_flag, lim, 572)) break;
@@ -816,9 +817,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           a.join[blockIdx.x] = Join{sg, it.at, it.cost, plan.total, plan.share, 1};
           left = true;
         }
-      }
+        ++i;
+      } while (more);
       if (!left) a.join[blockIdx.x].used = 0;
     }
+    __syncwarp();
   } else if (warp >= 4) {
     // ============================================================ softmax + epilogue (slot h)
     const int h = (warp - 4) >> 2;
@@ -863,24 +866,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const bool bad = *reinterpret_cast<volatile int*>(&sm.bad_block) != 0;
           const int tile = sg.t0 + j;
           const bool masked = tile >= clean || bad;
-          uint32_t lm[2] = {0, 0};
+          uint64_t lm = 0;
           if (masked) tile_limits(a, sg.r, bad, tile, vis, lm);
-          auto mask = [&](uint32_t (&x)[32], int c) {
-            const uint32_t b = lm[c >> 1] >> (16 * (c & 1));
-            const int l0 = b & 255, l1 = (b >> 8) & 255;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (i >= l0) x[i] = __float_as_uint(-CUDART_INF_F);
-              if (i >= l1) x[16 + i] = __float_as_uint(-CUDART_INF_F);
-            }
-          };
-          uint32_t pk[BN / 2];
-          const float alpha = softmax_step(t_lane + colS, n_mine == 0, masked, row_ok, mask, a.scale_log2, m, l, pk);
+          const float alpha = softmax_step(t_lane + colS, n_mine == 0, masked, row_ok, lm, a.scale_log2, m, l);
           if (n_mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
             // O_h must hold the previous P.V before it is rescaled
             if (!(ok = warp_wait(smem_u32(&sm.pv_done[h]), (pv_cnt[h] + n_mine - 1) & 1, abort_flag, lim, 552 + h))) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c4 = 0; c4 < D / 32; ++c4) {
               uint32_t orr[32];
               tmem_ld32(t_lane + colO + 32 * c4, orr);
@@ -890,8 +883,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               tmem_st32(t_lane + colO + 32 * c4, orr);
             }
           }
-          tmem_st32(t_lane + colS, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
-          tmem_st32(t_lane + colS + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
           tmem_wait_st();
         }
         ++n_mine;
@@ -934,7 +925,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       f1 *= inv_l;
       if (warp_live) {
         float* po = a.o_part + ((part * 2 + (pair ? h : 0)) * BM + row) * D;
-#pragma unroll
+#pragma unroll 1
         for (int c4 = 0; c4 < D / 32; ++c4) {
           uint32_t x[32];
           tmem_ld32(t_lane + colO + 32 * c4, x);
@@ -1039,7 +1030,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] *= old;
       const int np = min(32, used - p0);
-#pragma unroll 4
+#pragma unroll 8
       for (int p = 0; p < np; ++p) {
         const float wp = __shfl_sync(0xffffffffu, w, p);
         const float* src = a.o_part + (static_cast<int64_t>(parts[p0 + p] * 2 + h) * BM + row) * D + E * lane;
