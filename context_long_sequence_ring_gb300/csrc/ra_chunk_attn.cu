@@ -39,6 +39,7 @@
 // Tensor memory: S_h = columns [128h, +128) with P_h (bf16) over its first 64,
 // O_h = columns [256 + 128h, +D).
 #include <algorithm>
+#include <cmath>
 
 #include "ra_attn_tc.cuh"
 #include "ra_paged.cuh"
@@ -59,7 +60,9 @@ struct ChunkArgs {
   int R, Hq, G, causal, out_bf16;
   int lu, lupt, nsub;             // log2 slots of a unit, log2 units of a tile, units of a block
   FastDiv by_vbu;                 // by the units of a virtual block
-  int tpt;                        // tokens of a row tile
+  int tpt, f_split, over;         // tokens of a row tile; cost of a key in a split tile (5 in a pair), see Req
+  int cost_shift;
+  FastDiv by_tpi;                 // by the tokens of a pair of row tiles
   float scale_log2;
   void* o;                        // [T, Hq, D]
   float* lse;                     // [T, Hq] or NULL
@@ -70,18 +73,17 @@ struct ChunkArgs {
 };
 
 // ------------------------------------------------------------------ work
-// A request as the work division sees it.  Costs are in keys times a factor:
-// a pair tile takes about 5/4 of the time of a split tile.
+// A request as the work division sees it.  The cost of an item is in keys times what a key costs: a pair tile
+// against a split tile takes about 5/4 of the time at D = 128 (the one bound by the tensor cores, the other by
+// HBM) and twice the time at D = 64 (both bound by the exps); prologue and epilogue of an item take
+// as long as `over` keys of its mode.  Costs are 32-bit numbers, in units of 2^cost_shift that the host
+// chooses from the sizes so that their sum fits.
 struct Req {
   int r, q0, n, L, items;         // request, first query row, queries, context, row tiles (pairs of them) per head
   long long pos0;                 // position of query 0
-  long long base, slope, f;       // cost of item k: f * (base + slope * (k + 1))
+  uint32_t base, slope;           // cost of item k: base + slope * (k + 1)
   bool pair;
-  __device__ long long prefix(long long k) const { return f * (k * base + slope * (k * (k + 1) / 2)); }
 };
-
-constexpr long long kItemOverhead = 192;  // keys: prologue and epilogue of a row tile
-constexpr long long kMinShare = 4 * 256;  // cost of the smallest part of a CTA
 
 __device__ __forceinline__ Req load_req(const ChunkArgs& a, int r) {
   Req q;
@@ -91,12 +93,12 @@ __device__ __forceinline__ Req load_req(const ChunkArgs& a, int r) {
   q.L = paged_len(a.c, ctx, 511);
   q.pos0 = static_cast<long long>(ctx) - q.n;
   q.pair = q.n > a.tpt;
-  const int tpi = q.pair ? 2 * a.tpt : a.tpt;
-  q.items = (q.n + tpi - 1) / tpi;
+  q.items = q.pair ? a.by_tpi.div(q.n + 2 * a.tpt - 1) : (q.n > 0);
   const long long before = q.pos0 < 0 ? 0 : (q.pos0 < q.L ? q.pos0 : q.L);
-  q.base = kItemOverhead + (a.causal ? before : q.L);
-  q.slope = a.causal ? tpi : 0;
-  q.f = q.pair ? 5 : 4;
+  const long long keys = (q.pair ? 160 : a.over) + (a.causal ? before : q.L);
+  const int f = q.pair ? 5 : a.f_split;
+  q.base = static_cast<uint32_t>(keys * f >> a.cost_shift) + 1;
+  q.slope = a.causal ? static_cast<uint32_t>((q.pair ? 2 : 1) * a.tpt * f) >> a.cost_shift : 0;
   return q;
 }
 
@@ -137,62 +139,93 @@ __device__ __forceinline__ int tiles_of(const ChunkArgs& a, const Req& q, int k)
 
 // Tiles [t0, t1) of an item of nt tiles and cost [at, at + cost) that part [lo, hi) takes.  Fractions are
 // taken in fp32: a boundary gives the same tile to both of its sides, whatever its rounding.
-__device__ __forceinline__ int cut_at(long long off, long long cost, int nt) {
+__device__ __forceinline__ int cut_at(uint32_t off, uint32_t cost, int nt) {
   return min(nt, static_cast<int>(__fdividef(static_cast<float>(off), static_cast<float>(cost)) * static_cast<float>(nt)));
 }
-__device__ __forceinline__ void cut(long long lo, long long hi, long long at, long long cost, int nt, int& t0, int& t1) {
+__device__ __forceinline__ void cut(uint32_t lo, uint32_t hi, uint32_t at, uint32_t cost, int nt, int& t0, int& t1) {
   t0 = lo <= at ? 0 : cut_at(lo - at, cost, nt);
   t1 = hi >= at + cost ? nt : cut_at(hi - at, cost, nt);
 }
 
-// Part c of the work is [lo(c), lo(c + 1)), empty from the first c with lo(c) = total on.
+// Part c of the work is [lo(c), lo(c + 1)), empty from the first c with lo(c) = total on.  Where an equal
+// cut leaves few items to a part, and cutting each item into pieces of its own costs less than the second item
+// that a part would take up, lengths are counted in such pieces (piece > 0: the cost of one; share is 1 then).
 struct Plan {
-  long long total, share;
-  __device__ long long lo(int c) const { return min(total, share * c); }
+  uint32_t total, share;
+  float piece;
+  __device__ uint32_t lo(int c) const { return min(total, share * c); }
+  __device__ uint32_t cost(const Req& q, int k) const {
+    const uint32_t c = q.base + q.slope * (k + 1);
+    return piece > 0.f ? static_cast<uint32_t>(__fdividef(static_cast<float>(c), piece)) + 1 : c;
+  }
+  // cost of items 0 .. k-1 of a head
+  __device__ uint32_t prefix(const Req& q, int k) const {
+    if (piece <= 0.f) return k * q.base + q.slope * (static_cast<uint32_t>(k) * (k + 1) / 2);
+    uint32_t sum = 0;
+#pragma unroll 1
+    for (int i = 0; i < k; ++i) sum += cost(q, i);
+    return sum;
+  }
 };
 
-// The total cost and, in the lane that returns true, the request that holds the start of part `part` with the
+// The plan and, in the lane that returns true, the request that holds the start of part `part` with the
 // cost before it (none: the part is empty).  One warp, a request per lane.
-__device__ __forceinline__ bool make_plan(const ChunkArgs& a, int part, Plan& plan, Req& q, long long& pre) {
+__device__ __forceinline__ bool make_plan(const ChunkArgs& a, int part, Plan& plan, Req& q, uint32_t& pre) {
   const int lane = threadIdx.x & 31;
-  long long total = 0, cost = 0;
+  uint32_t total = 0, items = 0;
+  plan.piece = 0.f;
+#pragma unroll 1
   for (int base = 0; base < a.R; base += 32) {
-    cost = 0;
-    if (base + lane < a.R) {
-      q = load_req(a, base + lane);
-      cost = a.c.Hkv * q.prefix(q.items);
-    }
-    pre = cost;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre += y;
-    }
-    const long long sum = __shfl_sync(0xffffffffu, pre, 31);
-    pre += total - cost;
-    total += sum;
+    q.items = 0;
+    if (base + lane < a.R) q = load_req(a, base + lane);
+    total += a.c.Hkv * plan.prefix(q, q.items);
+    items += a.c.Hkv * q.items;
   }
+  total = __reduce_add_sync(0xffffffffu, total);
+  items = __reduce_add_sync(0xffffffffu, items);
   plan.total = total;
-  plan.share = max(kMinShare, (total + kCtas - 1) / kCtas);
-  const long long lo = plan.lo(part);
-  if (lo >= total) return false;
-  if (a.R <= 32) return pre <= lo && lo < pre + cost;
-  long long at = 0;
-  for (int base = 0; base < a.R; base += 32) {
-    cost = 0;
-    if (base + lane < a.R) {
-      q = load_req(a, base + lane);
-      cost = a.c.Hkv * q.prefix(q.items);
+  plan.share = max((256u * a.f_split) >> a.cost_shift, (total + kCtas - 1) / kCtas);
+  if (items <= kCtas / 2) {
+    // pieces of at most total / (kCtas - items): at most kCtas of them, since an item has one incomplete piece
+    const float p = max(static_cast<float>(plan.share), __fdividef(1.001f * static_cast<float>(total), static_cast<float>(kCtas - items)));
+    if (p < static_cast<float>(plan.share + ((a.f_split * a.over) >> a.cost_shift))) {
+      plan.piece = p;
+      uint32_t n = 0;
+#pragma unroll 1
+      for (int base = 0; base < a.R; base += 32) {
+        if (a.R > 32) {
+          q.items = 0;
+          if (base + lane < a.R) q = load_req(a, base + lane);
+        }
+        n += a.c.Hkv * plan.prefix(q, q.items);
+      }
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (n <= kCtas) {
+        plan.total = n;
+        plan.share = 1;
+      } else {
+        plan.piece = 0.f;
+      }
     }
-    pre = cost;
+  }
+  const uint32_t lo = plan.lo(part);
+  if (lo >= plan.total) return false;
+  uint32_t at = 0;
+#pragma unroll 1
+  for (int base = 0; base < a.R; base += 32) {
+    if (a.R > 32) {
+      q.items = 0;
+      if (base + lane < a.R) q = load_req(a, base + lane);
+    }
+    const uint32_t cost = a.c.Hkv * plan.prefix(q, q.items);
+    uint32_t x = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre += y;
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    const long long sum = __shfl_sync(0xffffffffu, pre, 31);
-    pre += at - cost;
-    at += sum;
+    pre = at + x - cost;
+    at += __shfl_sync(0xffffffffu, x, 31);
     if (at > lo) return pre <= lo && lo < pre + cost;
   }
   return false;
@@ -210,38 +243,37 @@ struct Segment {
 // A row tile that several parts share, as its first part leaves it for the joining kernel.
 struct Join {
   Segment s;
-  long long at, cost, total, share;
+  uint32_t at, cost;
+  Plan plan;
   int used;                  // 0: this part has none
 };
 
 // Walks the items of part [lo, hi) in order.
 struct SegIter {
   const ChunkArgs& a;
-  long long lo, hi, at, cost;
+  const Plan& plan;
+  uint32_t lo, hi, at, cost;
   Req q;
   int r, g, k;
   bool live, fresh;          // fresh: (r, g, k) has not been looked at yet
-  __device__ SegIter(const ChunkArgs& args, const Plan& plan, int part, const Req& first, long long pre, bool any)
-      : a(args), q(first) {
+  __device__ SegIter(const ChunkArgs& args, const Plan& pl, int part, const Req& first, uint32_t pre, bool any)
+      : a(args), plan(pl), q(first) {
     live = any;
     if (!any) return;
     lo = plan.lo(part);
     hi = plan.lo(part + 1);
     r = q.r;
     fresh = true;
-    const long long per_head = q.prefix(q.items), d = lo - pre;
-    g = static_cast<int>(__fdividef(static_cast<float>(d), static_cast<float>(per_head)));   // one off at most
-    g = min(g, a.c.Hkv - 1);
-    if (g * per_head > d) --g;
-    if ((g + 1) * per_head <= d) ++g;
-    const long long off = d - g * per_head;
+    const uint32_t per_head = plan.prefix(q, q.items), d = lo - pre;
+    g = d / per_head;
+    const uint32_t off = d - g * per_head;
     int x = 0, y = q.items - 1;   // largest k with prefix(k) <= off
     while (x < y) {
       const int mid = (x + y + 1) >> 1;
-      if (q.prefix(mid) <= off) x = mid; else y = mid - 1;
+      if (plan.prefix(q, mid) <= off) x = mid; else y = mid - 1;
     }
     k = x;
-    at = pre + g * per_head + q.prefix(k);
+    at = pre + g * per_head + plan.prefix(q, k);
   }
   __device__ void advance() {
     at += cost;
@@ -260,7 +292,7 @@ struct SegIter {
       if (!fresh) advance();
       fresh = false;
       if (!live || at >= hi) return false;
-      cost = q.f * (q.base + q.slope * (k + 1));
+      cost = plan.cost(q, k);
       s.all = tiles_of(a, q, k);
       int t1;
       cut(lo, hi, at, cost, s.all, s.t0, t1);
@@ -511,6 +543,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     tmem_alloc(smem_u32(&sm.tmem_base), kTmemCols);
     tmem_relinquish();
   }
+  Plan plan;
+  Req first{};
+  uint32_t pre = 0;
+  bool mine = false;
+  if (warp == 3) mine = make_plan(a, blockIdx.x, plan, first, pre);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -539,21 +576,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int nt = sg.nt;
       if (nt <= 0) continue;
       const int la = sg.pair ? 1 : 2, nq = sg.pair ? 2 : 1;
-      for (int h = 0; h < nq && ok; ++h) {
-        const int b = sg.pair ? h : q_next;
-        ok = warp_wait(smem_u32(&sm.q_empty[b]), (q_cnt[b] & 1) ^ 1, abort_flag, lim, 520);
-        if (!ok) break;
-        ++q_cnt[b];
-        if (lane == 0) {
-          const uint32_t qb = smem_u32(&sm.q_full[b]);
-          mbar_arrive_expect_tx(qb, SLABS * a.tpt * a.G * 128);
-          const int row = sg.q0 + sg.tok0 + h * a.tpt;
-          for (int s = 0; s < SLABS; ++s)
-            tma_load_3d(smem_u32(sm.q[b] + s * BM * 128), &tmQ, qb, 64 * s, sg.g * a.G, row);
-        }
-        __syncwarp();
-      }
-      if (!sg.pair) q_next ^= 1;
       auto load_tile = [&](const CUtensorMap* map, int blk, int s0, int w, bool to_clean) -> bool {
         if (!warp_wait(smem_u32(&sm.kv_empty[ring.st]), ring.ph ^ 1, abort_flag, lim, 521)) return false;
         const uint32_t bar = smem_u32(&sm.kv_full[ring.st]);
@@ -606,6 +628,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         checked(k1);
         ok = load_tile(&tmK, k1.blk, k1.s0, k1.w, false);
       }
+      for (int h = 0; h < nq && ok; ++h) {
+        const int b = sg.pair ? h : q_next;
+        ok = warp_wait(smem_u32(&sm.q_empty[b]), (q_cnt[b] & 1) ^ 1, abort_flag, lim, 520);
+        if (!ok) break;
+        ++q_cnt[b];
+        if (lane == 0) {
+          const uint32_t qb = smem_u32(&sm.q_full[b]);
+          mbar_arrive_expect_tx(qb, SLABS * a.tpt * a.G * 128);
+          const int row = sg.q0 + sg.tok0 + h * a.tpt;
+          for (int s = 0; s < SLABS; ++s)
+            tma_load_3d(smem_u32(sm.q[b] + s * BM * 128), &tmQ, qb, 64 * s, sg.g * a.G, row);
+        }
+        __syncwarp();
+      }
+      if (!sg.pair) q_next ^= 1;
       for (int j = 0; j < nt && ok; ++j) {
         const Unit ahead = locate(j + la + 1);
         if (!(ok = load_tile(&tmV, v.blk, v.s0, v.w, j >= sg.dirty))) break;
@@ -796,14 +833,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   } else if (warp == 3) {
     // ============================================================ segments of this part, announced to the other roles
-    Plan plan;
-    Req first;
-    long long pre;
-    const bool mine = make_plan(a, blockIdx.x, plan, first, pre);
     const unsigned owner = __ballot_sync(0xffffffffu, mine);
     if (mine || (owner == 0 && lane == 0)) {
       bool more = mine, left = false;
-      if (!mine) first = Req{};
       SegIter it(a, plan, blockIdx.x, first, pre, mine);
       uint32_t i = 0;
       do {
@@ -814,7 +846,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         sm.seg[b] = sg;
         mbar_arrive(smem_u32(&sm.seg_full[b]));
         if (more && sg.t0 == 0 && sg.nt < sg.all) {
-          a.join[blockIdx.x] = Join{sg, it.at, it.cost, plan.total, plan.share, 1};
+          a.join[blockIdx.x] = Join{sg, it.at, it.cost, plan, 1};
           left = true;
         }
         ++i;
@@ -991,8 +1023,8 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
   if (static_cast<int>(blockIdx.y) * (kMergeThreads / 32) >= rows) return;
   if (warp == 0) {
     // the partials, in order: of this part, and of those that follow
-    const Plan plan{jn.total, jn.share};
-    const long long at = jn.at, cost = jn.cost;
+    const Plan plan = jn.plan;
+    const uint32_t at = jn.at, cost = jn.cost;
     int n = 0;
     for (int c0 = blockIdx.x; c0 < kCtas && plan.lo(c0) < at + cost; c0 += 32) {
       const int c = c0 + lane;
@@ -1145,6 +1177,14 @@ extern "C" ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const 
   a.nsub = block_size >> a.lu;
   a.by_vbu = fast_div(static_cast<int64_t>(a.nsub) * a.c.W);
   a.tpt = BM / a.G;
+  a.by_tpi = fast_div(2 * a.tpt);
+  a.f_split = d == 128 ? 4 : 2;
+  a.over = d == 128 ? 224 : 384;
+  // the largest sum of costs these sizes allow stays below 2^31
+  const double most = static_cast<double>(Hkv) * (static_cast<double>(T) / a.tpt + R) *
+                      (5.0 * (static_cast<double>(max_vblocks) * a.c.V + T + 512) + 1);
+  a.cost_shift = 0;
+  while (std::ldexp(most, -a.cost_shift) > 1.0e9) ++a.cost_shift;
   a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(d))) * 1.4426950408889634f;
   a.o = o; a.lse = lse;
   a.o_part = static_cast<float*>(workspace);
