@@ -1,61 +1,549 @@
 // The attention weight that every cached token receives from a chunk of
 // queries: the column sums of the softmax, from the scores and the rows' LSE.
 //
-// Simple form: one warp per (token, K/V head) runs over the queries.
-#include <math_constants.h>
-
+// Mathematics.  w[x, g] += sum_{i, h in g} 2^(s_ihx * scale log2 e - lse_ih log2 e)
+// over the queries i that see token x.  The rows' LSE is known, so that nothing
+// is rescaled and one pass over K suffices.
+//
+// The score tile is computed transposed, S^T = K Q^T (128 keys x up to 128 query
+// rows): a key is a lane of tensor memory, a thread sums its key's row, and no sum
+// crosses threads.  A CTA holds two key tiles ("slots") and lets the
+// request's query tiles pass by: each Q tile that TMA brings in serves both.
+// Scores are double buffered per slot in tensor memory (2 x 2 x 128 columns),
+// so that the exps never wait for the tensor core.
+//
+// What bounds it: one exp per (query row, key); the SM's 16 exps per cycle make
+// a 128 x 128 tile 1024 cycles, twice the score product's.  For single tokens
+// (few query rows) the columns are trimmed to the rows there are, and HBM is
+// the bound: K is read once (a pair of tiles of one head follows the next on the
+// same CTA, and the Q tile stays).
+//
+// Work.  The key tile pairs of all requests and heads lie on one axis of cost,
+// cut into 152 equal parts at pairs' borders; a pair's sum is made by one CTA in
+// a fixed order.
+//
+// Roles (384 threads): warp 0 TMA, warp 1 MMA issue, warp 2 LSE rows, warp 3
+// schedule, warps 4-7 and 8-11 exps and sums of slots 0 and 1.
 #include <algorithm>
 
-#include "ra_paged.cuh"
+#include "ra_key_units.cuh"
 
 RA_DEFINE_ERROR_FETCH(fetch_error_attn_weights)
 
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kCtas = 152;
+constexpr int kWeightThreads = 384;
+constexpr int kSegs = 4, kSegReaders = 11;
+constexpr int kLseStages = 2;
 
-struct WeightParams {
-  const __nv_bfloat16 *q, *kc;
-  const float* lse;
+struct WeightArgs : KeyUnits {
   const int32_t *qsl, *ctx;
-  Paged c;
+  const float* lse;
   int64_t T;
   int R, Hq, G, causal;
+  int tpt, pair_q;        // tokens of a query tile; query tiles that a pair of key tiles spans under the causal mask
+  FastDiv by_tpt, by_G;
   float scale_log2;
   const float* w_in;
   float* w_out;
+  long long wait_limit;
 };
 
-template <int D>
-__global__ void __launch_bounds__(256) weights_simple_kernel(const WeightParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y, g = blockIdx.z;
-  int q0, n;
-  query_range(p.qsl, r, p.T, q0, n, 600);
-  const int L = paged_len(p.c, p.ctx[r], 601);
-  const int64_t pos0 = p.causal ? static_cast<int64_t>(p.ctx[r]) - n : L;  // position of the first query
-  for (int x = blockIdx.x * 8 + (threadIdx.x >> 5); x < L; x += gridDim.x * 8) {
-    const int64_t at = paged_row(p.c, r, x, g, 602);
-    if (at < 0) continue;
-    float k[E];
+// ------------------------------------------------------------------ work
+struct Req {
+  int r, q0, n, L, tiles, nq;   // request, first query row, queries, context, key tiles, query tiles
+  long long pos0;               // position of query 0
+  int k0;                       // pairs before it: the later ones meet fewer and fewer query tiles
+  __device__ int pairs() const { return (tiles + 1) >> 1; }
+};
+
+__device__ __forceinline__ Req load_req(const WeightArgs& a, int r) {
+  Req q;
+  q.r = r;
+  query_range(a.qsl, r, a.T, q.q0, q.n, 600);
+  const int32_t ctx = a.ctx[r];
+  q.L = paged_len(a.c, ctx, 601);
+  q.pos0 = static_cast<long long>(ctx) - q.n;
+  q.tiles = (units_below(a, q.L) + (1 << a.lupt) - 1) >> a.lupt;
+  q.nq = a.by_tpt.div(q.n + a.tpt - 1);
+  q.k0 = a.causal ? (q.pos0 <= 0 ? 0 : static_cast<int>(min(q.pos0 >> 8, 1ll << 30))) : 1 << 30;
+  return q;
+}
+
+// Cost of a pair: 5 for its loads, 4 for each query tile.
+__device__ __forceinline__ long long cost_of(const WeightArgs& a, const Req& q, int k) {
+  return 5 + 4ll * max(0, q.nq - max(0, k - q.k0) * a.pair_q);
+}
+// Cost of pairs 0 .. k-1.
+__device__ __forceinline__ long long prefix(const WeightArgs& a, const Req& q, int k) {
+  const long long full = min(k, q.k0 + 1);               // pairs that meet all query tiles
+  const long long m = min(k - static_cast<int>(full), a.pair_q > 0 ? q.nq / a.pair_q : 1 << 30);
+  return 5ll * k + 4 * (full * q.nq + m * q.nq - a.pair_q * (m * (m + 1) / 2));
+}
+
+struct Item {
+  int r, g, q0, n, L, pos0;     // as in Req; pos0 cut below at -n
+  int tile0, nkt;               // first key tile, key tiles (1 or 2)
+  int qf, nq;                   // first query tile and how many
+  int load_q, keep_q;           // single query tile: bring it in, keep it for the next item
+  int more;                     // 0: end of the part
+};
+
+__device__ __forceinline__ long long warp_scan(long long v) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) k[e] = __bfloat162float(p.kc[at * D + lane + 32 * e]) * p.scale_log2;
-    float w = 0.f;
-    for (int64_t i = pos0 >= x ? 0 : x - pos0; i < n; ++i)
-      for (int h = g * p.G; h < (g + 1) * p.G; ++h) {
-        const int64_t row = (q0 + i) * p.Hq + h;
-        const float lse = p.lse[row];
-        if (lse == -CUDART_INF_F) continue;
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s += k[e] * __bfloat162float(p.q[row * D + lane + 32 * e]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        w += exp2f(s - lse * kLog2e);
-      }
-    if (lane == 0) p.w_out[at] = (p.w_in && x < pos0 ? p.w_in[at] : 0.f) + w;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) >= o) v += y;
   }
+  return v;
+}
+
+// Walks the pairs whose start lies in part [lo, hi) of the cost axis.
+struct ItemIter {
+  const WeightArgs& a;
+  long long lo, hi, at;
+  Req q;
+  int g, k, pairs;
+  bool live, loaded;
+  __device__ ItemIter(const WeightArgs& args) : a(args), live(false), loaded(false) {}
+  // The request with the first cost at or past lo, found by the whole warp; the returned lane walks.
+  __device__ bool find(int part) {
+    const int lane = threadIdx.x & 31;
+    long long total = 0;
+#pragma unroll 1
+    for (int base = 0; base < a.R; base += 32) {
+      long long c = 0;
+      if (base + lane < a.R) {
+        q = load_req(a, base + lane);
+        c = a.c.Hkv * prefix(a, q, q.pairs());
+      }
+      total += __shfl_sync(0xffffffffu, warp_scan(c), 31);
+    }
+    const long long share = (total + kCtas - 1) / kCtas;
+    lo = min(total, share * part);
+    hi = min(total, share * (part + 1));
+    if (lo >= hi) return false;
+    long long before = 0;
+#pragma unroll 1
+    for (int base = 0; base < a.R; base += 32) {
+      long long c = 0;
+      if (base + lane < a.R) {
+        q = load_req(a, base + lane);
+        c = a.c.Hkv * prefix(a, q, q.pairs());
+      }
+      const long long x = warp_scan(c), pre = before + x - c;
+      before += __shfl_sync(0xffffffffu, x, 31);
+      if (before > lo) {
+        if (!(pre <= lo && lo < pre + c)) return false;
+        pairs = q.pairs();
+        const long long per_head = prefix(a, q, pairs);
+        g = static_cast<int>((lo - pre) / per_head);
+        const long long off = lo - pre - g * per_head;
+        int u = 0, v = pairs;               // first pair with prefix >= off (pairs: the next head's first)
+        while (u < v) {
+          const int mid = (u + v) >> 1;
+          if (prefix(a, q, mid) >= off) v = mid; else u = mid + 1;
+        }
+        k = u;
+        at = pre + g * per_head + prefix(a, q, k);
+        live = true;
+        skip();
+        return true;
+      }
+    }
+    return false;
+  }
+  // Past the last pair of a head: on to the next head, the next request that has any.
+  __device__ void skip() {
+    while (live && k >= pairs) {
+      k = 0;
+      loaded = false;
+      if (++g < a.c.Hkv) continue;
+      g = 0;
+      do {
+        if (++q.r >= a.R) { live = false; return; }
+        q = load_req(a, q.r);
+        pairs = q.pairs();
+      } while (pairs == 0);
+    }
+  }
+  __device__ bool next(Item& s) {
+    if (!live || at >= hi) return false;
+    s.r = q.r; s.g = g; s.q0 = q.q0; s.n = q.n; s.L = q.L;
+    s.pos0 = static_cast<int>(q.pos0 < -q.n ? -q.n : q.pos0);
+    s.tile0 = 2 * k;
+    s.nkt = min(2, q.tiles - 2 * k);
+    s.qf = 0;
+    if (a.causal) {   // the query tiles before the first that can see a key of the pair
+      int rem, off;
+      const int vb = a.by_vbu.div(s.tile0 << a.lupt, rem), s0 = a.c.by_W.div(rem) << a.lu;
+      const int first = vb * a.c.V + a.c.by_I.div(s0, off) * a.c.W * a.c.I + off;   // no key is before it
+      s.qf = first <= s.pos0 ? 0 : min(q.nq, a.by_tpt.div(first - s.pos0));
+    }
+    s.nq = q.nq - s.qf;
+    s.load_q = !loaded;
+    at += cost_of(a, q, k);
+    ++k;
+    loaded = q.nq == 1;
+    s.keep_q = loaded && k < pairs && at < hi;
+    s.more = 1;
+    skip();
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------ the kernel
+template <int D>
+constexpr int kKStages = D == 128 ? 4 : 8;
+template <int D>
+constexpr int kQStages = D == 128 ? 3 : 4;
+
+template <int D>
+struct __align__(1024) WeightSmem {
+  uint8_t k[kKStages<D>][BN * D * 2];
+  uint8_t q[kQStages<D>][BM * D * 2];
+  uint64_t k_full[kKStages<D>], k_empty[kKStages<D>], q_full[kQStages<D>], q_empty[kQStages<D>];
+  uint64_t l_full[kLseStages], l_empty[kLseStages], seg_full[kSegs], seg_empty[kSegs];
+  uint64_t s_full[2][2], s_empty[2][2], drain;
+  __align__(16) float neg_lse[kLseStages][BM];   // -lse * log2 e; -inf: the row adds nothing
+  Item item[kSegs];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(WeightSmem<128>) + 1024 <= 232448 && sizeof(WeightSmem<64>) + 1024 <= 232448, "227 KB of shared memory");
+
+struct ItemReader {
+  uint32_t at = 0;
+  template <class Smem>
+  __device__ bool next(Smem& sm, Item& s, volatile int* abort_flag, long long limit, bool whole_warp) {
+    const int i = at & (kSegs - 1);
+    const uint32_t bar = smem_u32(&sm.seg_full[i]), ph = (at / kSegs) & 1;
+    const bool ok = whole_warp ? warp_wait(bar, ph, abort_flag, limit, 670) : mbar_wait(bar, ph, abort_flag, limit, 671);
+    if (!ok) return false;
+    s = sm.item[i];
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || (threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.seg_empty[i]));
+    ++at;
+    return s.more != 0;
+  }
+};
+
+// Valid columns of a query tile.
+__device__ __forceinline__ int columns(const WeightArgs& a, const Item& s, int t) {
+  return min(s.n - t * a.tpt, a.tpt) * a.G;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWeightThreads, 1)
+    weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
+                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ WeightArgs a) {
+  constexpr int SLABS = D / 64, NK = kKStages<D>, NQ = kQStages<D>;
+  constexpr uint32_t kTileBytes = BM * D * 2;
+  extern __shared__ uint8_t smem_raw[];
+  WeightSmem<D>& sm = *reinterpret_cast<WeightSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sm.abort_flag;
+  const long long lim = a.wait_limit;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(smem_u32(&sm.k_full[s]), 1);
+      mbar_init(smem_u32(&sm.k_empty[s]), 1);
+    }
+    for (int s = 0; s < NQ; ++s) {
+      mbar_init(smem_u32(&sm.q_full[s]), 1);
+      mbar_init(smem_u32(&sm.q_empty[s]), 1);
+    }
+    for (int s = 0; s < kLseStages; ++s) {
+      mbar_init(smem_u32(&sm.l_full[s]), 1);
+      mbar_init(smem_u32(&sm.l_empty[s]), 8);
+    }
+    for (int s = 0; s < kSegs; ++s) {
+      mbar_init(smem_u32(&sm.seg_full[s]), 1);
+      mbar_init(smem_u32(&sm.seg_empty[s]), kSegReaders);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&sm.s_full[i >> 1][i & 1]), 1);
+      mbar_init(smem_u32(&sm.s_empty[i >> 1][i & 1]), 128);
+    }
+    mbar_init(smem_u32(&sm.drain), 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sm.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  ItemIter it(a);
+  bool mine = false;
+  if (warp == 3) mine = it.find(blockIdx.x);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  ItemReader items;
+  Item s;
+
+  if (warp == 0) {
+    // ============================================================ TMA producer (whole warp: a unit or a token per lane)
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmQ1);
+      tma_prefetch_desc(&tmK);
+    }
+    Ring<NK> kr;
+    Ring<NQ> qr;
+    uint32_t k_issued = 0, q_issued = 0;
+    bool ok = true;
+    const int oob = static_cast<int>(a.c.W * a.c.num_blocks * a.c.Hkv);   // past the last block: zero fill
+    while (ok && items.next(sm, s, abort_flag, lim, true)) {
+      if (s.nq <= 0) continue;
+      // blocks of both tiles first, so that their loads overlap
+      int blk[2], s0[2], w[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        int rem;
+        const int vb = a.by_vbu.div(((s.tile0 + h) << a.lupt) + lane, rem);
+        s0[h] = a.c.by_W.div(rem, w[h]) << a.lu;
+        blk[h] = -1;
+        if (h < s.nkt && lane >> a.lupt == 0 && static_cast<int64_t>(vb) * a.c.V < s.L)
+          blk[h] = a.c.table[static_cast<int64_t>(s.r) * a.c.max_vb + vb];
+      }
+      for (int h = 0; h < s.nkt && ok; ++h) {
+        ok = warp_wait(smem_u32(&sm.k_empty[kr.st]), kr.ph ^ 1, abort_flag, lim, 620);
+        if (!ok) break;
+        const uint32_t bar = smem_u32(&sm.k_full[kr.st]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
+        __syncwarp();
+        if (lane >> a.lupt == 0) {
+          const int b = h ? blk[1] : blk[0];
+          const int hb = b < 0 || b >= a.c.num_blocks ? oob
+                                                      : static_cast<int>(((h ? w[1] : w[0]) * a.c.num_blocks + b) * a.c.Hkv + s.g);
+          for (int sl = 0; sl < SLABS; ++sl)
+            tma_load_3d(smem_u32(sm.k[kr.st] + sl * BN * 128 + (lane << a.lu) * 128), &tmK, bar, 64 * sl, h ? s0[1] : s0[0], hb);
+        }
+        ++k_issued;
+        kr.advance();
+      }
+      for (int t = s.qf; t < s.qf + s.nq && ok; ++t) {
+        if (s.nq == 1 && s.qf == 0 && !s.load_q) break;   // still there
+        ok = warp_wait(smem_u32(&sm.q_empty[qr.st]), qr.ph ^ 1, abort_flag, lim, 621);
+        if (!ok) break;
+        const uint32_t bar = smem_u32(&sm.q_full[qr.st]);
+        const int tokens = min(s.n - t * a.tpt, a.tpt), row = s.q0 + t * a.tpt;
+        if (lane == 0) mbar_arrive_expect_tx(bar, SLABS * tokens * a.G * 128);
+        __syncwarp();
+        if (tokens == a.tpt) {
+          if (lane < SLABS)
+            tma_load_3d(smem_u32(sm.q[qr.st] + lane * BM * 128), &tmQ, bar, 64 * lane, s.g * a.G, row);
+        } else {   // a token's heads at a time: no rows of other requests
+          for (int i = lane; i < tokens; i += 32)
+            for (int sl = 0; sl < SLABS; ++sl)
+              tma_load_3d(smem_u32(sm.q[qr.st] + sl * BM * 128 + i * a.G * 128), &tmQ1, bar, 64 * sl, s.g * a.G, row + i);
+        }
+        ++q_issued;
+        qr.advance();
+      }
+    }
+    if ((!ok || *abort_flag) && lane == 0) {
+      // let the copies already in flight land before the CTA exits
+      for (int i = 0; i < NK; ++i) {
+        const uint32_t n = k_issued / NK + (static_cast<uint32_t>(i) < k_issued % NK ? 1 : 0);
+        if (n) mbar_wait_quiesce(smem_u32(&sm.k_full[i]), (n - 1) & 1, 1 << 22);
+      }
+      for (int i = 0; i < NQ; ++i) {
+        const uint32_t n = q_issued / NQ + (static_cast<uint32_t>(i) < q_issued % NQ ? 1 : 0);
+        if (n) mbar_wait_quiesce(smem_u32(&sm.q_full[i]), (n - 1) & 1, 1 << 22);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ============================================================ MMA issuer
+    if (lane == 0) {
+      Ring<NK> kr;
+      Ring<NQ> qr;
+      uint32_t cnt[2] = {0, 0};
+      int q_at = 0;
+      bool ok = true;
+      const uint64_t dk = desc_sw128(smem_u32(sm.k[0]), 16, 1024), dq = desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+      while (ok && items.next(sm, s, abort_flag, lim, false)) {
+        if (s.nq <= 0) continue;
+        int ks[2] = {0, 0};
+        for (int h = 0; h < s.nkt && ok; ++h) {
+          ok = mbar_wait(smem_u32(&sm.k_full[kr.st]), kr.ph, abort_flag, lim, 630);
+          ks[h] = kr.st;
+          kr.advance();
+        }
+        const bool one = s.nq == 1 && s.qf == 0;
+        for (int t = s.qf; t < s.qf + s.nq && ok; ++t) {
+          if (!one || s.load_q) {
+            if (!(ok = mbar_wait(smem_u32(&sm.q_full[qr.st]), qr.ph, abort_flag, lim, 631))) break;
+            q_at = qr.st;
+            qr.advance();
+          }
+          const uint32_t idesc = idesc_bf16_f32(BM, (columns(a, s, t) + 15) & ~15, 0, 0);
+          for (int h = 0; h < s.nkt; ++h) {
+            const uint32_t b = cnt[h] & 1;
+            if (!(ok = mbar_wait(smem_u32(&sm.s_empty[h][b]), ((cnt[h] >> 1) & 1) ^ 1, abort_flag, lim, 632))) break;
+            ++cnt[h];
+            tc_fence_after();
+            const uint64_t d0 = dk + ks[h] * (kTileBytes >> 4), d1 = dq + q_at * (kTileBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+              mma_bf16_ss(tmem + (2 * h + b) * BN, d0 + off16, d1 + off16, idesc, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(smem_u32(&sm.s_full[h][b]));
+          }
+          if (ok && !(one && s.keep_q)) mma_commit(smem_u32(&sm.q_empty[q_at]));
+        }
+        for (int h = 0; h < s.nkt && ok; ++h) mma_commit(smem_u32(&sm.k_empty[ks[h]]));
+      }
+      mma_commit(smem_u32(&sm.drain));
+      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, ok ? lim : (1 << 22)) && ok) {
+        *abort_flag = 1;
+        ra_record_error(RA_ERR_TIMEOUT, 639);
+      }
+    }
+  } else if (warp == 2) {
+    // ============================================================ LSE of the query rows
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && items.next(sm, s, abort_flag, lim, true)) {
+      for (int t = s.qf; t < s.qf + s.nq && ok; ++t, ++n) {
+        const int cols = columns(a, s, t);
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = 32 * j + lane;
+          int head;
+          const int tok = a.by_G.div(i, head);
+          const float x = i < cols ? a.lse[static_cast<int64_t>(s.q0 + t * a.tpt + tok) * a.Hq + s.g * a.G + head] : -CUDART_INF_F;
+          v[j] = x == -CUDART_INF_F ? x : -x * kLog2e;
+        }
+        const int b = n % kLseStages;
+        if (!(ok = warp_wait(smem_u32(&sm.l_empty[b]), ((n / kLseStages) & 1) ^ 1, abort_flag, lim, 640))) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sm.neg_lse[b][32 * j + lane] = v[j];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.l_full[b]));
+      }
+    }
+  } else if (warp == 3) {
+    // ============================================================ items of this part, announced to the other roles
+    const unsigned owner = __ballot_sync(0xffffffffu, mine);
+    if (mine || (owner == 0 && lane == 0)) {
+      bool more = true;
+      for (uint32_t i = 0; more; ++i) {
+        more = mine && it.next(s);
+        if (!more) s.more = 0;
+        const int b = i & (kSegs - 1);
+        if (!mbar_wait(smem_u32(&sm.seg_empty[b]), ((i / kSegs) & 1) ^ 1, abort_flag, lim, 672)) break;
+        sm.item[b] = s;
+        mbar_arrive(smem_u32(&sm.seg_full[b]));
+      }
+    }
+    __syncwarp();
+  } else {
+    // ============================================================ exps and sums (slot h): a key per thread
+    const int h = (warp - 4) >> 2;
+    const int quarter = warp & 3, key = quarter * 32 + lane;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint64_t sc2 = f2pack(a.scale_log2, a.scale_log2);
+    uint32_t n = 0, cnt = 0;
+    bool ok = true;
+    while (ok && items.next(sm, s, abort_flag, lim, true)) {
+      const bool active = h < s.nkt;
+      // this thread's token, its slot and its weight so far
+      int rem, w;
+      const int vb = a.by_vbu.div(((s.tile0 + h) << a.lupt) + (key >> a.lu), rem);
+      const int slot = (a.c.by_W.div(rem, w) << a.lu) + (key & ((1 << a.lu) - 1));
+      int off;
+      const int x = vb * a.c.V + (a.c.by_I.div(slot, off) * a.c.W + w) * a.c.I + off;
+      int64_t at = -1;
+      float old = 0.f;
+      if (active && x < s.L) {
+        const int64_t b = paged_block(a.c, s.r, vb, 602);
+        if (b >= 0) {
+          at = ((w * a.c.num_blocks + b) * a.c.Hkv + s.g) * a.c.bs + slot;
+          if (a.w_in && (!a.causal || x < s.pos0)) old = a.w_in[at];
+        }
+      }
+      const int first = a.causal ? max(0, x - s.pos0) : 0;   // first query that sees the token
+      float sum = 0.f;
+      for (int t = s.qf; t < s.qf + s.nq; ++t, ++n) {
+        const int lb = n % kLseStages;
+        if (!(ok = warp_wait(smem_u32(&sm.l_full[lb]), (n / kLseStages) & 1, abort_flag, lim, 650))) break;
+        if (active) {
+          const uint32_t b = cnt & 1;
+          if (!(ok = warp_wait(smem_u32(&sm.s_full[h][b]), (cnt >> 1) & 1, abort_flag, lim, 651))) break;
+          ++cnt;
+          tc_fence_after();
+          const int hi = columns(a, s, t), lo = min(BN, max(0, first - t * a.tpt) * a.G);
+          const uint32_t addr = t_lane + (2 * h + b) * BN;
+          const int chunks = (hi + 31) >> 5;
+          uint32_t xa[32], xb[32];
+          tmem_ld32(addr, xa);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c >= chunks) break;
+            uint32_t (&y)[32] = (c & 1) ? xb : xa;
+            uint32_t (&z)[32] = (c & 1) ? xa : xb;
+            if (c + 1 < chunks) tmem_ld32(addr + 32 * (c + 1), z);
+            if (__any_sync(0xffffffffu, lo > 32 * c) || hi < 32 * c + 32) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (32 * c + i < lo || 32 * c + i >= hi) y[i] = __float_as_uint(-CUDART_INF_F);
+            }
+            uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(&sm.neg_lse[lb][32 * c + i]);
+              float e0, e1, e2, e3;
+              f2unpack(ffma2(f2pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), sc2, nl.x), e0, e1);
+              f2unpack(ffma2(f2pack(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3])), sc2, nl.y), e2, e3);
+              acc0 = fadd2(acc0, f2pack(ex2(e0), ex2(e1)));
+              acc1 = fadd2(acc1, f2pack(ex2(e2), ex2(e3)));
+            }
+            float p0, p1, p2, p3;
+            f2unpack(acc0, p0, p1);
+            f2unpack(acc1, p2, p3);
+            sum += (p0 + p1) + (p2 + p3);
+            if (c + 1 < chunks) tmem_wait_ld();
+          }
+          tc_fence_before();
+          mbar_arrive(smem_u32(&sm.s_empty[h][b]));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.l_empty[lb]));
+      }
+      if (ok && at >= 0) a.w_out[at] = old + sum;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D>
+ra_status launch_weights(const void* q, const void* k, const WeightArgs& a, cudaStream_t stream) {
+  CUtensorMap mq, mq1, mk;
+  ra_status st;
+  const int64_t T = std::max<int64_t>(a.T, 1);   // without queries Q is not read: any address serves the map
+  const void* qb = a.T > 0 ? q : k;
+  if ((st = box_map(&mq, qb, D, a.Hq, T, a.G, a.tpt)) != RA_OK) return st;
+  if ((st = box_map(&mq1, qb, D, a.Hq, T, a.G, 1)) != RA_OK) return st;
+  if ((st = box_map(&mk, k, D, a.c.bs, a.c.W * a.c.num_blocks * a.c.Hkv, 1 << a.lu, 1)) != RA_OK) return st;
+  const size_t smem = sizeof(WeightSmem<D>) + 1024;
+  RA_CUDA_TRY(cudaFuncSetAttribute(weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+  weights_kernel<D><<<kCtas, kWeightThreads, smem, stream>>>(mq, mq1, mk, a);
+  RA_LAUNCH_CHECK("weights_kernel");
+  return RA_OK;
 }
 
 }  // namespace
@@ -79,19 +567,17 @@ extern "C" ra_status ra_cp_attn_weights(const void* q, const float* lse, const v
   RA_REQUIRE(reinterpret_cast<uintptr_t>(lse) % 4 == 0 && reinterpret_cast<uintptr_t>(w_in) % 4 == 0 &&
                  reinterpret_cast<uintptr_t>(w_out) % 4 == 0,
              "lse and the weights must be 4-byte aligned");
-  RA_REQUIRE(R <= 65535 && Hkv <= 65535, "R and Hkv must be at most 65535");
-  WeightParams p;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.kc = static_cast<const __nv_bfloat16*>(k_cache);
-  p.lse = lse; p.qsl = query_start_loc; p.ctx = ctx_lens;
-  p.c = make_paged(block_table, Hkv, block_size, interleave, pcp, dcp, max_vblocks, num_blocks);
-  p.T = T; p.R = R; p.Hq = Hq; p.G = Hq / Hkv; p.causal = causal ? 1 : 0;
-  p.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(d))) * kLog2e;
-  p.w_in = w_in; p.w_out = w_out;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ra::ceil_div(static_cast<int64_t>(max_vblocks) * p.c.V, 8), 512)),
-                  R, Hkv);
-  if (d == 128) weights_simple_kernel<128><<<grid, 256, 0, stream>>>(p);
-  else weights_simple_kernel<64><<<grid, 256, 0, stream>>>(p);
-  RA_LAUNCH_CHECK("weights_simple_kernel");
-  return RA_OK;
+  WeightArgs a;
+  static_cast<KeyUnits&>(a) =
+      make_units(make_paged(block_table, Hkv, block_size, interleave, pcp, dcp, max_vblocks, num_blocks));
+  a.qsl = query_start_loc; a.ctx = ctx_lens; a.lse = lse;
+  a.T = T; a.R = R; a.Hq = Hq; a.G = Hq / Hkv; a.causal = causal ? 1 : 0;
+  a.tpt = BM / a.G;
+  a.pair_q = a.causal ? 2 * BN / a.tpt : 0;
+  a.by_tpt = fast_div(a.tpt);
+  a.by_G = fast_div(a.G);
+  a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(d))) * kLog2e;
+  a.w_in = w_in; a.w_out = w_out;
+  a.wait_limit = ra::wait_limit();
+  return d == 128 ? launch_weights<128>(q, k_cache, a, stream) : launch_weights<64>(q, k_cache, a, stream);
 }

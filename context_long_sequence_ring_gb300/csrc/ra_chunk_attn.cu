@@ -17,12 +17,8 @@
 //          HBM bandwidth about 1.45 us, one slot's chain of score product, softmax
 //          and P.V about 1.3 us, two of them half of that).
 //
-// Keys.  The cache is read where it lies: a "unit" is u consecutive slots of a
-// block on one device (u = 16, 32 or 64, a divisor of the block size), one TMA
-// box per 64 columns; units are ordered by virtual block, slot, device, so that
-// a prefix of the units covers a prefix of the context up to one interleave
-// group, and a tile is 128/u units.  Within a unit positions grow with the
-// slot, so every mask is a prefix per unit.  V rows of slots past the context
+// Keys.  The cache is read where it lies, in units of 16 or 32 slots
+// (ra_key_units.cuh).  V rows of slots past the context
 // (which may hold NaN) are zeroed in shared memory by a warp of their own in
 // the tiles that have any; units of a bad block are read out of bounds, which
 // TMA fills with zeros.
@@ -41,8 +37,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "ra_attn_tc.cuh"
-#include "ra_paged.cuh"
+#include "ra_key_units.cuh"
 
 RA_DEFINE_ERROR_FETCH(fetch_error_chunk_attn)
 
@@ -53,16 +48,13 @@ constexpr int kChunkThreads = 384;
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRowBlocks = 8;
 
-struct ChunkArgs {
+struct ChunkArgs : KeyUnits {
   const int32_t *qsl, *ctx;
-  Paged c;
   int64_t T;
   int R, Hq, G, causal, out_bf16;
-  int lu, lupt, nsub;             // log2 slots of a unit, log2 units of a tile, units of a block
-  FastDiv by_vbu;                 // by the units of a virtual block
   int tpt, f_split, over;         // tokens of a row tile; cost of a key in a split tile (5 in a pair), see Req
   int cost_shift;
-  FastDiv by_tpi;                 // by the tokens of a pair of row tiles
+  FastDiv by_G, by_tpi;                // by the tokens of a pair of row tiles
   float scale_log2;
   void* o;                        // [T, Hq, D]
   float* lse;                     // [T, Hq] or NULL
@@ -107,28 +99,6 @@ __device__ __forceinline__ int limit_of(const ChunkArgs& a, const Req& q, int i)
   if (!a.causal) return q.L;
   const long long lim = q.pos0 + i + 1;
   return lim < 0 ? 0 : (lim < q.L ? static_cast<int>(lim) : q.L);
-}
-
-// Units that hold a token below lim: a prefix of the units.
-__device__ __forceinline__ int units_below(const ChunkArgs& a, int lim) {
-  if (lim <= 0) return 0;
-  int o, rem;
-  int k = a.c.by_V.div(lim, o) * a.nsub * a.c.W;
-  if (o > 0) {
-    const int q = a.c.by_WI.div(o - 1, rem);
-    const int sub = (q * a.c.I + min(rem, a.c.I - 1)) >> a.lu;   // last unit row with a token below
-    int off;
-    const int first = a.c.by_I.div(sub << a.lu, off) * a.c.W * a.c.I + off;
-    k += sub * a.c.W + min(a.c.W, a.c.by_I.div(o - first + a.c.I - 1));
-  }
-  return k;
-}
-
-// Units from the start all of whose tokens are below lim.
-__device__ __forceinline__ int units_within(const ChunkArgs& a, int lim) {
-  int o;
-  const int vb = a.c.by_V.div(lim, o);
-  return (vb * a.nsub + ((a.c.by_WI.div(o) * a.c.I) >> a.lu)) * a.c.W;
 }
 
 __device__ __forceinline__ int tiles_of(const ChunkArgs& a, const Req& q, int k) {
@@ -311,15 +281,6 @@ struct SegIter {
 };
 
 // ------------------------------------------------------------------ softmax
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
 // One online-softmax step of the row at tensor-memory address s_addr (BN fp32
 // columns, raw Q.K^T): P in bf16 pairs goes over the first BN/2 columns, m
 // (log2 units) and l are updated; returns the factor O must be scaled by.
@@ -406,42 +367,6 @@ __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool 
   return first ? 1.f : alpha;
 }
 
-// Visible slots (a prefix, 0..u) of unit (vb, sub, w) for a row that sees positions below lim.
-__device__ __forceinline__ int unit_visible(const ChunkArgs& a, int vb, int sub, int w, int lim) {
-  const int y = lim - vb * a.c.V - w * a.c.I;
-  if (y <= 0) return 0;
-  int part;
-  const int q = a.c.by_WI.div(y, part);
-  return max(0, min(1 << a.lu, q * a.c.I + min(part, a.c.I) - (sub << a.lu)));
-}
-
-// Visible columns (a prefix, 0..16) of each 16 columns of a tile, 8 bits each.  `check`: some block of this
-// CTA's work was bad, leave out the tokens of such blocks.
-__device__ __forceinline__ void tile_limits(const ChunkArgs& a, int r, bool check, int tile, int lim, uint64_t& lm) {
-  int rem, w, v = 0;
-  int vb = a.by_vbu.div(tile << a.lupt, rem), sub = a.c.by_W.div(rem, w);
-  lm = 0;
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    if (a.lu == 4 || !(i & 1)) {
-      v = unit_visible(a, vb, sub, w, lim);
-      if (check && v > 0) {
-        const int32_t b = vb < a.c.max_vb ? a.c.table[static_cast<int64_t>(r) * a.c.max_vb + vb] : -1;
-        if (b < 0 || b >= a.c.num_blocks) v = 0;
-      }
-      if (++w == a.c.W) {
-        w = 0;
-        if (++sub == a.nsub) {
-          sub = 0;
-          ++vb;
-        }
-      }
-    }
-    lm |= static_cast<uint64_t>(min(v, 16)) << (8 * i);
-    v = max(v - 16, 0);
-  }
-}
-
 // ------------------------------------------------------------------ the kernel
 constexpr int kSegs = 4;          // segments announced ahead
 constexpr int kSegReaders = 11;   // warps that read them: TMA, MMA, zeroing and 8 of softmax
@@ -463,23 +388,6 @@ struct __align__(1024) ChunkSmem {
 };
 
 static_assert(sizeof(ChunkSmem<128>) + 1024 <= 232448 && sizeof(ChunkSmem<64>) + 1024 <= 232448, "227 KB of shared memory");
-
-// mbar_wait by a whole warp with one outcome for all lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit, int site) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit, site));
-}
-
-template <int NS>
-struct Ring {
-  int st = 0;
-  uint32_t ph = 0;
-  __device__ void advance() {
-    if (++st == NS) {
-      st = 0;
-      ph ^= 1;
-    }
-  }
-};
 
 // A role's reading of the announced segments, in order.
 struct SegReader {
@@ -1020,7 +928,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
   const Segment sg = jn.s;
   const int slots = sg.pair ? 2 : 1;
   const int rows = min(sg.n - sg.tok0, slots * a.tpt) * a.G;
-  if (static_cast<int>(blockIdx.y) * (kMergeThreads / 32) >= rows) return;
+  if (static_cast<int>(blockIdx.y) * (kMergeThreads / 32) * 2 >= rows) return;
   if (warp == 0) {
     // the partials, in order: of this part, and of those that follow
     const Plan plan = jn.plan;
@@ -1038,72 +946,78 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
   }
   __syncthreads();
   const int used = n_parts;
-  for (int i = blockIdx.y * (kMergeThreads / 32) + warp; i < rows; i += gridDim.y * (kMergeThreads / 32)) {
-    const int tok = i / a.G, h = tok >= a.tpt ? 1 : 0, row = i - h * a.tpt * a.G;
+  // two rows at a time, for the loads' latency
+  constexpr int kRows = 2;
+  for (int i0 = kRows * (blockIdx.y * (kMergeThreads / 32) + warp); i0 < rows; i0 += kRows * gridDim.y * (kMergeThreads / 32)) {
+    int at_row[kRows];   // row of the partials
+    float M[kRows], l[kRows];
+    __align__(16) float acc[kRows][E];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int i = min(i0 + j, rows - 1), h = i >= a.tpt * a.G ? 1 : 0;
+      at_row[j] = h * BM + i - h * a.tpt * a.G;
+      M[j] = -CUDART_INF_F;
+      l[j] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[j][e] = 0.f;
+    }
     // lane p holds (m, l) of partial p, then its weight 2^(m - M); partials that saw nothing have weight 0
-    float M = -CUDART_INF_F, l = 0.f;
-    __align__(16) float acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
     for (int p0 = 0; p0 < used; p0 += 32) {
-      float2 ml = make_float2(-CUDART_INF_F, 0.f);
-      if (p0 + lane < used) ml = a.ml_part[(parts[p0 + lane] * 2 + h) * BM + row];
-      float mn = ml.y > 0.f ? ml.x : -CUDART_INF_F;
+      float w[kRows];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      mn = fmaxf(M, mn);
-      if (mn == -CUDART_INF_F) continue;
-      const float w = ml.y > 0.f ? ex2(ml.x - mn) : 0.f, old = ex2(M - mn);
-      float ls = w * ml.y;
+      for (int j = 0; j < kRows; ++j) {
+        float2 ml = make_float2(-CUDART_INF_F, 0.f);
+        if (p0 + lane < used) ml = a.ml_part[parts[p0 + lane] * 2 * BM + at_row[j]];
+        float mn = ml.y > 0.f ? ml.x : -CUDART_INF_F;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-      M = mn;
-      l = l * old + ls;
+        for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mn = fmaxf(M[j], mn);
+        w[j] = ml.y > 0.f ? ex2(ml.x - mn) : 0.f;
+        const float old = M[j] == -CUDART_INF_F ? 0.f : ex2(M[j] - mn);
+        float ls = w[j] * ml.y;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= old;
+        for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+        M[j] = mn;
+        l[j] = l[j] * old + ls;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[j][e] *= old;
+      }
       const int np = min(32, used - p0);
-#pragma unroll 8
+#pragma unroll 4
       for (int p = 0; p < np; ++p) {
-        const float wp = __shfl_sync(0xffffffffu, w, p);
-        const float* src = a.o_part + (static_cast<int64_t>(parts[p0 + p] * 2 + h) * BM + row) * D + E * lane;
-        __align__(16) float v[E];
-        if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-        else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+        const float* src = a.o_part + static_cast<int64_t>(parts[p0 + p]) * 2 * BM * D + E * lane;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += wp * v[e];
+        for (int j = 0; j < kRows; ++j) {
+          const float wp = __shfl_sync(0xffffffffu, w[j], p);
+          __align__(16) float v[E];
+          if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src + at_row[j] * D);
+          else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src + at_row[j] * D);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[j][e] += wp * v[e];
+        }
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int64_t orow = static_cast<int64_t>(sg.q0 + sg.tok0 + tok) * a.Hq + sg.g * a.G + (i - tok * a.G);
-    if (a.out_bf16) {
-      __align__(8) uint32_t w[E / 2];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) w[e / 2] = f2_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + orow * D + E * lane);
-      if (E == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(w);
-      else *dst = w[0];
-    } else {
-      float* dst = static_cast<float*>(a.o) + orow * D + E * lane;
+    for (int j = 0; j < kRows; ++j) {
+      if (i0 + j >= rows) break;
+      const int tok = a.by_G.div(i0 + j), head = i0 + j - tok * a.G;
+      const float inv = l[j] > 0.f ? 1.f / l[j] : 0.f;
+      const int64_t orow = static_cast<int64_t>(sg.q0 + sg.tok0 + tok) * a.Hq + sg.g * a.G + head;
+      if (a.out_bf16) {
+        __align__(8) uint32_t w[E / 2];
 #pragma unroll
-      for (int e = 0; e < E; ++e) dst[e] = acc[e] * inv;
+        for (int e = 0; e < E; e += 2) w[e / 2] = f2_bf16x2(acc[j][e] * inv, acc[j][e + 1] * inv);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + orow * D + E * lane);
+        if (E == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(w);
+        else *dst = w[0];
+      } else {
+        float* dst = static_cast<float*>(a.o) + orow * D + E * lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) dst[e] = acc[j][e] * inv;
+      }
+      if (a.lse && lane == 0) a.lse[orow] = l[j] > 0.f ? (M[j] + log2f(l[j])) * kLn2 : -CUDART_INF_F;
     }
-    if (a.lse && lane == 0) a.lse[orow] = l > 0.f ? (M + log2f(l)) * kLn2 : -CUDART_INF_F;
   }
-}
-
-// Three-dimensional bf16 map with 64-column boxes in the 128-byte swizzle the MMA descriptors expect.
-ra_status chunk_map(CUtensorMap* map, const void* base, int D, int64_t n1, int64_t n2, uint32_t box1, uint32_t box2) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(n1) * D * 2};
-  cuuint32_t box[3] = {64, box1, box2};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
-  return RA_OK;
 }
 
 template <int D>
@@ -1111,9 +1025,9 @@ ra_status launch_chunk(const void* q, const void* k, const void* v, const ChunkA
   CUtensorMap mq, mk, mv;
   ra_status st;
   const int64_t blocks = a.c.W * a.c.num_blocks * a.c.Hkv;
-  if ((st = chunk_map(&mq, q, D, a.Hq, a.T, a.G, a.tpt)) != RA_OK) return st;
-  if ((st = chunk_map(&mk, k, D, a.c.bs, blocks, 1 << a.lu, 1)) != RA_OK) return st;
-  if ((st = chunk_map(&mv, v, D, a.c.bs, blocks, 1 << a.lu, 1)) != RA_OK) return st;
+  if ((st = box_map(&mq, q, D, a.Hq, a.T, a.G, a.tpt)) != RA_OK) return st;
+  if ((st = box_map(&mk, k, D, a.c.bs, blocks, 1 << a.lu, 1)) != RA_OK) return st;
+  if ((st = box_map(&mv, v, D, a.c.bs, blocks, 1 << a.lu, 1)) != RA_OK) return st;
   const size_t smem = sizeof(ChunkSmem<D>) + 1024;
   RA_CUDA_TRY(cudaFuncSetAttribute(chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    static_cast<int>(smem)));
@@ -1170,13 +1084,11 @@ extern "C" ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const 
   RA_REQUIRE(ws_bytes >= need, "workspace too small (%zu < %zu bytes)", ws_bytes, need);
   ChunkArgs a;
   a.qsl = query_start_loc; a.ctx = ctx_lens;
-  a.c = make_paged(block_table, Hkv, block_size, interleave, pcp, dcp, max_vblocks, num_blocks);
+  static_cast<KeyUnits&>(a) =
+      make_units(make_paged(block_table, Hkv, block_size, interleave, pcp, dcp, max_vblocks, num_blocks));
   a.T = T; a.R = R; a.Hq = Hq; a.G = Hq / Hkv; a.causal = causal ? 1 : 0; a.out_bf16 = out_dt == RA_BF16;
-  a.lu = block_size % 32 == 0 ? 5 : 4;
-  a.lupt = 7 - a.lu;
-  a.nsub = block_size >> a.lu;
-  a.by_vbu = fast_div(static_cast<int64_t>(a.nsub) * a.c.W);
   a.tpt = BM / a.G;
+  a.by_G = fast_div(a.G);
   a.by_tpi = fast_div(2 * a.tpt);
   a.f_split = d == 128 ? 4 : 2;
   a.over = d == 128 ? 224 : 384;
