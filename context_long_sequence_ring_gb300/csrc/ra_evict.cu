@@ -5,7 +5,14 @@
 // +0), and a radix select finds the key of the m-th heaviest token of the
 // middle part, m = keep - n_sink - n_recent, 8 bits at a time from the top:
 // all larger keys are kept, and of the equal ones the first as many as are
-// missing.  A scan over the tokens in order then numbers the kept ones.
+// missing.  Counts before each token, in token order, then number the kept ones.
+//
+// One cluster of up to 8 CTAs takes a (request, K/V head) from the weights to
+// the moved rows in one launch.  Each CTA holds the keys of a contiguous part of
+// the context in shared memory; histograms and counts meet through distributed
+// shared memory, every CTA summing them for itself.  The move is bound by HBM
+// (2 x 512 bytes per kept token of head dim 128 in bf16); selecting reads the
+// weights once, 4 bytes per token.
 #include <algorithm>
 
 #include "ra_paged.cuh"
@@ -14,15 +21,19 @@ RA_DEFINE_ERROR_FETCH(fetch_error_evict)
 
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kRowWords = 16;  // 16-byte words of a batch that a thread holds
+constexpr int kThreads = 512;
+constexpr int kMaxCluster = 8;
+constexpr int kKeysCap = 24576;   // keys in shared memory: 96 KB, so that two CTAs share an SM
+constexpr int kBatch = 256;       // tokens a CTA moves at a time
+constexpr int kInFlight = 8;      // 16-byte words that a thread holds
 
 struct EvictParams {
   uint4 *kc, *vc;
   float* w;
   Paged src, dst;  // dst.table may be src.table
   const int32_t* ctx;
-  int row_words, keep, n_sink, n_recent, in_place;
+  int row_words, keep, n_sink, n_recent, in_place, keys_cap;
+  FastDiv by_words;   // by the words of a token's K and V
   int32_t *kept, *new_lens;
 };
 
@@ -33,127 +44,218 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive sum over the block of a 0/1 flag; total of the block in `sum`.
-__device__ __forceinline__ int block_rank(bool flag, int* warp_sums, int& sum) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned b = __ballot_sync(0xffffffffu, flag);
-  __syncthreads();
-  if (lane == 0) warp_sums[warp] = __popc(b);
-  __syncthreads();
-  int before = 0;
-  sum = 0;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    const int c = warp_sums[i];
-    if (i < warp) before += c;
-    sum += c;
-  }
-  return before + __popc(b & ((1u << lane) - 1));
+// All threads of all CTAs of the cluster; what was written before is visible to them after.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The 32-bit word at p in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ int peer_word(const void* p, int rank) {
+  uint32_t at, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return static_cast<int>(v);
 }
 
-__global__ void __launch_bounds__(kThreads) evict_simple_kernel(const EvictParams p) {
-  __shared__ int hist[256];
+// Exclusive sum over the block and its total.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += warp_sums[i];
+    total += warp_sums[i];
+  }
+  return before + x - v;
+}
+
+__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ uint32_t keys[];
+  __shared__ int hist[4][256], sums[256];
   __shared__ int warp_sums[kThreads / 32];
+  __shared__ int counts[2];              // of this CTA's part: kept for certain, ties
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  const int r = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
+  __shared__ int64_t row_src[kBatch], row_dst[kBatch];
+  const int C = gridDim.x, rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const int r = blockIdx.y / p.src.Hkv, g = blockIdx.y - r * p.src.Hkv;
   const int N = paged_len(p.src, p.ctx[r], 700);
   const int n_new = min(N, p.keep);
-  int32_t* kept = p.kept + (static_cast<int64_t>(r) * p.src.Hkv + g) * p.keep;
-  if (g == 0 && tid == 0) p.new_lens[r] = n_new;
-  for (int j = n_new + tid; j < p.keep; j += kThreads) kept[j] = -1;
+  int32_t* kept = p.kept + static_cast<int64_t>(blockIdx.y) * p.keep;
+  if (g == 0 && rank == 0 && tid == 0) p.new_lens[r] = n_new;
+  for (int j = n_new + rank * kThreads + tid; j < p.keep; j += C * kThreads) kept[j] = -1;
 
   if (N <= p.keep) {
-    for (int j = tid; j < N; j += kThreads) kept[j] = j;
+    for (int j = rank * kThreads + tid; j < N; j += C * kThreads) kept[j] = j;
+    if (p.in_place) return;              // the same for all CTAs of the cluster
+    cluster_barrier();                   // kept is read by all of them
   } else {
-    const int m0 = p.n_sink, m1 = N - p.n_recent;  // the middle part [m0, m1)
-    auto key = [&](int x) {
+    const int m0 = p.n_sink, m1 = N - p.n_recent;      // the middle part [m0, m1)
+    const int per = (N + C - 1) / C;
+    const int lo = min(N, rank * per), hi = min(N, lo + per);
+    auto load_key = [&](int x) {
       const int64_t at = paged_row(p.src, r, x, g, 701);
       return at < 0 ? 0u : key_of(p.w[at]);
     };
+    auto key = [&](int x) { return x - lo < p.keys_cap ? keys[x - lo] : load_key(x); };
     int need = p.keep - p.n_sink - p.n_recent;
-    uint32_t prefix = 0;
-    if (need > 0) {
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
-        __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int x = m0 + tid; x < m1; x += kThreads) {
-          const uint32_t k = key(x);
-          if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+    uint32_t prefix = need > 0 ? 0 : 0xffffffffu;      // 0xffffffff: above every key
+    for (int i = tid; i < 4 * 256; i += kThreads) hist[i >> 8][i & 255] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+      if (need <= 0 && pass > 0) break;                // nothing to choose: the keys were not needed but are cheap
+      const int shift = 24 - 8 * pass;
+      const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
+      for (int x0 = lo; x0 < hi; x0 += kThreads) {
+        const int x = x0 + tid;
+        uint32_t k = 0;
+        if (x < hi) {
+          if (pass == 0) {
+            k = load_key(x);
+            if (x - lo < p.keys_cap) keys[x - lo] = k;
+          } else {
+            k = key(x);
+          }
         }
-        __syncthreads();
-        if (tid == 0) {
-          int b = 255;
-          for (; b > 0 && hist[b] < need; --b) need -= hist[b];
-          s_prefix = prefix | (static_cast<uint32_t>(b) << shift);
-          s_need = need;
-        }
-        __syncthreads();
-        prefix = s_prefix;
-        need = s_need;
-        __syncthreads();
+        const bool in = x >= m0 && x < min(m1, hi) && (k & mask) == prefix;
+        const int digit = in ? static_cast<int>(k >> shift) & 255 : 256;
+        const unsigned same = __match_any_sync(0xffffffffu, digit);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[pass][digit], __popc(same));
       }
-    } else {
-      prefix = 0xffffffffu;  // above every key of a number
+      cluster_barrier();
+      if (need <= 0) break;
+      if (tid < 256) {                                 // bin tid from the top, over the cluster
+        int t = 0;
+#pragma unroll 4
+        for (int c = 0; c < C; ++c) t += peer_word(&hist[pass][255 - tid], c);
+        sums[tid] = t;
+      }
+      __syncthreads();
+      if (tid < 32) {
+        // bins 8*lane .. 8*lane+7 from the top: lane 0 holds the largest digits
+        int b[8], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = sums[8 * lane + i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += b[i];
+        int above = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, above, o);
+          if (lane >= o) above += y;
+        }
+        above -= sum;                                  // tokens in larger digits than this lane's
+        if (above < need && need <= above + sum) {     // one lane: the digit of the need-th largest key
+          int i = 0;
+#pragma unroll
+          for (int u = 0; u < 7; ++u)
+            if (i == u && above + b[u] < need) {
+              above += b[u];
+              i = u + 1;
+            }
+          s_prefix = prefix | (static_cast<uint32_t>(255 - (8 * lane + i)) << shift);
+          s_need = need - above;
+        }
+      }
+      __syncthreads();
+      prefix = s_prefix;
+      need = s_need;
+      __syncthreads();
     }
-    // tokens with a larger key and the first `need` of the equal ones
-    int out = 0, ties = 0;
-    for (int x0 = 0; x0 < N; x0 += kThreads) {
-      const int x = x0 + tid;
+    // Each thread takes a run of consecutive tokens (an odd number, so that the threads' keys lie in
+    // different banks): tokens kept for certain and ties, counted, then numbered in order.
+    const int run = ((hi - lo + kThreads - 1) / kThreads) | 1;
+    const int x0 = min(hi, lo + tid * run), x1 = min(hi, x0 + run);
+    int sure = 0, ties = 0;
+    for (int x = x0; x < x1; ++x) {
       const bool mid = x >= m0 && x < m1;
-      const uint32_t k = mid ? key(x) : 0u;
-      int sum;
-      const bool tie = mid && k == prefix;
-      const int tr = ties + block_rank(tie, warp_sums, sum);
-      ties += sum;
-      const bool sel = x < N && (!mid || k > prefix || (tie && tr < need));
-      const int at = out + block_rank(sel, warp_sums, sum);
-      out += sum;
-      if (sel) kept[at] = x;
+      const uint32_t k = mid ? key(x) : 0xffffffffu;
+      sure += !mid || k > prefix;
+      ties += mid && k == prefix;
     }
+    int all_sure, all_ties;
+    const int sure_before = block_scan(sure, warp_sums, all_sure), ties_before = block_scan(ties, warp_sums, all_ties);
+    if (tid == 0) {
+      counts[0] = all_sure;
+      counts[1] = all_ties;
+    }
+    cluster_barrier();
+    int at = sure_before, tie = ties_before;           // before this thread, in the whole context
+    for (int c = 0; c < rank; ++c) {
+      at += peer_word(&counts[0], c);
+      tie += peer_word(&counts[1], c);
+    }
+    at += min(tie, need);
+    for (int x = x0; x < x1; ++x) {
+      const bool mid = x >= m0 && x < m1;
+      const uint32_t k = mid ? key(x) : 0xffffffffu;
+      const bool is_tie = mid && k == prefix;
+      if (!mid || k > prefix || (is_tie && tie < need)) kept[at++] = x;
+      tie += is_tie;
+    }
+    cluster_barrier();                                 // kept is complete; no CTA reads another's memory any more
   }
-  __syncthreads();
-  if (p.in_place && N <= p.keep) return;
 
-  // Pack in ascending batches.  A batch is read whole before it is written,
-  // and token j comes from a place >= j, so no later batch reads what an
-  // earlier one wrote, in place or not.
+  // Pack in ascending batches of the whole cluster.  In place a batch is read whole before it is written: token j
+  // comes from a place >= j, so no later batch reads what an earlier one wrote.
   const int rw = p.row_words, words = 2 * rw;
-  const int per = (kThreads * kRowWords) / words > 0 ? (kThreads * kRowWords) / words : 1;
-  for (int j0 = 0; j0 < n_new; j0 += per) {
-    const int nj = min(per, n_new - j0);
-    uint4 v[kRowWords];
-#pragma unroll
-    for (int u = 0; u < kRowWords; ++u) {
-      const int e = u * kThreads + tid, j = e / words, c = e % words;
-      if (j < nj) {
-        const int64_t at = paged_row(p.src, r, kept[j0 + j], g, 701);
-        v[u] = at < 0 ? make_uint4(0, 0, 0, 0) : (c < rw ? p.kc[at * rw + c] : p.vc[at * rw + c - rw]);
-      }
+  const int sub = max(1, (kThreads * kInFlight) / words);   // tokens whose words the CTA holds at a time
+  const int step = p.in_place ? min(kBatch, sub) : kBatch;
+#pragma unroll 1
+  for (int b0 = 0; b0 < n_new; b0 += C * step) {
+    const int j0 = b0 + rank * step, nj = max(0, min(step, n_new - j0));
+    float wt = 0.f;
+    __syncthreads();
+    if (tid < nj) {
+      const int j = j0 + tid, vb = p.dst.by_V.div(j);
+      const int64_t src = paged_row(p.src, r, __ldcg(&kept[j]), g, 701);
+      int64_t dst = -1;
+      if (vb < p.dst.max_vb) dst = paged_row(p.dst, r, j, g, 702);
+      else ra_record_error(RA_ERR_DEVICE_BOUNDS, 703);
+      row_src[tid] = src;
+      row_dst[tid] = src == dst ? -1 : dst;
+      if (src >= 0) wt = p.w[src];
     }
     __syncthreads();
+    if (!p.in_place && tid < nj && row_dst[tid] >= 0) p.w[row_dst[tid]] = wt;
+    for (int t0 = 0; t0 < step; t0 += sub) {           // once in place
+      const int total = max(0, min(sub, nj - t0)) * words;
+      uint4 v[kInFlight];
 #pragma unroll
-    for (int u = 0; u < kRowWords; ++u) {
-      const int e = u * kThreads + tid, j = e / words, c = e % words;
-      if (j < nj) {
-        const int vb = (j0 + j) / p.dst.V;
-        const int64_t at = vb < p.dst.max_vb ? paged_row(p.dst, r, j0 + j, g, 702) : -1;
-        if (vb >= p.dst.max_vb) ra_record_error(RA_ERR_DEVICE_BOUNDS, 703);
-        if (at >= 0) (c < rw ? p.kc[at * rw + c] : p.vc[at * rw + c - rw]) = v[u];
+      for (int u = 0; u < kInFlight; ++u) {
+        const int e = u * kThreads + tid;
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (e < total) {
+          int c;
+          const int j = t0 + p.by_words.div(e, c);
+          const int64_t at = row_src[j];
+          if (at >= 0 && row_dst[j] >= 0) v[u] = c < rw ? p.kc[at * rw + c] : p.vc[at * rw + c - rw];
+        }
       }
-    }
-  }
-  for (int j0 = 0; j0 < n_new; j0 += kThreads) {
-    const int j = j0 + tid;
-    float w = 0.f;
-    if (j < n_new) {
-      const int64_t at = paged_row(p.src, r, kept[j], g, 701);
-      if (at >= 0) w = p.w[at];
-    }
-    __syncthreads();
-    if (j < n_new && j / p.dst.V < p.dst.max_vb) {
-      const int64_t at = paged_row(p.dst, r, j, g, 702);
-      if (at >= 0) p.w[at] = w;
+      if (p.in_place) {
+        cluster_barrier();
+        if (tid < nj && row_dst[tid] >= 0) p.w[row_dst[tid]] = wt;
+      }
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        const int e = u * kThreads + tid;
+        if (e < total) {
+          int c;
+          const int j = t0 + p.by_words.div(e, c);
+          const int64_t at = row_dst[j];
+          if (at >= 0) (c < rw ? p.kc[at * rw + c] : p.vc[at * rw + c - rw]) = v[u];
+        }
+      }
     }
   }
 }
@@ -175,7 +277,7 @@ extern "C" ra_status ra_cp_evict(void* k_cache, void* v_cache, float* weights, c
              "keep >= 1 and 0 <= n_sink + n_recent <= keep required (keep %d, n_sink %d, n_recent %d)", keep, n_sink,
              n_recent);
   RA_REQUIRE(dst_block_table == nullptr || dst_max_vblocks >= 1, "dst_max_vblocks must be >= 1");
-  RA_REQUIRE(R <= 65535 && Hkv <= 65535, "R and Hkv must be at most 65535");
+  RA_REQUIRE(static_cast<int64_t>(R) * Hkv <= 65535, "R*Hkv must be at most 65535");
   const int64_t row_bytes = static_cast<int64_t>(d) * (dt == RA_BF16 ? 2 : 4);
   if (row_bytes % 16 != 0 || row_bytes > 16384)
     return ra::fail(RA_ERR_UNSUPPORTED, "d*elem_size must be a multiple of 16, at most 16384");
@@ -196,7 +298,25 @@ extern "C" ra_status ra_cp_evict(void* k_cache, void* v_cache, float* weights, c
   p.row_words = static_cast<int>(row_bytes / 16);
   p.keep = keep; p.n_sink = n_sink; p.n_recent = n_recent;
   p.kept = kept; p.new_lens = new_lens;
-  evict_simple_kernel<<<dim3(R, Hkv), kThreads, 0, stream>>>(p);
-  RA_LAUNCH_CHECK("evict_simple_kernel");
+  p.by_words = fast_div(2 * p.row_words);
+  // CTAs of a cluster: as many as fill the GPU once (2 per SM), so that few heads still use all of it
+  int C = 1;
+  while (C < kMaxCluster && static_cast<int64_t>(R) * Hkv * 2 * C <= 152 * 2) C *= 2;
+  p.keys_cap = static_cast<int>(
+      std::min<int64_t>(kKeysCap, ra::ceil_div(static_cast<int64_t>(max_vblocks) * p.src.V, C)));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C, R * Hkv);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.keys_cap) * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = C;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  RA_CUDA_TRY(cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysCap * 4));
+  RA_CUDA_TRY(cudaLaunchKernelEx(&cfg, evict_kernel, p));
   return RA_OK;
 }

@@ -11,7 +11,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "ra_common.cuh"
+#include "ra_paged.cuh"
 
 RA_DEFINE_ERROR_FETCH(fetch_error_rope_apply)
 
@@ -28,6 +28,11 @@ struct Params {
   const int32_t* positions;
   int64_t src_rows, src_rs, src_hs, dst_rs, dst_hs, rows;
   int32_t H, d, rot;
+  // rows of whole words: rows row0 .. row0 + row_end of this launch, threads of a row, its units that turn,
+  // heads of a thread
+  int64_t row0;
+  int32_t row_end, per_row, turn_units, heads;
+  FastDiv by_units, by_groups;
   float mscale, sign;
   float2 phase[kMaxPairs];  // phi_i as hi + lo
 };
@@ -68,6 +73,125 @@ __device__ __forceinline__ float load1(const float* x) { return *x; }
 __device__ __forceinline__ void store1(__nv_bfloat16* x, float v) { *x = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store1(float* x, float v) { *x = v; }
 
+// A word of 16 or 8 bytes as fp32 values, and back (rounded to nearest even).
+template <typename T, typename W> struct Word;
+template <typename W> struct Word<float, W> {
+  static constexpr int N = sizeof(W) / 4;
+  __device__ static void unpack(const W& u, float (&f)[N]) {
+    const float* x = reinterpret_cast<const float*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = x[i];
+  }
+  __device__ static W pack(const float (&f)[N]) {
+    W u;
+    float* x = reinterpret_cast<float*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = f[i];
+    return u;
+  }
+};
+template <typename W> struct Word<__nv_bfloat16, W> {
+  static constexpr int N = sizeof(W) / 2;
+  __device__ static void unpack(const W& u, float (&f)[N]) {
+    const uint32_t* x = reinterpret_cast<const uint32_t*>(&u);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      f[2 * i] = __uint_as_float(x[i] << 16);
+      f[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+    }
+  }
+  __device__ static W pack(const float (&f)[N]) {
+    W u;
+    uint32_t* x = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      x[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return u;
+  }
+};
+
+// The turned pair: real and imaginary part.  One form for all kernels, so that they agree to the bit.
+__device__ __forceinline__ float turn_re(float a, float b, float c, float s) { return fmaf(a, c, -__fmul_rn(b, s)); }
+__device__ __forceinline__ float turn_im(float a, float b, float c, float s) { return fmaf(b, c, __fmul_rn(a, s)); }
+
+// Rows of whole words.  A "unit" of a head is one word of pairs (interleaved),
+// a word of real parts and its partner word of imaginary parts (half), or a word
+// past rot, which is copied.  A thread owns a unit for p.heads heads of a row: it
+// forms the unit's angles once and applies them to each head, the loads of
+// kInFlight heads issued together.  Bound by HBM: a row is read and written
+// once.  heads is all H when there are rows enough to fill the GPU; with few rows the
+// heads are spread over threads, for latency (host side).
+template <typename T, typename W, bool INTER>
+__global__ void __launch_bounds__(kThreads) rope_words_kernel(const __grid_constant__ Params p) {
+  using V = Word<T, W>;
+  constexpr int N = V::N, P = INTER ? N / 2 : N;      // values of a word, pairs of a unit
+  constexpr int kInFlight = 4;
+  const uint32_t w = blockIdx.x * kThreads + threadIdx.x;   // (row, head group, unit)
+  if (w >= static_cast<uint32_t>(p.row_end) * p.per_row) return;
+  int u, group;
+  const int r32 = p.by_units.div(static_cast<int>(w), u);
+  const int64_t r = p.row0 + p.by_groups.div(r32, group);
+  const int64_t s = source_row(p, r);
+  const bool turns = u < p.turn_units;
+  const int e0 = turns ? u * N : p.rot + (u - p.turn_units) * N;
+  const int h0 = group * p.heads, h1 = min(p.H, h0 + p.heads);
+  T* y = static_cast<T*>(p.dst) + r * p.dst_rs + h0 * p.dst_hs + e0;
+  const T* x = static_cast<const T*>(p.src) + (s < 0 ? 0 : s) * p.src_rs + h0 * p.src_hs + e0;
+  const int half = p.rot / 2;
+  W a[kInFlight], b[kInFlight];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int j = 0; j < kInFlight; ++j)
+      if (h + j < h1) {
+        a[j] = *reinterpret_cast<const W*>(x + (h + j - h0) * p.src_hs);
+        if (!INTER && turns) b[j] = *reinterpret_cast<const W*>(x + (h + j - h0) * p.src_hs + half);
+      }
+  };
+  if (s >= 0) load(h0);
+  float c[P], sn[P];
+  if (s >= 0 && turns) {
+    const float m = position(p, r);
+#pragma unroll
+    for (int i = 0; i < P; ++i) turn(p, u * P + i, m, c[i], sn[i]);
+  }
+  for (int h = h0; h < h1; h += kInFlight) {
+    if (s >= 0 && h > h0) load(h);
+#pragma unroll
+    for (int j = 0; j < kInFlight; ++j) {
+      if (h + j >= h1) break;
+      T* out = y + (h + j - h0) * p.dst_hs;
+      if (s < 0) a[j] = b[j] = W{};
+      if (s < 0 || !turns) {
+        *reinterpret_cast<W*>(out) = a[j];
+        if (!INTER && turns) *reinterpret_cast<W*>(out + half) = b[j];
+        continue;
+      }
+      float f[N], o[N];
+      V::unpack(a[j], f);
+      if (INTER) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          o[2 * i] = turn_re(f[2 * i], f[2 * i + 1], c[i], sn[i]);
+          o[2 * i + 1] = turn_im(f[2 * i], f[2 * i + 1], c[i], sn[i]);
+        }
+        *reinterpret_cast<W*>(out) = V::pack(o);
+      } else {
+        float f2[N], o2[N];
+        V::unpack(b[j], f2);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          o[i] = turn_re(f[i], f2[i], c[i], sn[i]);
+          o2[i] = turn_im(f[i], f2[i], c[i], sn[i]);
+        }
+        *reinterpret_cast<W*>(out) = V::pack(o);
+        *reinterpret_cast<W*>(out + half) = V::pack(o2);
+      }
+    }
+  }
+}
+
 // Element-wise form for any stride and alignment: one thread per (row, unit),
 // units 0 .. rot/2-1 the pairs, the others the elements past rot.
 template <typename T, bool INTER>
@@ -93,10 +217,37 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
         continue;
       }
       const float a = s >= 0 ? load1(x + e0) : 0.f, b = s >= 0 ? load1(x + e1) : 0.f;
-      store1(y + e0, a * c - b * sn);
-      store1(y + e1, b * c + a * sn);
+      store1(y + e0, turn_re(a, b, c, sn));
+      store1(y + e1, turn_im(a, b, c, sn));
     }
   }
+}
+
+// Launches the kernel on rows of words W; more than 2^31 threads in several launches.
+template <typename T, typename W>
+ra_status launch_words(Params& p, bool inter, cudaStream_t stream) {
+  constexpr int N = Word<T, W>::N;
+  p.turn_units = inter ? p.rot / N : p.rot / 2 / N;
+  const bool copies = p.src != p.dst;                   // in place the rest of a head stays where it is
+  const int units = p.turn_units + (copies ? (p.d - p.rot) / N : 0);
+  // heads of a thread: all where that leaves about 1024 threads to each SM, else as few as fill them
+  // (32768 rows of 40 heads: 40 heads a thread 115 us, 4 heads 132; 64 rows: 1 head 3 us, 40 heads 8)
+  const int64_t want = 152 * 1024;
+  int64_t groups = std::min<int64_t>(p.H, std::max<int64_t>(1, ra::ceil_div(want, p.rows * units)));
+  p.heads = static_cast<int32_t>(ra::ceil_div(p.H, groups));
+  groups = ra::ceil_div(p.H, p.heads);
+  p.by_units = fast_div(units);
+  p.by_groups = fast_div(groups);
+  p.per_row = static_cast<int32_t>(units * groups);
+  const int64_t rows = p.rows, most = ((int64_t(1) << 31) - kThreads) / p.per_row;
+  for (p.row0 = 0; p.row0 < rows; p.row0 += most) {
+    p.row_end = static_cast<int32_t>(std::min(most, rows - p.row0));
+    const unsigned blocks = static_cast<unsigned>(ra::ceil_div(static_cast<int64_t>(p.row_end) * p.per_row, kThreads));
+    if (inter) rope_words_kernel<T, W, true><<<blocks, kThreads, 0, stream>>>(p);
+    else rope_words_kernel<T, W, false><<<blocks, kThreads, 0, stream>>>(p);
+    RA_LAUNCH_CHECK("rope_words_kernel");
+  }
+  return RA_OK;
 }
 
 // Whether the elements of [rows, H, d] at these strides are all apart.
@@ -157,6 +308,20 @@ extern "C" ra_status ra_rope_apply(const void* src, int64_t src_rows, int64_t sr
     const float hi = static_cast<float>(phi);
     p.phase[i] = make_float2(hi, static_cast<float>(phi - static_cast<double>(hi)));
   }
+  // whole words: every address that is read or written as one is a multiple of its size
+  auto words = [&](int bytes) {
+    const int n = bytes / es;
+    uint64_t m = s0 | d0;
+    if (rows > 1 || idx) m |= static_cast<uint64_t>(src_row_stride * es) | static_cast<uint64_t>(dst_row_stride * es);
+    if (H > 1) m |= static_cast<uint64_t>(src_head_stride * es) | static_cast<uint64_t>(dst_head_stride * es);
+    return m % bytes == 0 && d % n == 0 && rot % n == 0 && (style == RA_ROPE_INTERLEAVED || (rot / 2) % n == 0);
+  };
+  if (words(16))
+    return dt == RA_BF16 ? launch_words<__nv_bfloat16, uint4>(p, style == RA_ROPE_INTERLEAVED, stream)
+                         : launch_words<float, uint4>(p, style == RA_ROPE_INTERLEAVED, stream);
+  if (words(8))
+    return dt == RA_BF16 ? launch_words<__nv_bfloat16, uint2>(p, style == RA_ROPE_INTERLEAVED, stream)
+                         : launch_words<float, uint2>(p, style == RA_ROPE_INTERLEAVED, stream);
   const int64_t units = rot / 2 + (d - rot);
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ra::ceil_div(rows * units, kThreads), 152 * 64));
   const bool inter = style == RA_ROPE_INTERLEAVED;
