@@ -116,18 +116,20 @@ template <typename W> struct Word<__nv_bfloat16, W> {
 __device__ __forceinline__ float turn_re(float a, float b, float c, float s) { return fmaf(a, c, -__fmul_rn(b, s)); }
 __device__ __forceinline__ float turn_im(float a, float b, float c, float s) { return fmaf(b, c, __fmul_rn(a, s)); }
 
+constexpr int kHeads = 8;   // heads of a thread, at most
+
 // Rows of whole words.  A "unit" of a head is one word of pairs (interleaved),
 // a word of real parts and its partner word of imaginary parts (half), or a word
-// past rot, which is copied.  A thread owns a unit for p.heads heads of a row: it
-// forms the unit's angles once and applies them to each head, the loads of
-// kInFlight heads issued together.  Bound by HBM: a row is read and written
-// once.  heads is all H when there are rows enough to fill the GPU; with few rows the
-// heads are spread over threads, for latency (host side).
+// past rot, which is copied.  A thread owns a unit for up to 8 heads of a row:
+// it issues all their loads, forms the unit's angles meanwhile and applies them to each head.
+// Bound by HBM, a row being read and written once: 32768 rows of 40 heads of 128
+// in bf16 (half) take 99 us, 6.8 TB/s, the rate of a plain copy.  4 heads a thread:
+// 103 us; all 40 in a loop that has 8 in flight: 140 us, since a thread's loads then
+// wait for its stores.
 template <typename T, typename W, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_words_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 2) rope_words_kernel(const __grid_constant__ Params p) {
   using V = Word<T, W>;
   constexpr int N = V::N, P = INTER ? N / 2 : N;      // values of a word, pairs of a unit
-  constexpr int kInFlight = 4;
   const uint32_t w = blockIdx.x * kThreads + threadIdx.x;   // (row, head group, unit)
   if (w >= static_cast<uint32_t>(p.row_end) * p.per_row) return;
   int u, group;
@@ -136,58 +138,53 @@ __global__ void __launch_bounds__(kThreads) rope_words_kernel(const __grid_const
   const int64_t s = source_row(p, r);
   const bool turns = u < p.turn_units;
   const int e0 = turns ? u * N : p.rot + (u - p.turn_units) * N;
-  const int h0 = group * p.heads, h1 = min(p.H, h0 + p.heads);
+  const int h0 = group * p.heads;
   T* y = static_cast<T*>(p.dst) + r * p.dst_rs + h0 * p.dst_hs + e0;
   const T* x = static_cast<const T*>(p.src) + (s < 0 ? 0 : s) * p.src_rs + h0 * p.src_hs + e0;
   const int half = p.rot / 2;
-  W a[kInFlight], b[kInFlight];
-  auto load = [&](int h) {
+  const int nh = min(p.H - h0, p.heads);
+  W a[kHeads], b[kHeads];
 #pragma unroll
-    for (int j = 0; j < kInFlight; ++j)
-      if (h + j < h1) {
-        a[j] = *reinterpret_cast<const W*>(x + (h + j - h0) * p.src_hs);
-        if (!INTER && turns) b[j] = *reinterpret_cast<const W*>(x + (h + j - h0) * p.src_hs + half);
-      }
-  };
-  if (s >= 0) load(h0);
+  for (int j = 0; j < kHeads; ++j)
+    if (j < nh && s >= 0) {
+      a[j] = *reinterpret_cast<const W*>(x + j * p.src_hs);
+      if (!INTER && turns) b[j] = *reinterpret_cast<const W*>(x + j * p.src_hs + half);
+    }
   float c[P], sn[P];
   if (s >= 0 && turns) {
     const float m = position(p, r);
 #pragma unroll
     for (int i = 0; i < P; ++i) turn(p, u * P + i, m, c[i], sn[i]);
   }
-  for (int h = h0; h < h1; h += kInFlight) {
-    if (s >= 0 && h > h0) load(h);
 #pragma unroll
-    for (int j = 0; j < kInFlight; ++j) {
-      if (h + j >= h1) break;
-      T* out = y + (h + j - h0) * p.dst_hs;
-      if (s < 0) a[j] = b[j] = W{};
-      if (s < 0 || !turns) {
-        *reinterpret_cast<W*>(out) = a[j];
-        if (!INTER && turns) *reinterpret_cast<W*>(out + half) = b[j];
-        continue;
+  for (int j = 0; j < kHeads; ++j) {
+    if (j >= nh) break;
+    T* out = y + j * p.dst_hs;
+    if (s < 0) a[j] = b[j] = W{};
+    if (s < 0 || !turns) {
+      *reinterpret_cast<W*>(out) = a[j];
+      if (!INTER && turns) *reinterpret_cast<W*>(out + half) = b[j];
+      continue;
+    }
+    float f[N], o[N];
+    V::unpack(a[j], f);
+    if (INTER) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        o[2 * i] = turn_re(f[2 * i], f[2 * i + 1], c[i], sn[i]);
+        o[2 * i + 1] = turn_im(f[2 * i], f[2 * i + 1], c[i], sn[i]);
       }
-      float f[N], o[N];
-      V::unpack(a[j], f);
-      if (INTER) {
+      *reinterpret_cast<W*>(out) = V::pack(o);
+    } else {
+      float f2[N], o2[N];
+      V::unpack(b[j], f2);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          o[2 * i] = turn_re(f[2 * i], f[2 * i + 1], c[i], sn[i]);
-          o[2 * i + 1] = turn_im(f[2 * i], f[2 * i + 1], c[i], sn[i]);
-        }
-        *reinterpret_cast<W*>(out) = V::pack(o);
-      } else {
-        float f2[N], o2[N];
-        V::unpack(b[j], f2);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          o[i] = turn_re(f[i], f2[i], c[i], sn[i]);
-          o2[i] = turn_im(f[i], f2[i], c[i], sn[i]);
-        }
-        *reinterpret_cast<W*>(out) = V::pack(o);
-        *reinterpret_cast<W*>(out + half) = V::pack(o2);
+      for (int i = 0; i < P; ++i) {
+        o[i] = turn_re(f[i], f2[i], c[i], sn[i]);
+        o2[i] = turn_im(f[i], f2[i], c[i], sn[i]);
       }
+      *reinterpret_cast<W*>(out) = V::pack(o);
+      *reinterpret_cast<W*>(out + half) = V::pack(o2);
     }
   }
 }
@@ -230,10 +227,10 @@ ra_status launch_words(Params& p, bool inter, cudaStream_t stream) {
   p.turn_units = inter ? p.rot / N : p.rot / 2 / N;
   const bool copies = p.src != p.dst;                   // in place the rest of a head stays where it is
   const int units = p.turn_units + (copies ? (p.d - p.rot) / N : 0);
-  // heads of a thread: all where that leaves about 1024 threads to each SM, else as few as fill them
-  // (32768 rows of 40 heads: 40 heads a thread 115 us, 4 heads 132; 64 rows: 1 head 3 us, 40 heads 8)
+  // Heads of a thread: 8 where that leaves about 1024 threads to each SM, else as few as it takes for latency
+  // (64 rows of 40 heads: 2.4 us with one or two heads a thread, 3.2 with 8).
   const int64_t want = 152 * 1024;
-  int64_t groups = std::min<int64_t>(p.H, std::max<int64_t>(1, ra::ceil_div(want, p.rows * units)));
+  int64_t groups = std::min<int64_t>(p.H, std::max(ra::ceil_div(p.H, kHeads), ra::ceil_div(want, p.rows * units)));
   p.heads = static_cast<int32_t>(ra::ceil_div(p.H, groups));
   groups = ra::ceil_div(p.H, p.heads);
   p.by_units = fast_div(units);
