@@ -44,6 +44,11 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __noinline__ uint32_t load_key(const EvictParams& p, int r, int g, int x) {
+  const int64_t at = paged_row(p.src, r, x, g, 701);
+  return at < 0 ? 0u : key_of(p.w[at]);
+}
+
 // All threads of all CTAs of the cluster; what was written before is visible to them after.
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -56,19 +61,19 @@ __device__ __forceinline__ int peer_word(const void* p, int rank) {
   return static_cast<int>(v);
 }
 
-// Exclusive sum over the block and its total.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+// Exclusive sum over the block and its total (two 32-bit counts in one word).
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_sums, uint64_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  uint64_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  int before = 0;
+  uint64_t before = 0;
   total = 0;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) {
@@ -81,7 +86,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
 __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t keys[];
   __shared__ int hist[4][256], sums[256];
-  __shared__ int warp_sums[kThreads / 32];
+  __shared__ uint64_t warp_sums[kThreads / 32];
   __shared__ int counts[2];              // of this CTA's part: kept for certain, ties
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
@@ -102,38 +107,57 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     const int m0 = p.n_sink, m1 = N - p.n_recent;      // the middle part [m0, m1)
     const int per = (N + C - 1) / C;
     const int lo = min(N, rank * per), hi = min(N, lo + per);
-    auto load_key = [&](int x) {
-      const int64_t at = paged_row(p.src, r, x, g, 701);
-      return at < 0 ? 0u : key_of(p.w[at]);
-    };
-    auto key = [&](int x) { return x - lo < p.keys_cap ? keys[x - lo] : load_key(x); };
+    const bool fits = per <= p.keys_cap;               // else keys past the capacity are read again each time
+    auto key = [&](int x) { return fits || x - lo < p.keys_cap ? keys[x - lo] : load_key(p, r, g, x); };
     int need = p.keep - p.n_sink - p.n_recent;
     uint32_t prefix = need > 0 ? 0 : 0xffffffffu;      // 0xffffffff: above every key
     for (int i = tid; i < 4 * 256; i += kThreads) hist[i >> 8][i & 255] = 0;
+    // the weights, four tokens of a thread in flight
+    for (int x0 = lo; x0 < hi; x0 += 4 * kThreads) {
+      float w[4];
+      int64_t at[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int x = x0 + u * kThreads + tid;
+        at[u] = x < hi && x - lo < p.keys_cap ? paged_row(p.src, r, x, g, 701) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u] = at[u] >= 0 ? p.w[at[u]] : __int_as_float(0x7fffffff);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int x = x0 + u * kThreads + tid;
+        if (x < hi && x - lo < p.keys_cap) keys[x - lo] = key_of(w[u]);
+      }
+    }
     __syncthreads();
 #pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
-      if (need <= 0 && pass > 0) break;                // nothing to choose: the keys were not needed but are cheap
+      if (need <= 0) break;                            // nothing to choose
       const int shift = 24 - 8 * pass;
       const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
-      for (int x0 = lo; x0 < hi; x0 += kThreads) {
-        const int x = x0 + tid;
-        uint32_t k = 0;
-        if (x < hi) {
-          if (pass == 0) {
-            k = load_key(x);
-            if (x - lo < p.keys_cap) keys[x - lo] = k;
-          } else {
-            k = key(x);
-          }
+      const int c0 = max(lo, m0), c1 = min(hi, m1);    // this CTA's share of the middle part
+      for (int x0 = c0 + (tid & ~31); x0 < c1; x0 += 4 * kThreads) {
+        uint32_t k[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int x = x0 + u * kThreads + lane;
+          k[u] = x < c1 ? key(x) : 0;
         }
-        const bool in = x >= m0 && x < min(m1, hi) && (k & mask) == prefix;
-        const int digit = in ? static_cast<int>(k >> shift) & 255 : 256;
-        const unsigned same = __match_any_sync(0xffffffffu, digit);
-        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[pass][digit], __popc(same));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          // keys on the prefix: few lanes after the first passes, often with one digit in the first
+          const bool in = x0 + u * kThreads + lane < c1 && (k[u] & mask) == prefix;
+          const unsigned who = __ballot_sync(0xffffffffu, in);
+          if (who == 0) continue;
+          const int digit = static_cast<int>(k[u] >> shift) & 255;
+          if (in) {
+            const unsigned same = __match_any_sync(who, digit);
+            if (lane == __ffs(same) - 1) atomicAdd(&hist[pass][digit], __popc(same));
+          }
+          __syncwarp();
+        }
       }
       cluster_barrier();
-      if (need <= 0) break;
       if (tid < 256) {                                 // bin tid from the top, over the cluster
         int t = 0;
 #pragma unroll 4
@@ -177,25 +201,27 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     const int run = ((hi - lo + kThreads - 1) / kThreads) | 1;
     const int x0 = min(hi, lo + tid * run), x1 = min(hi, x0 + run);
     int sure = 0, ties = 0;
+#pragma unroll 4
     for (int x = x0; x < x1; ++x) {
       const bool mid = x >= m0 && x < m1;
       const uint32_t k = mid ? key(x) : 0xffffffffu;
       sure += !mid || k > prefix;
       ties += mid && k == prefix;
     }
-    int all_sure, all_ties;
-    const int sure_before = block_scan(sure, warp_sums, all_sure), ties_before = block_scan(ties, warp_sums, all_ties);
+    uint64_t all;
+    const uint64_t earlier = block_scan(static_cast<uint64_t>(ties) << 32 | static_cast<uint32_t>(sure), warp_sums, all);
     if (tid == 0) {
-      counts[0] = all_sure;
-      counts[1] = all_ties;
+      counts[0] = static_cast<int>(all);
+      counts[1] = static_cast<int>(all >> 32);
     }
     cluster_barrier();
-    int at = sure_before, tie = ties_before;           // before this thread, in the whole context
+    int at = static_cast<int>(earlier), tie = static_cast<int>(earlier >> 32);   // before this thread, in the whole context
     for (int c = 0; c < rank; ++c) {
       at += peer_word(&counts[0], c);
       tie += peer_word(&counts[1], c);
     }
     at += min(tie, need);
+#pragma unroll 4
     for (int x = x0; x < x1; ++x) {
       const bool mid = x >= m0 && x < m1;
       const uint32_t k = mid ? key(x) : 0xffffffffu;
