@@ -83,6 +83,8 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_sums, 
   return before + x - v;
 }
 
+// FITS: a CTA's part of any context is in shared memory whole; else what is past the capacity is read again.
+template <bool FITS>
 __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t keys[];
   __shared__ int hist[4][256], sums[256];
@@ -107,8 +109,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     const int m0 = p.n_sink, m1 = N - p.n_recent;      // the middle part [m0, m1)
     const int per = (N + C - 1) / C;
     const int lo = min(N, rank * per), hi = min(N, lo + per);
-    const bool fits = per <= p.keys_cap;               // else keys past the capacity are read again each time
-    auto key = [&](int x) { return fits || x - lo < p.keys_cap ? keys[x - lo] : load_key(p, r, g, x); };
+    auto key = [&](int x) { return FITS || x - lo < p.keys_cap ? keys[x - lo] : load_key(p, r, g, x); };
     int need = p.keep - p.n_sink - p.n_recent;
     uint32_t prefix = need > 0 ? 0 : 0xffffffffu;      // 0xffffffff: above every key
     for (int i = tid; i < 4 * 256; i += kThreads) hist[i >> 8][i & 255] = 0;
@@ -119,14 +120,14 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int x = x0 + u * kThreads + tid;
-        at[u] = x < hi && x - lo < p.keys_cap ? paged_row(p.src, r, x, g, 701) : -1;
+        at[u] = x < hi && (FITS || x - lo < p.keys_cap) ? paged_row(p.src, r, x, g, 701) : -1;
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) w[u] = at[u] >= 0 ? p.w[at[u]] : __int_as_float(0x7fffffff);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int x = x0 + u * kThreads + tid;
-        if (x < hi && x - lo < p.keys_cap) keys[x - lo] = key_of(w[u]);
+        if (x < hi && (FITS || x - lo < p.keys_cap)) keys[x - lo] = key_of(w[u]);
       }
     }
     __syncthreads();
@@ -145,16 +146,8 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          // keys on the prefix: few lanes after the first passes, often with one digit in the first
           const bool in = x0 + u * kThreads + lane < c1 && (k[u] & mask) == prefix;
-          const unsigned who = __ballot_sync(0xffffffffu, in);
-          if (who == 0) continue;
-          const int digit = static_cast<int>(k[u] >> shift) & 255;
-          if (in) {
-            const unsigned same = __match_any_sync(who, digit);
-            if (lane == __ffs(same) - 1) atomicAdd(&hist[pass][digit], __popc(same));
-          }
-          __syncwarp();
+          if (in) atomicAdd(&hist[pass][(k[u] >> shift) & 255], 1);
         }
       }
       cluster_barrier();
@@ -196,15 +189,16 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
       need = s_need;
       __syncthreads();
     }
-    // Each thread takes a run of consecutive tokens (an odd number, so that the threads' keys lie in
-    // different banks): tokens kept for certain and ties, counted, then numbered in order.
-    const int run = ((hi - lo + kThreads - 1) / kThreads) | 1;
-    const int x0 = min(hi, lo + tid * run), x1 = min(hi, x0 + run);
+    // Each warp takes a run of whole groups of 32 tokens: tokens kept for certain and ties are counted, then
+    // numbered in order.
+    const int warp = tid >> 5;
+    const int run = (((hi - lo + 31) >> 5) + kThreads / 32 - 1) / (kThreads / 32) * 32;
+    const int x0 = min(hi, lo + warp * run), x1 = min(hi, x0 + run);
     int sure = 0, ties = 0;
 #pragma unroll 4
-    for (int x = x0; x < x1; ++x) {
+    for (int x = x0 + lane; x < x1; x += 32) {
       const bool mid = x >= m0 && x < m1;
-      const uint32_t k = mid ? key(x) : 0xffffffffu;
+      const uint32_t k = key(x);
       sure += !mid || k > prefix;
       ties += mid && k == prefix;
     }
@@ -215,28 +209,36 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
       counts[1] = static_cast<int>(all >> 32);
     }
     cluster_barrier();
-    int at = static_cast<int>(earlier), tie = static_cast<int>(earlier >> 32);   // before this thread, in the whole context
+    const uint64_t warp_start = __shfl_sync(0xffffffffu, earlier, 0);
+    int at = static_cast<int>(warp_start), tie = static_cast<int>(warp_start >> 32);   // before this warp, in the context
     for (int c = 0; c < rank; ++c) {
       at += peer_word(&counts[0], c);
       tie += peer_word(&counts[1], c);
     }
     at += min(tie, need);
-#pragma unroll 4
-    for (int x = x0; x < x1; ++x) {
+    const unsigned below = (1u << lane) - 1;
+    for (int xb = x0; xb < x1; xb += 32) {
+      const int x = xb + lane;
       const bool mid = x >= m0 && x < m1;
-      const uint32_t k = mid ? key(x) : 0xffffffffu;
-      const bool is_tie = mid && k == prefix;
-      if (!mid || k > prefix || (is_tie && tie < need)) kept[at++] = x;
-      tie += is_tie;
+      const uint32_t k = x < x1 ? key(x) : 0;
+      const bool is_tie = x < x1 && mid && k == prefix;
+      const unsigned tied = __ballot_sync(0xffffffffu, is_tie);
+      const bool keeps = x < x1 && (!mid || k > prefix || (is_tie && tie + __popc(tied & below) < need));
+      const unsigned kept_mask = __ballot_sync(0xffffffffu, keeps);
+      if (keeps) kept[at + __popc(kept_mask & below)] = x;
+      at += __popc(kept_mask);
+      tie += __popc(tied);
     }
     cluster_barrier();                                 // kept is complete; no CTA reads another's memory any more
   }
 
+  if (n_new == 0) return;
   // Pack in ascending batches of the whole cluster.  In place a batch is read whole before it is written: token j
   // comes from a place >= j, so no later batch reads what an earlier one wrote.
   const int rw = p.row_words, words = 2 * rw;
   const int sub = max(1, (kThreads * kInFlight) / words);   // tokens whose words the CTA holds at a time
-  const int step = p.in_place ? min(kBatch, sub) : kBatch;
+  const int most = p.in_place ? min(kBatch, sub) : kBatch;
+  const int batches = (n_new + C * most - 1) / (C * most), step = (n_new + C * batches - 1) / (C * batches);   // evenly
 #pragma unroll 1
   for (int b0 = 0; b0 < n_new; b0 += C * step) {
     const int j0 = b0 + rank * step, nj = max(0, min(step, n_new - j0));
@@ -328,8 +330,8 @@ extern "C" ra_status ra_cp_evict(void* k_cache, void* v_cache, float* weights, c
   // CTAs of a cluster: as many as fill the GPU once (2 per SM), so that few heads still use all of it
   int C = 1;
   while (C < kMaxCluster && static_cast<int64_t>(R) * Hkv * 2 * C <= 152 * 2) C *= 2;
-  p.keys_cap = static_cast<int>(
-      std::min<int64_t>(kKeysCap, ra::ceil_div(static_cast<int64_t>(max_vblocks) * p.src.V, C)));
+  const int64_t most = ra::ceil_div(static_cast<int64_t>(max_vblocks) * p.src.V, C);
+  p.keys_cap = static_cast<int>(std::min<int64_t>(kKeysCap, most));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, R * Hkv);
   cfg.blockDim = dim3(kThreads);
@@ -342,7 +344,8 @@ extern "C" ra_status ra_cp_evict(void* k_cache, void* v_cache, float* weights, c
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  RA_CUDA_TRY(cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysCap * 4));
-  RA_CUDA_TRY(cudaLaunchKernelEx(&cfg, evict_kernel, p));
+  auto* kernel = most <= kKeysCap ? evict_kernel<true> : evict_kernel<false>;
+  RA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysCap * 4));
+  RA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, p));
   return RA_OK;
 }
