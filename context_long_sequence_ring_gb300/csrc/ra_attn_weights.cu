@@ -36,7 +36,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kCtas = 152;
 constexpr int kWeightThreads = 384;
 constexpr int kSegs = 4, kSegReaders = 11;
-constexpr int kLseStages = 2;
+template <int D>
+constexpr int kLseStagesOf = D == 128 ? 2 : 4;   // not below the query tiles that stay
 
 struct WeightArgs : KeyUnits {
   const int32_t *qsl, *ctx;
@@ -44,6 +45,7 @@ struct WeightArgs : KeyUnits {
   int64_t T;
   int R, Hq, G, causal;
   int tpt, pair_q;        // tokens of a query tile; query tiles that a pair of key tiles spans under the causal mask
+  int q_stages;           // query tiles that fit in shared memory
   FastDiv by_tpt, by_G;
   float scale_log2;
   const float* w_in;
@@ -72,24 +74,30 @@ __device__ __forceinline__ Req load_req(const WeightArgs& a, int r) {
   return q;
 }
 
-// Cost of a pair: 5 for its loads, 4 for each query tile.
-__device__ __forceinline__ long long cost_of(const WeightArgs& a, const Req& q, int k) {
-  return 5 + 4ll * max(0, q.nq - max(0, k - q.k0) * a.pair_q);
-}
-// Cost of pairs 0 .. k-1.
+// Cost of pairs 0 .. k-1: each 5 for its loads and 4 for each query tile it meets.
 __device__ __forceinline__ long long prefix(const WeightArgs& a, const Req& q, int k) {
   const long long full = min(k, q.k0 + 1);               // pairs that meet all query tiles
   const long long m = min(k - static_cast<int>(full), a.pair_q > 0 ? q.nq / a.pair_q : 1 << 30);
   return 5ll * k + 4 * (full * q.nq + m * q.nq - a.pair_q * (m * (m + 1) / 2));
 }
 
+// Key tiles of one head.  Where the request's query tiles all stay in shared memory (nqt > 0) an item is a run
+// of pairs, else it is one pair and the query tiles qf .. qf + nq - 1 pass by.
 struct Item {
   int r, g, q0, n, L, pos0;     // as in Req; pos0 cut below at -n
-  int tile0, nkt;               // first key tile, key tiles (1 or 2)
-  int qf, nq;                   // first query tile and how many
-  int load_q, keep_q;           // single query tile: bring it in, keep it for the next item
+  int tile0, tiles;             // first key tile, key tiles
+  int nqt, qf, nq;
   int more;                     // 0: end of the part
 };
+
+// First query tile that can see a key of tile `tile` or of a later one.
+__device__ __forceinline__ int first_query_tile(const WeightArgs& a, int tile, int pos0) {
+  if (!a.causal) return 0;
+  int rem, off;
+  const int vb = a.by_vbu.div(tile << a.lupt, rem), s0 = a.c.by_W.div(rem) << a.lu;
+  const int first = vb * a.c.V + a.c.by_I.div(s0, off) * a.c.W * a.c.I + off;   // no key of them is before it
+  return first <= pos0 ? 0 : a.by_tpt.div(first - pos0);
+}
 
 __device__ __forceinline__ long long warp_scan(long long v) {
 #pragma unroll
@@ -106,8 +114,8 @@ struct ItemIter {
   long long lo, hi, at;
   Req q;
   int g, k, pairs;
-  bool live, loaded;
-  __device__ ItemIter(const WeightArgs& args) : a(args), live(false), loaded(false) {}
+  bool live;
+  __device__ ItemIter(const WeightArgs& args) : a(args), live(false) {}
   // The request with the first cost at or past lo, found by the whole warp; the returned lane walks.
   __device__ bool find(int part) {
     const int lane = threadIdx.x & 31;
@@ -159,7 +167,6 @@ struct ItemIter {
   __device__ void skip() {
     while (live && k >= pairs) {
       k = 0;
-      loaded = false;
       if (++g < a.c.Hkv) continue;
       g = 0;
       do {
@@ -174,20 +181,18 @@ struct ItemIter {
     s.r = q.r; s.g = g; s.q0 = q.q0; s.n = q.n; s.L = q.L;
     s.pos0 = static_cast<int>(q.pos0 < -q.n ? -q.n : q.pos0);
     s.tile0 = 2 * k;
-    s.nkt = min(2, q.tiles - 2 * k);
-    s.qf = 0;
-    if (a.causal) {   // the query tiles before the first that can see a key of the pair
-      int rem, off;
-      const int vb = a.by_vbu.div(s.tile0 << a.lupt, rem), s0 = a.c.by_W.div(rem) << a.lu;
-      const int first = vb * a.c.V + a.c.by_I.div(s0, off) * a.c.W * a.c.I + off;   // no key is before it
-      s.qf = first <= s.pos0 ? 0 : min(q.nq, a.by_tpt.div(first - s.pos0));
-    }
+    s.nqt = q.nq <= a.q_stages ? q.nq : 0;
+    s.qf = s.nqt ? 0 : min(q.nq, first_query_tile(a, s.tile0, s.pos0));
     s.nq = q.nq - s.qf;
-    s.load_q = !loaded;
-    at += cost_of(a, q, k);
-    ++k;
-    loaded = q.nq == 1;
-    s.keep_q = loaded && k < pairs && at < hi;
+    const long long here = prefix(a, q, k);
+    int u = k + 1, v = s.nqt || q.nq == 0 ? pairs : k + 1;   // past the last pair of the item: its start is below hi
+    while (u < v) {
+      const int mid = (u + v + 1) >> 1;
+      if (at + prefix(a, q, mid - 1) - here < hi) u = mid; else v = mid - 1;
+    }
+    at += prefix(a, q, u) - here;
+    s.tiles = min(2 * u, q.tiles) - 2 * k;
+    k = u;
     s.more = 1;
     skip();
     return true;
@@ -196,15 +201,16 @@ struct ItemIter {
 
 // ------------------------------------------------------------------ the kernel
 template <int D>
-constexpr int kKStages = D == 128 ? 4 : 8;
+constexpr int kKStages = D == 128 ? 5 : 9;
 template <int D>
-constexpr int kQStages = D == 128 ? 3 : 4;
+constexpr int kQStages = D == 128 ? 2 : 4;
 
 template <int D>
 struct __align__(1024) WeightSmem {
   uint8_t k[kKStages<D>][BN * D * 2];
   uint8_t q[kQStages<D>][BM * D * 2];
   uint64_t k_full[kKStages<D>], k_empty[kKStages<D>], q_full[kQStages<D>], q_empty[kQStages<D>];
+  static constexpr int kLseStages = kLseStagesOf<D>;
   uint64_t l_full[kLseStages], l_empty[kLseStages], seg_full[kSegs], seg_empty[kSegs];
   uint64_t s_full[2][2], s_empty[2][2], drain;
   __align__(16) float neg_lse[kLseStages][BM];   // -lse * log2 e; -inf: the row adds nothing
@@ -239,7 +245,8 @@ template <int D>
 __global__ void __launch_bounds__(kWeightThreads, 1)
     weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ WeightArgs a) {
-  constexpr int SLABS = D / 64, NK = kKStages<D>, NQ = kQStages<D>;
+  constexpr int SLABS = D / 64, NK = kKStages<D>, NQ = kQStages<D>, kLseStages = kLseStagesOf<D>;
+  static_assert(kLseStages >= NQ);
   constexpr uint32_t kTileBytes = BM * D * 2;
   extern __shared__ uint8_t smem_raw[];
   WeightSmem<D>& sm = *reinterpret_cast<WeightSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -284,7 +291,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   ItemReader items;
-  Item s;
+  Item s = {};
 
   if (warp == 0) {
     // ============================================================ TMA producer (whole warp: a unit or a token per lane)
@@ -298,54 +305,64 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     uint32_t k_issued = 0, q_issued = 0;
     bool ok = true;
     const int oob = static_cast<int>(a.c.W * a.c.num_blocks * a.c.Hkv);   // past the last block: zero fill
+    // the lane's unit of a key tile; its block is looked up a tile ahead
+    struct Unit {
+      int s0, w, blk;
+    };
+    auto locate = [&](int tile) {
+      Unit x;
+      int rem;
+      const int vb = a.by_vbu.div((tile << a.lupt) + lane, rem);
+      x.s0 = a.c.by_W.div(rem, x.w) << a.lu;
+      x.blk = -1;
+      if (tile < s.tile0 + s.tiles && lane >> a.lupt == 0 && static_cast<int64_t>(vb) * a.c.V < s.L)
+        x.blk = a.c.table[static_cast<int64_t>(s.r) * a.c.max_vb + vb];
+      return x;
+    };
+    auto load_k = [&](const Unit& x) -> bool {
+      if (!warp_wait(smem_u32(&sm.k_empty[kr.st]), kr.ph ^ 1, abort_flag, lim, 620)) return false;
+      const uint32_t bar = smem_u32(&sm.k_full[kr.st]);
+      if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
+      __syncwarp();
+      if (lane >> a.lupt == 0) {
+        const int hb = x.blk < 0 || x.blk >= a.c.num_blocks ? oob : static_cast<int>((x.w * a.c.num_blocks + x.blk) * a.c.Hkv + s.g);
+        for (int sl = 0; sl < SLABS; ++sl)
+          tma_load_3d(smem_u32(sm.k[kr.st] + sl * BN * 128 + (lane << a.lu) * 128), &tmK, bar, 64 * sl, x.s0, hb);
+      }
+      ++k_issued;
+      kr.advance();
+      return true;
+    };
+    auto load_q = [&](int t) -> bool {
+      if (!warp_wait(smem_u32(&sm.q_empty[qr.st]), qr.ph ^ 1, abort_flag, lim, 621)) return false;
+      const uint32_t bar = smem_u32(&sm.q_full[qr.st]);
+      const int tokens = min(s.n - t * a.tpt, a.tpt), row = s.q0 + t * a.tpt;
+      if (lane == 0) mbar_arrive_expect_tx(bar, SLABS * tokens * a.G * 128);
+      __syncwarp();
+      if (tokens == a.tpt) {
+        if (lane < SLABS)
+          tma_load_3d(smem_u32(sm.q[qr.st] + lane * BM * 128), &tmQ, bar, 64 * lane, s.g * a.G, row);
+      } else {   // a token's heads at a time: no rows of other requests
+        for (int i = lane; i < tokens; i += 32)
+          for (int sl = 0; sl < SLABS; ++sl)
+            tma_load_3d(smem_u32(sm.q[qr.st] + sl * BM * 128 + i * a.G * 128), &tmQ1, bar, 64 * sl, s.g * a.G, row + i);
+      }
+      ++q_issued;
+      qr.advance();
+      return true;
+    };
     while (ok && items.next(sm, s, abort_flag, lim, true)) {
       if (s.nq <= 0) continue;
-      // blocks of both tiles first, so that their loads overlap
-      int blk[2], s0[2], w[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int rem;
-        const int vb = a.by_vbu.div(((s.tile0 + h) << a.lupt) + lane, rem);
-        s0[h] = a.c.by_W.div(rem, w[h]) << a.lu;
-        blk[h] = -1;
-        if (h < s.nkt && lane >> a.lupt == 0 && static_cast<int64_t>(vb) * a.c.V < s.L)
-          blk[h] = a.c.table[static_cast<int64_t>(s.r) * a.c.max_vb + vb];
+      Unit x = locate(s.tile0), y = locate(s.tile0 + 1);
+      ok = load_k(x);
+      for (int t = 0; t < s.nqt && ok; ++t) ok = load_q(t);
+      for (int i = 1; i < s.tiles && ok; ++i) {
+        x = y;
+        y = locate(s.tile0 + i + 1);
+        ok = load_k(x);
       }
-      for (int h = 0; h < s.nkt && ok; ++h) {
-        ok = warp_wait(smem_u32(&sm.k_empty[kr.st]), kr.ph ^ 1, abort_flag, lim, 620);
-        if (!ok) break;
-        const uint32_t bar = smem_u32(&sm.k_full[kr.st]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
-        __syncwarp();
-        if (lane >> a.lupt == 0) {
-          const int b = h ? blk[1] : blk[0];
-          const int hb = b < 0 || b >= a.c.num_blocks ? oob
-                                                      : static_cast<int>(((h ? w[1] : w[0]) * a.c.num_blocks + b) * a.c.Hkv + s.g);
-          for (int sl = 0; sl < SLABS; ++sl)
-            tma_load_3d(smem_u32(sm.k[kr.st] + sl * BN * 128 + (lane << a.lu) * 128), &tmK, bar, 64 * sl, h ? s0[1] : s0[0], hb);
-        }
-        ++k_issued;
-        kr.advance();
-      }
-      for (int t = s.qf; t < s.qf + s.nq && ok; ++t) {
-        if (s.nq == 1 && s.qf == 0 && !s.load_q) break;   // still there
-        ok = warp_wait(smem_u32(&sm.q_empty[qr.st]), qr.ph ^ 1, abort_flag, lim, 621);
-        if (!ok) break;
-        const uint32_t bar = smem_u32(&sm.q_full[qr.st]);
-        const int tokens = min(s.n - t * a.tpt, a.tpt), row = s.q0 + t * a.tpt;
-        if (lane == 0) mbar_arrive_expect_tx(bar, SLABS * tokens * a.G * 128);
-        __syncwarp();
-        if (tokens == a.tpt) {
-          if (lane < SLABS)
-            tma_load_3d(smem_u32(sm.q[qr.st] + lane * BM * 128), &tmQ, bar, 64 * lane, s.g * a.G, row);
-        } else {   // a token's heads at a time: no rows of other requests
-          for (int i = lane; i < tokens; i += 32)
-            for (int sl = 0; sl < SLABS; ++sl)
-              tma_load_3d(smem_u32(sm.q[qr.st] + sl * BM * 128 + i * a.G * 128), &tmQ1, bar, 64 * sl, s.g * a.G, row + i);
-        }
-        ++q_issued;
-        qr.advance();
-      }
+      if (s.nqt == 0)
+        for (int t = s.qf; t < s.qf + s.nq && ok; ++t) ok = load_q(t);
     }
     if ((!ok || *abort_flag) && lane == 0) {
       // let the copies already in flight land before the CTA exits
@@ -364,42 +381,64 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     if (lane == 0) {
       Ring<NK> kr;
       Ring<NQ> qr;
-      uint32_t cnt[2] = {0, 0};
-      int q_at = 0;
+      uint32_t cnt0 = 0, cnt1 = 0;   // score tiles of each slot so far
       bool ok = true;
       const uint64_t dk = desc_sw128(smem_u32(sm.k[0]), 16, 1024), dq = desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+      // S_h of the key tile at stage ks and the query tile t at stage qs
+      auto issue = [&](int h, int ks, int qs, int t) -> bool {
+        const uint32_t c = h ? cnt1 : cnt0, b = 2 * h + (c & 1);
+        if (!mbar_wait(smem_u32(&sm.s_empty[0][0] + b), ((c >> 1) & 1) ^ 1, abort_flag, lim, 632)) return false;
+        if (h) ++cnt1; else ++cnt0;
+        tc_fence_after();
+        const uint32_t idesc = idesc_bf16_f32(BM, (columns(a, s, t) + 15) & ~15, 0, 0);
+        const uint64_t d0 = dk + ks * (kTileBytes >> 4), d1 = dq + qs * (kTileBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+          mma_bf16_ss(tmem + b * BN, d0 + off16, d1 + off16, idesc, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(smem_u32(&sm.s_full[0][0] + b));
+        return true;
+      };
       while (ok && items.next(sm, s, abort_flag, lim, false)) {
         if (s.nq <= 0) continue;
-        int ks[2] = {0, 0};
-        for (int h = 0; h < s.nkt && ok; ++h) {
-          ok = mbar_wait(smem_u32(&sm.k_full[kr.st]), kr.ph, abort_flag, lim, 630);
-          ks[h] = kr.st;
-          kr.advance();
-        }
-        const bool one = s.nq == 1 && s.qf == 0;
-        for (int t = s.qf; t < s.qf + s.nq && ok; ++t) {
-          if (!one || s.load_q) {
-            if (!(ok = mbar_wait(smem_u32(&sm.q_full[qr.st]), qr.ph, abort_flag, lim, 631))) break;
-            q_at = qr.st;
+        if (s.nqt) {
+          const int q0 = qr.st;
+          int qf = 0;
+#pragma unroll 1
+          for (int i = 0; i < s.tiles && ok; ++i) {
+            if ((i & 1) == 0 && s.nqt > 1) qf = first_query_tile(a, s.tile0 + i, s.pos0);
+            if (!(ok = mbar_wait(smem_u32(&sm.k_full[kr.st]), kr.ph, abort_flag, lim, 630))) break;
+            if (i == 0)
+              for (int t = 0; t < s.nqt && ok; ++t) {
+                ok = mbar_wait(smem_u32(&sm.q_full[qr.st]), qr.ph, abort_flag, lim, 631);
+                qr.advance();
+              }
+#pragma unroll 1
+            for (int t = qf; t < s.nqt && ok; ++t) ok = issue(i & 1, kr.st, q0 + t < NQ ? q0 + t : q0 + t - NQ, t);
+            if (!ok) break;
+            mma_commit(smem_u32(&sm.k_empty[kr.st]));
+            kr.advance();
+          }
+          for (int t = 0; t < s.nqt && ok; ++t) mma_commit(smem_u32(&sm.q_empty[q0 + t < NQ ? q0 + t : q0 + t - NQ]));
+        } else {
+          int ks[2] = {0, 0};
+          for (int h = 0; h < s.tiles && ok; ++h) {
+            ok = mbar_wait(smem_u32(&sm.k_full[kr.st]), kr.ph, abort_flag, lim, 633);
+            if (h) ks[1] = kr.st; else ks[0] = kr.st;
+            kr.advance();
+          }
+#pragma unroll 1
+          for (int t = s.qf; t < s.qf + s.nq && ok; ++t) {
+            if (!(ok = mbar_wait(smem_u32(&sm.q_full[qr.st]), qr.ph, abort_flag, lim, 634))) break;
+            ok = issue(0, ks[0], qr.st, t) && (s.tiles < 2 || issue(1, ks[1], qr.st, t));
+            if (!ok) break;
+            mma_commit(smem_u32(&sm.q_empty[qr.st]));
             qr.advance();
           }
-          const uint32_t idesc = idesc_bf16_f32(BM, (columns(a, s, t) + 15) & ~15, 0, 0);
-          for (int h = 0; h < s.nkt; ++h) {
-            const uint32_t b = cnt[h] & 1;
-            if (!(ok = mbar_wait(smem_u32(&sm.s_empty[h][b]), ((cnt[h] >> 1) & 1) ^ 1, abort_flag, lim, 632))) break;
-            ++cnt[h];
-            tc_fence_after();
-            const uint64_t d0 = dk + ks[h] * (kTileBytes >> 4), d1 = dq + q_at * (kTileBytes >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-              mma_bf16_ss(tmem + (2 * h + b) * BN, d0 + off16, d1 + off16, idesc, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(smem_u32(&sm.s_full[h][b]));
-          }
-          if (ok && !(one && s.keep_q)) mma_commit(smem_u32(&sm.q_empty[q_at]));
+          if (ok) mma_commit(smem_u32(&sm.k_empty[ks[0]]));
+          if (ok && s.tiles > 1) mma_commit(smem_u32(&sm.k_empty[ks[1]]));
         }
-        for (int h = 0; h < s.nkt && ok; ++h) mma_commit(smem_u32(&sm.k_empty[ks[h]]));
       }
       mma_commit(smem_u32(&sm.drain));
       if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, ok ? lim : (1 << 22)) && ok) {
@@ -452,75 +491,112 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     const int quarter = warp & 3, key = quarter * 32 + lane;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint64_t sc2 = f2pack(a.scale_log2, a.scale_log2);
-    uint32_t n = 0, cnt = 0;
+    uint32_t n = 0, cnt = 0;   // LSE tiles, score tiles so far
     bool ok = true;
+    // adds the score tile of query tile t; `first`: first query that sees this thread's token
+    float sum = 0.f;
+    auto add_tile = [&](int t, int first) -> bool {
+      const uint32_t b = cnt & 1;
+      if (!warp_wait(smem_u32(&sm.s_full[h][b]), (cnt >> 1) & 1, abort_flag, lim, 651)) return false;
+      ++cnt;
+      tc_fence_after();
+      const int hi = columns(a, s, t), lo = min(BN, max(0, first - t * a.tpt) * a.G);
+      const float* nlse = sm.neg_lse[(s.nqt ? n + t : n) % kLseStages];
+      const uint32_t addr = t_lane + (2 * h + b) * BN;
+      const int chunks = (hi + 31) >> 5;
+      uint32_t xa[32], xb[32];
+      tmem_ld32(addr, xa);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c >= chunks) break;
+        uint32_t (&y)[32] = (c & 1) ? xb : xa;
+        uint32_t (&z)[32] = (c & 1) ? xa : xb;
+        if (c + 1 < chunks) tmem_ld32(addr + 32 * (c + 1), z);
+        if (__any_sync(0xffffffffu, lo > 32 * c) || hi < 32 * c + 32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * c + i < lo || 32 * c + i >= hi) y[i] = __float_as_uint(-CUDART_INF_F);
+        }
+        uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(&nlse[32 * c + i]);
+          float e0, e1, e2, e3;
+          f2unpack(ffma2(f2pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), sc2, nl.x), e0, e1);
+          f2unpack(ffma2(f2pack(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3])), sc2, nl.y), e2, e3);
+          acc0 = fadd2(acc0, f2pack(ex2(e0), ex2(e1)));
+          acc1 = fadd2(acc1, f2pack(ex2(e2), ex2(e3)));
+        }
+        float p0, p1, p2, p3;
+        f2unpack(acc0, p0, p1);
+        f2unpack(acc1, p2, p3);
+        sum += (p0 + p1) + (p2 + p3);
+        if (c + 1 < chunks) tmem_wait_ld();
+      }
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sm.s_empty[h][b]));
+      return true;
+    };
+    // This thread's token of a key tile: position, row of the weights but for the block, and the block's id, looked
+    // up a pair ahead.
+    struct Token {
+      int x, slot, w, blk;
+    };
+    auto locate = [&](int tile) {
+      Token k;
+      int rem, off;
+      const int vb = a.by_vbu.div((tile << a.lupt) + (key >> a.lu), rem);
+      k.slot = (a.c.by_W.div(rem, k.w) << a.lu) + (key & ((1 << a.lu) - 1));
+      k.x = vb * a.c.V + (a.c.by_I.div(k.slot, off) * a.c.W + k.w) * a.c.I + off;
+      k.blk = tile < s.tile0 + s.tiles && k.x < s.L ? a.c.table[static_cast<int64_t>(s.r) * a.c.max_vb + vb] : INT32_MIN;
+      return k;
+    };
     while (ok && items.next(sm, s, abort_flag, lim, true)) {
-      const bool active = h < s.nkt;
-      // this thread's token, its slot and its weight so far
-      int rem, w;
-      const int vb = a.by_vbu.div(((s.tile0 + h) << a.lupt) + (key >> a.lu), rem);
-      const int slot = (a.c.by_W.div(rem, w) << a.lu) + (key & ((1 << a.lu) - 1));
-      int off;
-      const int x = vb * a.c.V + (a.c.by_I.div(slot, off) * a.c.W + w) * a.c.I + off;
-      int64_t at = -1;
-      float old = 0.f;
-      if (active && x < s.L) {
-        const int64_t b = paged_block(a.c, s.r, vb, 602);
-        if (b >= 0) {
-          at = ((w * a.c.num_blocks + b) * a.c.Hkv + s.g) * a.c.bs + slot;
-          if (a.w_in && (!a.causal || x < s.pos0)) old = a.w_in[at];
-        }
-      }
-      const int first = a.causal ? max(0, x - s.pos0) : 0;   // first query that sees the token
-      float sum = 0.f;
-      for (int t = s.qf; t < s.qf + s.nq; ++t, ++n) {
-        const int lb = n % kLseStages;
-        if (!(ok = warp_wait(smem_u32(&sm.l_full[lb]), (n / kLseStages) & 1, abort_flag, lim, 650))) break;
-        if (active) {
-          const uint32_t b = cnt & 1;
-          if (!(ok = warp_wait(smem_u32(&sm.s_full[h][b]), (cnt >> 1) & 1, abort_flag, lim, 651))) break;
-          ++cnt;
-          tc_fence_after();
-          const int hi = columns(a, s, t), lo = min(BN, max(0, first - t * a.tpt) * a.G);
-          const uint32_t addr = t_lane + (2 * h + b) * BN;
-          const int chunks = (hi + 31) >> 5;
-          uint32_t xa[32], xb[32];
-          tmem_ld32(addr, xa);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c >= chunks) break;
-            uint32_t (&y)[32] = (c & 1) ? xb : xa;
-            uint32_t (&z)[32] = (c & 1) ? xa : xb;
-            if (c + 1 < chunks) tmem_ld32(addr + 32 * (c + 1), z);
-            if (__any_sync(0xffffffffu, lo > 32 * c) || hi < 32 * c + 32) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (32 * c + i < lo || 32 * c + i >= hi) y[i] = __float_as_uint(-CUDART_INF_F);
-            }
-            uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(&sm.neg_lse[lb][32 * c + i]);
-              float e0, e1, e2, e3;
-              f2unpack(ffma2(f2pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), sc2, nl.x), e0, e1);
-              f2unpack(ffma2(f2pack(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3])), sc2, nl.y), e2, e3);
-              acc0 = fadd2(acc0, f2pack(ex2(e0), ex2(e1)));
-              acc1 = fadd2(acc1, f2pack(ex2(e2), ex2(e3)));
-            }
-            float p0, p1, p2, p3;
-            f2unpack(acc0, p0, p1);
-            f2unpack(acc1, p2, p3);
-            sum += (p0 + p1) + (p2 + p3);
-            if (c + 1 < chunks) tmem_wait_ld();
+      Token ahead = locate(s.tile0 + h);
+      const uint32_t n_lse = s.nqt;   // tiles of LSE that stay for the item
+      for (uint32_t t = 0; t < n_lse && ok; ++t)
+        ok = warp_wait(smem_u32(&sm.l_full[(n + t) % kLseStages]), ((n + t) / kLseStages) & 1, abort_flag, lim, 650);
+#pragma unroll 1
+      for (int i = h; i < max(s.tiles, 2) && ok; i += 2) {
+        const bool active = i < s.tiles;   // false: slot 1 of an item of one tile, or past the last
+        const Token tk = ahead;
+        ahead = locate(s.tile0 + i + 2);
+        int64_t at = -1;
+        float old = 0.f;
+        if (tk.blk != INT32_MIN) {
+          if (tk.blk >= 0 && tk.blk < a.c.num_blocks) {
+            at = ((tk.w * a.c.num_blocks + tk.blk) * a.c.Hkv + s.g) * a.c.bs + tk.slot;
+            if (a.w_in && (!a.causal || tk.x < s.pos0)) old = a.w_in[at];
+          } else {
+            ra_record_error(RA_ERR_DEVICE_BOUNDS, 602);
           }
-          tc_fence_before();
-          mbar_arrive(smem_u32(&sm.s_empty[h][b]));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.l_empty[lb]));
+        const int first = a.causal ? max(0, tk.x - s.pos0) : 0;
+        sum = 0.f;
+        if (s.nqt) {
+          if (active) {
+            const int qf = s.nqt > 1 ? first_query_tile(a, s.tile0 + (i & ~1), s.pos0) : 0;
+#pragma unroll 1
+            for (int t = qf; t < s.nqt && ok; ++t) ok = add_tile(t, first);
+          }
+        } else {
+#pragma unroll 1
+          for (int t = s.qf; t < s.qf + s.nq && ok; ++t, ++n) {
+            const int lb = n % kLseStages;
+            if (!(ok = warp_wait(smem_u32(&sm.l_full[lb]), (n / kLseStages) & 1, abort_flag, lim, 652))) break;
+            if (active) ok = add_tile(t, first);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.l_empty[lb]));
+          }
+        }
+        if (ok && at >= 0) a.w_out[at] = old + sum;
       }
-      if (ok && at >= 0) a.w_out[at] = old + sum;
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0)
+        for (uint32_t t = 0; t < n_lse; ++t) mbar_arrive(smem_u32(&sm.l_empty[(n + t) % kLseStages]));
+      n += n_lse;
     }
   }
 
@@ -574,6 +650,7 @@ extern "C" ra_status ra_cp_attn_weights(const void* q, const float* lse, const v
   a.T = T; a.R = R; a.Hq = Hq; a.G = Hq / Hkv; a.causal = causal ? 1 : 0;
   a.tpt = BM / a.G;
   a.pair_q = a.causal ? 2 * BN / a.tpt : 0;
+  a.q_stages = d == 128 ? kQStages<128> : kQStages<64>;
   a.by_tpt = fast_div(a.tpt);
   a.by_G = fast_div(a.G);
   a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(d))) * kLog2e;

@@ -113,19 +113,19 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     int need = p.keep - p.n_sink - p.n_recent;
     uint32_t prefix = need > 0 ? 0 : 0xffffffffu;      // 0xffffffff: above every key
     for (int i = tid; i < 4 * 256; i += kThreads) hist[i >> 8][i & 255] = 0;
-    // the weights, four tokens of a thread in flight
-    for (int x0 = lo; x0 < hi; x0 += 4 * kThreads) {
-      float w[4];
-      int64_t at[4];
+    // the weights, eight tokens of a thread in flight
+    for (int x0 = lo; x0 < hi; x0 += 8 * kThreads) {
+      float w[8];
+      int64_t at[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 8; ++u) {
         const int x = x0 + u * kThreads + tid;
         at[u] = x < hi && (FITS || x - lo < p.keys_cap) ? paged_row(p.src, r, x, g, 701) : -1;
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) w[u] = at[u] >= 0 ? p.w[at[u]] : __int_as_float(0x7fffffff);
+      for (int u = 0; u < 8; ++u) w[u] = at[u] >= 0 ? p.w[at[u]] : __int_as_float(0x7fffffff);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 8; ++u) {
         const int x = x0 + u * kThreads + tid;
         if (x < hi && (FITS || x - lo < p.keys_cap)) keys[x - lo] = key_of(w[u]);
       }
