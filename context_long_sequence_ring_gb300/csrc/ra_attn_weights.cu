@@ -384,18 +384,28 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       uint32_t cnt0 = 0, cnt1 = 0;   // score tiles of each slot so far
       bool ok = true;
       const uint64_t dk = desc_sw128(smem_u32(sm.k[0]), 16, 1024), dq = desc_sw128(smem_u32(sm.q[0]), 16, 1024);
-      // S_h of the key tile at stage ks and the query tile t at stage qs
-      auto issue = [&](int h, int ks, int qs, int t) -> bool {
+      // A wait that passes at once still takes its 130 cycles or so, with the tensor core idle: the barriers of the
+      // next product (its score buffer, its key tile) are looked at while the last products of this one are
+      // queued.
+      bool s_ready = false, k_ready = false;
+      // S_h of the key tile at stage ks and the query tile t at stage qs; slot h_next is next, and its key tile at
+      // stage k_next (-1: this one, or none)
+      auto issue = [&](int h, int ks, int qs, int t, int h_next, int k_next, uint32_t k_next_ph) -> bool {
         const uint32_t c = h ? cnt1 : cnt0, b = 2 * h + (c & 1);
-        if (!mbar_wait(smem_u32(&sm.s_empty[0][0] + b), ((c >> 1) & 1) ^ 1, abort_flag, lim, 632)) return false;
+        if (!s_ready && !mbar_wait(smem_u32(&sm.s_empty[0][0] + b), ((c >> 1) & 1) ^ 1, abort_flag, lim, 632)) return false;
         if (h) ++cnt1; else ++cnt0;
         tc_fence_after();
         const uint32_t idesc = idesc_bf16_f32(BM, (columns(a, s, t) + 15) & ~15, 0, 0);
         const uint64_t d0 = dk + ks * (kTileBytes >> 4), d1 = dq + qs * (kTileBytes >> 4);
+        const uint32_t cn = h_next ? cnt1 : cnt0;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
           mma_bf16_ss(tmem + b * BN, d0 + off16, d1 + off16, idesc, kk > 0 ? 1u : 0u);
+          if (kk == D / 16 - 3) {
+            s_ready = mbar_test_wait(smem_u32(&sm.s_empty[0][0] + 2 * h_next + (cn & 1)), ((cn >> 1) & 1) ^ 1);
+            k_ready = k_next >= 0 && mbar_test_wait(smem_u32(&sm.k_full[k_next]), k_next_ph);
+          }
         }
         mma_commit(smem_u32(&sm.s_full[0][0] + b));
         return true;
@@ -404,22 +414,37 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         if (s.nq <= 0) continue;
         if (s.nqt) {
           const int q0 = qr.st;
-          int qf = 0;
+          // The slots take turns, so that neither waits behind the other's score buffers.
 #pragma unroll 1
-          for (int i = 0; i < s.tiles && ok; ++i) {
-            if ((i & 1) == 0 && s.nqt > 1) qf = first_query_tile(a, s.tile0 + i, s.pos0);
-            if (!(ok = mbar_wait(smem_u32(&sm.k_full[kr.st]), kr.ph, abort_flag, lim, 630))) break;
+          for (int i = 0; i < s.tiles && ok; i += 2) {
+            const int qf = s.nqt > 1 ? first_query_tile(a, s.tile0 + i, s.pos0) : 0;
+            const bool two = i + 1 < s.tiles, more = i + 2 < s.tiles;
+            int ks[2];
+            uint32_t kph[2];
+            ks[0] = kr.st; kph[0] = kr.ph;
+            kr.advance();
+            ks[1] = kr.st; kph[1] = kr.ph;
+            if (two) kr.advance();
+            if (!k_ready && !(ok = mbar_wait(smem_u32(&sm.k_full[ks[0]]), kph[0], abort_flag, lim, 630))) break;
             if (i == 0)
               for (int t = 0; t < s.nqt && ok; ++t) {
                 ok = mbar_wait(smem_u32(&sm.q_full[qr.st]), qr.ph, abort_flag, lim, 631);
                 qr.advance();
               }
 #pragma unroll 1
-            for (int t = qf; t < s.nqt && ok; ++t) ok = issue(i & 1, kr.st, q0 + t < NQ ? q0 + t : q0 + t - NQ, t);
-            if (!ok) break;
-            mma_commit(smem_u32(&sm.k_empty[kr.st]));
-            kr.advance();
+            for (int t = qf; t < s.nqt && ok; ++t) {
+              const bool last = t + 1 == s.nqt;
+              const int qs = q0 + t < NQ ? q0 + t : q0 + t - NQ;
+              const int k_after = last && more ? kr.st : -1;
+              if (!(ok = issue(0, ks[0], qs, t, two ? 1 : 0, two ? (t == qf ? ks[1] : -1) : k_after, two ? kph[1] : kr.ph))) break;
+              if (last) mma_commit(smem_u32(&sm.k_empty[ks[0]]));
+              if (!two) continue;
+              if (t == qf && !k_ready && !(ok = mbar_wait(smem_u32(&sm.k_full[ks[1]]), kph[1], abort_flag, lim, 635))) break;
+              if (!(ok = issue(1, ks[1], qs, t, 0, k_after, kr.ph))) break;
+              if (last) mma_commit(smem_u32(&sm.k_empty[ks[1]]));
+            }
           }
+          s_ready = k_ready = false;   // the next item starts anew
           for (int t = 0; t < s.nqt && ok; ++t) mma_commit(smem_u32(&sm.q_empty[q0 + t < NQ ? q0 + t : q0 + t - NQ]));
         } else {
           int ks[2] = {0, 0};
@@ -431,11 +456,12 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 #pragma unroll 1
           for (int t = s.qf; t < s.qf + s.nq && ok; ++t) {
             if (!(ok = mbar_wait(smem_u32(&sm.q_full[qr.st]), qr.ph, abort_flag, lim, 634))) break;
-            ok = issue(0, ks[0], qr.st, t) && (s.tiles < 2 || issue(1, ks[1], qr.st, t));
+            ok = issue(0, ks[0], qr.st, t, s.tiles < 2 ? 0 : 1, -1, 0) && (s.tiles < 2 || issue(1, ks[1], qr.st, t, 0, -1, 0));
             if (!ok) break;
             mma_commit(smem_u32(&sm.q_empty[qr.st]));
             qr.advance();
           }
+          s_ready = k_ready = false;
           if (ok) mma_commit(smem_u32(&sm.k_empty[ks[0]]));
           if (ok && s.tiles > 1) mma_commit(smem_u32(&sm.k_empty[ks[1]]));
         }

@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       Ring<NS> ring;
       uint32_t pf[2] = {0, 0}, q_cnt[2] = {0, 0}, seg = 0, clean_ph = 0;
       int q_next = 0;
-      bool ok = true;
+      bool ok = true, p_ready = false;
       const uint64_t dq0 = desc_sw128(smem_u32(sm.q[0]), 16, 1024);
       const uint64_t dk0 = desc_sw128(smem_u32(sm.kv[0]), 16, 1024);
       const uint64_t dv0 = desc_sw128(smem_u32(sm.kv[0]), BN * 128, 1024);
@@ -589,6 +589,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
           mma_bf16_ss(tmem + h * BN, dq + off16, dk + off16, kIdescS, kk > 0 ? 1u : 0u);
+          // the other slot's P, looked at while the last products are queued: a wait that passes at once takes
+          // some 130 cycles with the tensor core idle
+          if (kk == D / 16 - 3) p_ready = mbar_test_wait(smem_u32(&sm.p_full[h ^ 1]), pf[h ^ 1] & 1);
         }
         mma_commit(smem_u32(&sm.s_full[h]));
       };
@@ -649,7 +652,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             tc_fence_after();
             issue_pv(0, sv, j == 0);
             if (more) issue_s(0, 0, ring.st);
-            if (!(ok = mbar_wait(smem_u32(&sm.p_full[1]), pf[1] & 1, abort_flag, lim, 538))) break;
+            if (!(more && p_ready) && !(ok = mbar_wait(smem_u32(&sm.p_full[1]), pf[1] & 1, abort_flag, lim, 538))) break;
             ++pf[1];
             tc_fence_after();
             issue_pv(1, sv, j == 0);
