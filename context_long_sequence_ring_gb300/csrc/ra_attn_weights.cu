@@ -241,6 +241,25 @@ __device__ __forceinline__ int columns(const WeightArgs& a, const Item& s, int t
   return min(s.n - t * a.tpt, a.tpt) * a.G;
 }
 
+// Sum of 2^(x * scale - lse) over 32 columns.
+__device__ __forceinline__ float chunk_sum(const uint32_t (&x)[32], uint64_t sc2, const float* neg_lse) {
+  uint64_t acc[4];
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(neg_lse + i);
+    float e0, e1, e2, e3;
+    f2unpack(ffma2(f2pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2, nl.x), e0, e1);
+    f2unpack(ffma2(f2pack(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), sc2, nl.y), e2, e3);
+    const uint64_t u = f2pack(ex2(e0), ex2(e1)), v = f2pack(ex2(e2), ex2(e3));
+    const int k = (i >> 2) & 1;
+    acc[k] = i < 8 ? u : fadd2(acc[k], u);
+    acc[2 + k] = i < 8 ? v : fadd2(acc[2 + k], v);
+  }
+  float p0, p1;
+  f2unpack(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), p0, p1);
+  return p0 + p1;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kWeightThreads, 1)
     weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
@@ -529,36 +548,32 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       const int hi = columns(a, s, t), lo = min(BN, max(0, first - t * a.tpt) * a.G);
       const float* nlse = sm.neg_lse[(s.nqt ? n + t : n) % kLseStages];
       const uint32_t addr = t_lane + (2 * h + b) * BN;
-      const int chunks = (hi + 31) >> 5;
-      uint32_t xa[32], xb[32];
-      tmem_ld32(addr, xa);
-      tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c >= chunks) break;
-        uint32_t (&y)[32] = (c & 1) ? xb : xa;
-        uint32_t (&z)[32] = (c & 1) ? xa : xb;
-        if (c + 1 < chunks) tmem_ld32(addr + 32 * (c + 1), z);
-        if (__any_sync(0xffffffffu, lo > 32 * c) || hi < 32 * c + 32) {
+      if (hi == BN && !__any_sync(0xffffffffu, lo > 0)) {
+        // all columns count: two chunks a turn, the next one's load in flight (a rolled loop, that its code
+        // stays in the instruction cache)
+        uint32_t xa[32], xb[32];
+        tmem_ld32(addr, xa);
+        tmem_wait_ld();
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 64) {
+          tmem_ld32(addr + c + 32, xb);
+          sum += chunk_sum(xa, sc2, nlse + c);
+          tmem_wait_ld();
+          if (c == 0) tmem_ld32(addr + 64, xa);
+          sum += chunk_sum(xb, sc2, nlse + c + 32);
+          if (c == 0) tmem_wait_ld();
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < hi; c += 32) {
+          uint32_t x[32];
+          tmem_ld32(addr + c, x);
+          tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (32 * c + i < lo || 32 * c + i >= hi) y[i] = __float_as_uint(-CUDART_INF_F);
+            if (c + i < lo || c + i >= hi) x[i] = __float_as_uint(-CUDART_INF_F);
+          sum += chunk_sum(x, sc2, nlse + c);
         }
-        uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(&nlse[32 * c + i]);
-          float e0, e1, e2, e3;
-          f2unpack(ffma2(f2pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), sc2, nl.x), e0, e1);
-          f2unpack(ffma2(f2pack(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3])), sc2, nl.y), e2, e3);
-          acc0 = fadd2(acc0, f2pack(ex2(e0), ex2(e1)));
-          acc1 = fadd2(acc1, f2pack(ex2(e2), ex2(e3)));
-        }
-        float p0, p1, p2, p3;
-        f2unpack(acc0, p0, p1);
-        f2unpack(acc1, p2, p3);
-        sum += (p0 + p1) + (p2 + p3);
-        if (c + 1 < chunks) tmem_wait_ld();
       }
       tc_fence_before();
       mbar_arrive(smem_u32(&sm.s_empty[h][b]));
