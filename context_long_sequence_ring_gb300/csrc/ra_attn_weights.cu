@@ -46,7 +46,7 @@ struct WeightArgs : KeyUnits {
   int R, Hq, G, causal;
   int tpt, pair_q;        // tokens of a query tile; query tiles that a pair of key tiles spans under the causal mask
   int q_stages;           // query tiles that fit in shared memory
-  FastDiv by_tpt, by_G;
+  FastDiv by_tpt, by_G, by_pair_q;
   float scale_log2;
   const float* w_in;
   float* w_out;
@@ -77,7 +77,7 @@ __device__ __forceinline__ Req load_req(const WeightArgs& a, int r) {
 // Cost of pairs 0 .. k-1: each 5 for its loads and 4 for each query tile it meets.
 __device__ __forceinline__ long long prefix(const WeightArgs& a, const Req& q, int k) {
   const long long full = min(k, q.k0 + 1);               // pairs that meet all query tiles
-  const long long m = min(k - static_cast<int>(full), a.pair_q > 0 ? q.nq / a.pair_q : 1 << 30);
+  const long long m = min(k - static_cast<int>(full), a.pair_q > 0 ? a.by_pair_q.div(q.nq) : 1 << 30);
   return 5ll * k + 4 * (full * q.nq + m * q.nq - a.pair_q * (m * (m + 1) / 2));
 }
 
@@ -129,7 +129,7 @@ struct ItemIter {
       }
       total += __shfl_sync(0xffffffffu, warp_scan(c), 31);
     }
-    const long long share = (total + kCtas - 1) / kCtas;
+    const long long share = (total + kCtas - 1) / kCtas;   // by a constant
     lo = min(total, share * part);
     hi = min(total, share * (part + 1));
     if (lo >= hi) return false;
@@ -138,7 +138,7 @@ struct ItemIter {
     for (int base = 0; base < a.R; base += 32) {
       long long c = 0;
       if (base + lane < a.R) {
-        q = load_req(a, base + lane);
+        if (a.R > 32) q = load_req(a, base + lane);
         c = a.c.Hkv * prefix(a, q, q.pairs());
       }
       const long long x = warp_scan(c), pre = before + x - c;
@@ -147,7 +147,8 @@ struct ItemIter {
         if (!(pre <= lo && lo < pre + c)) return false;
         pairs = q.pairs();
         const long long per_head = prefix(a, q, pairs);
-        g = static_cast<int>((lo - pre) / per_head);
+        g = 0;
+        while (g + 1 < a.c.Hkv && (g + 1) * per_head <= lo - pre) ++g;
         const long long off = lo - pre - g * per_head;
         int u = 0, v = pairs;               // first pair with prefix >= off (pairs: the next head's first)
         while (u < v) {
@@ -694,6 +695,7 @@ extern "C" ra_status ra_cp_attn_weights(const void* q, const float* lse, const v
   a.q_stages = d == 128 ? kQStages<128> : kQStages<64>;
   a.by_tpt = fast_div(a.tpt);
   a.by_G = fast_div(a.G);
+  a.by_pair_q = fast_div(std::max(a.pair_q, 1));
   a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(d))) * kLog2e;
   a.w_in = w_in; a.w_out = w_out;
   a.wait_limit = ra::wait_limit();

@@ -285,23 +285,24 @@ struct SegIter {
 // columns, raw Q.K^T): P in bf16 pairs goes over the first BN/2 columns, m
 // (log2 units) and l are updated; returns the factor O must be scaled by.
 // As in the ring kernel a tile is first taken in one pass against the running
-// maximum, which stands while no chunk's sum of p exceeds 2^8; a tile in which it
-// does, a first tile and a masked one take two passes (maximum, then exps).
-// The two passes are rolled loops: they run once or twice per row tile, where
-// fetching unrolled code took longer than running it.
+// maximum (in a first tile: that of its first 32 columns), which stands while no
+// chunk's sum of p exceeds 2^8; a tile in which it does and a masked one take two
+// passes (maximum, then exps).  The two passes are rolled loops: they run once or
+// twice per row tile, where fetching unrolled code took longer than running it.
 // lm: visible columns of each 16, 8 bits each.  Rows that are not in use may
 // hold NaN scores: they are left out of the votes.
 __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool masked, bool row_ok, uint64_t lm,
                                               float scale, float& m, float& l) {
   const uint64_t sc2 = f2pack(scale, scale);
-  if (!first && !masked) {
+  if (!masked) {
     uint32_t pk[BN / 2];
-    const uint64_t negm2 = f2pack(-m, -m);
-    bool grow = __any_sync(0xffffffffu, row_ok && m == -CUDART_INF_F);
     float lsum = 0.f;
     uint32_t xa[32], xb[32];
     tmem_ld32(s_addr, xa);
     tmem_wait_ld();
+    if (first) m = chunk_mask_max(xa, 0, false, 0) * scale;
+    const uint64_t negm2 = f2pack(-m, -m);
+    bool grow = __any_sync(0xffffffffu, row_ok && m == -CUDART_INF_F);
 #pragma unroll
     for (int c = 0; c < BN / 32; ++c) {
       if (grow) break;

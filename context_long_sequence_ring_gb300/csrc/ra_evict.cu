@@ -32,7 +32,7 @@ struct EvictParams {
   float* w;
   Paged src, dst;  // dst.table may be src.table
   const int32_t* ctx;
-  int row_words, keep, n_sink, n_recent, in_place, keys_cap;
+  int row_words, keep, n_sink, n_recent, in_place, keys_cap, by_four;
   FastDiv by_words;   // by the words of a token's K and V
   int32_t *kept, *new_lens;
 };
@@ -86,7 +86,7 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_sums, 
 // FITS: a CTA's part of any context is in shared memory whole; else what is past the capacity is read again.
 template <bool FITS>
 __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ int hist[4][256], sums[256];
   __shared__ uint64_t warp_sums[kThreads / 32];
   __shared__ int counts[2];              // of this CTA's part: kept for certain, ties
@@ -107,27 +107,51 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     cluster_barrier();                   // kept is read by all of them
   } else {
     const int m0 = p.n_sink, m1 = N - p.n_recent;      // the middle part [m0, m1)
-    const int per = (N + C - 1) / C;
+    const int per = ((N + C - 1) / C + 3) & ~3;
     const int lo = min(N, rank * per), hi = min(N, lo + per);
     auto key = [&](int x) { return FITS || x - lo < p.keys_cap ? keys[x - lo] : load_key(p, r, g, x); };
     int need = p.keep - p.n_sink - p.n_recent;
     uint32_t prefix = need > 0 ? 0 : 0xffffffffu;      // 0xffffffff: above every key
     for (int i = tid; i < 4 * 256; i += kThreads) hist[i >> 8][i & 255] = 0;
-    // the weights, eight tokens of a thread in flight
-    for (int x0 = lo; x0 < hi; x0 += 8 * kThreads) {
-      float w[8];
-      int64_t at[8];
+    if (FITS && p.by_four) {
+      // four tokens lie together: one place, one load and one store for them; two such of a thread in flight
+      for (int x0 = lo + 4 * tid; x0 < hi; x0 += 8 * kThreads) {
+        int64_t at[2];
+        float4 w[2];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int x = x0 + u * kThreads + tid;
-        at[u] = x < hi && (FITS || x - lo < p.keys_cap) ? paged_row(p.src, r, x, g, 701) : -1;
+        for (int u = 0; u < 2; ++u) {
+          const int x = x0 + u * 4 * kThreads;
+          at[u] = x < hi ? paged_row(p.src, r, x, g, 701) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float nan = __int_as_float(0x7fffffff);
+          w[u] = at[u] >= 0 ? *reinterpret_cast<const float4*>(p.w + at[u]) : make_float4(nan, nan, nan, nan);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int x = x0 + u * 4 * kThreads;   // keys past hi (of the same four) are in the buffer, never read
+          if (x < hi)
+            *reinterpret_cast<uint4*>(keys + x - lo) = make_uint4(key_of(w[u].x), key_of(w[u].y), key_of(w[u].z), key_of(w[u].w));
+        }
       }
+    } else {
+      // four tokens of a thread in flight
+      for (int x0 = lo; x0 < hi; x0 += 4 * kThreads) {
+        float w[4];
+        int64_t at[4];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) w[u] = at[u] >= 0 ? p.w[at[u]] : __int_as_float(0x7fffffff);
+        for (int u = 0; u < 4; ++u) {
+          const int x = x0 + u * kThreads + tid;
+          at[u] = x < hi && (FITS || x - lo < p.keys_cap) ? paged_row(p.src, r, x, g, 701) : -1;
+        }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int x = x0 + u * kThreads + tid;
-        if (x < hi && (FITS || x - lo < p.keys_cap)) keys[x - lo] = key_of(w[u]);
+        for (int u = 0; u < 4; ++u) w[u] = at[u] >= 0 ? p.w[at[u]] : __int_as_float(0x7fffffff);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int x = x0 + u * kThreads + tid;
+          if (x < hi && (FITS || x - lo < p.keys_cap)) keys[x - lo] = key_of(w[u]);
+        }
       }
     }
     __syncthreads();
@@ -330,7 +354,8 @@ extern "C" ra_status ra_cp_evict(void* k_cache, void* v_cache, float* weights, c
   // CTAs of a cluster: as many as fill the GPU once (2 per SM), so that few heads still use all of it
   int C = 1;
   while (C < kMaxCluster && static_cast<int64_t>(R) * Hkv * 2 * C <= 152 * 2) C *= 2;
-  const int64_t most = ra::ceil_div(static_cast<int64_t>(max_vblocks) * p.src.V, C);
+  const int64_t most = ra::ceil_div(ra::ceil_div(static_cast<int64_t>(max_vblocks) * p.src.V, C), 4) * 4;
+  p.by_four = interleave % 4 == 0 && ra::aligned16(weights);   // then rows of four tokens are 16-byte words
   p.keys_cap = static_cast<int>(std::min<int64_t>(kKeysCap, most));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, R * Hkv);
