@@ -47,13 +47,15 @@ constexpr int kCtas = 152;         // parts of the work, one CTA per SM of a GB3
 constexpr int kChunkThreads = 384;
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRowBlocks = 8;
+constexpr int kFewRows = 32;       // rows of a tile that get a block each
+constexpr int kPairCost = 10;      // cost of a key in a pair tile
 
 struct ChunkArgs : KeyUnits {
   const int32_t *qsl, *ctx;
   int64_t T;
   int R, Hq, G, causal, out_bf16;
-  int tpt, f_split, over;         // tokens of a row tile; cost of a key in a split tile (5 in a pair), see Req
-  int cost_shift;
+  int tpt;                        // tokens of a row tile
+  int f_split, over_pair, over_split, cost_shift;   // costs, see Req
   FastDiv by_G, by_tpi;                // by the tokens of a pair of row tiles
   float scale_log2;
   void* o;                        // [T, Hq, D]
@@ -65,11 +67,11 @@ struct ChunkArgs : KeyUnits {
 };
 
 // ------------------------------------------------------------------ work
-// A request as the work division sees it.  The cost of an item is in keys times what a key costs: a pair tile
-// against a split tile takes about 5/4 of the time at D = 128 (the one bound by the tensor cores, the other by
-// HBM) and twice the time at D = 64 (both bound by the exps); prologue and epilogue of an item take
-// as long as `over` keys of its mode.  Costs are 32-bit numbers, in units of 2^cost_shift that the host
-// chooses from the sizes so that their sum fits.
+// A request as the work division sees it.  The cost of an item is in keys times what a key costs.  Measured over
+// the CTAs of one call: a pair tile 1.59 us at D = 128 and 1.60 at 64 (tensor core; exps), a split tile 1.24 (HBM)
+// and 1.11 (latency of one slot's chain, halved), and prologue and epilogue of an item as many keys as
+// `over_pair` and `over_split`.  Costs are 32-bit numbers, in units of 2^cost_shift that the host chooses from the
+// sizes so that their sum fits.
 struct Req {
   int r, q0, n, L, items;         // request, first query row, queries, context, row tiles (pairs of them) per head
   long long pos0;                 // position of query 0
@@ -87,8 +89,8 @@ __device__ __forceinline__ Req load_req(const ChunkArgs& a, int r) {
   q.pair = q.n > a.tpt;
   q.items = q.pair ? a.by_tpi.div(q.n + 2 * a.tpt - 1) : (q.n > 0);
   const long long before = q.pos0 < 0 ? 0 : (q.pos0 < q.L ? q.pos0 : q.L);
-  const long long keys = (q.pair ? 160 : a.over) + (a.causal ? before : q.L);
-  const int f = q.pair ? 5 : a.f_split;
+  const long long keys = (q.pair ? a.over_pair : a.over_split) + (a.causal ? before : q.L);
+  const int f = q.pair ? kPairCost : a.f_split;
   q.base = static_cast<uint32_t>(keys * f >> a.cost_shift) + 1;
   q.slope = a.causal ? static_cast<uint32_t>((q.pair ? 2 : 1) * a.tpt * f) >> a.cost_shift : 0;
   return q;
@@ -158,7 +160,7 @@ __device__ __forceinline__ bool make_plan(const ChunkArgs& a, int part, Plan& pl
   if (items <= kCtas / 2) {
     // pieces of at most total / (kCtas - items): at most kCtas of them, since an item has one incomplete piece
     const float p = max(static_cast<float>(plan.share), __fdividef(1.001f * static_cast<float>(total), static_cast<float>(kCtas - items)));
-    if (p < static_cast<float>(plan.share + ((a.f_split * a.over) >> a.cost_shift))) {
+    if (p < static_cast<float>(plan.share + ((a.f_split * a.over_split) >> a.cost_shift))) {
       plan.piece = p;
       uint32_t n = 0;
 #pragma unroll 1
@@ -924,6 +926,7 @@ template <int D>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkArgs a) {
   constexpr int E = D / 32;
   __shared__ int parts[kCtas], n_parts;
+  __shared__ __align__(16) float sums[kMergeThreads / 32][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // what the first kernel wrote is complete, and visible, once it has ended
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -932,7 +935,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
   const Segment sg = jn.s;
   const int slots = sg.pair ? 2 : 1;
   const int rows = min(sg.n - sg.tok0, slots * a.tpt) * a.G;
-  if (static_cast<int>(blockIdx.y) * (kMergeThreads / 32) * 2 >= rows) return;
+  if (static_cast<int>(blockIdx.y) * (rows <= kFewRows ? 1 : (kMergeThreads / 32) * 2) >= rows) return;   // no row in either scheme
   if (warp == 0) {
     // the partials, in order: of this part, and of those that follow
     const Plan plan = jn.plan;
@@ -950,6 +953,60 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
   }
   __syncthreads();
   const int used = n_parts;
+  if (rows <= kMergeRowBlocks || (rows <= kFewRows && used > kMergeThreads / 32)) {
+    // A row for each block, or few rows of many parts: a block a row, a warp every eighth part, joined in shared
+    // memory.  Against the form below a whole call takes 90 us instead of 94 with tiles of 4 rows in 19 parts, 19.1
+    // instead of 20.3 with 4 rows in 4, but 292 instead of 287 with 24 rows in two or three.
+    constexpr int kWarps = kMergeThreads / 32;
+    for (int i = blockIdx.y; i < rows; i += gridDim.y) {
+      const int h = i >= a.tpt * a.G ? 1 : 0, at_row = h * BM + i - h * a.tpt * a.G;
+      float M = -CUDART_INF_F, l = 0.f;
+      for (int p0 = 0; p0 < used; p0 += 32) {
+        float2 ml = make_float2(-CUDART_INF_F, 0.f);
+        if (p0 + lane < used) ml = a.ml_part[parts[p0 + lane] * 2 * BM + at_row];
+        float mn = ml.y > 0.f ? ml.x : -CUDART_INF_F;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mn = fmaxf(M, mn);
+        const float old = M == -CUDART_INF_F ? 0.f : ex2(M - mn);
+        float ls = ml.y > 0.f ? ex2(ml.x - mn) * ml.y : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+        M = mn;
+        l = l * old + ls;
+      }
+      __align__(16) float acc[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+      for (int p = warp; p < used; p += kWarps) {
+        const int64_t at = static_cast<int64_t>(parts[p]) * 2 * BM + at_row;
+        const float2 ml = a.ml_part[at];
+        const float w = ml.y > 0.f ? ex2(ml.x - M) : 0.f;
+        __align__(16) float v[E];
+        if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.o_part + at * D + E * lane);
+        else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.o_part + at * D + E * lane);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += w * v[e];
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) sums[warp][E * lane + e] = acc[e];
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) < D) {
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) x += sums[w][threadIdx.x];
+        x *= l > 0.f ? 1.f / l : 0.f;
+        const int tok = a.by_G.div(i), head = i - tok * a.G;
+        const int64_t orow = static_cast<int64_t>(sg.q0 + sg.tok0 + tok) * a.Hq + sg.g * a.G + head;
+        if (a.out_bf16) static_cast<__nv_bfloat16*>(a.o)[orow * D + threadIdx.x] = __float2bfloat16_rn(x);
+        else static_cast<float*>(a.o)[orow * D + threadIdx.x] = x;
+        if (a.lse && threadIdx.x == 0) a.lse[orow] = l > 0.f ? (M + log2f(l)) * kLn2 : -CUDART_INF_F;
+      }
+      __syncthreads();
+    }
+    return;
+  }
   // two rows at a time, for the loads' latency
   constexpr int kRows = 2;
   for (int i0 = kRows * (blockIdx.y * (kMergeThreads / 32) + warp); i0 < rows; i0 += kRows * gridDim.y * (kMergeThreads / 32)) {
@@ -1094,11 +1151,12 @@ extern "C" ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const 
   a.tpt = BM / a.G;
   a.by_G = fast_div(a.G);
   a.by_tpi = fast_div(2 * a.tpt);
-  a.f_split = d == 128 ? 4 : 2;
-  a.over = d == 128 ? 224 : 384;
+  a.f_split = d == 128 ? 8 : 7;
+  a.over_pair = d == 128 ? 470 : 400;
+  a.over_split = d == 128 ? 255 : 270;
   // the largest sum of costs these sizes allow stays below 2^31
   const double most = static_cast<double>(Hkv) * (static_cast<double>(T) / a.tpt + R) *
-                      (5.0 * (static_cast<double>(max_vblocks) * a.c.V + T + 512) + 1);
+                      (kPairCost * (static_cast<double>(max_vblocks) * a.c.V + T + 512) + 1);
   a.cost_shift = 0;
   while (std::ldexp(most, -a.cost_shift) > 1.0e9) ++a.cost_shift;
   a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(d))) * 1.4426950408889634f;
