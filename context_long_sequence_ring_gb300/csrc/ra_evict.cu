@@ -325,6 +325,7 @@ extern "C" ra_status ra_cp_evict(void* k_cache, void* v_cache, float* weights, c
   if (st != RA_OK) return st;
   RA_REQUIRE(dt == RA_BF16 || dt == RA_F32, "unknown dtype");
   RA_REQUIRE(d >= 1, "d must be >= 1");
+  RA_REQUIRE(keep <= (1 << 30), "keep must be at most 2^30");
   RA_REQUIRE(keep >= 1 && n_sink >= 0 && n_recent >= 0 && static_cast<int64_t>(n_sink) + n_recent <= keep,
              "keep >= 1 and 0 <= n_sink + n_recent <= keep required (keep %d, n_sink %d, n_recent %d)", keep, n_sink,
              n_recent);

@@ -40,9 +40,9 @@ struct Paged {
   int64_t num_blocks;
 };
 
-// Tokens of a context that the block table can hold; a longer one is cut.
+// Tokens of a context that the block table can hold, at most 2^30; a longer one is cut.
 __device__ __forceinline__ int paged_len(const Paged& c, int32_t ctx, int site) {
-  const int64_t cap = static_cast<int64_t>(c.max_vb) * c.V;
+  const int64_t table = static_cast<int64_t>(c.max_vb) * c.V, cap = table < (1 << 30) ? table : 1 << 30;
   if (ctx > cap) {
     ra_record_error(RA_ERR_DEVICE_BOUNDS, site);
     return static_cast<int>(cap);
@@ -93,7 +93,7 @@ inline ra_status check_paged(int32_t R, int32_t Hkv, int32_t block_size, int32_t
              interleave);
   RA_REQUIRE(static_cast<int64_t>(pcp) * dcp <= 4096, "pcp*dcp too large");
   const int64_t W = static_cast<int64_t>(pcp) * dcp;
-  RA_REQUIRE(W * block_size < (int64_t(1) << 31), "virtual block too large");
+  RA_REQUIRE(W * block_size <= (int64_t(1) << 24), "a virtual block holds at most 2^24 tokens");
   RA_REQUIRE(num_blocks < (int64_t(1) << 31) && W * num_blocks < (int64_t(1) << 31) / Hkv,
              "pcp*dcp*num_blocks*Hkv must be below 2^31");
   return RA_OK;

@@ -132,19 +132,20 @@ def _need_cuda(*ts):
             raise ValueError("tensor must be contiguous")
 
 
-def _need_here(dtype, *ts):
-    """Contiguous tensors of one dtype (None: any) on the current CUDA device."""
-    dev = None
+def _here(first, *ts) -> int:
+    """The current CUDA device, which all the (contiguous) tensors must be on; None is left out."""
+    dev = first.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError("tensor must be on the current CUDA device")
+    for t in (first,) + ts:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous and on the current CUDA device")
+    return dev
+
+
+def _of(dtype, *ts):
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda or not t.is_contiguous():
-            _need_cuda(t)
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError("tensor must be on the current CUDA device")
-        if dtype is not None and t.dtype != dtype:
+        if t is not None and t.dtype != dtype:
             raise ValueError("dtype must be %s, not %s" % (dtype, t.dtype))
 
 
@@ -228,27 +229,32 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     (``rope_frequencies``); positions int32, one per OUTPUT row.  out[r] comes from x[idx[r]] with idx
     (zero rows where idx < 0), else from x[r]; without idx, out may be x (in place).  ``backward`` turns
     by the negative angles: the gradient of x from the gradient of out."""
-    _need_here(torch.int32, positions, idx)
-    if x.dim() != 3 or (out is not None and out.dim() != 3):
-        raise ValueError("x and out must be [rows, H, d]")
+    dev = _here(positions, idx)
+    _of(torch.int32, positions, idx)
+    if x.dim() != 3:
+        raise ValueError("x must be [rows, H, d]")
     rows, H, d = x.shape
     n = rows if idx is None else idx.numel()
-    if out is None:
-        out = torch.empty((n, H, d), dtype=x.dtype, device=x.device)
-    if not (x.is_cuda and x.device == out.device == positions.device):
-        raise ValueError("x and out must be on the current CUDA device")
-    if out.shape != (n, H, d) or out.dtype != x.dtype:
-        raise ValueError("out must be %s of x's dtype" % ((n, H, d),))
-    if d > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
-        raise ValueError("the elements of a head must be contiguous")
     if positions.numel() != n:
         raise ValueError("one position per output row")
     if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 vector on the host")
-    xs, os_ = x.stride(), out.stride()
+    xs = x.stride()
+    if out is None:
+        out = torch.empty((n, H, d), dtype=x.dtype, device=positions.device)
+        os_ = (H * d, d, 1)
+    else:
+        if out.shape != (n, H, d) or out.dtype != x.dtype:
+            raise ValueError("out must be %s of x's dtype" % ((n, H, d),))
+        os_ = out.stride()
+    if x.get_device() != dev or out.get_device() != dev:
+        raise ValueError("x and out must be on the current CUDA device")
+    if d > 1 and (xs[2] != 1 or os_[2] != 1):
+        raise ValueError("the elements of a head must be contiguous")
     _check(lib().ra_rope_apply(x.data_ptr(), rows, xs[0], xs[1], out.data_ptr(), os_[0], os_[1], n, H, d,
                                2 * inv_freq.numel(), _dt(x), ROPE_STYLES[style], _ptr(idx), positions.data_ptr(),
-                               inv_freq.data_ptr(), float(mscale), 1 if backward else 0, _stream()))
+                               inv_freq.data_ptr(), mscale, 1 if backward else 0,
+                               torch._C._cuda_getCurrentRawStream(dev)))
     return out
 
 
@@ -570,18 +576,21 @@ def cp_lse_rescale_fn():
 
 
 def _need_paged(q, cache, block_table, query_start_loc, ctx_lens, pcp: int, dcp: int):
-    """Checks shared by the operators on a packed batch of queries and the paged cache."""
-    _need_here(torch.bfloat16, q, cache)
-    _need_here(torch.int32, block_table, query_start_loc, ctx_lens)
+    """Checks of types and sizes shared by the operators on a packed batch of queries and the paged cache."""
+    _of(torch.bfloat16, q, cache)
+    _of(torch.int32, block_table, query_start_loc, ctx_lens)
     if q.dim() != 3 or cache.dim() != 5 or block_table.dim() != 2:
         raise ValueError("q must be [T, Hq, d], the cache [W, NB, Hkv, bs, d], block_table [R, max_vblocks]")
-    if cache.shape[0] != pcp * dcp:
-        raise ValueError("cache has %d devices, pcp*dcp = %d" % (cache.shape[0], pcp * dcp))
-    if cache.shape[4] != q.shape[2]:
+    T, Hq, d = q.shape
+    W, NB, Hkv, bs, dk = cache.shape
+    R, max_vb = block_table.shape
+    if W != pcp * dcp:
+        raise ValueError("cache has %d devices, pcp*dcp = %d" % (W, pcp * dcp))
+    if dk != d:
         raise ValueError("q and the cache must have the same head dim")
-    R = block_table.shape[0]
     if query_start_loc.numel() != R + 1 or ctx_lens.numel() != R:
         raise ValueError("block_table has %d requests: query_start_loc needs R+1 entries, ctx_lens R" % R)
+    return T, Hq, d, NB, Hkv, bs, R, max_vb
 
 
 def cp_chunk_attn_workspace_size(Hq: int, Hkv: int, d: int) -> int:
@@ -596,27 +605,25 @@ def cp_chunk_attn(q, k_cache, v_cache, block_table, query_start_loc, ctx_lens, i
     """Attention of a packed batch of new tokens, q [T, Hq, d] (request r has rows query_start_loc[r] ..
     query_start_loc[r+1], the last ones of its ctx_lens[r] cached tokens), over the sharded paged cache
     -> (O [T, Hq, d], LSE [T, Hq]).  Rows of no request are left as they were (undefined in a new O)."""
-    _need_paged(q, k_cache, block_table, query_start_loc, ctx_lens, pcp, dcp)
-    T, Hq, d = q.shape
-    _, NB, Hkv, bs, _ = k_cache.shape
-    _need_here(torch.bfloat16, v_cache)
-    _need_here(None, workspace, o)
-    _need_here(torch.float32, lse)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
+    dev = _here(q, k_cache, v_cache, block_table, query_start_loc, ctx_lens, workspace, o, lse)
+    T, Hq, d, NB, Hkv, bs, R, max_vb = _need_paged(q, k_cache, block_table, query_start_loc, ctx_lens, pcp, dcp)
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("v_cache must be like k_cache")
     if workspace is None:
         workspace = torch.empty(cp_chunk_attn_workspace_size(Hq, Hkv, d), dtype=torch.uint8, device=q.device)
     if o is None:
         o = torch.empty((T, Hq, d), dtype=out_dtype, device=q.device)
+    elif o.shape != q.shape:
+        raise ValueError("o must be [T, Hq, d]")
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    if o.shape != q.shape or lse.shape != q.shape[:2]:
-        raise ValueError("o must be [T, Hq, d], lse [T, Hq]")
+    elif lse.shape != (T, Hq) or lse.dtype != torch.float32:
+        raise ValueError("lse must be float32 [T, Hq]")
     _check(lib().ra_cp_chunk_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                                  query_start_loc.data_ptr(), ctx_lens.data_ptr(), T, block_table.shape[0], Hq, Hkv, d,
-                                  bs, interleave, pcp, dcp, block_table.shape[1], NB, 1 if causal else 0,
-                                  float(scale or 0.0), o.data_ptr(), _dt(o), lse.data_ptr(), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _stream()))
+                                  query_start_loc.data_ptr(), ctx_lens.data_ptr(), T, R, Hq, Hkv, d, bs, interleave,
+                                  pcp, dcp, max_vb, NB, 1 if causal else 0, scale or 0.0, o.data_ptr(), _dt(o),
+                                  lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                  torch._C._cuda_getCurrentRawStream(dev)))
     return o, lse
 
 
@@ -625,20 +632,20 @@ def cp_attn_weights(q, lse, k_cache, block_table, query_start_loc, ctx_lens, int
     """Accumulated attention weight of every cached token, per K/V head -> w_out fp32 [W, NB, Hkv, bs]: w_in
     (None: 0; the chunk's own tokens start from 0) plus the softmax weights of the queries q [T, Hq, d] with
     their lse [T, Hq].  w_out may be w_in; slots of no token are left as they were (0 in a new w_out)."""
-    _need_paged(q, k_cache, block_table, query_start_loc, ctx_lens, pcp, dcp)
-    _need_here(torch.float32, lse, w_in, w_out)
-    T, Hq, d = q.shape
-    _, NB, Hkv, bs, _ = k_cache.shape
+    dev = _here(q, lse, k_cache, block_table, query_start_loc, ctx_lens, w_in, w_out)
+    T, Hq, d, NB, Hkv, bs, R, max_vb = _need_paged(q, k_cache, block_table, query_start_loc, ctx_lens, pcp, dcp)
+    _of(torch.float32, lse, w_in, w_out)
+    shape = k_cache.shape[:4]
     if w_out is None:
-        w_out = torch.zeros(k_cache.shape[:4], dtype=torch.float32, device=q.device)
-    if lse.shape != q.shape[:2]:
+        w_out = torch.zeros(shape, dtype=torch.float32, device=q.device)
+    if lse.shape != (T, Hq):
         raise ValueError("lse must be [T, Hq]")
-    if w_out.shape != k_cache.shape[:4] or (w_in is not None and w_in.shape != k_cache.shape[:4]):
+    if w_out.shape != shape or (w_in is not None and w_in.shape != shape):
         raise ValueError("the weights must be [W, NB, Hkv, bs]")
     _check(lib().ra_cp_attn_weights(q.data_ptr(), lse.data_ptr(), k_cache.data_ptr(), block_table.data_ptr(),
-                                    query_start_loc.data_ptr(), ctx_lens.data_ptr(), T, block_table.shape[0], Hq, Hkv,
-                                    d, bs, interleave, pcp, dcp, block_table.shape[1], NB, 1 if causal else 0,
-                                    float(scale or 0.0), _ptr(w_in), w_out.data_ptr(), _stream()))
+                                    query_start_loc.data_ptr(), ctx_lens.data_ptr(), T, R, Hq, Hkv, d, bs, interleave,
+                                    pcp, dcp, max_vb, NB, 1 if causal else 0, scale or 0.0, _ptr(w_in),
+                                    w_out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)))
     return w_out
 
 
@@ -648,30 +655,37 @@ def cp_evict(k_cache, v_cache, weights, block_table, ctx_lens, keep: int, interl
     and the heaviest of the others by ``weights`` fp32 [W, NB, Hkv, bs]) and pack them in order, with their
     weights, into the blocks of dst_block_table [R, .] (None: the request's own blocks).  Returns (kept int32
     [R, Hkv, keep]: former positions, -1 past the end; new_lens int32 [R])."""
-    _need_here(None, k_cache, v_cache)
-    _need_here(torch.float32, weights)
-    _need_here(torch.int32, block_table, ctx_lens, dst_block_table, kept, new_lens)
+    dev = _here(k_cache, v_cache, weights, block_table, ctx_lens, dst_block_table, kept, new_lens)
+    _of(torch.float32, weights)
+    _of(torch.int32, block_table, ctx_lens, dst_block_table, kept, new_lens)
     if k_cache.dim() != 5 or block_table.dim() != 2:
         raise ValueError("the cache must be [W, NB, Hkv, bs, d], block_table [R, max_vblocks]")
-    W, NB, Hkv, bs, d = k_cache.shape
-    R = block_table.shape[0]
+    shape = k_cache.shape
+    W, NB, Hkv, bs, d = shape
+    R, max_vb = block_table.shape
     if W != pcp * dcp:
         raise ValueError("cache has %d devices, pcp*dcp = %d" % (W, pcp * dcp))
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or weights.shape != k_cache.shape[:4]:
+    if v_cache.shape != shape or v_cache.dtype != k_cache.dtype or weights.shape != shape[:4]:
         raise ValueError("v_cache must be like k_cache, weights [W, NB, Hkv, bs]")
-    if ctx_lens.numel() != R or (dst_block_table is not None and
-                                 (dst_block_table.dim() != 2 or dst_block_table.shape[0] != R)):
-        raise ValueError("ctx_lens and dst_block_table must have one entry per request")
+    dst_vb = 0
+    if dst_block_table is not None:
+        if dst_block_table.dim() != 2 or dst_block_table.shape[0] != R:
+            raise ValueError("dst_block_table must be [R, dst_max_vblocks]")
+        dst_vb = dst_block_table.shape[1]
+    if ctx_lens.numel() != R:
+        raise ValueError("ctx_lens must have one entry per request")
     if kept is None:
         kept = torch.empty((R, Hkv, max(keep, 0)), dtype=torch.int32, device=k_cache.device)
+    elif kept.numel() != R * Hkv * keep:
+        raise ValueError("kept must be [R, Hkv, keep]")
     if new_lens is None:
         new_lens = torch.empty(R, dtype=torch.int32, device=k_cache.device)
-    if kept.numel() != R * Hkv * keep or new_lens.numel() != R:
-        raise ValueError("kept must be [R, Hkv, keep], new_lens [R]")
+    elif new_lens.numel() != R:
+        raise ValueError("new_lens must be [R]")
     _check(lib().ra_cp_evict(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), block_table.data_ptr(),
                              _ptr(dst_block_table), ctx_lens.data_ptr(), R, Hkv, d, _dt(k_cache), bs, interleave, pcp,
-                             dcp, block_table.shape[1], 0 if dst_block_table is None else dst_block_table.shape[1], NB,
-                             keep, n_sink, n_recent, kept.data_ptr(), new_lens.data_ptr(), _stream()))
+                             dcp, max_vb, dst_vb, NB, keep, n_sink, n_recent, kept.data_ptr(), new_lens.data_ptr(),
+                             torch._C._cuda_getCurrentRawStream(dev)))
     return kept, new_lens
 
 

@@ -590,11 +590,11 @@ ra_status ra_cp_head_split(const float* o_local, const float* lse_local, int32_t
  *             16-byte aligned: fp32 partials of contexts that several CTAs
  *             share.  Calls that overlap on the GPU need one each.
  * Requires Hq % Hkv == 0, Hq/Hkv <= 64, d in {64, 128}, block_size % 16 == 0,
- * block_size % interleave == 0, T*Hq < 2^31, pcp*dcp*num_blocks*Hkv < 2^31;
- * bf16 only.  The work is split over the GPU on the device from the lengths found
+ * block_size % interleave == 0, a virtual block of at most 2^24 tokens, T*Hq < 2^31,
+ * pcp*dcp*num_blocks*Hkv < 2^31; bf16 only.  The work is split over the GPU on the device from the lengths found
  * there, so a captured call may be replayed with other lengths.
  * Device bounds errors: a request whose query range is decreasing or outside [0, T]
- * (left out), a context longer than max_vblocks virtual blocks (cut), a block
+ * (left out), a context longer than max_vblocks virtual blocks or 2^30 tokens (cut), a block
  * id outside [0, num_blocks) (its tokens are left out).
  * ---------------------------------------------------------------------- */
 ra_status ra_cp_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t d, size_t* bytes);
@@ -658,9 +658,10 @@ ra_status ra_cp_attn_weights(const void* q, const float* lse, const void* k_cach
  * No block may be in two requests' tables below their ctx_lens (or in two
  * destination tables).
  * Requires 0 <= n_sink, n_recent; n_sink + n_recent <= keep, keep >= 1;
- * block_size % interleave == 0; d * element size a multiple of 16 bytes.
- * Device bounds errors: a context longer than max_vblocks virtual blocks
- * (cut), a bad source block id (its tokens count as lightest and move as zeros), a
+ * keep <= 2^30; R*Hkv <= 65535; block_size % interleave == 0; d * element size a
+ * multiple of 16 bytes, at most 16384 (RA_ERR_UNSUPPORTED otherwise).
+ * Device bounds errors: a context longer than max_vblocks virtual blocks or
+ * 2^30 tokens (cut), a bad source block id (its tokens count as lightest and move as zeros), a
  * destination outside the table or the cache (not written).
  * ---------------------------------------------------------------------- */
 ra_status ra_cp_evict(void* k_cache, void* v_cache, float* weights, const int32_t* block_table,

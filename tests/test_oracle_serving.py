@@ -235,7 +235,7 @@ def test_chunk_attn_and_weights_refusals(ra):
     for kw in [dict(v=None), dict(v=odd), dict(o=None), dict(o=odd), dict(dt=7), dict(ws=None), dict(ws=odd), dict(wsb=8)]:
         assert chunk(**kw) == INV, kw
     assert "workspace" in ra.last_error()
-    for kw in [dict(lse=None), dict(w=None), dict(w=ctypes.c_void_p((1 << 20) + 2)), dict(R=65536)]:
+    for kw in [dict(lse=None), dict(w=None), dict(w=ctypes.c_void_p((1 << 20) + 2))]:
         assert weights(**kw) == INV, kw
     assert chunk(T=0) == 0
     assert ra.cp_chunk_attn_workspace_size(8, 4, 128) >= 16
@@ -255,7 +255,8 @@ def test_evict_refusals(ra):
                    (dict(I=12), INV), (dict(dt=3), INV), (dict(d=0), INV), (dict(d=4), UNS), (dict(d=16384), UNS),
                    (dict(dbt=P), INV), (dict(k=None), INV), (dict(v=P), INV), (dict(w=None), INV), (dict(kept=None), INV),
                    (dict(new=P), INV), (dict(new=None), INV), (dict(k=ctypes.c_void_p((1 << 20) + 4)), INV),
-                   (dict(sink=2 ** 31 - 1, rec=2 ** 31 - 1, keep=2 ** 31 - 1), INV), (dict(R=65536), INV)]:
+                   (dict(sink=2 ** 31 - 1, rec=2 ** 31 - 1, keep=2 ** 31 - 1), INV), (dict(R=65536), INV), (dict(keep=2 ** 30 + 1), INV),
+                   (dict(R=16384), INV), (dict(bs=2 ** 24, I=16), INV)]:
         assert run(**kw) == st and ra.last_error() != "", kw
 
 
