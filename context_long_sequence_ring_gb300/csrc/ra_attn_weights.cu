@@ -61,18 +61,19 @@ struct Req {
   __device__ int pairs() const { return (tiles + 1) >> 1; }
 };
 
-__device__ __forceinline__ Req load_req(const WeightArgs& a, int r) {
+__device__ __forceinline__ Req make_req(const WeightArgs& a, int r, const Lens& x) {
   Req q;
   q.r = r;
-  query_range(a.qsl, r, a.T, q.q0, q.n, 600);
-  const int32_t ctx = a.ctx[r];
-  q.L = paged_len(a.c, ctx, 601);
-  q.pos0 = static_cast<long long>(ctx) - q.n;
+  query_range(x, a.T, q.q0, q.n, 600);
+  q.L = paged_len(a.c, x.ctx, 601);
+  q.pos0 = static_cast<long long>(x.ctx) - q.n;
   q.tiles = (units_below(a, q.L) + (1 << a.lupt) - 1) >> a.lupt;
   q.nq = a.by_tpt.div(q.n + a.tpt - 1);
   q.k0 = a.causal ? (q.pos0 <= 0 ? 0 : static_cast<int>(min(q.pos0 >> 8, 1ll << 30))) : 1 << 30;
   return q;
 }
+
+__device__ __forceinline__ Req load_req(const WeightArgs& a, int r) { return make_req(a, r, load_lens(a.qsl, a.ctx, r, a.R)); }
 
 // Cost of pairs 0 .. k-1: each 5 for its loads and 4 for each query tile it meets.
 __device__ __forceinline__ long long prefix(const WeightArgs& a, const Req& q, int k) {
@@ -116,53 +117,70 @@ struct ItemIter {
   int g, k, pairs;
   bool live;
   __device__ ItemIter(const WeightArgs& args) : a(args), live(false) {}
-  // The request with the first cost at or past lo, found by the whole warp; the returned lane walks.
-  __device__ bool find(int part) {
+  // f(request) for all requests in order, as in the chunk attention's plan.
+  template <class F>
+  __device__ __forceinline__ bool for_requests(const F& f) {
     const int lane = threadIdx.x & 31;
-    long long total = 0;
 #pragma unroll 1
-    for (int base = 0; base < a.R; base += 32) {
-      long long c = 0;
-      if (base + lane < a.R) {
-        q = load_req(a, base + lane);
-        c = a.c.Hkv * prefix(a, q, q.pairs());
-      }
-      total += __shfl_sync(0xffffffffu, warp_scan(c), 31);
-    }
-    const long long share = (total + kCtas - 1) / kCtas;   // by a constant
-    lo = min(total, share * part);
-    hi = min(total, share * (part + 1));
-    if (lo >= hi) return false;
-    long long before = 0;
+    for (int base = 0; base < a.R; base += 128) {
+      Lens x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = load_lens(a.qsl, a.ctx, base + 32 * j + lane, a.R);
 #pragma unroll 1
-    for (int base = 0; base < a.R; base += 32) {
-      long long c = 0;
-      if (base + lane < a.R) {
-        if (a.R > 32) q = load_req(a, base + lane);
-        c = a.c.Hkv * prefix(a, q, q.pairs());
-      }
-      const long long x = warp_scan(c), pre = before + x - c;
-      before += __shfl_sync(0xffffffffu, x, 31);
-      if (before > lo) {
-        if (!(pre <= lo && lo < pre + c)) return false;
-        pairs = q.pairs();
-        const long long per_head = prefix(a, q, pairs);
-        g = 0;
-        while (g + 1 < a.c.Hkv && (g + 1) * per_head <= lo - pre) ++g;
-        const long long off = lo - pre - g * per_head;
-        int u = 0, v = pairs;               // first pair with prefix >= off (pairs: the next head's first)
-        while (u < v) {
-          const int mid = (u + v) >> 1;
-          if (prefix(a, q, mid) >= off) v = mid; else u = mid + 1;
-        }
-        k = u;
-        at = pre + g * per_head + prefix(a, q, k);
-        live = true;
-        skip();
-        return true;
+      for (int j = 0; j < 4 && base + 32 * j < a.R; ++j) {
+        const Lens y = j == 0 ? x[0] : j == 1 ? x[1] : j == 2 ? x[2] : x[3];
+        if (f(make_req(a, base + 32 * j + lane, y))) return true;
       }
     }
     return false;
+  }
+  // The request with the first cost at or past the part's start, found by the whole warp; the lane that gets true
+  // walks.
+  __device__ bool find(int part) {
+    const int lane = threadIdx.x & 31;
+    const bool few = a.R <= 32;            // then each lane keeps its request
+    long long total = 0;
+    auto add = [&](const Req& x) {
+      total += a.c.Hkv * prefix(a, x, x.pairs());
+      return false;
+    };
+    if (few) {
+      q = load_req(a, lane);
+      add(q);
+    } else {
+      for_requests(add);
+    }
+    total = __shfl_sync(0xffffffffu, warp_scan(total), 31);
+    const long long share = (total + kCtas - 1) / kCtas;
+    lo = min(total, share * part);
+    hi = min(total, share * (part + 1));
+    if (lo >= hi) return false;
+    long long before = 0, pre = 0;
+    auto look = [&](const Req& x) {
+      const long long c = a.c.Hkv * prefix(a, x, x.pairs()), s = warp_scan(c);
+      pre = before + s - c;
+      before += __shfl_sync(0xffffffffu, s, 31);
+      if (before <= lo) return false;
+      live = pre <= lo && lo < pre + c;
+      if (live) q = x;
+      return true;
+    };
+    if (few) look(q); else for_requests(look);
+    if (!live) return false;
+    pairs = q.pairs();
+    const long long per_head = prefix(a, q, pairs);
+    g = 0;
+    while (g + 1 < a.c.Hkv && (g + 1) * per_head <= lo - pre) ++g;
+    const long long off = lo - pre - g * per_head;
+    int u = 0, v = pairs;               // first pair with prefix >= off (pairs: the next head's first)
+    while (u < v) {
+      const int mid = (u + v) >> 1;
+      if (prefix(a, q, mid) >= off) v = mid; else u = mid + 1;
+    }
+    k = u;
+    at = pre + g * per_head + prefix(a, q, k);
+    skip();
+    return true;
   }
   // Past the last pair of a head: on to the next head, the next request that has any.
   __device__ void skip() {

@@ -79,13 +79,12 @@ struct Req {
   bool pair;
 };
 
-__device__ __forceinline__ Req load_req(const ChunkArgs& a, int r) {
+__device__ __forceinline__ Req make_req(const ChunkArgs& a, int r, const Lens& x) {
   Req q;
   q.r = r;
-  query_range(a.qsl, r, a.T, q.q0, q.n, 510);
-  const int32_t ctx = a.ctx[r];
-  q.L = paged_len(a.c, ctx, 511);
-  q.pos0 = static_cast<long long>(ctx) - q.n;
+  query_range(x, a.T, q.q0, q.n, 510);
+  q.L = paged_len(a.c, x.ctx, 511);
+  q.pos0 = static_cast<long long>(x.ctx) - q.n;
   q.pair = q.n > a.tpt;
   q.items = q.pair ? a.by_tpi.div(q.n + 2 * a.tpt - 1) : (q.n > 0);
   const long long before = q.pos0 < 0 ? 0 : (q.pos0 < q.L ? q.pos0 : q.L);
@@ -95,6 +94,8 @@ __device__ __forceinline__ Req load_req(const ChunkArgs& a, int r) {
   q.slope = a.causal ? static_cast<uint32_t>((q.pair ? 2 : 1) * a.tpt * f) >> a.cost_shift : 0;
   return q;
 }
+
+__device__ __forceinline__ Req load_req(const ChunkArgs& a, int r) { return make_req(a, r, load_lens(a.qsl, a.ctx, r, a.R)); }
 
 // Visible tokens of query i: positions below the returned value.
 __device__ __forceinline__ int limit_of(const ChunkArgs& a, const Req& q, int i) {
@@ -140,18 +141,42 @@ struct Plan {
   }
 };
 
+// f(request) for all requests in order, each lane those at lane, lane + 32, ...; four loads in flight where there
+// are many (f may stop the walk: it returns true in all lanes or in none).
+template <class F>
+__device__ __forceinline__ bool for_requests(const ChunkArgs& a, const F& f) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int base = 0; base < a.R; base += 128) {
+    Lens x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = load_lens(a.qsl, a.ctx, base + 32 * j + lane, a.R);
+#pragma unroll 1
+    for (int j = 0; j < 4 && base + 32 * j < a.R; ++j) {
+      const Lens y = j == 0 ? x[0] : j == 1 ? x[1] : j == 2 ? x[2] : x[3];
+      if (f(make_req(a, base + 32 * j + lane, y))) return true;
+    }
+  }
+  return false;
+}
+
 // The plan and, in the lane that returns true, the request that holds the start of part `part` with the
 // cost before it (none: the part is empty).  One warp, a request per lane.
 __device__ __forceinline__ bool make_plan(const ChunkArgs& a, int part, Plan& plan, Req& q, uint32_t& pre) {
   const int lane = threadIdx.x & 31;
+  const bool few = a.R <= 32;            // then each lane keeps its request
   uint32_t total = 0, items = 0;
   plan.piece = 0.f;
-#pragma unroll 1
-  for (int base = 0; base < a.R; base += 32) {
-    q.items = 0;
-    if (base + lane < a.R) q = load_req(a, base + lane);
-    total += a.c.Hkv * plan.prefix(q, q.items);
-    items += a.c.Hkv * q.items;
+  auto add = [&](const Req& x) {
+    total += a.c.Hkv * plan.prefix(x, x.items);
+    items += a.c.Hkv * x.items;
+    return false;
+  };
+  if (few) {
+    q = load_req(a, lane);
+    add(q);
+  } else {
+    for_requests(a, add);
   }
   total = __reduce_add_sync(0xffffffffu, total);
   items = __reduce_add_sync(0xffffffffu, items);
@@ -162,18 +187,11 @@ __device__ __forceinline__ bool make_plan(const ChunkArgs& a, int part, Plan& pl
     const float p = max(static_cast<float>(plan.share), __fdividef(1.001f * static_cast<float>(total), static_cast<float>(kCtas - items)));
     if (p < static_cast<float>(plan.share + ((a.f_split * a.over_split) >> a.cost_shift))) {
       plan.piece = p;
-      uint32_t n = 0;
-#pragma unroll 1
-      for (int base = 0; base < a.R; base += 32) {
-        if (a.R > 32) {
-          q.items = 0;
-          if (base + lane < a.R) q = load_req(a, base + lane);
-        }
-        n += a.c.Hkv * plan.prefix(q, q.items);
-      }
-      n = __reduce_add_sync(0xffffffffu, n);
-      if (n <= kCtas) {
-        plan.total = n;
+      total = 0;
+      if (few) add(q); else for_requests(a, add);
+      total = __reduce_add_sync(0xffffffffu, total);
+      if (total <= kCtas) {
+        plan.total = total;
         plan.share = 1;
       } else {
         plan.piece = 0.f;
@@ -183,24 +201,24 @@ __device__ __forceinline__ bool make_plan(const ChunkArgs& a, int part, Plan& pl
   const uint32_t lo = plan.lo(part);
   if (lo >= plan.total) return false;
   uint32_t at = 0;
-#pragma unroll 1
-  for (int base = 0; base < a.R; base += 32) {
-    if (a.R > 32) {
-      q.items = 0;
-      if (base + lane < a.R) q = load_req(a, base + lane);
-    }
-    const uint32_t cost = a.c.Hkv * plan.prefix(q, q.items);
-    uint32_t x = cost;
+  bool mine = false;
+  auto find = [&](const Req& x) {
+    const uint32_t cost = a.c.Hkv * plan.prefix(x, x.items);
+    uint32_t s = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
     }
-    pre = at + x - cost;
-    at += __shfl_sync(0xffffffffu, x, 31);
-    if (at > lo) return pre <= lo && lo < pre + cost;
-  }
-  return false;
+    pre = at + s - cost;
+    at += __shfl_sync(0xffffffffu, s, 31);
+    if (at <= lo) return false;
+    mine = pre <= lo && lo < pre + cost;
+    if (mine) q = x;
+    return true;
+  };
+  if (few) find(q); else for_requests(a, find);
+  return mine;
 }
 
 // One row tile (pair) of a part, as the roles read it: K/V tiles [t0, t0 + nt) of `all`.

@@ -69,17 +69,24 @@ __device__ __forceinline__ int64_t paged_row(const Paged& c, int64_t r, int x, i
   return (((lbi - q * c.W) * c.num_blocks + b) * c.Hkv + g) * c.bs + q * c.I + (o - lbi * c.I);
 }
 
+// What the work division reads of a request.
+struct Lens {
+  int32_t q_begin, q_end, ctx;
+};
+__device__ __forceinline__ Lens load_lens(const int32_t* qsl, const int32_t* ctx, int r, int R) {
+  if (r >= R) return Lens{0, 0, 0};
+  return Lens{qsl[r], qsl[r + 1], ctx[r]};
+}
+
 // The request's queries [q0, q0 + n); n = 0 where the range is bad.
-__device__ __forceinline__ void query_range(const int32_t* __restrict__ qsl, int r, int64_t T, int& q0, int& n,
-                                            int site) {
-  const int32_t a = qsl[r], b = qsl[r + 1];
-  if (a < 0 || b < a || b > T) {
+__device__ __forceinline__ void query_range(const Lens& x, int64_t T, int& q0, int& n, int site) {
+  if (x.q_begin < 0 || x.q_end < x.q_begin || x.q_end > T) {
     ra_record_error(RA_ERR_DEVICE_BOUNDS, site);
     q0 = n = 0;
     return;
   }
-  q0 = a;
-  n = b - a;
+  q0 = x.q_begin;
+  n = x.q_end - x.q_begin;
 }
 
 // Host checks of the sizes that every paged operator shares.
