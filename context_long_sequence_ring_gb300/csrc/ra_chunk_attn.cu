@@ -346,11 +346,12 @@ __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool 
       return 1.f;
     }
   }
-  auto load = [&](uint32_t (&x)[32], int c) {
+  // A chunk of a masked tile is whole for the warp, out of sight for all of it, or neither.
+  auto load = [&](uint32_t (&x)[32], int c, uint32_t f) {
     tmem_ld32(s_addr + 32 * c, x);
     tmem_wait_ld();
-    if (masked) {
-      const int l0 = static_cast<int>(lm >> (16 * c)) & 255, l1 = static_cast<int>(lm >> (16 * c + 8)) & 255;
+    if (masked && !__all_sync(0xffffffffu, f == 0x1010u)) {
+      const int l0 = f & 255, l1 = f >> 8;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         if (i >= l0) x[i] = __float_as_uint(-CUDART_INF_F);
@@ -361,8 +362,10 @@ __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool 
   float mx = -CUDART_INF_F;
 #pragma unroll 1
   for (int c = 0; c < BN / 32; ++c) {
+    const uint32_t f = static_cast<uint32_t>(lm >> (16 * c)) & 0xffffu;
+    if (masked && !__any_sync(0xffffffffu, f != 0)) continue;
     uint32_t x[32];
-    load(x, c);
+    load(x, c, f);
     mx = fmaxf(mx, chunk_mask_max(x, 0, false, 0));
   }
   const float m_tile = mx * scale;
@@ -374,9 +377,15 @@ __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool 
   uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
 #pragma unroll 1
   for (int c = 0; c < BN / 32; ++c) {   // P of chunk c goes over scores that have been read
+    const uint32_t f = static_cast<uint32_t>(lm >> (16 * c)) & 0xffffu;
     uint32_t x[32], pk[16];
-    load(x, c);
-    chunk_exp_pack(x, sc2, negm2, acc0, acc1, pk);
+    if (masked && !__any_sync(0xffffffffu, f != 0)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[i] = 0;
+    } else {
+      load(x, c, f);
+      chunk_exp_pack(x, sc2, negm2, acc0, acc1, pk);
+    }
     tmem_st16(s_addr + 16 * c, pk);
   }
   float a0, a1, b0, b1;
@@ -741,8 +750,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (!(ok = warp_wait(smem_u32(&sm.v_dirty[ring.st]), (dirty_ph >> ring.st) & 1, abort_flag, lim, 540))) break;
           dirty_ph ^= 1u << ring.st;
           if (!(ok = warp_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 541))) break;
-          uint64_t lm;
-          tile_limits(a, sg.r, false, sg.t0 + j, sg.L, lm);
+          const uint64_t lm = tile_limits(a, sg.r, false, sg.t0 + j, sg.L);
 #pragma unroll 1
           for (int i0 = 0; i0 < BN; i0 += 32) {
             const int i = i0 + lane;
@@ -830,8 +838,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const bool bad = *reinterpret_cast<volatile int*>(&sm.bad_block) != 0;
           const int tile = sg.t0 + j;
           const bool masked = tile >= clean || bad;
-          uint64_t lm = 0;
-          if (masked) tile_limits(a, sg.r, bad, tile, vis, lm);
+          const uint64_t lm = masked ? tile_limits(a, sg.r, bad, tile, vis) : 0;
           const float alpha = softmax_step(t_lane + colS, n_mine == 0, masked, row_ok, lm, a.scale_log2, m, l);
           if (n_mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
             // O_h must hold the previous P.V before it is rescaled

@@ -63,31 +63,37 @@ __device__ __forceinline__ int unit_visible(const KeyUnits& a, int vb, int sub, 
   return max(0, min(1 << a.lu, q * a.c.I + min(part, a.c.I) - (sub << a.lu)));
 }
 
-// Visible columns (a prefix, 0..16) of each 16 columns of a tile, 8 bits each.  `check`: some block of this
-// CTA's work was bad, leave out the tokens of such blocks.
-__device__ __forceinline__ void tile_limits(const KeyUnits& a, int r, bool check, int tile, int lim, uint64_t& lm) {
-  int rem, w, v = 0;
-  int vb = a.by_vbu.div(tile << a.lupt, rem), sub = a.c.by_W.div(rem, w);
-  lm = 0;
+// Visible slots of unit `unit` of request r.  `check`: some block of this CTA's work was bad, leave out the tokens
+// of such blocks.
+__device__ __forceinline__ int visible_in(const KeyUnits& a, int r, bool check, int unit, int lim) {
+  int rem, w;
+  const int vb = a.by_vbu.div(unit, rem), sub = a.c.by_W.div(rem, w);
+  const int v = unit_visible(a, vb, sub, w, lim);
+  if (!check || v == 0) return v;
+  const int32_t b = vb < a.c.max_vb ? a.c.table[static_cast<int64_t>(r) * a.c.max_vb + vb] : -1;
+  return b < 0 || b >= a.c.num_blocks ? 0 : v;
+}
+
+// Visible columns (a prefix, 0..16) of each 16 columns of a tile, 8 bits each, for a row that sees positions below
+// lim.  By a whole warp: where all lanes have the same lim (the rows of one token) each computes one of the eight.
+__device__ __forceinline__ uint64_t tile_limits(const KeyUnits& a, int r, bool check, int tile, int lim) {
+  const int units = tile << a.lupt, per = a.lu - 4;   // 16-column groups of a unit: 2^per
+  if (__all_sync(0xffffffffu, lim == __shfl_sync(0xffffffffu, lim, 0))) {
+    const int i = threadIdx.x & 7;
+    const int v = visible_in(a, r, check, units + (i >> per), lim) - 16 * (i & ((1 << per) - 1));
+    const uint32_t byte = static_cast<uint32_t>(max(0, min(v, 16))) << (8 * (i & 3));
+    const uint32_t lo = __reduce_or_sync(0xffffffffu, i < 4 ? byte : 0u), hi = __reduce_or_sync(0xffffffffu, i < 4 ? 0u : byte);
+    return static_cast<uint64_t>(hi) << 32 | lo;
+  }
+  uint64_t lm = 0;
+  int v = 0;
 #pragma unroll 1
   for (int i = 0; i < 8; ++i) {
-    if ((i & ((1 << (a.lu - 4)) - 1)) == 0) {   // the next unit
-      v = unit_visible(a, vb, sub, w, lim);
-      if (check && v > 0) {
-        const int32_t b = vb < a.c.max_vb ? a.c.table[static_cast<int64_t>(r) * a.c.max_vb + vb] : -1;
-        if (b < 0 || b >= a.c.num_blocks) v = 0;
-      }
-      if (++w == a.c.W) {
-        w = 0;
-        if (++sub == a.nsub) {
-          sub = 0;
-          ++vb;
-        }
-      }
-    }
+    if ((i & ((1 << per) - 1)) == 0) v = visible_in(a, r, check, units + (i >> per), lim);   // the next unit
     lm |= static_cast<uint64_t>(min(v, 16)) << (8 * i);
     v = max(v - 16, 0);
   }
+  return lm;
 }
 
 // ------------------------------------------------------------------ pipeline pieces
