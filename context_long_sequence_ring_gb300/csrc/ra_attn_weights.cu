@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     Ring<NQ> qr;
     uint32_t k_issued = 0, q_issued = 0;
     bool ok = true;
+    const uint64_t once = policy_once();      // a key tile is read by one CTA, once
     const int oob = static_cast<int>(a.c.W * a.c.num_blocks * a.c.Hkv);   // past the last block: zero fill
     // the lane's unit of a key tile; its block is looked up a tile ahead
     struct Unit {
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       if (lane >> a.lupt == 0) {
         const int hb = x.blk < 0 || x.blk >= a.c.num_blocks ? oob : static_cast<int>((x.w * a.c.num_blocks + x.blk) * a.c.Hkv + s.g);
         for (int sl = 0; sl < SLABS; ++sl)
-          tma_load_3d(smem_u32(sm.k[kr.st] + sl * BN * 128 + (lane << a.lu) * 128), &tmK, bar, 64 * sl, x.s0, hb);
+          tma_load_3d_once(smem_u32(sm.k[kr.st] + sl * BN * 128 + (lane << a.lu) * 128), &tmK, bar, 64 * sl, x.s0, hb, once);
       }
       ++k_issued;
       kr.advance();

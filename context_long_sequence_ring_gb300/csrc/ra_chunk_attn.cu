@@ -509,11 +509,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint32_t q_cnt[2] = {0, 0};
     int q_next = 0;
     bool ok = true;
+    const uint64_t once = policy_once();      // a split tile's keys are read by one CTA
     const int oob = static_cast<int>(a.c.W * a.c.num_blocks * a.c.Hkv);   // past the last block: zero fill
     while (ok && segs.next(sm, sg, abort_flag, lim, true)) {
       const int nt = sg.nt;
       if (nt <= 0) continue;
-      const int la = sg.pair ? 1 : 2, nq = sg.pair ? 2 : 1;
+      const bool pair = sg.pair;
+      const int la = pair ? 1 : 2, nq = pair ? 2 : 1;
       auto load_tile = [&](const CUtensorMap* map, int blk, int s0, int w, bool to_clean) -> bool {
         if (!warp_wait(smem_u32(&sm.kv_empty[ring.st]), ring.ph ^ 1, abort_flag, lim, 521)) return false;
         const uint32_t bar = smem_u32(&sm.kv_full[ring.st]);
@@ -524,8 +526,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         __syncwarp();
         if (lane >> a.lupt == 0) {
           const int hb = blk < 0 ? oob : static_cast<int>((w * a.c.num_blocks + blk) * a.c.Hkv + sg.g);
-          for (int s = 0; s < SLABS; ++s)
-            tma_load_3d(smem_u32(sm.kv[ring.st] + s * BN * 128 + (lane << a.lu) * 128), map, bar, 64 * s, s0, hb);
+          for (int s = 0; s < SLABS; ++s) {
+            const uint32_t dst = smem_u32(sm.kv[ring.st] + s * BN * 128 + (lane << a.lu) * 128);
+            if (pair) tma_load_3d(dst, map, bar, 64 * s, s0, hb);
+            else tma_load_3d_once(dst, map, bar, 64 * s, s0, hb, once);
+          }
         }
         ++issued;
         ring.advance();
@@ -891,7 +896,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         m = M;
       }
       tc_fence_after();
-      const float inv_l = !whole ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+      const float inv_l = !whole ? 1.f : (l != 0.f ? 1.f / l : 0.f);
       f0 *= inv_l;
       f1 *= inv_l;
       if (warp_live) {
@@ -934,7 +939,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (!pair) mbar_arrive(smem_u32(&sm.o_empty[1]));
       if (row_ok) {
         if (!whole) a.ml_part[(part * 2 + (pair ? h : 0)) * BM + row] = make_float2(m, l);
-        else if (a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+        else if (a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
       }
     }
   }
@@ -989,12 +994,12 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
       for (int p0 = 0; p0 < used; p0 += 32) {
         float2 ml = make_float2(-CUDART_INF_F, 0.f);
         if (p0 + lane < used) ml = a.ml_part[parts[p0 + lane] * 2 * BM + at_row];
-        float mn = ml.y > 0.f ? ml.x : -CUDART_INF_F;
+        float mn = ml.y != 0.f ? ml.x : -CUDART_INF_F;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
         mn = fmaxf(M, mn);
         const float old = M == -CUDART_INF_F ? 0.f : ex2(M - mn);
-        float ls = ml.y > 0.f ? ex2(ml.x - mn) * ml.y : 0.f;
+        float ls = ml.y != 0.f ? ex2(ml.x - mn) * ml.y : 0.f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
         M = mn;
@@ -1007,7 +1012,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
       for (int p = warp; p < used; p += kWarps) {
         const int64_t at = static_cast<int64_t>(parts[p]) * 2 * BM + at_row;
         const float2 ml = a.ml_part[at];
-        const float w = ml.y > 0.f ? ex2(ml.x - M) : 0.f;
+        const float w = ml.y != 0.f ? ex2(ml.x - M) : 0.f;
         __align__(16) float v[E];
         if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.o_part + at * D + E * lane);
         else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.o_part + at * D + E * lane);
@@ -1021,12 +1026,12 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
         float x = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) x += sums[w][threadIdx.x];
-        x *= l > 0.f ? 1.f / l : 0.f;
+        x *= l != 0.f ? 1.f / l : 0.f;
         const int tok = a.by_G.div(i), head = i - tok * a.G;
         const int64_t orow = static_cast<int64_t>(sg.q0 + sg.tok0 + tok) * a.Hq + sg.g * a.G + head;
         if (a.out_bf16) static_cast<__nv_bfloat16*>(a.o)[orow * D + threadIdx.x] = __float2bfloat16_rn(x);
         else static_cast<float*>(a.o)[orow * D + threadIdx.x] = x;
-        if (a.lse && threadIdx.x == 0) a.lse[orow] = l > 0.f ? (M + log2f(l)) * kLn2 : -CUDART_INF_F;
+        if (a.lse && threadIdx.x == 0) a.lse[orow] = l != 0.f ? (M + log2f(l)) * kLn2 : -CUDART_INF_F;
       }
       __syncthreads();
     }
@@ -1054,11 +1059,11 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
       for (int j = 0; j < kRows; ++j) {
         float2 ml = make_float2(-CUDART_INF_F, 0.f);
         if (p0 + lane < used) ml = a.ml_part[parts[p0 + lane] * 2 * BM + at_row[j]];
-        float mn = ml.y > 0.f ? ml.x : -CUDART_INF_F;
+        float mn = ml.y != 0.f ? ml.x : -CUDART_INF_F;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
         mn = fmaxf(M[j], mn);
-        w[j] = ml.y > 0.f ? ex2(ml.x - mn) : 0.f;
+        w[j] = ml.y != 0.f ? ex2(ml.x - mn) : 0.f;
         const float old = M[j] == -CUDART_INF_F ? 0.f : ex2(M[j] - mn);
         float ls = w[j] * ml.y;
 #pragma unroll
@@ -1087,7 +1092,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
     for (int j = 0; j < kRows; ++j) {
       if (i0 + j >= rows) break;
       const int tok = a.by_G.div(i0 + j), head = i0 + j - tok * a.G;
-      const float inv = l[j] > 0.f ? 1.f / l[j] : 0.f;
+      const float inv = l[j] != 0.f ? 1.f / l[j] : 0.f;
       const int64_t orow = static_cast<int64_t>(sg.q0 + sg.tok0 + tok) * a.Hq + sg.g * a.G + head;
       if (a.out_bf16) {
         __align__(8) uint32_t w[E / 2];
@@ -1101,7 +1106,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
 #pragma unroll
         for (int e = 0; e < E; ++e) dst[e] = acc[j][e] * inv;
       }
-      if (a.lse && lane == 0) a.lse[orow] = l[j] > 0.f ? (M[j] + log2f(l[j])) * kLn2 : -CUDART_INF_F;
+      if (a.lse && lane == 0) a.lse[orow] = l[j] != 0.f ? (M[j] + log2f(l[j])) * kLn2 : -CUDART_INF_F;
     }
   }
 }

@@ -90,9 +90,18 @@ CHUNKS = [
     ([1029, 64, 3], [4, 1, 2], 40, 8, 128, 80, 80, 1, 2),
     ([2100], [1], 32, 8, 128, 128, 16, 2, 4),
 ]
+# few rows a tile (up to 16: held by all lane quarters) and just above, units of 16 and 32, every group size
+FEW = [
+    ([900, 40, 17], [1, 4, 16], 3, 3, 128, 16, 1, 1, 1),
+    ([513, 260], [5, 3], 10, 2, 64, 32, 2, 2, 2),
+    ([400, 1300, 31], [2, 1, 3], 16, 2, 128, 64, 16, 1, 2),
+    ([700, 129], [1, 2], 32, 2, 64, 48, 48, 1, 1),
+    ([1500], [4], 4, 1, 128, 128, 128, 1, 4),
+    ([1600, 5], [1, 1], 34, 2, 128, 32, 8, 1, 1),
+]
 
 
-@pytest.mark.parametrize("case", CHUNKS, ids=lambda c: "%s-%s-h%d.%d-d%d-b%d.%d-w%d" % (c[0], c[1], c[2], c[3], c[4], c[5],
+@pytest.mark.parametrize("case", CHUNKS + FEW, ids=lambda c: "%s-%s-h%d.%d-d%d-b%d.%d-w%d" % (c[0], c[1], c[2], c[3], c[4], c[5],
                                                                                   c[6], c[7] * c[8]))
 @pytest.mark.parametrize("causal", [True, False])
 def test_chunk_attn(ra, case, causal):
@@ -106,6 +115,46 @@ def test_chunk_attn(ra, case, causal):
     assert_chunk(o, lse, ref)
     o32, lse32 = ra.cp_chunk_attn(qd, kd, vd, td, sd, cd, I, pcp, dcp, causal=causal, out_dtype=torch.float32)
     assert o32.dtype == torch.float32 and torch.equal(o32.to(BF), o) and torch.equal(lse32, lse)
+
+
+@pytest.mark.parametrize("d,bs,Hq,Hkv", [(128, 32, 8, 2), (64, 16, 12, 3)])
+def test_chunk_attn_many_requests_of_all_kinds(ra, d, bs, Hq, Hkv):
+    """Several tiles to a CTA, one kind after another: single tokens, drafts, pieces of prompts, nothing."""
+    rng = np.random.default_rng(d)
+    n = rng.choice([0, 1, 1, 2, 4, 6, 20, 50, 90], size=330)
+    ctx = np.maximum(n + rng.integers(-3, 70, size=330), 0)
+    k, v, table, _ = paged(d, ctx.tolist(), Hkv, d, bs, 4, 1, 2)
+    q, qsl = batch(d, n, Hq, d)
+    ref = S.chunk_attn(q, k, v, table, qsl, ctx, bs, 4, 1, 2)
+    args = dev(q, k, v, table, qsl, torch.tensor(ctx, dtype=torch.int32))
+    o, lse = ra.cp_chunk_attn(*args, 4, 1, 2)
+    check_status(ra)
+    assert_chunk(o, lse, ref)
+    w = ra.cp_attn_weights(args[0], lse, args[1], *args[3:], 4, 1, 2)
+    check_status(ra)
+    want = S.attn_weights(q, lse.cpu(), k, table, qsl, ctx, bs, 4, 1, 2)
+    assert_weights(w, want)
+
+
+def test_chunk_attn_nan_queries_and_keys_reach_only_who_sees_them(ra):
+    ctx, n, Hq, Hkv, d = [300, 40, 70], [1, 9, 40], 4, 2, 128
+    k, v, table, _ = paged(31, ctx, Hkv, d, 16, 16, 1, 1)
+    q, qsl = batch(31, n, Hq, d)
+    ref = S.chunk_attn(q, k, v, table, qsl, ctx, 16, 16, 1, 1)
+    q[1, 0] = float("nan")                       # one head of a query of request 1
+    k[0, table[2, 4], 1, 5] = float("nan")       # token 69 of request 2: K/V head 1, seen by its last query alone
+    o, lse = ra.cp_chunk_attn(*dev(q, k, v, table, qsl, torch.tensor(ctx, dtype=torch.int32)), 16, 1, 1)
+    check_status(ra)
+    bad = torch.zeros((50, Hq), dtype=torch.bool)
+    bad[1, 0] = True
+    bad[49, 2:] = True
+    assert o.cpu()[bad].isnan().all() and lse.cpu()[bad].isnan().all()
+    assert not o.cpu()[~bad].isnan().any()
+    good = ~bad.numpy()
+    O, L, A = ref
+    err = np.abs(o.double().cpu().numpy() - O)
+    assert (err[good] <= (2.0 ** -8 * (A + np.abs(O)) + 2.0 ** -11 * A)[good]).all()
+    assert (np.abs(lse.double().cpu().numpy() - L)[good] <= 2.0 ** -12).all()
 
 
 def test_chunk_attn_rows_that_see_nothing_and_rows_of_nobody(ra):
