@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
           int c;
           const int j = t0 + p.by_words.div(e, c);
           const int64_t at = row_src[j];
-          if (at >= 0 && row_dst[j] >= 0) v[u] = c < rw ? p.kc[at * rw + c] : p.vc[at * rw + c - rw];
+          if (at >= 0 && row_dst[j] >= 0) v[u] = __ldcs(c < rw ? &p.kc[at * rw + c] : &p.vc[at * rw + c - rw]);
         }
       }
       if (p.in_place) {
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
           int c;
           const int j = t0 + p.by_words.div(e, c);
           const int64_t at = row_dst[j];
-          if (at >= 0) (c < rw ? p.kc[at * rw + c] : p.vc[at * rw + c - rw]) = v[u];
+          if (at >= 0) __stcs(c < rw ? &p.kc[at * rw + c] : &p.vc[at * rw + c - rw], v[u]);
         }
       }
     }
