@@ -135,9 +135,9 @@ def _need_cuda(*ts):
 def _here(first, *ts) -> int:
     """The current CUDA device, which all the (contiguous) tensors must be on; None is left out."""
     dev = first.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
-        raise ValueError("tensor must be on the current CUDA device")
-    for t in (first,) + ts:
+    if dev < 0 or dev != torch._C._cuda_getDevice() or not first.is_contiguous():
+        raise ValueError("tensors must be contiguous and on the current CUDA device")
+    for t in ts:
         if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous and on the current CUDA device")
     return dev
@@ -230,31 +230,31 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     (zero rows where idx < 0), else from x[r]; without idx, out may be x (in place).  ``backward`` turns
     by the negative angles: the gradient of x from the gradient of out."""
     dev = _here(positions, idx)
-    _of(torch.int32, positions, idx)
+    if positions.dtype != torch.int32 or (idx is not None and idx.dtype != torch.int32):
+        raise ValueError("positions and idx must be int32")
+    if x.get_device() != dev:
+        raise ValueError("x must be on the current CUDA device")
+    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 vector on the host")
     if x.dim() != 3:
         raise ValueError("x must be [rows, H, d]")
     rows, H, d = x.shape
+    rs, hs, es = x.stride()
     n = rows if idx is None else idx.numel()
     if positions.numel() != n:
         raise ValueError("one position per output row")
-    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous float64 vector on the host")
-    xs = x.stride()
     if out is None:
         out = torch.empty((n, H, d), dtype=x.dtype, device=positions.device)
-        os_ = (H * d, d, 1)
+        ors, ohs, oes = H * d, d, 1
     else:
-        if out.shape != (n, H, d) or out.dtype != x.dtype:
-            raise ValueError("out must be %s of x's dtype" % ((n, H, d),))
-        os_ = out.stride()
-    if x.get_device() != dev or out.get_device() != dev:
-        raise ValueError("x and out must be on the current CUDA device")
-    if d > 1 and (xs[2] != 1 or os_[2] != 1):
+        if out.shape != (n, H, d) or out.dtype != x.dtype or out.get_device() != dev:
+            raise ValueError("out must be %s of x's dtype, on its device" % ((n, H, d),))
+        ors, ohs, oes = out.stride()
+    if (es != 1 or oes != 1) and d > 1:
         raise ValueError("the elements of a head must be contiguous")
-    _check(lib().ra_rope_apply(x.data_ptr(), rows, xs[0], xs[1], out.data_ptr(), os_[0], os_[1], n, H, d,
-                               2 * inv_freq.numel(), _dt(x), ROPE_STYLES[style], _ptr(idx), positions.data_ptr(),
-                               inv_freq.data_ptr(), mscale, 1 if backward else 0,
-                               torch._C._cuda_getCurrentRawStream(dev)))
+    _check(lib().ra_rope_apply(x.data_ptr(), rows, rs, hs, out.data_ptr(), ors, ohs, n, H, d, 2 * inv_freq.numel(),
+                               _dt(x), ROPE_STYLES[style], _ptr(idx), positions.data_ptr(), inv_freq.data_ptr(), mscale,
+                               1 if backward else 0, torch._C._cuda_getCurrentRawStream(dev)))
     return out
 
 
