@@ -15,7 +15,9 @@
 //          tiles, each with its own running (m, l, O), joined at the end from
 //          tensor memory (HBM-bound: a K/V tile of 64 KB takes the SM's share of
 //          HBM bandwidth about 1.45 us, one slot's chain of score product, softmax
-//          and P.V about 1.3 us, two of them half of that).
+//          and P.V about 1.3 us, two of them half of that).  Its tiles are read by
+//          one CTA once and leave L2 first (drafts 286 -> 279 us, a token at 131072
+//          92 -> 87 us).
 //
 // Keys.  The cache is read where it lies, in units of 16 or 32 slots
 // (ra_key_units.cuh).  V rows of slots past the context
@@ -30,8 +32,14 @@
 // (m, l, O) go to the workspace (at most two per CTA) and a second small kernel
 // joins them.
 //
+// Measured (32/8 heads of 128, 8 devices, captured calls): 48 requests with 1-6 drafted
+// tokens over 2048-16384: 279 us, 6.6 TB/s, 96 % of the copy rate; one token over
+// 131072: 87 us, 6.2 TB/s; 4 single tokens over 200-2000: 20 us; 4096 tokens of a
+// prompt of 32768: 1.46 ms, 1410 TFLOP/s.  12 requests (24/8 heads of 64, blocks of
+// 16), prompts of 300-511 new tokens among single ones: 46 us.
+//
 // Roles (384 threads): warp 0 TMA, warp 1 MMA issue, warp 2 zeroing of dead V
-// rows, warps 4-7 and 8-11 softmax of slots 0 and 1.
+// rows, warp 3 schedule, warps 4-7 and 8-11 softmax of slots 0 and 1.
 // Tensor memory: S_h = columns [128h, +128) with P_h (bf16) over its first 64,
 // O_h = columns [256 + 128h, +D).
 #include <algorithm>

@@ -12,7 +12,10 @@
 // the context in shared memory; histograms and counts meet through distributed
 // shared memory, every CTA summing them for itself.  The move is bound by HBM
 // (2 x 512 bytes per kept token of head dim 128 in bf16); selecting reads the
-// weights once, 4 bytes per token.
+// weights once, 4 bytes per token, and is bound by latency: 4 digits of 2 us, reading
+// 2.5, counting and numbering 4.  16 prompts of 8192-16384 cut to 2048 (8 heads of
+// 128): 61 us, of which the move of 268 MB takes 41 (6.5 TB/s); moved with plain
+// loads and stores 63.  2 requests of 900-1301 cut to 512: 13 us.
 #include <algorithm>
 
 #include "ra_paged.cuh"

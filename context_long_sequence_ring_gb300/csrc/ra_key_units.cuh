@@ -8,7 +8,7 @@
 // is a prefix per unit.  u = 32 where the block size allows, else 16: with u = 64
 // and 128 the last virtual block of a sharded cache is read more coarsely
 // (chunk attention of 48 requests of 2k-16k tokens on 8 devices: 283 us at 32, 294 at
-// 64, 348 at 128; one long context is the same within 1 %).
+// 64, 348 at 128, before the loads left L2 first; one long context is the same within 1 %).
 #pragma once
 
 #include "ra_attn_tc.cuh"
