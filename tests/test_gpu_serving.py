@@ -649,3 +649,85 @@ def test_calls_on_a_side_stream(ra):
     s.synchronize()
     check_status(ra)
     assert torch.equal(o0, o1) and torch.equal(l0, l1) and torch.equal(w0, w1) and torch.equal(r0, r1)
+
+
+def test_calls_on_two_streams_at_once(ra):
+    """Two streams, a workspace each: every operator gives what it gives alone, however the calls overlap."""
+    ctx, n, Hq, Hkv, d = [3000, 700, 41], [1, 90, 5], 8, 2, 128
+    sets = []
+    for seed in (31, 32):
+        k, v, table, _ = paged(seed, ctx, Hkv, d, 32, 16, 2, 1)
+        q, qsl = batch(seed, n, Hq, d)
+        sets.append(dev(q, k, v, table, qsl, torch.tensor(ctx, dtype=torch.int32), torch.rand(k.shape[:4])))
+    f, _ = ra.rope_frequencies(d)
+    pos = torch.arange(sum(n), dtype=torch.int32, device=DEV)
+
+    def step(q, k, v, t, s, c, w):
+        o, lse = ra.cp_chunk_attn(q, k, v, t, s, c, 16, 2, 1)
+        new = ra.cp_attn_weights(q, lse, k, t, s, c, 16, 2, 1)
+        k2, v2, w2 = k.clone(), v.clone(), w.clone()
+        kept, lens = ra.cp_evict(k2, v2, w2, t, c, 256, 16, 2, 1, n_sink=3, n_recent=50)
+        return [o, lse, new, ra.rope_apply(q, pos, f), kept, lens, k2.view(torch.int16), v2.view(torch.int16), w2]
+
+    alone = [step(*x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for st, x in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append(step(*x))
+        torch.cuda.synchronize()
+        check_status(ra)
+        for a, b in zip(alone, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_caches_past_32_bit_offsets(ra):
+    """The same tokens at the far end of a cache of more than 2^31 elements: the same results to the bit."""
+    ctx, n, Hq, Hkv, d, bs, NB = [1500, 260], [3, 70], 16, 8, 128, 128, 17000
+    k, v, table, spare = paged(33, ctx, Hkv, d, bs, 16, 1, 1, spare=6)
+    q, qsl = batch(33, n, Hq, d)
+    w = torch.rand(k.shape[:4])
+    dst = spare[:6].view(2, 3)
+    far = lambda t: torch.where(t >= 0, NB - 1 - t, t).to(torch.int32)  # noqa: E731
+    small = dev(k, v, w)
+    big = [torch.empty((1, NB) + tuple(t.shape[2:]), dtype=t.dtype, device=DEV) for t in small]
+    assert big[0].numel() > 2 ** 31
+    at = far(torch.arange(k.shape[1])).long().to(DEV)
+    for b, t in zip(big, small):
+        b[:, at] = t
+    qd, sd, cd = dev(q, qsl, torch.tensor(ctx, dtype=torch.int32))
+    out = []
+    for (kc, vc, wc), tab, to in ((small, table, dst), (big, far(table), far(dst))):
+        td = tab.to(DEV)
+        o, lse = ra.cp_chunk_attn(qd, kc, vc, td, sd, cd, 16, 1, 1)
+        ra.cp_attn_weights(qd, lse, kc, td, sd, cd, 16, 1, 1, w_in=wc, w_out=wc)
+        kept, lens = ra.cp_evict(kc, vc, wc, td, cd, 300, 16, 1, 1, n_sink=2, n_recent=20, dst_block_table=to.to(DEV))
+        check_status(ra)
+        out.append([o, lse, kept, lens])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    for b, t in zip(big, small):
+        a, c = b[:, at], t
+        if a.dtype == BF:
+            a, c = a.view(torch.int16), c.view(torch.int16)
+        assert torch.equal(a, c)
+
+
+def test_rope_apply_more_threads_than_a_launch(ra):
+    """2^31 - 1 rows of one word each, in place: two launches, element offsets past 32 bits."""
+    rows, d, m = 2 ** 31 - 1, 4, 400
+    g = torch.Generator().manual_seed(34)
+    x = torch.zeros((rows, 1, d), dtype=BF, device=DEV)
+    pos = torch.zeros(rows, dtype=torch.int32, device=DEV)
+    f, _ = ra.rope_frequencies(d)
+    parts = []
+    for a in (0, 2 ** 30, rows - m):
+        xs, ps = dev(torch.randn((m, 1, d), generator=g).to(BF), torch.randint(0, 100000, (m,), generator=g).to(torch.int32))
+        x[a:a + m], pos[a:a + m] = xs, ps
+        parts.append((a, ra.rope_apply(xs, ps, f, style="interleaved")))
+    ra.rope_apply(x, pos, f, style="interleaved", out=x)
+    check_status(ra)
+    for a, want in parts:
+        assert torch.equal(x[a:a + m], want)
+    assert not x[m:2 ** 30].any()
