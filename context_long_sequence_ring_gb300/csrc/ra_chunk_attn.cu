@@ -40,8 +40,8 @@
 //
 // Roles (384 threads): warp 0 TMA, warp 1 MMA issue, warp 2 zeroing of dead V
 // rows, warp 3 schedule, warps 4-7 and 8-11 softmax of slots 0 and 1.
-// Tensor memory: S_h = columns [128h, +128) with P_h (bf16) over its first 64,
-// O_h = columns [256 + 128h, +D).
+// Tensor memory: two (D = 128) or three (D = 64) score tiles S_b = columns [128b, +128) with P (bf16)
+// over the first 64 of each, then O_0 and O_1, D columns each.
 #include <algorithm>
 #include <cmath>
 
@@ -416,16 +416,29 @@ __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool 
 constexpr int kSegs = 4;          // segments announced ahead
 constexpr int kSegReaders = 11;   // warps that read them: TMA, MMA, zeroing and 8 of softmax
 
+// A stage of the K/V ring holds one tile (D = 128: 32 KB), or V_j with the K tile that is used right after it
+// (D = 64: 2 x 16 KB): there the MMA thread and the TMA warp, at some 130 cycles for each wait, would take longer
+// than HBM for tiles of their own.
 template <int D>
-constexpr int kStages = D == 128 ? 5 : 8;   // K/V tiles in flight (32 or 16 KB each)
+constexpr bool kJoint = D == 64;
+template <int D>
+constexpr int kStages = D == 128 ? 5 : 6;
+
+// Score tiles in tensor memory.  With three (where the accumulators leave room: D = 64) the score product of a
+// split tile runs while both slots are at their softmax.
+template <int D>
+constexpr int kScores = D == 64 ? 3 : 2;
 
 template <int D>
 struct __align__(1024) ChunkSmem {
   uint8_t q[2][BM * D * 2];
-  uint8_t kv[kStages<D>][BN * D * 2];
+  uint8_t kv[kStages<D>][(kJoint<D> ? 2 : 1) * BN * D * 2];   // joint: V, K
   uint64_t q_full[2], q_empty[2], kv_full[kStages<D>], kv_empty[kStages<D>], v_dirty[kStages<D>], v_clean[kStages<D>];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2], ml_full, ml_empty, drain;
+  // With three score tiles slot h uses 2h and 2h + 1 in turn, so that a phase never ends before the one before it
+  // has been seen; else h.
+  uint64_t s_full[4], p_full[4], pv_done[4];
+  uint64_t o_empty[2], ml_full, ml_empty, drain;
   float2 ml[BM];
   Segment seg[kSegs];
   uint32_t tmem_base;
@@ -455,8 +468,11 @@ template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ChunkArgs a) {
-  constexpr int SLABS = D / 64, NS = kStages<D>;
-  constexpr uint32_t kTileBytes = BM * D * 2;
+  constexpr int SLABS = D / 64, NS = kStages<D>, NB = kScores<D>;
+  constexpr uint32_t kTileBytes = BM * D * 2, kStageBytes = (kJoint<D> ? 2 : 1) * kTileBytes;
+  constexpr uint32_t kInStage = kStageBytes - kTileBytes;   // of K
+  constexpr uint32_t kColAcc = NB * BN;   // accumulator of slot h: D columns from kColAcc + h * D
+  static_assert(kColAcc + 2 * D <= kTmemCols && NS > (kJoint<D> ? NB : 2 * NB - 1));
   constexpr uint32_t kIdescS = idesc_bf16_f32(BM, BN, 0, 0);
   constexpr uint32_t kIdescO = idesc_bf16_f32(BM, D, 0, 1);
 
@@ -465,15 +481,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm.abort_flag;
   const long long lim = a.wait_limit;
+  // barrier (of four) and parity of a slot's c-th use
+  auto turn = [](int h, uint32_t c) { return NB == 3 ? 2 * h + (c & 1) : h; };
+  auto phase = [](uint32_t c) { return NB == 3 ? (c >> 1) & 1 : c & 1; };
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sm.q_full[b]), 1);
       mbar_init(smem_u32(&sm.q_empty[b]), 1);
+      mbar_init(smem_u32(&sm.o_empty[b]), 128);
+    }
+    for (int b = 0; b < 4; ++b) {
       mbar_init(smem_u32(&sm.s_full[b]), 1);
       mbar_init(smem_u32(&sm.p_full[b]), 128);
       mbar_init(smem_u32(&sm.pv_done[b]), 1);
-      mbar_init(smem_u32(&sm.o_empty[b]), 128);
     }
     for (int s = 0; s < kSegs; ++s) {
       mbar_init(smem_u32(&sm.seg_full[s]), 1);
@@ -510,10 +531,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   SegReader segs;
   Segment sg;
 
-  // Order of the K/V ring in a segment: K_0 .. K_{la-1}, then V_j, K_{j+la} for each j, with la = 1
-  // (pair: both slots meet tile j) or 2 (split: slot j & 1 meets tile j).
+  // Order of the K/V ring in a segment: K_0 .. K_{la-1}, then V_j, K_{j+la} for each j (joint: in one stage), with
+  // la = 1 (pair: both slots meet tile j) or NB (split: slot j & 1 meets tile j).
   if (warp == 0) {
-    // ============================================================ TMA producer (whole warp: a unit per lane)
+    // ============================================================ TMA producer (whole warp: 64 columns of a unit per lane)
+    // lanes below `half` for V, the others for K
+    const int unit = lane & ((1 << a.lupt) - 1), slab = (lane >> a.lupt) & (SLABS - 1), half = SLABS << a.lupt;
+    const bool is_k = lane >= half, used = lane < 2 * half;
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
@@ -530,22 +554,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int nt = sg.nt;
       if (nt <= 0) continue;
       const bool pair = sg.pair;
-      const int la = pair ? 1 : 2, nq = pair ? 2 : 1;
-      auto load_tile = [&](const CUtensorMap* map, int blk, int s0, int w, bool to_clean) -> bool {
+      const int la = pair ? 1 : NB, nq = pair ? 2 : 1;
+      struct Unit {
+        int s0, w, blk;
+      };
+      // A stage: a tile of V, of K, or both.
+      auto load = [&](const Unit* v, bool to_clean, const Unit* k) -> bool {
         if (!warp_wait(smem_u32(&sm.kv_empty[ring.st]), ring.ph ^ 1, abort_flag, lim, 521)) return false;
         const uint32_t bar = smem_u32(&sm.kv_full[ring.st]);
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar, kTileBytes);
-          if (to_clean) mbar_arrive(smem_u32(&sm.v_dirty[ring.st]));
+          mbar_arrive_expect_tx(bar, v && k ? 2 * kTileBytes : kTileBytes);
+          if (v && to_clean) mbar_arrive(smem_u32(&sm.v_dirty[ring.st]));
         }
         __syncwarp();
-        if (lane >> a.lupt == 0) {
-          const int hb = blk < 0 ? oob : static_cast<int>((w * a.c.num_blocks + blk) * a.c.Hkv + sg.g);
-          for (int s = 0; s < SLABS; ++s) {
-            const uint32_t dst = smem_u32(sm.kv[ring.st] + s * BN * 128 + (lane << a.lu) * 128);
-            if (pair) tma_load_3d(dst, map, bar, 64 * s, s0, hb);
-            else tma_load_3d_once(dst, map, bar, 64 * s, s0, hb, once);
-          }
+        if (used && (is_k ? k != nullptr : v != nullptr)) {
+          const Unit x = is_k ? *k : *v;
+          const CUtensorMap* map = is_k ? &tmK : &tmV;
+          const uint32_t dst = smem_u32(sm.kv[ring.st] + (is_k ? kInStage : 0) + slab * BN * 128 + (unit << a.lu) * 128);
+          const int hb = x.blk < 0 ? oob : static_cast<int>((x.w * a.c.num_blocks + x.blk) * a.c.Hkv + sg.g);
+          if (pair) tma_load_3d(dst, map, bar, 64 * slab, x.s0, hb);
+          else tma_load_3d_once(dst, map, bar, 64 * slab, x.s0, hb, once);
         }
         ++issued;
         ring.advance();
@@ -553,16 +581,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       };
       // lane's unit of tile j: device, slot, id of its block; the id is looked at one tile later, so that its
       // load is in flight while the ring is waited for
-      struct Unit {
-        int s0, w, blk;
-      };
       auto locate = [&](int j) {
         Unit x;
         int rem;
-        const int vb = a.by_vbu.div(((sg.t0 + j) << a.lupt) + lane, rem);
+        const int vb = a.by_vbu.div(((sg.t0 + j) << a.lupt) + unit, rem);
         x.s0 = a.c.by_W.div(rem, x.w) << a.lu;
         x.blk = -1;
-        if (j < nt && lane >> a.lupt == 0 && static_cast<int64_t>(vb) * a.c.V < sg.L) {
+        if (j < nt && used && static_cast<int64_t>(vb) * a.c.V < sg.L) {
           x.blk = a.c.table[static_cast<int64_t>(sg.r) * a.c.max_vb + vb];
           if (x.blk < 0) x.blk = INT32_MAX;   // in the context, so that a bad id is one
         }
@@ -576,16 +601,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         __syncwarp();
       };
-      // v: unit of V_j, (k1: of the K tile after it when la = 2), k: of K_{j+la}, ahead: the one after that
-      Unit v = locate(0), k1 = v, k;
-      if (la == 2) k1 = locate(1);
-      k = locate(la);
-      checked(v);
-      ok = load_tile(&tmK, v.blk, v.s0, v.w, false);
-      if (ok && la == 2 && nt > 1) {
-        checked(k1);
-        ok = load_tile(&tmK, k1.blk, k1.s0, k1.w, false);
-      }
+      // u[i]: unit of tile j + i; the K tiles up to j + la have been issued but for the last
+      Unit u[NB + 1];
+#pragma unroll
+      for (int i = 0; i <= NB; ++i) u[i] = locate(i);
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        if (ok && i < la && i < nt) {
+          checked(u[i]);
+          ok = load(nullptr, false, &u[i]);
+        }
       for (int h = 0; h < nq && ok; ++h) {
         const int b = sg.pair ? h : q_next;
         ok = warp_wait(smem_u32(&sm.q_empty[b]), (q_cnt[b] & 1) ^ 1, abort_flag, lim, 520);
@@ -602,15 +627,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       if (!sg.pair) q_next ^= 1;
       for (int j = 0; j < nt && ok; ++j) {
-        const Unit ahead = locate(j + la + 1);
-        if (!(ok = load_tile(&tmV, v.blk, v.s0, v.w, j >= sg.dirty))) break;
-        if (j + la < nt) {
+        const Unit ahead = locate(j + NB + 1);
+        Unit k = pair ? u[1] : u[NB];
+        const bool more = j + la < nt;
+        if (more) {
           checked(k);
-          if (!(ok = load_tile(&tmK, k.blk, k.s0, k.w, false))) break;
+          if (pair) u[1] = k; else u[NB] = k;
         }
-        v = la == 2 ? k1 : k;
-        k1 = k;
-        k = ahead;
+        if (kJoint<D>) {
+          ok = load(&u[0], j >= sg.dirty, more ? &k : nullptr);
+        } else {
+          ok = load(&u[0], j >= sg.dirty, nullptr) && (!more || load(nullptr, false, &k));
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) u[i] = u[i + 1];
+        u[NB] = ahead;
       }
     }
     if ((!ok || *abort_flag) && lane == 0) {
@@ -627,35 +659,53 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // ============================================================ MMA issuer
     if (lane == 0) {
       Ring<NS> ring;
-      uint32_t pf[2] = {0, 0}, q_cnt[2] = {0, 0}, seg = 0, clean_ph = 0;
+      uint32_t s0 = 0, s1 = 0, p0 = 0, p1 = 0;   // score tiles issued, P taken, of each slot
+      uint32_t q_cnt[2] = {0, 0}, seg = 0, clean_ph = 0;
       int q_next = 0;
-      bool ok = true, p_ready = false;
+      bool ok = true, p_ready = false, v_ready = false, k_ready = false;
       const uint64_t dq0 = desc_sw128(smem_u32(sm.q[0]), 16, 1024);
-      const uint64_t dk0 = desc_sw128(smem_u32(sm.kv[0]), 16, 1024);
+      const uint64_t dk0 = desc_sw128(smem_u32(sm.kv[0] + kInStage), 16, 1024);
       const uint64_t dv0 = desc_sw128(smem_u32(sm.kv[0]), BN * 128, 1024);
-      auto issue_s = [&](int h, int b, int st) {
-        const uint64_t dq = dq0 + b * (kTileBytes >> 4), dk = dk0 + st * (kTileBytes >> 4);
+      // A wait that passes at once takes some 130 cycles with the tensor core idle, so the next barriers are looked
+      // at while the last products are queued.
+      auto test_p = [&](int h) {
+        const uint32_t c = h ? p1 : p0;
+        return mbar_test_wait(smem_u32(&sm.p_full[turn(h, c)]), phase(c));
+      };
+      auto test_kv = [&] { return mbar_test_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph); };
+      auto wait_p = [&](int h, int site) -> bool {
+        const uint32_t c = h ? p1 : p0;
+        if (!p_ready && !mbar_wait(smem_u32(&sm.p_full[turn(h, c)]), phase(c), abort_flag, lim, site)) return false;
+        p_ready = false;
+        if (h) ++p1; else ++p0;
+        return true;
+      };
+      // scores of slot h into tile b: Q tile qb, K tile st; `then` is called while the last products are queued
+      auto issue_s = [&](int h, int b, int qb, int st, auto then) {
+        const uint64_t dq = dq0 + qb * (kTileBytes >> 4), dk = dk0 + st * (kStageBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-          mma_bf16_ss(tmem + h * BN, dq + off16, dk + off16, kIdescS, kk > 0 ? 1u : 0u);
-          // the other slot's P, looked at while the last products are queued: a wait that passes at once takes
-          // some 130 cycles with the tensor core idle
-          if (kk == D / 16 - 3) p_ready = mbar_test_wait(smem_u32(&sm.p_full[h ^ 1]), pf[h ^ 1] & 1);
+          mma_bf16_ss(tmem + b * BN, dq + off16, dk + off16, kIdescS, kk > 0 ? 1u : 0u);
+          if (kk == D / 16 - 3) then();
         }
-        mma_commit(smem_u32(&sm.s_full[h]));
+        mma_commit(smem_u32(&sm.s_full[turn(h, h ? s1++ : s0++)]));
       };
-      auto issue_pv = [&](int h, int st, bool first) {
-        const uint64_t dv = dv0 + st * (kTileBytes >> 4);
+      auto issue_pv = [&](int h, int b, int st, bool first, auto then) {
+        const uint64_t dv = dv0 + st * (kStageBytes >> 4);
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_bf16_ts(tmem + kColO + h * BN, tmem + h * BN + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdescO,
+        for (int kk = 0; kk < BN / 16; ++kk) {
+          mma_bf16_ts(tmem + kColAcc + h * D, tmem + b * BN + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdescO,
                       (kk > 0 || !first) ? 1u : 0u);
-        mma_commit(smem_u32(&sm.pv_done[h]));
+          if (kk == BN / 16 - 3) then();
+        }
+        mma_commit(smem_u32(&sm.pv_done[turn(h, (h ? p1 : p0) - 1)]));   // its P has been counted
       };
+      auto nothing = [] {};
       // the V tile at the ring's head is in place, its dead rows zeroed
       auto wait_v = [&](int j, int dirty) -> bool {
-        if (!mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 531)) return false;
+        if (!v_ready && !mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 531)) return false;
+        v_ready = false;
         if (j >= dirty) {
           if (!mbar_wait(smem_u32(&sm.v_clean[ring.st]), (clean_ph >> ring.st) & 1, abort_flag, lim, 532)) return false;
           clean_ph ^= 1u << ring.st;
@@ -684,8 +734,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (pair) {
           if (!(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 533))) break;
           tc_fence_after();
-          issue_s(0, 0, ring.st);
-          issue_s(1, 1, ring.st);
+          issue_s(0, 0, 0, ring.st, nothing);
+          issue_s(1, 1, 1, ring.st, nothing);
           mma_commit(smem_u32(&sm.kv_empty[ring.st]));
           ring.advance();
           if (nt == 1) q_release();
@@ -694,54 +744,57 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (!(ok = wait_v(j, dirty))) break;
             const int sv = ring.st;
             ring.advance();
-            if (more && !(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 534))) break;
+            if (!kJoint<D> && more && !(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 534))) break;
+            const int sk = kJoint<D> ? sv : ring.st;
             if (j == 0 && !(ok = mbar_wait(smem_u32(&sm.o_empty[0]), oph, abort_flag, lim, 535))) break;
             if (j == 0 && !(ok = mbar_wait(smem_u32(&sm.o_empty[1]), oph, abort_flag, lim, 536))) break;
-            if (!(ok = mbar_wait(smem_u32(&sm.p_full[0]), pf[0] & 1, abort_flag, lim, 537))) break;
-            ++pf[0];
+            if (!(ok = wait_p(0, 537))) break;
             tc_fence_after();
-            issue_pv(0, sv, j == 0);
-            if (more) issue_s(0, 0, ring.st);
-            if (!(more && p_ready) && !(ok = mbar_wait(smem_u32(&sm.p_full[1]), pf[1] & 1, abort_flag, lim, 538))) break;
-            ++pf[1];
+            issue_pv(0, 0, sv, j == 0, nothing);
+            if (more) issue_s(0, 0, 0, sk, [&] { p_ready = test_p(1); });
+            if (!(ok = wait_p(1, 538))) break;
             tc_fence_after();
-            issue_pv(1, sv, j == 0);
-            mma_commit(smem_u32(&sm.kv_empty[sv]));
+            issue_pv(1, 1, sv, j == 0, nothing);
+            if (!kJoint<D> || !more) mma_commit(smem_u32(&sm.kv_empty[sv]));
             if (more) {
-              issue_s(1, 1, ring.st);
-              mma_commit(smem_u32(&sm.kv_empty[ring.st]));
-              ring.advance();
+              issue_s(1, 1, 1, sk, nothing);
+              mma_commit(smem_u32(&sm.kv_empty[sk]));
+              if (!kJoint<D>) ring.advance();
               if (j + 2 == nt) q_release();
             }
           }
         } else {
-          for (int j = 0; j < 2 && j < nt; ++j) {
+          for (int j = 0; j < NB && j < nt; ++j) {
             if (!(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 533))) break;
             tc_fence_after();
-            issue_s(j, qb, ring.st);
+            issue_s(j & 1, j, qb, ring.st, nothing);
             mma_commit(smem_u32(&sm.kv_empty[ring.st]));
             ring.advance();
           }
           if (!ok) break;
-          if (nt <= 2) q_release();
-          for (int j = 0; j < nt; ++j) {
+          if (nt <= NB) q_release();
+          for (int j = 0, b = 0; j < nt; ++j, b = b + 1 == NB ? 0 : b + 1) {
             const int h = j & 1;
-            const bool more = j + 2 < nt;
+            const bool more = j + NB < nt;
             if (!(ok = wait_v(j, dirty))) break;
             const int sv = ring.st;
             ring.advance();
-            if (more && !(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 534))) break;
             if (j < 2 && !(ok = mbar_wait(smem_u32(&sm.o_empty[h]), oph, abort_flag, lim, 535))) break;
-            if (!(ok = mbar_wait(smem_u32(&sm.p_full[h]), pf[h] & 1, abort_flag, lim, 537))) break;
-            ++pf[h];
+            if (!(ok = wait_p(h, 537))) break;
             tc_fence_after();
-            issue_pv(h, sv, j < 2);
-            mma_commit(smem_u32(&sm.kv_empty[sv]));
+            k_ready = kJoint<D>;
+            issue_pv(h, b, sv, j < 2, [&] { if (!kJoint<D>) k_ready = more && test_kv(); });
+            if (!kJoint<D> || !more) mma_commit(smem_u32(&sm.kv_empty[sv]));
             if (more) {
-              issue_s(h, qb, ring.st);
-              mma_commit(smem_u32(&sm.kv_empty[ring.st]));
-              ring.advance();
-              if (j + 3 == nt) q_release();
+              if (!k_ready && !(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 534))) break;
+              const int sk = kJoint<D> ? sv : ring.st;
+              if (!kJoint<D>) ring.advance();
+              issue_s((j + NB) & 1, b, qb, sk, [&] {
+                v_ready = test_kv();
+                p_ready = test_p(h ^ 1);
+              });
+              mma_commit(smem_u32(&sm.kv_empty[sk]));
+              if (j + NB + 1 == nt) q_release();
             }
           }
         }
@@ -763,7 +816,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     while (ok && segs.next(sm, sg, abort_flag, lim, true)) {
       const int nt = sg.nt;
       if (nt <= 0) continue;
-      const int la = sg.pair ? 1 : 2;
+      const int la = sg.pair ? 1 : NB;
       for (int j = 0; j < min(la, nt); ++j) ring.advance();
       for (int j = 0; j < nt; ++j) {
         if (j >= sg.dirty) {
@@ -788,7 +841,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           __syncwarp();
         }
         ring.advance();
-        if (j + la < nt) ring.advance();
+        if (!kJoint<D> && j + la < nt) ring.advance();
       }
     }
   } else if (warp == 3) {
@@ -820,9 +873,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t colS = h * BN, colO = kColO + h * BN;
+    const uint32_t colO = kColAcc + h * D;
     const int row_tok = row / a.G, row_head = row - row_tok * a.G;
     uint32_t s_cnt = 0, pv_cnt[2] = {0, 0}, splits = 0;
+    // product i of a slot is in its accumulator
+    auto wait_pv = [&](int slot, uint32_t i, int site) {
+      return warp_wait(smem_u32(&sm.pv_done[turn(slot, i)]), phase(i), abort_flag, lim, site);
+    };
     bool ok = true;
     while (ok && segs.next(sm, sg, abort_flag, lim, true)) {
       const int nt = sg.nt;
@@ -850,10 +907,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       float m = -CUDART_INF_F, l = 0.f;
       const int step = pair ? 1 : 2;
       int n_mine = 0;                      // tiles of this slot so far
+      int b = h;                           // score tile
       for (int j = pair ? 0 : h; j < nt; j += step) {
-        if (!(ok = warp_wait(smem_u32(&sm.s_full[h]), s_cnt & 1, abort_flag, lim, 550 + h))) break;
+        const int use = turn(h, s_cnt);
+        if (!(ok = warp_wait(smem_u32(&sm.s_full[use]), phase(s_cnt), abort_flag, lim, 550 + h))) break;
         ++s_cnt;
         tc_fence_after();
+        const uint32_t colS = (NB == 3 ? b : h) * BN;
         if (warp_live) {
           const bool bad = *reinterpret_cast<volatile int*>(&sm.bad_block) != 0;
           const int tile = sg.t0 + j;
@@ -862,7 +922,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const float alpha = softmax_step(t_lane + colS, n_mine == 0, masked, row_ok, lm, a.scale_log2, m, l);
           if (n_mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
             // O_h must hold the previous P.V before it is rescaled
-            if (!(ok = warp_wait(smem_u32(&sm.pv_done[h]), (pv_cnt[h] + n_mine - 1) & 1, abort_flag, lim, 552 + h))) break;
+            if (!(ok = wait_pv(h, pv_cnt[h] + n_mine - 1, 552 + h))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c4 = 0; c4 < D / 32; ++c4) {
@@ -878,7 +938,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         ++n_mine;
         tc_fence_before();
-        mbar_arrive(smem_u32(&sm.p_full[h]));
+        mbar_arrive(smem_u32(&sm.p_full[use]));
+        if (NB == 3 && !pair) b = b == 0 ? 2 : b - 1;   // two tiles on
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
@@ -894,7 +955,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         ++splits;
         continue;
       }
-      if (!(ok = warp_wait(smem_u32(&sm.pv_done[h]), (pv_cnt[h] - 1) & 1, abort_flag, lim, 554 + h))) break;
+      if (!(ok = wait_pv(h, pv_cnt[h] - 1, 554 + h))) break;
       float f0 = 1.f, f1 = 0.f;
       bool two = false;
       if (!pair) {
@@ -903,7 +964,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const float2 ml1 = sm.ml[row];
         mbar_arrive(smem_u32(&sm.ml_empty));
         two = nt > 1;
-        if (two && !(ok = warp_wait(smem_u32(&sm.pv_done[1]), (pv_cnt[1] - 1) & 1, abort_flag, lim, 556))) break;
+        if (two && !(ok = wait_pv(1, pv_cnt[1] - 1, 556))) break;
         const float M = fmaxf(m, ml1.x);
         f0 = M == -CUDART_INF_F ? 0.f : ex2(m - M);
         f1 = M == -CUDART_INF_F ? 0.f : ex2(ml1.x - M);
@@ -925,7 +986,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f0);
           if (two) {
             uint32_t y[32];
-            tmem_ld32(t_lane + kColO + BN + 32 * c4, y);
+            tmem_ld32(t_lane + kColAcc + D + 32 * c4, y);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(y[i]) * f1);
