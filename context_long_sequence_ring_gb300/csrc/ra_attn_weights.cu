@@ -265,11 +265,12 @@ __device__ __forceinline__ int columns(const WeightArgs& a, const Item& s, int t
   return min(s.n - t * a.tpt, a.tpt) * a.G;
 }
 
-// Sum of 2^(x * scale - lse) over 32 columns.
-__device__ __forceinline__ float chunk_sum(const uint32_t (&x)[32], uint64_t sc2, const float* neg_lse) {
+// Sum of 2^(x * scale - lse) over N columns.
+template <int N>
+__device__ __forceinline__ float chunk_sum(const uint32_t (&x)[N], uint64_t sc2, const float* neg_lse) {
   uint64_t acc[4];
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
+  for (int i = 0; i < N; i += 4) {
     const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(neg_lse + i);
     float e0, e1, e2, e3;
     f2unpack(ffma2(f2pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2, nl.x), e0, e1);
@@ -588,6 +589,14 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           sum += chunk_sum(xb, sc2, nlse + c + 32);
           if (c == 0) tmem_wait_ld();
         }
+      } else if (hi <= 16) {   // a token or a few: half a chunk
+        uint32_t x[16];
+        tmem_ld16(addr, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < lo || i >= hi) x[i] = __float_as_uint(-CUDART_INF_F);
+        sum += chunk_sum(x, sc2, nlse);
       } else {
 #pragma unroll 1
         for (int c = 0; c < hi; c += 32) {
