@@ -1036,7 +1036,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // what the first kernel wrote is complete, and visible, once it has ended
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Join& jn = a.join[blockIdx.x];
+  const Join jn = a.join[blockIdx.x];   // whole, in one latency
   if (jn.used == 0) return;
   const Segment sg = jn.s;
   const int slots = sg.pair ? 2 : 1;
@@ -1066,6 +1066,17 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
     constexpr int kWarps = kMergeThreads / 32;
     for (int i = blockIdx.y; i < rows; i += gridDim.y) {
       const int h = i >= a.tpt * a.G ? 1 : 0, at_row = h * BM + i - h * a.tpt * a.G;
+      auto load = [&](int p, float2& ml, float (&v)[E]) {
+        const int64_t at = static_cast<int64_t>(parts[p]) * 2 * BM + at_row;
+        ml = a.ml_part[at];
+        if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.o_part + at * D + E * lane);
+        else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.o_part + at * D + E * lane);
+      };
+      float2 ml0 = make_float2(0.f, 0.f);   // of this warp's first part, in flight beside the maxima
+      __align__(16) float v0[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v0[e] = 0.f;
+      if (warp < used) load(warp, ml0, v0);
       float M = -CUDART_INF_F, l = 0.f;
       for (int p0 = 0; p0 < used; p0 += 32) {
         float2 ml = make_float2(-CUDART_INF_F, 0.f);
@@ -1082,16 +1093,15 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
         l = l * old + ls;
       }
       __align__(16) float acc[E];
+      const float w0 = ml0.y != 0.f ? ex2(ml0.x - M) : 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = 0.f;
+      for (int e = 0; e < E; ++e) acc[e] = w0 * v0[e];
 #pragma unroll 4
-      for (int p = warp; p < used; p += kWarps) {
-        const int64_t at = static_cast<int64_t>(parts[p]) * 2 * BM + at_row;
-        const float2 ml = a.ml_part[at];
-        const float w = ml.y != 0.f ? ex2(ml.x - M) : 0.f;
+      for (int p = warp + kWarps; p < used; p += kWarps) {
+        float2 ml;
         __align__(16) float v[E];
-        if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.o_part + at * D + E * lane);
-        else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.o_part + at * D + E * lane);
+        load(p, ml, v);
+        const float w = ml.y != 0.f ? ex2(ml.x - M) : 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] += w * v[e];
       }
