@@ -15,7 +15,7 @@
 // What bounds it: for single tokens (few query rows; the columns are trimmed to the
 // rows there are) HBM: K is read once, the pairs of tiles of one head follow one
 // another on a CTA while the Q tile stays, and K leaves L2 first.  32 single tokens
-// over 2048-16384 (32/8 heads of 128): 100 us, 6.6 TB/s, 97 % of the copy rate.
+// over 2048-16384 (32/8 heads of 128): 99 us, 6.65 TB/s, 98 % of the copy rate.
 // For more queries one exp per (query row, key), 32 a cycle and SM: 512 cycles for a
 // 128 x 128 tile, as many as its score product.  With two warps to an SM quarter a
 // tile takes 1650-1900 instead, two slots side by side, and the MMA thread's turn over

@@ -17,7 +17,8 @@
 //          HBM bandwidth about 1.45 us, one slot's chain of score product, softmax
 //          and P.V about 1.3 us, two of them half of that).  Its tiles are read by
 //          one CTA once and leave L2 first (drafts 286 -> 279 us, a token at 131072
-//          92 -> 87 us).
+//          92 -> 87 us).  At D = 64 the fixed work of a tile would take longer than
+//          HBM: see kScores and kJoint.
 //
 // Keys.  The cache is read where it lies, in units of 16 or 32 slots
 // (ra_key_units.cuh).  V rows of slots past the context
@@ -33,10 +34,10 @@
 // joins them.
 //
 // Measured (32/8 heads of 128, 8 devices, captured calls): 48 requests with 1-6 drafted
-// tokens over 2048-16384: 279 us, 6.6 TB/s, 96 % of the copy rate; one token over
-// 131072: 87 us, 6.2 TB/s; 4 single tokens over 200-2000: 20 us; 4096 tokens of a
-// prompt of 32768: 1.46 ms, 1410 TFLOP/s.  12 requests (24/8 heads of 64, blocks of
-// 16), prompts of 300-511 new tokens among single ones: 46 us.
+// tokens over 2048-16384: 275-279 us, 6.6 TB/s, 97 % of the copy rate; one token over
+// 131072: 85 us, 6.3 TB/s; 4 single tokens over 200-2000: 18.7 us; 4096 tokens of a
+// prompt of 32768: 1.44 ms, 1430 TFLOP/s (1.54 sustained).  12 requests (24/8 heads of
+// 64, blocks of 16), prompts of 300-511 new tokens among single ones: 42 us.
 //
 // Roles (384 threads): warp 0 TMA, warp 1 MMA issue, warp 2 zeroing of dead V
 // rows, warp 3 schedule, warps 4-7 and 8-11 softmax of slots 0 and 1.
@@ -76,9 +77,10 @@ struct ChunkArgs : KeyUnits {
 
 // ------------------------------------------------------------------ work
 // A request as the work division sees it.  The cost of an item is in keys times what a key costs.  Measured over
-// the CTAs of one call: a pair tile 1.59 us at D = 128 and 1.60 at 64 (tensor core; exps), a split tile 1.24 (HBM)
-// and 1.11 (latency of one slot's chain, halved), and prologue and epilogue of an item as many keys as
-// `over_pair` and `over_split`.  Costs are 32-bit numbers, in units of 2^cost_shift that the host chooses from the
+// the CTAs of one call at D = 128: a pair tile 1.59 us (tensor core), a split tile 1.24 (HBM), and prologue and
+// epilogue of an item as many keys as `over_pair` and `over_split`.  At D = 64 the numbers are those with the least
+// time over batches of prompts, single tokens and both (split tiles at 6 tenths of a pair tile: 24 requests of both
+// kinds 102 us, at 5 or 7 tenths 105).  Costs are 32-bit numbers, in units of 2^cost_shift that the host chooses from the
 // sizes so that their sum fits.
 struct Req {
   int r, q0, n, L, items;         // request, first query row, queries, context, row tiles (pairs of them) per head
@@ -425,7 +427,8 @@ template <int D>
 constexpr int kStages = D == 128 ? 5 : 6;
 
 // Score tiles in tensor memory.  With three (where the accumulators leave room: D = 64) the score product of a
-// split tile runs while both slots are at their softmax.
+// split tile runs while both slots are at their softmax.  With the joint stages below: 64 requests of 1-4 tokens
+// over 2000-9000, blocks of 128, 135 us (5.2 TB/s) instead of 155.
 template <int D>
 constexpr int kScores = D == 64 ? 3 : 2;
 
@@ -1267,7 +1270,7 @@ extern "C" ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const 
   a.tpt = BM / a.G;
   a.by_G = fast_div(a.G);
   a.by_tpi = fast_div(2 * a.tpt);
-  a.f_split = d == 128 ? 8 : 7;
+  a.f_split = d == 128 ? 8 : 6;
   a.over_pair = d == 128 ? 470 : 460;
   a.over_split = d == 128 ? 255 : 270;
   // the largest sum of costs these sizes allow stays below 2^31
