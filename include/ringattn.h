@@ -615,6 +615,8 @@ ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const void* v_cac
  * own tokens (the last n_r, the positions of the queries) are not old: they
  * start from 0, so that a slot's former content is of no account.  causal = 0:
  * all tokens are old.
+ * Where the queries are only the last ones of a longer chunk, that chunk's
+ * earlier tokens count as old: their w_in must have been set (w_in = NULL: 0).
  *
  * q, query_start_loc, ctx_lens, k_cache, block table and sizes: as
  * ra_cp_chunk_attn.  The queries may be the last ones of a longer chunk.

@@ -90,7 +90,7 @@ CHUNKS = [
     ([1029, 64, 3], [4, 1, 2], 40, 8, 128, 80, 80, 1, 2),
     ([2100], [1], 32, 8, 128, 128, 16, 2, 4),
 ]
-# few rows a tile (up to 16: held by all lane quarters) and just above, units of 16 and 32, every group size
+# few rows a tile, units of 16 and 32, every group size
 FEW = [
     ([900, 40, 17], [1, 4, 16], 3, 3, 128, 16, 1, 1, 1),
     ([513, 260], [5, 3], 10, 2, 64, 32, 2, 2, 2),
@@ -134,6 +134,22 @@ def test_chunk_attn_many_requests_of_all_kinds(ra, d, bs, Hq, Hkv):
     check_status(ra)
     want = S.attn_weights(q, lse.cpu(), k, table, qsl, ctx, bs, 4, 1, 2)
     assert_weights(w, want)
+
+
+@pytest.mark.parametrize("d,bs,I,pcp", [(64, 16, 16, 1), (64, 64, 8, 2), (128, 32, 16, 2)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_chunk_attn_long_parts(ra, d, bs, I, pcp, causal):
+    """Enough keys that each CTA walks many tiles of several row tiles of both kinds, borders anywhere."""
+    rng = np.random.default_rng(bs)
+    n = rng.choice([1, 1, 3, 7, 70, 150], size=40)
+    ctx = n + rng.integers(200, 1900, size=40)
+    Hq, Hkv = 12, 4
+    k, v, table, _ = paged(bs, ctx.tolist(), Hkv, d, bs, I, pcp, 1)
+    q, qsl = batch(bs, n, Hq, d)
+    ref = S.chunk_attn(q, k, v, table, qsl, ctx, bs, I, pcp, 1, causal)
+    o, lse = ra.cp_chunk_attn(*dev(q, k, v, table, qsl, torch.tensor(ctx, dtype=torch.int32)), I, pcp, 1, causal=causal)
+    check_status(ra)
+    assert_chunk(o, lse, ref)
 
 
 def test_chunk_attn_nan_queries_and_keys_reach_only_who_sees_them(ra):
