@@ -409,8 +409,9 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       if (s.nqt == 0)
         for (int t = s.qf; t < s.qf + s.nq && ok; ++t) ok = load_q(t);
     }
-    if ((!ok || *abort_flag) && lane == 0) {
-      // let the copies already in flight land before the CTA exits
+    if (lane == 0) {
+      // The last load of each buffer lands before the CTA exits, also where another role has given up, or gives up
+      // from here on (else each has been waited for by its reader).
       for (int i = 0; i < NK; ++i) {
         const uint32_t n = k_issued / NK + (static_cast<uint32_t>(i) < k_issued % NK ? 1 : 0);
         if (n) mbar_wait_quiesce(smem_u32(&sm.k_full[i]), (n - 1) & 1, 1 << 22);
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         }
       }
       mma_commit(smem_u32(&sm.drain));
-      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, ok ? lim : (1 << 22)) && ok) {
+      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, ok ? max(lim, 1ll << 22) : 1 << 22) && ok) {
         *abort_flag = 1;
         ra_record_error(RA_ERR_TIMEOUT, 639);
       }

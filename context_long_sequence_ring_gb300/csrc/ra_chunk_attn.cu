@@ -648,8 +648,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         u[NB] = ahead;
       }
     }
-    if ((!ok || *abort_flag) && lane == 0) {
-      // let the copies already in flight land before the CTA exits: the last load of each buffer
+    if (lane == 0) {
+      // The last load of each buffer lands before the CTA exits, also where another role has given up, or gives up
+      // from here on (else each has been waited for by its reader).
       for (int b = 0; b < 2; ++b)
         if (q_cnt[b]) mbar_wait_quiesce(smem_u32(&sm.q_full[b]), (q_cnt[b] - 1) & 1, 1 << 22);
       for (int s = 0; s < NS; ++s) {
@@ -804,7 +805,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         ++seg;
       }
       mma_commit(smem_u32(&sm.drain));
-      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, ok ? lim : (1 << 22)) && ok) {
+      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, ok ? max(lim, 1ll << 22) : 1 << 22) && ok) {
         *abort_flag = 1;
         ra_record_error(RA_ERR_TIMEOUT, 539);
       }

@@ -10,6 +10,11 @@ Weights: each term e^{s - lse} is off by 2^-14 (score) + |s - lse| 2^-23, sums o
 within 2^-12 of the value for the sizes here.
 Rotations: the angle is off by 2^-23 turns (7.5e-7 rad), sin and cos by 2^-22 and products by three fp32
 roundings: 1.2e-6 < 2^-19 of |a| + |b|, plus the output's rounding."""
+import json
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -747,3 +752,49 @@ def test_rope_apply_more_threads_than_a_launch(ra):
     for a, want in parts:
         assert torch.equal(x[a:a + m], want)
     assert not x[m:2 ** 30].any()
+
+
+# ---------------------------------------------------------------------- failure detection
+
+CHILD = r"""
+import json, sys, torch
+sys.path.insert(0, sys.argv[1])
+from context_long_sequence_ring_gb300 import ringattn as ra
+dev = torch.device("cuda:0")
+g = torch.Generator().manual_seed(3)
+rnd = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(dev)
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)
+out = {}
+for d in (64, 128):
+    k, v, table = rnd(1, 40, 2, 64, d), rnd(1, 40, 2, 64, d), torch.arange(40, dtype=torch.int32, device=dev).view(2, 20)
+    for name, n in (("single", 1), ("prompt", 300)):
+        q, qsl, ctx = rnd(2 * n, 8, d), i32(0, n, 2 * n), i32(1200, 1000)
+        lse = torch.zeros((2 * n, 8), device=dev)
+        ra.cp_chunk_attn(q, k, v, table, qsl, ctx, 16, 1, 1)
+        st = ra.device_status()
+        out["chunk %s %d" % (name, d)] = [int(st), ra.last_error() if st else ""]
+        ra.cp_attn_weights(q, lse, k, table, qsl, ctx, 16, 1, 1)
+        st = ra.device_status()
+        out["weights %s %d" % (name, d)] = [int(st), ra.last_error() if st else ""]
+# the context still works: a kernel without waits gives the exact result
+src = torch.arange(64 * 8, dtype=torch.float32, device=dev).view(64, 8)
+idx = torch.randperm(64, generator=g).to(torch.int32).to(dev)
+out["gather_ok"] = bool(torch.equal(ra.gather_rows(src, idx).cpu(), src.cpu()[idx.long().cpu()]))
+out["final_status"] = int(ra.device_status())
+print(json.dumps(out))
+"""
+
+
+def test_timeouts_are_reported_and_the_context_survives():
+    """As for the other tensor-core kernels: with a wait limit of 64 cycles the first wait that is not satisfied at once
+    expires; the kernel records it, lets its copies and products land, frees tensor memory and returns."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CHILD, root], env=dict(os.environ, RA_WAIT_LIMIT_CYCLES="64"),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    res = json.loads(r.stdout.strip().splitlines()[-1])
+    from context_long_sequence_ring_gb300 import ringattn
+    for name, (st, msg) in ((n, x) for n, x in res.items() if isinstance(x, list)):
+        assert st == ringattn.RA_ERR_TIMEOUT, (name, st, msg)
+        assert ("chunk attention" if "chunk" in name else "attention weights") in msg, (name, msg)
+    assert len(res) == 10 and res["gather_ok"] and res["final_status"] == 0
