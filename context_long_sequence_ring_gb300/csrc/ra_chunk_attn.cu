@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         ++seg;
       }
       mma_commit(smem_u32(&sm.drain));
-      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, ok ? max(lim, 1ll << 22) : 1 << 22) && ok) {
+      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, ok ? lim : (1 << 22)) && ok) {
         *abort_flag = 1;
         ra_record_error(RA_ERR_TIMEOUT, 539);
       }
