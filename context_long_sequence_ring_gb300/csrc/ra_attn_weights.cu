@@ -56,6 +56,7 @@ struct WeightArgs : KeyUnits {
   const float* w_in;
   float* w_out;
   long long wait_limit;
+  long long drain_limit;  // of the last wait for products in flight: not below 2^22 cycles
 };
 
 // ------------------------------------------------------------------ work
@@ -246,11 +247,12 @@ static_assert(sizeof(WeightSmem<128>) + 1024 <= 232448 && sizeof(WeightSmem<64>)
 
 struct ItemReader {
   uint32_t at = 0;
+  bool ok = true;   // false: a wait expired, the part has not ended
   template <class Smem>
   __device__ bool next(Smem& sm, Item& s, volatile int* abort_flag, long long limit, bool whole_warp) {
     const int i = at & (kSegs - 1);
     const uint32_t bar = smem_u32(&sm.seg_full[i]), ph = (at / kSegs) & 1;
-    const bool ok = whole_warp ? warp_wait(bar, ph, abort_flag, limit, 670) : mbar_wait(bar, ph, abort_flag, limit, 671);
+    ok = whole_warp ? warp_wait(bar, ph, abort_flag, limit, 670) : mbar_wait(bar, ph, abort_flag, limit, 671);
     if (!ok) return false;
     s = sm.item[i];
     if (whole_warp) __syncwarp();
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         }
       }
       mma_commit(smem_u32(&sm.drain));
-      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, ok ? max(lim, 1ll << 22) : 1 << 22) && ok) {
+      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, a.drain_limit) && ok && items.ok) {
         *abort_flag = 1;
         ra_record_error(RA_ERR_TIMEOUT, 639);
       }
@@ -733,5 +735,6 @@ extern "C" ra_status ra_cp_attn_weights(const void* q, const float* lse, const v
   a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(d))) * kLog2e;
   a.w_in = w_in; a.w_out = w_out;
   a.wait_limit = ra::wait_limit();
+  a.drain_limit = std::max<long long>(a.wait_limit, 1ll << 22);
   return d == 128 ? launch_weights<128>(q, k_cache, a, stream) : launch_weights<64>(q, k_cache, a, stream);
 }

@@ -73,6 +73,7 @@ struct ChunkArgs : KeyUnits {
   float2* ml_part;                // [2 * kCtas][256]
   struct Join* join;              // [kCtas]
   long long wait_limit;
+  long long drain_limit;          // of the last wait for products in flight: not below 2^22 cycles
 };
 
 // ------------------------------------------------------------------ work
@@ -453,11 +454,12 @@ static_assert(sizeof(ChunkSmem<128>) + 1024 <= 232448 && sizeof(ChunkSmem<64>) +
 // A role's reading of the announced segments, in order.
 struct SegReader {
   uint32_t at = 0;
+  bool ok = true;   // false: a wait expired, the part has not ended
   template <class Smem>
   __device__ bool next(Smem& sm, Segment& s, volatile int* abort_flag, long long limit, bool whole_warp) {
     const int i = at & (kSegs - 1);
     const uint32_t bar = smem_u32(&sm.seg_full[i]), ph = (at / kSegs) & 1;
-    const bool ok = whole_warp ? warp_wait(bar, ph, abort_flag, limit, 570) : mbar_wait(bar, ph, abort_flag, limit, 571);
+    ok = whole_warp ? warp_wait(bar, ph, abort_flag, limit, 570) : mbar_wait(bar, ph, abort_flag, limit, 571);
     if (!ok) return false;
     s = sm.seg[i];
     if (whole_warp) __syncwarp();
@@ -804,8 +806,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         ++seg;
       }
+      // Every product lands before tensor memory is given back, however short the limit of the other waits and
+      // whichever of them expired (in its own loop, or for a segment).
       mma_commit(smem_u32(&sm.drain));
-      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, ok ? lim : (1 << 22)) && ok) {
+      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, a.drain_limit) && ok && segs.ok) {
         *abort_flag = 1;
         ra_record_error(RA_ERR_TIMEOUT, 539);
       }
@@ -1285,5 +1289,6 @@ extern "C" ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const 
   a.ml_part = reinterpret_cast<float2*>(a.o_part + part_floats(d));
   a.join = reinterpret_cast<Join*>(a.ml_part + part_floats(1));
   a.wait_limit = ra::wait_limit();
+  a.drain_limit = std::max<long long>(a.wait_limit, 1ll << 22);
   return d == 128 ? launch_chunk<128>(q, k_cache, v_cache, a, stream) : launch_chunk<64>(q, k_cache, v_cache, a, stream);
 }
