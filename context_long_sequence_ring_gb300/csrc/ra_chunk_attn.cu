@@ -1026,6 +1026,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         else if (a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
       }
     }
+    tmem_wait_st();   // a wait that expires between P's stores and their own wait leaves them in flight
   }
 
   tc_fence_before();
