@@ -267,17 +267,23 @@ __device__ __forceinline__ int columns(const WeightArgs& a, const Item& s, int t
   return min(s.n - t * a.tpt, a.tpt) * a.G;
 }
 
-// Sum of 2^(x * scale - lse) over N columns.
-template <int N>
-__device__ __forceinline__ float chunk_sum(const uint32_t (&x)[N], uint64_t sc2, const float* neg_lse) {
+// Sum of 2^(x * scale - lse) over N columns; MASK: over those in [lo, hi) alone.  Columns are left out after their
+// exponent is formed, so that a NaN in the score or the LSE of a row that does not see the token stays outside.
+template <bool MASK, int N>
+__device__ __forceinline__ float chunk_sum(const uint32_t (&x)[N], uint64_t sc2, const float* neg_lse, int lo, int hi) {
   uint64_t acc[4];
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
     const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(neg_lse + i);
-    float e0, e1, e2, e3;
-    f2unpack(ffma2(f2pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2, nl.x), e0, e1);
-    f2unpack(ffma2(f2pack(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), sc2, nl.y), e2, e3);
-    const uint64_t u = f2pack(ex2(e0), ex2(e1)), v = f2pack(ex2(e2), ex2(e3));
+    float e[4];
+    f2unpack(ffma2(f2pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2, nl.x), e[0], e[1]);
+    f2unpack(ffma2(f2pack(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), sc2, nl.y), e[2], e[3]);
+    if (MASK) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < lo || i + j >= hi) e[j] = -CUDART_INF_F;
+    }
+    const uint64_t u = f2pack(ex2(e[0]), ex2(e[1])), v = f2pack(ex2(e[2]), ex2(e[3]));
     const int k = (i >> 2) & 1;
     acc[k] = i < 8 ? u : fadd2(acc[k], u);
     acc[2 + k] = i < 8 ? v : fadd2(acc[2 + k], v);
@@ -586,30 +592,24 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < BN; c += 64) {
           tmem_ld32(addr + c + 32, xb);
-          sum += chunk_sum(xa, sc2, nlse + c);
+          sum += chunk_sum<false>(xa, sc2, nlse + c, 0, 0);
           tmem_wait_ld();
           if (c == 0) tmem_ld32(addr + 64, xa);
-          sum += chunk_sum(xb, sc2, nlse + c + 32);
+          sum += chunk_sum<false>(xb, sc2, nlse + c + 32, 0, 0);
           if (c == 0) tmem_wait_ld();
         }
       } else if (hi <= 16) {   // a token or a few: half a chunk
         uint32_t x[16];
         tmem_ld16(addr, x);
         tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < lo || i >= hi) x[i] = __float_as_uint(-CUDART_INF_F);
-        sum += chunk_sum(x, sc2, nlse);
+        sum += chunk_sum<true>(x, sc2, nlse, lo, hi);
       } else {
 #pragma unroll 1
         for (int c = 0; c < hi; c += 32) {
           uint32_t x[32];
           tmem_ld32(addr + c, x);
           tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < lo || c + i >= hi) x[i] = __float_as_uint(-CUDART_INF_F);
-          sum += chunk_sum(x, sc2, nlse + c);
+          sum += chunk_sum<true>(x, sc2, nlse + c, lo - c, hi - c);
         }
       }
       tc_fence_before();

@@ -125,6 +125,37 @@ def evict(k_cache, v_cache, weights, block_table, ctx_lens, keep, bs, I, pcp, dc
     return kept, new, k, v, w
 
 
+def evict_by_sort(weights, block_table, ctx_lens, keep, bs, I, pcp, dcp, n_sink=0, n_recent=0, dst_block_table=None):
+    """The same choice by sorting whole rows, for long contexts: (kept [R, Hkv, keep], moves), where moves lists, per
+    request and head, (device, block, slot) arrays of the tokens' old places and of their new ones."""
+    w = np.asarray(weights, dtype=np.float64)
+    R, Hkv = len(ctx_lens), w.shape[2]
+    table = np.asarray(block_table, dtype=np.int64)
+    dst = table if dst_block_table is None else np.asarray(dst_block_table, dtype=np.int64)
+    V = bs * pcp * dcp
+
+    def at(row, x):
+        lbi = x % V // I
+        return lbi % (pcp * dcp), row[x // V], lbi // (pcp * dcp) * I + x % V % I
+
+    kept, moves = np.full((R, Hkv, keep), -1, dtype=np.int64), []
+    for r in range(R):
+        N = int(ctx_lens[r])
+        pos = np.arange(N)
+        dev, blk, off = at(table[r], pos)
+        for g in range(Hkv):
+            ids = pos
+            if N > keep:
+                mid = pos[n_sink:N - n_recent]
+                val = w[dev, blk, g, off][mid]
+                nan = np.isnan(val)
+                order = np.lexsort((mid, -np.where(nan, 0.0, val), nan))[:keep - n_sink - n_recent]
+                ids = np.concatenate([pos[:n_sink], np.sort(mid[order]), pos[N - n_recent:]])
+            kept[r, g, :len(ids)] = ids
+            moves.append((r, g, (dev[ids], blk[ids], off[ids]), at(dst[r], np.arange(len(ids)))))
+    return kept, moves
+
+
 def rope_frequencies(rot, base=10000.0, scaling="none", factor=1.0, trained_len=32768.0):
     """(inv_freq [rot/2], mscale): theta_i = base^(-2i/rot) and its changes for longer contexts."""
     i = np.arange(rot // 2, dtype=np.float64)
@@ -157,4 +188,4 @@ def rope_apply(x, positions, inv_freq, mscale=1.0, style="half", backward=False,
     return y
 
 
-__all__ = ["token_rows", "chunk_attn", "attn_weights", "evict_choice", "evict", "rope_frequencies", "rope_apply"]
+__all__ = ["token_rows", "chunk_attn", "attn_weights", "evict_choice", "evict", "evict_by_sort", "rope_frequencies", "rope_apply"]

@@ -1,0 +1,68 @@
+"""Edges of the serving operators: queries whose LSE is not a number or that are marked as seeing nothing, evictions of
+every cluster size and past the keys that shared memory holds, ranges that are left out, and batches whose work is
+counted in coarser units.  Tolerances as in the parity tests of the same operators."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving as S
+from tests._gpu import ra_lib, check_status
+from tests.test_gpu_serving import BF, DEV, assert_chunk, assert_weights, batch, dev, paged
+
+pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
+
+
+@pytest.fixture(scope="module")
+def ra():
+    return ra_lib()
+
+
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+# ---------------------------------------------------------------------- weights
+
+# ctx, n, Hq, Hkv, d, bs, I, W: query tiles that stay in shared memory, that pass by, one token, a few
+WEIGHTS = [
+    ([300], [40], 8, 2, 128, 32, 16, 2),
+    ([700], [517], 8, 2, 128, 48, 16, 1),
+    ([257, 300], [33, 300], 6, 2, 64, 64, 16, 2),
+    ([900, 77], [1, 3], 8, 2, 64, 16, 16, 1),
+]
+
+
+def weights_inputs(case):
+    ctx, n, Hq, Hkv, d, bs, I, W = case
+    k, v, table, _ = paged(sum(ctx), ctx, Hkv, d, bs, I, W, 1)
+    q, qsl = batch(sum(ctx), n, Hq, d)
+    _, L, _ = S.chunk_attn(q, k, v, table, qsl, ctx, bs, I, W, 1)
+    return q, torch.from_numpy(L).float(), k, table, qsl
+
+
+def run_weights(ra, case, q, lse, k, table, qsl, causal=True):
+    got = ra.cp_attn_weights(*dev(q, lse, k, table, qsl, i32(*case[0])), case[6], case[7], 1, causal=causal)
+    check_status(ra)
+    return got
+
+
+@pytest.mark.parametrize("case", WEIGHTS, ids=lambda c: "%s-%s-d%d" % (c[0], c[1], c[4]))
+def test_weights_of_a_nan_lse_reach_only_the_tokens_it_sees(ra, case):
+    ctx, n, Hq, Hkv, d, bs, I, W = case
+    q, lse, k, table, qsl = weights_inputs(case)
+    for r in range(len(ctx)):
+        for i in {0, n[r] // 2, n[r] - 1}:
+            bad = lse.clone()
+            bad[int(qsl[r]) + i, 1] = float("nan")           # head 1, of K/V head 0
+            left = lse.clone()
+            left[int(qsl[r]) + i, 1] = -float("inf")
+            want = S.attn_weights(q, left, k, table, qsl, ctx, bs, I, W, 1)
+            got = run_weights(ra, case, q, bad, k, table, qsl).double().cpu().numpy()
+            x = np.arange(ctx[r] - n[r] + i + 1)             # the tokens that this query sees
+            lbi = x % (bs * W) // I
+            seen = np.zeros(want.shape, dtype=bool)
+            seen[lbi % W, table[r].numpy()[x // (bs * W)], 0, lbi // W * I + x % (bs * W) % I] = True
+            assert np.isnan(got[seen]).all()
+            assert not np.isnan(got[~seen]).any()
+            want[seen] = np.nan                              # left out of the comparison
+            assert_weights(torch.from_numpy(got), want)

@@ -270,3 +270,24 @@ def test_binding_refusals_without_a_device(ra):
         ra.cp_chunk_attn(c[0, :, 0, :2], c, c, i[None], i, i[:1], 16, 1, 1)
     with pytest.raises(ValueError):
         ra.cp_evict(c, c, torch.zeros(1, 2, 1, 16), i[None], i[:1], 4, 16, 1, 1)
+
+
+@pytest.mark.parametrize("fresh", [False, True])
+def test_evict_by_sort_is_the_same_choice(fresh):
+    ctx, bs, I, pcp, dcp, keep = [29, 5, 40], 4, 2, 1, 2, 12
+    k, v, table, _ = _cache(17, ctx, 2, 4, bs, I, pcp, dcp)
+    w = np.floor(np.random.default_rng(18).random(k.shape[:4]) * 6)
+    w[w == 5], w[w == 4], w[w == 3] = np.nan, -0.0, -1.0
+    dst = None
+    if fresh:
+        grow = lambda t: np.concatenate([np.full_like(t[:, :6], -7.0), t], axis=1)  # noqa: E731
+        k, v, w, table, dst = grow(k), grow(v), grow(w), np.where(table >= 0, table + 6, table), np.arange(6).reshape(3, 2)
+    for sink, recent in ((0, 0), (1, 3), (12, 0)):
+        want, _, k2, v2, w2 = S.evict(k, v, w, table, ctx, keep, bs, I, pcp, dcp, sink, recent, dst)
+        kept, moves = S.evict_by_sort(w, table, ctx, keep, bs, I, pcp, dcp, sink, recent, dst)
+        assert np.array_equal(kept, want)
+        for old, new in ((k, k2), (v, v2), (w, w2)):
+            got = old.copy()
+            for _, g, src, to in moves:
+                got[to[0], to[1], g, to[2]] = old[src[0], src[1], g, src[2]]
+            assert np.array_equal(got, new, equal_nan=True)
