@@ -238,7 +238,8 @@ struct __align__(1024) WeightSmem {
   static constexpr int kLseStages = kLseStagesOf<D>;
   uint64_t l_full[kLseStages], l_empty[kLseStages], seg_full[kSegs], seg_empty[kSegs];
   uint64_t s_full[2][2], s_empty[2][2], drain;
-  __align__(16) float neg_lse[kLseStages][BM];   // -lse * log2 e; -inf: the row adds nothing
+  __align__(16) float neg_lse[kLseStages][BM];   // -lse * log2 e; -inf: the row adds nothing (also where there is none)
+  int all_count[kLseStages];                     // all 128 rows add
   Item item[kSegs];
   uint32_t tmem_base;
   int abort_flag;
@@ -267,21 +268,24 @@ __device__ __forceinline__ int columns(const WeightArgs& a, const Item& s, int t
   return min(s.n - t * a.tpt, a.tpt) * a.G;
 }
 
-// Sum of 2^(x * scale - lse) over N columns; MASK: over those in [lo, hi) alone.  Columns are left out after their
-// exponent is formed, so that a NaN in the score or the LSE of a row that does not see the token stays outside.
+// Sum of 2^(x * scale - lse) over N columns; MASK: over those from lo on that count (neg_lse above -inf) alone.
+// Columns are left out after their exponent is formed, so that what a row that does not count, or does not see the
+// token, holds (NaN in its score or its LSE) stays outside.
 template <bool MASK, int N>
-__device__ __forceinline__ float chunk_sum(const uint32_t (&x)[N], uint64_t sc2, const float* neg_lse, int lo, int hi) {
+__device__ __forceinline__ float chunk_sum(const uint32_t (&x)[N], uint64_t sc2, const float* neg_lse, int lo) {
   uint64_t acc[4];
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
     const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(neg_lse + i);
-    float e[4];
+    float e[4], l[4];
     f2unpack(ffma2(f2pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2, nl.x), e[0], e[1]);
     f2unpack(ffma2(f2pack(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), sc2, nl.y), e[2], e[3]);
     if (MASK) {
+      f2unpack(nl.x, l[0], l[1]);
+      f2unpack(nl.y, l[2], l[3]);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (i + j < lo || i + j >= hi) e[j] = -CUDART_INF_F;
+        if (i + j < lo || l[j] == -CUDART_INF_F) e[j] = -CUDART_INF_F;
     }
     const uint64_t u = f2pack(ex2(e[0]), ex2(e[1])), v = f2pack(ex2(e[2]), ex2(e[3]));
     const int k = (i >> 2) & 1;
@@ -542,10 +546,13 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           const float x = i < cols ? a.lse[static_cast<int64_t>(s.q0 + t * a.tpt + tok) * a.Hq + s.g * a.G + head] : -CUDART_INF_F;
           v[j] = x == -CUDART_INF_F ? x : -x * kLog2e;
         }
+        const bool all_count = __all_sync(0xffffffffu, v[0] != -CUDART_INF_F && v[1] != -CUDART_INF_F &&
+                                                           v[2] != -CUDART_INF_F && v[3] != -CUDART_INF_F);
         const int b = n % kLseStages;
         if (!(ok = warp_wait(smem_u32(&sm.l_empty[b]), ((n / kLseStages) & 1) ^ 1, abort_flag, lim, 640))) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j) sm.neg_lse[b][32 * j + lane] = v[j];
+        if (lane == 0) sm.all_count[b] = all_count;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.l_full[b]));
       }
@@ -581,9 +588,10 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       ++cnt;
       tc_fence_after();
       const int hi = columns(a, s, t), lo = min(BN, max(0, first - t * a.tpt) * a.G);
-      const float* nlse = sm.neg_lse[(s.nqt ? n + t : n) % kLseStages];
+      const int lb = (s.nqt ? n + t : n) % kLseStages;
+      const float* nlse = sm.neg_lse[lb];
       const uint32_t addr = t_lane + (2 * h + b) * BN;
-      if (hi == BN && !__any_sync(0xffffffffu, lo > 0)) {
+      if (sm.all_count[lb] && !__any_sync(0xffffffffu, lo > 0)) {
         // all columns count: two chunks a turn, the next one's load in flight (a rolled loop, that its code
         // stays in the instruction cache)
         uint32_t xa[32], xb[32];
@@ -592,24 +600,24 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < BN; c += 64) {
           tmem_ld32(addr + c + 32, xb);
-          sum += chunk_sum<false>(xa, sc2, nlse + c, 0, 0);
+          sum += chunk_sum<false>(xa, sc2, nlse + c, 0);
           tmem_wait_ld();
           if (c == 0) tmem_ld32(addr + 64, xa);
-          sum += chunk_sum<false>(xb, sc2, nlse + c + 32, 0, 0);
+          sum += chunk_sum<false>(xb, sc2, nlse + c + 32, 0);
           if (c == 0) tmem_wait_ld();
         }
       } else if (hi <= 16) {   // a token or a few: half a chunk
         uint32_t x[16];
         tmem_ld16(addr, x);
         tmem_wait_ld();
-        sum += chunk_sum<true>(x, sc2, nlse, lo, hi);
+        sum += chunk_sum<true>(x, sc2, nlse, lo);
       } else {
 #pragma unroll 1
         for (int c = 0; c < hi; c += 32) {
           uint32_t x[32];
           tmem_ld32(addr + c, x);
           tmem_wait_ld();
-          sum += chunk_sum<true>(x, sc2, nlse + c, lo - c, hi - c);
+          sum += chunk_sum<true>(x, sc2, nlse + c, lo - c);
         }
       }
       tc_fence_before();

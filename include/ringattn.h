@@ -622,7 +622,8 @@ ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const void* v_cac
  * ra_cp_chunk_attn.  The queries may be the last ones of a longer chunk.
  * lse         device float [T, Hq]: natural-log sum of exp(scaled scores), as
  *             ra_cp_chunk_attn or ra_cp_decode gives it; a query whose lse is
- *             -inf (it saw nothing) adds nothing.
+ *             -inf (it saw nothing) adds nothing, whatever its row of q holds;
+ *             a NaN reaches the tokens that the query sees and no others.
  * w_in        device float [W, num_blocks, Hkv, block_size], or NULL for all 0.
  * w_out       device float, same shape, out; may be w_in.  Slots that hold no
  *             token < ctx_lens[r] of a request are left as they were.

@@ -66,3 +66,18 @@ def test_weights_of_a_nan_lse_reach_only_the_tokens_it_sees(ra, case):
             assert not np.isnan(got[~seen]).any()
             want[seen] = np.nan                              # left out of the comparison
             assert_weights(torch.from_numpy(got), want)
+
+
+@pytest.mark.parametrize("case", WEIGHTS, ids=lambda c: "%s-%s-d%d" % (c[0], c[1], c[4]))
+@pytest.mark.parametrize("causal", [True, False])
+def test_weights_of_queries_marked_as_seeing_nothing(ra, case, causal):
+    """An LSE of -inf (or +inf: e^-inf) leaves a query out whatever its row holds, e.g. padding that was never written."""
+    ctx, n, Hq, Hkv, d, bs, I, W = case
+    q, lse, k, table, qsl = weights_inputs(case)
+    ends = [int(qsl[r + 1]) - 1 for r in range(len(ctx))]
+    for mark in (-float("inf"), float("inf")):
+        left, qs, ref = lse.clone(), q.clone(), lse.clone()
+        for row, junk in zip([0, q.shape[0] // 2] + ends, (float("nan"), float("inf"), float("nan"), 3e38)):
+            left[row], ref[row], qs[row] = mark, -float("inf"), junk
+        want = S.attn_weights(q, ref, k, table, qsl, ctx, bs, I, W, 1, causal=causal)
+        assert_weights(run_weights(ra, case, qs, left, k, table, qsl, causal), want)
