@@ -265,6 +265,7 @@ extern "C" ra_status ra_rope_apply(const void* src, int64_t src_rows, int64_t sr
   RA_REQUIRE(dt == RA_BF16 || dt == RA_F32, "dtype must be RA_BF16 or RA_F32");
   RA_REQUIRE(style == RA_ROPE_HALF || style == RA_ROPE_INTERLEAVED, "unknown rope style");
   RA_REQUIRE(H >= 1 && d >= 1 && d <= 1024, "H >= 1 and 1 <= d <= 1024 required");
+  RA_REQUIRE(static_cast<int64_t>(H) * d < (int64_t(1) << 31), "H*d must be below 2^31");   // threads of a row: 32 bits
   RA_REQUIRE(rot >= 2 && rot % 2 == 0 && rot <= d && rot <= 2 * kMaxPairs, "rot must be even, in [2, min(d, %d)]",
              2 * kMaxPairs);
   RA_REQUIRE(rows >= 0 && src_rows >= 0, "negative size");

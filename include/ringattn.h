@@ -154,6 +154,7 @@ ra_status ra_rope_gather(const void* src, int64_t src_rows, int32_t H, int32_t d
  *            idx is NULL (in place); otherwise the two extents must not overlap.
  * rows       output rows; src_rows: rows of src (== rows without idx).
  * d, rot     head dim 1 .. 1024 and the rotated part, even, 2 .. min(d, 256).
+ *            H*d < 2^31.
  * style      RA_ROPE_HALF: pair i is (i, i + rot/2); RA_ROPE_INTERLEAVED:
  *            (2i, 2i+1).
  * positions  device int32 [rows]: position of each OUTPUT row, in [0, 2^24)

@@ -291,3 +291,12 @@ def test_evict_by_sort_is_the_same_choice(fresh):
             for _, g, src, to in moves:
                 got[to[0], to[1], g, to[2]] = old[src[0], src[1], g, src[2]]
             assert np.array_equal(got, new, equal_nan=True)
+
+
+def test_rope_apply_rows_past_32_bits_are_refused(ra):
+    """A row of 2^31 components or more: the threads of a row would not fit in 32 bits."""
+    f = (ctypes.c_double * 128)(*([1.0] * 128))
+    for H, d, rows in [(1 << 25, 64, 1), (1 << 29, 128, 1), (1 << 30, 64, 3), ((1 << 31) - 1, 2, 1)]:
+        st = ra.lib().ra_rope_apply(P, rows, 0, 0, ctypes.c_void_p(1 << 44), H * d, d, rows, H, d, 2, 1, 0, None, P, f, 1.0, 0,
+                                    None)
+        assert st == INV and "H*d" in ra.last_error(), (H, d)
