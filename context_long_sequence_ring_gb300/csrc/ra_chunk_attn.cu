@@ -44,27 +44,25 @@
 // Tensor memory: two (D = 128) or three (D = 64) score tiles S_b = columns [128b, +128) with P (bf16)
 // over the first 64 of each, then O_0 and O_1, D columns each.
 #include <algorithm>
-#include <cmath>
 
+#include "ra_chunk_plan.cuh"
 #include "ra_key_units.cuh"
 
 RA_DEFINE_ERROR_FETCH(fetch_error_chunk_attn)
 
 namespace {
 
-constexpr int kCtas = 152;         // parts of the work, one CTA per SM of a GB300
 constexpr int kChunkThreads = 384;
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRowBlocks = 8;
 constexpr int kFewRows = 32;       // rows of a tile that get a block each
-constexpr int kPairCost = 10;      // cost of a key in a pair tile
 
 struct ChunkArgs : KeyUnits {
   const int32_t *qsl, *ctx;
   int64_t T;
   int R, Hq, G, causal, out_bf16;
   int tpt;                        // tokens of a row tile
-  int f_split, over_pair, over_split, cost_shift;   // costs, see Req
+  Rates rates;
   FastDiv by_G, by_tpi;                // by the tokens of a pair of row tiles
   float scale_log2;
   void* o;                        // [T, Hq, D]
@@ -77,17 +75,10 @@ struct ChunkArgs : KeyUnits {
 };
 
 // ------------------------------------------------------------------ work
-// A request as the work division sees it.  The cost of an item is in keys times what a key costs.  Measured over
-// the CTAs of one call at D = 128: a pair tile 1.59 us (tensor core), a split tile 1.24 (HBM), and prologue and
-// epilogue of an item as many keys as `over_pair` and `over_split`.  At D = 64 the numbers are those with the least
-// time over batches of prompts, single tokens and both (split tiles at 6 tenths of a pair tile: 24 requests of both
-// kinds 102 us, at 5 or 7 tenths 105).  Costs are 32-bit numbers, in units of 2^cost_shift that the host chooses from the
-// sizes so that their sum fits.
-struct Req {
-  int r, q0, n, L, items;         // request, first query row, queries, context, row tiles (pairs of them) per head
+// A request as the work division sees it.
+struct Req : Items {
+  int r, q0, n, L;                // request, first query row, queries, context
   long long pos0;                 // position of query 0
-  uint32_t base, slope, over;     // cost of item k: base + slope * (k + 1), of which `over` for its start and end
-  bool pair;
 };
 
 __device__ __forceinline__ Req make_req(const ChunkArgs& a, int r, const Lens& x) {
@@ -96,14 +87,7 @@ __device__ __forceinline__ Req make_req(const ChunkArgs& a, int r, const Lens& x
   query_range(x, a.T, q.q0, q.n, 510);
   q.L = paged_len(a.c, x.ctx, 511);
   q.pos0 = static_cast<long long>(x.ctx) - q.n;
-  q.pair = q.n > a.tpt;
-  q.items = q.pair ? a.by_tpi.div(q.n + 2 * a.tpt - 1) : (q.n > 0);
-  const long long before = q.pos0 < 0 ? 0 : (q.pos0 < q.L ? q.pos0 : q.L);
-  const long long keys = (q.pair ? a.over_pair : a.over_split) + (a.causal ? before : q.L);
-  const int f = q.pair ? kPairCost : a.f_split;
-  q.base = static_cast<uint32_t>(keys * f >> a.cost_shift) + 1;
-  q.over = static_cast<uint32_t>((q.pair ? a.over_pair : a.over_split) * f) >> a.cost_shift;
-  q.slope = a.causal ? static_cast<uint32_t>((q.pair ? 2 : 1) * a.tpt * f) >> a.cost_shift : 0;
+  q.set(a.rates, q.n, q.n > a.tpt ? a.by_tpi.div(q.n + 2 * a.tpt - 1) : (q.n > 0), a.tpt, q.pos0, q.L, a.causal);
   return q;
 }
 
@@ -121,43 +105,6 @@ __device__ __forceinline__ int tiles_of(const ChunkArgs& a, const Req& q, int k)
   const int last = min(q.n, (k + 1) * tpi) - 1;
   return (units_below(a, limit_of(a, q, last)) + (1 << a.lupt) - 1) >> a.lupt;
 }
-
-// Tiles [t0, t1) of an item of nt tiles and cost [at, at + cost) that part [lo, hi) takes.  The first `over` of the
-// cost stand for the start and end of a segment: a part pays for each item that begins in it (and all parts alike for
-// the one they begin inside of).  Spread over the item instead, a batch of short items (12 requests, heads of
-// 64) took 46.3 us instead of 43.6.  Fractions are taken in fp32: a boundary gives the same tile to both of its
-// sides, whatever its rounding.
-__device__ __forceinline__ int cut_at(uint32_t off, uint32_t over, uint32_t cost, int nt) {
-  if (off <= over) return 0;
-  return min(nt, static_cast<int>(__fdividef(static_cast<float>(off - over), static_cast<float>(cost - over)) * static_cast<float>(nt)));
-}
-__device__ __forceinline__ void cut(uint32_t lo, uint32_t hi, uint32_t at, uint32_t over, uint32_t cost, int nt, int& t0,
-                                    int& t1) {
-  t0 = lo <= at ? 0 : cut_at(lo - at, over, cost, nt);
-  t1 = hi >= at + cost ? nt : cut_at(hi - at, over, cost, nt);
-}
-
-// Part c of the work is [lo(c), lo(c + 1)), empty from the first c with lo(c) = total on.  Where an equal
-// cut leaves few items to a part, and cutting each item into pieces of its own costs less than the second item
-// that a part would take up, lengths are counted in such pieces (piece > 0: the cost of one; share is 1 then).
-struct Plan {
-  uint32_t total, share;
-  float piece;
-  __device__ uint32_t lo(int c) const { return min(total, share * c); }
-  __device__ uint32_t cost(const Req& q, int k) const {
-    const uint32_t c = q.base + q.slope * (k + 1);
-    return piece > 0.f ? static_cast<uint32_t>(__fdividef(static_cast<float>(c), piece)) + 1 : c;
-  }
-  __device__ uint32_t over(const Req& q) const { return piece > 0.f ? 0 : q.over; }
-  // cost of items 0 .. k-1 of a head
-  __device__ uint32_t prefix(const Req& q, int k) const {
-    if (piece <= 0.f) return k * q.base + q.slope * (static_cast<uint32_t>(k) * (k + 1) / 2);
-    uint32_t sum = 0;
-#pragma unroll 1
-    for (int i = 0; i < k; ++i) sum += cost(q, i);
-    return sum;
-  }
-};
 
 // f(request) for all requests in order, each lane those at lane, lane + 32, ...; four loads in flight where there
 // are many (f may stop the walk: it returns true in all lanes or in none).
@@ -183,10 +130,10 @@ __device__ __forceinline__ bool for_requests(const ChunkArgs& a, const F& f) {
 __device__ __forceinline__ bool make_plan(const ChunkArgs& a, int part, Plan& plan, Req& q, uint32_t& pre) {
   const int lane = threadIdx.x & 31;
   const bool few = a.R <= 32;            // then each lane keeps its request
-  uint32_t total = 0, items = 0;
-  plan.piece = 0.f;
+  uint64_t sum = 0;
+  uint32_t items = 0;
   auto add = [&](const Req& x) {
-    total += a.c.Hkv * plan.prefix(x, x.items);
+    sum += a.c.Hkv * x.upto(x.items);
     items += a.c.Hkv * x.items;
     return false;
   };
@@ -196,25 +143,29 @@ __device__ __forceinline__ bool make_plan(const ChunkArgs& a, int part, Plan& pl
   } else {
     for_requests(a, add);
   }
-  total = __reduce_add_sync(0xffffffffu, total);
+  constexpr uint32_t kPart = (1u << 26) - 1;   // 64 bits over the warp in three sums that fit in 32
+  const uint32_t s0 = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(sum) & kPart);
+  const uint32_t s1 = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(sum >> 26) & kPart);
+  const uint32_t s2 = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(sum >> 52));
   items = __reduce_add_sync(0xffffffffu, items);
-  plan.total = total;
-  plan.share = max((256u * a.f_split) >> a.cost_shift, (total + kCtas - 1) / kCtas);
-  if (items <= kCtas / 2) {
-    // pieces of at most total / (kCtas - items): at most kCtas of them, since an item has one incomplete piece
-    const float p = max(static_cast<float>(plan.share), __fdividef(1.001f * static_cast<float>(total), static_cast<float>(kCtas - items)));
-    if (p < static_cast<float>(plan.share + ((a.f_split * a.over_split) >> a.cost_shift))) {
-      plan.piece = p;
-      total = 0;
-      if (few) add(q); else for_requests(a, add);
-      total = __reduce_add_sync(0xffffffffu, total);
-      if (total <= kCtas) {
-        plan.total = total;
-        plan.share = 1;
-      } else {
-        plan.piece = 0.f;
-      }
-    }
+  sum = (static_cast<uint64_t>(s2) << 52) + (static_cast<uint64_t>(s1) << 26) + s0;
+  plan.scale(sum);
+  uint32_t total = 0;
+  auto add_scaled = [&](const Req& x) {
+    total += a.c.Hkv * plan.prefix(x, x.items);
+    return false;
+  };
+  auto sum_scaled = [&] {
+    total = 0;
+    if (few) add_scaled(q); else for_requests(a, add_scaled);
+    total = __reduce_add_sync(0xffffffffu, total);
+  };
+  if (plan.shift == 0) total = static_cast<uint32_t>(sum) + items;   // the same sum
+  else sum_scaled();
+  plan.divide(total, a.rates);
+  if (plan.try_pieces(items, a.rates)) {
+    sum_scaled();
+    plan.use_pieces(total);
   }
   const uint32_t lo = plan.lo(part);
   if (lo >= plan.total) return false;
@@ -1276,14 +1227,7 @@ extern "C" ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const 
   a.tpt = BM / a.G;
   a.by_G = fast_div(a.G);
   a.by_tpi = fast_div(2 * a.tpt);
-  a.f_split = d == 128 ? 8 : 6;
-  a.over_pair = d == 128 ? 470 : 460;
-  a.over_split = d == 128 ? 255 : 270;
-  // the largest sum of costs these sizes allow stays below 2^31
-  const double most = static_cast<double>(Hkv) * (static_cast<double>(T) / a.tpt + R) *
-                      (kPairCost * (static_cast<double>(max_vblocks) * a.c.V + T + 512) + 1);
-  a.cost_shift = 0;
-  while (std::ldexp(most, -a.cost_shift) > 1.0e9) ++a.cost_shift;
+  a.rates = rates_of(d);
   a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(d))) * 1.4426950408889634f;
   a.o = o; a.lse = lse;
   a.o_part = static_cast<float*>(workspace);

@@ -81,3 +81,42 @@ def test_weights_of_queries_marked_as_seeing_nothing(ra, case, causal):
             left[row], ref[row], qs[row] = mark, -float("inf"), junk
         want = S.attn_weights(q, ref, k, table, qsl, ctx, bs, I, W, 1, causal=causal)
         assert_weights(run_weights(ra, case, qs, left, k, table, qsl, causal), want)
+
+
+# ---------------------------------------------------------------------- chunk attention
+
+def test_chunk_attn_work_in_coarser_units(ra):
+    """A long piece with two tokens to a row tile among single tokens: the sum of its costs is past 2^30, so parts are
+    cut, and joined, in coarser units.  Sampled rows against 64 bits; a wide block table changes nothing."""
+    Hq, Hkv, d, bs, n = 512, 8, 64, 64, 20000
+    g = torch.Generator(device=DEV).manual_seed(41)
+    ctx = [3000, 20000] + [700 + 97 * i for i in range(30)]
+    new = [1, n] + [1] * 30
+    nvb = [-(-x // bs) for x in ctx]
+    NB = sum(nvb)
+    k, v = (torch.randn((1, NB, Hkv, bs, d), generator=g, device=DEV).to(BF) for _ in range(2))
+    table = torch.full((32, 1 << 14), -1, dtype=torch.int32)
+    ids = torch.randperm(NB, generator=torch.Generator().manual_seed(42)).to(torch.int32)
+    at = 0
+    for r, x in enumerate(nvb):
+        table[r, :x] = ids[at:at + x]
+        at += x
+    qsl = i32(*np.concatenate([[0], np.cumsum(new)]).tolist())
+    q = torch.randn((int(qsl[-1]), Hq, d), generator=g, device=DEV).to(BF)
+    args = [*dev(table[:, :max(nvb)].contiguous(), qsl, i32(*ctx)), bs, 1, 1]
+    o, lse = ra.cp_chunk_attn(q, k, v, *args)
+    check_status(ra)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    rng = np.random.default_rng(43)
+    for r in range(32):
+        kt, vt = (t[0, table[r, :nvb[r]].long().to(DEV)].permute(1, 0, 2, 3).reshape(Hkv, -1, d)[:, :ctx[r]].double()
+                  for t in (k, v))
+        for i in (rng.integers(0, n, 40).tolist() + [0, n - 1] if new[r] > 1 else [0]):
+            row, see = int(qsl[r]) + i, ctx[r] - new[r] + i + 1
+            s = torch.matmul(q[row].double().view(Hkv, -1, d), kt[:, :see].transpose(1, 2)) * d ** -0.5
+            p = torch.softmax(s, -1)
+            ref = [torch.matmul(p, vt[:, :see]), torch.logsumexp(s, -1), torch.matmul(p, vt[:, :see].abs())]
+            assert_chunk(o[row], lse[row], [t.reshape(Hq, *t.shape[2:]).cpu().numpy() for t in ref])
+    o2, lse2 = ra.cp_chunk_attn(q, k, v, table.to(DEV), *args[1:])
+    check_status(ra)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
