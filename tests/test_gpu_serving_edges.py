@@ -7,7 +7,7 @@ import torch
 
 from oracle import serving as S
 from tests._gpu import ra_lib, check_status
-from tests.test_gpu_serving import BF, DEV, assert_chunk, assert_weights, batch, dev, paged
+from tests.test_gpu_serving import BF, DEV, _same, assert_chunk, assert_weights, batch, dev, paged
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
 
@@ -120,3 +120,100 @@ def test_chunk_attn_work_in_coarser_units(ra):
     o2, lse2 = ra.cp_chunk_attn(q, k, v, table.to(DEV), *args[1:])
     check_status(ra)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+# ---------------------------------------------------------------------- eviction
+
+# ctx, width of the table in tokens (0: as needed), keep, sink, recent, Hkv, d, bs, I, pcp, dcp: clusters of 8, 4, 2 and 1,
+# keys in shared memory whole, cut off (24576 to a CTA), or cut off by the table alone
+LONG = {
+    "8, past the keys": ([200001, 70], 0, 5000, 4, 1000, 1, 8, 64, 16, 1, 1),
+    "4": ([900 + 37 * r for r in range(5)], 0, 300, 2, 50, 8, 8, 32, 4, 1, 2),
+    "4, past the keys": ([100003, 5, 300, 99, 1001], 0, 777, 0, 0, 8, 8, 128, 16, 2, 1),
+    "2": ([600 + 41 * r for r in range(10)], 0, 256, 4, 100, 8, 8, 16, 2, 1, 1),
+    "1": ([31 * r for r in range(20)], 0, 128, 1, 7, 8, 8, 16, 16, 1, 1),
+    "1, past the keys": ([30001] + [47 * r for r in range(1, 20)], 0, 600, 3, 64, 8, 8, 64, 1, 1, 1),
+    "1, a wide table": ([800 - 31 * r for r in range(20)], 50000, 100, 4, 16, 8, 8, 64, 16, 1, 1),
+}
+
+
+@pytest.mark.parametrize("name", LONG)
+@pytest.mark.parametrize("fresh", [False, True])
+@pytest.mark.parametrize("weights", ["spread", "ties", "odd"])
+def test_evict_with_clusters_of_every_size(ra, name, fresh, weights):
+    ctx, wide, keep, sink, recent, Hkv, d, bs, I, pcp, dcp = LONG[name]
+    R, V = len(ctx), bs * pcp * dcp
+    more = -(-min(keep, max(ctx)) // V)
+    k, v, table, spare = paged(keep, ctx, Hkv, d, bs, I, pcp, dcp, spare=R * more + 1)
+    if wide:
+        table = torch.nn.functional.pad(table, (0, wide // V - table.shape[1]), value=-1)
+    g = torch.Generator().manual_seed(keep)
+    w = torch.rand(k.shape[:4], generator=g) * 4
+    if weights == "ties":
+        w = torch.floor(w * 2) / 2
+    if weights == "odd":
+        r = torch.rand(w.shape, generator=g)
+        for hi, val in [(0.999, float("nan")), (0.95, -0.0), (0.9, 0.0), (0.6, -1.0), (0.05, float("inf")), (0.04, 1e-42),
+                        (0.02, -float("inf"))]:
+            w[r < hi] = val
+    dst = spare[:R * more].view(R, more) if fresh else None
+    ref, moves = S.evict_by_sort(w.numpy(), table, ctx, keep, bs, I, pcp, dcp, sink, recent, dst)
+    kd, vd, wd = dev(k, v, w)
+    kept, new = ra.cp_evict(kd, vd, wd, *dev(table, i32(*ctx)), keep, I, pcp, dcp, n_sink=sink, n_recent=recent,
+                            dst_block_table=None if dst is None else dst.to(DEV))
+    check_status(ra)
+    assert np.array_equal(kept.cpu().numpy(), ref) and new.tolist() == [min(x, keep) for x in ctx]
+    for got, t, bits in ((kd, k, torch.int16), (vd, v, torch.int16), (wd, w, torch.int32)):
+        old = t.view(bits)
+        want = old.clone()
+        for _, h, src, to in moves:
+            want[to[0], to[1], h, to[2]] = old[src[0], src[1], h, src[2]]
+        assert _same(got, want)
+
+
+# ---------------------------------------------------------------------- ranges that are left out
+
+def test_requests_with_bad_query_ranges_are_left_out_and_the_others_computed(ra):
+    ctx, Hq, Hkv, d, bs = [40, 90, 33], 4, 2, 64, 16
+    k, v, table, _ = paged(51, ctx, Hkv, d, bs, 16, 1, 1)
+    q, _ = batch(51, [9], Hq, d)
+    w_in = torch.rand(k.shape[:4])
+    for qsl, good in [([-1, 2, 5, 9], [1, 2]), ([0, 2, 5, 10], [0, 1]), ([4, 6, 0, 4], [0, 2]), ([7, 3, 9, 2 ** 31 - 1], [1]),
+                      ([-2 ** 31, -1, 3, 5], [2])]:
+        args = dev(k, v, table, i32(*qsl), i32(*ctx))
+        o = torch.full(q.shape, 7.0, dtype=BF, device=DEV)
+        lse = torch.full(q.shape[:2], 7.0, device=DEV)
+        ra.cp_chunk_attn(q.to(DEV), *args, 16, 1, 1, o=o, lse=lse)
+        assert ra.device_status() == ra.RA_ERR_DEVICE_BOUNDS, qsl
+        w = ra.cp_attn_weights(q.to(DEV), lse, args[0], *args[2:], 16, 1, 1, w_in=w_in.to(DEV))
+        assert ra.device_status() == ra.RA_ERR_DEVICE_BOUNDS, qsl
+        rest = np.ones(9, dtype=bool)
+        for r in range(3):
+            if r in good:
+                a, b = qsl[r], qsl[r + 1]
+                one = (q[a:b], k, v, table[r:r + 1], [0, b - a], ctx[r:r + 1], bs, 16, 1, 1)
+                assert_chunk(o[a:b], lse[a:b], S.chunk_attn(*one))
+                rest[a:b] = False
+                want = S.attn_weights(one[0], lse[a:b].cpu(), k, *one[3:], w_in=w_in.numpy())
+            else:      # its tokens keep what they had
+                want = S.attn_weights(q[:0], lse[:0].cpu(), k, table[r:r + 1], [0, 0], ctx[r:r + 1], bs, 16, 1, 1, w_in=w_in.numpy())
+            assert_weights(w, want)
+        assert (o[torch.from_numpy(rest)] == 7).all()
+        assert (lse[torch.from_numpy(rest)] == 7).all()
+
+
+def test_a_context_past_the_table_is_cut_to_it(ra):
+    """All tokens of the table are seen (the queries' positions are past them); the other requests are untouched."""
+    Hq, Hkv, d, bs = 4, 2, 64, 16
+    ctx, n = [40, 96, 33], [2, 3, 4]
+    k, v, table, _ = paged(52, ctx, Hkv, d, bs, 16, 1, 1)
+    table = table[:, :6].contiguous()                     # 96 tokens
+    q, qsl = batch(52, n, Hq, d)
+    for long in (97 + 3, 5000, 2 ** 31 - 1):
+        args = dev(k, v, table, qsl, i32(40, long, 33))
+        o, lse = ra.cp_chunk_attn(q.to(DEV), *args, 16, 1, 1)
+        assert ra.device_status() == ra.RA_ERR_DEVICE_BOUNDS
+        rows = np.r_[0:2, 5:9]
+        assert_chunk(o[rows], lse[rows], S.chunk_attn(q, k, v, table, qsl, ctx, bs, 16, 1, 1), rows)
+        ref = S.chunk_attn(q[2:5], k, v, table[1:2], [0, 3], [96], bs, 16, 1, 1, causal=False)
+        assert_chunk(o[2:5], lse[2:5], ref)
