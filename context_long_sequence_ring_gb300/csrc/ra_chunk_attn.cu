@@ -17,7 +17,8 @@
 //          HBM bandwidth about 1.45 us, one slot's chain of score product, softmax
 //          and P.V about 1.3 us, two of them half of that).  Its tiles are read by
 //          one CTA once and leave L2 first (drafts 286 -> 279 us, a token at 131072
-//          92 -> 87 us).  At D = 64 the fixed work of a tile would take longer than
+//          92 -> 87 us; where requests share prefix blocks it makes no difference: 48
+//          on one prefix of 16384, 384 us with it and 385 without).  At D = 64 the fixed work of a tile would take longer than
 //          HBM: see kScores and kJoint.
 //
 // Keys.  The cache is read where it lies, in units of 16 or 32 slots
@@ -27,9 +28,9 @@
 // TMA fills with zeros.
 //
 // Work.  The keys that all row tiles of all heads and requests meet are laid
-// out on one axis of cost, cut into equal parts, one per CTA (152): long and
-// short contexts, prompts and single tokens balance without any plan from the
-// host.  A part starts or ends inside at most two row tiles; their partial
+// out on one axis of cost, cut into equal parts, one per CTA (152;
+// ra_chunk_plan.cuh): long and short contexts, prompts and single tokens
+// balance without any plan from the host.  A part starts or ends inside at most two row tiles; their partial
 // (m, l, O) go to the workspace (at most two per CTA) and a second small kernel
 // joins them.
 //
@@ -278,6 +279,9 @@ struct SegIter {
 // chunk's sum of p exceeds 2^8; a tile in which it does and a masked one take two
 // passes (maximum, then exps).  The two passes are rolled loops: they run once or
 // twice per row tile, where fetching unrolled code took longer than running it.
+// P is rounded to bf16, V's type: both operands of a product on the tensor cores have one, and fp32 or split
+// operands would take two products and more for a gain below the rounding of a bf16 output.  l sums p as it is
+// before the rounding, so that the LSE is fp32's.
 // lm: visible columns of each 16, 8 bits each.  Rows that are not in use may
 // hold NaN scores: they are left out of the votes.
 __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool masked, bool row_ok, uint64_t lm,

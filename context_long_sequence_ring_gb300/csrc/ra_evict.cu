@@ -15,7 +15,13 @@
 // weights once, 4 bytes per token, and is bound by latency: 4 digits of 2 us, reading
 // 2.5, counting and numbering 4.  16 prompts of 8192-16384 cut to 2048 (8 heads of
 // 128): 61 us, of which the move of 268 MB takes 41 (6.5 TB/s); moved with plain
-// loads and stores 63.  2 requests of 900-1301 cut to 512: 13 us.
+// loads and stores 63.  16 of 16384: 65 us, in place 66.  2 requests of 900-1301 cut to 512: 13 us.
+//
+// Where the table has room for more tokens than a cluster's shared memory has keys
+// (24576 to a CTA), the keys past that are read again for each digit and for the
+// numbering, and single weights instead of four are read: 8 requests of 131072 cut to 2048
+// take 217 us on a floor of 25, 32 of 32768 292 on 85; 16 of 16384 with a table for
+// 131072 84 us instead of 65.
 #include <algorithm>
 
 #include "ra_paged.cuh"

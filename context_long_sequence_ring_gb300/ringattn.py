@@ -604,7 +604,8 @@ def cp_chunk_attn(q, k_cache, v_cache, block_table, query_start_loc, ctx_lens, i
                   o=None, lse=None):
     """Attention of a packed batch of new tokens, q [T, Hq, d] (request r has rows query_start_loc[r] ..
     query_start_loc[r+1], the last ones of its ctx_lens[r] cached tokens), over the sharded paged cache
-    -> (O [T, Hq, d], LSE [T, Hq]).  Rows of no request are left as they were (undefined in a new O)."""
+    -> (O [T, Hq, d], LSE [T, Hq]).  Rows of no request are left as they were (undefined in a new O).  The
+    probabilities are rounded to bf16 for the product with V, for out_dtype float32 too."""
     dev = _here(q, k_cache, v_cache, block_table, query_start_loc, ctx_lens, workspace, o, lse)
     T, Hq, d, NB, Hkv, bs, R, max_vb = _need_paged(q, k_cache, block_table, query_start_loc, ctx_lens, pcp, dcp)
     if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
@@ -631,7 +632,8 @@ def cp_attn_weights(q, lse, k_cache, block_table, query_start_loc, ctx_lens, int
                     w_in=None, w_out=None, causal: bool = True, scale: Optional[float] = None):
     """Accumulated attention weight of every cached token, per K/V head -> w_out fp32 [W, NB, Hkv, bs]: w_in
     (None: 0; the chunk's own tokens start from 0) plus the softmax weights of the queries q [T, Hq, d] with
-    their lse [T, Hq].  w_out may be w_in; slots of no token are left as they were (0 in a new w_out)."""
+    their lse [T, Hq] (a query of lse -inf adds nothing).  w_out may be w_in; slots of no token are left as they
+    were (0 in a new w_out).  A block that several requests share gets the value of one of them."""
     dev = _here(q, lse, k_cache, block_table, query_start_loc, ctx_lens, w_in, w_out)
     T, Hq, d, NB, Hkv, bs, R, max_vb = _need_paged(q, k_cache, block_table, query_start_loc, ctx_lens, pcp, dcp)
     _of(torch.float32, lse, w_in, w_out)
@@ -653,7 +655,8 @@ def cp_evict(k_cache, v_cache, weights, block_table, ctx_lens, keep: int, interl
              n_sink: int = 0, n_recent: int = 0, dst_block_table=None, kept=None, new_lens=None):
     """Cut every request's cached context to ``keep`` tokens per K/V head (the first n_sink, the last n_recent
     and the heaviest of the others by ``weights`` fp32 [W, NB, Hkv, bs]) and pack them in order, with their
-    weights, into the blocks of dst_block_table [R, .] (None: the request's own blocks).  Returns (kept int32
+    weights, into the blocks of dst_block_table [R, .] (None: the request's own blocks; else none of the blocks
+    that hold a context), no block being two requests'.  Returns (kept int32
     [R, Hkv, keep]: former positions, -1 past the end; new_lens int32 [R])."""
     dev = _here(k_cache, v_cache, weights, block_table, ctx_lens, dst_block_table, kept, new_lens)
     _of(torch.float32, weights)

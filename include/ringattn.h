@@ -187,7 +187,10 @@ ra_status ra_rope_apply(const void* src, int64_t src_rows, int64_t src_row_strid
  *                   theta_0 and divides the last theta by factor
  *   RA_ROPE_YARN    (1-g) theta_i / factor + g theta_i, g the ramp from 0 at 1
  *                   turn to 1 at 32 turns of theta_i over trained_len, linear in the
- *                   number of turns trained_len * theta_i / 2 pi
+ *                   number of turns trained_len * theta_i / 2 pi, as the method is
+ *                   published.  Models are also run with a ramp that is linear in the
+ *                   index i between the i of 32 and of 1 turns, which is another
+ *                   table: form that one and hand it to ra_rope_apply
  * mscale (may be NULL): 1, or 0.1 ln(factor) + 1 for RA_ROPE_YARN (the
  * attention temperature, applied to Q and K each).
  * Needs base > 1, factor >= 1, trained_len >= 1 (YARN), all finite.
@@ -583,7 +586,9 @@ ra_status ra_cp_head_split(const float* o_local, const float* lse_local, int32_t
  *             query_start_loc[0], from query_start_loc[R] on) are left as
  *             they were.  A query that sees nothing (ctx_lens[r] <
  *             n_r leaves the first ones at negative positions; ctx_lens[r] = 0)
- *             gets O 0, LSE -inf.
+ *             gets O 0, LSE -inf.  Scores, sums and partials are fp32; the
+ *             probabilities are rounded to bf16 for their product with V (at
+ *             most 2^-8 of each term), in an RA_F32 o too.
  * Slots past ctx_lens[r] are never used, whatever they hold (NaN too); V of a
  * token below ctx_lens[r] must be finite where a query of the same request
  * does not see it.
@@ -628,8 +633,10 @@ ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const void* v_cac
  * w_in        device float [W, num_blocks, Hkv, block_size], or NULL for all 0.
  * w_out       device float, same shape, out; may be w_in.  Slots that hold no
  *             token < ctx_lens[r] of a request are left as they were.
- * A block that holds tokens of several requests (below their ctx_lens) gets
- * the value of one of them, which one is not defined.
+ * A block that holds tokens of several requests (below their ctx_lens, e.g. a
+ * shared prefix) gets the value of one of them, which one is not defined; with
+ * w_out = w_in that value may have the other requests' weights in it as well.
+ * For the sum over all of them make one call per request.
  * Sums are fp32 in an order fixed by the sizes.  Same limits and device bounds errors
  * as ra_cp_chunk_attn (tokens of a bad block are left out).
  * ---------------------------------------------------------------------- */
