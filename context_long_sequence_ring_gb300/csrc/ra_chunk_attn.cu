@@ -18,8 +18,9 @@
 //          and P.V about 1.3 us, two of them half of that).  Its tiles are read by
 //          one CTA once and leave L2 first (drafts 286 -> 279 us, a token at 131072
 //          92 -> 87 us; where requests share prefix blocks it makes no difference: 48
-//          on one prefix of 16384, 384 us with it and 385 without).  At D = 64 the fixed work of a tile would take longer than
-//          HBM: see kScores and kJoint.
+//          on one prefix of 16384, 384 us with it and 385 without).  At D = 64
+//          the fixed work of a tile would take longer than HBM: see kScores and
+//          kJoint.
 //
 // Keys.  The cache is read where it lies, in units of 16 or 32 slots
 // (ra_key_units.cuh).  V rows of slots past the context
@@ -30,9 +31,9 @@
 // Work.  The keys that all row tiles of all heads and requests meet are laid
 // out on one axis of cost, cut into equal parts, one per CTA (152;
 // ra_chunk_plan.cuh): long and short contexts, prompts and single tokens
-// balance without any plan from the host.  A part starts or ends inside at most two row tiles; their partial
-// (m, l, O) go to the workspace (at most two per CTA) and a second small kernel
-// joins them.
+// balance without any plan from the host.  A part starts or ends inside at most
+// two row tiles; their partial (m, l, O) go to the workspace (at most two per
+// CTA) and a second small kernel joins them.
 //
 // Measured (32/8 heads of 128, 8 devices, captured calls): 48 requests with 1-6 drafted
 // tokens over 2048-16384: 275-279 us, 6.6 TB/s, 97 % of the copy rate; one token over

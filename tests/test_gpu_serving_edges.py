@@ -83,6 +83,36 @@ def test_weights_of_queries_marked_as_seeing_nothing(ra, case, causal):
         assert_weights(run_weights(ra, case, qs, left, k, table, qsl, causal), want)
 
 
+def test_weights_replayed_with_other_lengths(ra):
+    """A captured call replayed with other lengths: query tiles that stay, that pass by, single tokens, none."""
+    Hq, Hkv, d, bs, I, W = 8, 2, 128, 16, 16, 2
+    q, lse = torch.zeros((520, Hq, d), dtype=BF, device=DEV), torch.zeros((520, Hq), device=DEV)
+    k, w = torch.zeros((W, 90, Hkv, bs, d), dtype=BF, device=DEV), torch.zeros((W, 90, Hkv, bs), device=DEV)
+    t, s, c = (torch.zeros(x, dtype=torch.int32, device=DEV) for x in ((3, 40), 4, 3))
+    call = lambda: ra.cp_attn_weights(q, lse, k, t, s, c, I, W, 1, w_in=w, w_out=w)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for ctx, n in [([1000, 3, 64], [1, 1, 1]), ([700, 40, 1], [500, 9, 1]), ([5, 1200, 0], [0, 20, 0]), ([300, 40, 64], [64, 0, 5])]:
+        kc, _, table, _ = paged(sum(ctx), ctx, Hkv, d, bs, I, W, 1)
+        qc, qsl = batch(sum(ctx), n, Hq, d)
+        _, L, _ = S.chunk_attn(qc, kc, kc, table, qsl, ctx, bs, I, W, 1)
+        L = torch.from_numpy(L).float()
+        old = torch.rand(w.shape)
+        q[:qc.shape[0]], lse[:qc.shape[0]], k[:, :kc.shape[1]] = qc.to(DEV), L.to(DEV), kc.to(DEV)
+        t[:, :table.shape[1]] = table.to(DEV)
+        s.copy_(qsl)
+        c.copy_(i32(*ctx))
+        w.copy_(old)
+        graph.replay()
+        check_status(ra)
+        want = S.attn_weights(qc, L, kc, table, qsl, ctx, bs, I, W, 1, w_in=old[:, :kc.shape[1]].numpy())
+        live = assert_weights(w[:, :kc.shape[1]], want)
+        assert torch.equal(w.cpu()[:, :kc.shape[1]][torch.from_numpy(~live)], old[:, :kc.shape[1]][torch.from_numpy(~live)])
+
+
 # ---------------------------------------------------------------------- chunk attention
 
 def test_chunk_attn_work_in_coarser_units(ra):
