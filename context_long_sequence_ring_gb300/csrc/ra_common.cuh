@@ -34,6 +34,8 @@ int fetch_error_rope_apply(int* where);
 int fetch_error_chunk_attn(int* where);
 int fetch_error_attn_weights(int* where);
 int fetch_error_evict(int* where);
+int fetch_error_rope_append(int* where);
+int fetch_error_window_attn(int* where);
 
 }  // namespace ra
 

@@ -3,29 +3,27 @@
 //
 // Mathematics.  Pair i of a row at position m is turned by the angle
 // m * f_i: (a, b) -> mscale * (a cos - b sin, b cos + a sin).  The backward
-// direction is the transposed rotation, i.e. the angle -m * f_i.
-// Angles are taken in turns, m * phi_i with phi_i = f_i / 2 pi held as an
-// unevaluated sum of two floats.  m * hi is split exactly into p + e with one
-// FMA, the whole turns rint(p) drop out exactly, and the rest goes to
-// sincospif: the angle error is about 1e-7 turns at any position below 2^24.
+// direction is the transposed rotation, i.e. the angle -m * f_i.  With several
+// axes m is the position of the pair's own axis.  How angles are formed:
+// ra_rope_turn.cuh.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "ra_paged.cuh"
+#include "ra_rope_turn.cuh"
 
 RA_DEFINE_ERROR_FETCH(fetch_error_rope_apply)
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxPairs = 128;           // rot <= 256
-constexpr int kPositionLimit = 1 << 24;  // positions are exact in a float below this
 
-struct Params {
+struct Params : Turns {
   const void* src;
   void* dst;
   const int32_t* idx;
-  const int32_t* positions;
+  const int32_t* positions;   // of axis a: positions + a * rows
   int64_t src_rows, src_rs, src_hs, dst_rs, dst_hs, rows;
   int32_t H, d, rot;
   // rows of whole words: rows row0 .. row0 + row_end of this launch, threads of a row, its units that turn,
@@ -33,20 +31,7 @@ struct Params {
   int64_t row0;
   int32_t row_end, per_row, turn_units, heads;
   FastDiv by_units, by_groups;
-  float mscale, sign;
-  float2 phase[kMaxPairs];  // phi_i as hi + lo
 };
-
-// mscale * cos and mscale * sin (signed by the direction) of pair i at position m.
-__device__ __forceinline__ void turn(const Params& p, int i, float m, float& c, float& s) {
-  const float2 ph = p.phase[i];
-  const float t = m * ph.x;
-  const float err = fmaf(m, ph.x, -t);           // m * hi = t + err exactly
-  const float f = (t - rintf(t)) + fmaf(m, ph.y, err);
-  sincospif(2.0f * f, &s, &c);
-  c *= p.mscale;
-  s *= p.mscale * p.sign;
-}
 
 // Source row of output row r; -1 for a zero row.
 __device__ __forceinline__ int64_t source_row(const Params& p, int64_t r) {
@@ -59,13 +44,19 @@ __device__ __forceinline__ int64_t source_row(const Params& p, int64_t r) {
   return s;
 }
 
-__device__ __forceinline__ float position(const Params& p, int64_t r) {
-  const int32_t m = p.positions[r];
-  if (m < 0 || m >= kPositionLimit) {
-    ra_record_error(RA_ERR_DEVICE_BOUNDS, 401);
-    return 0.f;
+// The angles of pairs i0 .. i0 + P - 1 at row r.  Several axes: neighbouring pairs mostly have the same one, whose
+// position is loaded once.
+template <bool AXES, int P>
+__device__ __forceinline__ void turns_of(const Params& p, int i0, int64_t r, float (&c)[P], float (&s)[P]) {
+  float m = 0.f;
+  int last = -1;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int a = AXES ? p.axis[i0 + i] : 0;
+    if (a != last) m = position_at(p.positions, a * p.rows + r, 401);
+    last = a;
+    turn(p, i0 + i, m, c[i], s[i]);
   }
-  return static_cast<float>(m);
 }
 
 __device__ __forceinline__ float load1(const __nv_bfloat16* x) { return __bfloat162float(*x); }
@@ -112,10 +103,6 @@ template <typename W> struct Word<__nv_bfloat16, W> {
   }
 };
 
-// The turned pair: real and imaginary part.  One form for all kernels, so that they agree to the bit.
-__device__ __forceinline__ float turn_re(float a, float b, float c, float s) { return fmaf(a, c, -__fmul_rn(b, s)); }
-__device__ __forceinline__ float turn_im(float a, float b, float c, float s) { return fmaf(b, c, __fmul_rn(a, s)); }
-
 constexpr int kHeads = 8;   // heads of a thread, at most
 
 // Rows of whole words.  A "unit" of a head is one word of pairs (interleaved),
@@ -126,7 +113,7 @@ constexpr int kHeads = 8;   // heads of a thread, at most
 // in bf16 (half) take 99 us, 6.8 TB/s, the rate of a plain copy.  4 heads a thread:
 // 103 us; all 40 in a loop that has 8 in flight: 140 us, since a thread's loads then
 // wait for its stores.
-template <typename T, typename W, bool INTER>
+template <typename T, typename W, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kThreads, 2) rope_words_kernel(const __grid_constant__ Params p) {
   using V = Word<T, W>;
   constexpr int N = V::N, P = INTER ? N / 2 : N;      // values of a word, pairs of a unit
@@ -151,11 +138,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_words_kernel(const __grid_co
       if (!INTER && turns) b[j] = *reinterpret_cast<const W*>(x + j * p.src_hs + half);
     }
   float c[P], sn[P];
-  if (s >= 0 && turns) {
-    const float m = position(p, r);
-#pragma unroll
-    for (int i = 0; i < P; ++i) turn(p, u * P + i, m, c[i], sn[i]);
-  }
+  if (s >= 0 && turns) turns_of<AXES>(p, u * P, r, c, sn);
 #pragma unroll
   for (int j = 0; j < kHeads; ++j) {
     if (j >= nh) break;
@@ -191,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_words_kernel(const __grid_co
 
 // Element-wise form for any stride and alignment: one thread per (row, unit),
 // units 0 .. rot/2-1 the pairs, the others the elements past rot.
-template <typename T, bool INTER>
+template <typename T, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constant__ Params p) {
   const int half = p.rot / 2;
   const int units = half + (p.d - p.rot);
@@ -204,8 +187,9 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
     const bool pair = u < half;
     const int e0 = pair ? (INTER ? 2 * u : u) : p.rot + (u - half);
     const int e1 = INTER ? e0 + 1 : e0 + half;
-    float c = 1.f, sn = 0.f;
-    if (pair && s >= 0) turn(p, u, position(p, r), c, sn);
+    float cs[1] = {1.f}, sns[1] = {0.f};
+    if (pair && s >= 0) turns_of<AXES>(p, u, r, cs, sns);
+    const float c = cs[0], sn = sns[0];
     const T* x = static_cast<const T*>(p.src) + s * p.src_rs;
     T* y = static_cast<T*>(p.dst) + r * p.dst_rs;
     for (int h = 0; h < p.H; ++h, x += p.src_hs, y += p.dst_hs) {
@@ -221,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
 }
 
 // Launches the kernel on rows of words W; more than 2^31 threads in several launches.
-template <typename T, typename W>
+template <typename T, typename W, bool AXES>
 ra_status launch_words(Params& p, bool inter, cudaStream_t stream) {
   constexpr int N = Word<T, W>::N;
   p.turn_units = inter ? p.rot / N : p.rot / 2 / N;
@@ -240,34 +224,22 @@ ra_status launch_words(Params& p, bool inter, cudaStream_t stream) {
   for (p.row0 = 0; p.row0 < rows; p.row0 += most) {
     p.row_end = static_cast<int32_t>(std::min(most, rows - p.row0));
     const unsigned blocks = static_cast<unsigned>(ra::ceil_div(static_cast<int64_t>(p.row_end) * p.per_row, kThreads));
-    if (inter) rope_words_kernel<T, W, true><<<blocks, kThreads, 0, stream>>>(p);
-    else rope_words_kernel<T, W, false><<<blocks, kThreads, 0, stream>>>(p);
+    if (inter) rope_words_kernel<T, W, true, AXES><<<blocks, kThreads, 0, stream>>>(p);
+    else rope_words_kernel<T, W, false, AXES><<<blocks, kThreads, 0, stream>>>(p);
     RA_LAUNCH_CHECK("rope_words_kernel");
   }
   return RA_OK;
 }
 
-// Whether the elements of [rows, H, d] at these strides are all apart.
-bool apart(int64_t rows, int64_t rs, int64_t H, int64_t hs, int64_t d) {
-  if (rows > 1 && H > 1)
-    return (hs >= d && rs >= (H - 1) * hs + d) || (rs >= d && hs >= (rows - 1) * rs + d);
-  return (rows <= 1 || rs >= d) && (H <= 1 || hs >= d);
-}
-
-}  // namespace
-
-extern "C" ra_status ra_rope_apply(const void* src, int64_t src_rows, int64_t src_row_stride,
-                                   int64_t src_head_stride, void* dst, int64_t dst_row_stride,
-                                   int64_t dst_head_stride, int64_t rows, int32_t H, int32_t d, int32_t rot,
-                                   ra_dtype dt, ra_rope_style style, const int32_t* idx, const int32_t* positions,
-                                   const double* inv_freq, double mscale, int32_t backward, ra_stream stream) {
+// idx NULL: rows in order.  axis NULL: one axis.
+ra_status rope_apply(const void* src, int64_t src_rows, int64_t src_row_stride, int64_t src_head_stride, void* dst,
+                     int64_t dst_row_stride, int64_t dst_head_stride, int64_t rows, int32_t H, int32_t d, int32_t rot,
+                     ra_dtype dt, ra_rope_style style, const int32_t* idx, const int32_t* positions, int32_t n_axes,
+                     const double* inv_freq, const int32_t* axis, double mscale, int32_t backward, cudaStream_t stream) {
   ra::clear_error();
   RA_REQUIRE(dt == RA_BF16 || dt == RA_F32, "dtype must be RA_BF16 or RA_F32");
-  RA_REQUIRE(style == RA_ROPE_HALF || style == RA_ROPE_INTERLEAVED, "unknown rope style");
   RA_REQUIRE(H >= 1 && d >= 1 && d <= 1024, "H >= 1 and 1 <= d <= 1024 required");
   RA_REQUIRE(static_cast<int64_t>(H) * d < (int64_t(1) << 31), "H*d must be below 2^31");   // threads of a row: 32 bits
-  RA_REQUIRE(rot >= 2 && rot % 2 == 0 && rot <= d && rot <= 2 * kMaxPairs, "rot must be even, in [2, min(d, %d)]",
-             2 * kMaxPairs);
   RA_REQUIRE(rows >= 0 && src_rows >= 0, "negative size");
   RA_REQUIRE(idx || rows == src_rows, "without idx, rows must equal src_rows");
   const int64_t lim = int64_t(1) << 40;
@@ -275,10 +247,9 @@ extern "C" ra_status ra_rope_apply(const void* src, int64_t src_rows, int64_t sr
                  src_row_stride < lim && src_head_stride < lim && dst_row_stride < lim && dst_head_stride < lim &&
                  rows < (int64_t(1) << 31) && src_rows < (int64_t(1) << 31),
              "strides must be in [0, 2^40), rows in [0, 2^31)");
-  RA_REQUIRE(inv_freq != nullptr && std::isfinite(mscale), "inv_freq must be given and mscale finite");
-  const double two_pi = 6.283185307179586476925286766559;
-  for (int i = 0; i < rot / 2; ++i)
-    RA_REQUIRE(std::fabs(inv_freq[i]) <= two_pi, "inv_freq[%d] must be in [-2 pi, 2 pi]", i);
+  Params p;
+  const ra_status st = make_turns(p, d, rot, style, inv_freq, axis, n_axes, mscale, backward != 0);
+  if (st != RA_OK) return st;
   if (rows == 0) return RA_OK;
   RA_REQUIRE(src && dst && positions, "NULL pointer");
   RA_REQUIRE(apart(rows, dst_row_stride, H, dst_head_stride, d), "the elements of dst must not alias one another");
@@ -294,44 +265,62 @@ extern "C" ra_status ra_rope_apply(const void* src, int64_t src_rows, int64_t sr
     RA_REQUIRE(d1 <= s0 || s1 <= d0, "dst must be src itself with its strides (without idx) or not overlap it");
   }
 
-  Params p;
   p.src = src; p.dst = dst; p.idx = idx; p.positions = positions;
   p.src_rows = src_rows; p.src_rs = src_row_stride; p.src_hs = src_head_stride;
   p.dst_rs = dst_row_stride; p.dst_hs = dst_head_stride; p.rows = rows;
   p.H = H; p.d = d; p.rot = rot;
-  p.mscale = static_cast<float>(mscale);
-  p.sign = backward ? -1.f : 1.f;
-  for (int i = 0; i < kMaxPairs; ++i) {
-    const double phi = i < rot / 2 ? inv_freq[i] / two_pi : 0.0;
-    const float hi = static_cast<float>(phi);
-    p.phase[i] = make_float2(hi, static_cast<float>(phi - static_cast<double>(hi)));
-  }
+  const bool inter = style == RA_ROPE_INTERLEAVED;
   // whole words: every address that is read or written as one is a multiple of its size
   auto words = [&](int bytes) {
     const int n = bytes / es;
     uint64_t m = s0 | d0;
     if (rows > 1 || idx) m |= static_cast<uint64_t>(src_row_stride * es) | static_cast<uint64_t>(dst_row_stride * es);
     if (H > 1) m |= static_cast<uint64_t>(src_head_stride * es) | static_cast<uint64_t>(dst_head_stride * es);
-    return m % bytes == 0 && d % n == 0 && rot % n == 0 && (style == RA_ROPE_INTERLEAVED || (rot / 2) % n == 0);
+    return m % bytes == 0 && d % n == 0 && rot % n == 0 && (inter || (rot / 2) % n == 0);
   };
-  if (words(16))
-    return dt == RA_BF16 ? launch_words<__nv_bfloat16, uint4>(p, style == RA_ROPE_INTERLEAVED, stream)
-                         : launch_words<float, uint4>(p, style == RA_ROPE_INTERLEAVED, stream);
-  if (words(8))
-    return dt == RA_BF16 ? launch_words<__nv_bfloat16, uint2>(p, style == RA_ROPE_INTERLEAVED, stream)
-                         : launch_words<float, uint2>(p, style == RA_ROPE_INTERLEAVED, stream);
-  const int64_t units = rot / 2 + (d - rot);
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ra::ceil_div(rows * units, kThreads), 152 * 64));
-  const bool inter = style == RA_ROPE_INTERLEAVED;
-  if (dt == RA_BF16) {
-    if (inter) rope_any_kernel<__nv_bfloat16, true><<<blocks, kThreads, 0, stream>>>(p);
-    else rope_any_kernel<__nv_bfloat16, false><<<blocks, kThreads, 0, stream>>>(p);
-  } else {
-    if (inter) rope_any_kernel<float, true><<<blocks, kThreads, 0, stream>>>(p);
-    else rope_any_kernel<float, false><<<blocks, kThreads, 0, stream>>>(p);
-  }
-  RA_LAUNCH_CHECK("rope_any_kernel");
-  return RA_OK;
+  auto launch = [&](auto axes) -> ra_status {
+    constexpr bool AXES = decltype(axes)::value;
+    if (words(16))
+      return dt == RA_BF16 ? launch_words<__nv_bfloat16, uint4, AXES>(p, inter, stream)
+                           : launch_words<float, uint4, AXES>(p, inter, stream);
+    if (words(8))
+      return dt == RA_BF16 ? launch_words<__nv_bfloat16, uint2, AXES>(p, inter, stream)
+                           : launch_words<float, uint2, AXES>(p, inter, stream);
+    const int64_t units = rot / 2 + (d - rot);
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ra::ceil_div(rows * units, kThreads), 152 * 64));
+    if (dt == RA_BF16) {
+      if (inter) rope_any_kernel<__nv_bfloat16, true, AXES><<<blocks, kThreads, 0, stream>>>(p);
+      else rope_any_kernel<__nv_bfloat16, false, AXES><<<blocks, kThreads, 0, stream>>>(p);
+    } else {
+      if (inter) rope_any_kernel<float, true, AXES><<<blocks, kThreads, 0, stream>>>(p);
+      else rope_any_kernel<float, false, AXES><<<blocks, kThreads, 0, stream>>>(p);
+    }
+    RA_LAUNCH_CHECK("rope_any_kernel");
+    return RA_OK;
+  };
+  return axis ? launch(std::true_type{}) : launch(std::false_type{});
+}
+
+}  // namespace
+
+extern "C" ra_status ra_rope_apply(const void* src, int64_t src_rows, int64_t src_row_stride,
+                                   int64_t src_head_stride, void* dst, int64_t dst_row_stride,
+                                   int64_t dst_head_stride, int64_t rows, int32_t H, int32_t d, int32_t rot,
+                                   ra_dtype dt, ra_rope_style style, const int32_t* idx, const int32_t* positions,
+                                   const double* inv_freq, double mscale, int32_t backward, ra_stream stream) {
+  return rope_apply(src, src_rows, src_row_stride, src_head_stride, dst, dst_row_stride, dst_head_stride, rows, H, d, rot,
+                    dt, style, idx, positions, 1, inv_freq, nullptr, mscale, backward, stream);
+}
+
+extern "C" ra_status ra_rope_apply_axes(const void* src, int64_t src_row_stride, int64_t src_head_stride, void* dst,
+                                        int64_t dst_row_stride, int64_t dst_head_stride, int64_t rows, int32_t H, int32_t d,
+                                        int32_t rot, ra_dtype dt, ra_rope_style style, const int32_t* positions,
+                                        int32_t n_axes, const double* inv_freq, const int32_t* axis, double mscale,
+                                        int32_t backward, ra_stream stream) {
+  ra::clear_error();
+  RA_REQUIRE(axis != nullptr, "the axis of each pair must be given");
+  return rope_apply(src, rows, src_row_stride, src_head_stride, dst, dst_row_stride, dst_head_stride, rows, H, d, rot, dt,
+                    style, nullptr, positions, n_axes, inv_freq, axis, mscale, backward, stream);
 }
 
 extern "C" ra_status ra_rope_frequencies(ra_rope_scaling scaling, double base, int32_t rot, double factor,

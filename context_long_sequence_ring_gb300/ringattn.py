@@ -69,6 +69,19 @@ SIGNATURES = {
                            _i64, _i32, _f32, _vp, _vp, _vp],
     "ra_cp_evict": [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _c.c_int, _i32, _i32, _i32, _i32, _i32, _i32, _i64,
                     _i32, _i32, _i32, _vp, _vp, _vp],
+    "ra_rope_apply_axes": [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _c.c_int, _c.c_int, _vp, _i32, _vp,
+                           _vp, _c.c_double, _i32, _vp],
+    "ra_cp_rope_append": [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64,
+                          _i32, _i32, _i32, _i32, _c.c_int, _i32, _i32, _i32, _i32, _i32, _i64, _vp, _i32, _i32, _c.c_int,
+                          _vp, _vp, _c.c_double, _vp],
+    "ra_cp_window_attn_workspace_size": [_i32, _i32, _i32, _c.POINTER(_sz)],
+    "ra_cp_window_attn": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i64,
+                          _i32, _i32, _f32, _vp, _c.c_int, _vp, _vp, _sz, _vp],
+    "ra_window_attn_workspace_size": [_i64, _i32, _i32, _i32, _i32, _c.POINTER(_sz)],
+    "ra_window_attn_fwd": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp,
+                           _c.c_int, _vp, _vp, _sz, _vp],
+    "ra_window_attn_bwd": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
+                           _f32, _vp, _i64, _vp, _i64, _vp, _i64, _c.c_int, _vp, _sz, _vp],
     "ra_selftest_wait_timeout": [_i64, _vp],
     "ra_synth_fill": [_u64, _i64, _vp, _i32, _vp, _vp],
 }
@@ -234,8 +247,7 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
         raise ValueError("positions and idx must be int32")
     if x.get_device() != dev:
         raise ValueError("x must be on the current CUDA device")
-    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous float64 vector on the host")
+    _frequency_table(inv_freq)
     if x.dim() != 3:
         raise ValueError("x must be [rows, H, d]")
     rows, H, d = x.shape
@@ -255,6 +267,52 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     _check(lib().ra_rope_apply(x.data_ptr(), rows, rs, hs, out.data_ptr(), ors, ohs, n, H, d, 2 * inv_freq.numel(),
                                _dt(x), ROPE_STYLES[style], _ptr(idx), positions.data_ptr(), inv_freq.data_ptr(), mscale,
                                1 if backward else 0, torch._C._cuda_getCurrentRawStream(dev)))
+    return out
+
+
+def _axis_table(axis, inv_freq):
+    if axis.dtype != torch.int32 or axis.is_cuda or axis.shape != inv_freq.shape or not axis.is_contiguous():
+        raise ValueError("axis must be a contiguous int32 vector on the host, one entry per frequency")
+
+
+def _frequency_table(inv_freq):
+    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 vector on the host")
+
+
+def _heads_of(x, what, dev, dtype):
+    """Row and head stride of [rows, heads, d] with dense heads' elements."""
+    if x.dim() != 3 or x.get_device() != dev or x.dtype != dtype:
+        raise ValueError("%s must be [rows, heads, d] of %s on the current CUDA device" % (what, dtype))
+    rs, hs, es = x.stride()
+    if es != 1 and x.shape[2] > 1:
+        raise ValueError("the elements of a head of %s must be contiguous" % what)
+    return rs, hs
+
+
+def rope_apply_axes(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, axis: torch.Tensor,
+                    mscale: float = 1.0, style: str = "half", backward: bool = False, out: Optional[torch.Tensor] = None):
+    """Rotary positions with several axes: ``rope_apply`` of x [rows, H, d] (any strides with the last one 1)
+    with pair i turned by positions[axis[i]] * inv_freq[i].  positions int32 [axes, rows] (e.g. time, height
+    and width); inv_freq float64 and axis int32, both [rot/2] on the host.  out may be x (in place).
+    ``backward`` turns by the negative angles: the gradient of x from the gradient of out."""
+    dev = _here(positions)
+    _of(torch.int32, positions)
+    _frequency_table(inv_freq)
+    _axis_table(axis, inv_freq)
+    rs, hs = _heads_of(x, "x", dev, x.dtype)
+    rows, H, d = x.shape
+    if positions.dim() != 2 or positions.shape[1] != rows:
+        raise ValueError("positions must be [axes, rows]")
+    if out is None:
+        out = torch.empty((rows, H, d), dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape:
+        raise ValueError("out must be like x")
+    ors, ohs = _heads_of(out, "out", dev, x.dtype)
+    _check(lib().ra_rope_apply_axes(x.data_ptr(), rs, hs, out.data_ptr(), ors, ohs, rows, H, d, 2 * inv_freq.numel(), _dt(x),
+                                    ROPE_STYLES[style], positions.data_ptr(), positions.shape[0], inv_freq.data_ptr(),
+                                    axis.data_ptr(), mscale, 1 if backward else 0,
+                                    torch._C._cuda_getCurrentRawStream(dev)))
     return out
 
 
@@ -690,6 +748,173 @@ def cp_evict(k_cache, v_cache, weights, block_table, ctx_lens, keep: int, interl
                              dcp, max_vb, dst_vb, NB, keep, n_sink, n_recent, kept.data_ptr(), new_lens.data_ptr(),
                              torch._C._cuda_getCurrentRawStream(dev)))
     return kept, new_lens
+
+
+def cp_rope_append(k, v, k_cache, v_cache, block_table, query_start_loc, ctx_lens, interleave: int, pcp: int, dcp: int,
+                   positions=None, inv_freq=None, axis=None, mscale: float = 1.0, style: str = "half", q=None,
+                   q_out=None):
+    """New tokens into the sharded paged cache: k and v [T, Hkv, d] (any strides with the last one 1; request r's
+    are rows query_start_loc[r] .. query_start_loc[r+1], the last ones of its ctx_lens[r] tokens), k turned by its
+    rotary positions.  q [T, Hq, d] is turned beside them into q_out (new if not given; may be q) and returned.
+    positions int32 [T], or [axes, T] with axis int32 [rot/2] on the host; None: the token's place in its context.
+    inv_freq float64 [rot/2] on the host; None: nothing is turned."""
+    dev = _here(k_cache, v_cache, block_table, query_start_loc, ctx_lens, positions)
+    _of(torch.int32, block_table, query_start_loc, ctx_lens, positions)
+    if k_cache.dim() != 5 or block_table.dim() != 2:
+        raise ValueError("the cache must be [W, NB, Hkv, bs, d], block_table [R, max_vblocks]")
+    W, NB, Hkv, bs, d = k_cache.shape
+    R, max_vb = block_table.shape
+    dt = k_cache.dtype
+    if W != pcp * dcp:
+        raise ValueError("cache has %d devices, pcp*dcp = %d" % (W, pcp * dcp))
+    if v_cache.shape != k_cache.shape or v_cache.dtype != dt:
+        raise ValueError("v_cache must be like k_cache")
+    if query_start_loc.numel() != R + 1 or ctx_lens.numel() != R:
+        raise ValueError("block_table has %d requests: query_start_loc needs R+1 entries, ctx_lens R" % R)
+    krs, khs = _heads_of(k, "k", dev, dt)
+    vrs, vhs = _heads_of(v, "v", dev, dt)
+    T = k.shape[0]
+    if k.shape != (T, Hkv, d) or v.shape != (T, Hkv, d):
+        raise ValueError("k and v must be [T, Hkv, d] of the cache's heads")
+    n_axes, rot = 1, 0
+    if inv_freq is not None:
+        _frequency_table(inv_freq)
+        rot = 2 * inv_freq.numel()
+        if axis is not None:
+            _axis_table(axis, inv_freq)
+            if positions is None:
+                raise ValueError("several axes need positions")
+    if positions is not None:
+        n_axes = positions.shape[0] if axis is not None and positions.dim() == 2 else 1
+        if positions.shape != ((n_axes, T) if axis is not None else (T,)):
+            raise ValueError("positions must be [T], or [axes, T] with axis")
+    Hq, qrs, qhs, ors, ohs = 0, 0, 0, 0, 0
+    if q is not None:
+        qrs, qhs = _heads_of(q, "q", dev, dt)
+        Hq = q.shape[1]
+        if q.shape != (T, Hq, d):
+            raise ValueError("q must be [T, Hq, d]")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must be like q")
+        ors, ohs = _heads_of(q_out, "q_out", dev, dt)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check(lib().ra_cp_rope_append(k.data_ptr(), krs, khs, v.data_ptr(), vrs, vhs, _ptr(q), qrs, qhs, _ptr(q_out), ors, ohs,
+                                   k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                   query_start_loc.data_ptr(), ctx_lens.data_ptr(), T, R, Hq, Hkv, d, _dt(k_cache), bs,
+                                   interleave, pcp, dcp, max_vb, NB, _ptr(positions), n_axes, rot, ROPE_STYLES[style],
+                                   _ptr(inv_freq), _ptr(axis), mscale, torch._C._cuda_getCurrentRawStream(dev)))
+    return q_out
+
+
+def _out_rows(o, lse, T: int, Hq: int, d: int, out_dtype, device):
+    if o is None:
+        o = torch.empty((T, Hq, d), dtype=out_dtype, device=device)
+    elif o.shape != (T, Hq, d):
+        raise ValueError("o must be [T, Hq, d]")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=device)
+    elif lse.shape != (T, Hq) or lse.dtype != torch.float32:
+        raise ValueError("lse must be float32 [T, Hq]")
+    return o, lse
+
+
+def cp_window_attn_workspace_size(Hq: int, Hkv: int, d: int) -> int:
+    n = _sz(0)
+    _check(lib().ra_cp_window_attn_workspace_size(Hq, Hkv, d, _c.byref(n)))
+    return n.value
+
+
+def cp_window_attn(q, k_cache, v_cache, block_table, query_start_loc, ctx_lens, window: int, interleave: int, pcp: int,
+                   dcp: int, n_sink: int = 0, scale: Optional[float] = None, out_dtype=torch.bfloat16, workspace=None,
+                   o=None, lse=None):
+    """``cp_chunk_attn`` with a sliding window: the query at position p sees the tokens x <= p with x > p - window or
+    x < n_sink -> (O [T, Hq, d], LSE [T, Hq]).  Blocks that no query of the request sees are not looked at (their
+    entries in block_table may hold anything)."""
+    dev = _here(q, k_cache, v_cache, block_table, query_start_loc, ctx_lens, workspace, o, lse)
+    T, Hq, d, NB, Hkv, bs, R, max_vb = _need_paged(q, k_cache, block_table, query_start_loc, ctx_lens, pcp, dcp)
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("v_cache must be like k_cache")
+    if workspace is None:
+        workspace = torch.empty(cp_window_attn_workspace_size(Hq, Hkv, d), dtype=torch.uint8, device=q.device)
+    o, lse = _out_rows(o, lse, T, Hq, d, out_dtype, q.device)
+    _check(lib().ra_cp_window_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                   query_start_loc.data_ptr(), ctx_lens.data_ptr(), T, R, Hq, Hkv, d, bs, interleave, pcp,
+                                   dcp, max_vb, NB, window, n_sink, scale or 0.0, o.data_ptr(), _dt(o), lse.data_ptr(),
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   torch._C._cuda_getCurrentRawStream(dev)))
+    return o, lse
+
+
+def window_attn_workspace_size(T: int, R: int, Hq: int, Hkv: int, d: int) -> int:
+    n = _sz(0)
+    _check(lib().ra_window_attn_workspace_size(T, R, Hq, Hkv, d, _c.byref(n)))
+    return n.value
+
+
+def _packed_rows(x, what, dev, dtype, shape=None):
+    """Row stride of [rows, heads, d] whose rows are dense."""
+    rs, hs = _heads_of(x, what, dev, dtype)
+    if shape is not None and x.shape != shape:
+        raise ValueError("%s must be %s" % (what, tuple(shape)))
+    if hs != x.shape[2] and x.shape[1] > 1:
+        raise ValueError("the heads of a row of %s must be contiguous" % what)
+    # a single row's stride is of no account
+    return rs if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def _need_packed(q, k, v, query_start_loc, workspace, *others):
+    dev = _here(query_start_loc, workspace, *others)
+    _of(torch.int32, query_start_loc)
+    bf = torch.bfloat16
+    qrs = _packed_rows(q, "q", dev, bf)
+    T, Hq, d = q.shape
+    krs, vrs = _packed_rows(k, "k", dev, bf), _packed_rows(v, "v", dev, bf, k.shape)
+    if k.shape[0] != T or k.shape[2] != d:
+        raise ValueError("k and v must be [T, Hkv, d] with q's tokens and head dim")
+    R, Hkv = query_start_loc.numel() - 1, k.shape[1]
+    if workspace is None:
+        workspace = torch.empty(window_attn_workspace_size(T, R, Hq, Hkv, d), dtype=torch.uint8, device=q.device)
+    return dev, qrs, krs, vrs, T, R, Hq, Hkv, d, workspace
+
+
+def window_attn_fwd(q, k, v, query_start_loc, window: int, n_sink: int = 0, scale: Optional[float] = None,
+                    out_dtype=torch.bfloat16, workspace=None, o=None, lse=None):
+    """Causal attention of packed sequences (rows query_start_loc[r] .. query_start_loc[r+1] of q [T, Hq, d] and
+    k, v [T, Hkv, d] bf16, rows any multiple of 8 elements apart) with a sliding window: position p sees x <= p with
+    x > p - window or x < n_sink -> (O [T, Hq, d], LSE [T, Hq]).  Rows of no sequence are left as they were."""
+    dev, qrs, krs, vrs, T, R, Hq, Hkv, d, workspace = _need_packed(q, k, v, query_start_loc, workspace, o, lse)
+    o, lse = _out_rows(o, lse, T, Hq, d, out_dtype, q.device)
+    _check(lib().ra_window_attn_fwd(q.data_ptr(), qrs, k.data_ptr(), krs, v.data_ptr(), vrs, query_start_loc.data_ptr(), T,
+                                    R, Hq, Hkv, d, window, n_sink, scale or 0.0, o.data_ptr(), _dt(o), lse.data_ptr(),
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    torch._C._cuda_getCurrentRawStream(dev)))
+    return o, lse
+
+
+def window_attn_bwd(do, q, k, v, o, lse, query_start_loc, window: int, n_sink: int = 0, scale: Optional[float] = None,
+                    out_dtype=torch.bfloat16, workspace=None, dq=None, dk=None, dv=None):
+    """Gradient of ``window_attn_fwd``: do, o [T, Hq, d] bf16 and lse [T, Hq] (what it gave) -> (dQ [T, Hq, d],
+    dK, dV [T, Hkv, d]) in out_dtype, or in the dtype of given outputs, whose rows may be any multiple of 16 bytes
+    apart (parts of the gradient of a fused projection)."""
+    dev, qrs, krs, vrs, T, R, Hq, Hkv, d, workspace = _need_packed(q, k, v, query_start_loc, workspace, do, o, lse)
+    _of(torch.bfloat16, do, o)
+    _of(torch.float32, lse)
+    if do.shape != q.shape or o.shape != q.shape or lse.shape != (T, Hq):
+        raise ValueError("do and o must be [T, Hq, d], lse [T, Hq]")
+    given = [x for x in (dq, dk, dv) if x is not None]
+    dt = given[0].dtype if given else out_dtype
+    new = lambda x: torch.empty(x.shape, dtype=dt, device=q.device)
+    dq, dk, dv = (new(x) if g is None else g for x, g in ((q, dq), (k, dk), (v, dv)))
+    rs = [_packed_rows(g, what, dev, dt, x.shape) for g, what, x in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v))]
+    _check(lib().ra_window_attn_bwd(q.data_ptr(), qrs, k.data_ptr(), krs, v.data_ptr(), vrs, o.data_ptr(), lse.data_ptr(),
+                                    do.data_ptr(), query_start_loc.data_ptr(), T, R, Hq, Hkv, d, window, n_sink,
+                                    scale or 0.0, dq.data_ptr(), rs[0], dk.data_ptr(), rs[1], dv.data_ptr(), rs[2],
+                                    _dt(dq), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    torch._C._cuda_getCurrentRawStream(dev)))
+    return dq, dk, dv
 
 
 # ---------------------------------------------------------------------- misc

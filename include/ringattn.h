@@ -176,6 +176,29 @@ ra_status ra_rope_apply(const void* src, int64_t src_rows, int64_t src_row_strid
                         ra_stream stream);
 
 /* ------------------------------------------------------------------------
+ * ra_rope_apply_axes -- rotary positions with several axes (time, height and
+ * width of a film's patches, height and width of a picture's): as
+ * ra_rope_apply, but pair i turns by the position on its own axis,
+ *   dst[r, h, :rot] = mscale * Rot_i(positions[axis[i]][r] * inv_freq[i]) src[r, h, :rot],
+ * rows in order (no idx).  axis in sections (0 .. 0, 1 .. 1, 2 .. 2), in turns
+ * (0, 1, 2, 0, 1, 2, ..) or any other order, with one table of frequencies for
+ * all axes or one for each, laid side by side.
+ * Sources: rotary form as ra_rope_gather; one axis of it is ra_rope_apply.
+ *
+ * positions  device int32 [n_axes, rows], in [0, 2^24).  Of an axis that no pair
+ *            has, nothing is read.
+ * n_axes     1 .. 16.
+ * axis       host int32 [rot/2]: axis of each pair, in [0, n_axes).
+ * The rest, backward and errors included: as ra_rope_apply without idx.  With all
+ * positions of a row equal the result is that of ra_rope_apply to the bit.
+ * ---------------------------------------------------------------------- */
+ra_status ra_rope_apply_axes(const void* src, int64_t src_row_stride, int64_t src_head_stride, void* dst,
+                             int64_t dst_row_stride, int64_t dst_head_stride, int64_t rows, int32_t H, int32_t d,
+                             int32_t rot, ra_dtype dt, ra_rope_style style, const int32_t* positions, int32_t n_axes,
+                             const double* inv_freq, const int32_t* axis, double mscale, int32_t backward,
+                             ra_stream stream);
+
+/* ------------------------------------------------------------------------
  * ra_rope_frequencies -- the frequency tables of ra_rope_apply, on the host.
  * theta_i = base^(-2i/rot), i = 0 .. rot/2-1, changed for contexts `factor`
  * times the trained length (guijiagi.com tag page "Ring Attention", article on
@@ -680,6 +703,126 @@ ra_status ra_cp_evict(void* k_cache, void* v_cache, float* weights, const int32_
                       ra_dtype dt, int32_t block_size, int32_t interleave, int32_t pcp, int32_t dcp,
                       int32_t max_vblocks, int32_t dst_max_vblocks, int64_t num_blocks, int32_t keep,
                       int32_t n_sink, int32_t n_recent, int32_t* kept, int32_t* new_lens, ra_stream stream);
+
+/* ------------------------------------------------------------------------
+ * ra_cp_rope_append -- a batch's new tokens into the sharded paged cache in one
+ * launch, K turned by its rotary positions on the way, Q turned beside it:
+ *   K[x] = mscale Rot(pos) k,  V[x] = v,  q_out = mscale Rot(pos) q
+ * for every token i of request r, which is token x = ctx_lens[r] - n_r + i of its
+ * context (n_r new tokens, counted in ctx_lens[r]: the convention of
+ * ra_cp_chunk_attn, which can read what this call has stored).  It does the work of
+ * ra_rope_apply on Q and on K, ra_cp_slot_mapping and ra_cp_kv_scatter, with the
+ * same results to the bit.  Sources: as those.
+ *
+ * k, v, q     device dt (RA_BF16 or RA_F32): element (token, head, e) at + token*row_stride
+ *             + head*head_stride + e (strides in elements, >= 0; e.g. the K, V and Q heads
+ *             of a fused projection), T tokens packed request after request.  q may be
+ *             NULL (then q_out, Hq and their strides are not looked at).
+ * q_out       device dt out, addressed the same way, its elements apart; q itself with the
+ *             same strides (in place), or apart from q, k and v.  The caches, q, k and v do
+ *             not overlap.
+ * k_cache, v_cache device dt [W, num_blocks, Hkv, block_size, d], 16-byte aligned.
+ * query_start_loc device int32 [R+1], non-decreasing, within [0, T]; ctx_lens device
+ *             int32 [R]; block_table device int32 [R, max_vblocks].
+ * positions   device int32 [n_axes, T], in [0, 2^24): the rotary position of each token on
+ *             each axis (see ra_rope_apply_axes), which need not be x: a context that was
+ *             cut, or pictures in it, move them.  NULL (one axis): x.
+ * rot, style, inv_freq, axis, mscale: as ra_rope_apply_axes; axis NULL: one axis (n_axes 1).
+ *             inv_freq NULL and rot 0: nothing is turned, K is stored and Q copied as they are.
+ * Tokens of no request are not stored and their q_out is left as it was.  A slot that
+ * several tokens of a call have (requests that share a block) gets one of them.
+ * Requires d <= 1024, d * element size a multiple of 16 bytes (RA_ERR_UNSUPPORTED
+ * otherwise), heads * d < 2^29, T < 2^31, sizes of the cache as ra_cp_chunk_attn's but any
+ * block size.
+ * Device bounds errors: a query_start_loc that decreases or leaves [0, T] (which tokens are
+ * stored is not defined then), a token with x < 0, past the table or 2^30 (not stored), a
+ * block id outside [0, num_blocks) (not stored), a position out of range (taken as 0).
+ * ---------------------------------------------------------------------- */
+ra_status ra_cp_rope_append(const void* k, int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                            int64_t v_row_stride, int64_t v_head_stride, const void* q, int64_t q_row_stride,
+                            int64_t q_head_stride, void* q_out, int64_t q_out_row_stride, int64_t q_out_head_stride,
+                            void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* query_start_loc,
+                            const int32_t* ctx_lens, int64_t T, int32_t R, int32_t Hq, int32_t Hkv, int32_t d, ra_dtype dt,
+                            int32_t block_size, int32_t interleave, int32_t pcp, int32_t dcp, int32_t max_vblocks,
+                            int64_t num_blocks, const int32_t* positions, int32_t n_axes, int32_t rot, ra_rope_style style,
+                            const double* inv_freq, const int32_t* axis, double mscale, ra_stream stream);
+
+/* ------------------------------------------------------------------------
+ * ra_cp_window_attn -- ra_cp_chunk_attn with a sliding window and first tokens
+ * that stay visible ("sinks"): the query at position p sees the tokens x <= p with
+ * x > p - window or x < n_sink.  Source: as ra_cp_chunk_attn; the mask is the definition.
+ * The keys out of sight cost nothing, and a context may be longer than what is kept of it:
+ * a virtual block none of whose tokens a query of the request sees is not looked at, whatever its
+ * entry in block_table holds (-1, a block that is another request's by now).
+ *
+ * window      >= 1, in tokens, the query's own included; n_sink >= 0.
+ * The rest as ra_cp_chunk_attn with causal = 1 (rows of no request, queries that see
+ * nothing, limits, device bounds errors for the blocks that are looked at).  V of a token in a
+ * block that is looked at must be finite below ctx_lens[r].
+ * workspace   device scratch of ra_cp_window_attn_workspace_size() bytes, 16-byte aligned.
+ *             Calls that overlap on the GPU need one each.
+ * ---------------------------------------------------------------------- */
+ra_status ra_cp_window_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t d, size_t* bytes);
+
+ra_status ra_cp_window_attn(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                            const int32_t* query_start_loc, const int32_t* ctx_lens, int64_t T, int32_t R, int32_t Hq,
+                            int32_t Hkv, int32_t d, int32_t block_size, int32_t interleave, int32_t pcp, int32_t dcp,
+                            int32_t max_vblocks, int64_t num_blocks, int32_t window, int32_t n_sink, float scale, void* o,
+                            ra_dtype out_dt, float* lse, void* workspace, size_t ws_bytes, ra_stream stream);
+
+/* ------------------------------------------------------------------------
+ * ra_window_attn_fwd -- causal attention with the same window and first tokens on
+ * packed sequences (a whole prompt, a training step): row t of sequence r is position
+ * t - query_start_loc[r] and sees tokens of its own sequence only.
+ * Source: guijiagi.com "Ring Attention" tag page, blockwise decomposition (attention in one
+ * pass over key blocks with a running max and sum); the mask is the definition above.
+ *
+ * q           device bf16 [T, Hq, d], k, v device bf16 [T, Hkv, d]: rows row_stride elements
+ *             apart (multiples of 8, e.g. parts of a fused projection), a row's heads dense.
+ * query_start_loc device int32 [R+1], non-decreasing, within [0, T].
+ * window      >= 1 (2^31 - 1: no window); n_sink >= 0.
+ * o           device [T, Hq, d] out in out_dt, dense; lse device float [T, Hq] out, natural log
+ *             (may be NULL).  Rows of no sequence are left as they were.
+ * Scores, sums and partials are fp32; probabilities are rounded to bf16 for their product.
+ * What a row does not see does not reach it, NaN included, except V rows of its own sequence that
+ * are not finite.
+ * workspace   device scratch of ra_window_attn_workspace_size() bytes, 16-byte aligned, for
+ *             either direction.  Calls that overlap on the GPU need one each.
+ * Requires Hq % Hkv == 0, Hq/Hkv <= 64, d in {64, 128}, T*Hq < 2^31; q, k, v, o 16-byte aligned.
+ * Lengths are read on the device: a captured call may be replayed with others.
+ * Device bounds error: a sequence whose range is decreasing or outside [0, T] (left out).
+ * ---------------------------------------------------------------------- */
+ra_status ra_window_attn_workspace_size(int64_t T, int32_t R, int32_t Hq, int32_t Hkv, int32_t d, size_t* bytes);
+
+ra_status ra_window_attn_fwd(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+                             int64_t v_row_stride, const int32_t* query_start_loc, int64_t T, int32_t R, int32_t Hq,
+                             int32_t Hkv, int32_t d, int32_t window, int32_t n_sink, float scale, void* o, ra_dtype out_dt,
+                             float* lse, void* workspace, size_t ws_bytes, ra_stream stream);
+
+/* ------------------------------------------------------------------------
+ * ra_window_attn_bwd -- the gradient of ra_window_attn_fwd: with P = e^{scale q.k - lse} on
+ * the visible pairs and delta = sum dO O of each row and head,
+ *   dV = P^T dO,  dS = P (dO V^T - delta),  dQ = scale dS K,  dK = scale dS^T Q,
+ * dK and dV summed over the query heads of their K/V head.
+ *
+ * q, k, v, query_start_loc, window, n_sink, scale, workspace: as the forward call's.
+ * o           device bf16 [T, Hq, d] and lse device float [T, Hq]: what it gave.
+ * d_o         device bf16 [T, Hq, d]: the gradient of o, dense.
+ * dq, dk, dv  device out in out_dt ([T, Hq, d], [T, Hkv, d], [T, Hkv, d]), rows row_stride
+ *             elements apart (multiples of 16 bytes; e.g. parts of the gradient of a fused projection).
+ *             They do not overlap one another nor the inputs.  Rows of no sequence are left as
+ *             they were.
+ * P and dS are rounded to bf16 for their products, all sums are fp32, in an order fixed by the
+ * lengths (the same call gives the same bits).
+ * A row whose lse is +inf has no weight, so that its gradient is 0.
+ * Requires what the forward call requires; o, d_o, dq, dk, dv 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+ra_status ra_window_attn_bwd(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+                             int64_t v_row_stride, const void* o, const float* lse, const void* d_o,
+                             const int32_t* query_start_loc, int64_t T, int32_t R, int32_t Hq, int32_t Hkv, int32_t d,
+                             int32_t window, int32_t n_sink, float scale, void* dq, int64_t dq_row_stride, void* dk,
+                             int64_t dk_row_stride, void* dv, int64_t dv_row_stride, ra_dtype out_dt, void* workspace,
+                             size_t ws_bytes, ra_stream stream);
 
 /* ------------------------------------------------------------------------
  * ra_cp_decode_noalloc -- ra_cp_decode for callers that cannot allocate
