@@ -66,6 +66,33 @@ struct Items {
   }
 };
 
+// The items of one head of a request whose queries see a window and some first tokens: an item's keys grow with k
+// up to those of a whole window.
+struct WindowItems {
+  uint64_t base;                  // cost of item k: base + slope * min(k + 1, full)
+  uint32_t slope, start;
+  int items, full;
+  bool pair;
+  RA_HD uint64_t upto(int k) const {
+    const uint64_t m = k < full ? k : full;
+    return static_cast<uint64_t>(k) * base + slope * (m * (m + 1) / 2 + static_cast<uint64_t>(k - m) * full);
+  }
+  RA_HD void set(const Rates& rt, int n, int n_items, int tpt, long long pos0, int L, int window, int n_sink) {
+    items = n_items;
+    pair = n > tpt;
+    const int f = pair ? kPairCost : rt.f_split, over = pair ? rt.over_pair : rt.over_split, tpi = (pair ? 2 : 1) * tpt;
+    // half a tile past either end of the window, and a tile of first tokens
+    const long long most = static_cast<long long>(window) + tpi + 128 + (n_sink + 127ll) / 128 * 128;
+    const long long cap = most < L ? most : L, before = pos0 < 0 ? 0 : (pos0 < cap ? pos0 : cap);
+    const long long steps = (cap - before) / tpi;
+    full = static_cast<int>(steps < n_items ? steps : n_items);
+    if (full < 1) full = 1;
+    base = static_cast<uint64_t>(over + before) * f;
+    start = over * f;
+    slope = tpi * f;
+  }
+};
+
 // Part c of the work is [lo(c), lo(c + 1)), empty from the first c with lo(c) = total on.  Where an equal
 // cut leaves few items to a part, and cutting each item into pieces of its own costs less than the second item
 // that a part would take up, lengths are counted in such pieces (piece > 0: the cost of one; share is 1 then).
@@ -78,18 +105,21 @@ struct Plan {
     return x < total ? x : total;
   }
   // Item k, and items 0 .. k-1 of a head: at least 1 each, so that none is lost.
-  RA_HD uint32_t cost(const Items& q, int k) const {
+  template <class I>
+  RA_HD uint32_t cost(const I& q, int k) const {
     const uint32_t c = static_cast<uint32_t>((q.upto(k + 1) >> shift) - (q.upto(k) >> shift)) + 1;
     return piece > 0.f ? static_cast<uint32_t>(quotient(static_cast<float>(c), piece)) + 1 : c;
   }
-  RA_HD uint32_t prefix(const Items& q, int k) const {
+  template <class I>
+  RA_HD uint32_t prefix(const I& q, int k) const {
     if (piece <= 0.f) return static_cast<uint32_t>(q.upto(k) >> shift) + k;
     uint32_t sum = 0;
 #pragma unroll 1
     for (int i = 0; i < k; ++i) sum += cost(q, i);
     return sum;
   }
-  RA_HD uint32_t over(const Items& q) const { return piece > 0.f ? 0 : q.start >> shift; }
+  template <class I>
+  RA_HD uint32_t over(const I& q) const { return piece > 0.f ? 0 : q.start >> shift; }
 
   // The steps of a plan: the unit, from the sum of upto() over all heads; the equal cut, from the sum of
   // prefix() in that unit; whether to try pieces; and their number, in which case they are taken or not.

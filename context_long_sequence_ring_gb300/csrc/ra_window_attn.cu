@@ -5,9 +5,7 @@
 // or x < n_sink).  O = sum_x e^{s_x - lse} v_x with lse = ln sum_x e^{s_x}, s_x = scale q.k_x.
 // Backward, with P = e^{s - lse} and delta = sum dO O of each row:
 //   dV = P^T dO,  dS = P (dO V^T - delta),  dQ = scale dS K,  dK = scale dS^T Q.
-#include <math_constants.h>
-
-#include "ra_paged.cuh"
+#include "ra_chunk_attn.cuh"
 
 RA_DEFINE_ERROR_FETCH(fetch_error_window_attn)
 
@@ -59,50 +57,6 @@ __device__ __forceinline__ float dot(const float (&x)[D / 32], const __nv_bfloat
 __device__ __forceinline__ void store_out(void* out, bool bf, int64_t at, float x) {
   if (bf) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(x);
   else static_cast<float*>(out)[at] = x;
-}
-
-// A warp per row and head.
-template <int D, bool PAGED>
-__global__ void __launch_bounds__(kRowThreads) window_rows_kernel(const __grid_constant__ WindowArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-  if (w >= a.T * a.Hq) return;
-  const int64_t t = w / a.Hq;
-  const int h = static_cast<int>(w - t * a.Hq), g = h / (a.Hq / a.Hkv);
-  int r, q0, n, L;
-  if (!find_row(a, t, r, q0, n, L)) return;
-  const int64_t ctx = PAGED ? a.ctx[r] : n, p = ctx - n + (t - q0);
-  float x[E], acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    x[e] = __bfloat162float(a.q[t * a.q_rs + h * D + lane * E + e]) * a.scale;
-    acc[e] = 0.f;
-  }
-  float m = -CUDART_INF_F, l = 0.f;
-  const int64_t lo = max(int64_t(0), p - a.window + 1);
-  for (int64_t y = 0; y <= p && y < L; ++y) {
-    if (y >= a.n_sink && y < lo) y = lo;
-    if (y >= L) break;             // a context that was cut: the window is past it
-    const __nv_bfloat16 *k, *v;
-    if (PAGED) {
-      const int64_t row = paged_row(a.c, r, static_cast<int>(y), g, 802);
-      if (row < 0) continue;
-      k = a.k + row * D; v = a.v + row * D;
-    } else {
-      k = a.k + (q0 + y) * a.k_rs + g * D; v = a.v + (q0 + y) * a.v_rs + g * D;
-    }
-    const float s = dot<D>(x, k + lane * E), mn = fmaxf(m, s);
-    const float f = m == -CUDART_INF_F ? 0.f : expf(m - mn), pr = expf(s - mn);
-    l = l * f + pr;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + pr * __bfloat162float(v[lane * E + e]);
-    m = mn;
-  }
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) store_out(a.o, a.out_bf16, w * D + lane * E + e, acc[e] * inv);
-  if (a.lse && lane == 0) a.lse[w] = l != 0.f ? m + logf(l) : -CUDART_INF_F;
 }
 
 // dQ of a row and head by a warp, and the row's delta.
@@ -179,7 +133,7 @@ __global__ void __launch_bounds__(kRowThreads) window_dkv_kernel(const __grid_co
 ra_status check_heads(int64_t T, int32_t R, int32_t Hq, int32_t Hkv, int32_t d, int32_t window, int32_t n_sink, ra_dtype out_dt) {
   RA_REQUIRE(out_dt == RA_F32 || out_dt == RA_BF16, "unknown out dtype");
   RA_REQUIRE(R >= 1 && Hkv >= 1 && Hq >= 1 && Hq % Hkv == 0, "R >= 1 and Hq (%d) a multiple of Hkv (%d) required", Hq, Hkv);
-  RA_REQUIRE(T >= 0 && T < (int64_t(1) << 31) / Hq, "T*Hq must be in [0, 2^31)");
+  RA_REQUIRE(T >= 0 && T < (int64_t(1) << 31) / Hq && T < (1 << 30), "T must be in [0, 2^30), T*Hq below 2^31");
   RA_REQUIRE(window >= 1 && n_sink >= 0, "window >= 1 and n_sink >= 0 required");
   if (d != 64 && d != 128) return ra::fail(RA_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", d);
   if (Hq / Hkv > 64) return ra::fail(RA_ERR_UNSUPPORTED, "GQA group %d > 64 not supported", Hq / Hkv);
@@ -190,8 +144,32 @@ unsigned row_blocks(int64_t rows) { return static_cast<unsigned>(ra::ceil_div(ro
 
 }  // namespace
 
+// The map of [T, heads, D] rows `stride` elements apart: boxes of 64 columns, box_heads heads, box_rows rows.
+namespace {
+ra_status row_map(CUtensorMap* map, const void* base, int D, int heads, int64_t rows, int64_t stride, uint32_t box_heads,
+                  uint32_t box_rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return RA_OK;
+}
+
+constexpr int kFar = 1 << 30;    // no position is further: contexts and sequences are shorter
+}  // namespace
+
 extern "C" ra_status ra_cp_window_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t d, size_t* bytes) {
-  return ra_cp_chunk_attn_workspace_size(Hq, Hkv, d, bytes);
+  ra::clear_error();
+  RA_REQUIRE(bytes != nullptr, "bytes is NULL");
+  RA_REQUIRE(Hq >= 1 && Hkv >= 1 && d >= 1, "sizes must be >= 1");
+  *bytes = chunk_workspace<WindowPaged>(d);
+  return RA_OK;
 }
 
 extern "C" ra_status ra_cp_window_attn(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -201,40 +179,27 @@ extern "C" ra_status ra_cp_window_attn(const void* q, const void* k_cache, const
                                        int32_t n_sink, float scale, void* o, ra_dtype out_dt, float* lse, void* workspace,
                                        size_t ws_bytes, ra_stream stream) {
   ra::clear_error();
-  ra_status st = check_paged(R, Hkv, block_size, interleave, pcp, dcp, max_vblocks, num_blocks);
-  if (st != RA_OK) return st;
-  if ((st = check_heads(T, R, Hq, Hkv, d, window, n_sink, out_dt)) != RA_OK) return st;
-  if (block_size % 16 != 0) return ra::fail(RA_ERR_UNSUPPORTED, "block_size must be a multiple of 16");
-  if (T == 0) return RA_OK;
-  RA_REQUIRE(q && k_cache && v_cache && block_table && query_start_loc && ctx_lens && o && workspace, "NULL pointer");
-  RA_REQUIRE(ra::aligned16(q) && ra::aligned16(k_cache) && ra::aligned16(v_cache) && ra::aligned16(o) &&
-                 ra::aligned16(workspace),
-             "q, the caches, o and workspace must be 16-byte aligned");
-  size_t need = 0;
-  if ((st = ra_cp_window_attn_workspace_size(Hq, Hkv, d, &need)) != RA_OK) return st;
-  RA_REQUIRE(ws_bytes >= need, "workspace too small (%zu < %zu bytes)", ws_bytes, need);
-  WindowArgs a = {};
-  a.c = make_paged(block_table, Hkv, block_size, interleave, pcp, dcp, max_vblocks, num_blocks);
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.k = static_cast<const __nv_bfloat16*>(k_cache);
-  a.v = static_cast<const __nv_bfloat16*>(v_cache);
-  a.q_rs = static_cast<int64_t>(Hq) * d;
-  a.qsl = query_start_loc; a.ctx = ctx_lens; a.T = T; a.R = R; a.Hq = Hq; a.Hkv = Hkv;
-  a.window = window; a.n_sink = n_sink; a.out_bf16 = out_dt == RA_BF16;
-  a.scale = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(d));
-  a.o = o; a.lse = lse;
-  if (d == 128) window_rows_kernel<128, true><<<row_blocks(T * Hq), kRowThreads, 0, stream>>>(a);
-  else window_rows_kernel<64, true><<<row_blocks(T * Hq), kRowThreads, 0, stream>>>(a);
-  RA_LAUNCH_CHECK("window_rows_kernel");
-  return RA_OK;
+  RA_REQUIRE(window >= 1 && n_sink >= 0, "window >= 1 and n_sink >= 0 required");
+  const ra_status st = check_chunk_paged(q, k_cache, v_cache, block_table, query_start_loc, ctx_lens, T, R, Hq, Hkv, d,
+                                         block_size, interleave, pcp, dcp, max_vblocks, num_blocks, o, out_dt, workspace,
+                                         ws_bytes, chunk_workspace<WindowPaged>(d));
+  if (st != RA_OK || T == 0) return st;
+  ChunkArgs a;
+  static_cast<KeyUnits&>(a) =
+      make_units(make_paged(block_table, Hkv, block_size, interleave, pcp, dcp, max_vblocks, num_blocks));
+  set_chunk_args(a, query_start_loc, ctx_lens, T, R, Hq, Hkv, d, scale, o, out_dt, lse, workspace);
+  a.window = std::min(window, kFar);
+  a.n_sink = std::min(n_sink, kFar);
+  return d == 128 ? launch_chunk_paged<128, WindowPaged>(q, k_cache, v_cache, a, stream)
+                  : launch_chunk_paged<64, WindowPaged>(q, k_cache, v_cache, a, stream);
 }
 
 extern "C" ra_status ra_window_attn_workspace_size(int64_t T, int32_t R, int32_t Hq, int32_t Hkv, int32_t d,
                                                    size_t* bytes) {
   ra::clear_error();
   RA_REQUIRE(bytes != nullptr, "bytes is NULL");
-  RA_REQUIRE(T >= 0 && R >= 1 && Hq >= 1 && Hkv >= 1 && d >= 1 && T < (int64_t(1) << 31) / Hq, "bad sizes");
-  *bytes = static_cast<size_t>(T * Hq * 8 + 256);
+  RA_REQUIRE(T >= 0 && R >= 1 && Hq >= 1 && Hkv >= 1 && d >= 1 && T < kFar && T < (int64_t(1) << 31) / Hq, "bad sizes");
+  *bytes = std::max(chunk_workspace<WindowPacked>(d), static_cast<size_t>(T * Hq * 8 + 256));
   return RA_OK;
 }
 
@@ -279,11 +244,21 @@ extern "C" ra_status ra_window_attn_fwd(const void* q, int64_t q_row_stride, con
   if (st != RA_OK) return st;
   if (T == 0) return RA_OK;
   RA_REQUIRE(o != nullptr && ra::aligned16(o), "o must be given and 16-byte aligned");
-  a.o = o; a.lse = lse;
-  if (d == 128) window_rows_kernel<128, false><<<row_blocks(T * Hq), kRowThreads, 0, stream>>>(a);
-  else window_rows_kernel<64, false><<<row_blocks(T * Hq), kRowThreads, 0, stream>>>(a);
-  RA_LAUNCH_CHECK("window_rows_kernel");
-  return RA_OK;
+  ChunkArgs c;
+  c.c = Paged{};
+  c.c.Hkv = Hkv;
+  c.lu = 7; c.lupt = 0; c.nsub = 1;
+  c.by_vbu = fast_div(1);
+  set_chunk_args(c, query_start_loc, nullptr, T, R, Hq, Hkv, d, scale, o, out_dt, lse, workspace);
+  c.window = std::min(window, kFar);
+  c.n_sink = std::min(n_sink, kFar);
+  CUtensorMap mq, mk, mv;
+  ra_status s;
+  if ((s = row_map(&mq, q, d, Hq, T, q_row_stride, c.G, c.tpt)) != RA_OK) return s;
+  if ((s = row_map(&mk, k, d, Hkv, T, k_row_stride, 1, BN)) != RA_OK) return s;
+  if ((s = row_map(&mv, v, d, Hkv, T, v_row_stride, 1, BN)) != RA_OK) return s;
+  return d == 128 ? launch_chunk<128, WindowPacked>(mq, mk, mv, c, stream)
+                  : launch_chunk<64, WindowPacked>(mq, mk, mv, c, stream);
 }
 
 extern "C" ra_status ra_window_attn_bwd(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride,

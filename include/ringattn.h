@@ -788,7 +788,8 @@ ra_status ra_cp_window_attn(const void* q, const void* k_cache, const void* v_ca
  * are not finite.
  * workspace   device scratch of ra_window_attn_workspace_size() bytes, 16-byte aligned, for
  *             either direction.  Calls that overlap on the GPU need one each.
- * Requires Hq % Hkv == 0, Hq/Hkv <= 64, d in {64, 128}, T*Hq < 2^31; q, k, v, o 16-byte aligned.
+ * Requires Hq % Hkv == 0, Hq/Hkv <= 64, d in {64, 128}, T < 2^30, T*Hq < 2^31; q, k, v, o 16-byte
+ * aligned.
  * Lengths are read on the device: a captured call may be replayed with others.
  * Device bounds error: a sequence whose range is decreasing or outside [0, T] (left out).
  * ---------------------------------------------------------------------- */
