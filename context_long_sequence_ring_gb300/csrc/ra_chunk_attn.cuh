@@ -48,10 +48,10 @@
 //
 // Forms.  The kernel is written once for the causal mask over the cache, for a
 // sliding window with first tokens that stay visible over the cache, and for the
-// latter on packed sequences, whose keys are rows of one tensor (a unit is then a
-// whole tile).  With a window an item's tiles are those that hold first tokens, if
-// they end before the window starts, and then those from the first that any of its rows sees;
-// tiles at the window's lower end are masked like those at the diagonal.
+// latter on packed sequences, whose keys are rows of one tensor (units of 32
+// rows).  With a window the units of an item are those that hold first tokens, if they end
+// before the window starts, and from there on those from the first that any of its rows sees;
+// its tiles are cut out of that row of units, so that few first tokens take up a unit, not a tile.
 #pragma once
 
 #include <algorithm>
@@ -94,26 +94,6 @@ struct ChunkArgs : KeyUnits {
   long long drain_limit;          // of the last wait for products in flight: not below 2^22 cycles
   int window, n_sink;             // at most 2^30
 };
-
-// Units that hold a token below lim, units all of whose tokens are, as prefixes of the units.
-template <class F>
-__device__ __forceinline__ int units_to(const ChunkArgs& a, int lim) {
-  if (F::kPacked) return lim <= 0 ? 0 : ((lim - 1) >> 7) + 1;
-  return units_below(a, lim);
-}
-template <class F>
-__device__ __forceinline__ int units_inside(const ChunkArgs& a, int lim) {
-  if (F::kPacked) return lim >> 7;
-  return units_within(a, lim);
-}
-template <class F>
-__device__ __forceinline__ int tiles_to(const ChunkArgs& a, int lim) {
-  return (units_to<F>(a, lim) + (1 << a.lupt) - 1) >> a.lupt;
-}
-template <class F>
-__device__ __forceinline__ int tiles_inside(const ChunkArgs& a, int lim) {
-  return units_inside<F>(a, lim) >> a.lupt;
-}
 
 // ------------------------------------------------------------------ work
 // A request as the work division sees it.
@@ -166,26 +146,38 @@ __device__ __forceinline__ int low_of(const ChunkArgs& a, const Req<F>& q, int i
   return lo < 0 ? 0 : (lo < q.L ? static_cast<int>(lo) : q.L);
 }
 
-// The tiles of an item: [0, first) hold first tokens, then from first + skip on.
-struct Tiles {
-  int all, first, skip;
+__device__ __forceinline__ int tiles_over(const ChunkArgs& a, int units) { return (units + (1 << a.lupt) - 1) >> a.lupt; }
+
+// The units of an item: unit j is j of the context where j < first, and `skip` units (packed: tokens) further from there on.
+struct Run {
+  int first, skip;
 };
+// Units of the run that hold a token below lim, and units all of whose tokens are below lim (both as prefixes; first
+// tokens' units left aside, which are before the window).
 template <class F>
-__device__ __forceinline__ Tiles tiles_of(const ChunkArgs& a, const Req<F>& q, int k) {
-  const int tpi = q.pair ? 2 * a.tpt : a.tpt;
-  const int lim = limit_of<F>(a, q, min(q.n, (k + 1) * tpi) - 1);
-  Tiles t;
-  t.all = tiles_to<F>(a, lim);
-  t.first = t.skip = 0;
+__device__ __forceinline__ int run_to(const ChunkArgs& a, const Run& u, int lim) {
+  if (F::kPacked) return (max(lim - u.skip, 0) + 31) >> 5;
+  return units_below(a, lim) - u.skip;
+}
+template <class F>
+__device__ __forceinline__ int run_inside(const ChunkArgs& a, const Run& u, int lim) {
+  if (F::kPacked) return max(lim - u.skip, 0) >> 5;
+  return units_within(a, lim) - u.skip;
+}
+template <class F>
+__device__ __forceinline__ Run run_of(const ChunkArgs& a, const Req<F>& q, int k, int lim) {
+  Run u{0, 0};
   if (F::kWindow) {
-    const int low = tiles_inside<F>(a, low_of<F>(a, q, k * tpi)), first = tiles_to<F>(a, min(a.n_sink, lim));
-    if (low > first) {   // else one run of tiles
-      t.first = first;
-      t.skip = min(low, t.all) - first;
-      t.all -= t.skip;
+    const int low = low_of<F>(a, q, k * (q.pair ? 2 * a.tpt : a.tpt)), sinks = min(a.n_sink, lim);
+    if (F::kPacked) {
+      const int first = (sinks + 31) >> 5;
+      if (low >= 32 * first) u = Run{first, low - 32 * first};
+    } else {
+      const int first = units_below(a, sinks), start = units_within(a, min(low, lim));
+      if (start >= first) u = Run{first, start - first};
     }
   }
-  return t;
+  return u;
 }
 
 // f(request) for all requests in order, each lane those at lane, lane + 32, ...; four loads in flight where there
@@ -280,15 +272,13 @@ struct Segment {
   int dirty, clean0, clean1; // first tile (of this segment) with slots past the context; first tile of the item
                              // that rows of slot 0 / 1 see a part of only
   int pair;                  // 1 pair, 0 split, -1 end of the part
-  __device__ __forceinline__ int tile(int j) const { return t0 + j; }
 };
 
-// With a window: t0 and nt count the item's tiles (struct Tiles), clean0 and clean1 are tiles of the context.
+// With a window: t0 and nt count the item's tiles, and so do clean0 and clean1, low0 and low1.
 struct WindowSegment : Segment {
-  int first, skip, sinks;    // sinks: tiles that hold first tokens
-  int low, border;           // first position of the item's windows; first tile without a token below it
-  int low0, low1;            // first tile whose tokens all rows of slot 0 / 1 have in their windows, as far as they go down
-  __device__ __forceinline__ int tile(int j) const { return t0 + j + (t0 + j < first ? 0 : skip); }
+  Run run;
+  int low, border;           // first position of the item's windows; first unit of the context without a token below it
+  int low0, low1;            // first tile from which the rows of slot 0 / 1 see all of a tile, as far as it goes down
 };
 
 template <class F>
@@ -349,30 +339,26 @@ struct SegIter {
       fresh = false;
       if (!live || at >= hi) return false;
       cost = plan.cost(q, k);
-      const Tiles tiles = tiles_of<F>(a, q, k);
-      s.all = tiles.all;
+      const int per = q.pair ? 2 * a.tpt : a.tpt, lim = limit_of<F>(a, q, min(q.n, (k + 1) * per) - 1);
+      const Run run = run_of<F>(a, q, k, lim);
+      s.all = tiles_over(a, run_to<F>(a, run, lim));
       int t1;
       cut(lo, hi, at, plan.over(q), cost, s.all, s.t0, t1);
       if (s.all == 0 ? lo > at : t1 <= s.t0) continue;
       s.r = r; s.g = g; s.q0 = q.q0; s.n = q.n; s.L = q.L;
       s.pos0 = static_cast<int>(q.pos0 < -q.n ? -q.n : q.pos0);   // below -n: nothing is visible either way
       s.pair = q.pair;
-      s.tok0 = k * (q.pair ? 2 * a.tpt : a.tpt);
+      s.tok0 = k * per;
       s.nt = t1 - s.t0;
-      const int dirty = tiles_inside<F>(a, q.L);
-      s.clean0 = tiles_inside<F>(a, limit_of<F>(a, q, s.tok0));
-      s.clean1 = q.pair ? tiles_inside<F>(a, limit_of<F>(a, q, min(s.tok0 + a.tpt, q.n - 1))) : s.clean0;
+      s.dirty = (run_inside<F>(a, run, q.L) >> a.lupt) - s.t0;
+      s.clean0 = run_inside<F>(a, run, limit_of<F>(a, q, s.tok0)) >> a.lupt;
+      s.clean1 = q.pair ? run_inside<F>(a, run, limit_of<F>(a, q, min(s.tok0 + a.tpt, q.n - 1))) >> a.lupt : s.clean0;
       if constexpr (F::kWindow) {
-        s.first = tiles.first;
-        s.skip = tiles.skip;
-        s.sinks = tiles_to<F>(a, min(a.n_sink, q.L));
-        s.dirty = (dirty <= s.first ? dirty : max(s.first, dirty - s.skip)) - s.t0;
+        s.run = run;
         s.low = low_of<F>(a, q, s.tok0);
-        s.border = tiles_to<F>(a, s.low);
-        s.low0 = tiles_to<F>(a, low_of<F>(a, q, min(s.tok0 + a.tpt, q.n) - 1));
-        s.low1 = q.pair ? tiles_to<F>(a, low_of<F>(a, q, min(s.tok0 + 2 * a.tpt, q.n) - 1)) : s.low0;
-      } else {
-        s.dirty = dirty - s.t0;
+        s.border = F::kPacked ? 0 : units_below(a, s.low);
+        s.low0 = tiles_over(a, run_to<F>(a, run, low_of<F>(a, q, min(s.tok0 + a.tpt, q.n) - 1)));
+        s.low1 = q.pair ? tiles_over(a, run_to<F>(a, run, low_of<F>(a, q, min(s.tok0 + 2 * a.tpt, q.n) - 1))) : s.low0;
       }
       return true;
     }
@@ -415,26 +401,55 @@ struct BitMask {
       if (!(f >> i & 1)) x[i] = __float_as_uint(-CUDART_INF_F);
   }
 };
-// Positions below `lim` and not below `low`, or below `sink`, by their prefixes of each 16 columns.
-struct WindowMask : BitMask {
-  uint64_t lim, low, sink;
-  __device__ static __forceinline__ uint32_t bits(uint64_t p, int c) {
-    const uint32_t f = static_cast<uint32_t>(p >> (16 * c));
-    return ((1u << (f & 255)) - 1) | ((1u << (f >> 8 & 255)) - 1) << 16;
-  }
-  __device__ __forceinline__ uint32_t part(int c) const { return (bits(lim, c) & ~bits(low, c)) | bits(sink, c); }
-};
-// The same where columns are positions: limits relative to the tile.
-struct PackedMask : BitMask {
-  int lim, low, sink;
-  __device__ static __forceinline__ uint32_t bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
-  __device__ __forceinline__ uint32_t part(int c) const {
-    return (bits(lim - 32 * c) & ~bits(low - 32 * c)) | bits(sink - 32 * c);
-  }
-};
-template <class F>
-using MaskOf = std::conditional_t<!F::kWindow, PrefixMask, std::conditional_t<F::kPacked, PackedMask, WindowMask>>;
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
 
+// Positions below `lim` and not below `low`, or below `sink`.  Packed: column i of unit j is position 32 j + i, `skip`
+// further from unit `first` on.
+struct PackedMask : BitMask {
+  Run run;
+  int lim, low, sink, unit;      // unit: first of the tile
+  __device__ __forceinline__ uint32_t part(int c) const {
+    const int j = unit + c, at = 32 * j + (j < run.first ? 0 : run.skip);
+    return (low_bits(lim - at) & ~low_bits(low - at)) | low_bits(sink - at);
+  }
+};
+// A position's place: its virtual block, and there the slots before it on device w: `full`, and I more on the devices
+// below `w`, `rem` more on w itself.
+struct Place {
+  int vb, full, w, rem;
+  __device__ __forceinline__ void set(const KeyUnits& a, int x) {
+    int o, r;
+    vb = a.c.by_V.div(x, o);
+    full = a.c.by_WI.div(o, r) * a.c.I;
+    w = a.c.by_I.div(r, rem);
+  }
+  // slots of unit (vb, sub, w) that hold tokens before it: unit_visible() without divisions
+  __device__ __forceinline__ int before(const KeyUnits& a, int v, int sub, int dev) const {
+    if (v != vb) return v < vb ? 1 << a.lu : 0;
+    return full + (dev < w ? a.c.I : dev == w ? rem : 0) - (sub << a.lu);
+  }
+};
+struct WindowMask : BitMask {
+  const ChunkArgs& a;
+  const Place &lim, &low, &sink;
+  Run run;
+  int unit, r;
+  bool bad;
+  __device__ __forceinline__ uint32_t one(int j) const {
+    int rem, w;
+    const int vb = a.by_vbu.div(j + (j < run.first ? 0 : run.skip), rem), sub = a.c.by_W.div(rem, w);
+    const uint32_t all = low_bits(1 << a.lu);
+    const uint32_t m = (low_bits(lim.before(a, vb, sub, w)) & ~low_bits(low.before(a, vb, sub, w))) |
+                       low_bits(sink.before(a, vb, sub, w));
+    if (!bad || m == 0) return m & all;
+    const int32_t b = vb < a.c.max_vb ? a.c.table[static_cast<int64_t>(r) * a.c.max_vb + vb] : -1;
+    return b < 0 || b >= a.c.num_blocks ? 0 : m & all;
+  }
+  __device__ __forceinline__ uint32_t part(int c) const {
+    if (a.lu == 5) return one(unit + c);
+    return one(unit + 2 * c) | one(unit + 2 * c + 1) << 16;
+  }
+};
 template <class Mask>
 __device__ __forceinline__ float softmax_step(uint32_t s_addr, bool first, bool masked, bool row_ok, const Mask& mask,
                                               float scale, float& m, float& l) {
@@ -693,21 +708,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // load is in flight while the ring is waited for
       auto locate = [&](int j) {
         Unit x;
-        if (F::kPacked) {
-          x.s0 = sg.q0 + BN * sg.tile(j);
-          x.w = x.blk = 0;
-          return x;
+        int j_unit = ((sg.t0 + j) << a.lupt) + unit;
+        bool first = false;   // first tokens
+        if constexpr (F::kWindow) {
+          first = j_unit < sg.run.first;
+          if (F::kPacked) {
+            x.s0 = sg.q0 + 32 * j_unit + (first ? 0 : sg.run.skip);
+            x.w = x.blk = 0;
+            return x;
+          }
+          if (!first) j_unit += sg.run.skip;
         }
         int rem;
-        const int tile = sg.tile(j);
-        const int vb = a.by_vbu.div((tile << a.lupt) + unit, rem);
+        const int vb = a.by_vbu.div(j_unit, rem);
         const int sub = a.c.by_W.div(rem, x.w);
         x.s0 = sub << a.lu;
         x.blk = -1;
         bool sees = j < nt && used && static_cast<int64_t>(vb) * a.c.V < sg.L;
         // a unit none of whose tokens is in sight is not looked at: its block may be gone
         if constexpr (F::kWindow)
-          if (sees && tile < sg.border)
+          if (sees && (first || j_unit < sg.border))
             sees = unit_visible(a, vb, sub, x.w, a.n_sink) > 0 || unit_visible(a, vb, sub, x.w, sg.low) < (1 << a.lu);
         if (sees) {
           x.blk = a.c.table[static_cast<int64_t>(sg.r) * a.c.max_vb + vb];
@@ -949,12 +969,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (!(ok = warp_wait(smem_u32(&sm.v_dirty[ring.st]), (dirty_ph >> ring.st) & 1, abort_flag, lim, 540))) break;
           dirty_ph ^= 1u << ring.st;
           if (!(ok = warp_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 541))) break;
-          const uint64_t lm = F::kPacked ? 0 : tile_limits(a, sg.r, false, sg.tile(j), sg.L);
-          const int left = sg.L - BN * sg.tile(j);   // rows of the sequence in this tile
+          const uint64_t lm = F::kWindow ? 0 : tile_limits(a, sg.r, false, sg.t0 + j, sg.L);
 #pragma unroll 1
           for (int i0 = 0; i0 < BN; i0 += 32) {
             const int i = i0 + lane;
-            if (F::kPacked ? i >= left : (lane & 15) >= (static_cast<int>(lm >> (8 * (i >> 4))) & 255)) {
+            bool dead = (lane & 15) >= (static_cast<int>(lm >> (8 * (i >> 4))) & 255);
+            if constexpr (F::kWindow) {
+              const int j_unit = ((sg.t0 + j) << a.lupt) + (i >> a.lu), shift = j_unit < sg.run.first ? 0 : sg.run.skip;
+              if (F::kPacked) {
+                dead = 32 * j_unit + (i & 31) + shift >= sg.L;
+              } else {
+                int rem, w;
+                const int vb = a.by_vbu.div(j_unit + shift, rem), sub = a.c.by_W.div(rem, w);
+                dead = (i & ((1 << a.lu) - 1)) >= unit_visible(a, vb, sub, w, sg.L);
+              }
+            }
+            if (dead) {
 #pragma unroll
               for (int s = 0; s < SLABS; ++s)
 #pragma unroll
@@ -1032,6 +1062,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int seen = sg.pos0 + min(tok, sg.n - 1) + 1;
       const int vis = F::kWindow || a.causal ? max(0, min(sg.L, seen)) : sg.L;
       const int clean = h ? sg.clean1 : sg.clean0;
+      // with a window: its first position, the first tokens that are there, and tiles below which it is masked
+      int low = 0, low_tile = 0;
+      [[maybe_unused]] const int sinks = F::kWindow ? min(a.n_sink, vis) : 0;
+      [[maybe_unused]] Place lim_place, low_place, sink_place;
+      if constexpr (F::kWindow) {
+        low = seen > a.window ? min(sg.L, seen - a.window) : 0;
+        low_tile = h ? sg.low1 : sg.low0;
+        if constexpr (!F::kPacked) {
+          lim_place.set(a, vis);
+          low_place.set(a, low);
+          sink_place.set(a, sinks);
+        }
+      }
       const bool warp_live = __any_sync(0xffffffffu, row_ok);
       float m = -CUDART_INF_F, l = 0.f;
       const int step = pair ? 1 : 2;
@@ -1045,24 +1088,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t colS = (NB == 3 ? b : h) * BN;
         if (warp_live) {
           const bool bad = *reinterpret_cast<volatile int*>(&sm.bad_block) != 0;
-          const int tile = sg.tile(j);
-          bool masked = tile >= clean || bad;
-          MaskOf<F> mask;
-          if constexpr (F::kWindow) {
-            masked = masked || tile < (h ? sg.low1 : sg.low0);
-            const int low = seen > a.window ? min(sg.L, seen - a.window) : 0;
-            if constexpr (F::kPacked) {
-              const int at = BN * tile;
-              mask.lim = vis - at; mask.low = low - at; mask.sink = min(a.n_sink, vis) - at;
-            } else if (masked) {
-              mask.lim = tile_limits(a, sg.r, bad, tile, vis);
-              mask.low = tile < (h ? sg.low1 : sg.low0) ? tile_limits(a, sg.r, false, tile, low) : 0;
-              // first tokens below the window: above it all of the window is in sight already
-              mask.sink = tile < sg.sinks ? tile_limits(a, sg.r, bad, tile, min(a.n_sink, vis)) : 0;
-            }
-          } else {
-            mask.lm = masked ? tile_limits(a, sg.r, bad, tile, vis) : 0;
-          }
+          const int tile = sg.t0 + j;
+          const bool masked = tile >= clean || bad || (F::kWindow && tile < low_tile);
+          auto mask = [&] {
+            if constexpr (!F::kWindow) return PrefixMask{masked ? tile_limits(a, sg.r, bad, tile, vis) : 0};
+            else if constexpr (F::kPacked) return PackedMask{{}, sg.run, vis, low, sinks, tile << a.lupt};
+            else return WindowMask{{}, a, lim_place, low_place, sink_place, sg.run, tile << a.lupt, sg.r, bad};
+          }();
           const float alpha = softmax_step(t_lane + colS, n_mine == 0, masked, row_ok, mask, a.scale_log2, m, l);
           if (n_mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
             // O_h must hold the previous P.V before it is rescaled

@@ -81,8 +81,8 @@ struct WindowItems {
     items = n_items;
     pair = n > tpt;
     const int f = pair ? kPairCost : rt.f_split, over = pair ? rt.over_pair : rt.over_split, tpi = (pair ? 2 : 1) * tpt;
-    // half a tile past either end of the window, and a tile of first tokens
-    const long long most = static_cast<long long>(window) + tpi + 128 + (n_sink + 127ll) / 128 * 128;
+    // half a tile past either end of the window, and the units of first tokens
+    const long long most = static_cast<long long>(window) + tpi + 128 + (n_sink + 31ll) / 32 * 32;
     const long long cap = most < L ? most : L, before = pos0 < 0 ? 0 : (pos0 < cap ? pos0 : cap);
     const long long steps = (cap - before) / tpi;
     full = static_cast<int>(steps < n_items ? steps : n_items);

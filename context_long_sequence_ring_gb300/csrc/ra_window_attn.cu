@@ -247,7 +247,7 @@ extern "C" ra_status ra_window_attn_fwd(const void* q, int64_t q_row_stride, con
   ChunkArgs c;
   c.c = Paged{};
   c.c.Hkv = Hkv;
-  c.lu = 7; c.lupt = 0; c.nsub = 1;
+  c.lu = 5; c.lupt = 2; c.nsub = 1;
   c.by_vbu = fast_div(1);
   set_chunk_args(c, query_start_loc, nullptr, T, R, Hq, Hkv, d, scale, o, out_dt, lse, workspace);
   c.window = std::min(window, kFar);
@@ -255,8 +255,8 @@ extern "C" ra_status ra_window_attn_fwd(const void* q, int64_t q_row_stride, con
   CUtensorMap mq, mk, mv;
   ra_status s;
   if ((s = row_map(&mq, q, d, Hq, T, q_row_stride, c.G, c.tpt)) != RA_OK) return s;
-  if ((s = row_map(&mk, k, d, Hkv, T, k_row_stride, 1, BN)) != RA_OK) return s;
-  if ((s = row_map(&mv, v, d, Hkv, T, v_row_stride, 1, BN)) != RA_OK) return s;
+  if ((s = row_map(&mk, k, d, Hkv, T, k_row_stride, 1, 32)) != RA_OK) return s;
+  if ((s = row_map(&mv, v, d, Hkv, T, v_row_stride, 1, 32)) != RA_OK) return s;
   return d == 128 ? launch_chunk<128, WindowPacked>(mq, mk, mv, c, stream)
                   : launch_chunk<64, WindowPacked>(mq, mk, mv, c, stream);
 }
