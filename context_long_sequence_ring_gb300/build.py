@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libringattn.so")
 
 SOURCES = ["ra_api.cu", "ra_cache.cu", "ra_decode.cu", "ra_attn_f32.cu", "ra_attn_bf16.cu", "ra_attn_block.cu",
            "ra_rope.cu", "ra_ring_step.cu", "ra_rope_apply.cu", "ra_chunk_attn.cu", "ra_attn_weights.cu", "ra_evict.cu",
-           "ra_rope_append.cu", "ra_window_attn.cu"]
+           "ra_rope_append.cu", "ra_window_attn.cu", "ra_window_grad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

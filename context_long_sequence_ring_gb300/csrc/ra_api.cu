@@ -48,10 +48,11 @@ extern "C" ra_status ra_device_status(ra_stream stream) {
                           ra::fetch_error_attn_f32, ra::fetch_error_attn_bf16, ra::fetch_error_attn_block,
                           ra::fetch_error_rope, ra::fetch_error_ring_step, ra::fetch_error_rope_apply,
                           ra::fetch_error_chunk_attn, ra::fetch_error_attn_weights, ra::fetch_error_evict,
-                          ra::fetch_error_rope_append, ra::fetch_error_window_attn};
+                          ra::fetch_error_rope_append, ra::fetch_error_window_attn, ra::fetch_error_window_grad};
   const char* names[] = {"partition/gather", "kv cache", "decode/merge", "attention fp32",
                          "ring attention bf16", "block attention bf16", "rope gather", "ring step", "rope apply",
-                         "chunk attention", "attention weights", "cache eviction", "rope append", "window attention"};
+                         "chunk attention", "attention weights", "cache eviction", "rope append", "window attention",
+                         "window attention gradient"};
   static_assert(sizeof(fetch) / sizeof(fetch[0]) == sizeof(names) / sizeof(names[0]),
                 "one name per module error word");
   ra_status first = RA_OK;

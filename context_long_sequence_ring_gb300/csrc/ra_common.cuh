@@ -36,6 +36,7 @@ int fetch_error_attn_weights(int* where);
 int fetch_error_evict(int* where);
 int fetch_error_rope_append(int* where);
 int fetch_error_window_attn(int* where);
+int fetch_error_window_grad(int* where);
 
 }  // namespace ra
 

@@ -1,0 +1,60 @@
+// Shared host pieces of the window attention on packed sequences, forward and backward.
+#pragma once
+
+#include <algorithm>
+
+#include "ra_attn_tc.cuh"
+#include "ra_paged.cuh"
+
+namespace {
+
+constexpr int kFar = 1 << 30;    // no position is further: contexts and sequences are shorter
+
+// The map of [rows, heads, D] rows `stride` elements apart: boxes of 64 columns, box_heads heads, box_rows rows.
+inline ra_status row_map(CUtensorMap* map, const void* base, int D, int heads, int64_t rows, int64_t stride,
+                         uint32_t box_heads, uint32_t box_rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return RA_OK;
+}
+
+// What both directions require of their arguments.
+inline ra_status check_packed(const void* q, int64_t q_rs, const void* k, int64_t k_rs, const void* v, int64_t v_rs,
+                              const int32_t* qsl, int64_t T, int32_t R, int32_t Hq, int32_t Hkv, int32_t d, int32_t window,
+                              int32_t n_sink, ra_dtype out_dt, const void* workspace, size_t ws_bytes) {
+  RA_REQUIRE(out_dt == RA_F32 || out_dt == RA_BF16, "unknown out dtype");
+  RA_REQUIRE(R >= 1 && Hkv >= 1 && Hq >= 1 && Hq % Hkv == 0, "R >= 1 and Hq (%d) a multiple of Hkv (%d) required", Hq, Hkv);
+  RA_REQUIRE(T >= 0 && T < kFar && T < (int64_t(1) << 31) / Hq, "T must be in [0, 2^30), T*Hq below 2^31");
+  RA_REQUIRE(window >= 1 && n_sink >= 0, "window >= 1 and n_sink >= 0 required");
+  if (d != 64 && d != 128) return ra::fail(RA_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", d);
+  if (Hq / Hkv > 64) return ra::fail(RA_ERR_UNSUPPORTED, "GQA group %d > 64 not supported", Hq / Hkv);
+  const int64_t lim = int64_t(1) << 31;
+  RA_REQUIRE(q_rs >= static_cast<int64_t>(Hq) * d && k_rs >= static_cast<int64_t>(Hkv) * d &&
+                 v_rs >= static_cast<int64_t>(Hkv) * d && q_rs < lim && k_rs < lim && v_rs < lim,
+             "row strides must be at least heads * d, below 2^31");
+  RA_REQUIRE(q_rs % 8 == 0 && k_rs % 8 == 0 && v_rs % 8 == 0, "row strides must be multiples of 8 elements");
+  if (T == 0) return RA_OK;
+  RA_REQUIRE(q && k && v && qsl && workspace, "NULL pointer");
+  RA_REQUIRE(ra::aligned16(q) && ra::aligned16(k) && ra::aligned16(v) && ra::aligned16(workspace),
+             "q, k, v and workspace must be 16-byte aligned");
+  size_t need = 0;
+  const ra_status st = ra_window_attn_workspace_size(T, R, Hq, Hkv, d, &need);
+  if (st != RA_OK) return st;
+  RA_REQUIRE(ws_bytes >= need, "workspace too small (%zu < %zu bytes)", ws_bytes, need);
+  return RA_OK;
+}
+
+}  // namespace
+
+namespace ra {
+size_t window_forward_workspace(int d);                                              // in ra_window_attn.cu
+size_t window_backward_workspace(int64_t T, int32_t R, int32_t Hq, int32_t Hkv, int32_t d);   // in ra_window_grad.cu
+}  // namespace ra
