@@ -201,6 +201,24 @@ __device__ __forceinline__ float softmax_row(uint32_t s_addr, int j, bool masked
   return (j == 0) ? 1.f : alpha;
 }
 
+// ------------------------------------------------------------------ pipeline pieces
+// mbar_wait by a whole warp with one outcome for all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit, int site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit, site));
+}
+
+template <int NS>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ void advance() {
+    if (++st == NS) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
 // ------------------------------------------------------------------ host side
 using EncodeTiledFn = decltype(&cuTensorMapEncodeTiled);
 

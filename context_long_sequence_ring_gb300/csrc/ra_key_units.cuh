@@ -113,39 +113,6 @@ __device__ __forceinline__ void tma_load_3d_once(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-// mbar_wait by a whole warp with one outcome for all lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit, int site) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit, site));
-}
-
-template <int NS>
-struct Ring {
-  int st = 0;
-  uint32_t ph = 0;
-  __device__ void advance() {
-    if (++st == NS) {
-      st = 0;
-      ph ^= 1;
-    }
-  }
-};
-
 // ------------------------------------------------------------------ host side
 // Three-dimensional bf16 map with 64-column boxes in the 128-byte swizzle the MMA descriptors expect.
 inline ra_status box_map(CUtensorMap* map, const void* base, int D, int64_t n1, int64_t n2, uint32_t box1, uint32_t box2) {

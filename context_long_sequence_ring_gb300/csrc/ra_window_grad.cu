@@ -16,8 +16,15 @@
 //             S^T = K Q^T, dP^T = V dO^T; P^T and dS^T (bf16) over them are operands from tensor memory of
 //             dV += P^T dO and dK += dS^T Q.
 //   join      sums the parts of key tiles that several CTAs share.
-// A thread holds half a row of a score tile; 256 threads of softmax, one of products, a warp of loads and one
-// that zeroes rows past a sequence's end (0 * NaN).
+// 16 warps of softmax, a thread holding 32 columns of a row of a score tile: tensor memory has room for one tile of
+// each kind only, so that the chain of a tile (scores, exponentials, next product) sets the pace, and
+// 8 warps with 64 columns each took 1.5 times as long for it.  One thread issues the products, a warp the loads, and one
+// zeroes rows past a sequence's end (0 * NaN).
+//
+// Rounding.  P and dS are rounded to bf16, the type of the other operand.  delta is formed from an o that has been rounded,
+// whose error all keys of a row share: dS sums to 0 over a row, so the dQ kernel's row sums of dS in fp32 are that error, and
+// dK gets the delta without it.  In dQ itself it counts where a row sees few keys; there dS is split into two bf16
+// parts (an error of 2^-17 instead of 2^-9), which leaves the place for it.
 //
 // Work of dK, dV.  Tiles in rounds of one whole tile per CTA, neighbours at the same time, so that the queries they share
 // are in L2; the last one or two rounds, and the tiles of first tokens that all later queries see, are laid on one axis
@@ -31,7 +38,10 @@ RA_DEFINE_ERROR_FETCH(fetch_error_window_grad)
 namespace {
 
 constexpr int kGradCtas = 152;         // one CTA per SM of a GB300
-constexpr int kGradThreads = 384;
+constexpr int kGroups = 4;             // softmax warpgroups, 32 columns each
+constexpr int kSoftmax = 128 * kGroups;
+constexpr int kGradThreads = 128 + kSoftmax;
+constexpr int kFewTiles = 2;           // row tiles of so many key tiles or fewer have dS in two parts
 constexpr int kPlanThreads = 1024;
 constexpr int kOver = 4;               // start and end of a key tile, in query tiles
 
@@ -299,22 +309,6 @@ __global__ void __launch_bounds__(kPlanThreads) grad_prepare_kernel(const __grid
 }
 
 // ------------------------------------------------------------------ pieces of both kernels
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit, int site) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit, site));
-}
-
-template <int NS>
-struct Ring {
-  int st = 0;
-  uint32_t ph = 0;
-  __device__ void advance() {
-    if (++st == NS) {
-      st = 0;
-      ph ^= 1;
-    }
-  }
-};
-
 // p = 2^(s * scale + nl) of a pair of columns.
 __device__ __forceinline__ void exp_pair(uint32_t s0, uint32_t s1, uint64_t sc2, uint64_t nl2, float& p0, float& p1) {
   float t0, t1;
@@ -377,12 +371,14 @@ struct __align__(1024) RowSmem {
   static constexpr int KS = D == 128 ? 3 : 6, VS = D == 128 ? 2 : 4;
   uint8_t q[BM * D * 2], d_o[BM * D * 2], k[KS][BN * D * 2], v[VS][BN * D * 2];
   uint64_t q_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], k_dirty[KS], k_clean[KS];
-  uint64_t s_full[2], dp_full, dp_free, ds_full[2], acc_full, acc_empty, drain;
+  uint64_t s_full[2], dp_full, dp_free, ds_full[2], acc_full, acc_empty, sums_full, sums_free, drain;
+  float sums[kGroups - 1][BM];
   uint32_t tmem_base;
   int abort_flag;
 };
 
-// Tensor memory: dQ, then two score tiles (dS of each half over its own columns), then dP.
+// Tensor memory: dQ, then two score tiles (dS of each 32 columns over the first half of them, what its rounding leaves
+// over the second), then dP.
 template <int D>
 __global__ void __launch_bounds__(kGradThreads, 1)
     grad_q_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -420,12 +416,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sm.s_full[b]), 1);
-      mbar_init(smem_u32(&sm.ds_full[b]), 256);
+      mbar_init(smem_u32(&sm.ds_full[b]), kSoftmax);
     }
     mbar_init(smem_u32(&sm.dp_full), 1);
-    mbar_init(smem_u32(&sm.dp_free), 256);
+    mbar_init(smem_u32(&sm.dp_free), kSoftmax);
+    mbar_init(smem_u32(&sm.sums_full), kSoftmax - 128);
+    mbar_init(smem_u32(&sm.sums_free), 128);
     mbar_init(smem_u32(&sm.acc_full), 1);
-    mbar_init(smem_u32(&sm.acc_empty), 256);
+    mbar_init(smem_u32(&sm.acc_empty), kSoftmax);
     mbar_init(smem_u32(&sm.drain), 1);
     sm.abort_flag = 0;
     fence_barrier_init();
@@ -580,8 +578,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
-            mma_bf16_ts(tmem, tmem + kColS + (at & 1) * BN + (kk >> 2) * 64 + (kk & 3) * 8,
+            mma_bf16_ts(tmem, tmem + kColS + (at & 1) * BN + (kk >> 1) * 32 + (kk & 1) * 8,
                         dkt + kd.st * (kTileBytes >> 4) + ((kk * 16 * 128) >> 4), kIdescQ, (kk > 0 || j > 0) ? 1u : 0u);
+          if (it.nt <= kFewTiles)
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              mma_bf16_ts(tmem, tmem + kColS + (at & 1) * BN + 16 + (kk >> 1) * 32 + (kk & 1) * 8,
+                          dkt + kd.st * (kTileBytes >> 4) + ((kk * 16 * 128) >> 4), kIdescQ, 1u);
           mma_commit(smem_u32(&sm.k_empty[kd.st]));
           kd.advance();
           if (j + 2 < it.nt && !(ok = issue_s(j + 2))) break;
@@ -624,7 +627,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
     }
   } else if (warp >= 4) {
-    // ============================================================ dS and epilogue: rows by lane, half the columns
+    // ============================================================ dS and epilogue: rows by lane, 32 columns of a tile
     const int h = (warp - 4) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -640,58 +643,76 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       const float nl = row_ok ? a.neg_lse[at] : -CUDART_INF_F, nd = row_ok ? a.neg_delta[at] : 0.f;
       const uint64_t nl2 = f2pack(nl, nl), nd2 = f2pack(nd, nd);
       const int p = row_ok ? pos : -1, low = max(0, p + 1 - a.window), sinks = min(a.n_sink, p + 1);
+      uint64_t sum2 = f2pack(0.f, 0.f);
       for (int j = 0; j < it.nt; ++j) {
         const uint32_t b = s_n & 1;
         if (!(ok = warp_wait(smem_u32(&sm.s_full[b]), (s_n >> 1) & 1, abort_flag, lim, 940))) break;
         if (!(ok = warp_wait(smem_u32(&sm.dp_full), s_n & 1, abort_flag, lim, 941))) break;
         ++s_n;
         tc_fence_after();
-        const uint32_t s_addr = t_lane + kColS + b * BN + 64 * h, p_addr = t_lane + kColP + 64 * h;
-        const bool masked = j < it.low0 || j >= it.clean;
-        uint32_t x[2][32], y[2][32];
-        tmem_ld32(s_addr, x[0]);
-        tmem_ld32(p_addr, y[0]);
-        tmem_ld32(s_addr + 32, x[1]);
-        tmem_ld32(p_addr + 32, y[1]);
+        const uint32_t s_addr = t_lane + kColS + b * BN + 32 * h;
+        uint32_t x[32], y[32], pk[16];
+        tmem_ld32(s_addr, x);
+        tmem_ld32(t_lane + kColP + 32 * h, y);
         tmem_wait_ld();
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.dp_free));
-        uint32_t pk[32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t f = 0xffffffffu;
-          if (masked) {
-            const int u = 4 * j + 2 * h + c, from = 32 * u + (u < it.first ? 0 : it.skip);
-            f = (low_bits(p + 1 - from) & ~low_bits(low - from)) | low_bits(sinks - from);
-          }
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float p0, p1, d0, d1;
-            exp_pair(x[c][i], x[c][i + 1], sc2, nl2, p0, p1);
-            f2unpack(fmul2(fadd2(f2pack(__uint_as_float(y[c][i]), __uint_as_float(y[c][i + 1])), nd2), f2pack(p0, p1)), d0, d1);
-            if (masked) {
-              d0 = f >> i & 1 ? d0 : 0.f;
-              d1 = f >> (i + 1) & 1 ? d1 : 0.f;
-            }
-            pk[16 * c + i / 2] = f2_bf16x2(d0, d1);
-          }
+        for (int i = 0; i < 32; i += 2) {
+          float p0, p1, d0, d1;
+          exp_pair(x[i], x[i + 1], sc2, nl2, p0, p1);
+          f2unpack(fmul2(fadd2(f2pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), nd2), f2pack(p0, p1)), d0, d1);
+          y[i] = __float_as_uint(d0);
+          y[i + 1] = __float_as_uint(d1);
         }
-        tmem_st32(s_addr, pk);
+        if (j < it.low0 || j >= it.clean) {                            // not all of the tile is seen by all rows
+          const int u = 4 * j + h, from = 32 * u + (u < it.first ? 0 : it.skip);
+          const uint32_t f = (low_bits(p + 1 - from) & ~low_bits(low - from)) | low_bits(sinks - from);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(f >> i & 1)) y[i] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          sum2 = fadd2(sum2, f2pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1])));
+          pk[i / 2] = f2_bf16x2(__uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+        }
+        tmem_st16(s_addr, pk);
+        if (it.nt <= kFewTiles) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            pk[i / 2] = f2_bf16x2(__uint_as_float(y[i]) - __uint_as_float(pk[i / 2] << 16),
+                                  __uint_as_float(y[i + 1]) - __uint_as_float(pk[i / 2] & 0xffff0000u));
+          tmem_st16(s_addr + 16, pk);
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.ds_full[b]));
       }
       if (!ok) break;
+      // the row's sum of dS is the error of its delta
+      float s0, s1;
+      f2unpack(sum2, s0, s1);
+      if (h > 0) {
+        if (!(ok = warp_wait(smem_u32(&sm.sums_free), (done & 1) ^ 1, abort_flag, lim, 943))) break;
+        sm.sums[h - 1][row] = s0 + s1;
+        mbar_arrive(smem_u32(&sm.sums_full));
+      } else {
+        if (!(ok = warp_wait(smem_u32(&sm.sums_full), done & 1, abort_flag, lim, 944))) break;
+        float sum = s0 + s1;
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g) sum += sm.sums[g - 1][row];
+        mbar_arrive(smem_u32(&sm.sums_free));
+        if (row_ok) a.neg_delta[at] = nd - sum;
+      }
       if (!(ok = warp_wait(smem_u32(&sm.acc_full), done & 1, abort_flag, lim, 942))) break;
       ++done;
       tc_fence_after();
-      const int64_t out = (it.q0 + static_cast<int64_t>(pos)) * a.dq_rs + head * D + h * (D / 2);
-#pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
+      if (h < D / 32) {
         uint32_t z[32];
-        tmem_ld32(t_lane + h * (D / 2) + 32 * c, z);
+        tmem_ld32(t_lane + 32 * h, z);
         tmem_wait_ld();
-        if (row_ok) store_cols(a.dq, a.out_bf16, out + 32 * c, z, a.scale);
+        if (row_ok) store_cols(a.dq, a.out_bf16, (it.q0 + static_cast<int64_t>(pos)) * a.dq_rs + head * D + 32 * h, z, a.scale);
       }
       tc_fence_before();
       mbar_arrive(smem_u32(&sm.acc_empty));
@@ -786,7 +807,7 @@ static_assert(sizeof(RowSmem<128>) <= 232448 && sizeof(RowSmem<64>) <= 232448 &&
                   sizeof(KeySmem<64>) <= 232448,
               "227 KB of shared memory");
 
-// Tensor memory: dK, dV, then S^T with P^T of each half over its own columns, then dP^T with dS^T likewise.
+// Tensor memory: dK, dV, then S^T with P^T of each 32 columns over the first half of them, then dP^T with dS^T likewise.
 template <int D>
 __global__ void __launch_bounds__(kGradThreads, 1)
     grad_kv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -824,14 +845,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     for (int s = 0; s < XS; ++s) {
       mbar_init(smem_u32(&sm.x_full[s]), 1);
-      mbar_init(smem_u32(&sm.x_empty[s]), 8);
+      mbar_init(smem_u32(&sm.x_empty[s]), kSoftmax / 32);
     }
     mbar_init(smem_u32(&sm.s_full), 1);
-    mbar_init(smem_u32(&sm.p_full), 256);
+    mbar_init(smem_u32(&sm.p_full), kSoftmax);
     mbar_init(smem_u32(&sm.dp_full), 1);
-    mbar_init(smem_u32(&sm.ds_full), 256);
+    mbar_init(smem_u32(&sm.ds_full), kSoftmax);
     mbar_init(smem_u32(&sm.acc_full), 1);
-    mbar_init(smem_u32(&sm.acc_empty), 256);
+    mbar_init(smem_u32(&sm.acc_empty), kSoftmax);
     mbar_init(smem_u32(&sm.drain), 1);
     sm.abort_flag = 0;
     fence_barrier_init();
@@ -929,7 +950,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       auto add = [&](uint32_t acc, uint32_t col, uint64_t db, bool first) {
 #pragma unroll
         for (int kk = 0; kk < BM / 16; ++kk)
-          mma_bf16_ts(tmem + acc, tmem + col + (kk >> 2) * 64 + (kk & 3) * 8, db + ((kk * 16 * 128) >> 4), kIdescA,
+          mma_bf16_ts(tmem + acc, tmem + col + (kk >> 1) * 32 + (kk & 1) * 8, db + ((kk * 16 * 128) >> 4), kIdescA,
                       (kk > 0 || !first) ? 1u : 0u);
       };
       while (ok && items.get(it)) {
@@ -1051,11 +1072,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     __syncwarp();
   } else {
-    // ============================================================ P^T, dS^T and epilogue: keys by lane, half the queries
+    // ============================================================ P^T, dS^T and epilogue: keys by lane, 32 queries of a tile
     const int h = (warp - 4) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t s_addr = t_lane + kColS + 64 * h, p_addr = t_lane + kColP + 64 * h;
+    const uint32_t s_addr = t_lane + kColS + 32 * h, p_addr = t_lane + kColP + 32 * h;
     const uint64_t sc2 = f2pack(a.scale_log2, a.scale_log2);
     Ring<XS> xr;
     uint32_t it_n = 0, done = 0;
@@ -1068,69 +1089,62 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       const int far = static_cast<int>(far64);
       const bool tile_sinks = BN * (it.k + 1) <= a.n_sink;             // all keys of the tile are first tokens
       for (int j = 0; j < it.its; ++j) {
-        const int from = BM * qt + 64 * h;                            // position of this half's first query
         // the diagonal, the window's far end for the tile's first key, the sequence's end
         const bool masked = qt == it.k || BM * qt + BM > it.n || (!tile_sinks && BM * (qt - it.k) + BM > a.window);
         if (!(ok = warp_wait(smem_u32(&sm.x_full[xr.st]), xr.ph, abort_flag, lim, 980))) break;
         if (!(ok = warp_wait(smem_u32(&sm.s_full), it_n & 1, abort_flag, lim, 981))) break;
         tc_fence_after();
-        const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sm.neg_lse[xr.st] + 64 * h);
-        const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(sm.neg_delta[xr.st] + 64 * h);
-        float p[64];
+        const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sm.neg_lse[xr.st] + 32 * h);
+        const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(sm.neg_delta[xr.st] + 32 * h);
+        float p[32];
+        uint32_t x[32], pk[16];
+        tmem_ld32(s_addr, x);
+        tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t x[32];
-          tmem_ld32(s_addr + 32 * c, x);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const ulonglong2 l = nl[8 * c + i / 4];
-            exp_pair(x[i], x[i + 1], sc2, l.x, p[32 * c + i], p[32 * c + i + 1]);
-            exp_pair(x[i + 2], x[i + 3], sc2, l.y, p[32 * c + i + 2], p[32 * c + i + 3]);
-          }
-          if (masked) {
-            const uint32_t f = low_bits(far - from - 32 * c) & ~low_bits(key - from - 32 * c);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) p[32 * c + i] = f >> i & 1 ? p[32 * c + i] : 0.f;
-          }
+        for (int i = 0; i < 32; i += 4) {
+          const ulonglong2 l = nl[i / 4];
+          exp_pair(x[i], x[i + 1], sc2, l.x, p[i], p[i + 1]);
+          exp_pair(x[i + 2], x[i + 3], sc2, l.y, p[i + 2], p[i + 3]);
         }
-        {
-          uint32_t pk[32];
+        uint32_t seen = 0xffffffffu;
+        if (masked) {
+          const int from = BM * qt + 32 * h;                          // position of the first of these queries
+          seen = low_bits(far - from) & ~low_bits(key - from);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) pk[i] = f2_bf16x2(p[2 * i], p[2 * i + 1]);
-          tmem_st32(s_addr, pk);
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(smem_u32(&sm.p_full));
+          for (int i = 0; i < 32; ++i)
+            if (!(seen >> i & 1)) p[i] = 0.f;
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[i] = f2_bf16x2(p[2 * i], p[2 * i + 1]);
+        tmem_st16(s_addr, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sm.p_full));
         if (!(ok = warp_wait(smem_u32(&sm.dp_full), it_n & 1, abort_flag, lim, 982))) break;
         ++it_n;
         tc_fence_after();
-        uint32_t pk[32];
-        uint32_t y[2][32];
-        tmem_ld32(p_addr, y[0]);
-        tmem_ld32(p_addr + 32, y[1]);
+        tmem_ld32(p_addr, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int i = 0; i < 32; i += 4) {
+          const ulonglong2 dl = nd[i / 4];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const ulonglong2 dl = nd[8 * c + i / 4];
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              float d0, d1;
-              f2unpack(fmul2(fadd2(f2pack(__uint_as_float(y[c][i + e]), __uint_as_float(y[c][i + e + 1])), e ? dl.y : dl.x),
-                             f2pack(p[32 * c + i + e], p[32 * c + i + e + 1])),
-                       d0, d1);
-              if (masked) {   // 0 * inf
-                d0 = p[32 * c + i + e] == 0.f ? 0.f : d0;
-                d1 = p[32 * c + i + e + 1] == 0.f ? 0.f : d1;
-              }
-              pk[16 * c + (i + e) / 2] = f2_bf16x2(d0, d1);
-            }
+          for (int e = 0; e < 4; e += 2) {
+            float d0, d1;
+            f2unpack(fmul2(fadd2(f2pack(__uint_as_float(x[i + e]), __uint_as_float(x[i + e + 1])), e ? dl.y : dl.x),
+                           f2pack(p[i + e], p[i + e + 1])),
+                     d0, d1);
+            x[i + e] = __float_as_uint(d0);
+            x[i + e + 1] = __float_as_uint(d1);
           }
         }
-        tmem_st32(p_addr, pk);
+        if (masked)   // 0 * inf
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(seen >> i & 1)) x[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[i] = f2_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+        tmem_st16(p_addr, pk);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.ds_full));
@@ -1146,20 +1160,21 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       ++done;
       tc_fence_after();
       const bool part = it.its < it.all;
-      // warpgroup 0 takes dK, 1 dV
-      float* to = a.parts + ((2 * static_cast<int64_t>(blockIdx.x) + (it.it0 == 0 ? 1 : 0)) * 2 + h) * (BN * D);
-      const int64_t out = (it.q0 + static_cast<int64_t>(key)) * (h ? a.dv_rs : a.dk_rs) + it.g * D;
+      // warpgroups 0 and 1 take dK, 2 and 3 dV, half the columns each
+      const int v = h >> 1, col0 = (h & 1) * (D / 2);
+      float* to = a.parts + ((2 * static_cast<int64_t>(blockIdx.x) + (it.it0 == 0 ? 1 : 0)) * 2 + v) * (BN * D);
+      const int64_t out = (it.q0 + static_cast<int64_t>(key)) * (v ? a.dv_rs : a.dk_rs) + it.g * D;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = col0; c < col0 + D / 2; c += 32) {
         uint32_t z[32];
-        tmem_ld32(t_lane + (h ? kColV : 0) + 32 * c, z);
+        tmem_ld32(t_lane + (v ? kColV : 0) + c, z);
         tmem_wait_ld();
         if (part) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(to + ((8 * c + i) * BN + row) * 4) = make_uint4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
+            *reinterpret_cast<uint4*>(to + ((c / 4 + i) * BN + row) * 4) = make_uint4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
         } else if (key < it.n) {
-          store_cols(h ? a.dv : a.dk, a.out_bf16, out + 32 * c, z, h ? 1.f : a.scale);
+          store_cols(v ? a.dv : a.dk, a.out_bf16, out + c, z, v ? 1.f : a.scale);
         }
       }
       tc_fence_before();
