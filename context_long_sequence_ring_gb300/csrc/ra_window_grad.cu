@@ -309,6 +309,12 @@ __global__ void __launch_bounds__(kPlanThreads) grad_prepare_kernel(const __grid
 }
 
 // ------------------------------------------------------------------ pieces of both kernels
+// One arrival for a warp, whose lanes have all done what it stands for.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // p = 2^(s * scale + nl) of a pair of columns.
 __device__ __forceinline__ void exp_pair(uint32_t s0, uint32_t s1, uint64_t sc2, uint64_t nl2, float& p0, float& p1) {
   float t0, t1;
@@ -371,7 +377,7 @@ struct __align__(1024) RowSmem {
   static constexpr int KS = D == 128 ? 3 : 6, VS = D == 128 ? 2 : 4;
   uint8_t q[BM * D * 2], d_o[BM * D * 2], k[KS][BN * D * 2], v[VS][BN * D * 2];
   uint64_t q_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], k_dirty[KS], k_clean[KS];
-  uint64_t s_full[2], dp_full, dp_free, ds_full[2], acc_full, acc_empty, sums_full, sums_free, drain;
+  uint64_t s_full[2], dp_full, ds_full[2], acc_full, acc_empty, sums_full, sums_free, drain;
   float sums[kGroups - 1][BM];
   uint32_t tmem_base;
   int abort_flag;
@@ -416,14 +422,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sm.s_full[b]), 1);
-      mbar_init(smem_u32(&sm.ds_full[b]), kSoftmax);
+      mbar_init(smem_u32(&sm.ds_full[b]), kSoftmax / 32);
     }
     mbar_init(smem_u32(&sm.dp_full), 1);
-    mbar_init(smem_u32(&sm.dp_free), kSoftmax);
-    mbar_init(smem_u32(&sm.sums_full), kSoftmax - 128);
-    mbar_init(smem_u32(&sm.sums_free), 128);
+    mbar_init(smem_u32(&sm.sums_full), kSoftmax / 32 - 4);
+    mbar_init(smem_u32(&sm.sums_free), 4);
     mbar_init(smem_u32(&sm.acc_full), 1);
-    mbar_init(smem_u32(&sm.acc_empty), kSoftmax);
+    mbar_init(smem_u32(&sm.acc_empty), kSoftmax / 32);
     mbar_init(smem_u32(&sm.drain), 1);
     sm.abort_flag = 0;
     fence_barrier_init();
@@ -519,13 +524,20 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     if (lane == 0) {
       Ring<KS> kr, kd;                  // K tile of the next S, of the next dQ
       Ring<VS> vr;
-      uint32_t q_n = 0, done = 0, s_n = 0, p_n = 0, clean_ph = 0;
+      uint32_t q_n = 0, done = 0, s_n = 0, clean_ph = 0;
       bool ok = true;
       const uint64_t dq = desc_sw128(smem_u32(sm.q), 16, 1024), ddo = desc_sw128(smem_u32(sm.d_o), 16, 1024);
       const uint64_t dk = desc_sw128(smem_u32(sm.k[0]), 16, 1024), dv = desc_sw128(smem_u32(sm.v[0]), 16, 1024);
       const uint64_t dkt = desc_sw128(smem_u32(sm.k[0]), BN * 128, 1024);
-      auto issue_s = [&](int j) -> bool {
-        if (!mbar_wait(smem_u32(&sm.k_full[kr.st]), kr.ph, abort_flag, lim, 920)) return false;
+      // A wait that passes at once takes some 130 cycles with the tensor core idle, so the next barriers are looked at
+      // while the last products are queued.
+      bool k_ready = false, v_ready = false, ds_ready = false;
+      auto nothing = [] {};
+      auto test_k = [&] { return mbar_test_wait(smem_u32(&sm.k_full[kr.st]), kr.ph); };
+      auto test_v = [&] { return mbar_test_wait(smem_u32(&sm.v_full[vr.st]), vr.ph); };
+      auto issue_s = [&](int j, auto then) -> bool {
+        if (!k_ready && !mbar_wait(smem_u32(&sm.k_full[kr.st]), kr.ph, abort_flag, lim, 920)) return false;
+        k_ready = false;
         if (j >= it.dirty) {
           if (!mbar_wait(smem_u32(&sm.k_clean[kr.st]), (clean_ph >> kr.st) & 1, abort_flag, lim, 921)) return false;
           clean_ph ^= 1u << kr.st;
@@ -536,6 +548,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
           mma_bf16_ss(tmem + kColS + b * BN, dq + off16, dk + kr.st * (kTileBytes >> 4) + off16, kIdescS, kk > 0 ? 1u : 0u);
+          if (kk == D / 16 - 3) then();
         }
         mma_commit(smem_u32(&sm.s_full[b]));
         ++s_n;
@@ -543,9 +556,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         return true;
       };
       auto issue_dp = [&]() -> bool {
-        if (!mbar_wait(smem_u32(&sm.v_full[vr.st]), vr.ph, abort_flag, lim, 922)) return false;
-        // the softmax has taken the dP before it
-        if (!mbar_wait(smem_u32(&sm.dp_free), (p_n & 1) ^ 1, abort_flag, lim, 923)) return false;
+        if (!v_ready && !mbar_wait(smem_u32(&sm.v_full[vr.st]), vr.ph, abort_flag, lim, 922)) return false;
+        v_ready = false;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -554,7 +566,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         }
         mma_commit(smem_u32(&sm.dp_full));
         mma_commit(smem_u32(&sm.v_empty[vr.st]));
-        ++p_n;
         vr.advance();
         return true;
       };
@@ -563,23 +574,27 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         if (!(ok = mbar_wait(smem_u32(&sm.q_full), q_n & 1, abort_flag, lim, 924))) break;
         ++q_n;
         tc_fence_after();
-        if (!(ok = issue_s(0))) break;
+        if (!(ok = issue_s(0, nothing))) break;
         if (!(ok = issue_dp())) break;
-        if (it.nt > 1 && !(ok = issue_s(1))) break;
+        if (it.nt > 1 && !(ok = issue_s(1, nothing))) break;
         if (it.nt == 1) mma_commit(smem_u32(&sm.q_empty));
         for (int j = 0; j < it.nt; ++j) {
+          const uint32_t at = s_n - (j + 1 < it.nt ? 2 : 1);          // this tile among all
+          if (j == 0 && !(ok = mbar_wait(smem_u32(&sm.acc_empty), (done & 1) ^ 1, abort_flag, lim, 925))) break;
+          if (!ds_ready && !(ok = mbar_wait(smem_u32(&sm.ds_full[at & 1]), (at >> 1) & 1, abort_flag, lim, 926))) break;
+          ds_ready = false;
+          tc_fence_after();
+          // dS tells that dP has been read as well
           if (j + 1 < it.nt) {
             if (!(ok = issue_dp())) break;
             if (j + 2 == it.nt) mma_commit(smem_u32(&sm.q_empty));   // the last S and dP
           }
-          if (j == 0 && !(ok = mbar_wait(smem_u32(&sm.acc_empty), (done & 1) ^ 1, abort_flag, lim, 925))) break;
-          const uint32_t at = s_n - (j + 1 < it.nt ? 2 : 1);          // this tile among all
-          if (!(ok = mbar_wait(smem_u32(&sm.ds_full[at & 1]), (at >> 1) & 1, abort_flag, lim, 926))) break;
-          tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
+          for (int kk = 0; kk < BN / 16; ++kk) {
             mma_bf16_ts(tmem, tmem + kColS + (at & 1) * BN + (kk >> 1) * 32 + (kk & 1) * 8,
                         dkt + kd.st * (kTileBytes >> 4) + ((kk * 16 * 128) >> 4), kIdescQ, (kk > 0 || j > 0) ? 1u : 0u);
+            if (kk == BN / 16 - 3) k_ready = j + 2 < it.nt && test_k();
+          }
           if (it.nt <= kFewTiles)
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)
@@ -587,7 +602,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                           dkt + kd.st * (kTileBytes >> 4) + ((kk * 16 * 128) >> 4), kIdescQ, 1u);
           mma_commit(smem_u32(&sm.k_empty[kd.st]));
           kd.advance();
-          if (j + 2 < it.nt && !(ok = issue_s(j + 2))) break;
+          if (j + 2 < it.nt && !(ok = issue_s(j + 2, [&] {
+                ds_ready = mbar_test_wait(smem_u32(&sm.ds_full[(at + 1) & 1]), ((at + 1) >> 1) & 1);
+                v_ready = test_v();
+              })))
+            break;
         }
         if (!ok) break;
         mma_commit(smem_u32(&sm.acc_full));
@@ -647,21 +666,29 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (int j = 0; j < it.nt; ++j) {
         const uint32_t b = s_n & 1;
         if (!(ok = warp_wait(smem_u32(&sm.s_full[b]), (s_n >> 1) & 1, abort_flag, lim, 940))) break;
-        if (!(ok = warp_wait(smem_u32(&sm.dp_full), s_n & 1, abort_flag, lim, 941))) break;
-        ++s_n;
         tc_fence_after();
         const uint32_t s_addr = t_lane + kColS + b * BN + 32 * h;
         uint32_t x[32], y[32], pk[16];
         tmem_ld32(s_addr, x);
-        tmem_ld32(t_lane + kColP + 32 * h, y);
         tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(smem_u32(&sm.dp_free));
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          float p0, p1, d0, d1;
+          float p0, p1;
           exp_pair(x[i], x[i + 1], sc2, nl2, p0, p1);
-          f2unpack(fmul2(fadd2(f2pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), nd2), f2pack(p0, p1)), d0, d1);
+          x[i] = __float_as_uint(p0);
+          x[i + 1] = __float_as_uint(p1);
+        }
+        if (!(ok = warp_wait(smem_u32(&sm.dp_full), s_n & 1, abort_flag, lim, 941))) break;
+        ++s_n;
+        tc_fence_after();
+        tmem_ld32(t_lane + kColP + 32 * h, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          float d0, d1;
+          f2unpack(fmul2(fadd2(f2pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), nd2),
+                         f2pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1]))),
+                   d0, d1);
           y[i] = __float_as_uint(d0);
           y[i + 1] = __float_as_uint(d1);
         }
@@ -687,7 +714,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_u32(&sm.ds_full[b]));
+        warp_arrive(smem_u32(&sm.ds_full[b]));
       }
       if (!ok) break;
       // the row's sum of dS is the error of its delta
@@ -696,13 +723,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       if (h > 0) {
         if (!(ok = warp_wait(smem_u32(&sm.sums_free), (done & 1) ^ 1, abort_flag, lim, 943))) break;
         sm.sums[h - 1][row] = s0 + s1;
-        mbar_arrive(smem_u32(&sm.sums_full));
+        warp_arrive(smem_u32(&sm.sums_full));
       } else {
         if (!(ok = warp_wait(smem_u32(&sm.sums_full), done & 1, abort_flag, lim, 944))) break;
         float sum = s0 + s1;
 #pragma unroll
         for (int g = 1; g < kGroups; ++g) sum += sm.sums[g - 1][row];
-        mbar_arrive(smem_u32(&sm.sums_free));
+        warp_arrive(smem_u32(&sm.sums_free));
         if (row_ok) a.neg_delta[at] = nd - sum;
       }
       if (!(ok = warp_wait(smem_u32(&sm.acc_full), done & 1, abort_flag, lim, 942))) break;
@@ -715,7 +742,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         if (row_ok) store_cols(a.dq, a.out_bf16, (it.q0 + static_cast<int64_t>(pos)) * a.dq_rs + head * D + 32 * h, z, a.scale);
       }
       tc_fence_before();
-      mbar_arrive(smem_u32(&sm.acc_empty));
+      warp_arrive(smem_u32(&sm.acc_empty));
     }
     tmem_wait_st();   // a wait that expires between the stores and their own wait leaves them in flight
   }
@@ -848,11 +875,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       mbar_init(smem_u32(&sm.x_empty[s]), kSoftmax / 32);
     }
     mbar_init(smem_u32(&sm.s_full), 1);
-    mbar_init(smem_u32(&sm.p_full), kSoftmax);
+    mbar_init(smem_u32(&sm.p_full), kSoftmax / 32);
     mbar_init(smem_u32(&sm.dp_full), 1);
-    mbar_init(smem_u32(&sm.ds_full), kSoftmax);
+    mbar_init(smem_u32(&sm.ds_full), kSoftmax / 32);
     mbar_init(smem_u32(&sm.acc_full), 1);
-    mbar_init(smem_u32(&sm.acc_empty), kSoftmax);
+    mbar_init(smem_u32(&sm.acc_empty), kSoftmax / 32);
     mbar_init(smem_u32(&sm.drain), 1);
     sm.abort_flag = 0;
     fence_barrier_init();
@@ -939,36 +966,45 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       const uint64_t dk = desc_sw128(smem_u32(sm.k), 16, 1024), dv = desc_sw128(smem_u32(sm.v), 16, 1024);
       const uint64_t dq = desc_sw128(smem_u32(sm.q[0]), 16, 1024), ddo = desc_sw128(smem_u32(sm.d_o[0]), 16, 1024);
       const uint64_t dqt = desc_sw128(smem_u32(sm.q[0]), BM * 128, 1024), dot = desc_sw128(smem_u32(sm.d_o[0]), BM * 128, 1024);
-      auto scores = [&](uint32_t col, uint64_t da, uint64_t db, uint64_t* bar) {
+      // As in the dQ kernel the next barrier is looked at while the last products are queued.
+      bool q_ready = false, o_ready = false, p_ready = false, ds_ready = false;
+      auto scores = [&](uint32_t col, uint64_t da, uint64_t db, uint64_t* bar, auto then) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
           mma_bf16_ss(tmem + col, da + off16, db + off16, kIdescS, kk > 0 ? 1u : 0u);
+          if (kk == D / 16 - 3) then();
         }
         mma_commit(smem_u32(bar));
       };
-      auto add = [&](uint32_t acc, uint32_t col, uint64_t db, bool first) {
+      auto add = [&](uint32_t acc, uint32_t col, uint64_t db, bool first, auto then) {
 #pragma unroll
-        for (int kk = 0; kk < BM / 16; ++kk)
+        for (int kk = 0; kk < BM / 16; ++kk) {
           mma_bf16_ts(tmem + acc, tmem + col + (kk >> 1) * 32 + (kk & 1) * 8, db + ((kk * 16 * 128) >> 4), kIdescA,
                       (kk > 0 || !first) ? 1u : 0u);
+          if (kk == BM / 16 - 3) then();
+        }
       };
       while (ok && items.get(it)) {
         // pairs of the sequence's last query tile, where it is not full, wait for its rows past the end to be zeroed
         const int last = it.n % BM == 0 ? INT32_MAX : ((it.n / BM) - it.k) * a.G - it.it0;
         auto issue_s = [&](int j) -> bool {
-          if (!mbar_wait(smem_u32(&sm.q_full[qs.st]), qs.ph, abort_flag, lim, 960)) return false;
+          if (!q_ready && !mbar_wait(smem_u32(&sm.q_full[qs.st]), qs.ph, abort_flag, lim, 960)) return false;
+          q_ready = false;
           if (j >= last && !mbar_wait(smem_u32(&sm.x_full[xs.st]), xs.ph, abort_flag, lim, 961)) return false;
           xs.advance();
           tc_fence_after();
-          scores(kColS, dk, dq + qs.st * (kTileBytes >> 4), &sm.s_full);
+          scores(kColS, dk, dq + qs.st * (kTileBytes >> 4), &sm.s_full,
+                 [&] { ds_ready = j > 0 && mbar_test_wait(smem_u32(&sm.ds_full), it_n & 1); });
           qs.advance();
           return true;
         };
         auto issue_dp = [&]() -> bool {
-          if (!mbar_wait(smem_u32(&sm.o_full[op.st]), op.ph, abort_flag, lim, 962)) return false;
+          if (!o_ready && !mbar_wait(smem_u32(&sm.o_full[op.st]), op.ph, abort_flag, lim, 962)) return false;
+          o_ready = false;
           tc_fence_after();
-          scores(kColP, dv, ddo + op.st * (kTileBytes >> 4), &sm.dp_full);
+          scores(kColP, dv, ddo + op.st * (kTileBytes >> 4), &sm.dp_full,
+                 [&] { p_ready = mbar_test_wait(smem_u32(&sm.p_full), it_n & 1); });
           op.advance();
           return true;
         };
@@ -982,19 +1018,23 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         for (int j = 0; j < it.its; ++j) {
           const bool more = j + 1 < it.its;
           if (j == 0 && !(ok = mbar_wait(smem_u32(&sm.acc_empty), (done & 1) ^ 1, abort_flag, lim, 965))) break;
-          if (!(ok = mbar_wait(smem_u32(&sm.p_full), it_n & 1, abort_flag, lim, 966))) break;
+          if (!p_ready && !(ok = mbar_wait(smem_u32(&sm.p_full), it_n & 1, abort_flag, lim, 966))) break;
+          p_ready = ds_ready = false;
           tc_fence_after();
-          add(kColV, kColS, dot + od.st * (kTileBytes >> 4), j == 0);
+          add(kColV, kColS, dot + od.st * (kTileBytes >> 4), j == 0,
+              [&] { q_ready = more && mbar_test_wait(smem_u32(&sm.q_full[qs.st]), qs.ph); });
           mma_commit(smem_u32(&sm.o_empty[od.st]));
           od.advance();
           if (more) {
             if (!(ok = issue_s(j + 1))) break;
             if (j + 2 == it.its) mma_commit(smem_u32(&sm.k_empty));
           }
-          if (!(ok = mbar_wait(smem_u32(&sm.ds_full), it_n & 1, abort_flag, lim, 967))) break;
+          if (!ds_ready && !(ok = mbar_wait(smem_u32(&sm.ds_full), it_n & 1, abort_flag, lim, 967))) break;
+          ds_ready = false;
           ++it_n;
           tc_fence_after();
-          add(0, kColP, dqt + qd.st * (kTileBytes >> 4), j == 0);
+          add(0, kColP, dqt + qd.st * (kTileBytes >> 4), j == 0,
+              [&] { o_ready = more && mbar_test_wait(smem_u32(&sm.o_full[op.st]), op.ph); });
           mma_commit(smem_u32(&sm.q_empty[qd.st]));
           qd.advance();
           if (more) {
@@ -1119,7 +1159,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         tmem_st16(s_addr, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_u32(&sm.p_full));
+        warp_arrive(smem_u32(&sm.p_full));
         if (!(ok = warp_wait(smem_u32(&sm.dp_full), it_n & 1, abort_flag, lim, 982))) break;
         ++it_n;
         tc_fence_after();
@@ -1147,8 +1187,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         tmem_st16(p_addr, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_u32(&sm.ds_full));
-        if (lane == 0) mbar_arrive(smem_u32(&sm.x_empty[xr.st]));
+        warp_arrive(smem_u32(&sm.ds_full));
+        warp_arrive(smem_u32(&sm.x_empty[xr.st]));
         xr.advance();
         if (++head == a.G) {
           head = 0;
@@ -1178,7 +1218,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(smem_u32(&sm.acc_empty));
+      warp_arrive(smem_u32(&sm.acc_empty));
     }
     tmem_wait_st();
   }
