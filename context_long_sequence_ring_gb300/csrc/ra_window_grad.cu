@@ -309,6 +309,10 @@ __global__ void __launch_bounds__(kPlanThreads) grad_prepare_kernel(const __grid
 }
 
 // ------------------------------------------------------------------ pieces of both kernels
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+}
+
 // One arrival for a warp, whose lanes have all done what it stands for.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();
@@ -521,7 +525,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ============================================================ products
-    if (lane == 0) {
+    {
+      const uint32_t leader = elect_one();
       Ring<KS> kr, kd;                  // K tile of the next S, of the next dQ
       Ring<VS> vr;
       uint32_t q_n = 0, done = 0, s_n = 0, clean_ph = 0;
@@ -533,13 +538,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       // while the last products are queued.
       bool k_ready = false, v_ready = false, ds_ready = false;
       auto nothing = [] {};
-      auto test_k = [&] { return mbar_test_wait(smem_u32(&sm.k_full[kr.st]), kr.ph); };
-      auto test_v = [&] { return mbar_test_wait(smem_u32(&sm.v_full[vr.st]), vr.ph); };
+      auto test_k = [&] { return warp_test(smem_u32(&sm.k_full[kr.st]), kr.ph); };
+      auto test_v = [&] { return warp_test(smem_u32(&sm.v_full[vr.st]), vr.ph); };
       auto issue_s = [&](int j, auto then) -> bool {
-        if (!k_ready && !mbar_wait(smem_u32(&sm.k_full[kr.st]), kr.ph, abort_flag, lim, 920)) return false;
+        if (!k_ready && !warp_wait(smem_u32(&sm.k_full[kr.st]), kr.ph, abort_flag, lim, 920)) return false;
         k_ready = false;
         if (j >= it.dirty) {
-          if (!mbar_wait(smem_u32(&sm.k_clean[kr.st]), (clean_ph >> kr.st) & 1, abort_flag, lim, 921)) return false;
+          if (!warp_wait(smem_u32(&sm.k_clean[kr.st]), (clean_ph >> kr.st) & 1, abort_flag, lim, 921)) return false;
           clean_ph ^= 1u << kr.st;
         }
         tc_fence_after();
@@ -547,73 +552,73 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-          mma_bf16_ss(tmem + kColS + b * BN, dq + off16, dk + kr.st * (kTileBytes >> 4) + off16, kIdescS, kk > 0 ? 1u : 0u);
+          mma_bf16_ss_by(leader, tmem + kColS + b * BN, dq + off16, dk + kr.st * (kTileBytes >> 4) + off16, kIdescS, kk > 0 ? 1u : 0u);
           if (kk == D / 16 - 3) then();
         }
-        mma_commit(smem_u32(&sm.s_full[b]));
+        mma_commit_by(leader, smem_u32(&sm.s_full[b]));
         ++s_n;
         kr.advance();
         return true;
       };
       auto issue_dp = [&]() -> bool {
-        if (!v_ready && !mbar_wait(smem_u32(&sm.v_full[vr.st]), vr.ph, abort_flag, lim, 922)) return false;
+        if (!v_ready && !warp_wait(smem_u32(&sm.v_full[vr.st]), vr.ph, abort_flag, lim, 922)) return false;
         v_ready = false;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-          mma_bf16_ss(tmem + kColP, ddo + off16, dv + vr.st * (kTileBytes >> 4) + off16, kIdescS, kk > 0 ? 1u : 0u);
+          mma_bf16_ss_by(leader, tmem + kColP, ddo + off16, dv + vr.st * (kTileBytes >> 4) + off16, kIdescS, kk > 0 ? 1u : 0u);
         }
-        mma_commit(smem_u32(&sm.dp_full));
-        mma_commit(smem_u32(&sm.v_empty[vr.st]));
+        mma_commit_by(leader, smem_u32(&sm.dp_full));
+        mma_commit_by(leader, smem_u32(&sm.v_empty[vr.st]));
         vr.advance();
         return true;
       };
       for (int m = 0; m < rounds && ok; ++m) {
         if (!get(m, it)) continue;
-        if (!(ok = mbar_wait(smem_u32(&sm.q_full), q_n & 1, abort_flag, lim, 924))) break;
+        if (!(ok = warp_wait(smem_u32(&sm.q_full), q_n & 1, abort_flag, lim, 924))) break;
         ++q_n;
         tc_fence_after();
         if (!(ok = issue_s(0, nothing))) break;
         if (!(ok = issue_dp())) break;
         if (it.nt > 1 && !(ok = issue_s(1, nothing))) break;
-        if (it.nt == 1) mma_commit(smem_u32(&sm.q_empty));
+        if (it.nt == 1) mma_commit_by(leader, smem_u32(&sm.q_empty));
         for (int j = 0; j < it.nt; ++j) {
           const uint32_t at = s_n - (j + 1 < it.nt ? 2 : 1);          // this tile among all
-          if (j == 0 && !(ok = mbar_wait(smem_u32(&sm.acc_empty), (done & 1) ^ 1, abort_flag, lim, 925))) break;
-          if (!ds_ready && !(ok = mbar_wait(smem_u32(&sm.ds_full[at & 1]), (at >> 1) & 1, abort_flag, lim, 926))) break;
+          if (j == 0 && !(ok = warp_wait(smem_u32(&sm.acc_empty), (done & 1) ^ 1, abort_flag, lim, 925))) break;
+          if (!ds_ready && !(ok = warp_wait(smem_u32(&sm.ds_full[at & 1]), (at >> 1) & 1, abort_flag, lim, 926))) break;
           ds_ready = false;
           tc_fence_after();
           // dS tells that dP has been read as well
           if (j + 1 < it.nt) {
             if (!(ok = issue_dp())) break;
-            if (j + 2 == it.nt) mma_commit(smem_u32(&sm.q_empty));   // the last S and dP
+            if (j + 2 == it.nt) mma_commit_by(leader, smem_u32(&sm.q_empty));   // the last S and dP
           }
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk) {
-            mma_bf16_ts(tmem, tmem + kColS + (at & 1) * BN + (kk >> 1) * 32 + (kk & 1) * 8,
+            mma_bf16_ts_by(leader, tmem, tmem + kColS + (at & 1) * BN + (kk >> 1) * 32 + (kk & 1) * 8,
                         dkt + kd.st * (kTileBytes >> 4) + ((kk * 16 * 128) >> 4), kIdescQ, (kk > 0 || j > 0) ? 1u : 0u);
             if (kk == BN / 16 - 3) k_ready = j + 2 < it.nt && test_k();
           }
           if (it.nt <= kFewTiles)
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)
-              mma_bf16_ts(tmem, tmem + kColS + (at & 1) * BN + 16 + (kk >> 1) * 32 + (kk & 1) * 8,
+              mma_bf16_ts_by(leader, tmem, tmem + kColS + (at & 1) * BN + 16 + (kk >> 1) * 32 + (kk & 1) * 8,
                           dkt + kd.st * (kTileBytes >> 4) + ((kk * 16 * 128) >> 4), kIdescQ, 1u);
-          mma_commit(smem_u32(&sm.k_empty[kd.st]));
+          mma_commit_by(leader, smem_u32(&sm.k_empty[kd.st]));
           kd.advance();
           if (j + 2 < it.nt && !(ok = issue_s(j + 2, [&] {
-                ds_ready = mbar_test_wait(smem_u32(&sm.ds_full[(at + 1) & 1]), ((at + 1) >> 1) & 1);
+                ds_ready = warp_test(smem_u32(&sm.ds_full[(at + 1) & 1]), ((at + 1) >> 1) & 1);
                 v_ready = test_v();
               })))
             break;
         }
         if (!ok) break;
-        mma_commit(smem_u32(&sm.acc_full));
+        mma_commit_by(leader, smem_u32(&sm.acc_full));
         ++done;
       }
-      mma_commit(smem_u32(&sm.drain));
-      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, a.drain_limit) && ok) {
+      mma_commit_by(leader, smem_u32(&sm.drain));
+      if (!__all_sync(0xffffffffu, mbar_wait_quiesce(smem_u32(&sm.drain), 0, a.drain_limit)) && ok) {
         *abort_flag = 1;
         ra_record_error(RA_ERR_TIMEOUT, 927);
       }
@@ -957,7 +962,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ============================================================ products
-    if (lane == 0) {
+    {
+      const uint32_t leader = elect_one();
       Ring<QS> qs, qd;                  // Q tile of the next S, of the next dK
       Ring<OS> op, od;                  // dO tile of the next dP, of the next dV
       Ring<XS> xs;
@@ -972,15 +978,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-          mma_bf16_ss(tmem + col, da + off16, db + off16, kIdescS, kk > 0 ? 1u : 0u);
+          mma_bf16_ss_by(leader, tmem + col, da + off16, db + off16, kIdescS, kk > 0 ? 1u : 0u);
           if (kk == D / 16 - 3) then();
         }
-        mma_commit(smem_u32(bar));
+        mma_commit_by(leader, smem_u32(bar));
       };
       auto add = [&](uint32_t acc, uint32_t col, uint64_t db, bool first, auto then) {
 #pragma unroll
         for (int kk = 0; kk < BM / 16; ++kk) {
-          mma_bf16_ts(tmem + acc, tmem + col + (kk >> 1) * 32 + (kk & 1) * 8, db + ((kk * 16 * 128) >> 4), kIdescA,
+          mma_bf16_ts_by(leader, tmem + acc, tmem + col + (kk >> 1) * 32 + (kk & 1) * 8, db + ((kk * 16 * 128) >> 4), kIdescA,
                       (kk > 0 || !first) ? 1u : 0u);
           if (kk == BM / 16 - 3) then();
         }
@@ -989,65 +995,65 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         // pairs of the sequence's last query tile, where it is not full, wait for its rows past the end to be zeroed
         const int last = it.n % BM == 0 ? INT32_MAX : ((it.n / BM) - it.k) * a.G - it.it0;
         auto issue_s = [&](int j) -> bool {
-          if (!q_ready && !mbar_wait(smem_u32(&sm.q_full[qs.st]), qs.ph, abort_flag, lim, 960)) return false;
+          if (!q_ready && !warp_wait(smem_u32(&sm.q_full[qs.st]), qs.ph, abort_flag, lim, 960)) return false;
           q_ready = false;
-          if (j >= last && !mbar_wait(smem_u32(&sm.x_full[xs.st]), xs.ph, abort_flag, lim, 961)) return false;
+          if (j >= last && !warp_wait(smem_u32(&sm.x_full[xs.st]), xs.ph, abort_flag, lim, 961)) return false;
           xs.advance();
           tc_fence_after();
           scores(kColS, dk, dq + qs.st * (kTileBytes >> 4), &sm.s_full,
-                 [&] { ds_ready = j > 0 && mbar_test_wait(smem_u32(&sm.ds_full), it_n & 1); });
+                 [&] { ds_ready = j > 0 && warp_test(smem_u32(&sm.ds_full), it_n & 1); });
           qs.advance();
           return true;
         };
         auto issue_dp = [&]() -> bool {
-          if (!o_ready && !mbar_wait(smem_u32(&sm.o_full[op.st]), op.ph, abort_flag, lim, 962)) return false;
+          if (!o_ready && !warp_wait(smem_u32(&sm.o_full[op.st]), op.ph, abort_flag, lim, 962)) return false;
           o_ready = false;
           tc_fence_after();
           scores(kColP, dv, ddo + op.st * (kTileBytes >> 4), &sm.dp_full,
-                 [&] { p_ready = mbar_test_wait(smem_u32(&sm.p_full), it_n & 1); });
+                 [&] { p_ready = warp_test(smem_u32(&sm.p_full), it_n & 1); });
           op.advance();
           return true;
         };
-        if (!(ok = mbar_wait(smem_u32(&sm.k_full), kv_n & 1, abort_flag, lim, 963))) break;
+        if (!(ok = warp_wait(smem_u32(&sm.k_full), kv_n & 1, abort_flag, lim, 963))) break;
         if (!(ok = issue_s(0))) break;
-        if (it.its == 1) mma_commit(smem_u32(&sm.k_empty));
-        if (!(ok = mbar_wait(smem_u32(&sm.v_full), kv_n & 1, abort_flag, lim, 964))) break;
+        if (it.its == 1) mma_commit_by(leader, smem_u32(&sm.k_empty));
+        if (!(ok = warp_wait(smem_u32(&sm.v_full), kv_n & 1, abort_flag, lim, 964))) break;
         ++kv_n;
         if (!(ok = issue_dp())) break;
-        if (it.its == 1) mma_commit(smem_u32(&sm.v_empty));
+        if (it.its == 1) mma_commit_by(leader, smem_u32(&sm.v_empty));
         for (int j = 0; j < it.its; ++j) {
           const bool more = j + 1 < it.its;
-          if (j == 0 && !(ok = mbar_wait(smem_u32(&sm.acc_empty), (done & 1) ^ 1, abort_flag, lim, 965))) break;
-          if (!p_ready && !(ok = mbar_wait(smem_u32(&sm.p_full), it_n & 1, abort_flag, lim, 966))) break;
+          if (j == 0 && !(ok = warp_wait(smem_u32(&sm.acc_empty), (done & 1) ^ 1, abort_flag, lim, 965))) break;
+          if (!p_ready && !(ok = warp_wait(smem_u32(&sm.p_full), it_n & 1, abort_flag, lim, 966))) break;
           p_ready = ds_ready = false;
           tc_fence_after();
           add(kColV, kColS, dot + od.st * (kTileBytes >> 4), j == 0,
-              [&] { q_ready = more && mbar_test_wait(smem_u32(&sm.q_full[qs.st]), qs.ph); });
-          mma_commit(smem_u32(&sm.o_empty[od.st]));
+              [&] { q_ready = more && warp_test(smem_u32(&sm.q_full[qs.st]), qs.ph); });
+          mma_commit_by(leader, smem_u32(&sm.o_empty[od.st]));
           od.advance();
           if (more) {
             if (!(ok = issue_s(j + 1))) break;
-            if (j + 2 == it.its) mma_commit(smem_u32(&sm.k_empty));
+            if (j + 2 == it.its) mma_commit_by(leader, smem_u32(&sm.k_empty));
           }
-          if (!ds_ready && !(ok = mbar_wait(smem_u32(&sm.ds_full), it_n & 1, abort_flag, lim, 967))) break;
+          if (!ds_ready && !(ok = warp_wait(smem_u32(&sm.ds_full), it_n & 1, abort_flag, lim, 967))) break;
           ds_ready = false;
           ++it_n;
           tc_fence_after();
           add(0, kColP, dqt + qd.st * (kTileBytes >> 4), j == 0,
-              [&] { o_ready = more && mbar_test_wait(smem_u32(&sm.o_full[op.st]), op.ph); });
-          mma_commit(smem_u32(&sm.q_empty[qd.st]));
+              [&] { o_ready = more && warp_test(smem_u32(&sm.o_full[op.st]), op.ph); });
+          mma_commit_by(leader, smem_u32(&sm.q_empty[qd.st]));
           qd.advance();
           if (more) {
             if (!(ok = issue_dp())) break;
-            if (j + 2 == it.its) mma_commit(smem_u32(&sm.v_empty));
+            if (j + 2 == it.its) mma_commit_by(leader, smem_u32(&sm.v_empty));
           }
         }
         if (!ok) break;
-        mma_commit(smem_u32(&sm.acc_full));
+        mma_commit_by(leader, smem_u32(&sm.acc_full));
         ++done;
       }
-      mma_commit(smem_u32(&sm.drain));
-      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, a.drain_limit) && ok) {
+      mma_commit_by(leader, smem_u32(&sm.drain));
+      if (!__all_sync(0xffffffffu, mbar_wait_quiesce(smem_u32(&sm.drain), 0, a.drain_limit)) && ok) {
         *abort_flag = 1;
         ra_record_error(RA_ERR_TIMEOUT, 968);
       }
