@@ -207,6 +207,40 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit, site));
 }
 
+// The same for a wait that is long at a kernel's start.  A try by a whole warp suspends it for microseconds, past short
+// limits; with one the barrier is only looked at, so that such a wait expires.
+__device__ __forceinline__ bool warp_try(uint32_t bar, uint32_t parity, bool look) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, l;\n\t"
+      "setp.ne.b32 l, %3, 0;\n\t"
+      "@l mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@!l mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(static_cast<uint32_t>(look))
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+__device__ __forceinline__ bool warp_wait_first(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit,
+                                                int site) {
+  const bool look = limit < 4096;
+  if (warp_try(bar, parity, look)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (warp_try(bar, parity, look)) return true;
+    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+    if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
+      *abort_flag = 1;
+      ra_record_error(RA_ERR_TIMEOUT, site);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+}
+
 template <int NS>
 struct Ring {
   int st = 0;

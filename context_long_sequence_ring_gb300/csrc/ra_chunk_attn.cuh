@@ -801,7 +801,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ============================================================ MMA issuer
-    if (lane == 0) {
+    {
+      // The whole warp runs this, with one lane elected to issue: operands are then in uniform registers.  Issued by a branch
+      // of one thread, a product of 8 instructions took it some 560 cycles whatever its size.
+      const uint32_t leader = elect_one();
       Ring<NS> ring;
       uint32_t s0 = 0, s1 = 0, p0 = 0, p1 = 0;   // score tiles issued, P taken, of each slot
       uint32_t q_cnt[2] = {0, 0}, seg = 0, clean_ph = 0;
@@ -814,12 +817,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // at while the last products are queued.
       auto test_p = [&](int h) {
         const uint32_t c = h ? p1 : p0;
-        return mbar_test_wait(smem_u32(&sm.p_full[turn(h, c)]), phase(c));
+        return warp_test(smem_u32(&sm.p_full[turn(h, c)]), phase(c));
       };
-      auto test_kv = [&] { return mbar_test_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph); };
+      auto test_kv = [&] { return warp_test(smem_u32(&sm.kv_full[ring.st]), ring.ph); };
       auto wait_p = [&](int h, int site) -> bool {
         const uint32_t c = h ? p1 : p0;
-        if (!p_ready && !mbar_wait(smem_u32(&sm.p_full[turn(h, c)]), phase(c), abort_flag, lim, site)) return false;
+        if (!p_ready && !warp_wait(smem_u32(&sm.p_full[turn(h, c)]), phase(c), abort_flag, lim, site)) return false;
         p_ready = false;
         if (h) ++p1; else ++p0;
         return true;
@@ -830,57 +833,57 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off16 = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-          mma_bf16_ss(tmem + b * BN, dq + off16, dk + off16, kIdescS, kk > 0 ? 1u : 0u);
+          mma_bf16_ss_by(leader, tmem + b * BN, dq + off16, dk + off16, kIdescS, kk > 0 ? 1u : 0u);
           if (kk == D / 16 - 3) then();
         }
-        mma_commit(smem_u32(&sm.s_full[turn(h, h ? s1++ : s0++)]));
+        mma_commit_by(leader, smem_u32(&sm.s_full[turn(h, h ? s1++ : s0++)]));
       };
       auto issue_pv = [&](int h, int b, int st, bool first, auto then) {
         const uint64_t dv = dv0 + st * (kStageBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk) {
-          mma_bf16_ts(tmem + kColAcc + h * D, tmem + b * BN + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdescO,
+          mma_bf16_ts_by(leader, tmem + kColAcc + h * D, tmem + b * BN + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdescO,
                       (kk > 0 || !first) ? 1u : 0u);
           if (kk == BN / 16 - 3) then();
         }
-        mma_commit(smem_u32(&sm.pv_done[turn(h, (h ? p1 : p0) - 1)]));   // its P has been counted
+        mma_commit_by(leader, smem_u32(&sm.pv_done[turn(h, (h ? p1 : p0) - 1)]));   // its P has been counted
       };
       auto nothing = [] {};
       // the V tile at the ring's head is in place, its dead rows zeroed
       auto wait_v = [&](int j, int dirty) -> bool {
-        if (!v_ready && !mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 531)) return false;
+        if (!v_ready && !warp_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 531)) return false;
         v_ready = false;
         if (j >= dirty) {
-          if (!mbar_wait(smem_u32(&sm.v_clean[ring.st]), (clean_ph >> ring.st) & 1, abort_flag, lim, 532)) return false;
+          if (!warp_wait(smem_u32(&sm.v_clean[ring.st]), (clean_ph >> ring.st) & 1, abort_flag, lim, 532)) return false;
           clean_ph ^= 1u << ring.st;
         }
         return true;
       };
-      while (ok && segs.next(sm, sg, abort_flag, lim, false)) {
+      while (ok && segs.next(sm, sg, abort_flag, lim, true)) {
         const int nt = sg.nt;
         if (nt <= 0) continue;
         const int dirty = sg.dirty;
         const bool pair = sg.pair;
         const int qb = pair ? 0 : q_next;
-        if (!(ok = mbar_wait(smem_u32(&sm.q_full[qb]), q_cnt[qb] & 1, abort_flag, lim, 530))) break;
+        if (!(ok = warp_wait(smem_u32(&sm.q_full[qb]), q_cnt[qb] & 1, abort_flag, lim, 530))) break;
         ++q_cnt[qb];
         if (pair) {
-          if (!(ok = mbar_wait(smem_u32(&sm.q_full[1]), q_cnt[1] & 1, abort_flag, lim, 530))) break;
+          if (!(ok = warp_wait(smem_u32(&sm.q_full[1]), q_cnt[1] & 1, abort_flag, lim, 530))) break;
           ++q_cnt[1];
         } else {
           q_next ^= 1;
         }
         auto q_release = [&] {
-          mma_commit(smem_u32(&sm.q_empty[qb]));
-          if (pair) mma_commit(smem_u32(&sm.q_empty[1]));
+          mma_commit_by(leader, smem_u32(&sm.q_empty[qb]));
+          if (pair) mma_commit_by(leader, smem_u32(&sm.q_empty[1]));
         };
         const uint32_t oph = (seg & 1) ^ 1;
         if (pair) {
-          if (!(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 533))) break;
+          if (!(ok = warp_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 533))) break;
           tc_fence_after();
           issue_s(0, 0, 0, ring.st, nothing);
           issue_s(1, 1, 1, ring.st, nothing);
-          mma_commit(smem_u32(&sm.kv_empty[ring.st]));
+          mma_commit_by(leader, smem_u32(&sm.kv_empty[ring.st]));
           ring.advance();
           if (nt == 1) q_release();
           for (int j = 0; j < nt; ++j) {
@@ -888,10 +891,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (!(ok = wait_v(j, dirty))) break;
             const int sv = ring.st;
             ring.advance();
-            if (!kJoint<D> && more && !(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 534))) break;
+            if (!kJoint<D> && more && !(ok = warp_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 534))) break;
             const int sk = kJoint<D> ? sv : ring.st;
-            if (j == 0 && !(ok = mbar_wait(smem_u32(&sm.o_empty[0]), oph, abort_flag, lim, 535))) break;
-            if (j == 0 && !(ok = mbar_wait(smem_u32(&sm.o_empty[1]), oph, abort_flag, lim, 536))) break;
+            if (j == 0 && !(ok = warp_wait(smem_u32(&sm.o_empty[0]), oph, abort_flag, lim, 535))) break;
+            if (j == 0 && !(ok = warp_wait(smem_u32(&sm.o_empty[1]), oph, abort_flag, lim, 536))) break;
             if (!(ok = wait_p(0, 537))) break;
             tc_fence_after();
             issue_pv(0, 0, sv, j == 0, nothing);
@@ -899,20 +902,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (!(ok = wait_p(1, 538))) break;
             tc_fence_after();
             issue_pv(1, 1, sv, j == 0, nothing);
-            if (!kJoint<D> || !more) mma_commit(smem_u32(&sm.kv_empty[sv]));
+            if (!kJoint<D> || !more) mma_commit_by(leader, smem_u32(&sm.kv_empty[sv]));
             if (more) {
               issue_s(1, 1, 1, sk, nothing);
-              mma_commit(smem_u32(&sm.kv_empty[sk]));
+              mma_commit_by(leader, smem_u32(&sm.kv_empty[sk]));
               if (!kJoint<D>) ring.advance();
               if (j + 2 == nt) q_release();
             }
           }
         } else {
           for (int j = 0; j < NB && j < nt; ++j) {
-            if (!(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 533))) break;
+            if (!(ok = warp_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 533))) break;
             tc_fence_after();
             issue_s(j & 1, j, qb, ring.st, nothing);
-            mma_commit(smem_u32(&sm.kv_empty[ring.st]));
+            mma_commit_by(leader, smem_u32(&sm.kv_empty[ring.st]));
             ring.advance();
           }
           if (!ok) break;
@@ -923,21 +926,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (!(ok = wait_v(j, dirty))) break;
             const int sv = ring.st;
             ring.advance();
-            if (j < 2 && !(ok = mbar_wait(smem_u32(&sm.o_empty[h]), oph, abort_flag, lim, 535))) break;
+            if (j < 2 && !(ok = warp_wait(smem_u32(&sm.o_empty[h]), oph, abort_flag, lim, 535))) break;
             if (!(ok = wait_p(h, 537))) break;
             tc_fence_after();
             k_ready = kJoint<D>;
             issue_pv(h, b, sv, j < 2, [&] { if (!kJoint<D>) k_ready = more && test_kv(); });
-            if (!kJoint<D> || !more) mma_commit(smem_u32(&sm.kv_empty[sv]));
+            if (!kJoint<D> || !more) mma_commit_by(leader, smem_u32(&sm.kv_empty[sv]));
             if (more) {
-              if (!k_ready && !(ok = mbar_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 534))) break;
+              if (!k_ready && !(ok = warp_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 534))) break;
               const int sk = kJoint<D> ? sv : ring.st;
               if (!kJoint<D>) ring.advance();
               issue_s((j + NB) & 1, b, qb, sk, [&] {
                 v_ready = test_kv();
                 p_ready = test_p(h ^ 1);
               });
-              mma_commit(smem_u32(&sm.kv_empty[sk]));
+              mma_commit_by(leader, smem_u32(&sm.kv_empty[sk]));
               if (j + NB + 1 == nt) q_release();
             }
           }
@@ -946,8 +949,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       // Every product lands before tensor memory is given back, however short the limit of the other waits and
       // whichever of them expired (in its own loop, or for a segment).
-      mma_commit(smem_u32(&sm.drain));
-      if (!mbar_wait_quiesce(smem_u32(&sm.drain), 0, a.drain_limit) && ok && segs.ok) {
+      mma_commit_by(leader, smem_u32(&sm.drain));
+      if (!__all_sync(0xffffffffu, mbar_wait_quiesce(smem_u32(&sm.drain), 0, a.drain_limit)) && ok && segs.ok) {
         *abort_flag = 1;
         ra_record_error(RA_ERR_TIMEOUT, 539);
       }
@@ -1082,7 +1085,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       int b = h;                           // score tile
       for (int j = pair ? 0 : h; j < nt; j += step) {
         const int use = turn(h, s_cnt);
-        if (!(ok = warp_wait(smem_u32(&sm.s_full[use]), phase(s_cnt), abort_flag, lim, 550 + h))) break;
+        if (!(ok = warp_wait_first(smem_u32(&sm.s_full[use]), phase(s_cnt), abort_flag, lim, 550 + h))) break;
         ++s_cnt;
         tc_fence_after();
         const uint32_t colS = (NB == 3 ? b : h) * BN;

@@ -309,10 +309,6 @@ __global__ void __launch_bounds__(kPlanThreads) grad_prepare_kernel(const __grid
 }
 
 // ------------------------------------------------------------------ pieces of both kernels
-__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
-}
-
 // One arrival for a warp, whose lanes have all done what it stands for.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();
@@ -526,6 +522,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   } else if (warp == 1) {
     // ============================================================ products
     {
+      // The whole warp runs this, with one lane elected to issue: operands are then in uniform registers.  Issued by a branch
+      // of one thread, a product of 8 instructions took it some 560 cycles whatever its size.
       const uint32_t leader = elect_one();
       Ring<KS> kr, kd;                  // K tile of the next S, of the next dQ
       Ring<VS> vr;
@@ -670,7 +668,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       uint64_t sum2 = f2pack(0.f, 0.f);
       for (int j = 0; j < it.nt; ++j) {
         const uint32_t b = s_n & 1;
-        if (!(ok = warp_wait(smem_u32(&sm.s_full[b]), (s_n >> 1) & 1, abort_flag, lim, 940))) break;
+        if (!(ok = warp_wait_first(smem_u32(&sm.s_full[b]), (s_n >> 1) & 1, abort_flag, lim, 940))) break;
         tc_fence_after();
         const uint32_t s_addr = t_lane + kColS + b * BN + 32 * h;
         uint32_t x[32], y[32], pk[16];
@@ -1138,7 +1136,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         // the diagonal, the window's far end for the tile's first key, the sequence's end
         const bool masked = qt == it.k || BM * qt + BM > it.n || (!tile_sinks && BM * (qt - it.k) + BM > a.window);
         if (!(ok = warp_wait(smem_u32(&sm.x_full[xr.st]), xr.ph, abort_flag, lim, 980))) break;
-        if (!(ok = warp_wait(smem_u32(&sm.s_full), it_n & 1, abort_flag, lim, 981))) break;
+        if (!(ok = warp_wait_first(smem_u32(&sm.s_full), it_n & 1, abort_flag, lim, 981))) break;
         tc_fence_after();
         const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sm.neg_lse[xr.st] + 32 * h);
         const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(sm.neg_delta[xr.st] + 32 * h);
