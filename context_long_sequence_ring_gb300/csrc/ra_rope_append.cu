@@ -6,11 +6,10 @@
 // rotation of ra_rope_turn.cuh and the place of x of ra_paged.cuh.
 //
 // One launch in place of four (the rotation of Q, that of K, the slot mapping, the
-// scatter), so that K passes through the chip once.  A thread owns a "unit" of a
-// token, a word of pairs (interleaved), a word of real parts with its partner of
-// imaginary parts (half) or a word that is copied, for up to 8 of Q's, K's or V's
-// heads: it issues all their loads, finds the token's request, place and angles
-// meanwhile, and then turns and stores each head.
+// scatter), so that K passes through the chip once.  A block takes a run of
+// tokens, a few at a time: one thread each finds a token's request and place, all of
+// them form the angles of the tokens' pairs once (for all heads, in shared memory), and
+// then take the words of their heads, whose first loads have been in flight since the start.
 #include <algorithm>
 #include <type_traits>
 
@@ -22,7 +21,9 @@ RA_DEFINE_ERROR_FETCH(fetch_error_rope_append)
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendHeads = 8;   // heads of a thread, at most
+constexpr int kAppendBlocks = 4;  // of an SM
+constexpr int kTokens = 8;        // at a time, at most
+constexpr int kAppendHeads = 2;   // of a thread, whose loads are in flight together
 
 struct AppendParams : Turns {
   Paged c;
@@ -31,176 +32,256 @@ struct AppendParams : Turns {
   const int32_t *qsl, *ctx;
   const int32_t* positions;      // of axis a: positions + a * T; NULL: the token's place in its context
   int64_t T, k_rs, k_hs, v_rs, v_hs, q_rs, q_hs, qo_rs, qo_hs;
-  int64_t t0;                    // tokens t0 .. t0 + n_t - 1 of this launch
-  int R, Hq, d, rot, n_t;
-  int turn_units, per_token, k_first, v_first, heads;   // threads of a token: Q's, from k_first on K's, from v_first on V's
-  FastDiv by_token, by_q, by_k, by_v;                   // by the threads of a token, the units of a head of each
+  int R, d, rot;
+  int tokens, run;               // of a block at a time, and in all
+  // a unit is a word of pairs (interleaved), a word of real parts with its partner of imaginary parts (half) or a word that
+  // is copied; a thread's work is a unit of one or two heads: of a token Q's, from k_first on K's, from v_first on V's
+  int turn_units, per_token, k_first, v_first, heads, Hq;
+  FastDiv by_token, by_q, by_k, by_v, by_pairs;   // by the work of a token, the units of a head of each; the pairs of a head
 };
 
+// N values aligned to A bytes, and as fp32 ones (rounded to nearest even on the way back).
 template <typename T, int N, int A>
 struct alignas(A) Vec {
   T x[N];
 };
+template <int N, int A>
+__device__ __forceinline__ void unpack(const Vec<float, N, A>& v, float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = v.x[i];
+}
+template <int N, int A>
+__device__ __forceinline__ void pack(Vec<float, N, A>& v, const float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v.x[i] = f[i];
+}
+template <int N, int A>
+__device__ __forceinline__ void unpack(const Vec<__nv_bfloat16, N, A>& v, float (&f)[N]) {
+  if constexpr (A >= 4) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __bfloat162float(v.x[i]);
+  }
+}
+template <int N, int A>
+__device__ __forceinline__ void pack(Vec<__nv_bfloat16, N, A>& v, const float (&f)[N]) {
+  if constexpr (A >= 4) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v.x[i] = __float2bfloat16_rn(f[i]);
+  }
+}
 
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_float(float& y, float x) { y = x; }
-__device__ __forceinline__ void from_float(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
+// What the threads of a block know of a token.
+struct TokenPlace {
+  int64_t row;                   // of the cache, for head 0; -1: not stored
+  int live;                      // of a request
+};
 
 // N values to a word, aligned to A bytes; P pairs to a unit that turns.
 template <typename T, int N, int A, bool INTER, bool AXES>
-__global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(const __grid_constant__ AppendParams p) {
   using V = Vec<T, N, A>;
   constexpr int P = INTER ? N / 2 : N;
-  const uint32_t w = blockIdx.x * kAppendThreads + threadIdx.x;
-  const bool used = w < static_cast<uint32_t>(p.n_t) * p.per_token;
-  int sub = 0;
-  const int64_t t = p.t0 + (used ? p.by_token.div(static_cast<int>(w), sub) : 0);
-  // Q, K or V, the unit of a head and the first head
-  const int what = sub < p.k_first ? 0 : sub < p.v_first ? 1 : 2;
-  int u;
-  const int h0 = (what == 0 ? p.by_q.div(sub, u) : what == 1 ? p.by_k.div(sub - p.k_first, u) : p.by_v.div(sub - p.v_first, u)) * p.heads;
-  const int nh = min((what == 0 ? p.Hq : p.c.Hkv) - h0, p.heads);
-  const bool turns = what < 2 && u < p.turn_units;
-  const int half = p.rot / 2;
-  const int e0 = what == 2 ? u * N : turns ? u * N : p.rot + (u - p.turn_units) * N;
-  const int64_t rs = what == 0 ? p.q_rs : what == 1 ? p.k_rs : p.v_rs, hs = what == 0 ? p.q_hs : what == 1 ? p.k_hs : p.v_hs;
-  const T* x = static_cast<const T*>(what == 0 ? p.q : what == 1 ? p.k : p.v) + t * rs + h0 * hs + e0;
+  __shared__ TokenPlace place[kTokens];
+  __shared__ float position[kTokens][kMaxAxes];
+  __shared__ float2 turns[kTokens][kMaxPairs];   // (cos, sin) of pair i of unit u at i * turn_units + u
+  const int half = p.rot / 2, tid = threadIdx.x;
+  const int64_t t_first = static_cast<int64_t>(blockIdx.x) * p.run, t_end = min(p.T, t_first + p.run);
+
+  // A thread's work: unit e of heads h0 .. h0 + nh - 1.
+  int token, what, e, h0, nh;
+  bool turn_it;
   V a[kAppendHeads], b[kAppendHeads];
-  if (used) {
+  auto load = [&](int64_t t0, int i, int all) {
+    nh = 0;
+    if (i >= all) return;
+    int sub;
+    token = p.by_token.div(i, sub);
+    what = sub < p.k_first ? 0 : sub < p.v_first ? 1 : 2;
+    h0 = (what == 0 ? p.by_q.div(sub, e) : what == 1 ? p.by_k.div(sub - p.k_first, e) : p.by_v.div(sub - p.v_first, e)) * p.heads;
+    nh = min((what == 0 ? p.Hq : p.c.Hkv) - h0, p.heads);
+    turn_it = what < 2 && e < p.turn_units;
+    const int64_t t = t0 + token, hs = what == 0 ? p.q_hs : what == 1 ? p.k_hs : p.v_hs;
+    const T* x = (what == 0 ? static_cast<const T*>(p.q) + t * p.q_rs
+                            : what == 1 ? static_cast<const T*>(p.k) + t * p.k_rs : static_cast<const T*>(p.v) + t * p.v_rs) +
+                 h0 * hs + (what == 2 || turn_it ? e * N : p.rot + (e - p.turn_units) * N);
 #pragma unroll
     for (int j = 0; j < kAppendHeads; ++j)
       if (j < nh) {
         a[j] = *reinterpret_cast<const V*>(x + j * hs);
-        if (!INTER && turns) b[j] = *reinterpret_cast<const V*>(x + j * hs + half);
+        if (!INTER && turn_it) b[j] = *reinterpret_cast<const V*>(x + j * hs + half);
       }
-  }
-  // the request of the block's first token, by all threads together; from there each thread walks to its own
-  const int64_t first = p.t0 + p.by_token.div(static_cast<int>(blockIdx.x * kAppendThreads));
+  };
+  auto store = [&](int64_t t0) {
+    if (nh == 0) return;
+    T* y;
+    int64_t hs;
+    if (what == 0) {
+      if (!place[token].live) return;
+      y = static_cast<T*>(p.q_out) + (t0 + token) * p.qo_rs;
+      hs = p.qo_hs;
+    } else {
+      const int64_t row = place[token].row;
+      if (row < 0) return;
+      y = static_cast<T*>(what == 1 ? p.k_cache : p.v_cache) + row * p.d;
+      hs = static_cast<int64_t>(p.c.bs) * p.d;
+    }
+    y += h0 * hs + (what == 2 || turn_it ? e * N : p.rot + (e - p.turn_units) * N);
+    if (!turn_it) {
+#pragma unroll
+      for (int j = 0; j < kAppendHeads; ++j)
+        if (j < nh) *reinterpret_cast<V*>(y + j * hs) = a[j];
+      return;
+    }
+    float c[P], s[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const float2 t = turns[token][i * p.turn_units + e];
+      c[i] = t.x;
+      s[i] = t.y;
+    }
+#pragma unroll
+    for (int j = 0; j < kAppendHeads; ++j) {
+      if (j >= nh) break;
+      float f[N], o[N];
+      V v;
+      unpack(a[j], f);
+      if (INTER) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          o[2 * i % N] = turn_re(f[2 * i % N], f[(2 * i + 1) % N], c[i], s[i]);
+          o[(2 * i + 1) % N] = turn_im(f[2 * i % N], f[(2 * i + 1) % N], c[i], s[i]);
+        }
+        pack(v, o);
+        *reinterpret_cast<V*>(y + j * hs) = v;
+      } else {
+        float g[N], o2[N];
+        unpack(b[j], g);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          o[i] = turn_re(f[i], g[i], c[i % P], s[i % P]);
+          o2[i] = turn_im(f[i], g[i], c[i % P], s[i % P]);
+        }
+        pack(v, o);
+        *reinterpret_cast<V*>(y + j * hs) = v;
+        pack(v, o2);
+        *reinterpret_cast<V*>(y + j * hs + half) = v;
+      }
+    }
+  };
+  load(t_first, tid, static_cast<int>(min(static_cast<int64_t>(p.tokens), t_end - t_first)) * p.per_token);
+  // the request of the block's first token, by all threads together
   int r = 0;
   for (int base = 0; base < p.R; base += kAppendThreads) {
-    const int i = base + threadIdx.x;
+    const int i = base + tid;
     int32_t end = INT32_MAX;
     if (i < p.R) {
       end = p.qsl[i + 1];
-      if (blockIdx.x == 0 && p.t0 == 0) {
+      if (blockIdx.x == 0) {
         const int32_t begin = p.qsl[i];
         if (begin < 0 || end < begin || end > p.T) ra_record_error(RA_ERR_DEVICE_BOUNDS, 700);
       }
     }
-    r += __syncthreads_count(i < p.R && end <= first);
+    r += __syncthreads_count(i < p.R && end <= t_first);
   }
-  if (!used) return;
-  while (r < p.R && p.qsl[r + 1] <= t) ++r;
-  if (r >= p.R || t < p.qsl[r]) return;   // a token of no request
-  const int64_t place = static_cast<int64_t>(p.ctx[r]) - (p.qsl[r + 1] - t);
-  T* y;
-  int64_t yhs;
-  if (what == 0) {
-    y = static_cast<T*>(p.q_out) + t * p.qo_rs + h0 * p.qo_hs + e0;
-    yhs = p.qo_hs;
-  } else {
-    if (place < 0 || place >= (int64_t(1) << 30) || place >= static_cast<int64_t>(p.c.max_vb) * p.c.V) {
-      ra_record_error(RA_ERR_DEVICE_BOUNDS, 701);
-      return;
-    }
-    const int64_t row = paged_row(p.c, r, static_cast<int>(place), h0, 702);
-    if (row < 0) return;
-    y = static_cast<T*>(what == 1 ? p.k_cache : p.v_cache) + row * p.d + e0;
-    yhs = static_cast<int64_t>(p.c.bs) * p.d;
-  }
-  float c[P], s[P];
-  if (turns) {
-    float m = 0.f;
-    int last = -1;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int ax = AXES ? p.axis[u * P + i] : 0;
-      if (ax != last) {
-        if (p.positions) {
-          m = position_at(p.positions, ax * p.T + t, 703);
-        } else if (place < 0 || place >= kPositionLimit) {
-          ra_record_error(RA_ERR_DEVICE_BOUNDS, 703);
-        } else {
-          m = static_cast<float>(place);
-        }
+  for (int64_t t0 = t_first; t0 < t_end; t0 += p.tokens) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(p.tokens), t_end - t0)), all = n * p.per_token;
+    if (t0 > t_first) load(t0, tid, all);
+    if (tid < n) {
+      const int64_t t = t0 + tid;
+      while (r < p.R && p.qsl[r + 1] <= t) ++r;
+      TokenPlace at{-1, 0};
+      int64_t x = -1;
+      if (r < p.R && t >= p.qsl[r]) {
+        at.live = 1;
+        x = static_cast<int64_t>(p.ctx[r]) - (p.qsl[r + 1] - t);
+        if (x < 0 || x >= (int64_t(1) << 30) || x >= static_cast<int64_t>(p.c.max_vb) * p.c.V)
+          ra_record_error(RA_ERR_DEVICE_BOUNDS, 701);
+        else
+          at.row = paged_row(p.c, r, static_cast<int>(x), 0, 702);
       }
-      last = ax;
-      turn(p, u * P + i, m, c[i], s[i]);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kAppendHeads; ++j) {
-    if (j >= nh) break;
-    T* out = y + j * yhs;
-    if (!turns) {
-      *reinterpret_cast<V*>(out) = a[j];
-      continue;
-    }
-    V o, o2;
-    if (INTER) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float re = to_float(a[j].x[2 * i]), im = to_float(a[j].x[2 * i + 1]);
-        from_float(o.x[2 * i], turn_re(re, im, c[i], s[i]));
-        from_float(o.x[2 * i + 1], turn_im(re, im, c[i], s[i]));
+      place[tid] = at;
+      if (p.turn_units > 0 && !p.positions) {
+        const bool in = x >= 0 && x < kPositionLimit;
+        if (at.live && !in) ra_record_error(RA_ERR_DEVICE_BOUNDS, 703);
+        position[tid][0] = in ? static_cast<float>(x) : 0.f;
       }
-      *reinterpret_cast<V*>(out) = o;
-    } else {
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float re = to_float(a[j].x[i]), im = to_float(b[j].x[i]);
-        from_float(o.x[i], turn_re(re, im, c[i], s[i]));
-        from_float(o2.x[i], turn_im(re, im, c[i], s[i]));
-      }
-      *reinterpret_cast<V*>(out) = o;
-      *reinterpret_cast<V*>(out + half) = o2;
     }
+    __syncthreads();
+    if (p.turn_units > 0) {
+      for (int i = tid; i < n * half; i += kAppendThreads) {
+        int pair;
+        const int token = p.by_pairs.div(i, pair);
+        if (!place[token].live) continue;
+        const float m = p.positions ? position_at(p.positions, (AXES ? p.axis[pair] : 0) * p.T + t0 + token, 703) : position[token][0];
+        float2 cs;
+        turn(p, pair, m, cs.x, cs.y);
+        turns[token][pair % P * p.turn_units + pair / P] = cs;
+      }
+      __syncthreads();
+    }
+    for (int i = tid; i < all;) {
+      store(t0);
+      i += kAppendThreads;
+      load(t0, i, all);
+    }
+    __syncthreads();
   }
 }
 
-// Launches the kernel on words of N values aligned to A bytes; more than 2^31 threads in several launches.
+// Launches the kernel on words of N values aligned to A bytes.
 template <typename T, int N, int A>
-ra_status launch_append(AppendParams& p, bool inter, bool axes, cudaStream_t stream) {
-  const int Hkv = p.c.Hkv;
+ra_status launch_append(AppendParams& p, int32_t Hq, bool inter, bool axes, cudaStream_t stream) {
+  const int64_t Hkv = p.c.Hkv;
   p.turn_units = inter ? p.rot / N : p.rot / 2 / N;
   const bool q_moves = p.q && p.q != p.q_out;             // in place the rest of a head stays where it is
-  const int k_units = p.turn_units + (p.d - p.rot) / N, q_units = p.q ? p.turn_units + (q_moves ? (p.d - p.rot) / N : 0) : 0;
-  const int v_units = p.d / N;
-  // Heads of a thread: 8 where that leaves about 1024 threads to each SM, else fewer for latency.
-  const int64_t want = 152 * 1024;
-  int64_t per = 0;
-  for (p.heads = kAppendHeads;; p.heads /= 2) {
-    per = q_units * ra::ceil_div(p.Hq, p.heads) + (static_cast<int64_t>(k_units) + v_units) * ra::ceil_div(Hkv, p.heads);
-    if (p.heads == 1 || p.T * per >= want) break;
+  const int64_t k_units = p.turn_units + (p.d - p.rot) / N, v_units = p.d / N;
+  const int64_t q_units = p.q ? p.turn_units + (q_moves ? (p.d - p.rot) / N : 0) : 0;
+  // one round of blocks that share the tokens out; few tokens: one at a time, a block each, with fewer heads to a thread
+  p.run = static_cast<int>(ra::ceil_div(p.T, 152 * kAppendBlocks));
+  p.tokens = std::min(p.run, kTokens);
+  for (p.heads = kAppendHeads; p.heads > 1; p.heads /= 2) {
+    const int64_t work = q_units * ra::ceil_div(Hq, p.heads) + (k_units + v_units) * ra::ceil_div(Hkv, p.heads);
+    if (work * p.tokens >= kAppendThreads) break;
   }
-  p.per_token = static_cast<int>(per);
+  p.Hq = p.q ? Hq : 0;
   p.k_first = static_cast<int>(q_units * ra::ceil_div(p.Hq, p.heads));
   p.v_first = p.k_first + static_cast<int>(k_units * ra::ceil_div(Hkv, p.heads));
-  p.by_token = fast_div(per);
-  p.by_q = fast_div(std::max(1, q_units));
+  p.per_token = p.v_first + static_cast<int>(v_units * ra::ceil_div(Hkv, p.heads));
+  p.by_token = fast_div(p.per_token);
+  p.by_q = fast_div(std::max<int64_t>(1, q_units));
   p.by_k = fast_div(k_units);
   p.by_v = fast_div(v_units);
-  const int64_t most = ((int64_t(1) << 31) - kAppendThreads) / per;
-  for (p.t0 = 0; p.t0 < p.T; p.t0 += most) {
-    p.n_t = static_cast<int>(std::min(most, p.T - p.t0));
-    const unsigned blocks = static_cast<unsigned>(ra::ceil_div(p.n_t * per, kAppendThreads));
-    auto go = [&](auto in, auto ax) {
-      append_kernel<T, N, A, decltype(in)::value, decltype(ax)::value><<<blocks, kAppendThreads, 0, stream>>>(p);
-    };
-    if constexpr (N % 2 == 0) {
-      if (inter && axes) go(std::true_type{}, std::true_type{});
-      if (inter && !axes) go(std::true_type{}, std::false_type{});
-    }
-    if (!inter && axes) go(std::false_type{}, std::true_type{});
-    if (!inter && !axes) go(std::false_type{}, std::false_type{});
-    RA_LAUNCH_CHECK("append_kernel");
+  p.by_pairs = fast_div(std::max(1, p.rot / 2));
+  const unsigned blocks = static_cast<unsigned>(ra::ceil_div(p.T, p.run));
+  auto go = [&](auto in, auto ax) {
+    append_kernel<T, N, A, decltype(in)::value, decltype(ax)::value><<<blocks, kAppendThreads, 0, stream>>>(p);
+  };
+  if constexpr (N % 2 == 0) {
+    if (inter && axes) go(std::true_type{}, std::true_type{});
+    if (inter && !axes) go(std::true_type{}, std::false_type{});
   }
+  if (!inter && axes) go(std::false_type{}, std::true_type{});
+  if (!inter && !axes) go(std::false_type{}, std::false_type{});
+  RA_LAUNCH_CHECK("append_kernel");
   return RA_OK;
 }
 
 template <typename T>
-ra_status launch_append_type(AppendParams& p, bool inter, bool axes, cudaStream_t stream) {
+ra_status launch_append_type(AppendParams& p, int32_t Hq, bool inter, bool axes, cudaStream_t stream) {
   constexpr int es = sizeof(T);
   // whole words: every address that is read or written as one is a multiple of its size
   auto words = [&](int bytes) {
@@ -211,13 +292,13 @@ ra_status launch_append_type(AppendParams& p, bool inter, bool axes, cudaStream_
     if (p.T > 1) m |= static_cast<uint64_t>(p.k_rs * es) | static_cast<uint64_t>(p.v_rs * es);
     if (p.T > 1 && p.q) m |= static_cast<uint64_t>(p.q_rs * es) | static_cast<uint64_t>(p.qo_rs * es);
     if (p.c.Hkv > 1) m |= static_cast<uint64_t>(p.k_hs * es) | static_cast<uint64_t>(p.v_hs * es);
-    if (p.q && p.Hq > 1) m |= static_cast<uint64_t>(p.q_hs * es) | static_cast<uint64_t>(p.qo_hs * es);
+    if (p.q && Hq > 1) m |= static_cast<uint64_t>(p.q_hs * es) | static_cast<uint64_t>(p.qo_hs * es);
     return m % bytes == 0 && p.d % n == 0 && p.rot % n == 0 && (inter || (p.rot / 2) % n == 0);
   };
-  if (words(16)) return launch_append<T, 16 / es, 16>(p, inter, axes, stream);
-  if (words(8)) return launch_append<T, 8 / es, 8>(p, inter, axes, stream);
+  if (words(16)) return launch_append<T, 16 / es, 16>(p, Hq, inter, axes, stream);
+  if (words(8)) return launch_append<T, 8 / es, 8>(p, Hq, inter, axes, stream);
   // element by element: a pair to a unit (d is even here, the rows of the cache being 16-byte words)
-  return inter ? launch_append<T, 2, es>(p, inter, axes, stream) : launch_append<T, 1, es>(p, inter, axes, stream);
+  return inter ? launch_append<T, 2, es>(p, Hq, inter, axes, stream) : launch_append<T, 1, es>(p, Hq, inter, axes, stream);
 }
 
 }  // namespace
@@ -237,8 +318,8 @@ extern "C" ra_status ra_cp_rope_append(const void* k, int64_t k_row_stride, int6
   RA_REQUIRE(dt == RA_BF16 || dt == RA_F32, "dtype must be RA_BF16 or RA_F32");
   RA_REQUIRE(d >= 1 && d <= 1024, "1 <= d <= 1024 required");
   RA_REQUIRE(!q || Hq >= 1, "Hq must be >= 1");
-  RA_REQUIRE(static_cast<int64_t>(Hkv) * d < (int64_t(1) << 29) && (!q || static_cast<int64_t>(Hq) * d < (int64_t(1) << 29)),
-             "heads * d must be below 2^29");   // threads of a token: 32 bits
+  RA_REQUIRE(static_cast<int64_t>(Hkv) * d < (int64_t(1) << 26) && (!q || static_cast<int64_t>(Hq) * d < (int64_t(1) << 26)),
+             "heads * d must be below 2^26");   // units of kTokens tokens: 31 bits
   const int es = dt == RA_BF16 ? 2 : 4;
   if (d * es % 16 != 0) return ra::fail(RA_ERR_UNSUPPORTED, "d*elem_size must be a multiple of 16");
   RA_REQUIRE(T >= 0 && T < (int64_t(1) << 31), "T must be in [0, 2^31)");
@@ -288,8 +369,8 @@ extern "C" ra_status ra_cp_rope_append(const void* k, int64_t k_row_stride, int6
   p.k_rs = k_row_stride; p.k_hs = k_head_stride; p.v_rs = v_row_stride; p.v_hs = v_head_stride;
   p.q_rs = q_row_stride; p.q_hs = q_head_stride; p.qo_rs = q_out_row_stride; p.qo_hs = q_out_head_stride;
   p.qsl = query_start_loc; p.ctx = ctx_lens; p.positions = positions;
-  p.T = T; p.R = R; p.Hq = q ? Hq : 1; p.d = d; p.rot = inv_freq ? rot : 0;
+  p.T = T; p.R = R; p.d = d; p.rot = inv_freq ? rot : 0;
   const bool inter = inv_freq && style == RA_ROPE_INTERLEAVED;
-  return dt == RA_BF16 ? launch_append_type<__nv_bfloat16>(p, inter, inv_freq && axis, stream)
-                       : launch_append_type<float>(p, inter, inv_freq && axis, stream);
+  return dt == RA_BF16 ? launch_append_type<__nv_bfloat16>(p, Hq, inter, inv_freq && axis, stream)
+                       : launch_append_type<float>(p, Hq, inter, inv_freq && axis, stream);
 }

@@ -263,9 +263,11 @@ __device__ void make_lists(const GradArgs& a) {
   }
 }
 
-// Block 0: the lists.  The others: a warp takes 32 tokens of a head, half a warp a row at a time.
+// Block 0: the lists.  The others: a warp takes 8 tokens of a head, D/8 lanes a row (8 and not 32, so that the last of a
+// warp's tasks is short).
 template <int D>
 __global__ void __launch_bounds__(kPlanThreads) grad_prepare_kernel(const __grid_constant__ GradArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) {
     make_lists(a);
     return;
@@ -273,37 +275,40 @@ __global__ void __launch_bounds__(kPlanThreads) grad_prepare_kernel(const __grid
   constexpr int LANES = D / 8;                                      // of a row, 16 bytes each
   constexpr int ROWS = 32 / LANES;
   const int lane = threadIdx.x & 31;
-  const int64_t groups = (a.T + 31) / 32;
+  constexpr int TASK = 8;
+  const int64_t groups = (a.T + TASK - 1) / TASK;
   const int64_t w0 = static_cast<int64_t>(blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5);
   for (int64_t w = w0; w < groups * a.Hq; w += static_cast<int64_t>(gridDim.x - 1) * (kPlanThreads / 32)) {
-    const int64_t t0 = w / a.Hq * 32;
+    const int64_t t0 = w / a.Hq * TASK;
     const int h = static_cast<int>(w % a.Hq);
-    float mine = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < 32; i += ROWS) {
-      const int64_t t = t0 + i + lane / LANES;
-      float s = 0.f;
-      if (t < a.T) {
-        const int64_t at = (t * a.Hq + h) * D + (lane % LANES) * 8;
-        const uint4 x = *reinterpret_cast<const uint4*>(a.o + at), y = *reinterpret_cast<const uint4*>(a.d_o + at);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    const int64_t mine_t = t0 + (lane % TASK);
+    const float lse = mine_t < a.T ? a.lse[mine_t * a.Hq + h] : 0.f;
+    uint4 x[TASK / ROWS], y[TASK / ROWS];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s += __uint_as_float(xs[e] << 16) * __uint_as_float(ys[e] << 16) +
-               __uint_as_float(xs[e] & 0xffff0000u) * __uint_as_float(ys[e] & 0xffff0000u);
-      }
+    for (int i = 0; i < TASK / ROWS; ++i) {
+      const int64_t t = t0 + i * ROWS + lane / LANES, at = (t * a.Hq + h) * D + (lane % LANES) * 8;
+      x[i] = t < a.T ? *reinterpret_cast<const uint4*>(a.o + at) : make_uint4(0, 0, 0, 0);
+      y[i] = t < a.T ? *reinterpret_cast<const uint4*>(a.d_o + at) : make_uint4(0, 0, 0, 0);
+    }
+    float mine = 0.f;
+#pragma unroll
+    for (int i = 0; i < TASK / ROWS; ++i) {
+      const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, ys[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s += __uint_as_float(xs[e] << 16) * __uint_as_float(ys[e] << 16) +
+             __uint_as_float(xs[e] & 0xffff0000u) * __uint_as_float(ys[e] & 0xffff0000u);
 #pragma unroll
       for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      // lane i + r keeps the row of the r-th part of the warp
-      const float got = __shfl_sync(0xffffffffu, s, (lane - i) * LANES & 31);
-      if (lane >= i && lane < i + ROWS) mine = got;
+      // lane i * ROWS + r keeps the row of the r-th part of the warp
+      const float got = __shfl_sync(0xffffffffu, s, (lane - i * ROWS) * LANES & 31);
+      if (lane / ROWS == i) mine = got;
     }
-    const int64_t t = t0 + lane;
-    if (t < a.T) {
-      const float lse = a.lse[t * a.Hq + h];
+    if (lane < TASK && mine_t < a.T) {
       // a row that sees nothing has no weight
-      a.neg_lse[h * a.T + t] = lse == -CUDART_INF_F ? -CUDART_INF_F : -lse * 1.4426950408889634f;
-      a.neg_delta[h * a.T + t] = -mine;
+      a.neg_lse[h * a.T + mine_t] = lse == -CUDART_INF_F ? -CUDART_INF_F : -lse * 1.4426950408889634f;
+      a.neg_delta[h * a.T + mine_t] = -mine;
     }
   }
 }
@@ -441,6 +446,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // Items in rounds, every other one backwards: where they get longer along a sequence the CTAs' sums stay even.
   const int items = a.plan->row_tiles * a.Hkv;
   auto item_of = [&](int m) {
@@ -895,6 +902,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   KeyIter items(a);
   KeyItem it;
 
@@ -1237,23 +1246,41 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 // Block (c, y) sums the parts of the key tile that part c starts, if it does, four columns of all rows at a time, in order.
 template <int D>
 __global__ void __launch_bounds__(BN) grad_join_kernel(const __grid_constant__ GradArgs a) {
+  __shared__ int slots[kGradCtas], counts[BN / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Shared s = a.shared[blockIdx.x];
   if (!s.used) return;
-  const int row = threadIdx.x, key = BN * s.k + row;
+  const int row = threadIdx.x, lane = row & 31, key = BN * s.k + row;
   const int64_t cost = s.its + kOver;
+  int n = 0;
+  for (int c0 = blockIdx.x; c0 < kGradCtas; c0 += BN) {
+    const int c = c0 + row;
+    int it0 = 0, end = 0;
+    if (c < kGradCtas) {
+      // as KeyIter cuts it
+      const int64_t lo = a.plan->lo[c], hi = a.plan->lo[c + 1], from = lo - s.at - kOver, to = hi - s.at - kOver;
+      if (lo < s.at + cost) {
+        it0 = from > 0 ? static_cast<int>(from < s.its ? from : s.its) : 0;
+        end = hi >= s.at + cost ? s.its : to > 0 ? static_cast<int>(to < s.its ? to : s.its) : 0;
+      }
+    }
+    const unsigned b = __ballot_sync(0xffffffffu, end > it0);
+    if (lane == 0) counts[row >> 5] = __popc(b);
+    __syncthreads();
+    int at = n + __popc(b & ((1u << lane) - 1));
+    for (int w = 0; w < BN / 32; ++w) {
+      if (w < row >> 5) at += counts[w];
+      n += counts[w];
+    }
+    if (end > it0) slots[at] = 2 * c + (it0 == 0 ? 1 : 0);
+    __syncthreads();
+  }
   for (int u = blockIdx.y; u < 2 * (D / 4); u += gridDim.y) {
     const int h = u / (D / 4), col = u - h * (D / 4);
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = blockIdx.x; c < kGradCtas; ++c) {
-      const int64_t lo = a.plan->lo[c], hi = a.plan->lo[c + 1];
-      if (lo >= s.at + cost) break;
-      // as KeyIter cuts it
-      const int64_t from = lo - s.at - kOver, to = hi - s.at - kOver;
-      const int it0 = from > 0 ? static_cast<int>(from < s.its ? from : s.its) : 0;
-      const int end = hi >= s.at + cost ? s.its : to > 0 ? static_cast<int>(to < s.its ? to : s.its) : 0;
-      if (end <= it0) continue;
-      const float4 x = *reinterpret_cast<const float4*>(
-          a.parts + ((2 * static_cast<int64_t>(c) + (it0 == 0 ? 1 : 0)) * 2 + h) * (BN * D) + (col * BN + row) * 4);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(a.parts + (slots[i] * int64_t(2) + h) * (BN * D) + (col * BN + row) * 4);
       sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
     }
     if (key >= s.n) continue;
@@ -1307,19 +1334,31 @@ ra_status launch_grad(const void* q, int64_t q_rs, const void* k, int64_t k_rs, 
   if ((st = row_map(&mot, a.d_o, D, a.Hq, a.T, o_rs, 1, BM)) != RA_OK) return st;
   if ((st = row_map(&mkt, k, D, a.Hkv, a.T, k_rs, 1, BN)) != RA_OK) return st;
   if ((st = row_map(&mvt, v, D, a.Hkv, a.T, v_rs, 1, BN)) != RA_OK) return st;
-  const int64_t warps = (a.T + 31) / 32 * a.Hq;
+  const int64_t warps = (a.T + 7) / 8 * a.Hq;
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ra::ceil_div(warps, kPlanThreads / 32), 2 * 152)) + 1;
   grad_prepare_kernel<D><<<blocks, kPlanThreads, 0, stream>>>(a);
   RA_LAUNCH_CHECK("grad_prepare_kernel");
   const size_t rows = sizeof(RowSmem<D>), keys = sizeof(KeySmem<D>);
   RA_CUDA_TRY(cudaFuncSetAttribute(grad_q_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(rows)));
   RA_CUDA_TRY(cudaFuncSetAttribute(grad_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(keys)));
-  grad_q_kernel<D><<<kGradCtas, kGradThreads, rows, stream>>>(mq, mk, mv, mo, a);
-  RA_LAUNCH_CHECK("grad_q_kernel");
-  grad_kv_kernel<D><<<kGradCtas, kGradThreads, keys, stream>>>(mqt, mkt, mvt, mot, a);
-  RA_LAUNCH_CHECK("grad_kv_kernel");
-  grad_join_kernel<D><<<dim3(kGradCtas, 16), BN, 0, stream>>>(a);
-  RA_LAUNCH_CHECK("grad_join_kernel");
+  // Each kernel comes up while the one before it ends, and waits for its end before it reads what it wrote.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kGradCtas);
+  cfg.blockDim = dim3(kGradThreads);
+  cfg.dynamicSmemBytes = rows;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  RA_CUDA_TRY(cudaLaunchKernelEx(&cfg, grad_q_kernel<D>, mq, mk, mv, mo, a));
+  cfg.dynamicSmemBytes = keys;
+  RA_CUDA_TRY(cudaLaunchKernelEx(&cfg, grad_kv_kernel<D>, mqt, mkt, mvt, mot, a));
+  cfg.gridDim = dim3(kGradCtas, 16);
+  cfg.blockDim = dim3(BN);
+  cfg.dynamicSmemBytes = 0;
+  RA_CUDA_TRY(cudaLaunchKernelEx(&cfg, grad_join_kernel<D>, a));
   return RA_OK;
 }
 

@@ -732,7 +732,7 @@ ra_status ra_cp_evict(void* k_cache, void* v_cache, float* weights, const int32_
  * Tokens of no request are not stored and their q_out is left as it was.  A slot that
  * several tokens of a call have (requests that share a block) gets one of them.
  * Requires d <= 1024, d * element size a multiple of 16 bytes (RA_ERR_UNSUPPORTED
- * otherwise), heads * d < 2^29, T < 2^31, sizes of the cache as ra_cp_chunk_attn's but any
+ * otherwise), heads * d < 2^26, T < 2^31, sizes of the cache as ra_cp_chunk_attn's but any
  * block size.
  * Device bounds errors: a query_start_loc that decreases or leaves [0, T] (which tokens are
  * stored is not defined then), a token with x < 0, past the table or 2^30 (not stored), a
