@@ -253,6 +253,38 @@ struct Ring {
   }
 };
 
+// ------------------------------------------------------------------ epilogue
+// 32 accumulator columns of a row per lane, times f, as bf16 to out + at (at < 0: a row that is not stored), by a whole
+// warp.  Four lanes exchange 16 bytes each, so that a store writes 64 bytes of 8 rows instead of 16 of 32
+// (window attention of 16384 tokens, window 512: 203 us instead of 219).
+__device__ __forceinline__ void store_rows_bf16(__nv_bfloat16* out, int64_t at, const uint32_t (&x)[32], float f) {
+  const int lane = threadIdx.x & 31;
+  uint32_t w[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[i][e] = f2_bf16x2(__uint_as_float(x[8 * i + 2 * e]) * f, __uint_as_float(x[8 * i + 2 * e + 1]) * f);
+#pragma unroll
+  for (int k = 1; k < 4; k <<= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & k) continue;
+      const bool up = lane & k;       // keeps part i + k, gives part i
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, up ? w[i][e] : w[i + k][e], k);
+        if (up) w[i][e] = other; else w[i + k][e] = other;
+      }
+    }
+  // lane 4a + b holds part b of rows 4a .. 4a + 3
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t to = __shfl_sync(0xffffffffu, at, (lane & ~3) + i);
+    if (to >= 0) *reinterpret_cast<uint4*>(out + to + 8 * (lane & 3)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+  }
+}
+
 // ------------------------------------------------------------------ host side
 using EncodeTiledFn = decltype(&cuTensorMapEncodeTiled);
 

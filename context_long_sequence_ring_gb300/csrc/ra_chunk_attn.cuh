@@ -1170,22 +1170,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(y[i]) * f1);
           }
-          if (row_ok) {
-            if (whole && a.out_bf16) {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + orow * D + 32 * c4);
+          if (whole && a.out_bf16) {
+            store_rows_bf16(static_cast<__nv_bfloat16*>(a.o) + 32 * c4, row_ok ? orow * D : -1, x, 1.f);
+          } else if (row_ok) {
+            uint4* dst = reinterpret_cast<uint4*>((whole ? static_cast<float*>(a.o) + orow * D : po) + 32 * c4);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  w[e] = f2_bf16x2(__uint_as_float(x[8 * i + 2 * e]), __uint_as_float(x[8 * i + 2 * e + 1]));
-                dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>((whole ? static_cast<float*>(a.o) + orow * D : po) + 32 * c4);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-            }
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
         }
       }

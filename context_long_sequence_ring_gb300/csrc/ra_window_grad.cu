@@ -333,19 +333,11 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// 32 accumulator columns of a row to memory, times f.
+// 32 accumulator columns of a row per lane to memory, times f; at < 0: not stored.
 __device__ __forceinline__ void store_cols(void* out, bool bf, int64_t at, const uint32_t (&x)[32], float f) {
   if (bf) {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = f2_bf16x2(__uint_as_float(x[8 * i + 2 * e]) * f, __uint_as_float(x[8 * i + 2 * e + 1]) * f);
-      dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  } else {
+    store_rows_bf16(static_cast<__nv_bfloat16*>(out), at, x, f);
+  } else if (at >= 0) {
     float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -749,7 +741,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         uint32_t z[32];
         tmem_ld32(t_lane + 32 * h, z);
         tmem_wait_ld();
-        if (row_ok) store_cols(a.dq, a.out_bf16, (it.q0 + static_cast<int64_t>(pos)) * a.dq_rs + head * D + 32 * h, z, a.scale);
+        store_cols(a.dq, a.out_bf16, row_ok ? (it.q0 + static_cast<int64_t>(pos)) * a.dq_rs + head * D + 32 * h : -1, z, a.scale);
       }
       tc_fence_before();
       warp_arrive(smem_u32(&sm.acc_empty));
@@ -1226,8 +1218,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             *reinterpret_cast<uint4*>(to + ((c / 4 + i) * BN + row) * 4) = make_uint4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
-        } else if (key < it.n) {
-          store_cols(v ? a.dv : a.dk, a.out_bf16, out + c, z, v ? 1.f : a.scale);
+        } else {
+          store_cols(v ? a.dv : a.dk, a.out_bf16, key < it.n ? out + c : -1, z, v ? 1.f : a.scale);
         }
       }
       tc_fence_before();
