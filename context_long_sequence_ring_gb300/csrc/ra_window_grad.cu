@@ -115,8 +115,13 @@ __device__ __forceinline__ X block_scan(X x, X* warps) {
   __syncthreads();
   if (lane == 31) warps[warp] = x;
   __syncthreads();
-  X before = 0;
-  for (int w = 0; w < warp; ++w) before = MAX ? max(before, warps[w]) : before + warps[w];
+  // the warps before this one, each lane one of them
+  X before = lane < warp ? warps[lane] : X(0);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const X y = __shfl_xor_sync(0xffffffffu, before, o);
+    before = MAX ? max(before, y) : before + y;
+  }
   return MAX ? max(x, before) : x + before;
 }
 
@@ -148,9 +153,8 @@ __device__ void make_lists(const GradArgs& a) {
   __shared__ int64_t total, had_total, lo[kGradCtas + 1];
   const int tid = threadIdx.x;
   // plain key tiles of all sequences, so that the long ones can follow them in the list
-  int plain = 0, ended = 0;
+  int plain = 0, ended = 0, q0, n;
   for (int base = 0; base < a.R; base += kPlanThreads) {
-    int q0, n;
     load_seq(a, base, q0, n, ended, sums, ends[0]);
     plain += (n + BM - 1) / BM - long_tiles(a, n);
   }
@@ -162,8 +166,7 @@ __device__ void make_lists(const GradArgs& a) {
   int at[3] = {0, 0, plain};
   ended = 0;
   for (int base = 0; base < a.R; base += kPlanThreads) {
-    int q0, n;
-    load_seq(a, base, q0, n, ended, sums, &seq[0][0]);
+    if (a.R > kPlanThreads) load_seq(a, base, q0, n, ended, sums, &seq[0][0]);   // else they are in hand
     const int more = long_tiles(a, n);
     const int mine[3] = {(n + a.tpt - 1) / a.tpt, (n + BM - 1) / BM - more, more};
     __syncthreads();

@@ -116,6 +116,18 @@ def lib():
     return _lib
 
 
+class _Entries:
+    """Entry points as attributes, each looked up in the library the first time."""
+
+    def __getattr__(self, name):
+        f = getattr(lib(), name)
+        setattr(self, name, f)
+        return f
+
+
+_LIB = _Entries()
+
+
 def last_error() -> str:
     return lib().ra_last_error().decode()
 
@@ -270,11 +282,6 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     return out
 
 
-def _axis_table(axis, inv_freq):
-    if axis.dtype != torch.int32 or axis.is_cuda or axis.shape != inv_freq.shape or not axis.is_contiguous():
-        raise ValueError("axis must be a contiguous int32 vector on the host, one entry per frequency")
-
-
 def _frequency_table(inv_freq):
     if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 vector on the host")
@@ -296,23 +303,26 @@ def rope_apply_axes(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Te
     with pair i turned by positions[axis[i]] * inv_freq[i].  positions int32 [axes, rows] (e.g. time, height
     and width); inv_freq float64 and axis int32, both [rot/2] on the host.  out may be x (in place).
     ``backward`` turns by the negative angles: the gradient of x from the gradient of out."""
-    dev = _here(positions)
-    _of(torch.int32, positions)
-    _frequency_table(inv_freq)
-    _axis_table(axis, inv_freq)
-    rs, hs = _heads_of(x, "x", dev, x.dtype)
     rows, H, d = x.shape
-    if positions.dim() != 2 or positions.shape[1] != rows:
-        raise ValueError("positions must be [axes, rows]")
+    rs, hs, es = x.stride()
+    dt, dev, n_axes, half = x.dtype, x.get_device(), positions.shape[0], axis.numel()
     if out is None:
-        out = torch.empty((rows, H, d), dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape:
-        raise ValueError("out must be like x")
-    ors, ohs = _heads_of(out, "out", dev, x.dtype)
-    _check(lib().ra_rope_apply_axes(x.data_ptr(), rs, hs, out.data_ptr(), ors, ohs, rows, H, d, 2 * inv_freq.numel(), _dt(x),
-                                    ROPE_STYLES[style], positions.data_ptr(), positions.shape[0], inv_freq.data_ptr(),
-                                    axis.data_ptr(), mscale, 1 if backward else 0,
-                                    torch._C._cuda_getCurrentRawStream(dev)))
+        out = torch.empty((rows, H, d), dtype=dt, device=x.device)
+    ors, ohs, oes = out.stride()
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and positions.get_device() == dev and out.get_device() == dev):
+        raise ValueError("tensors must be on the current CUDA device")
+    if not (out.dtype == dt and out.shape == x.shape and ((es == 1 and oes == 1) or d <= 1)):
+        raise ValueError("x and out must be alike, [rows, H, d], the elements of a head contiguous")
+    if not (positions.dtype == torch.int32 and positions.shape == (n_axes, rows) and positions.is_contiguous()):
+        raise ValueError("positions must be contiguous int32 [axes, rows]")
+    if not (inv_freq.dtype == torch.float64 and axis.dtype == torch.int32 and inv_freq.shape == (half,) and axis.dim() == 1
+            and inv_freq.get_device() < 0 and axis.get_device() < 0 and inv_freq.is_contiguous() and axis.is_contiguous()):
+        raise ValueError("inv_freq must be a contiguous float64 vector on the host, axis an int32 one as long")
+    st = _LIB.ra_rope_apply_axes(x.data_ptr(), rs, hs, out.data_ptr(), ors, ohs, rows, H, d, 2 * half, _dt(x),
+                                 ROPE_STYLES[style], positions.data_ptr(), n_axes, inv_freq.data_ptr(), axis.data_ptr(),
+                                 mscale, 1 if backward else 0, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st)
     return out
 
 
@@ -758,54 +768,61 @@ def cp_rope_append(k, v, k_cache, v_cache, block_table, query_start_loc, ctx_len
     rotary positions.  q [T, Hq, d] is turned beside them into q_out (new if not given; may be q) and returned.
     positions int32 [T], or [axes, T] with axis int32 [rot/2] on the host; None: the token's place in its context.
     inv_freq float64 [rot/2] on the host; None: nothing is turned."""
-    dev = _here(k_cache, v_cache, block_table, query_start_loc, ctx_lens, positions)
-    _of(torch.int32, block_table, query_start_loc, ctx_lens, positions)
-    if k_cache.dim() != 5 or block_table.dim() != 2:
-        raise ValueError("the cache must be [W, NB, Hkv, bs, d], block_table [R, max_vblocks]")
-    W, NB, Hkv, bs, d = k_cache.shape
+    W, NB, Hkv, bs, d = shape = k_cache.shape
     R, max_vb = block_table.shape
-    dt = k_cache.dtype
-    if W != pcp * dcp:
-        raise ValueError("cache has %d devices, pcp*dcp = %d" % (W, pcp * dcp))
-    if v_cache.shape != k_cache.shape or v_cache.dtype != dt:
-        raise ValueError("v_cache must be like k_cache")
-    if query_start_loc.numel() != R + 1 or ctx_lens.numel() != R:
-        raise ValueError("block_table has %d requests: query_start_loc needs R+1 entries, ctx_lens R" % R)
-    krs, khs = _heads_of(k, "k", dev, dt)
-    vrs, vhs = _heads_of(v, "v", dev, dt)
-    T = k.shape[0]
-    if k.shape != (T, Hkv, d) or v.shape != (T, Hkv, d):
-        raise ValueError("k and v must be [T, Hkv, d] of the cache's heads")
-    n_axes, rot = 1, 0
+    T, heads, dk = k.shape
+    dt, dev, i32 = k_cache.dtype, k_cache.get_device(), torch.int32
+    krs, khs, kes = k.stride()
+    vrs, vhs, ves = v.stride()
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and v_cache.get_device() == dev
+            and block_table.get_device() == dev and query_start_loc.get_device() == dev and ctx_lens.get_device() == dev
+            and k.get_device() == dev and v.get_device() == dev):
+        raise ValueError("tensors must be on the current CUDA device")
+    if not (W == pcp * dcp and v_cache.shape == shape and v_cache.dtype == dt and k_cache.is_contiguous()
+            and v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be alike, contiguous [pcp*dcp, NB, Hkv, bs, d]")
+    if not (query_start_loc.numel() == R + 1 and ctx_lens.numel() == R and block_table.dtype == i32
+            and query_start_loc.dtype == i32 and ctx_lens.dtype == i32 and block_table.is_contiguous()
+            and query_start_loc.is_contiguous() and ctx_lens.is_contiguous()):
+        raise ValueError("block_table [R, max_vblocks], query_start_loc [R+1] and ctx_lens [R] must be contiguous int32")
+    if not (heads == Hkv and dk == d and v.shape == k.shape and k.dtype == dt and v.dtype == dt
+            and ((kes == 1 and ves == 1) or d == 1)):
+        raise ValueError("k and v must be [T, Hkv, d] of the caches' heads and dtype, the elements of a head contiguous")
+    n_axes, half, at = 1, 0, None
     if inv_freq is not None:
-        _frequency_table(inv_freq)
-        rot = 2 * inv_freq.numel()
-        if axis is not None:
-            _axis_table(axis, inv_freq)
-            if positions is None:
-                raise ValueError("several axes need positions")
+        half = inv_freq.numel()
+        if not (inv_freq.dtype == torch.float64 and inv_freq.dim() == 1 and inv_freq.get_device() < 0
+                and inv_freq.is_contiguous()):
+            raise ValueError("inv_freq must be a contiguous float64 vector on the host")
+        if axis is not None and not (axis.dtype == i32 and axis.shape == (half,) and axis.get_device() < 0
+                                     and axis.is_contiguous() and positions is not None):
+            raise ValueError("axis must be a contiguous int32 vector on the host as long as inv_freq, with positions")
     if positions is not None:
-        n_axes = positions.shape[0] if axis is not None and positions.dim() == 2 else 1
-        if positions.shape != ((n_axes, T) if axis is not None else (T,)):
-            raise ValueError("positions must be [T], or [axes, T] with axis")
-    Hq, qrs, qhs, ors, ohs = 0, 0, 0, 0, 0
+        at = positions.data_ptr()
+        n_axes = positions.shape[0] if axis is not None else 1
+        if not (positions.dtype == i32 and positions.get_device() == dev and positions.is_contiguous()
+                and positions.shape == ((n_axes, T) if axis is not None else (T,))):
+            raise ValueError("positions must be contiguous int32 [T], or [axes, T] with axis")
+    qp, op, Hq, qrs, qhs, ors, ohs = None, None, 0, 0, 0, 0, 0
     if q is not None:
-        qrs, qhs = _heads_of(q, "q", dev, dt)
-        Hq = q.shape[1]
-        if q.shape != (T, Hq, d):
-            raise ValueError("q must be [T, Hq, d]")
+        _, Hq, _ = q.shape
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
-        elif q_out.shape != q.shape:
-            raise ValueError("q_out must be like q")
-        ors, ohs = _heads_of(q_out, "q_out", dev, dt)
+            q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+        qrs, qhs, qes = q.stride()
+        ors, ohs, oes = q_out.stride()
+        if not (q.shape == (T, Hq, d) and q_out.shape == q.shape and q.dtype == dt and q_out.dtype == dt
+                and q.get_device() == dev and q_out.get_device() == dev and ((qes == 1 and oes == 1) or d == 1)):
+            raise ValueError("q and q_out must be alike, [T, Hq, d] of the caches' dtype, the elements of a head contiguous")
+        qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _check(lib().ra_cp_rope_append(k.data_ptr(), krs, khs, v.data_ptr(), vrs, vhs, _ptr(q), qrs, qhs, _ptr(q_out), ors, ohs,
-                                   k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                                   query_start_loc.data_ptr(), ctx_lens.data_ptr(), T, R, Hq, Hkv, d, _dt(k_cache), bs,
-                                   interleave, pcp, dcp, max_vb, NB, _ptr(positions), n_axes, rot, ROPE_STYLES[style],
-                                   _ptr(inv_freq), _ptr(axis), mscale, torch._C._cuda_getCurrentRawStream(dev)))
+    st = _LIB.ra_cp_rope_append(k.data_ptr(), krs, khs, v.data_ptr(), vrs, vhs, qp, qrs, qhs, op, ors, ohs,
+                                k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), query_start_loc.data_ptr(),
+                                ctx_lens.data_ptr(), T, R, Hq, Hkv, d, _dt(k_cache), bs, interleave, pcp, dcp, max_vb, NB,
+                                at, n_axes, 2 * half, ROPE_STYLES[style], None if inv_freq is None else inv_freq.data_ptr(),
+                                None if axis is None else axis.data_ptr(), mscale, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st)
     return q_out
 
 
