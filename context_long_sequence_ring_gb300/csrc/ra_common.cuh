@@ -21,6 +21,17 @@ void clear_error();
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Whether rows of a (`wa` bytes, `sa` apart) and of b share bytes: rows at the same distance lie side by side or not at
+// all; at different ones, nothing is said of rows whose spans meet.
+inline bool rows_meet(const void* pa, int64_t sa, int64_t wa, const void* pb, int64_t sb, int64_t wb, int64_t T) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(pa), b0 = reinterpret_cast<uintptr_t>(pb);
+  const uintptr_t a1 = a0 + (T - 1) * sa + wa, b1 = b0 + (T - 1) * sb + wb;
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (T == 1 || sa != sb || sa <= 0) return true;
+  const int64_t off = b0 >= a0 ? static_cast<int64_t>((b0 - a0) % sa) : sa - 1 - static_cast<int64_t>((a0 - b0 - 1) % sa);
+  return off < wa || off + wb > sa;
+}
+
 // Per-module device error words are fetched (and cleared) through these.
 int fetch_error_api(int* where);
 int fetch_error_cache(int* where);

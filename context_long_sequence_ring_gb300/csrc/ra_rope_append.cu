@@ -361,8 +361,17 @@ extern "C" ra_status ra_cp_rope_append(const void* k, int64_t k_row_stride, int6
     const bool same = q == q_out && (T == 1 || q_row_stride == q_out_row_stride) && (Hq == 1 || q_head_stride == q_out_head_stride);
     RA_REQUIRE(same || !meet(qs, qo), "q_out must be q itself with its strides or not overlap it");
     RA_REQUIRE(!meet(qs, kc) && !meet(qs, vc) && !meet(qo, kc) && !meet(qo, vc), "q and q_out must not overlap the caches");
-    // in place Q's elements lie between K's and V's where they come out of one projection: no element is in two of them
-    if (!same) RA_REQUIRE(!meet(qo, ks) && !meet(qo, vs), "q_out must not overlap k and v");
+    // Q's elements, turned in place, lie between K's and V's where they come out of one projection: by rows, each Q, K or V
+    // as a whole, or by heads
+    auto meets = [&](const void* x, int64_t rs, int64_t hs) {
+      if (!ra::rows_meet(q_out, es * q_out_row_stride, es * ((Hq - 1) * q_out_head_stride + d), x, es * rs,
+                         es * ((Hkv - 1) * hs + d), T))
+        return false;
+      if (hs != q_out_head_stride || hs <= 0 || (T > 1 && (rs != q_out_row_stride || rs % hs != 0))) return true;
+      const int64_t step = es * hs, off = ((static_cast<int64_t>(at(x) - at(q_out)) % step) + step) % step;
+      return off < es * d || off + es * d > step;
+    };
+    RA_REQUIRE(!meets(k, k_row_stride, k_head_stride) && !meets(v, v_row_stride, v_head_stride), "q_out must not overlap k and v");
   }
   p.c = make_paged(block_table, Hkv, block_size, interleave, pcp, dcp, max_vblocks, num_blocks);
   p.k = k; p.v = v; p.k_cache = k_cache; p.v_cache = v_cache;

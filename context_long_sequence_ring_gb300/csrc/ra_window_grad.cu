@@ -22,8 +22,9 @@
 // zeroes rows past a sequence's end (0 * NaN).
 //
 // Rounding.  P and dS are rounded to bf16, the type of the other operand.  delta is formed from an o that has been rounded,
-// whose error all keys of a row share: dS sums to 0 over a row, so the dQ kernel's row sums of dS in fp32 are that error, and
-// dK gets the delta without it.  In dQ itself it counts where a row sees few keys; there dS is split into two bf16
+// whose error all keys of a row share.  Where P sums to 1 over a row, dS sums to 0, so that the dQ kernel's row sums of dS in
+// fp32 are that error, and dK gets the delta without it.  (Where lse and o are those of more keys than these, P sums to
+// less, and delta stays.)  In dQ itself the error counts where a row sees few keys; there dS is split into two bf16
 // parts (an error of 2^-17 instead of 2^-9), which leaves the place for it.
 //
 // Work of dK, dV.  Tiles in rounds of one whole tile per CTA, neighbours at the same time, so that the queries they share
@@ -41,6 +42,7 @@ constexpr int kGradCtas = 152;         // one CTA per SM of a GB300
 constexpr int kGroups = 4;             // softmax warpgroups, 32 columns each
 constexpr int kSoftmax = 128 * kGroups;
 constexpr int kGradThreads = 128 + kSoftmax;
+constexpr float kUnit = 1.f / 32768.f; // of row sums of P between warps: only whether they sum to 1 is asked
 constexpr int kFewTiles = 2;           // row tiles of so many key tiles or fewer have dS in two parts
 constexpr int kPlanThreads = 1024;
 constexpr int kOver = 4;               // start and end of a key tile, in query tiles
@@ -378,7 +380,8 @@ struct __align__(1024) RowSmem {
   uint8_t q[BM * D * 2], d_o[BM * D * 2], k[KS][BN * D * 2], v[VS][BN * D * 2];
   uint64_t q_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], k_dirty[KS], k_clean[KS];
   uint64_t s_full[2], dp_full, ds_full[2], acc_full, acc_empty, sums_full, sums_free, drain;
-  float sums[kGroups - 1][BM];
+  float sums[kGroups - 1][BM];         // of dS
+  uint16_t p_sums[kGroups - 1][BM];    // of P, in units of kUnit
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -667,7 +670,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       const float nl = row_ok ? a.neg_lse[at] : -CUDART_INF_F, nd = row_ok ? a.neg_delta[at] : 0.f;
       const uint64_t nl2 = f2pack(nl, nl), nd2 = f2pack(nd, nd);
       const int p = row_ok ? pos : -1, low = max(0, p + 1 - a.window), sinks = min(a.n_sink, p + 1);
-      uint64_t sum2 = f2pack(0.f, 0.f);
+      uint64_t sum2 = f2pack(0.f, 0.f), p_sum2 = sum2;
       for (int j = 0; j < it.nt; ++j) {
         const uint32_t b = s_n & 1;
         if (!(ok = warp_wait_first(smem_u32(&sm.s_full[b]), (s_n >> 1) & 1, abort_flag, lim, 940))) break;
@@ -702,11 +705,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           const uint32_t f = (low_bits(p + 1 - from) & ~low_bits(low - from)) | low_bits(sinks - from);
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (!(f >> i & 1)) y[i] = 0;
+            if (!(f >> i & 1)) x[i] = y[i] = 0;
         }
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
           sum2 = fadd2(sum2, f2pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1])));
+          p_sum2 = fadd2(p_sum2, f2pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
           pk[i / 2] = f2_bf16x2(__uint_as_float(y[i]), __uint_as_float(y[i + 1]));
         }
         tmem_st16(s_addr, pk);
@@ -723,19 +727,24 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       if (!ok) break;
       // the row's sum of dS is the error of its delta
-      float s0, s1;
+      float s0, s1, p0, p1;
       f2unpack(sum2, s0, s1);
+      f2unpack(p_sum2, p0, p1);
       if (h > 0) {
         if (!(ok = warp_wait(smem_u32(&sm.sums_free), (done & 1) ^ 1, abort_flag, lim, 943))) break;
         sm.sums[h - 1][row] = s0 + s1;
+        sm.p_sums[h - 1][row] = static_cast<uint16_t>(fminf((p0 + p1) / kUnit + 0.5f, 65535.f));
         warp_arrive(smem_u32(&sm.sums_full));
       } else {
         if (!(ok = warp_wait(smem_u32(&sm.sums_full), done & 1, abort_flag, lim, 944))) break;
-        float sum = s0 + s1;
+        float sum = s0 + s1, p_sum = p0 + p1;
 #pragma unroll
-        for (int g = 1; g < kGroups; ++g) sum += sm.sums[g - 1][row];
+        for (int g = 1; g < kGroups; ++g) {
+          sum += sm.sums[g - 1][row];
+          p_sum += sm.p_sums[g - 1][row] * kUnit;
+        }
         warp_arrive(smem_u32(&sm.sums_free));
-        if (row_ok) a.neg_delta[at] = nd - sum;
+        if (row_ok && fabsf(p_sum - 1.f) < 1e-3f) a.neg_delta[at] = nd - sum;
       }
       if (!(ok = warp_wait(smem_u32(&sm.acc_full), done & 1, abort_flag, lim, 942))) break;
       ++done;
@@ -1357,17 +1366,6 @@ ra_status launch_grad(const void* q, int64_t q_rs, const void* k, int64_t k_rs, 
   return RA_OK;
 }
 
-// Whether rows of a (`wa` bytes, `sa` apart) and of b share bytes: rows at the same distance lie side by side or not at
-// all; at different ones, nothing is said of rows whose spans meet.
-bool rows_meet(const void* pa, int64_t sa, int64_t wa, const void* pb, int64_t sb, int64_t wb, int64_t T) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(pa), b0 = reinterpret_cast<uintptr_t>(pb);
-  const uintptr_t a1 = a0 + (T - 1) * sa + wa, b1 = b0 + (T - 1) * sb + wb;
-  if (a1 <= b0 || b1 <= a0) return false;
-  if (sa != sb) return true;
-  const int64_t off = b0 >= a0 ? static_cast<int64_t>((b0 - a0) % sa) : sa - 1 - static_cast<int64_t>((a0 - b0 - 1) % sa);
-  return off < wa || off + wb > sa;
-}
-
 }  // namespace
 
 namespace ra {
@@ -1408,9 +1406,9 @@ extern "C" ra_status ra_window_attn_bwd(const void* q, int64_t q_row_stride, con
                        {workspace, 1, 1}};
   for (int i = 0; i < 3; ++i) {
     for (int j = 0; j < i; ++j)
-      RA_REQUIRE(!rows_meet(outs[i].p, outs[i].s, outs[i].w, outs[j].p, outs[j].s, outs[j].w, T), "dq, dk and dv must not overlap");
+      RA_REQUIRE(!ra::rows_meet(outs[i].p, outs[i].s, outs[i].w, outs[j].p, outs[j].s, outs[j].w, T), "dq, dk and dv must not overlap");
     for (int j = 0; j < 6; ++j)
-      RA_REQUIRE(!rows_meet(outs[i].p, outs[i].s, outs[i].w, ins[j].p, ins[j].s, ins[j].w, T),
+      RA_REQUIRE(!ra::rows_meet(outs[i].p, outs[i].s, outs[i].w, ins[j].p, ins[j].s, ins[j].w, T),
                  "dq, dk and dv must not overlap the inputs");
   }
   const Layout at(T, R, Hq, Hkv, d);

@@ -791,7 +791,8 @@ ra_status ra_cp_window_attn(const void* q, const void* k_cache, const void* v_ca
  * Requires Hq % Hkv == 0, Hq/Hkv <= 64, d in {64, 128}, T < 2^30, T*Hq < 2^31; q, k, v, o 16-byte
  * aligned.
  * Lengths are read on the device: a captured call may be replayed with others.
- * Device bounds error: a sequence whose range is decreasing or outside [0, T] (left out).
+ * Device bounds error: a sequence whose range is decreasing or outside [0, T] (left out;
+ * the backward pass leaves out one that starts before an earlier one ends as well).
  * ---------------------------------------------------------------------- */
 ra_status ra_window_attn_workspace_size(int64_t T, int32_t R, int32_t Hq, int32_t Hkv, int32_t d, size_t* bytes);
 
@@ -807,15 +808,20 @@ ra_status ra_window_attn_fwd(const void* q, int64_t q_row_stride, const void* k,
  * dK and dV summed over the query heads of their K/V head.
  *
  * q, k, v, query_start_loc, window, n_sink, scale, workspace: as the forward call's.
- * o           device bf16 [T, Hq, d] and lse device float [T, Hq]: what it gave.
+ * o           device bf16 [T, Hq, d] and lse device float [T, Hq]: what it gave.  They may also be
+ *             those of a larger set of keys that holds these (a sequence shared over devices, merged by
+ *             ra_lse_merge): the call then gives what these keys contribute.
  * d_o         device bf16 [T, Hq, d]: the gradient of o, dense.
  * dq, dk, dv  device out in out_dt ([T, Hq, d], [T, Hkv, d], [T, Hkv, d]), rows row_stride
  *             elements apart (multiples of 16 bytes; e.g. parts of the gradient of a fused projection).
  *             They do not overlap one another nor the inputs.  Rows of no sequence are left as
  *             they were.
  * P and dS are rounded to bf16 for their products, all sums are fp32, in an order fixed by the
- * lengths (the same call gives the same bits).
- * A row whose lse is +inf has no weight, so that its gradient is 0.
+ * lengths (the same call gives the same bits).  The error of delta that the rounding of o brings is taken
+ * out of dK where P sums to 1 over a row.
+ * A row whose lse is +inf or -inf has no weight, so that its gradient is 0.
+ * Values of a sequence must be finite: one that is not may reach the gradients of tokens
+ * up to 128 positions from those that see it.  Other sequences' values do not matter.
  * Requires what the forward call requires; o, d_o, dq, dk, dv 16-byte aligned.
  * ---------------------------------------------------------------------- */
 ra_status ra_window_attn_bwd(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,

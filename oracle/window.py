@@ -56,9 +56,10 @@ def window_attn(q, k, v, qsl, window, n_sink=0, scale=None):
     return O, L, A
 
 
-def window_attn_grad(do, q, k, v, qsl, window, n_sink=0, scale=None):
+def window_attn_grad(do, q, k, v, qsl, window, n_sink=0, scale=None, o=None, lse=None):
     """(dQ, dK, dV) and, of each, a bound of the error that it may have where P and dS are rounded to bf16 (2^-8),
-    delta is formed from an O rounded to bf16 and all else is fp32 (2^-11 of what is summed); rows of no sequence NaN."""
+    delta is formed from an O rounded to bf16 and all else is fp32 (2^-11 of what is summed); rows of no sequence NaN.
+    o and lse: those of more keys than these (then P = e^{s - lse} sums to less than 1)."""
     do, q, k, v = _as64(do), _as64(q), _as64(k), _as64(v)
     T, Hq, d = q.shape
     Hkv = k.shape[1]
@@ -69,7 +70,9 @@ def window_attn_grad(do, q, k, v, qsl, window, n_sink=0, scale=None):
         a, b = int(qsl[r]), int(qsl[r + 1])
         seen = visible(b - a, b - a, window, n_sink)
         Q, D, K, V = q[a:b], do[a:b], np.repeat(k[a:b], G, axis=1), np.repeat(v[a:b], G, axis=1)
-        O, _, _, P = attend(Q, k[a:b], v[a:b], seen, scale)
+        O, L, _, P = attend(Q, k[a:b], v[a:b], seen, scale)
+        if lse is not None:
+            O, P = _as64(o)[a:b], P * np.exp(L - _as64(lse)[a:b])[:, :, None]
         dP = np.einsum("nhd,khd->nhk", D, V)
         aP = np.einsum("nhd,khd->nhk", np.abs(D), np.abs(V))
         delta, ad = (D * O).sum(2)[:, :, None], (np.abs(D) * np.abs(O)).sum(2)[:, :, None]
@@ -80,8 +83,8 @@ def window_attn_grad(do, q, k, v, qsl, window, n_sink=0, scale=None):
                 fold(np.einsum("nhk,nhd->khd", P, D)),
                 np.einsum("nhk,khd->nhd", E, np.abs(K)) * scale, fold(np.einsum("nhk,nhd->khd", E, np.abs(Q))) * scale,
                 fold(np.einsum("nhk,nhd->khd", P, np.abs(D))) * (r8 + r11)]
-        for o, x in zip(out, rows):
-            o[a:b] = x
+        for y, x in zip(out, rows):
+            y[a:b] = x
     return out[:3], out[3:]
 
 

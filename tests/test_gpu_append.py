@@ -260,6 +260,26 @@ def test_store_strides(ra):
     assert all(torch.equal(a, b) for a, b in zip(run(same, same), run(same.contiguous(), same.contiguous())))
 
 
+@pytest.mark.parametrize("T", [1, 33])
+def test_store_in_place_in_a_projection_by_heads(ra, T):
+    """q, k and v of each head side by side, [T, H, 3, d], q turned in place between them."""
+    case = ([50], [T], 2, 2, 64, 64, 16, 16, 1, 1, 0, "half")
+    ctx, n, H, _, d, rot, bs, I, pcp, dcp, _, style = case
+    _, kc, vc, table, qsl, pos = store_inputs(case, BF)
+    x = torch.randn((T, H, 3, d), generator=torch.Generator().manual_seed(3)).to(BF).to(DEV)
+    f, _ = ra.rope_frequencies(rot)
+    kd, vd, td, sd, pd, cd = dev(kc, vc, table, qsl, pos[0].contiguous(), i32(*ctx))
+    a, b, y = kd.clone(), vd.clone(), x.clone()
+    want = ra.cp_rope_append(x[:, :, 1], x[:, :, 2], kd, vd, td, sd, cd, I, pcp, dcp, positions=pd, inv_freq=f, q=x[:, :, 0])
+    ra.cp_rope_append(y[:, :, 1], y[:, :, 2], a, b, td, sd, cd, I, pcp, dcp, positions=pd, inv_freq=f, q=y[:, :, 0],
+                      q_out=y[:, :, 0])
+    check_status(ra)
+    assert torch.equal(a, kd) and torch.equal(b, vd) and torch.equal(y[:, :, 0], want) and torch.equal(y[:, :, 1:], x[:, :, 1:])
+    with pytest.raises(ra.RingAttnError):      # k itself
+        ra.cp_rope_append(y[:, :, 0], y[:, :, 2], a, b, td, sd, cd, I, pcp, dcp, positions=pd, inv_freq=f, q=y[:, :, 0],
+                          q_out=y[:, :, 0])
+
+
 def test_store_many_requests_and_empty_ones(ra):
     rng = np.random.default_rng(3)
     n = rng.choice([0, 0, 0, 1, 1, 2, 5], size=700)

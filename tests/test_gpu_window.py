@@ -334,6 +334,27 @@ def test_packed_gradient_of_rows_without_weight(ra):
     assert torch.equal(dv, dv2)
 
 
+@pytest.mark.parametrize("n,window,sink", [([300, 41], 60, 3), ([700], 600, 0)])
+def test_packed_gradient_of_a_part_of_the_keys(ra, n, window, sink):
+    """o and lse of a softmax over more keys than these (as on one of several devices): what these keys contribute."""
+    Hq, Hkv, d = 6, 2, 128
+    x, do, qsl = packed(8, n, Hq, Hkv, d)
+    q, k, v = parts(x, Hq, Hkv)
+    g = torch.Generator().manual_seed(9)
+    T = sum(n)
+    ref = O.window_attn(q, k, v, qsl, window, sink)
+    more = torch.rand((T, Hq), generator=g, dtype=torch.float64) * 3        # how much the other keys add to the LSE
+    more[::5] = 1e-6                                                       # next to nothing, for some rows
+    lse = (torch.from_numpy(ref[1]) + more).float()
+    w = torch.exp(-more)[..., None]
+    o = (torch.from_numpy(ref[0]) * w + torch.randn((T, Hq, d), generator=g, dtype=torch.float64) * (1 - w)).to(BF)
+    want, bound = O.window_attn_grad(do, q, k, v, qsl, window, sink, o=o, lse=lse)
+    xd, dd, sd, od, ld = dev(x, do, qsl, o, lse)
+    got = ra.window_attn_bwd(dd, *parts(xd, Hq, Hkv), od, ld, sd, window, n_sink=sink)
+    check_status(ra)
+    assert_grads(got, (want, bound))
+
+
 def test_packed_scale_sharp_and_large_values(ra):
     n, Hq, Hkv, d, window, sink, scale = [600], 4, 2, 64, 150, 4, 0.3
     x, do, qsl = packed(6, n, Hq, Hkv, d)

@@ -56,6 +56,30 @@ def test_the_gradient_against_differences(window, sink):
             assert np.isclose((loss(*hi) - loss(*lo)) / 2e-5, np.nansum(g * u), rtol=1e-6, atol=1e-8)
 
 
+def test_the_gradient_of_parts_of_the_keys_adds_up():
+    """With O and LSE of all keys, the gradients over the window's tokens and over the first tokens are those of both."""
+    q, k, v, do = rnd(1, 14, 4, 6), rnd(2, 14, 2, 6), rnd(3, 14, 2, 6), rnd(4, 14, 4, 6)
+    qsl = [0, 14]
+    O, L, _ = W.window_attn(q, k, v, qsl, 5, 3)
+    both, _ = W.window_attn_grad(do, q, k, v, qsl, 5, 3)
+    again, _ = W.window_attn_grad(do, q, k, v, qsl, 5, 3, o=O, lse=L)
+    assert all(np.allclose(a, b, atol=1e-12) for a, b in zip(both, again))
+    near, _ = W.window_attn_grad(do, q, k, v, qsl, 5, 0, o=O, lse=L)
+    far, _ = W.window_attn_grad(do, q, k, v, qsl, 1, 3, o=O, lse=L)
+    # first tokens that are in the window too, and each token itself, are counted twice: take them out
+    twice = [np.zeros_like(x) for x in both]
+    for p in range(14):
+        for x in {y for y in range(max(0, p - 4), p + 1) if y < 3 or y == p}:
+            for h in range(4):
+                pr = np.exp(q[p, h] @ k[x, h // 2] / np.sqrt(6) - L[p, h])
+                ds = pr * (do[p, h] @ (v[x, h // 2] - O[p, h])) / np.sqrt(6)
+                twice[0][p, h] += ds * k[x, h // 2]
+                twice[1][x, h // 2] += ds * q[p, h]
+                twice[2][x, h // 2] += pr * do[p, h]
+    for a, b, c, d in zip(near, far, twice, both):
+        assert np.allclose(a + b - c, d, atol=1e-10)
+
+
 def test_over_the_cache_as_on_packed_rows():
     ctx, n, bs, I, pcp, dcp = [20, 7, 0, 3], [5, 7, 0, 6], 4, 2, 1, 2
     qsl = np.concatenate([[0], np.cumsum(n)])
