@@ -774,6 +774,55 @@ struct KeyItem {
   int64_t at;                          // on the axis of cost, of a part
 };
 
+// Items on their way from the warp that finds them to the others (TMA, products, rows' numbers, softmax), three ahead, so
+// that nobody waits for their divisions and loads (window 512 over 16384 tokens, heads 32 on 8, d 128: 214 us; with every warp
+// finding its own 236).  The kernel of dQ finds its items with less, and keeps what it finds in registers: read from such a
+// ring they take that kernel's softmax beyond its 96 registers (254 us instead of 238).
+constexpr int kAhead = 3;
+constexpr int kReaders = 3 + kSoftmax / 32;
+struct ItemRing {
+  uint64_t full[kAhead], empty[kAhead];
+  KeyItem item[kAhead];                   // n = 0: the end
+  __device__ void init() {
+    for (int i = 0; i < kAhead; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), kReaders);
+    }
+  }
+};
+// By one thread.
+struct Announcer {
+  ItemRing& ring;
+  volatile int* abort_flag;
+  long long lim;
+  uint32_t at = 0;
+  __device__ bool put(const KeyItem& x) {
+    const int i = at % kAhead;
+    if (!mbar_wait(smem_u32(&ring.empty[i]), ((at / kAhead) & 1) ^ 1, abort_flag, lim, 906)) return false;
+    ring.item[i] = x;
+    mbar_arrive(smem_u32(&ring.full[i]));
+    ++at;
+    return true;
+  }
+};
+// By whole warps.
+struct ItemReader {
+  ItemRing& ring;
+  volatile int* abort_flag;
+  long long lim;
+  uint32_t at = 0;
+  bool ok = true;                      // false: a wait has expired
+  __device__ bool get(KeyItem& x) {
+    const int i = at % kAhead;
+    ok = warp_wait(smem_u32(&ring.full[i]), (at / kAhead) & 1, abort_flag, lim, 907);
+    if (!ok) return false;
+    x = ring.item[i];
+    warp_arrive(smem_u32(&ring.empty[i]));
+    ++at;
+    return x.n > 0;
+  }
+};
+
 // The items of a CTA: whole rounds, then its part of the rest.
 struct KeyIter {
   const GradArgs& a;
@@ -839,6 +888,7 @@ struct __align__(1024) KeySmem {
   uint8_t k[BN * D * 2], v[BN * D * 2], q[QS][BM * D * 2], d_o[OS][BM * D * 2];
   uint64_t k_full, k_empty, v_full, v_empty, q_full[QS], q_empty[QS], o_full[OS], o_empty[OS], x_full[XS], x_empty[XS];
   uint64_t s_full, p_full, dp_full, ds_full, acc_full, acc_empty, drain;
+  ItemRing items;
   __align__(16) float neg_lse[XS][BM], neg_delta[XS][BM];   // read four at a time
   uint32_t tmem_base;
   int abort_flag;
@@ -895,6 +945,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     mbar_init(smem_u32(&sm.acc_full), 1);
     mbar_init(smem_u32(&sm.acc_empty), kSoftmax / 32);
     mbar_init(smem_u32(&sm.drain), 1);
+    sm.items.init();
     sm.abort_flag = 0;
     fence_barrier_init();
   }
@@ -908,56 +959,58 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   const uint32_t tmem = sm.tmem_base;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  KeyIter items(a);
+  ItemReader items{sm.items, abort_flag, lim};
   KeyItem it;
 
   if (warp == 0) {
     // ============================================================ loads
+    Ring<QS> qr;
+    Ring<OS> orr;
+    uint32_t q_n = 0, o_n = 0, kv_n = 0, v_n = 0;
+    bool ok = true;
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
       tma_prefetch_desc(&tmO);
-      Ring<QS> qr;
-      Ring<OS> orr;
-      uint32_t q_n = 0, o_n = 0, kv_n = 0, v_n = 0;
-      bool ok = true;
-      while (ok && items.get(it)) {
-        int qt = it.k + a.by_G.div(it.it0);
-        int head = it.it0 - (qt - it.k) * a.G;
-        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint32_t bar, int hd, int row) {
-          for (int s = 0; s < SLABS; ++s) tma_load_3d(smem_u32(dst + s * BM * 128), map, bar, 64 * s, hd, row);
-        };
-        for (int j = 0; j < it.its; ++j) {
-          const int row = it.q0 + BM * qt, hd = it.g * a.G + head;
-          if (j == 0) {
-            if (!(ok = mbar_wait(smem_u32(&sm.k_empty), (kv_n & 1) ^ 1, abort_flag, lim, 950))) break;
-            ++kv_n;
-            mbar_arrive_expect_tx(smem_u32(&sm.k_full), kTileBytes);
-            load(sm.k, &tmK, smem_u32(&sm.k_full), it.g, it.q0 + BN * it.k);
-          }
-          if (!(ok = mbar_wait(smem_u32(&sm.q_empty[qr.st]), qr.ph ^ 1, abort_flag, lim, 951))) break;
-          mbar_arrive_expect_tx(smem_u32(&sm.q_full[qr.st]), kTileBytes);
-          load(sm.q[qr.st], &tmQ, smem_u32(&sm.q_full[qr.st]), hd, row);
-          ++q_n;
-          qr.advance();
-          if (j == 0) {
-            if (!(ok = mbar_wait(smem_u32(&sm.v_empty), (v_n & 1) ^ 1, abort_flag, lim, 952))) break;
-            ++v_n;
-            mbar_arrive_expect_tx(smem_u32(&sm.v_full), kTileBytes);
-            load(sm.v, &tmV, smem_u32(&sm.v_full), it.g, it.q0 + BN * it.k);
-          }
-          if (!(ok = mbar_wait(smem_u32(&sm.o_empty[orr.st]), orr.ph ^ 1, abort_flag, lim, 953))) break;
-          mbar_arrive_expect_tx(smem_u32(&sm.o_full[orr.st]), kTileBytes);
-          load(sm.d_o[orr.st], &tmO, smem_u32(&sm.o_full[orr.st]), hd, row);
-          ++o_n;
-          orr.advance();
-          if (++head == a.G) {
-            head = 0;
-            ++qt;
-          }
+    }
+    auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int hd, int row) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(smem_u32(bar), kTileBytes);
+        for (int s = 0; s < SLABS; ++s) tma_load_3d(smem_u32(dst + s * BM * 128), map, smem_u32(bar), 64 * s, hd, row);
+      }
+      __syncwarp();
+    };
+    while (ok && items.get(it)) {
+      int qt = it.k + a.by_G.div(it.it0);
+      int head = it.it0 - (qt - it.k) * a.G;
+      for (int j = 0; j < it.its; ++j) {
+        const int row = it.q0 + BM * qt, hd = it.g * a.G + head;
+        if (!(ok = warp_wait(smem_u32(&sm.q_empty[qr.st]), qr.ph ^ 1, abort_flag, lim, 951))) break;
+        load(sm.q[qr.st], &tmQ, &sm.q_full[qr.st], hd, row);
+        ++q_n;
+        qr.advance();
+        if (j == 0) {   // the keys after the first queries, which need not wait for the last keys
+          if (!(ok = warp_wait(smem_u32(&sm.k_empty), (kv_n & 1) ^ 1, abort_flag, lim, 950))) break;
+          ++kv_n;
+          load(sm.k, &tmK, &sm.k_full, it.g, it.q0 + BN * it.k);
+        }
+        if (!(ok = warp_wait(smem_u32(&sm.o_empty[orr.st]), orr.ph ^ 1, abort_flag, lim, 953))) break;
+        load(sm.d_o[orr.st], &tmO, &sm.o_full[orr.st], hd, row);
+        ++o_n;
+        orr.advance();
+        if (j == 0) {
+          if (!(ok = warp_wait(smem_u32(&sm.v_empty), (v_n & 1) ^ 1, abort_flag, lim, 952))) break;
+          ++v_n;
+          load(sm.v, &tmV, &sm.v_full, it.g, it.q0 + BN * it.k);
+        }
+        if (++head == a.G) {
+          head = 0;
+          ++qt;
         }
       }
+    }
+    if (lane == 0) {
       // the last load of each buffer lands before the CTA exits
       if (kv_n) mbar_wait_quiesce(smem_u32(&sm.k_full), (kv_n - 1) & 1, 1 << 22);
       if (v_n) mbar_wait_quiesce(smem_u32(&sm.v_full), (v_n - 1) & 1, 1 << 22);
@@ -1064,7 +1117,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         ++done;
       }
       mma_commit_by(leader, smem_u32(&sm.drain));
-      if (!__all_sync(0xffffffffu, mbar_wait_quiesce(smem_u32(&sm.drain), 0, a.drain_limit)) && ok) {
+      if (!__all_sync(0xffffffffu, mbar_wait_quiesce(smem_u32(&sm.drain), 0, a.drain_limit)) && ok && items.ok) {
         *abort_flag = 1;
         ra_record_error(RA_ERR_TIMEOUT, 968);
       }
@@ -1120,11 +1173,19 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
     }
   } else if (warp == 3) {
-    // ============================================================ the tile that this CTA's part starts and others go on with
+    // ============================================================ the items, and the tile that this CTA's part starts and
+    // others go on with
     if (lane == 0) {
+      Announcer out{sm.items, abort_flag, lim};
+      KeyIter found(a);
       Shared s = {};
-      while (items.get(it))
+      bool going = true;
+      while (going && found.get(it)) {
         if (it.at >= 0 && it.it0 == 0 && it.its < it.all) s = Shared{1, it.q0, it.n, it.k, it.g, it.all, it.at};
+        going = out.put(it);
+      }
+      it.n = 0;
+      if (going) out.put(it);
       a.shared[blockIdx.x] = s;
     }
     __syncwarp();
