@@ -6,10 +6,14 @@
 // rotation of ra_rope_turn.cuh and the place of x of ra_paged.cuh.
 //
 // One launch in place of four (the rotation of Q, that of K, the slot mapping, the
-// scatter), so that K passes through the chip once.  A block takes a run of
-// tokens, a few at a time: one thread each finds a token's request and place, all of
-// them form the angles of the tokens' pairs once (for all heads, in shared memory), and
-// then take the words of their heads, whose first loads have been in flight since the start.
+// scatter), so that K passes through the chip once.  A group of threads takes a token at a time: it finds the token's
+// request and place, forms the angles of its pairs once (for all heads, in shared memory), and takes the words of its
+// heads, whose loads are a step ahead of the stores and start before the place is known.
+//
+// Bound by memory: Q, K and V of a token are read once and written once.  16384 tokens with 32 + 8 + 8 heads of 128 (bf16)
+// move 403 MB in 72 us, 5.6 TB/s; 48 tokens take 6.4 us, the latency of request, block table, angles and stores.  A
+// group is a warp, so that nothing waits for a block (with barriers between every few tokens 77 to 82 us); where
+// the tokens are few it is a block, whose 256 threads are through with a token sooner (64 tokens 6.4 us, by warps 10.5).
 #include <algorithm>
 #include <type_traits>
 
@@ -21,9 +25,13 @@ RA_DEFINE_ERROR_FETCH(fetch_error_rope_append)
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendBlocks = 4;  // of an SM
-constexpr int kTokens = 8;        // at a time, at most
-constexpr int kAppendHeads = 2;   // of a thread, whose loads are in flight together
+// Of an SM, and the heads of a thread whose loads are in flight together: 3 and 2 are 80 registers (16384 tokens 72 us;
+// 4 and 2 spill, 92; 5 and 1 78; 2 and 4 86).
+constexpr int kAppendBlocks = 3;
+constexpr int kAppendHeads = 2;
+// So many tokens or fewer have a block each, two rounds of them: 608 tokens take 8.5 us (by warps 10.5), 912 10.5 (10.6),
+// 1216 12.8 (10.9), 16384 121 (70).
+constexpr int kBlockTokens = 912;
 
 struct AppendParams : Turns {
   Paged c;
@@ -33,11 +41,10 @@ struct AppendParams : Turns {
   const int32_t* positions;      // of axis a: positions + a * T; NULL: the token's place in its context
   int64_t T, k_rs, k_hs, v_rs, v_hs, q_rs, q_hs, qo_rs, qo_hs;
   int R, d, rot;
-  int tokens, run;               // of a block at a time, and in all
   // a unit is a word of pairs (interleaved), a word of real parts with its partner of imaginary parts (half) or a word that
   // is copied; a thread's work is a unit of one or two heads: of a token Q's, from k_first on K's, from v_first on V's
   int turn_units, per_token, k_first, v_first, heads, Hq;
-  FastDiv by_token, by_q, by_k, by_v, by_pairs;   // by the work of a token, the units of a head of each; the pairs of a head
+  FastDiv by_q, by_k, by_v;      // by the units of a head of each
 };
 
 // N values aligned to A bytes, and as fp32 ones (rounded to nearest even on the way back).
@@ -84,81 +91,94 @@ __device__ __forceinline__ void pack(Vec<__nv_bfloat16, N, A>& v, const float (&
   }
 }
 
-// What the threads of a block know of a token.
-struct TokenPlace {
-  int64_t row;                   // of the cache, for head 0; -1: not stored
-  int live;                      // of a request
-};
+// The first request whose end lies after token t (R: none), by a warp: ends of 32 parts at a time.
+__device__ __forceinline__ int request_of(const int32_t* qsl, int R, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  int r = 0;
+  for (int n = R; n > 0;) {
+    const int step = (n + 31) / 32, last = min((lane + 1) * step, n);
+    const int before = min(__popc(__ballot_sync(0xffffffffu, qsl[r + last] <= t)) * step, n);
+    n = min(step, n - before) - 1;   // the part's own end lies after t
+    r += before;
+  }
+  return r;
+}
 
-// N values to a word, aligned to A bytes; P pairs to a unit that turns.
-template <typename T, int N, int A, bool INTER, bool AXES>
+// N values to a word, aligned to A bytes; P pairs to a unit that turns; GROUP threads, a warp or a block, to a token at a time.
+template <typename T, int N, int A, bool INTER, bool AXES, int GROUP>
 __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(const __grid_constant__ AppendParams p) {
+  static_assert(GROUP == 32 || GROUP == kAppendThreads);
   using V = Vec<T, N, A>;
-  constexpr int P = INTER ? N / 2 : N;
-  __shared__ TokenPlace place[kTokens];
-  __shared__ float position[kTokens][kMaxAxes];
-  __shared__ float2 turns[kTokens][kMaxPairs];   // (cos, sin) of pair i of unit u at i * turn_units + u
-  const int half = p.rot / 2, tid = threadIdx.x;
-  const int64_t t_first = static_cast<int64_t>(blockIdx.x) * p.run, t_end = min(p.T, t_first + p.run);
+  constexpr int P = INTER ? N / 2 : N, kGroups = kAppendThreads / GROUP;
+  __shared__ float2 all_turns[kGroups][kMaxPairs];
+  const int half = p.rot / 2, tid = threadIdx.x % GROUP;
+  float2* turns = all_turns[threadIdx.x / GROUP];   // (cos, sin) of pair i of unit u at i * turn_units + u
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * kGroups;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / GROUP;
+  auto sync = [] {
+    if constexpr (GROUP == 32) __syncwarp();
+    else __syncthreads();
+  };
 
-  // A thread's work: unit e of heads h0 .. h0 + nh - 1.
-  int token, what, e, h0, nh;
-  bool turn_it;
-  V a[kAppendHeads], b[kAppendHeads];
-  auto load = [&](int64_t t0, int i, int all) {
-    nh = 0;
-    if (i >= all) return;
-    int sub;
-    token = p.by_token.div(i, sub);
-    what = sub < p.k_first ? 0 : sub < p.v_first ? 1 : 2;
-    h0 = (what == 0 ? p.by_q.div(sub, e) : what == 1 ? p.by_k.div(sub - p.k_first, e) : p.by_v.div(sub - p.v_first, e)) * p.heads;
-    nh = min((what == 0 ? p.Hq : p.c.Hkv) - h0, p.heads);
-    turn_it = what < 2 && e < p.turn_units;
-    const int64_t t = t0 + token, hs = what == 0 ? p.q_hs : what == 1 ? p.k_hs : p.v_hs;
-    const T* x = (what == 0 ? static_cast<const T*>(p.q) + t * p.q_rs
-                            : what == 1 ? static_cast<const T*>(p.k) + t * p.k_rs : static_cast<const T*>(p.v) + t * p.v_rs) +
-                 h0 * hs + (what == 2 || turn_it ? e * N : p.rot + (e - p.turn_units) * N);
+  // A thread's work: unit e of heads h0 .. h0 + nh - 1 (nh = 0: none).
+  struct Work {
+    int what, e, h0, nh;
+    bool turn_it;
+    V a[kAppendHeads], b[kAppendHeads];
+  };
+  auto load = [&](Work& w, int64_t t, int i) {
+    w.nh = 0;
+    if (i >= p.per_token || t >= p.T) return;
+    w.what = i < p.k_first ? 0 : i < p.v_first ? 1 : 2;
+    w.h0 = (w.what == 0 ? p.by_q.div(i, w.e) : w.what == 1 ? p.by_k.div(i - p.k_first, w.e) : p.by_v.div(i - p.v_first, w.e)) *
+           p.heads;
+    w.nh = min((w.what == 0 ? p.Hq : p.c.Hkv) - w.h0, p.heads);
+    w.turn_it = w.what < 2 && w.e < p.turn_units;
+    const int64_t hs = w.what == 0 ? p.q_hs : w.what == 1 ? p.k_hs : p.v_hs;
+    const T* x = (w.what == 0 ? static_cast<const T*>(p.q) + t * p.q_rs
+                              : w.what == 1 ? static_cast<const T*>(p.k) + t * p.k_rs : static_cast<const T*>(p.v) + t * p.v_rs) +
+                 w.h0 * hs + (w.what == 2 || w.turn_it ? w.e * N : p.rot + (w.e - p.turn_units) * N);
 #pragma unroll
     for (int j = 0; j < kAppendHeads; ++j)
-      if (j < nh) {
-        a[j] = *reinterpret_cast<const V*>(x + j * hs);
-        if (!INTER && turn_it) b[j] = *reinterpret_cast<const V*>(x + j * hs + half);
+      if (j < w.nh) {
+        w.a[j] = *reinterpret_cast<const V*>(x + j * hs);
+        if (!INTER && w.turn_it) w.b[j] = *reinterpret_cast<const V*>(x + j * hs + half);
       }
   };
-  auto store = [&](int64_t t0) {
-    if (nh == 0) return;
+  // `row`: of the cache, for head 0 (-1: not stored); `live`: of a request
+  auto store = [&](const Work& w, int64_t t, int64_t row, bool live) {
+    if (w.nh == 0) return;
     T* y;
     int64_t hs;
-    if (what == 0) {
-      if (!place[token].live) return;
-      y = static_cast<T*>(p.q_out) + (t0 + token) * p.qo_rs;
+    if (w.what == 0) {
+      if (!live) return;
+      y = static_cast<T*>(p.q_out) + t * p.qo_rs;
       hs = p.qo_hs;
     } else {
-      const int64_t row = place[token].row;
       if (row < 0) return;
-      y = static_cast<T*>(what == 1 ? p.k_cache : p.v_cache) + row * p.d;
+      y = static_cast<T*>(w.what == 1 ? p.k_cache : p.v_cache) + row * p.d;
       hs = static_cast<int64_t>(p.c.bs) * p.d;
     }
-    y += h0 * hs + (what == 2 || turn_it ? e * N : p.rot + (e - p.turn_units) * N);
-    if (!turn_it) {
+    y += w.h0 * hs + (w.what == 2 || w.turn_it ? w.e * N : p.rot + (w.e - p.turn_units) * N);
+    if (!w.turn_it) {
 #pragma unroll
       for (int j = 0; j < kAppendHeads; ++j)
-        if (j < nh) *reinterpret_cast<V*>(y + j * hs) = a[j];
+        if (j < w.nh) *reinterpret_cast<V*>(y + j * hs) = w.a[j];
       return;
     }
     float c[P], s[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const float2 t = turns[token][i * p.turn_units + e];
-      c[i] = t.x;
-      s[i] = t.y;
+      const float2 cs = turns[i * p.turn_units + w.e];
+      c[i] = cs.x;
+      s[i] = cs.y;
     }
 #pragma unroll
     for (int j = 0; j < kAppendHeads; ++j) {
-      if (j >= nh) break;
+      if (j >= w.nh) break;
       float f[N], o[N];
       V v;
-      unpack(a[j], f);
+      unpack(w.a[j], f);
       if (INTER) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -169,7 +189,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
         *reinterpret_cast<V*>(y + j * hs) = v;
       } else {
         float g[N], o2[N];
-        unpack(b[j], g);
+        unpack(w.b[j], g);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           o[i] = turn_re(f[i], g[i], c[i % P], s[i % P]);
@@ -182,63 +202,45 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
       }
     }
   };
-  load(t_first, tid, static_cast<int>(min(static_cast<int64_t>(p.tokens), t_end - t_first)) * p.per_token);
-  // the request of the block's first token, by all threads together
-  int r = 0;
-  for (int base = 0; base < p.R; base += kAppendThreads) {
-    const int i = base + tid;
-    int32_t end = INT32_MAX;
-    if (i < p.R) {
-      end = p.qsl[i + 1];
-      if (blockIdx.x == 0) {
-        const int32_t begin = p.qsl[i];
-        if (begin < 0 || end < begin || end > p.T) ra_record_error(RA_ERR_DEVICE_BOUNDS, 700);
-      }
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.R; i += kAppendThreads) {
+      const int32_t begin = p.qsl[i], end = p.qsl[i + 1];
+      if (begin < 0 || end < begin || end > p.T) ra_record_error(RA_ERR_DEVICE_BOUNDS, 700);
     }
-    r += __syncthreads_count(i < p.R && end <= t_first);
-  }
-  for (int64_t t0 = t_first; t0 < t_end; t0 += p.tokens) {
-    const int n = static_cast<int>(min(static_cast<int64_t>(p.tokens), t_end - t0)), all = n * p.per_token;
-    if (t0 > t_first) load(t0, tid, all);
-    if (tid < n) {
-      const int64_t t = t0 + tid;
-      while (r < p.R && p.qsl[r + 1] <= t) ++r;
-      TokenPlace at{-1, 0};
-      int64_t x = -1;
-      if (r < p.R && t >= p.qsl[r]) {
-        at.live = 1;
-        x = static_cast<int64_t>(p.ctx[r]) - (p.qsl[r + 1] - t);
-        if (x < 0 || x >= (int64_t(1) << 30) || x >= static_cast<int64_t>(p.c.max_vb) * p.c.V)
-          ra_record_error(RA_ERR_DEVICE_BOUNDS, 701);
-        else
-          at.row = paged_row(p.c, r, static_cast<int>(x), 0, 702);
-      }
-      place[tid] = at;
-      if (p.turn_units > 0 && !p.positions) {
+  Work work;
+  load(work, t, tid);
+  for (; t < p.T; t += groups) {
+    const int r = request_of(p.qsl, p.R, t);
+    int64_t x = -1, row = -1;
+    const bool live = r < p.R && t >= p.qsl[r];
+    if (live) {
+      x = static_cast<int64_t>(p.ctx[r]) - (p.qsl[r + 1] - t);
+      if (x < 0 || x >= (int64_t(1) << 30) || x >= static_cast<int64_t>(p.c.max_vb) * p.c.V)
+        ra_record_error(RA_ERR_DEVICE_BOUNDS, 701);
+      else
+        row = paged_row(p.c, r, static_cast<int>(x), 0, 702);
+      if (p.turn_units > 0) {
         const bool in = x >= 0 && x < kPositionLimit;
-        if (at.live && !in) ra_record_error(RA_ERR_DEVICE_BOUNDS, 703);
-        position[tid][0] = in ? static_cast<float>(x) : 0.f;
+        if (!p.positions && !in) ra_record_error(RA_ERR_DEVICE_BOUNDS, 703);
+        const float place = in ? static_cast<float>(x) : 0.f;
+        for (int i = tid; i < half; i += GROUP) {
+          const float m = p.positions ? position_at(p.positions, (AXES ? p.axis[i] : 0) * p.T + t, 703) : place;
+          float2 cs;
+          turn(p, i, m, cs.x, cs.y);
+          turns[i % P * p.turn_units + i / P] = cs;
+        }
       }
     }
-    __syncthreads();
-    if (p.turn_units > 0) {
-      for (int i = tid; i < n * half; i += kAppendThreads) {
-        int pair;
-        const int token = p.by_pairs.div(i, pair);
-        if (!place[token].live) continue;
-        const float m = p.positions ? position_at(p.positions, (AXES ? p.axis[pair] : 0) * p.T + t0 + token, 703) : position[token][0];
-        float2 cs;
-        turn(p, pair, m, cs.x, cs.y);
-        turns[token][pair % P * p.turn_units + pair / P] = cs;
-      }
-      __syncthreads();
+    sync();
+    for (int i = tid; i < p.per_token; i += 2 * GROUP) {
+      Work other;
+      load(other, t, i + GROUP);
+      store(work, t, row, live);
+      if (i + 2 * GROUP < p.per_token) load(work, t, i + 2 * GROUP);
+      else load(work, t + groups, tid);
+      store(other, t, row, live);
     }
-    for (int i = tid; i < all;) {
-      store(t0);
-      i += kAppendThreads;
-      load(t0, i, all);
-    }
-    __syncthreads();
+    sync();
   }
 }
 
@@ -250,25 +252,24 @@ ra_status launch_append(AppendParams& p, int32_t Hq, bool inter, bool axes, cuda
   const bool q_moves = p.q && p.q != p.q_out;             // in place the rest of a head stays where it is
   const int64_t k_units = p.turn_units + (p.d - p.rot) / N, v_units = p.d / N;
   const int64_t q_units = p.q ? p.turn_units + (q_moves ? (p.d - p.rot) / N : 0) : 0;
-  // one round of blocks that share the tokens out; few tokens: one at a time, a block each, with fewer heads to a thread
-  p.run = static_cast<int>(ra::ceil_div(p.T, 152 * kAppendBlocks));
-  p.tokens = std::min(p.run, kTokens);
+  const bool by_warps = p.T > kBlockTokens;
   for (p.heads = kAppendHeads; p.heads > 1; p.heads /= 2) {
     const int64_t work = q_units * ra::ceil_div(Hq, p.heads) + (k_units + v_units) * ra::ceil_div(Hkv, p.heads);
-    if (work * p.tokens >= kAppendThreads) break;
+    if (work >= (by_warps ? 32 : kAppendThreads)) break;
   }
   p.Hq = p.q ? Hq : 0;
   p.k_first = static_cast<int>(q_units * ra::ceil_div(p.Hq, p.heads));
   p.v_first = p.k_first + static_cast<int>(k_units * ra::ceil_div(Hkv, p.heads));
   p.per_token = p.v_first + static_cast<int>(v_units * ra::ceil_div(Hkv, p.heads));
-  p.by_token = fast_div(p.per_token);
   p.by_q = fast_div(std::max<int64_t>(1, q_units));
   p.by_k = fast_div(k_units);
   p.by_v = fast_div(v_units);
-  p.by_pairs = fast_div(std::max(1, p.rot / 2));
-  const unsigned blocks = static_cast<unsigned>(ra::ceil_div(p.T, p.run));
+  const unsigned blocks = static_cast<unsigned>(
+      std::min<int64_t>(152 * kAppendBlocks, by_warps ? ra::ceil_div(p.T, kAppendThreads / 32) : p.T));
   auto go = [&](auto in, auto ax) {
-    append_kernel<T, N, A, decltype(in)::value, decltype(ax)::value><<<blocks, kAppendThreads, 0, stream>>>(p);
+    constexpr bool I = decltype(in)::value, X = decltype(ax)::value;
+    if (by_warps) append_kernel<T, N, A, I, X, 32><<<blocks, kAppendThreads, 0, stream>>>(p);
+    else append_kernel<T, N, A, I, X, kAppendThreads><<<blocks, kAppendThreads, 0, stream>>>(p);
   };
   if constexpr (N % 2 == 0) {
     if (inter && axes) go(std::true_type{}, std::true_type{});
@@ -319,7 +320,7 @@ extern "C" ra_status ra_cp_rope_append(const void* k, int64_t k_row_stride, int6
   RA_REQUIRE(d >= 1 && d <= 1024, "1 <= d <= 1024 required");
   RA_REQUIRE(!q || Hq >= 1, "Hq must be >= 1");
   RA_REQUIRE(static_cast<int64_t>(Hkv) * d < (int64_t(1) << 26) && (!q || static_cast<int64_t>(Hq) * d < (int64_t(1) << 26)),
-             "heads * d must be below 2^26");   // units of kTokens tokens: 31 bits
+             "heads * d must be below 2^26");   // the work of a token: 31 bits
   const int es = dt == RA_BF16 ? 2 : 4;
   if (d * es % 16 != 0) return ra::fail(RA_ERR_UNSUPPORTED, "d*elem_size must be a multiple of 16");
   RA_REQUIRE(T >= 0 && T < (int64_t(1) << 31), "T must be in [0, 2^31)");

@@ -215,6 +215,24 @@ def test_store(ra, case, dt):
     assert torch.equal(yq[:2], q[:2]) and torch.equal(yq[-3:], q[-3:])
 
 
+# the same with so many tokens that a warp takes one instead of a block
+MANY_TOKENS = [
+    ([1500], [1111], 6, 2, 128, 128, 32, 4, 1, 2, 0, "half"),
+    ([5, 0, 997, 3, 800], [5, 0, 700, 1, 300], 5, 3, 64, 32, 16, 16, 1, 1, 3, "interleaved"),
+    ([i % 9 + 3 for i in range(700)], [i % 4 for i in range(700)], 4, 1, 80, 40, 16, 2, 1, 2, 0, "half"),
+    ([1300, 40], [1233, 7], 3, 3, 72, 22, 8, 2, 1, 1, 2, "interleaved"),       # pairs that are no whole words
+    ([2000], [913], 9, 1, 64, 0, 5, 5, 1, 1, 0, "half"),                       # nothing turned
+    ([1000], [908], 1, 1, 8, 8, 16, 16, 1, 1, 0, "half"),                      # less work than a warp has threads
+]
+
+
+@pytest.mark.parametrize("case", MANY_TOKENS, ids=lambda c: "n%d-h%d.%d-d%d.%d-a%d-%s" % (
+    sum(c[1]), c[2], c[3], c[4], c[5], c[10], c[11]))
+@pytest.mark.parametrize("dt", [BF, torch.float32])
+def test_store_many_tokens(ra, case, dt):
+    test_store(ra, case, dt)
+
+
 def test_store_positions_default_to_the_place(ra):
     case = ([300, 41], [30, 41], 4, 2, 64, 64, 16, 4, 1, 2, 0, "half")
     ctx, n, Hq, Hkv, d, rot, bs, I, pcp, dcp, _, style = case
