@@ -709,8 +709,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          sum2 = fadd2(sum2, f2pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1])));
-          p_sum2 = fadd2(p_sum2, f2pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
           pk[i / 2] = f2_bf16x2(__uint_as_float(y[i]), __uint_as_float(y[i + 1]));
         }
         tmem_st16(s_addr, pk);
@@ -724,6 +722,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(smem_u32(&sm.ds_full[b]));
+        // the sums, while the next tile is on its way
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          sum2 = fadd2(sum2, f2pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1])));
+          p_sum2 = fadd2(p_sum2, f2pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+        }
       }
       if (!ok) break;
       // the row's sum of dS is the error of its delta
