@@ -38,11 +38,16 @@
 // Measured (32/8 heads of 128, 8 devices, captured calls): 48 requests with 1-6 drafted
 // tokens over 2048-16384: 275-279 us, 6.6 TB/s, 97 % of the copy rate; one token over
 // 131072: 85 us, 6.3 TB/s; 4 single tokens over 200-2000: 18.7 us; 4096 tokens of a
-// prompt of 32768: 1.44 ms, 1430 TFLOP/s (1.54 sustained).  12 requests (24/8 heads of
+// prompt of 32768: 1.28-1.30 ms, 1580 TFLOP/s.  12 requests (24/8 heads of
 // 64, blocks of 16), prompts of 300-511 new tokens among single ones: 42 us.
+// With a window of 4096: 4096 tokens of a prompt 270 us (joining 20), 64 single tokens 195 us, 5.8 TB/s, 32768 packed tokens
+// 1.40 ms (a sequence of 16384 under no window 1.34 ms, 1640 TFLOP/s).  What a window costs is an item's start and end and
+// its masked tiles at either end, 11-13 thousand cycles, four tiles' time.
 //
 // Roles (384 threads): warp 0 TMA, warp 1 MMA issue, warp 2 zeroing of dead V
-// rows, warp 3 schedule, warps 4-7 and 8-11 softmax of slots 0 and 1.
+// rows, warp 3 schedule, warps 4-7 and 8-11 softmax of slots 0 and 1.  Warp 1 issues as a whole, with an elected thread as
+// the instructions' predicate: in a branch of one thread their operands are moved to uniform registers one by one
+// (about 70 cycles each; the prompt over 32768 1476 us instead of 1295).
 // Tensor memory: two (D = 128) or three (D = 64) score tiles S_b = columns [128b, +128) with P (bf16)
 // over the first 64 of each, then O_0 and O_1, D columns each.
 //

@@ -18,8 +18,13 @@
 //   join      sums the parts of key tiles that several CTAs share.
 // 16 warps of softmax, a thread holding 32 columns of a row of a score tile: tensor memory has room for one tile of
 // each kind only, so that the chain of a tile (scores, exponentials, next product) sets the pace, and
-// 8 warps with 64 columns each took 1.5 times as long for it.  One thread issues the products, a warp the loads, and one
-// zeroes rows past a sequence's end (0 * NaN).
+// 8 warps with 64 columns each took 1.5 times as long for it.  A whole warp issues the products (in a branch of one thread
+// dQ took 713 us instead of 529, dK and dV 835 instead of 622: operands moved to uniform registers one by one), one the
+// loads, and one zeroes rows past a sequence's end (0 * NaN).
+//
+// Bound by the tensor core where items are long, and by their starts and ends where a window makes them short.  Measured over
+// 16384 tokens, 32/8 heads, dQ / dK and dV in us: D = 128, window 512 227 / 214, 2048 510 / 597, none 1820 / 2400 (1.81 and
+// 1.83 PFLOP/s executed); D = 64 177 / 176, 408 / 485, 1421 / 1875.  prepare reads o and dO once, 5.6 TB/s; join 15 us.
 //
 // Rounding.  P and dS are rounded to bf16, the type of the other operand.  delta is formed from an o that has been rounded,
 // whose error all keys of a row share.  Where P sums to 1 over a row, dS sums to 0, so that the dQ kernel's row sums of dS in
