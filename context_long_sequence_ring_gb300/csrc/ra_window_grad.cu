@@ -799,15 +799,19 @@ struct ItemRing {
     }
   }
 };
-// By one thread.
+// By one thread.  It waits for whole items where the others wait for a tile, so its limit is that of a tile times the
+// tiles of the longest item.
 struct Announcer {
   ItemRing& ring;
   volatile int* abort_flag;
   long long lim;
   uint32_t at = 0;
+  int longest = 0;
   __device__ bool put(const KeyItem& x) {
     const int i = at % kAhead;
-    if (!mbar_wait(smem_u32(&ring.empty[i]), ((at / kAhead) & 1) ^ 1, abort_flag, lim, 906)) return false;
+    const long long far = 1ll << 62, most = lim < far / (longest + 1) ? lim * (longest + 1) : far;
+    if (!mbar_wait(smem_u32(&ring.empty[i]), ((at / kAhead) & 1) ^ 1, abort_flag, most, 906)) return false;
+    longest = max(longest, x.its);
     ring.item[i] = x;
     mbar_arrive(smem_u32(&ring.full[i]));
     ++at;
@@ -1193,7 +1197,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         if (it.at >= 0 && it.it0 == 0 && it.its < it.all) s = Shared{1, it.q0, it.n, it.k, it.g, it.all, it.at};
         going = out.put(it);
       }
-      it.n = 0;
+      it.n = it.its = 0;
       if (going) out.put(it);
       a.shared[blockIdx.x] = s;
     }

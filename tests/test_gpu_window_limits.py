@@ -81,3 +81,27 @@ def test_waits_that_expire(unlimited, limit):
             assert same[name], name
         else:
             assert ("window attention gradient" if "gradient" in name else "window attention") in msg, (name, msg)
+
+
+LONG = r"""
+import sys, torch
+sys.path.insert(0, sys.argv[1])
+from context_long_sequence_ring_gb300 import ringattn as ra
+dev = torch.device("cuda:0")
+T = 16384
+g = torch.Generator().manual_seed(1)
+x, do = (torch.randn(T, h, 64, generator=g).to(torch.bfloat16).to(dev) for h in (48, 32))
+s = torch.tensor([0, T], dtype=torch.int32, device=dev)
+q, k, v = x[:, :32], x[:, 32:40], x[:, 40:]
+o, lse = torch.zeros(T, 32, 64, dtype=torch.bfloat16, device=dev), torch.full((T, 32), 9.0, device=dev)
+ra.window_attn_bwd(do, q, k, v, o, lse, s, 1 << 30)
+print(ra.device_status(), ra.last_error())
+"""
+
+
+def test_a_limit_is_for_a_tile_and_not_for_an_item():
+    """A key tile of the first tokens meets 512 query tiles, some 10^6 cycles; no wait for one of them takes 2 * 10^5."""
+    env = dict(os.environ, RA_WAIT_LIMIT_CYCLES="200000")
+    r = subprocess.run([sys.executable, "-c", LONG, ROOT], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert r.stdout.split()[0] == "0", r.stdout
