@@ -29,8 +29,8 @@
 // Rounding.  P and dS are rounded to bf16, the type of the other operand.  delta is formed from an o that has been rounded,
 // whose error all keys of a row share.  Where P sums to 1 over a row, dS sums to 0, so that the dQ kernel's row sums of dS in
 // fp32 are that error, and dK gets the delta without it.  (Where lse and o are those of more keys than these, P sums to
-// less, and delta stays.)  In dQ itself the error counts where a row sees few keys; there dS is split into two bf16
-// parts (an error of 2^-17 instead of 2^-9), which leaves the place for it.
+// less, and delta stays.)  In dQ itself the error counts where a row sees few keys (2: 0.0033 of dQ, 3: 0.0026, 8: 0.0020);
+// where all of them are in one tile, delta is summed from P and dP before dS is formed, under the same condition.
 //
 // Work of dK, dV.  Tiles in rounds of one whole tile per CTA, neighbours at the same time, so that the queries they share
 // are in L2; the last one or two rounds, and the tiles of first tokens that all later queries see, are laid on one axis
@@ -48,7 +48,9 @@ constexpr int kGroups = 4;             // softmax warpgroups, 32 columns each
 constexpr int kSoftmax = 128 * kGroups;
 constexpr int kGradThreads = 128 + kSoftmax;
 constexpr float kUnit = 1.f / 32768.f; // of row sums of P between warps: only whether they sum to 1 is asked
-constexpr int kFewTiles = 2;           // row tiles of so many key tiles or fewer have dS in two parts
+// Row tiles of so many key tiles or fewer have dS in two parts: where a row sees 16 keys, dQ is then off by 0.0018 instead of
+// 0.0025 (its own rounding is 0.0017); a window of 128 over 16384 tokens takes 398 us instead of 378.
+constexpr int kFewTiles = 2;
 constexpr int kPlanThreads = 1024;
 constexpr int kOver = 4;               // start and end of a key tile, in query tiles
 
@@ -384,7 +386,7 @@ struct __align__(1024) RowSmem {
   static constexpr int KS = D == 128 ? 3 : 6, VS = D == 128 ? 2 : 4;
   uint8_t q[BM * D * 2], d_o[BM * D * 2], k[KS][BN * D * 2], v[VS][BN * D * 2];
   uint64_t q_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], k_dirty[KS], k_clean[KS];
-  uint64_t s_full[2], dp_full, ds_full[2], acc_full, acc_empty, sums_full, sums_free, drain;
+  uint64_t s_full[2], dp_full, ds_full[2], acc_full, acc_empty, sums_full, sums_free, all_read, drain;
   float sums[kGroups - 1][BM];         // of dS
   uint16_t p_sums[kGroups - 1][BM];    // of P, in units of kUnit
   uint32_t tmem_base;
@@ -435,6 +437,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     mbar_init(smem_u32(&sm.dp_full), 1);
     mbar_init(smem_u32(&sm.sums_full), kSoftmax / 32 - 4);
     mbar_init(smem_u32(&sm.sums_free), 4);
+    mbar_init(smem_u32(&sm.all_read), kSoftmax / 32);
     mbar_init(smem_u32(&sm.acc_full), 1);
     mbar_init(smem_u32(&sm.acc_empty), kSoftmax / 32);
     mbar_init(smem_u32(&sm.drain), 1);
@@ -665,17 +668,57 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const int row_tok = a.by_G.div(row), row_head = row - row_tok * a.G;
     const uint64_t sc2 = f2pack(a.scale_log2, a.scale_log2);
-    uint32_t s_n = 0, done = 0;
+    uint32_t s_n = 0, done = 0, wholes = 0;
     bool ok = true;
     for (int m = 0; m < rounds && ok; ++m) {
       if (!get(m, it)) continue;
       const int pos = it.tok0 + row_tok, head = it.g * a.G + row_head;
       const bool row_ok = row_tok < a.tpt && pos < it.n;
       const int64_t at = static_cast<int64_t>(head) * a.T + it.q0 + pos;
-      const float nl = row_ok ? a.neg_lse[at] : -CUDART_INF_F, nd = row_ok ? a.neg_delta[at] : 0.f;
-      const uint64_t nl2 = f2pack(nl, nl), nd2 = f2pack(nd, nd);
+      const float nl = row_ok ? a.neg_lse[at] : -CUDART_INF_F;
+      float nd = row_ok ? a.neg_delta[at] : 0.f;
+      const uint64_t nl2 = f2pack(nl, nl);
       const int p = row_ok ? pos : -1, low = max(0, p + 1 - a.window), sinks = min(a.n_sink, p + 1);
+      auto seen = [&](int u) {                                        // keys of unit u that the row sees
+        const int from = 32 * u + (u < it.first ? 0 : it.skip);
+        return (low_bits(p + 1 - from) & ~low_bits(low - from)) | low_bits(sinks - from);
+      };
       uint64_t sum2 = f2pack(0.f, 0.f), p_sum2 = sum2;
+      if (it.nt == 1) {
+        // delta = sum of P dP, by each group over all columns, before any of them stores dS over the scores
+        if (!(ok = warp_wait_first(smem_u32(&sm.s_full[s_n & 1]), (s_n >> 1) & 1, abort_flag, lim, 945))) break;
+        if (!(ok = warp_wait(smem_u32(&sm.dp_full), s_n & 1, abort_flag, lim, 946))) break;
+        tc_fence_after();
+        float pd = 0.f, ps = 0.f;
+#pragma unroll 1
+        for (int g = 0; g < kGroups; ++g) {
+          const uint32_t f = seen(g);
+          uint32_t x[32], y[32];
+          tmem_ld32(t_lane + kColS + (s_n & 1) * BN + 32 * g, x);
+          tmem_ld32(t_lane + kColP + 32 * g, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float p0, p1;
+            exp_pair(x[i], x[i + 1], sc2, nl2, p0, p1);
+            if (f >> i & 1) {
+              ps += p0;
+              pd = fmaf(p0, __uint_as_float(y[i]), pd);
+            }
+            if (f >> i & 2) {
+              ps += p1;
+              pd = fmaf(p1, __uint_as_float(y[i + 1]), pd);
+            }
+          }
+        }
+        if (row_ok && fabsf(ps - 1.f) < 1e-3f) nd = -pd;
+        tc_fence_before();
+        warp_arrive(smem_u32(&sm.all_read));
+        if (!(ok = warp_wait(smem_u32(&sm.all_read), wholes & 1, abort_flag, lim, 947))) break;
+        ++wholes;
+        tc_fence_after();
+      }
+      const uint64_t nd2 = f2pack(nd, nd);
       for (int j = 0; j < it.nt; ++j) {
         const uint32_t b = s_n & 1;
         if (!(ok = warp_wait_first(smem_u32(&sm.s_full[b]), (s_n >> 1) & 1, abort_flag, lim, 940))) break;
@@ -706,8 +749,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           y[i + 1] = __float_as_uint(d1);
         }
         if (j < it.low0 || j >= it.clean) {                            // not all of the tile is seen by all rows
-          const int u = 4 * j + h, from = 32 * u + (u < it.first ? 0 : it.skip);
-          const uint32_t f = (low_bits(p + 1 - from) & ~low_bits(low - from)) | low_bits(sinks - from);
+          const uint32_t f = seen(4 * j + h);
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (!(f >> i & 1)) x[i] = y[i] = 0;

@@ -818,7 +818,7 @@ ra_status ra_window_attn_fwd(const void* q, int64_t q_row_stride, const void* k,
  *             they were.
  * P and dS are rounded to bf16 for their products, all sums are fp32, in an order fixed by the
  * lengths (the same call gives the same bits).  The error of delta that the rounding of o brings is taken
- * out of dK where P sums to 1 over a row.
+ * out of dK where P sums to 1 over a row, and out of dQ where the row's keys are few as well.
  * A row whose lse is +inf or -inf has no weight, so that its gradient is 0.
  * Values of a sequence must be finite: one that is not may reach the gradients of tokens
  * up to 128 positions from those that see it.  Other sequences' values do not matter.

@@ -180,6 +180,64 @@ def test_paged_window_of_everything_is_chunk_attention_and_calls_repeat(ra):
     assert all(torch.equal(a, b) for a, b in zip(*twice))
 
 
+def test_paged_replayed_with_other_lengths_beside_another_stream(ra):
+    """One captured call for any lengths, next to another graph on its own workspace."""
+    Hq, Hkv, d, bs, I, window, sink, R, T = 8, 2, 64, 16, 4, 70, 3, 3, 320
+    graphs = []
+    for i in range(2):
+        k, v, _, _ = paged(20 + i, [800, 800, 800], Hkv, d, bs, I, 1, 2, poison=False)
+        table = torch.randperm(k.shape[1], generator=torch.Generator().manual_seed(i)).to(torch.int32)[:75].view(3, 25)
+        q = torch.randn((T, Hq, d), generator=torch.Generator().manual_seed(30 + i)).to(BF)
+        qd, kd, vd, td = dev(q, k, v, table)
+        s, c = (torch.zeros(m, dtype=torch.int32, device=DEV) for m in (R + 1, R))
+        ws = torch.empty(ra.cp_window_attn_workspace_size(Hq, Hkv, d), dtype=torch.uint8, device=DEV)
+        o, lse = torch.zeros((T, Hq, d), dtype=BF, device=DEV), torch.zeros((T, Hq), device=DEV)
+
+        def call():
+            ra.cp_window_attn(qd, kd, vd, td, s, c, window, I, 1, 2, n_sink=sink, workspace=ws, o=o, lse=lse)
+
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append((q, k, v, table, s, c, o, lse, g, (qd, kd, vd, td, ws)))
+    for n, ctx in (([1, 1, 1], [800, 3, 412]), ([300, 0, 20], [700, 0, 800]), ([0, 0, 0], [5, 5, 5]), ([7, 160, 1], [7, 161, 800])):
+        qsl = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32)
+        for x in graphs:
+            x[4].copy_(qsl)
+            x[5].copy_(i32(*ctx))
+            x[6].fill_(7.0)
+            x[7].fill_(7.0)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graphs[0][8].replay()
+        with torch.cuda.stream(side):
+            graphs[1][8].replay()
+        torch.cuda.current_stream().wait_stream(side)
+        check_status(ra)
+        m = sum(n)
+        for q, k, v, table, s, c, o, lse, _, _ in graphs:
+            if m:
+                assert_chunk(o[:m], lse[:m], O.cp_window_attn(q[:m], k, v, table, qsl, ctx, window, sink, bs, I, 1, 2))
+            assert (o[m:] == 7).all() and (lse[m:] == 7).all()
+
+
+def test_paged_past_32_bit_offsets(ra):
+    """Blocks at the far end of caches of more than 2^31 elements."""
+    NB, Hq, Hkv, d, bs, ctx, n, window, sink = 17000, 16, 8, 128, 128, [300, 200], [130, 1], 90, 4
+    k, v, table, _ = paged(40, ctx, Hkv, d, bs, 16, 1, 1, poison=False)
+    q, qsl = batch(40, n, Hq, d)
+    ref = O.cp_window_attn(q, k, v, table, qsl, ctx, window, sink, bs, 16, 1, 1)
+    far = NB - k.shape[1]
+    kc, vc = (torch.zeros((1, NB, Hkv, bs, d), dtype=BF, device=DEV) for _ in range(2))
+    kc[:, far:], vc[:, far:] = k.to(DEV), v.to(DEV)
+    o, lse = ra.cp_window_attn(*dev(q), kc, vc, *dev(torch.where(table < 0, table, table + far), qsl, i32(*ctx)), window, 16, 1, 1,
+                               n_sink=sink)
+    check_status(ra)
+    assert_chunk(o, lse, ref)
+
+
 # ---------------------------------------------------------------------- packed sequences
 
 # lengths, Hq, Hkv, d, window, sink
@@ -257,6 +315,26 @@ def test_packed(ra, case):
     c = ra.window_attn_bwd(dd, *(t.contiguous() for t in (qd, kd, vd)), oe, le, sd, window, n_sink=sink)
     check_status(ra)
     assert all(torch.equal(s, t) for s, t in zip(b, c))
+
+
+def test_packed_many_sequences(ra):
+    """More sequences than a block of the list building holds, empty ones among them; several rounds of key tiles, and first
+    tokens that long sequences see from afar."""
+    rng = np.random.default_rng(8)
+    n = rng.choice([0, 0, 1, 1, 2, 5, 40, 130], size=1500)
+    n[[3, 700, 1100, 1499]] = [600, 450, 513, 700]
+    Hq, Hkv, d, window, sink = 4, 2, 64, 100, 3
+    x, do, qsl = packed(8, n, Hq, Hkv, d)
+    q, k, v = parts(x, Hq, Hkv)
+    ref = O.window_attn(q, k, v, qsl, window, sink)
+    xd, dd, sd = dev(x, do, qsl)
+    o, lse = ra.window_attn_fwd(*parts(xd, Hq, Hkv), sd, window, n_sink=sink)
+    check_status(ra)
+    assert_chunk(o, lse, ref)
+    oe, le = torch.from_numpy(ref[0]).to(BF).to(DEV), torch.from_numpy(ref[1]).float().to(DEV)
+    got = ra.window_attn_bwd(dd, *parts(xd, Hq, Hkv), oe, le, sd, window, n_sink=sink)
+    check_status(ra)
+    assert_grads(got, O.window_attn_grad(do, q, k, v, qsl, window, sink))
 
 
 def test_packed_rows_of_nobody_and_ranges(ra):
@@ -375,6 +453,23 @@ def test_packed_scale_sharp_and_large_values(ra):
     check_status(ra)
     # bound holds 2^-11 (4.9e-4) of what is summed for the weights' own error: here it is 1.3e-3 + 4.9e-4, at most 4 times
     assert_grads(got, (want, [4 * b for b in bound]))
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,window", [(4, 2, 128, 64), (6, 2, 64, 3), (1, 1, 64, 8)])
+def test_packed_gradient_of_short_rows_is_exact(ra, Hq, Hkv, d, window):
+    """Rows of 2 to 8 keys, whose delta is summed from P and dP: o's rounding to bf16 (up to 2^-8 of the delta, 0.003 of
+    dQ's norm with 2 keys) does not reach dQ.  What is left is the arithmetic of fp32 and dS in two parts of bf16: a weight
+    off by 2^-11 at most, and with it dQ's norm."""
+    n = [2, 3, 4, 5, 8, 2, 7, 6] * 20
+    x, do, qsl = packed(d, n, Hq, Hkv, d)
+    q, k, v = parts(x, Hq, Hkv)
+    ref = O.window_attn(q, k, v, qsl, window, 0)
+    dq, _, _ = O.window_attn_grad(do, q, k, v, qsl, window, 0)[0]
+    xd, dd, sd = dev(x, do, qsl)
+    oe, le = torch.from_numpy(ref[0]).to(BF).to(DEV), torch.from_numpy(ref[1]).float().to(DEV)
+    got = ra.window_attn_bwd(dd, *parts(xd, Hq, Hkv), oe, le, sd, window, out_dtype=torch.float32)[0].double().cpu().numpy()
+    check_status(ra)
+    assert np.linalg.norm(got - dq) <= 2.0 ** -11 * np.linalg.norm(dq)
 
 
 def test_packed_gradient_against_differences(ra):
