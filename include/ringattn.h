@@ -730,7 +730,7 @@ ra_status ra_cp_evict(void* k_cache, void* v_cache, float* weights, const int32_
  * rot, style, inv_freq, axis, mscale: as ra_rope_apply_axes; axis NULL: one axis (n_axes 1).
  *             inv_freq NULL and rot 0: nothing is turned, K is stored and Q copied as they are.
  * Tokens of no request are not stored and their q_out is left as it was.  A slot that
- * several tokens of a call have (requests that share a block) gets one of them.
+ * several tokens of a call have (requests that share a block) holds elements of any of them.
  * Requires d <= 1024, d * element size a multiple of 16 bytes (RA_ERR_UNSUPPORTED
  * otherwise), heads * d < 2^26, T < 2^31, sizes of the cache as ra_cp_chunk_attn's but any
  * block size.
