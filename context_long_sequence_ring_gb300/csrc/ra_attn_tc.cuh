@@ -241,6 +241,13 @@ __device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
 }
 
+// Limit of a wait during which others may work off `tiles` tiles, each under the limit itself: in a role that has nothing to
+// do with most of them, or does something once for many.
+__device__ __forceinline__ long long limit_over(long long limit, long long tiles) {
+  constexpr long long kLongest = 1ll << 62;
+  return limit < kLongest / (tiles + 1) ? limit * (tiles + 1) : kLongest;
+}
+
 template <int NS>
 struct Ring {
   int st = 0;

@@ -637,15 +637,23 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   } else if (warp == 2) {
     // ============================================================ zeroing of K rows past the sequence
     // A dirty tile is taken up once the load has been announced: from then on its stage's barrier can
-    // only move from loading to loaded, so that the parity waited for is the right one.
+    // only move from loading to loaded, so that the parity waited for is the right one.  The tiles before it are passed over
+    // here while the others work them off (of one long sequence nearly all), which the limit allows for.
     Ring<KS> kr;
     uint32_t dirty_ph = 0;
+    long long past = 0;                // tiles, an item's start and end counted as one, since the last dirty one
     bool ok = true;
     for (int m = 0; m < rounds && ok; ++m) {
       if (!get(m, it)) continue;
+      ++past;
       for (int j = 0; j < it.nt; ++j, kr.advance()) {
-        if (j < it.dirty) continue;
-        if (!(ok = warp_wait(smem_u32(&sm.k_dirty[kr.st]), (dirty_ph >> kr.st) & 1, abort_flag, lim, 930))) break;
+        if (j < it.dirty) {
+          ++past;
+          continue;
+        }
+        if (!(ok = warp_wait(smem_u32(&sm.k_dirty[kr.st]), (dirty_ph >> kr.st) & 1, abort_flag, limit_over(lim, past), 930)))
+          break;
+        past = 0;
         dirty_ph ^= 1u << kr.st;
         if (!(ok = warp_wait(smem_u32(&sm.k_full[kr.st]), kr.ph, abort_flag, lim, 931))) break;
         const int left = it.n - it.skip - BN * j;                     // rows of the sequence in this tile
@@ -851,8 +859,7 @@ struct Announcer {
   int longest = 0;
   __device__ bool put(const KeyItem& x) {
     const int i = at % kAhead;
-    const long long far = 1ll << 62, most = lim < far / (longest + 1) ? lim * (longest + 1) : far;
-    if (!mbar_wait(smem_u32(&ring.empty[i]), ((at / kAhead) & 1) ^ 1, abort_flag, most, 906)) return false;
+    if (!mbar_wait(smem_u32(&ring.empty[i]), ((at / kAhead) & 1) ^ 1, abort_flag, limit_over(lim, longest), 906)) return false;
     longest = max(longest, x.its);
     ring.item[i] = x;
     mbar_arrive(smem_u32(&ring.full[i]));
