@@ -963,18 +963,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   } else if (warp == 2) {
     // ============================================================ zeroing of V rows past the context
     // A dirty tile is taken up once the producer has announced it: from then on its stage's barrier can
-    // only move from loading to loaded, so that the parity waited for is the right one.
+    // only move from loading to loaded, so that the parity waited for is the right one.  Other tiles are passed over here
+    // while the other roles work them off, which the limits allow for.
     Ring<NS> ring;
     uint32_t dirty_ph = 0;
+    long long past = 0;                // tiles, a segment's start and end counted as one, since the last dirty one
     bool ok = true;
-    while (ok && segs.next(sm, sg, abort_flag, lim, true)) {
+    while (ok && segs.next(sm, sg, abort_flag, limit_over(lim, past), true)) {
       const int nt = sg.nt;
+      ++past;
       if (nt <= 0) continue;
       const int la = sg.pair ? 1 : NB;
       for (int j = 0; j < min(la, nt); ++j) ring.advance();
       for (int j = 0; j < nt; ++j) {
         if (j >= sg.dirty) {
-          if (!(ok = warp_wait(smem_u32(&sm.v_dirty[ring.st]), (dirty_ph >> ring.st) & 1, abort_flag, lim, 540))) break;
+          if (!(ok = warp_wait(smem_u32(&sm.v_dirty[ring.st]), (dirty_ph >> ring.st) & 1, abort_flag, limit_over(lim, past), 540)))
+            break;
+          past = 0;
           dirty_ph ^= 1u << ring.st;
           if (!(ok = warp_wait(smem_u32(&sm.kv_full[ring.st]), ring.ph, abort_flag, lim, 541))) break;
           const uint64_t lm = F::kWindow ? 0 : tile_limits(a, sg.r, false, sg.t0 + j, sg.L);
@@ -1004,6 +1009,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sm.v_clean[ring.st]));
           __syncwarp();
+        } else {
+          ++past;
         }
         ring.advance();
         if (!kJoint<D> && j + la < nt) ring.advance();
@@ -1017,11 +1024,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       Join<F>* join = static_cast<Join<F>*>(a.join);
       SegIter<F> it(a, plan, blockIdx.x, first, pre, mine);
       uint32_t i = 0;
+      int longest = 0;                   // segment so far, in tiles: as long as one, the others may take to read the next
       do {
         if (more) more = it.next(sg);
         if (!more) sg.pair = -1;
         const int b = i & (kSegs - 1);
-        if (!mbar_wait(smem_u32(&sm.seg_empty[b]), ((i / kSegs) & 1) ^ 1, abort_flag, lim, 572)) break;
+        if (!mbar_wait(smem_u32(&sm.seg_empty[b]), ((i / kSegs) & 1) ^ 1, abort_flag, limit_over(lim, longest), 572)) break;
+        if (more) longest = max(longest, sg.nt);
         sm.seg[b] = sg;
         mbar_arrive(smem_u32(&sm.seg_full[b]));
         if (more && sg.t0 == 0 && sg.nt < sg.all) {

@@ -29,6 +29,15 @@ def gradient(d, *lens):
     q, k, v = x[:, :32], x[:, 32:40], x[:, 40:]
     o, lse = rnd(T, 32, d), torch.full((T, 32), 9.0, device=dev)
     call(lambda: ra.window_attn_bwd(do, q, k, v, o, lse, s, 1 << 30))
+def packed(d, *lens):
+    T, s = sum(lens), i32(*[sum(lens[:i]) for i in range(len(lens) + 1)])
+    x = rnd(T, 48, d)
+    call(lambda: ra.window_attn_fwd(x[:, :32], x[:, 32:40], x[:, 40:], s, 1 << 30))
+def paged(d, n, ctx, window):
+    nb = -(-ctx // 128)
+    q, k, v = rnd(n, 32, d), rnd(1, nb, 8, 128, d), rnd(1, nb, 8, 128, d)
+    a = q, k, v, torch.arange(nb, dtype=torch.int32, device=dev).view(1, nb), i32(0, n), i32(ctx)
+    call((lambda: ra.cp_window_attn(*a, window, 16, 1, 1, n_sink=4)) if window else (lambda: ra.cp_chunk_attn(*a, 16, 1, 1)))
 for what, *a in json.loads(sys.argv[2]):
     globals()[what](*a)
 if sys.argv[3] == "save":
@@ -66,3 +75,12 @@ def test_gradient_whose_last_tiles_alone_pass_a_sequences_end(d, lens, tmp_path)
     """The warp that zeroes rows past a sequence's end has its first tile after nearly all of the dQ kernel, which takes some
     10^6 cycles; no tile takes 2 * 10^5."""
     check(200000, [["gradient", d, *lens]], tmp_path)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("work", [["packed", 16383], ["packed", 9001, 40, 9003], ["paged", 8003, 16321, 12000],
+                                  ["paged", 8003, 16321, 0]], ids=str)
+def test_forward_of_items_of_many_tiles(d, work, tmp_path):
+    """Items are announced four ahead, so that one is waited for while another is worked off, some 100 tiles and 2 * 10^5
+    cycles; the warp that zeroes rows waits past several.  No tile takes 6 * 10^4 cycles."""
+    check(60000, [[work[0], d, *work[1:]]], tmp_path)
