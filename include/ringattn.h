@@ -818,7 +818,9 @@ ra_status ra_window_attn_fwd(const void* q, int64_t q_row_stride, const void* k,
  *             they were.
  * P and dS are rounded to bf16 for their products, all sums are fp32, in an order fixed by the
  * lengths (the same call gives the same bits).  The error of delta that the rounding of o brings is taken
- * out of dK where P sums to 1 over a row, and out of dQ where the row's keys are few as well.
+ * out of dK, and out of dQ where the row's keys are few, in rows whose P sum to 1 to within 2^-13 (and the
+ * rounding of lse), if it is one that this rounding can bring, at most 2^-8 sum |dO O|.  (With o and lse of more
+ * keys, the part in delta of others that hold as little weight as that may count as rounding and go with it.)
  * A row whose lse is +inf or -inf has no weight, so that its gradient is 0.
  * Values of a sequence must be finite: one that is not may reach the gradients of tokens
  * up to 128 positions from those that see it.  Other sequences' values do not matter.
