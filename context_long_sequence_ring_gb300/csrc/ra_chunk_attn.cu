@@ -21,7 +21,7 @@ extern "C" ra_status ra_cp_chunk_attn(const void* q, const void* k_cache, const 
                                       ra_stream stream) {
   ra::clear_error();
   const ra_status st = check_chunk_paged(q, k_cache, v_cache, block_table, query_start_loc, ctx_lens, T, R, Hq, Hkv, d,
-                                         block_size, interleave, pcp, dcp, max_vblocks, num_blocks, o, out_dt, workspace,
+                                         block_size, interleave, pcp, dcp, max_vblocks, num_blocks, o, out_dt, lse, workspace,
                                          ws_bytes, chunk_workspace<CausalPaged>(d));
   if (st != RA_OK || T == 0) return st;
   ChunkArgs a;

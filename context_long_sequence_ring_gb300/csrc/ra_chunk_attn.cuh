@@ -1444,7 +1444,7 @@ ra_status launch_chunk_paged(const void* q, const void* k, const void* v, const 
 inline ra_status check_chunk_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                                    const int32_t* query_start_loc, const int32_t* ctx_lens, int64_t T, int32_t R, int32_t Hq,
                                    int32_t Hkv, int32_t d, int32_t block_size, int32_t interleave, int32_t pcp, int32_t dcp,
-                                   int32_t max_vblocks, int64_t num_blocks, const void* o, ra_dtype out_dt,
+                                   int32_t max_vblocks, int64_t num_blocks, const void* o, ra_dtype out_dt, const void* lse,
                                    const void* workspace, size_t ws_bytes, size_t need) {
   const ra_status st = check_paged(R, Hkv, block_size, interleave, pcp, dcp, max_vblocks, num_blocks);
   if (st != RA_OK) return st;
@@ -1460,7 +1460,12 @@ inline ra_status check_chunk_paged(const void* q, const void* k_cache, const voi
                  ra::aligned16(workspace),
              "q, the caches, o and workspace must be 16-byte aligned");
   RA_REQUIRE(ws_bytes >= need, "workspace too small (%zu < %zu bytes)", ws_bytes, need);
-  return RA_OK;
+  const uint64_t rows = static_cast<uint64_t>(T) * Hq;
+  const uint64_t cache = static_cast<uint64_t>(pcp) * dcp * num_blocks * Hkv * block_size * d * 2;
+  return ra::check_workspace_apart(ra::Span{workspace, need}, ra::Span{q, rows * d * 2}, ra::Span{k_cache, cache},
+                                   ra::Span{v_cache, cache}, ra::Span{block_table, static_cast<uint64_t>(R) * max_vblocks * 4},
+                                   ra::Span{query_start_loc, (R + 1ull) * 4}, ra::Span{ctx_lens, R * 4ull},
+                                   ra::Span{o, rows * d * (out_dt == RA_BF16 ? 2 : 4)}, ra::Span{lse, rows * 4});
 }
 
 }  // namespace

@@ -32,6 +32,24 @@ inline bool rows_meet(const void* pa, int64_t sa, int64_t wa, const void* pb, in
   return off < wa || off + wb > sa;
 }
 
+// Bytes [p, p + n); of [T, w] rows s apart, from the first to the last.
+struct Span {
+  const void* p;
+  uint64_t n;
+};
+inline Span row_span(const void* p, int64_t T, int64_t s, int64_t w) { return Span{p, static_cast<uint64_t>((T - 1) * s + w)}; }
+inline bool spans_meet(const Span& a, const Span& b) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && x < y + b.n && y < x + a.n;
+}
+// A workspace lies over none of what a call reads and writes.
+template <class... S>
+ra_status check_workspace_apart(const Span& workspace, const S&... others) {
+  if ((spans_meet(workspace, others) || ...))
+    return fail(RA_ERR_INVALID_ARG, "the workspace must not overlap what the call reads and writes");
+  return RA_OK;
+}
+
 // Per-module device error words are fetched (and cleared) through these.
 int fetch_error_api(int* where);
 int fetch_error_cache(int* where);

@@ -26,10 +26,10 @@ inline ra_status row_map(CUtensorMap* map, const void* base, int D, int heads, i
   return RA_OK;
 }
 
-// What both directions require of their arguments.
+// What both directions require of their arguments; `need`: bytes of workspace.
 inline ra_status check_packed(const void* q, int64_t q_rs, const void* k, int64_t k_rs, const void* v, int64_t v_rs,
                               const int32_t* qsl, int64_t T, int32_t R, int32_t Hq, int32_t Hkv, int32_t d, int32_t window,
-                              int32_t n_sink, ra_dtype out_dt, const void* workspace, size_t ws_bytes) {
+                              int32_t n_sink, ra_dtype out_dt, const void* workspace, size_t ws_bytes, size_t& need) {
   RA_REQUIRE(out_dt == RA_F32 || out_dt == RA_BF16, "unknown out dtype");
   RA_REQUIRE(R >= 1 && Hkv >= 1 && Hq >= 1 && Hq % Hkv == 0, "R >= 1 and Hq (%d) a multiple of Hkv (%d) required", Hq, Hkv);
   RA_REQUIRE(T >= 0 && T < kFar && T < (int64_t(1) << 31) / Hq, "T must be in [0, 2^30), T*Hq below 2^31");
@@ -45,11 +45,12 @@ inline ra_status check_packed(const void* q, int64_t q_rs, const void* k, int64_
   RA_REQUIRE(q && k && v && qsl && workspace, "NULL pointer");
   RA_REQUIRE(ra::aligned16(q) && ra::aligned16(k) && ra::aligned16(v) && ra::aligned16(workspace),
              "q, k, v and workspace must be 16-byte aligned");
-  size_t need = 0;
   const ra_status st = ra_window_attn_workspace_size(T, R, Hq, Hkv, d, &need);
   if (st != RA_OK) return st;
   RA_REQUIRE(ws_bytes >= need, "workspace too small (%zu < %zu bytes)", ws_bytes, need);
-  return RA_OK;
+  const int64_t qw = static_cast<int64_t>(Hq) * d * 2, kw = static_cast<int64_t>(Hkv) * d * 2;
+  return ra::check_workspace_apart(ra::Span{workspace, need}, ra::row_span(q, T, 2 * q_rs, qw), ra::row_span(k, T, 2 * k_rs, kw),
+                                   ra::row_span(v, T, 2 * v_rs, kw), ra::Span{qsl, (R + 1ull) * 4});
 }
 
 }  // namespace

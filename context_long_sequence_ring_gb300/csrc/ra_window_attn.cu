@@ -27,7 +27,7 @@ extern "C" ra_status ra_cp_window_attn(const void* q, const void* k_cache, const
   ra::clear_error();
   RA_REQUIRE(window >= 1 && n_sink >= 0, "window >= 1 and n_sink >= 0 required");
   const ra_status st = check_chunk_paged(q, k_cache, v_cache, block_table, query_start_loc, ctx_lens, T, R, Hq, Hkv, d,
-                                         block_size, interleave, pcp, dcp, max_vblocks, num_blocks, o, out_dt, workspace,
+                                         block_size, interleave, pcp, dcp, max_vblocks, num_blocks, o, out_dt, lse, workspace,
                                          ws_bytes, chunk_workspace<WindowPaged>(d));
   if (st != RA_OK || T == 0) return st;
   ChunkArgs a;
@@ -57,10 +57,15 @@ extern "C" ra_status ra_window_attn_fwd(const void* q, int64_t q_row_stride, con
                                         float scale, void* o, ra_dtype out_dt, float* lse, void* workspace, size_t ws_bytes,
                                         ra_stream stream) {
   ra::clear_error();
-  const ra_status st = check_packed(q, q_row_stride, k, k_row_stride, v, v_row_stride, query_start_loc, T, R, Hq, Hkv, d,
-                                    window, n_sink, out_dt, workspace, ws_bytes);
+  size_t need = 0;
+  ra_status st = check_packed(q, q_row_stride, k, k_row_stride, v, v_row_stride, query_start_loc, T, R, Hq, Hkv, d, window,
+                              n_sink, out_dt, workspace, ws_bytes, need);
   if (st != RA_OK || T == 0) return st;
   RA_REQUIRE(o != nullptr && ra::aligned16(o), "o must be given and 16-byte aligned");
+  const uint64_t rows = static_cast<uint64_t>(T) * Hq;
+  if ((st = ra::check_workspace_apart(ra::Span{workspace, need}, ra::Span{o, rows * d * (out_dt == RA_BF16 ? 2 : 4)},
+                                      ra::Span{lse, rows * 4})) != RA_OK)
+    return st;
   ChunkArgs a;
   a.c = Paged{};
   a.c.Hkv = Hkv;
@@ -70,10 +75,9 @@ extern "C" ra_status ra_window_attn_fwd(const void* q, int64_t q_row_stride, con
   a.window = std::min(window, kFar);
   a.n_sink = std::min(n_sink, kFar);
   CUtensorMap mq, mk, mv;
-  ra_status s;
-  if ((s = row_map(&mq, q, d, Hq, T, q_row_stride, a.G, a.tpt)) != RA_OK) return s;
-  if ((s = row_map(&mk, k, d, Hkv, T, k_row_stride, 1, 32)) != RA_OK) return s;
-  if ((s = row_map(&mv, v, d, Hkv, T, v_row_stride, 1, 32)) != RA_OK) return s;
+  if ((st = row_map(&mq, q, d, Hq, T, q_row_stride, a.G, a.tpt)) != RA_OK) return st;
+  if ((st = row_map(&mk, k, d, Hkv, T, k_row_stride, 1, 32)) != RA_OK) return st;
+  if ((st = row_map(&mv, v, d, Hkv, T, v_row_stride, 1, 32)) != RA_OK) return st;
   return d == 128 ? launch_chunk<128, WindowPacked>(mq, mk, mv, a, stream)
                   : launch_chunk<64, WindowPacked>(mq, mk, mv, a, stream);
 }

@@ -1529,8 +1529,9 @@ extern "C" ra_status ra_window_attn_bwd(const void* q, int64_t q_row_stride, con
                                         int64_t dv_row_stride, ra_dtype out_dt, void* workspace, size_t ws_bytes,
                                         ra_stream stream) {
   ra::clear_error();
-  const ra_status st = check_packed(q, q_row_stride, k, k_row_stride, v, v_row_stride, query_start_loc, T, R, Hq, Hkv, d,
-                                    window, n_sink, out_dt, workspace, ws_bytes);
+  size_t need = 0;
+  ra_status st = check_packed(q, q_row_stride, k, k_row_stride, v, v_row_stride, query_start_loc, T, R, Hq, Hkv, d, window,
+                              n_sink, out_dt, workspace, ws_bytes, need);
   if (st != RA_OK) return st;
   const int64_t lim = int64_t(1) << 31, es = out_dt == RA_BF16 ? 2 : 4, qw = static_cast<int64_t>(Hq) * d,
                 kw = static_cast<int64_t>(Hkv) * d;
@@ -1548,17 +1549,20 @@ extern "C" ra_status ra_window_attn_bwd(const void* q, int64_t q_row_stride, con
     int64_t s, w;
   };
   const Rows outs[3] = {{dq, dq_row_stride * es, qw * es}, {dk, dk_row_stride * es, kw * es}, {dv, dv_row_stride * es, kw * es}};
-  const Rows ins[7] = {{q, q_row_stride * 2, qw * 2}, {k, k_row_stride * 2, kw * 2},    {v, v_row_stride * 2, kw * 2},
-                       {o, qw * 2, qw * 2},           {d_o, qw * 2, qw * 2},            {lse, Hq * 4, Hq * 4},
-                       {workspace, 1, 1}};
+  const Rows ins[6] = {{q, q_row_stride * 2, qw * 2}, {k, k_row_stride * 2, kw * 2}, {v, v_row_stride * 2, kw * 2},
+                       {o, qw * 2, qw * 2},           {d_o, qw * 2, qw * 2},         {lse, Hq * 4, Hq * 4}};
   for (int i = 0; i < 3; ++i) {
     for (int j = 0; j < i; ++j)
       RA_REQUIRE(!ra::rows_meet(outs[i].p, outs[i].s, outs[i].w, outs[j].p, outs[j].s, outs[j].w, T), "dq, dk and dv must not overlap");
-    for (int j = 0; j < 6; ++j)
-      RA_REQUIRE(!ra::rows_meet(outs[i].p, outs[i].s, outs[i].w, ins[j].p, ins[j].s, ins[j].w, T),
+    for (const Rows& in : ins)
+      RA_REQUIRE(!ra::rows_meet(outs[i].p, outs[i].s, outs[i].w, in.p, in.s, in.w, T),
                  "dq, dk and dv must not overlap the inputs");
   }
   const Layout at(T, R, Hq, Hkv, d);
+  auto span = [&](const Rows& x) { return ra::row_span(x.p, T, x.s, x.w); };
+  if ((st = ra::check_workspace_apart(ra::Span{workspace, need}, span(outs[0]), span(outs[1]), span(outs[2]), span(ins[3]),
+                                      span(ins[4]), span(ins[5]))) != RA_OK)
+    return st;
   uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
   GradArgs a = {};
   a.qsl = query_start_loc; a.T = T; a.R = R; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.D = d;

@@ -615,7 +615,7 @@ ra_status ra_cp_head_split(const float* o_local, const float* lse_local, int32_t
  * Slots past ctx_lens[r] are never used, whatever they hold (NaN too); V of a
  * token below ctx_lens[r] must be finite where a query of the same request
  * does not see it.
- * workspace   device scratch of ra_cp_chunk_attn_workspace_size() bytes,
+ * workspace   device scratch of ra_cp_chunk_attn_workspace_size() bytes, apart from all else of the call,
  *             16-byte aligned: fp32 partials of contexts that several CTAs
  *             share.  Calls that overlap on the GPU need one each.
  * Requires Hq % Hkv == 0, Hq/Hkv <= 64, d in {64, 128}, block_size % 16 == 0,
@@ -759,7 +759,7 @@ ra_status ra_cp_rope_append(const void* k, int64_t k_row_stride, int64_t k_head_
  * The rest as ra_cp_chunk_attn with causal = 1 (rows of no request, queries that see
  * nothing, limits, device bounds errors for the blocks that are looked at).  V of a token in a
  * block that is looked at must be finite below ctx_lens[r].
- * workspace   device scratch of ra_cp_window_attn_workspace_size() bytes, 16-byte aligned.
+ * workspace   device scratch of ra_cp_window_attn_workspace_size() bytes, 16-byte aligned, apart from all else of the call.
  *             Calls that overlap on the GPU need one each.
  * ---------------------------------------------------------------------- */
 ra_status ra_cp_window_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t d, size_t* bytes);
@@ -786,8 +786,8 @@ ra_status ra_cp_window_attn(const void* q, const void* k_cache, const void* v_ca
  * Scores, sums and partials are fp32; probabilities are rounded to bf16 for their product.
  * What a row does not see does not reach it, NaN included, except V rows of its own sequence that
  * are not finite.
- * workspace   device scratch of ra_window_attn_workspace_size() bytes, 16-byte aligned, for
- *             either direction.  Calls that overlap on the GPU need one each.
+ * workspace   device scratch of ra_window_attn_workspace_size() bytes, 16-byte aligned, apart
+ *             from all else of the call, for either direction.  Calls that overlap on the GPU need one each.
  * Requires Hq % Hkv == 0, Hq/Hkv <= 64, d in {64, 128}, T < 2^30, T*Hq < 2^31; q, k, v, o 16-byte
  * aligned.
  * Lengths are read on the device: a captured call may be replayed with others.
