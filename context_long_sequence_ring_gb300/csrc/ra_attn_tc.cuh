@@ -310,20 +310,36 @@ EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
-// Token-major [rows, H, D] bf16 tensor; box = 64 columns x 1 head x 128 rows,
-// 128-byte swizzle (the layout the MMA descriptors expect).
-ra_status make_map(CUtensorMap* map, const void* base, int D, int H, int64_t rows, uint32_t box_rows = 128) {
+// Map of a bf16 tensor of three dimensions, innermost first, strides (of the outer two) in elements: boxes of 64 columns in
+// the 128-byte swizzle the MMA descriptors expect.
+inline ra_status bf16_map(CUtensorMap* map, const void* base, int64_t D, int64_t n1, int64_t n2, int64_t stride1, int64_t stride2,
+                          uint32_t box1, uint32_t box2) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(H) * D * 2};
-  cuuint32_t box[3] = {64, 1, box_rows};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride1) * 2, static_cast<cuuint64_t>(stride2) * 2};
+  const cuuint32_t box[3] = {64, box1, box2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  auto encode = [&] {
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+    // a thread that has made no call of the runtime yet has no context; this gives it the current device's
+    int dev = 0;
+    RA_CUDA_TRY(cudaGetDevice(&dev));
+    RA_CUDA_TRY(cudaSetDevice(dev));
+    r = encode();
+  }
   if (r != CUDA_SUCCESS) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
   return RA_OK;
+}
+
+// Token-major [rows, H, D] bf16 tensor; box = 64 columns x 1 head x box_rows rows.
+inline ra_status make_map(CUtensorMap* map, const void* base, int D, int H, int64_t rows, uint32_t box_rows = 128) {
+  return bf16_map(map, base, D, H, rows, D, static_cast<int64_t>(H) * D, 1, box_rows);
 }
 
 }  // namespace

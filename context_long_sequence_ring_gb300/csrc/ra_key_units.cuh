@@ -114,19 +114,9 @@ __device__ __forceinline__ void tma_load_3d_once(uint32_t dst, const CUtensorMap
 }
 
 // ------------------------------------------------------------------ host side
-// Three-dimensional bf16 map with 64-column boxes in the 128-byte swizzle the MMA descriptors expect.
+// The map of dense [n2, n1, D].
 inline ra_status box_map(CUtensorMap* map, const void* base, int D, int64_t n1, int64_t n2, uint32_t box1, uint32_t box2) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(n1) * D * 2};
-  cuuint32_t box[3] = {64, box1, box2};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
-  return RA_OK;
+  return bf16_map(map, base, D, n1, n2, D, n1 * D, box1, box2);
 }
 
 }  // namespace

@@ -13,17 +13,7 @@ constexpr int kFar = 1 << 30;    // no position is further: contexts and sequenc
 // The map of [rows, heads, D] rows `stride` elements apart: boxes of 64 columns, box_heads heads, box_rows rows.
 inline ra_status row_map(CUtensorMap* map, const void* base, int D, int heads, int64_t rows, int64_t stride,
                          uint32_t box_heads, uint32_t box_rows) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
-  cuuint32_t box[3] = {64, box_heads, box_rows};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return ra::fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
-  return RA_OK;
+  return bf16_map(map, base, D, heads, rows, D, stride, box_heads, box_rows);
 }
 
 // What both directions require of their arguments; `need`: bytes of workspace.
