@@ -1,4 +1,5 @@
-"""Calls by threads that have made no CUDA call before, one after another."""
+"""Calls by threads that have made no CUDA call before, one after another, and a process's first calls by several threads at the
+same time, each with its stream, outputs and workspace."""
 import os
 import subprocess
 import sys
@@ -57,6 +58,25 @@ for name, f in calls.items():
     same(name, results, f(w, o))
 """
 
+TOGETHER = SETUP + r"""
+N = 12
+streams, spaces, last = [torch.cuda.Stream() for _ in range(N)], [space() for _ in range(N)], space()
+torch.cuda.synchronize()
+for name, f in calls.items():
+    gate, results = threading.Barrier(N), [None] * N
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            torch.cuda.current_stream().synchronize()      # this thread has its context
+            gate.wait()
+            collect(results, i, f, *spaces[i])
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(N)]
+    for t in threads: t.start()
+    for t in threads: t.join()
+    torch.cuda.synchronize()
+    results = [x if isinstance(x, str) else [y.clone() for y in x] for x in results]
+    same(name, results, f(*last))
+"""
+
 
 def run(child):
     r = subprocess.run([sys.executable, "-c", child, ROOT], capture_output=True, text=True, timeout=300)
@@ -65,3 +85,9 @@ def run(child):
 
 def test_a_thread_that_has_no_context():
     run(FRESH)
+
+
+@pytest.mark.parametrize("process", range(4))
+def test_several_threads_at_once(process):
+    """What a library looks up once must be there for all of them."""
+    run(TOGETHER)
