@@ -826,6 +826,11 @@ def cp_rope_append(k, v, k_cache, v_cache, block_table, query_start_loc, ctx_len
     return q_out
 
 
+def _reach(tokens: int) -> int:
+    """A window or a number of first tokens for the library, whose integers have 32 bits: no sequence is as long."""
+    return max(-1, min(tokens, 2 ** 31 - 1))
+
+
 def _out_rows(o, lse, T: int, Hq: int, d: int, out_dtype, device):
     if o is None:
         o = torch.empty((T, Hq, d), dtype=out_dtype, device=device)
@@ -859,8 +864,8 @@ def cp_window_attn(q, k_cache, v_cache, block_table, query_start_loc, ctx_lens, 
     o, lse = _out_rows(o, lse, T, Hq, d, out_dtype, q.device)
     _check(lib().ra_cp_window_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                    query_start_loc.data_ptr(), ctx_lens.data_ptr(), T, R, Hq, Hkv, d, bs, interleave, pcp,
-                                   dcp, max_vb, NB, window, n_sink, scale or 0.0, o.data_ptr(), _dt(o), lse.data_ptr(),
-                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   dcp, max_vb, NB, _reach(window), _reach(n_sink), scale or 0.0, o.data_ptr(), _dt(o),
+                                   lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                    torch._C._cuda_getCurrentRawStream(dev)))
     return o, lse
 
@@ -905,8 +910,8 @@ def window_attn_fwd(q, k, v, query_start_loc, window: int, n_sink: int = 0, scal
     dev, qrs, krs, vrs, T, R, Hq, Hkv, d, workspace = _need_packed(q, k, v, query_start_loc, workspace, o, lse)
     o, lse = _out_rows(o, lse, T, Hq, d, out_dtype, q.device)
     _check(lib().ra_window_attn_fwd(q.data_ptr(), qrs, k.data_ptr(), krs, v.data_ptr(), vrs, query_start_loc.data_ptr(), T,
-                                    R, Hq, Hkv, d, window, n_sink, scale or 0.0, o.data_ptr(), _dt(o), lse.data_ptr(),
-                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    R, Hq, Hkv, d, _reach(window), _reach(n_sink), scale or 0.0, o.data_ptr(), _dt(o),
+                                    lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                     torch._C._cuda_getCurrentRawStream(dev)))
     return o, lse
 
@@ -927,8 +932,8 @@ def window_attn_bwd(do, q, k, v, o, lse, query_start_loc, window: int, n_sink: i
     dq, dk, dv = (new(x) if g is None else g for x, g in ((q, dq), (k, dk), (v, dv)))
     rs = [_packed_rows(g, what, dev, dt, x.shape) for g, what, x in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v))]
     _check(lib().ra_window_attn_bwd(q.data_ptr(), qrs, k.data_ptr(), krs, v.data_ptr(), vrs, o.data_ptr(), lse.data_ptr(),
-                                    do.data_ptr(), query_start_loc.data_ptr(), T, R, Hq, Hkv, d, window, n_sink,
-                                    scale or 0.0, dq.data_ptr(), rs[0], dk.data_ptr(), rs[1], dv.data_ptr(), rs[2],
+                                    do.data_ptr(), query_start_loc.data_ptr(), T, R, Hq, Hkv, d, _reach(window),
+                                    _reach(n_sink), scale or 0.0, dq.data_ptr(), rs[0], dk.data_ptr(), rs[1], dv.data_ptr(), rs[2],
                                     _dt(dq), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                     torch._C._cuda_getCurrentRawStream(dev)))
     return dq, dk, dv
