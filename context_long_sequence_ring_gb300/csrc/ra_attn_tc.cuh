@@ -248,6 +248,8 @@ __device__ __forceinline__ long long limit_over(long long limit, long long tiles
   return __umul64hi(x, n) == 0 && most < 1ull << 62 ? static_cast<long long>(most) : 1ll << 62;
 }
 
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
+
 template <int NS>
 struct Ring {
   int st = 0;

@@ -406,7 +406,6 @@ struct BitMask {
       if (!(f >> i & 1)) x[i] = __float_as_uint(-CUDART_INF_F);
   }
 };
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
 
 // Positions below `lim` and not below `low`, or below `sink`.  Packed: column i of unit j is position 32 j + i, `skip`
 // further from unit `first` on.
@@ -572,19 +571,19 @@ struct __align__(1024) ChunkSmem {
 static_assert(sizeof(ChunkSmem<128, WindowPaged>) + 1024 <= 232448 && sizeof(ChunkSmem<64, WindowPaged>) + 1024 <= 232448,
               "227 KB of shared memory");
 
-// A role's reading of the announced segments, in order.
+// A role's reading of the announced segments, in order, by a whole warp.
 struct SegReader {
   uint32_t at = 0;
   bool ok = true;   // false: a wait expired, the part has not ended
   template <class Smem, class Seg>
-  __device__ bool next(Smem& sm, Seg& s, volatile int* abort_flag, long long limit, bool whole_warp) {
+  __device__ bool next(Smem& sm, Seg& s, volatile int* abort_flag, long long limit) {
     const int i = at & (kSegs - 1);
     const uint32_t bar = smem_u32(&sm.seg_full[i]), ph = (at / kSegs) & 1;
-    ok = whole_warp ? warp_wait(bar, ph, abort_flag, limit, 570) : mbar_wait(bar, ph, abort_flag, limit, 571);
+    ok = warp_wait(bar, ph, abort_flag, limit, 570);
     if (!ok) return false;
     s = sm.seg[i];
-    if (whole_warp) __syncwarp();
-    if (!whole_warp || (threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.seg_empty[i]));
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.seg_empty[i]));
     ++at;
     return s.pair >= 0;
   }
@@ -676,7 +675,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     bool ok = true;
     const uint64_t once = policy_once();      // a split tile's keys are read by one CTA
     const int oob = static_cast<int>(a.c.W * a.c.num_blocks * a.c.Hkv);   // past the last block: zero fill
-    while (ok && segs.next(sm, sg, abort_flag, lim, true)) {
+    while (ok && segs.next(sm, sg, abort_flag, lim)) {
       const int nt = sg.nt;
       if (nt <= 0) continue;
       const bool pair = sg.pair;
@@ -864,7 +863,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         return true;
       };
-      while (ok && segs.next(sm, sg, abort_flag, lim, true)) {
+      while (ok && segs.next(sm, sg, abort_flag, lim)) {
         const int nt = sg.nt;
         if (nt <= 0) continue;
         const int dirty = sg.dirty;
@@ -969,7 +968,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint32_t dirty_ph = 0;
     long long past = 0;                // tiles, a segment's start and end counted as one, since the last dirty one
     bool ok = true;
-    while (ok && segs.next(sm, sg, abort_flag, limit_over(lim, past), true)) {
+    while (ok && segs.next(sm, sg, abort_flag, limit_over(lim, past))) {
       const int nt = sg.nt;
       ++past;
       if (nt <= 0) continue;
@@ -1056,7 +1055,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       return warp_wait(smem_u32(&sm.pv_done[turn(slot, i)]), phase(i), abort_flag, lim, site);
     };
     bool ok = true;
-    while (ok && segs.next(sm, sg, abort_flag, lim, true)) {
+    while (ok && segs.next(sm, sg, abort_flag, lim)) {
       const int nt = sg.nt;
       const bool pair = sg.pair;
       const int tok = sg.tok0 + (pair ? h * a.tpt : 0) + row_tok;

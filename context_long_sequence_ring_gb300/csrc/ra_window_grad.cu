@@ -78,7 +78,7 @@ struct Shared {
 struct GradArgs {
   const int32_t* qsl;
   int64_t T;
-  int R, Hq, Hkv, G, D, window, n_sink, tpt, out_bf16;
+  int R, Hq, Hkv, G, window, n_sink, tpt, out_bf16;
   float scale, scale_log2;
   const __nv_bfloat16 *o, *d_o;
   const float* lse;
@@ -113,7 +113,6 @@ __device__ __forceinline__ int long_tiles(const GradArgs& a, int n) {
 __device__ __forceinline__ int64_t cost_of(const GradArgs& a, int n, int k) {
   return static_cast<int64_t>(query_tiles(a, n, k)) * a.G + kOver;
 }
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
 
 // ------------------------------------------------------------------ prepare
 // Inclusive prefix sum (or maximum, of values that are not negative) over the block.
@@ -1565,7 +1564,7 @@ extern "C" ra_status ra_window_attn_bwd(const void* q, int64_t q_row_stride, con
     return st;
   uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
   GradArgs a = {};
-  a.qsl = query_start_loc; a.T = T; a.R = R; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.D = d;
+  a.qsl = query_start_loc; a.T = T; a.R = R; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
   a.window = std::min(window, kFar);
   a.n_sink = std::min(n_sink, kFar);
   a.tpt = BM / a.G;
