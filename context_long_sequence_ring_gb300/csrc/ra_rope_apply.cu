@@ -64,45 +64,6 @@ __device__ __forceinline__ float load1(const float* x) { return *x; }
 __device__ __forceinline__ void store1(__nv_bfloat16* x, float v) { *x = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store1(float* x, float v) { *x = v; }
 
-// A word of 16 or 8 bytes as fp32 values, and back (rounded to nearest even).
-template <typename T, typename W> struct Word;
-template <typename W> struct Word<float, W> {
-  static constexpr int N = sizeof(W) / 4;
-  __device__ static void unpack(const W& u, float (&f)[N]) {
-    const float* x = reinterpret_cast<const float*>(&u);
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = x[i];
-  }
-  __device__ static W pack(const float (&f)[N]) {
-    W u;
-    float* x = reinterpret_cast<float*>(&u);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = f[i];
-    return u;
-  }
-};
-template <typename W> struct Word<__nv_bfloat16, W> {
-  static constexpr int N = sizeof(W) / 2;
-  __device__ static void unpack(const W& u, float (&f)[N]) {
-    const uint32_t* x = reinterpret_cast<const uint32_t*>(&u);
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      f[2 * i] = __uint_as_float(x[i] << 16);
-      f[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
-    }
-  }
-  __device__ static W pack(const float (&f)[N]) {
-    W u;
-    uint32_t* x = reinterpret_cast<uint32_t*>(&u);
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      x[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return u;
-  }
-};
-
 constexpr int kHeads = 8;   // heads of a thread, at most
 
 // Rows of whole words.  A "unit" of a head is one word of pairs (interleaved),
@@ -113,10 +74,10 @@ constexpr int kHeads = 8;   // heads of a thread, at most
 // in bf16 (half) take 99 us, 6.8 TB/s, the rate of a plain copy.  4 heads a thread:
 // 103 us; all 40 in a loop that has 8 in flight: 140 us, since a thread's loads then
 // wait for its stores.
-template <typename T, typename W, bool INTER, bool AXES>
+template <typename T, int BYTES, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kThreads, 2) rope_words_kernel(const __grid_constant__ Params p) {
-  using V = Word<T, W>;
-  constexpr int N = V::N, P = INTER ? N / 2 : N;      // values of a word, pairs of a unit
+  constexpr int N = BYTES / sizeof(T), P = INTER ? N / 2 : N;      // values of a word, pairs of a unit
+  using W = Vec<T, N, BYTES>;
   const uint32_t w = blockIdx.x * kThreads + threadIdx.x;   // (row, head group, unit)
   if (w >= static_cast<uint32_t>(p.row_end) * p.per_row) return;
   int u, group;
@@ -150,24 +111,27 @@ __global__ void __launch_bounds__(kThreads, 2) rope_words_kernel(const __grid_co
       continue;
     }
     float f[N], o[N];
-    V::unpack(a[j], f);
+    unpack(a[j], f);
     if (INTER) {
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         o[2 * i] = turn_re(f[2 * i], f[2 * i + 1], c[i], sn[i]);
         o[2 * i + 1] = turn_im(f[2 * i], f[2 * i + 1], c[i], sn[i]);
       }
-      *reinterpret_cast<W*>(out) = V::pack(o);
+      pack(a[j], o);
+      *reinterpret_cast<W*>(out) = a[j];
     } else {
       float f2[N], o2[N];
-      V::unpack(b[j], f2);
+      unpack(b[j], f2);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         o[i] = turn_re(f[i], f2[i], c[i], sn[i]);
         o2[i] = turn_im(f[i], f2[i], c[i], sn[i]);
       }
-      *reinterpret_cast<W*>(out) = V::pack(o);
-      *reinterpret_cast<W*>(out + half) = V::pack(o2);
+      pack(a[j], o);
+      pack(b[j], o2);
+      *reinterpret_cast<W*>(out) = a[j];
+      *reinterpret_cast<W*>(out + half) = b[j];
     }
   }
 }
@@ -204,10 +168,10 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
   }
 }
 
-// Launches the kernel on rows of words W; more than 2^31 threads in several launches.
-template <typename T, typename W, bool AXES>
+// Launches the kernel on rows of words of BYTES bytes; more than 2^31 threads in several launches.
+template <typename T, int BYTES, bool AXES>
 ra_status launch_words(Params& p, bool inter, cudaStream_t stream) {
-  constexpr int N = Word<T, W>::N;
+  constexpr int N = BYTES / sizeof(T);
   p.turn_units = inter ? p.rot / N : p.rot / 2 / N;
   const bool copies = p.src != p.dst;                   // in place the rest of a head stays where it is
   const int units = p.turn_units + (copies ? (p.d - p.rot) / N : 0);
@@ -224,8 +188,8 @@ ra_status launch_words(Params& p, bool inter, cudaStream_t stream) {
   for (p.row0 = 0; p.row0 < rows; p.row0 += most) {
     p.row_end = static_cast<int32_t>(std::min(most, rows - p.row0));
     const unsigned blocks = static_cast<unsigned>(ra::ceil_div(static_cast<int64_t>(p.row_end) * p.per_row, kThreads));
-    if (inter) rope_words_kernel<T, W, true, AXES><<<blocks, kThreads, 0, stream>>>(p);
-    else rope_words_kernel<T, W, false, AXES><<<blocks, kThreads, 0, stream>>>(p);
+    if (inter) rope_words_kernel<T, BYTES, true, AXES><<<blocks, kThreads, 0, stream>>>(p);
+    else rope_words_kernel<T, BYTES, false, AXES><<<blocks, kThreads, 0, stream>>>(p);
     RA_LAUNCH_CHECK("rope_words_kernel");
   }
   return RA_OK;
@@ -281,11 +245,11 @@ ra_status rope_apply(const void* src, int64_t src_rows, int64_t src_row_stride, 
   auto launch = [&](auto axes) -> ra_status {
     constexpr bool AXES = decltype(axes)::value;
     if (words(16))
-      return dt == RA_BF16 ? launch_words<__nv_bfloat16, uint4, AXES>(p, inter, stream)
-                           : launch_words<float, uint4, AXES>(p, inter, stream);
+      return dt == RA_BF16 ? launch_words<__nv_bfloat16, 16, AXES>(p, inter, stream)
+                           : launch_words<float, 16, AXES>(p, inter, stream);
     if (words(8))
-      return dt == RA_BF16 ? launch_words<__nv_bfloat16, uint2, AXES>(p, inter, stream)
-                           : launch_words<float, uint2, AXES>(p, inter, stream);
+      return dt == RA_BF16 ? launch_words<__nv_bfloat16, 8, AXES>(p, inter, stream)
+                           : launch_words<float, 8, AXES>(p, inter, stream);
     const int64_t units = rot / 2 + (d - rot);
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ra::ceil_div(rows * units, kThreads), 152 * 64));
     if (dt == RA_BF16) {

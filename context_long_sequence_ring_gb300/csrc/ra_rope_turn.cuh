@@ -38,6 +38,50 @@ __device__ __forceinline__ void turn(const Turns& p, int i, float m, float& c, f
 __device__ __forceinline__ float turn_re(float a, float b, float c, float s) { return fmaf(a, c, -__fmul_rn(b, s)); }
 __device__ __forceinline__ float turn_im(float a, float b, float c, float s) { return fmaf(b, c, __fmul_rn(a, s)); }
 
+// N values aligned to A bytes, and as fp32 ones (rounded to nearest even on the way back).
+template <typename T, int N, int A>
+struct alignas(A) Vec {
+  T x[N];
+};
+template <int N, int A>
+__device__ __forceinline__ void unpack(const Vec<float, N, A>& v, float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = v.x[i];
+}
+template <int N, int A>
+__device__ __forceinline__ void pack(Vec<float, N, A>& v, const float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v.x[i] = f[i];
+}
+template <int N, int A>
+__device__ __forceinline__ void unpack(const Vec<__nv_bfloat16, N, A>& v, float (&f)[N]) {
+  if constexpr (A >= 4) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __bfloat162float(v.x[i]);
+  }
+}
+template <int N, int A>
+__device__ __forceinline__ void pack(Vec<__nv_bfloat16, N, A>& v, const float (&f)[N]) {
+  if constexpr (A >= 4) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v.x[i] = __float2bfloat16_rn(f[i]);
+  }
+}
+
 // A position as a float; 0 where it is out of range.
 __device__ __forceinline__ float position_at(const int32_t* positions, int64_t at, int site) {
   const int32_t m = positions[at];
