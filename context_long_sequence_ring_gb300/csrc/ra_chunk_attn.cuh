@@ -35,14 +35,15 @@
 // two row tiles; their partial (m, l, O) go to the workspace (at most two per
 // CTA) and a second small kernel joins them.
 //
-// Measured (32/8 heads of 128, 8 devices, captured calls): 48 requests with 1-6 drafted
-// tokens over 2048-16384: 275-279 us, 6.6 TB/s, 97 % of the copy rate; one token over
-// 131072: 85 us, 6.3 TB/s; 4 single tokens over 200-2000: 18.7 us; 4096 tokens of a
-// prompt of 32768: 1.28-1.30 ms, 1580 TFLOP/s.  12 requests (24/8 heads of
-// 64, blocks of 16), prompts of 300-511 new tokens among single ones: 42 us.
-// With a window of 4096: 4096 tokens of a prompt 270 us (joining 20), 64 single tokens 195 us, 5.8 TB/s, 32768 packed tokens
-// 1.40 ms (a sequence of 16384 under no window 1.34 ms, 1640 TFLOP/s).  What a window costs is an item's start and end and
-// its masked tiles at either end, 11-13 thousand cycles, four tiles' time.
+// Measured (32/8 heads of 128, 8 devices; calls, joining included): 48 requests with 1-6 drafted
+// tokens over 2048-16384: 279-284 us, 6.5 TB/s, 96 % of the copy rate; one token over
+// 131072: 88-89 us, 6.1 TB/s; 4 single tokens over 200-2000: 22.4 us; 4096 tokens of a
+// prompt of 32768: 1.39-1.42 ms, 1.28-1.30 in short runs (1580 TFLOP/s).  12 requests (24/8 heads of
+// 64, blocks of 16), prompts of 300-511 new tokens among single ones: 45 us.
+// With a window of 4096: 4096 tokens of a prompt 284-297 us (this kernel 272, joining 22), 64 single tokens 195 us, 5.8 TB/s,
+// 32768 packed tokens 1.53-1.62 ms (this kernel alone 1.39; a sequence of 16384 under no window 1.34 ms, 1640 TFLOP/s).
+// What a window costs is an item's start and end, 11-13 thousand cycles on packed sequences, and masked tiles at either end:
+// over the cache 64 us of the prompt's piece, whose items have 5.2 of them among 34.8.
 //
 // Roles (384 threads): warp 0 TMA, warp 1 MMA issue, warp 2 zeroing of dead V
 // rows, warp 3 schedule, warps 4-7 and 8-11 softmax of slots 0 and 1.  Warp 1 issues as a whole, with an elected thread as

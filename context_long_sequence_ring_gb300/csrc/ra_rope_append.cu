@@ -25,8 +25,9 @@ RA_DEFINE_ERROR_FETCH(fetch_error_rope_append)
 namespace {
 
 constexpr int kAppendThreads = 256;
-// Of an SM, and the heads of a thread whose loads are in flight together: 3 and 2 are 80 registers (16384 tokens 72 us;
-// 4 and 2 spill, 92; 5 and 1 78; 2 and 4 86).
+// Of an SM, and the heads of a thread whose loads are in flight together: 3 and 2 are 80 registers, of which bf16 in halves
+// of 16-byte words spills 24 bytes (a block to a token) or 40 (a warp): 16384 tokens 72 us.  4 and 2 spill more, 92; 5 and 1
+// 78; 2 and 4 86.
 constexpr int kAppendBlocks = 3;
 constexpr int kAppendHeads = 2;
 // So many tokens or fewer have a block each, two rounds of them: 608 tokens take 8.5 us (by warps 10.5), 912 10.5 (10.6),

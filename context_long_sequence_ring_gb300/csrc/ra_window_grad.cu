@@ -24,7 +24,7 @@
 //
 // Bound by the tensor core where items are long, and by their starts and ends where a window makes them short.  Measured over
 // 16384 tokens, 32/8 heads, dQ / dK and dV in us: D = 128, window 512 227 / 214, 2048 510 / 597, none 1820 / 2400 (1.81 and
-// 1.83 PFLOP/s executed); D = 64 177 / 176, 408 / 485, 1421 / 1875.  prepare reads o and dO once, 5.6 TB/s; join 15 us.
+// 1.83 PFLOP/s executed); D = 64 177 / 176, 408 / 485, 1421 / 1875.  prepare reads o and dO once, 5.4 TB/s; join 16 us.
 //
 // Rounding.  P and dS are rounded to bf16, the type of the other operand.  delta is formed from an o that has been rounded,
 // whose error all keys of a row share.  Where P sums to 1 over a row, dS sums to 0, so that the dQ kernel's row sums of dS in
@@ -858,7 +858,7 @@ struct KeyItem {
 // Items on their way from the warp that finds them to the others (TMA, products, rows' numbers, softmax), three ahead, so
 // that nobody waits for their divisions and loads (window 512 over 16384 tokens, heads 32 on 8, d 128: 214 us; with every warp
 // finding its own 236).  The kernel of dQ finds its items with less, and keeps what it finds in registers: read from such a
-// ring they take that kernel's softmax beyond its 96 registers (254 us instead of 238).
+// ring they take that kernel's softmax further beyond its 96 registers (254 us instead of 238; as it is it spills 64 bytes).
 constexpr int kAhead = 3;
 constexpr int kReaders = 3 + kSoftmax / 32;
 struct ItemRing {
