@@ -566,11 +566,13 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     const unsigned owner = __ballot_sync(0xffffffffu, mine);
     if (mine || (owner == 0 && lane == 0)) {
       bool more = true;
+      int longest = 0;                   // item so far, in query tiles: as long as one, the others may take to read the next
       for (uint32_t i = 0; more; ++i) {
         more = mine && it.next(s);
         if (!more) s.more = 0;
         const int b = i & (kSegs - 1);
-        if (!mbar_wait(smem_u32(&sm.seg_empty[b]), ((i / kSegs) & 1) ^ 1, abort_flag, lim, 672)) break;
+        if (!mbar_wait(smem_u32(&sm.seg_empty[b]), ((i / kSegs) & 1) ^ 1, abort_flag, limit_over(lim, longest), 672)) break;
+        if (more) longest = max(longest, s.nq);
         sm.item[b] = s;
         mbar_arrive(smem_u32(&sm.seg_full[b]));
       }

@@ -1,4 +1,4 @@
-"""Limits of the window attention's waits are for a tile's time, however long the work between a warp's waits is: calls
+"""Limits of the attention kernels' waits are for a tile's time, however long the work between a warp's waits is: calls
 under a limit of a few tiles give what calls without one give, to the bit, and report nothing.  A wait that expires ends
 its kernel with an error status; no fault or endless wait is involved."""
 import json
@@ -38,6 +38,11 @@ def paged(d, n, ctx, window):
     q, k, v = rnd(n, 32, d), rnd(1, nb, 8, 128, d), rnd(1, nb, 8, 128, d)
     a = q, k, v, torch.arange(nb, dtype=torch.int32, device=dev).view(1, nb), i32(0, n), i32(ctx)
     call((lambda: ra.cp_window_attn(*a, window, 16, 1, 1, n_sink=4)) if window else (lambda: ra.cp_chunk_attn(*a, 16, 1, 1)))
+def weights(d, n, ctx):
+    nb = -(-ctx // 128)
+    q, k, lse = rnd(n, 32, d), rnd(1, nb, 8, 128, d), torch.full((n, 32), 9.0, device=dev)
+    table = torch.arange(nb, dtype=torch.int32, device=dev).view(1, nb)
+    call(lambda: (ra.cp_attn_weights(q, lse, k, table, i32(0, n), i32(ctx), 16, 1, 1),))
 for what, *a in json.loads(sys.argv[2]):
     globals()[what](*a)
 if sys.argv[3] == "save":
@@ -84,3 +89,9 @@ def test_forward_of_items_of_many_tiles(d, work, tmp_path):
     """Items are announced four ahead, so that one is waited for while another is worked off, some 100 tiles and 2 * 10^5
     cycles; the warp that zeroes rows waits past several.  No tile takes 6 * 10^4 cycles."""
     check(60000, [[work[0], d, *work[1:]]], tmp_path)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_of_items_of_many_query_tiles(d, tmp_path):
+    """As above, a pair of key tiles past 128 query tiles at a time."""
+    check(60000, [["weights", d, 4096, 65500]], tmp_path)
